@@ -381,6 +381,121 @@ dora_status dora_linear_fwd(const void *x, const void *W0, const void *xa, const
                             dora_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* (e) the step's activations and frozen weight in 8 bits                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The 8-bit form of a matrix [rows, cols]: q, one E4M3 byte per element
+ * [rows, cols], and scale, one byte b per block, standing for 2^(b - 127),
+ * [ceil(rows / block_rows), ceil(cols / 128)].  block_rows is 1 (an
+ * activation: 128 columns of one row) or 128 (a frozen weight: 128 x 128).
+ * An element's value is E4M3(q) 2^(b - 127).
+ *
+ * The scale of a block is the smallest power of two that brings its largest
+ * finite magnitude to at most 448, and at least 2^-117: every value is then
+ * exact in bf16 (except that a float32 within half a step of 2^128 rounds to
+ * infinity), rounding (nearest even) happens once, in E4M3, and a block of
+ * zeros keeps zeros.  A NaN or an infinity becomes NaN and does not enter its
+ * block's scale.
+ *
+ * The page keeps its activations in 16 bits; it names the memory that a step
+ * holds from forward to backward as what limits it (P1 ¶目前最流行的模型微调技术
+ * 叫做DoRA).  x and v = base + s lora in 8 bits are 2 bytes an element where x,
+ * base and lora in bf16 are 6.
+ */
+
+/*
+ * x into the 8-bit form, one pass.
+ *   act    DORA_F32 or DORA_BF16: dtype of x
+ *   x      [rows, cols] of `act`
+ *   block_rows  1 or 128
+ *   q      uint8 [rows, cols]  out
+ *   scale  uint8 [ceil(rows / block_rows), ceil(cols / 128)]  out
+ *   Sizes: rows, cols >= 0 (either 0 is a no-op), < 2^31.  Any cols and any
+ *   element alignment are accepted; the 128-bit path (block_rows = 1) is taken
+ *   when rows are whole 16-byte pieces of `act` and x and q are aligned to
+ *   16 and 16 / sizeof(act) bytes.
+ */
+dora_status dora_q8_store(dora_dtype act, const void *x, int64_t rows, int64_t cols, int block_rows,
+                          void *q, void *scale, dora_stream_t stream);
+
+/* The values of an 8-bit form: x[i,j] = E4M3(q[i,j]) 2^(b - 127), one pass.
+ * Arguments and sizes as dora_q8_store (x is written). */
+dora_status dora_q8_load(dora_dtype act, const void *q, const void *scale, int64_t rows, int64_t cols,
+                         int block_rows, void *x, dora_stream_t stream);
+
+/*
+ * dora_compose_fwd that also keeps v = base + s lora in the 8-bit form
+ * (block_rows = 1) for dora_compose_bwd_q8, in the same pass.  y is bitwise
+ * what dora_compose_fwd writes; v is rounded to fp32 after the product and
+ * after the sum, then stored as dora_q8_store would store it.
+ *   q, scale  uint8 [T, out] and [T, ceil(out / 128)]  out
+ *   the rest as dora_compose_fwd
+ */
+dora_status dora_compose_fwd_q8(dora_dtype act, const void *base, const void *lora,
+                                const float *g, float s, int64_t T, int64_t out,
+                                void *y, void *q, void *scale, dora_stream_t stream);
+
+/* Bytes of workspace dora_compose_bwd_q8 needs (as dora_compose_bwd_workspace). */
+size_t dora_compose_bwd_q8_workspace(int64_t T, int64_t out);
+
+/*
+ * dora_compose_bwd from the kept v: d_base = g*dy, d_lora = s*g*dy (bitwise
+ * dora_compose_bwd's), d_mag[j] = (sum_t dy[t,j] v[t,j]) / norm[j] with the
+ * 8-bit v, in fp32 and a fixed order.  base and lora are not read.
+ *   q, scale  uint8 [T, out] and [T, ceil(out / 128)] (dora_compose_fwd_q8)
+ *   the rest as dora_compose_bwd
+ */
+dora_status dora_compose_bwd_q8(dora_dtype act, const void *grad_out, const void *q, const void *scale,
+                                const float *g, const float *norm, float s, int64_t T, int64_t out,
+                                void *d_base, void *d_lora, float *d_mag,
+                                void *workspace, size_t workspace_bytes, dora_stream_t stream);
+
+/* Bytes of workspace dora_lora_grad_q8 needs (host arithmetic; 0 for an invalid shape). */
+size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r);
+
+/*
+ * dA = dxa^T x: the gradient of the lora down-projection xa = x A^T from the
+ * 8-bit x kept by the forward; fp32 accumulation and result.
+ *   dxa    bf16 [T, r]   xq uint8 [T, in]   (16-byte aligned, r % 8 == 0, in % 16 == 0)
+ *   xscale uint8 [T, ceil(in / 128)]
+ *   dA     float32 [r, in]  16-byte aligned, overwritten
+ *   workspace  >= dora_lora_grad_q8_workspace(T, in, r) bytes, 256-byte aligned
+ *   Sizes: T, in >= 0 (in == 0 is a no-op, T == 0 writes zeros), 1 <= r <= 1024.
+ */
+dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const void *xscale,
+                              int64_t T, int64_t in, int64_t r, float *dA,
+                              void *workspace, size_t workspace_bytes, dora_stream_t stream);
+
+/* Bytes of workspace dora_matmul_q8 and dora_matmul_q8_t need (host
+ * arithmetic; 0 for an invalid shape). */
+size_t dora_matmul_q8_workspace(int64_t T, int64_t out, int64_t in);
+size_t dora_matmul_q8_t_workspace(int64_t T, int64_t out, int64_t in);
+
+/*
+ * y = x W^T for x and the frozen W both in 8 bits (the base product of the
+ * layer); fp32 accumulation, y rounded once to bf16.
+ *   xq  uint8 [T, in]     xscale  uint8 [T, ceil(in / 128)]
+ *   wq  uint8 [out, in]   wscale  uint8 [ceil(out / 128), ceil(in / 128)]  (block_rows = 128)
+ *   y   bf16 [T, out];  xq, wq and y 16-byte aligned, out % 16 == 0, in % 16 == 0
+ *   workspace  >= dora_matmul_q8_workspace(T, out, in) bytes, 256-byte aligned
+ *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1.
+ */
+dora_status dora_matmul_q8(const void *xq, const void *xscale, const void *wq, const void *wscale,
+                           int64_t T, int64_t out, int64_t in, void *y,
+                           void *workspace, size_t workspace_bytes, dora_stream_t stream);
+
+/*
+ * dx = dy W for the same stored W (no transposed copy) and a dy in 8 bits
+ * (block_rows = 1): dyq [T, out], dyscale [T, ceil(out / 128)], dx bf16 [T, in].
+ * Alignment and errors as dora_matmul_q8.
+ *   Sizes: T, in >= 0 (either 0 is a no-op), out >= 1.
+ */
+dora_status dora_matmul_q8_t(const void *dyq, const void *dyscale, const void *wq, const void *wscale,
+                             int64_t T, int64_t out, int64_t in, void *dx,
+                             void *workspace, size_t workspace_bytes, dora_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 

@@ -31,6 +31,17 @@ __all__ = [
     "dora_compose_bwd_workspace",
     "dora_compose_bwd",
     "dora_compose_bwd_noalloc",
+    "dora_q8_store",
+    "dora_q8_load",
+    "dora_compose_fwd_q8",
+    "dora_compose_bwd_q8_workspace",
+    "dora_compose_bwd_q8",
+    "dora_lora_grad_q8_workspace",
+    "dora_lora_grad_q8",
+    "dora_matmul_q8_workspace",
+    "dora_matmul_q8",
+    "dora_matmul_q8_t_workspace",
+    "dora_matmul_q8_t",
     "dora_device_error",
     "dora_kernel_launches",
     "dora_test_stall_loads",
@@ -69,6 +80,17 @@ _SIGNATURES = {
     "dora_compose_bwd_workspace": (_sz, [_i64, _i64]),
     "dora_compose_bwd": (_int, [_int, _vp, _vp, _vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
     "dora_compose_bwd_noalloc": (_int, [_int, _vp, _vp, _vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "dora_q8_store": (_int, [_int, _vp, _i64, _i64, _int, _vp, _vp, _vp]),
+    "dora_q8_load": (_int, [_int, _vp, _vp, _i64, _i64, _int, _vp, _vp]),
+    "dora_compose_fwd_q8": (_int, [_int, _vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "dora_compose_bwd_q8_workspace": (_sz, [_i64, _i64]),
+    "dora_compose_bwd_q8": (_int, [_int, _vp, _vp, _vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dora_lora_grad_q8_workspace": (_sz, [_i64, _i64, _i64]),
+    "dora_lora_grad_q8": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "dora_matmul_q8_workspace": (_sz, [_i64, _i64, _i64]),
+    "dora_matmul_q8": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "dora_matmul_q8_t_workspace": (_sz, [_i64, _i64, _i64]),
+    "dora_matmul_q8_t": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
     "dora_device_error": (_int, [ctypes.POINTER(_int)]),
     "dora_kernel_launches": (ctypes.c_uint64, []),
     "dora_test_stall_loads": (_int, [_int, ctypes.c_uint64]),
@@ -256,6 +278,128 @@ def dora_compose_bwd_noalloc(grad_out, base, lora, g, norm, s: float, d_base, d_
         _act(grad_out), _ptr(grad_out), _ptr(base), _ptr(lora), _ptr(g), _ptr(norm), float(s), T, out,
         _ptr(d_base), _ptr(d_lora), _ptr(d_mag), _stream(stream))
     _check("dora_compose_bwd_noalloc", st)
+
+
+def _q8(name: str, rows: int, cols: int, block_rows: int, q, scale) -> None:
+    """The shapes of an 8-bit form; the C ABI sees only the matrix's."""
+    if q.element_size() != 1 or scale.element_size() != 1:
+        raise TypeError(f"{name}: the 8-bit form is bytes, got {q.dtype} and {scale.dtype}")
+    want = (-(-rows // block_rows), -(-cols // 128)) if block_rows in (1, 128) else None
+    if tuple(q.shape) != (rows, cols) or (want and tuple(scale.shape) != want):
+        raise ValueError(f"{name}: 8-bit form of [{rows}, {cols}] with {block_rows} rows a scale: "
+                         f"got q {tuple(q.shape)}, scale {tuple(scale.shape)}")
+
+
+def _dense(name: str, *ts) -> None:
+    for t in ts:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous (row-major)")
+
+
+def _same(name: str, shape, dtype, *ts) -> None:
+    for t in ts:
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+            raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+
+
+def dora_q8_store(x, block_rows: int, q, scale, stream=None) -> None:
+    """x [rows, cols] into its 8-bit form: q bytes and a scale per block_rows (1 or
+    128) x 128 elements (see include/dora.h)."""
+    rows, cols = x.shape
+    _q8("dora_q8_store", rows, cols, block_rows, q, scale)
+    _dense("dora_q8_store", x, q, scale)
+    st = load_library().dora_q8_store(_act(x), _ptr(x), rows, cols, block_rows, _ptr(q), _ptr(scale), _stream(stream))
+    _check("dora_q8_store", st)
+
+
+def dora_q8_load(q, scale, block_rows: int, x, stream=None) -> None:
+    """The values of an 8-bit form into x (see include/dora.h)."""
+    rows, cols = x.shape
+    _q8("dora_q8_load", rows, cols, block_rows, q, scale)
+    _dense("dora_q8_load", x, q, scale)
+    st = load_library().dora_q8_load(_act(x), _ptr(q), _ptr(scale), rows, cols, block_rows, _ptr(x), _stream(stream))
+    _check("dora_q8_load", st)
+
+
+def dora_compose_fwd_q8(base, lora, g, s: float, y, q, scale, stream=None) -> None:
+    """dora_compose_fwd that also keeps v = base + s lora in 8 bits (see include/dora.h)."""
+    T, out = base.shape
+    import torch
+    _same("dora_compose_fwd_q8", base.shape, base.dtype, lora, y)
+    _same("dora_compose_fwd_q8", (out,), torch.float32, g)
+    _q8("dora_compose_fwd_q8", T, out, 1, q, scale)
+    _dense("dora_compose_fwd_q8", base, lora, g, y, q, scale)
+    st = load_library().dora_compose_fwd_q8(_act(base), _ptr(base), _ptr(lora), _ptr(g), float(s), T, out, _ptr(y),
+                                            _ptr(q), _ptr(scale), _stream(stream))
+    _check("dora_compose_fwd_q8", st)
+
+
+def dora_compose_bwd_q8_workspace(T: int, out: int) -> int:
+    return int(load_library().dora_compose_bwd_q8_workspace(T, out))
+
+
+def dora_compose_bwd_q8(grad_out, q, scale, g, norm, s: float, d_base, d_lora, d_mag, workspace, stream=None) -> None:
+    """dora_compose_bwd with d_mag from the 8-bit v of dora_compose_fwd_q8 (see include/dora.h)."""
+    T, out = grad_out.shape
+    import torch
+    _same("dora_compose_bwd_q8", grad_out.shape, grad_out.dtype, d_base, d_lora)
+    _same("dora_compose_bwd_q8", (out,), torch.float32, g, norm, d_mag)
+    _q8("dora_compose_bwd_q8", T, out, 1, q, scale)
+    _dense("dora_compose_bwd_q8", grad_out, q, scale, g, norm, d_base, d_lora, d_mag)
+    st = load_library().dora_compose_bwd_q8(
+        _act(grad_out), _ptr(grad_out), _ptr(q), _ptr(scale), _ptr(g), _ptr(norm), float(s), T, out,
+        _ptr(d_base), _ptr(d_lora), _ptr(d_mag), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("dora_compose_bwd_q8", st)
+
+
+def dora_lora_grad_q8_workspace(T: int, inp: int, r: int) -> int:
+    return int(load_library().dora_lora_grad_q8_workspace(T, inp, r))
+
+
+def dora_lora_grad_q8(dxa, xq, xscale, dA, workspace, stream=None) -> None:
+    """dA = dxa^T x from the 8-bit x (see include/dora.h)."""
+    import torch
+    T, r = dxa.shape
+    inp = xq.shape[1]
+    _same("dora_lora_grad_q8", (T, r), torch.bfloat16, dxa)
+    _same("dora_lora_grad_q8", (r, inp), torch.float32, dA)
+    _q8("dora_lora_grad_q8", T, inp, 1, xq, xscale)
+    _dense("dora_lora_grad_q8", dxa, xq, xscale, dA)
+    st = load_library().dora_lora_grad_q8(_ptr(dxa), _ptr(xq), _ptr(xscale), T, inp, r, _ptr(dA), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("dora_lora_grad_q8", st)
+
+
+def dora_matmul_q8_workspace(T: int, out: int, inp: int) -> int:
+    return int(load_library().dora_matmul_q8_workspace(T, out, inp))
+
+
+def dora_matmul_q8_t_workspace(T: int, out: int, inp: int) -> int:
+    return int(load_library().dora_matmul_q8_t_workspace(T, out, inp))
+
+
+def _matmul_q8(name: str, q, scale, wq, wscale, y, workspace, stream, out_side: bool) -> None:
+    import torch
+    out, inp = wq.shape
+    T = q.shape[0]
+    _q8(name, T, inp if out_side else out, 1, q, scale)
+    _q8(name, out, inp, 128, wq, wscale)
+    _same(name, (T, out if out_side else inp), torch.bfloat16, y)
+    _dense(name, q, scale, wq, wscale, y)
+    st = getattr(load_library(), name)(_ptr(q), _ptr(scale), _ptr(wq), _ptr(wscale), T, out, inp, _ptr(y),
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(name, st)
+
+
+def dora_matmul_q8(xq, xscale, wq, wscale, y, workspace, stream=None) -> None:
+    """y = x W^T for x and W in 8 bits (see include/dora.h)."""
+    _matmul_q8("dora_matmul_q8", xq, xscale, wq, wscale, y, workspace, stream, True)
+
+
+def dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx, workspace, stream=None) -> None:
+    """dx = dy W for dy and the same W in 8 bits (see include/dora.h)."""
+    _matmul_q8("dora_matmul_q8_t", dyq, dyscale, wq, wscale, dx, workspace, stream, False)
 
 
 def dora_device_error() -> int:
