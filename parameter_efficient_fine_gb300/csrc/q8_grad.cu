@@ -1,18 +1,16 @@
-// Products of 8-bit matrices (see q8.cuh for the form) for GB300 (sm_103a).
+// The gradient of A from the 8-bit x (see q8.cuh for the form) for GB300
+// (sm_103a): dora_lora_grad_q8, dA = dxa^T x, dxa [T, r] bf16, x [T, in].
 //
-//   dora_matmul_q8     y  = x W^T      x [T, in], W [out, in] in 8 bits
-//   dora_matmul_q8_t   dx = dy W       dy [T, out] in 8 bits, the same W
-//   dora_lora_grad_q8  dA = dxa^T x    dxa [T, r] bf16, x [T, in] in 8 bits
-//
-// The first kernels: 64 x 64 tiles of the result on the CUDA cores, operands
-// decoded into shared memory in fp32, 16 k at a time, a 4 x 4 block a thread,
-// sums in chains of 256 k that are added up apart (a chain's rounding error
-// grows with its length).
+// 64 x 64 tiles of the result on the CUDA cores, operands decoded into shared
+// memory in fp32, 16 tokens at a time, a 4 x 4 block a thread, sums in chains
+// of 256 tokens that are added up apart (a chain's rounding error grows with
+// its length).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "q8.cuh"
+#include "tc_ptx.cuh"
 
 namespace {
 
@@ -106,53 +104,7 @@ dora_status run_tiles(const Operands &o, int64_t m, int64_t n, int64_t k, void *
 
 bool bad_size(int64_t v, int64_t least) { return v < least || v > kMaxDim; }
 
-dora_status matmul_check(const void *xq, const void *xscale, const void *wq, const void *wscale, int64_t out,
-                         int64_t in, const void *y, const void *workspace, size_t have, size_t need) {
-  if (!xq || !xscale || !wq || !wscale || !y) return DORA_ERR_NULL;
-  // TMA: 16-byte aligned bases and row strides
-  if (out % 16 != 0 || in % 16 != 0) return DORA_ERR_ALIGN;
-  if (!dora::aligned(xq, 16) || !dora::aligned(wq, 16) || !dora::aligned(y, 16)) return DORA_ERR_ALIGN;
-  if (!workspace || !dora::aligned(workspace, 256) || have < need) return DORA_ERR_WORKSPACE;
-  return DORA_OK;
-}
-
 }  // namespace
-
-extern "C" size_t dora_matmul_q8_workspace(int64_t T, int64_t out, int64_t in) {
-  if (bad_size(T, 0) || bad_size(out, 0) || bad_size(in, 1)) return 0;
-  return 256;
-}
-
-extern "C" size_t dora_matmul_q8_t_workspace(int64_t T, int64_t out, int64_t in) {
-  if (bad_size(T, 0) || bad_size(out, 1) || bad_size(in, 0)) return 0;
-  return 256;
-}
-
-extern "C" dora_status dora_matmul_q8(const void *xq, const void *xscale, const void *wq, const void *wscale, int64_t T,
-                                      int64_t out, int64_t in, void *y, void *workspace, size_t workspace_bytes,
-                                      dora_stream_t stream) {
-  if (bad_size(T, 0) || bad_size(out, 0) || bad_size(in, 1)) return DORA_ERR_SHAPE;
-  if (T == 0 || out == 0) return DORA_OK;
-  const dora_status st = matmul_check(xq, xscale, wq, wscale, out, in, y, workspace, workspace_bytes,
-                                      dora_matmul_q8_workspace(T, out, in));
-  if (st != DORA_OK) return st;
-  const Operands o = {static_cast<const uint8_t *>(xq), static_cast<const uint8_t *>(xscale),
-                      static_cast<const uint8_t *>(wq), static_cast<const uint8_t *>(wscale), nullptr, T, out, in, 0};
-  return run_tiles<kMatmul, __nv_bfloat16>(o, T, out, in, y, stream);
-}
-
-extern "C" dora_status dora_matmul_q8_t(const void *dyq, const void *dyscale, const void *wq, const void *wscale,
-                                        int64_t T, int64_t out, int64_t in, void *dx, void *workspace,
-                                        size_t workspace_bytes, dora_stream_t stream) {
-  if (bad_size(T, 0) || bad_size(out, 1) || bad_size(in, 0)) return DORA_ERR_SHAPE;
-  if (T == 0 || in == 0) return DORA_OK;
-  const dora_status st = matmul_check(dyq, dyscale, wq, wscale, out, in, dx, workspace, workspace_bytes,
-                                      dora_matmul_q8_t_workspace(T, out, in));
-  if (st != DORA_OK) return st;
-  const Operands o = {static_cast<const uint8_t *>(dyq), static_cast<const uint8_t *>(dyscale),
-                      static_cast<const uint8_t *>(wq), static_cast<const uint8_t *>(wscale), nullptr, T, out, in, 0};
-  return run_tiles<kMatmulT, __nv_bfloat16>(o, T, in, out, dx, stream);
-}
 
 extern "C" size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r) {
   if (bad_size(T, 0) || bad_size(in, 0) || r < 1 || r > 1024) return 0;

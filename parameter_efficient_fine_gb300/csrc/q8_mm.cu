@@ -1,0 +1,486 @@
+// Products of two 8-bit matrices (see q8.cuh for the form) on the tensor cores
+// of GB300 (sm_103a).
+//
+//   dora_matmul_q8     y  = x W^T      x [T, in], W [out, in]
+//   dora_matmul_q8_t   dx = dy W       dy [T, out], the same W
+//
+// One k block is 128 wide, the width of a scale block, so the scales of a k
+// block are one byte per token and one byte per 128 features.  The tensor core
+// applies them itself: tcgen05.mma kind::mxf8f6f4 with block scaling multiplies
+// every 32-wide step of k by a power of two per row of either operand, read
+// from tensor memory; the four steps of a k block name the same byte.  The
+// bytes of four consecutive k blocks form the 32-bit words that tensor memory
+// holds them in, and the instruction picks one of the four.
+//
+// The features are the M side (128 rows of the tile are 128 features, whose
+// scale is one byte), the tokens the N side, so a few tokens cost a narrow
+// MMA and not a wide one mostly idle.  W is read as it is stored in both
+// products: for x W^T a k block of a tile is 128 features x 128 bytes along k
+// (K-major), for dy W it is 128 rows of k x 128 bytes along the features
+// (M-major, the transpose bit of the instruction).
+//
+// q8_split_kernel: one tile of 128 features x NT tokens per cluster of CTAs,
+// which share its k range; each CTA streams its part through a ring of TMA
+// stages, and the parts meet in distributed shared memory, summed in rank
+// order (bitwise reproducible, no workspace).
+//   warp 0     TMA producer: per k block the W box (16 KB) and the token box
+//   warp 1     tensor memory, MMA issue (four 32-wide steps per k block)
+//   warps 2-5  scale words into tensor memory, four k blocks at a time, each
+//              warp its lane quadrant; then the result out of it
+// Every wait on a shared-memory barrier is bounded; a wait that gives up
+// records a code in the library's device error word and all roles leave.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "q8.cuh"
+#include "tc_ptx.cuh"
+
+namespace {
+
+constexpr int64_t kMaxDim = (1ll << 31) - 1;
+constexpr int kKB = 128;                    // k per block: one 128-byte swizzled row, one scale
+constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB
+constexpr int kSfSlots = 4;                 // scale words in flight, in groups of four k blocks
+constexpr int kSplitThreads = 192;
+constexpr int kMaxStages = 8;
+constexpr int kMaxCluster = 8;              // the portable limit
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+struct MmParams {
+  int T, nfeat, kdim;               // tokens, features of the result, k
+  int kblocks;
+  int ntiles, tiles;                // token tiles, all tiles
+  int stages;
+  int nsx, nsw;                     // scale bytes per row of x, of W
+  const uint8_t *xscale, *wscale;
+  __nv_bfloat16 *y;
+  int *err;
+  const int *stall;
+  const unsigned long long *limit_ns;
+};
+
+// D (+)= A B with a power-of-two scale per row of A and per row of B, E4M3
+// operands in shared memory, scale words in tensor memory
+__device__ __forceinline__ void mma_q8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                       uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+// instruction descriptor: E4M3 x E4M3, E8M0 scales, fp32 accumulator, M = m,
+// N = n, `byte` of the scale words on both sides, A transposed (M-major) or not
+__device__ __forceinline__ uint32_t idesc_q8(int m, int n, uint32_t byte, bool a_mmajor) {
+  return (byte << 4)                                  // B's scale byte
+         | (a_mmajor ? 1u << 15 : 0u)
+         | (static_cast<uint32_t>(n >> 3) << 17)
+         | (1u << 23)                                 // E8M0 scales
+         | (static_cast<uint32_t>(m >> 4) << 24)
+         | (byte << 29);                              // A's scale byte
+}
+// 16 consecutive fp32 columns of this thread's tensor-memory lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, SharedCtl *ctl, const MmParams &p, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_bounded_ns(bar, parity, ctl, p.err, code, *reinterpret_cast<const volatile unsigned long long *>(p.limit_ns));
+}
+
+// the scale bytes of k blocks 4 g .. 4 g + 3 of one row of an activation, a
+// byte each; 1 past the last k block
+__device__ __forceinline__ uint32_t token_word(const uint8_t *row, int g, int kblocks, bool words) {
+  if (words) return __ldg(reinterpret_cast<const uint32_t *>(row) + g);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= static_cast<uint32_t>(4 * g + i < kblocks ? __ldg(row + 4 * g + i) : 127) << (8 * i);
+  return w;
+}
+// the same of 128 features of W: along a row of its scales, or down a column
+template <bool TRANS>
+__device__ __forceinline__ uint32_t weight_word(const MmParams &p, int mt, int g) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int kb = 4 * g + i;
+    const int64_t at = TRANS ? static_cast<int64_t>(kb) * p.nsw + mt : static_cast<int64_t>(mt) * p.nsw + kb;
+    w |= static_cast<uint32_t>(kb < p.kblocks ? __ldg(p.wscale + at) : 127) << (8 * i);
+  }
+  return w;
+}
+
+template <int NT, bool TRANS>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const MmParams p) {
+  static_assert(NT % 16 == 0 && NT <= 128, "one chunk of scale words");
+  constexpr unsigned kXBytes = NT * kKB;
+  constexpr unsigned kStage = kWBytes + kXBytes;
+  constexpr int kSfCol = NT < 32 ? 32 : NT;          // first column of the scale words
+  constexpr int kCols = NT <= 32 ? 64 : NT == 64 ? 128 : 256;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = p.stages;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + static_cast<size_t>(S) * kStage);
+  // barriers: full[S], empty[S], scales full and empty [kSfSlots], accumulator
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, sff0 = empty0 + 8u * S, sfe0 = sff0 + 8u * kSfSlots,
+                 accf = sfe0 + 8u * kSfSlots;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * S + 2 * kSfSlots + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8u * s, 1);
+      mbar_init(empty0 + 8u * s, 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(sff0 + 8u * s, 4);
+      mbar_init(sfe0 + 8u * s, 1);
+    }
+    mbar_init(accf, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+    prefetch_map(&mW);
+    prefetch_map(&mX);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(smem_u32(&ctl->tmem_base), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  uint32_t csize;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const uint32_t rank = cluster_ctarank();
+  const int tile = static_cast<int>(blockIdx.x / csize);
+  const int mt = tile / p.ntiles, nt = tile % p.ntiles;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / csize);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / csize);
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- producer
+      ok = *reinterpret_cast<const volatile int *>(p.stall) == 0;
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        if (!mm_wait(empty0 + 8u * stage, phase ^ 1u, ctl, p, 21)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = full0 + 8u * stage;
+        const uint32_t at = smem_u32(smem + static_cast<size_t>(stage) * kStage);
+        mbar_expect_tx(fb, kStage);
+        if (TRANS) tma_load_2d(at, &mW, mt * kTcM, kb * kKB, fb);
+        else tma_load_2d(at, &mW, kb * kKB, mt * kTcM, fb);
+        tma_load_2d(at + kWBytes, &mX, kb * kKB, nt * NT, fb);
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok)
+        for (int k = 0; k < S && k < issued; ++k) {   // copies in flight
+          if (--stage < 0) {
+            stage = S - 1;
+            phase ^= 1u;
+          }
+          wait_drain_ns(full0 + 8u * stage, phase, kWaitNs);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int grp = kb / 4 - kb0 / 4, slot = grp % kSfSlots;
+        if (kb == kb0 || kb % 4 == 0) {
+          if (!mm_wait(sff0 + 8u * slot, static_cast<uint32_t>(grp / kSfSlots) & 1u, ctl, p, 22)) break;
+        }
+        if (!mm_wait(full0 + 8u * stage, phase, ctl, p, 23)) break;
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + static_cast<size_t>(stage) * kStage);
+        const uint32_t idesc = idesc_q8(kTcM, NT, static_cast<uint32_t>(kb & 3), TRANS);
+        const uint32_t sf = tmem + kSfCol + 8u * slot;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          // 32 k: 32 bytes along a K-major row; 32 rows of 128 bytes M-major
+          mma_q8(tmem, sdesc<32>(at + (TRANS ? 4096u : 32u) * k), sdesc<32>(at + kWBytes + 32u * k), idesc, sf, sf + 4,
+                 kb != kb0 || k != 0 ? 1u : 0u);
+        mma_commit(empty0 + 8u * stage);
+        if (kb % 4 == 3) mma_commit(sfe0 + 8u * slot);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      mma_commit(accf);
+      wait_drain_ns(accf, 0, kWaitNs);   // every MMA issued is done before this CTA's memory is given back
+    }
+  } else {
+    // ---------------------------------------------------------------- scales
+    const uint32_t quad = static_cast<uint32_t>(warp & 3);
+    const uint32_t lane_addr = tmem + ((quad * 32u) << 16);
+    const bool words = p.nsx % 4 == 0 && (reinterpret_cast<uintptr_t>(p.xscale) & 3) == 0;
+    const int g0 = kb0 / 4, g1 = kb1 > kb0 ? (kb1 - 1) / 4 + 1 : g0;
+    for (int g = g0; g < g1; ++g) {
+      uint32_t w[8];
+      w[0] = w[1] = w[2] = w[3] = weight_word<TRANS>(p, mt, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = nt * NT + 32 * j + lane;
+        w[4 + j] = 32 * j < NT && t < p.T ? token_word(p.xscale + static_cast<int64_t>(t) * p.nsx, g, p.kblocks, words)
+                                          : 0x7f7f7f7fu;
+      }
+      const int slot = (g - g0) % kSfSlots;
+      const bool got = mm_wait(sfe0 + 8u * slot, (static_cast<uint32_t>((g - g0) / kSfSlots) & 1u) ^ 1u, ctl, p, 24);
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_st8(lane_addr + kSfCol + 8u * slot, w);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sff0 + 8u * slot);
+    }
+    // ---------------------------------------------------------------- result
+    // into shared memory as [token][feature]: the stages are free once the
+    // last MMA is done
+    const bool got = mm_wait(accf, 0, ctl, p, 25);
+    ok = __all_sync(0xffffffffu, got) && ok && kb1 > kb0;
+    tc_fence_after();
+    float *part = reinterpret_cast<float *>(smem);
+    const int f = static_cast<int>(quad) * 32 + lane;
+    const int live = min(NT, p.T - nt * NT);
+#pragma unroll
+    for (int c = 0; c < NT; c += 16) {
+      if (c < live) {
+        float v[16];
+        tmem_ld16(lane_addr + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(c + i) * kTcM + f] = ok ? v[i] : 0.0f;
+      }
+    }
+  }
+  tc_fence_before();
+  if (csize > 1) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  {
+    // the parts of the cluster in rank order, one rounding to bf16: four
+    // features a thread, neighbouring threads on neighbouring features
+    const int live = min(NT, p.T - nt * NT) * 32;
+    const uint32_t base = smem_u32(smem);
+    for (int i = static_cast<int>(rank) * kSplitThreads + threadIdx.x; i < live;
+         i += static_cast<int>(csize) * kSplitThreads) {
+      float4 s = ld_cluster_f32x4(mapa_shared(base + 16u * i, 0));
+      for (uint32_t c = 1; c < csize; ++c) {
+        const float4 v = ld_cluster_f32x4(mapa_shared(base + 16u * i, c));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      const int t = nt * NT + i / 32, f = mt * kTcM + 4 * (i % 32);
+      if (f < p.nfeat)
+        *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(t) * p.nfeat + f) =
+            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  }
+  if (csize > 1) cluster_sync();   // no CTA leaves while another reads its part
+  else __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// bytes [rows, cols] (cols a multiple of 16) with a [box_rows x 128] box, 128-byte swizzle
+bool map_q8(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSmemMax = 232448;
+size_t split_smem(int nt, int stages) { return 1024 + static_cast<size_t>(stages) * (kWBytes + nt * kKB) + 512; }
+
+template <int NT, bool TRANS>
+dora_status launch_split(const CUtensorMap &mW, const CUtensorMap &mX, MmParams p, int cluster, cudaStream_t cs) {
+  constexpr auto kern = &q8_split_kernel<NT, TRANS>;
+  // two CTAs an SM: half of the shared memory each
+  p.stages = static_cast<int>((kSmemMax / 2 - 2048) / (kWBytes + NT * kKB));
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const size_t smem = split_smem(NT, p.stages);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * cluster));
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = cs;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, mW, mX, p) != cudaSuccess) {
+    cudaGetLastError();
+    return DORA_ERR_CUDA;
+  }
+  dora::count_launches(1);
+  return DORA_OK;
+}
+
+dora_status mm_init(int device, MmParams *p) {
+  static std::mutex mu;
+  static uint64_t done_ctx[64] = {};
+  static int *stall[64] = {};
+  static unsigned long long *limit[64] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (device < 0 || device >= 64) return DORA_ERR_CUDA;
+  dora_status st = dora::error_word(device, &p->err);
+  if (st != DORA_OK) return st;
+  st = dora::test_hooks(&stall[device], &limit[device]);
+  if (st != DORA_OK) return st;
+  p->stall = stall[device];
+  p->limit_ns = limit[device];
+  const uint64_t ctx = dora::context_id();
+  if (ctx == 0 || ctx != done_ctx[device]) {
+    const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const void *k[] = {(const void *)q8_split_kernel<16, false>, (const void *)q8_split_kernel<32, false>,
+                       (const void *)q8_split_kernel<64, false>, (const void *)q8_split_kernel<128, false>,
+                       (const void *)q8_split_kernel<16, true>,  (const void *)q8_split_kernel<32, true>,
+                       (const void *)q8_split_kernel<64, true>,  (const void *)q8_split_kernel<128, true>};
+    for (const void *f : k)
+      if (cudaFuncSetAttribute(f, a, kSmemMax) != cudaSuccess) return DORA_ERR_CUDA;
+    done_ctx[device] = dora::context_id();
+  }
+  return DORA_OK;
+}
+
+// q: the activation's bytes [T, kdim]; features and k are (out, in) or, for dy W, (in, out)
+template <bool TRANS>
+dora_status run_matmul(const void *q, const void *scale, const void *wq, const void *wscale, int64_t T, int64_t out,
+                       int64_t in, void *y, dora_stream_t stream) {
+  dora::DeviceInfo info;
+  int device = 0;
+  dora_status st = dora::current_device(&info, &device);
+  if (st != DORA_OK) return st;
+  MmParams p = {};
+  st = mm_init(device, &p);
+  if (st != DORA_OK) return st;
+  p.T = static_cast<int>(T);
+  p.nfeat = static_cast<int>(TRANS ? in : out);
+  p.kdim = static_cast<int>(TRANS ? out : in);
+  p.kblocks = static_cast<int>(dora::ceil_div(p.kdim, kKB));
+  p.nsx = p.kblocks;
+  p.nsw = static_cast<int>(dora::ceil_div(in, kQBlock));
+  p.xscale = static_cast<const uint8_t *>(scale);
+  p.wscale = static_cast<const uint8_t *>(wscale);
+  p.y = static_cast<__nv_bfloat16 *>(y);
+  const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  p.ntiles = static_cast<int>(dora::ceil_div(T, nt));
+  const int64_t tiles = dora::ceil_div(p.nfeat, kTcM) * p.ntiles;
+  if (tiles * kMaxCluster > kMaxDim) return DORA_ERR_SHAPE;
+  p.tiles = static_cast<int>(tiles);
+  // the k range over as many CTAs as keep all clusters resident at two CTAs an SM
+  int cluster = 1;
+  while (cluster < kMaxCluster && tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= p.kblocks) cluster *= 2;
+  CUtensorMap mW, mX;
+  if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, T, p.kdim, nt)) return DORA_ERR_CUDA;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  switch (nt) {
+    case 16: return launch_split<16, TRANS>(mW, mX, p, cluster, cs);
+    case 32: return launch_split<32, TRANS>(mW, mX, p, cluster, cs);
+    case 64: return launch_split<64, TRANS>(mW, mX, p, cluster, cs);
+  }
+  return launch_split<128, TRANS>(mW, mX, p, cluster, cs);
+}
+
+bool bad_size(int64_t v, int64_t least) { return v < least || v > kMaxDim; }
+
+dora_status matmul_check(const void *xq, const void *xscale, const void *wq, const void *wscale, int64_t out,
+                         int64_t in, const void *y, const void *workspace, size_t have, size_t need) {
+  if (!xq || !xscale || !wq || !wscale || !y) return DORA_ERR_NULL;
+  // TMA: 16-byte aligned bases and row strides
+  if (out % 16 != 0 || in % 16 != 0) return DORA_ERR_ALIGN;
+  if (!dora::aligned(xq, 16) || !dora::aligned(wq, 16) || !dora::aligned(y, 16)) return DORA_ERR_ALIGN;
+  if (!workspace || !dora::aligned(workspace, 256) || have < need) return DORA_ERR_WORKSPACE;
+  return DORA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t dora_matmul_q8_workspace(int64_t T, int64_t out, int64_t in) {
+  if (bad_size(T, 0) || bad_size(out, 0) || bad_size(in, 1)) return 0;
+  return 256;
+}
+
+extern "C" size_t dora_matmul_q8_t_workspace(int64_t T, int64_t out, int64_t in) {
+  if (bad_size(T, 0) || bad_size(out, 1) || bad_size(in, 0)) return 0;
+  return 256;
+}
+
+extern "C" dora_status dora_matmul_q8(const void *xq, const void *xscale, const void *wq, const void *wscale, int64_t T,
+                                      int64_t out, int64_t in, void *y, void *workspace, size_t workspace_bytes,
+                                      dora_stream_t stream) {
+  if (bad_size(T, 0) || bad_size(out, 0) || bad_size(in, 1)) return DORA_ERR_SHAPE;
+  if (T == 0 || out == 0) return DORA_OK;
+  const dora_status st = matmul_check(xq, xscale, wq, wscale, out, in, y, workspace, workspace_bytes,
+                                      dora_matmul_q8_workspace(T, out, in));
+  if (st != DORA_OK) return st;
+  return run_matmul<false>(xq, xscale, wq, wscale, T, out, in, y, stream);
+}
+
+extern "C" dora_status dora_matmul_q8_t(const void *dyq, const void *dyscale, const void *wq, const void *wscale,
+                                        int64_t T, int64_t out, int64_t in, void *dx, void *workspace,
+                                        size_t workspace_bytes, dora_stream_t stream) {
+  if (bad_size(T, 0) || bad_size(out, 1) || bad_size(in, 0)) return DORA_ERR_SHAPE;
+  if (T == 0 || in == 0) return DORA_OK;
+  const dora_status st = matmul_check(dyq, dyscale, wq, wscale, out, in, dx, workspace, workspace_bytes,
+                                      dora_matmul_q8_t_workspace(T, out, in));
+  if (st != DORA_OK) return st;
+  return run_matmul<true>(dyq, dyscale, wq, wscale, T, out, in, dx, stream);
+}
