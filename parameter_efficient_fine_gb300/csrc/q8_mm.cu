@@ -33,22 +33,19 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "common.cuh"
 #include "q8.cuh"
+#include "q8_tc.cuh"
 #include "tc_ptx.cuh"
 
 namespace {
 
-constexpr int64_t kMaxDim = (1ll << 31) - 1;
 constexpr int kKB = 128;                    // k per block: one 128-byte swizzled row, one scale
 constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB
 constexpr int kSfSlots = 4;                 // scale words in flight, in groups of four k blocks
 constexpr int kSplitThreads = 192;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;              // the portable limit
-constexpr unsigned long long kWaitNs = 2000000000ull;
 
 struct MmParams {
   int T, nfeat, kdim;               // tokens, features of the result, k
@@ -58,9 +55,7 @@ struct MmParams {
   int nsx, nsw;                     // scale bytes per row of x, of W
   const uint8_t *xscale, *wscale;
   __nv_bfloat16 *y;
-  int *err;
-  const int *stall;
-  const unsigned long long *limit_ns;
+  Guard guard;
 };
 
 // D (+)= A B with a power-of-two scale per row of A and per row of B, E4M3
@@ -84,20 +79,6 @@ __device__ __forceinline__ uint32_t idesc_q8(int m, int n, uint32_t byte, bool a
          | (static_cast<uint32_t>(m >> 4) << 24)
          | (byte << 29);                              // A's scale byte
 }
-// 16 consecutive fp32 columns of this thread's tensor-memory lane
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -105,11 +86,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-
-__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, SharedCtl *ctl, const MmParams &p, int code) {
-  if (mbar_try_wait(bar, parity)) return true;
-  return wait_bounded_ns(bar, parity, ctl, p.err, code, *reinterpret_cast<const volatile unsigned long long *>(p.limit_ns));
 }
 
 // the scale bytes of k blocks 4 g .. 4 g + 3 of one row of an activation, a
@@ -188,11 +164,11 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------------- producer
-      ok = *reinterpret_cast<const volatile int *>(p.stall) == 0;
+      ok = !loads_withheld(p.guard);
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       for (int kb = kb0; kb < kb1 && ok; ++kb) {
-        if (!mm_wait(empty0 + 8u * stage, phase ^ 1u, ctl, p, 21)) {
+        if (!guard_wait(empty0 + 8u * stage, phase ^ 1u, ctl, p.guard, 21)) {
           ok = false;
           break;
         }
@@ -225,9 +201,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
       for (int kb = kb0; kb < kb1; ++kb) {
         const int grp = kb / 4 - kb0 / 4, slot = grp % kSfSlots;
         if (kb == kb0 || kb % 4 == 0) {
-          if (!mm_wait(sff0 + 8u * slot, static_cast<uint32_t>(grp / kSfSlots) & 1u, ctl, p, 22)) break;
+          if (!guard_wait(sff0 + 8u * slot, static_cast<uint32_t>(grp / kSfSlots) & 1u, ctl, p.guard, 22)) break;
         }
-        if (!mm_wait(full0 + 8u * stage, phase, ctl, p, 23)) break;
+        if (!guard_wait(full0 + 8u * stage, phase, ctl, p.guard, 23)) break;
         tc_fence_after();
         const uint32_t at = smem_u32(smem + static_cast<size_t>(stage) * kStage);
         const uint32_t idesc = idesc_q8(kTcM, NT, static_cast<uint32_t>(kb & 3), TRANS);
@@ -263,7 +239,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
                                           : 0x7f7f7f7fu;
       }
       const int slot = (g - g0) % kSfSlots;
-      const bool got = mm_wait(sfe0 + 8u * slot, (static_cast<uint32_t>((g - g0) / kSfSlots) & 1u) ^ 1u, ctl, p, 24);
+      const bool got = guard_wait(sfe0 + 8u * slot, (static_cast<uint32_t>((g - g0) / kSfSlots) & 1u) ^ 1u, ctl, p.guard, 24);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
@@ -278,7 +254,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
     // ---------------------------------------------------------------- result
     // into shared memory as [token][feature]: the stages are free once the
     // last MMA is done
-    const bool got = mm_wait(accf, 0, ctl, p, 25);
+    const bool got = guard_wait(accf, 0, ctl, p.guard, 25);
     ok = __all_sync(0xffffffffu, got) && ok && kb1 > kb0;
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
@@ -288,7 +264,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
     for (int c = 0; c < NT; c += 16) {
       if (c < live) {
         float v[16];
-        tmem_ld16(lane_addr + c, v);
+        tmem_ld<16>(lane_addr + c, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) part[(c + i) * kTcM + f] = ok ? v[i] : 0.0f;
       }
@@ -330,20 +306,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// bytes [rows, cols] (cols a multiple of 16) with a [box_rows x 128] box, 128-byte swizzle
-bool map_q8(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-constexpr int kSmemMax = 232448;
 size_t split_smem(int nt, int stages) { return 1024 + static_cast<size_t>(stages) * (kWBytes + nt * kKB) + 512; }
 
 template <int NT, bool TRANS>
@@ -374,30 +336,12 @@ dora_status launch_split(const CUtensorMap &mW, const CUtensorMap &mX, MmParams 
 }
 
 dora_status mm_init(int device, MmParams *p) {
-  static std::mutex mu;
-  static uint64_t done_ctx[64] = {};
-  static int *stall[64] = {};
-  static unsigned long long *limit[64] = {};
-  std::lock_guard<std::mutex> lock(mu);
-  if (device < 0 || device >= 64) return DORA_ERR_CUDA;
-  dora_status st = dora::error_word(device, &p->err);
-  if (st != DORA_OK) return st;
-  st = dora::test_hooks(&stall[device], &limit[device]);
-  if (st != DORA_OK) return st;
-  p->stall = stall[device];
-  p->limit_ns = limit[device];
-  const uint64_t ctx = dora::context_id();
-  if (ctx == 0 || ctx != done_ctx[device]) {
-    const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    const void *k[] = {(const void *)q8_split_kernel<16, false>, (const void *)q8_split_kernel<32, false>,
-                       (const void *)q8_split_kernel<64, false>, (const void *)q8_split_kernel<128, false>,
-                       (const void *)q8_split_kernel<16, true>,  (const void *)q8_split_kernel<32, true>,
-                       (const void *)q8_split_kernel<64, true>,  (const void *)q8_split_kernel<128, true>};
-    for (const void *f : k)
-      if (cudaFuncSetAttribute(f, a, kSmemMax) != cudaSuccess) return DORA_ERR_CUDA;
-    done_ctx[device] = dora::context_id();
-  }
-  return DORA_OK;
+  static const void *const kernels[] = {
+      (const void *)q8_split_kernel<16, false>, (const void *)q8_split_kernel<32, false>,
+      (const void *)q8_split_kernel<64, false>, (const void *)q8_split_kernel<128, false>,
+      (const void *)q8_split_kernel<16, true>,  (const void *)q8_split_kernel<32, true>,
+      (const void *)q8_split_kernel<64, true>,  (const void *)q8_split_kernel<128, true>};
+  return tc_init(device, &p->guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
 }
 
 // q: the activation's bytes [T, kdim]; features and k are (out, in) or, for dy W, (in, out)
@@ -438,8 +382,6 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   }
   return launch_split<128, TRANS>(mW, mX, p, cluster, cs);
 }
-
-bool bad_size(int64_t v, int64_t least) { return v < least || v > kMaxDim; }
 
 dora_status matmul_check(const void *xq, const void *xscale, const void *wq, const void *wscale, int64_t out,
                          int64_t in, const void *y, const void *workspace, size_t have, size_t need) {
