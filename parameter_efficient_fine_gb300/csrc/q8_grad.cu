@@ -4,23 +4,37 @@
 //
 // Every value of an 8-bit form is exact in bf16, so the product runs as
 // kind::f16 bf16 MMAs with exact products: 128 features of x on the M side, up
-// to 256 columns of dxa on the N side, the tokens as k.  Both operands lie in
-// memory token by token, so both are M-/N-major: no transposed copy is made.
+// to 192 columns of dxa on the N side, the tokens as k.  dxa is read as it
+// lies, token by token (N-major).  x passes through registers once: transposed
+// loads from shared memory (ldmatrix) give a thread two features at two tokens
+// a register, a few bit operations and one product per pair turn them into
+// bf16 words of one feature each, and tcgen05.st puts them into tensor memory,
+// where the MMA takes its M side from.  Shared memory moves each byte of x
+// once in and once out; as a bf16 operand in shared memory (the form measured
+// first) it moved six times that and was the limit.
 //
 // The tensor core's fp32 sum rounds toward zero, so its error grows with the
-// length of a chain of MMAs.  A window of 256 tokens is one chain (16 MMAs of
-// k = 16); the windows are added up in registers with ordinary rounding.
+// length of a chain of MMAs.  A window of 256 or 512 tokens is one chain (16
+// or 32 MMAs of k = 16); the windows are added up in registers with ordinary
+// rounding.
 //
 // Work: a tile of the result is 128 features x N columns of r; its windows
 // are units, and each CTA (one per SM) takes an equal run of units over all
 // tiles.  A CTA that has a whole tile writes dA; otherwise it writes its part
 // to the workspace and grad_join_kernel adds the parts of a tile in order
 // (bitwise reproducible).
-//   warp 0      TMA producer: per stage (64 tokens) the x bytes of the tile's
-//               128 features (8 KB) and the dxa boxes (8 KB per 64 columns)
-//   warp 1      tensor memory (two window accumulators), MMA issue
-//   warps 2-9   bytes -> bf16 in shared memory, one stage after another;
-//               window w - 1 out of tensor memory while window w runs
+//   warp 0      x by TMA: 128 tokens x 128 features a stage (16 KB)
+//   warp 1      tensor memory (two window accumulators, a ring of M operands),
+//               MMA issue
+//   warps 2-17  bytes -> bf16, two groups on alternate stages, a lane quadrant
+//               and half of the tokens a warp; window w - 1 out of tensor
+//               memory while window w runs, a quarter of the columns a warp
+//   warp 18     the stage's 128 scales as bf16 factors in shared memory
+//   warp 19     dxa by TMA: 128 tokens x 64 columns a box (16 KB)
+// A hand-over through an mbarrier was measured at 230 cycles, and four of them
+// and a load from memory lie on the way of a stage, so each buffer is a ring of
+// its own that is freed as early as it can be: x once it is in registers, dxa
+// and the M operand when their MMAs are done.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -32,24 +46,34 @@
 
 namespace {
 
-constexpr int kTok = 64;                         // tokens per stage
-constexpr int kWin = 256;                        // tokens per window
-constexpr int kWorkers = 8;                      // conversion warps
-constexpr int kThreadsG = 64 + 32 * kWorkers;
-constexpr unsigned kRawBytes = kTok * 128;       // 8 KB of x
-constexpr unsigned kABytesG = kTok * 128 * 2;    // 16 KB of bf16: two halves of 64 features
-constexpr unsigned kBox = kTok * 128;            // 64 tokens x 64 columns of dxa
+constexpr int kTok = 128;                        // tokens per stage
+constexpr int kShortWin = 256, kLongWin = 512;   // tokens per window
+constexpr int kScaleWarp = 18;
+constexpr int kWorkers = 16;                     // conversion warps, in two groups that take alternate stages
+constexpr int kThreadsG = 128 + 32 * kWorkers;
+constexpr unsigned kRawBytes = kTok * 128;       // 16 KB of x
+constexpr unsigned kBox = kTok * 128;            // 128 tokens x 64 columns of dxa
 constexpr int kMaxR = 1024;
+constexpr int kMaxN = 192;                       // columns of a tile: two windows and the M operands fill tensor memory
 constexpr int kMaxCtasG = 256;
-constexpr int kMaxStagesG = 8;
+// Rings, by the columns of a tile: stages of x and of dxa in shared memory,
+// M operands in tensor memory (32 columns, half a stage of tokens) beside two
+// windows of the tile's columns
+struct Rings {
+  int x, d, ops;
+};
+__host__ __device__ constexpr Rings rings_of(int columns) {
+  return columns > 128 ? Rings{4, 3, 4} : columns > 64 ? Rings{4, 4, 8} : Rings{8, 4, 8};
+}
+constexpr int kOpTok = kTok / 2, kOpCols = kOpTok / 2;
+constexpr unsigned kFactorBytes = kTok * 2 + 16; // a stage's factors, and whether one is too large for bf16
 
 struct GradParams {
   int T, in, r;
   int mtiles, ntiles, windows;     // tiles are m fastest; windows per tile
+  int win;                         // tokens per window
   int ncols;                       // columns of r per tile (N of the MMA)
   int boxes;                       // dxa boxes per stage
-  int stages;
-  unsigned stage_bytes;
   int nsx;
   const uint8_t *scale;
   float *dA;
@@ -59,6 +83,27 @@ struct GradParams {
 
 // first unit of CTA i of n
 __host__ __device__ __forceinline__ int64_t first_unit(int64_t units, int i, int n) { return units * i / n; }
+
+// a unit's place: window w of tile (mt, nt).  Counted up unit by unit, as a
+// 64-bit division in every role's loop costs more than a stage of work
+struct Place {
+  int mt, nt, w;
+  __device__ __forceinline__ Place(const GradParams &p, int64_t u) {
+    const int tile = static_cast<int>(u / p.windows);
+    w = static_cast<int>(u - static_cast<int64_t>(tile) * p.windows);
+    nt = tile / p.mtiles;
+    mt = tile - nt * p.mtiles;
+  }
+  __device__ __forceinline__ void next(const GradParams &p) {
+    if (++w == p.windows) {
+      w = 0;
+      if (++mt == p.mtiles) {
+        mt = 0;
+        ++nt;
+      }
+    }
+  }
+};
 
 // shared-memory descriptor of an operand whose rows are k: 64 values (one
 // 128-byte swizzled row) of the M or N side, 8-row groups 1024 bytes apart,
@@ -72,45 +117,104 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
-// Four E4M3 bytes times the scale as bf16, in the order 0, 2, 1, 3.  The
-// exponent and mantissa bits of an E4M3 value, four places up in a bf16, are
-// that value times 2^-120 (subnormals too: their bits become a bf16
-// subnormal's), so one product with 2^120 scale finishes it, exactly.
-// `up` is that factor twice; it is a bf16 as long as the scale is at most 2^7
-__device__ __forceinline__ uint2 decode4(uint32_t w, uint32_t up) {
-  const uint32_t even = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
-  const uint32_t odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-  return make_uint2(mul_bf16x2(even, up), mul_bf16x2(odd, up));
+// Four E4M3 bytes (two features at two tokens) times the tokens' scales as
+// bf16 pairs: .x = bytes 0 and 2, .y = bytes 1 and 3.  The exponent and
+// mantissa bits of an E4M3 value, four places up in a bf16, are that value
+// times 2^-120 (subnormals too: their bits become a bf16 subnormal's), so one
+// product with 2^120 scale, with the value's sign, finishes it, exactly.  `up` holds the two tokens'
+// factors, which are bf16 as long as the scales are at most 2^7
+struct Mags {
+  uint32_t even, odd;
+};
+__device__ __forceinline__ Mags mags4(uint32_t w) { return {(w << 4) & 0x07f007f0u, (w >> 4) & 0x07f007f0u}; }
+__device__ __forceinline__ uint2 decode4(uint32_t w, Mags m, uint32_t up) {
+  return make_uint2(mul_bf16x2(m.even, ((w << 8) & 0x80008000u) ^ up), mul_bf16x2(m.odd, (w & 0x80008000u) ^ up));
 }
-// the same through fp32, for larger scales and for NaN bytes
-__device__ __noinline__ uint2 decode4_any(uint32_t w, uint32_t byte) {
-  const float s = scale_value(byte);
-  const float2 a = dequant2(w & 0xffffu, s), b = dequant2(w >> 16, s);
-  return make_uint2(pack_bf16x2(a.x, b.x), pack_bf16x2(a.y, b.y));
-}
-// feature of a tile at M row m: the order of decode4
-__device__ __forceinline__ int feature_of(int m) { return (m & ~3) | ((m & 1) << 1) | ((m >> 1) & 1); }
+// the largest magnitude so far in each half; 0x7f0 is a NaN byte's
+__device__ __forceinline__ uint32_t max_mag(uint32_t top, Mags m) { return __vimax3_u16x2(top, m.even, m.odd); }
+__device__ __forceinline__ bool has_nan(uint32_t top) { return (top & 0xffffu) == 0x07f0u || (top >> 16) == 0x07f0u; }
+constexpr uint32_t kMaxFast = 134;               // the scale byte of 2^7
+__device__ __forceinline__ uint32_t factor_of(uint32_t byte) { return (min(byte, kMaxFast) + 120u) << 7; }
+// feature of a tile at M row m: a 16 x 16 transposed load gives rows 0-7 the
+// even features and rows 8-15 the odd ones
+__device__ __forceinline__ int feature_of(int m) { return (m & ~15) | ((m & 7) << 1) | ((m >> 3) & 1); }
 
-// NC: columns of a tile per worker warp (half of the tile's, rounded up)
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 lanes x 16 columns of tensor memory: registers 0-3 the first 8 columns
+// (lane / 4 at columns 2 (lane % 4) and + 1, then the same of lane / 4 + 8)
+__device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// a warp's share of a stage through fp32, for larger scales and for NaN bytes.
+// The scales of tokens t0 + 16 g .. + 3 come from memory; out of line, and with
+// no arrays of the caller's, so that the common path keeps its registers
+__device__ __noinline__ void convert_any(const uint8_t *scale, int nsx, int T, int t0, uint32_t from0, uint32_t from1,
+                                         uint32_t to) {
+  uint32_t o[2][8];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    uint32_t raw[4];
+    ldmatrix_x4_trans(g ? from1 : from0, raw);
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 16 * g + i;
+      s[i] = scale_value(t < T ? __ldg(scale + static_cast<int64_t>(t) * nsx) : 127u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = i / 2, half = i % 2;
+      const float2 a = dequant2(raw[i] & 0xffffu, s[2 * half]), b = dequant2(raw[i] >> 16, s[2 * half + 1]);
+      o[h][4 * g + half] = pack_bf16x2(a.x, b.x);
+      o[h][4 * g + 2 + half] = pack_bf16x2(a.y, b.y);
+    }
+  }
+  tmem_st_16x256b_x2(to, o[0]);
+  tmem_st_16x256b_x2(to + (16u << 16), o[1]);
+}
+
+// NC: columns of a tile per worker warp (a quarter of the tile's, rounded up)
 template <int NC>
 __global__ void __launch_bounds__(kThreadsG, 1)
 lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mD, const GradParams p) {
-  constexpr int kN = 2 * NC;                             // columns of one window accumulator
-  constexpr int kCols = kN <= 16 ? 32 : kN <= 32 ? 64 : kN <= 64 ? 128 : kN <= 128 ? 256 : 512;
+  constexpr int kN = 4 * NC;                             // columns of one window accumulator
+  constexpr Rings kR = rings_of(kN);
+  constexpr int kUsed = 2 * kN + kOpCols * kR.ops;       // two windows, the M operands
+  constexpr int kCols = kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int S = p.stages;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + static_cast<size_t>(S) * p.stage_bytes);
-  // barriers: loaded[S], converted[S], free[S], window done[2], window read[2]
-  const uint32_t full0 = smem_u32(bars), conv0 = full0 + 8u * S, empty0 = conv0 + 8u * S, done0 = empty0 + 8u * S,
-                 read0 = done0 + 16, fin = read0 + 16;
-  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 3 * S + 5);
+  const uint32_t d_stage = p.boxes * kBox;
+  const uint32_t x_at = smem_u32(smem), d_at = x_at + kR.x * kRawBytes;
+  uint8_t *factors = smem + kR.x * kRawBytes + kR.d * d_stage;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(factors + kR.x * kFactorBytes);
+  // barriers: x loaded and free, dxa loaded and free, M operand written and
+  // consumed, window done[2] and read[2], the end
+  const uint32_t xfull = smem_u32(bars), xfree = xfull + 8u * kR.x, dfull = xfree + 8u * kR.x, dfree = dfull + 8u * kR.d,
+                 conv0 = dfree + 8u * kR.d, used0 = conv0 + 8u * kR.ops, done0 = used0 + 8u * kR.ops, read0 = done0 + 16,
+                 fin = read0 + 16;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * (kR.x + kR.d + kR.ops) + 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full0 + 8u * s, 1);
-      mbar_init(conv0 + 8u * s, kWorkers);
-      mbar_init(empty0 + 8u * s, 1);
+    for (int s = 0; s < kR.x; ++s) {
+      mbar_init(xfull + 8u * s, 2);               // the producer (and its bytes), the scale warp
+      mbar_init(xfree + 8u * s, kWorkers / 2);
+    }
+    for (int s = 0; s < kR.d; ++s) {
+      mbar_init(dfull + 8u * s, 1);
+      mbar_init(dfree + 8u * s, 1);
+    }
+    for (int s = 0; s < kR.ops; ++s) {
+      mbar_init(conv0 + 8u * s, kWorkers / 4);
+      mbar_init(used0 + 8u * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(done0 + 8u * b, 1);
@@ -131,105 +235,174 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  pdl_trigger();   // grad_join_kernel's launch overlaps this kernel; it waits for its end
   const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
-  const int64_t u0 = first_unit(units, blockIdx.x, gridDim.x), u1 = first_unit(units, blockIdx.x + 1, gridDim.x);
+  const int64_t u0 = first_unit(units, blockIdx.x, gridDim.x);
+  const int nu = static_cast<int>(first_unit(units, blockIdx.x + 1, gridDim.x) - u0);
+  Place at_unit(p, u0);
   // stages of a window
-  auto nstages = [&](int w) { return min(kWin, p.T - w * kWin + kTok - 1) / kTok; };
+  auto nstages = [&](int w) { return min(p.win, p.T - w * p.win + kTok - 1) / kTok; };
+  // use number i of a ring of n: wait until its place is filled, or free again
+  auto filled = [&](uint32_t bar, int i, int n, int code) {
+    return guard_wait(bar + 8u * (i % n), static_cast<uint32_t>(i / n) & 1u, ctl, p.guard, code);
+  };
+  auto freed = [&](uint32_t bar, int i, int n, int code) {
+    return guard_wait(bar + 8u * (i % n), (static_cast<uint32_t>(i / n) & 1u) ^ 1u, ctl, p.guard, code);
+  };
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- producer
-      bool ok = !loads_withheld(p.guard);
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int64_t u = u0; u < u1 && ok; ++u) {
-        const int tile = static_cast<int>(u / p.windows), w = static_cast<int>(u % p.windows);
-        const int mt = tile % p.mtiles, nt = tile / p.mtiles;
-        const int ns = nstages(w);
-        for (int k = 0; k < ns; ++k) {
-          if (!guard_wait(empty0 + 8u * stage, phase ^ 1u, ctl, p.guard, 31)) {
-            ok = false;
-            break;
+  if (warp == 0 || warp == kScaleWarp + 1) {
+    // ---------------------------------------------------------------- producers
+    const bool is_x = warp == 0;
+    bool ok = !loads_withheld(p.guard);
+    bool issued = false;
+    int c = 0;
+    for (int u = 0; u < nu && ok; ++u, at_unit.next(p)) {
+      const int f0 = at_unit.mt * kTcM, n0 = at_unit.nt * p.ncols, w = at_unit.w;
+      const int ns = nstages(w);
+      for (int k = 0; k < ns; ++k, ++c) {
+        ok = is_x ? freed(xfree, c, kR.x, 31) : freed(dfree, c, kR.d, 39);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int t0 = w * p.win + k * kTok;
+        if (is_x) {
+          const uint32_t fb = xfull + 8u * (c % kR.x);
+          if (elect_one()) {
+            mbar_expect_tx(fb, kRawBytes);
+            tma_load_2d(x_at + (c % kR.x) * kRawBytes, &mX, f0, t0, fb);
           }
-          const uint32_t fb = full0 + 8u * stage;
-          const uint32_t at = smem_u32(smem + static_cast<size_t>(stage) * p.stage_bytes);
-          const int t0 = w * kWin + k * kTok;
-          mbar_expect_tx(fb, kRawBytes + p.boxes * kBox);
-          tma_load_2d(at + kABytesG, &mX, mt * kTcM, t0, fb);
-          for (int b = 0; b < p.boxes; ++b)
-            tma_load_2d(at + kABytesG + kRawBytes + b * kBox, &mD, nt * p.ncols + 64 * b, t0, fb);
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+        } else {
+          const uint32_t fb = dfull + 8u * (c % kR.d), at = d_at + (c % kR.d) * d_stage;
+          if (elect_one()) {
+            mbar_expect_tx(fb, d_stage);
+#pragma unroll
+            for (int b = 0; b < (kN + 63) / 64; ++b)
+              if (b < p.boxes) tma_load_2d(at + b * kBox, &mD, n0 + 64 * b, t0, fb);
           }
         }
+        __syncwarp();
+        issued = true;
       }
-      if (!ok)
-        for (int k = 0; k < S && k < issued; ++k) {   // copies in flight
-          if (--stage < 0) {
-            stage = S - 1;
-            phase ^= 1u;
-          }
-          wait_drain_ns(full0 + 8u * stage, phase, kWaitNs);
-        }
+    }
+    if (!ok && issued) {
+      // copies may be in flight, and their barriers may also wait for a warp
+      // that has left: copies land within microseconds, wait 1 ms
+      const unsigned long long t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) {
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- MMA issuer
-      // bf16, fp32 accumulator, both operands transposed (M- and N-major)
-      const uint32_t idesc = idesc_bf16(p.ncols) | (1u << 15) | (1u << 16);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      int wi = 0;
-      for (int64_t u = u0; u < u1 && ok; ++u, ++wi) {
-        const int ns = nstages(static_cast<int>(u % p.windows));
-        const uint32_t d = tmem + static_cast<uint32_t>((wi & 1) * kN);
-        if (!guard_wait(read0 + 8u * (wi & 1), (static_cast<uint32_t>(wi >> 1) & 1u) ^ 1u, ctl, p.guard, 32)) break;
-        for (int k = 0; k < ns; ++k) {
-          if (!guard_wait(conv0 + 8u * stage, phase, ctl, p.guard, 33)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t at = smem_u32(smem + static_cast<size_t>(stage) * p.stage_bytes);
-          const uint32_t bt = at + kABytesG + kRawBytes;
+    // ---------------------------------------------------------------- MMA issuer
+    // bf16, fp32 accumulator, the N side N-major
+    const uint32_t idesc = idesc_bf16(p.ncols) | (1u << 16);
+    bool ok = true;
+    int c = 0;
+    for (int wi = 0; wi < nu && ok; ++wi, at_unit.next(p)) {
+      const int ns = nstages(at_unit.w);
+      const uint32_t d = tmem + static_cast<uint32_t>((wi & 1) * kN);
+      ok = freed(read0, wi, 2, 32);
+      for (int k = 0; k < ns && ok; ++k, ++c) {
+        ok = filled(dfull, c, kR.d, 36);
+        const uint64_t b = mn_desc(d_at + (c % kR.d) * d_stage, kBox);
 #pragma unroll
-          for (int j = 0; j < kTok / 16; ++j)   // 16 tokens: 16 rows of 128 bytes
-            mma_bf16_ss(d, mn_desc(at + 2048u * j, kABytesG / 2), mn_desc(bt + 2048u * j, kBox), idesc,
-                        k != 0 || j != 0 ? 1u : 0u);
-          mma_commit(empty0 + 8u * stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+        for (int h = 0; h < 2; ++h) {
+          const int i = 2 * c + h;
+          ok = ok && filled(conv0, i, kR.ops, 33);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = tmem + 2 * kN + static_cast<uint32_t>(kOpCols * (i % kR.ops));
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < kOpTok / 16; ++j)   // 16 tokens: 8 columns of the M operand, 16 rows of 128 bytes
+              mma_bf16_ta(d, a + 8u * j, b + 128u * (4 * h + j), idesc, k != 0 || h != 0 || j != 0 ? 1u : 0u);
+            mma_commit(used0 + 8u * (i % kR.ops));
+            if (h == 1) mma_commit(dfree + 8u * (c % kR.d));
+            if (h == 1 && k + 1 == ns) mma_commit(done0 + 8u * (wi & 1));
           }
+          __syncwarp();
         }
-        if (ok) mma_commit(done0 + 8u * (wi & 1));
       }
+    }
+    if (elect_one()) {
       mma_commit(fin);
       wait_drain_ns(fin, 0, kWaitNs);
     }
+    __syncwarp();
+  } else if (warp == kScaleWarp) {
+    // ---------------------------------------------------------------- scales
+    // four tokens a lane, requested kAhead stages before they are needed
+    // (one byte per token and tile: a sector each, often from memory)
+    constexpr int kAhead = 3;
+    uint32_t ring[kAhead][kTok / 32];
+    Place from = at_unit;   // of the stage that is requested next: stage fk of unit fu
+    int fk = 0, fu = 0;
+    auto fetch = [&](uint32_t (&dst)[kTok / 32]) {
+      const uint8_t *sp = p.scale + from.mt;
+#pragma unroll
+      for (int i = 0; i < kTok / 32; ++i) {
+        const int t = from.w * p.win + fk * kTok + 32 * i + lane;
+        dst[i] = 127u;
+        if (fu < nu && t < p.T)
+          // not moved down to its use by the compiler
+          asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(dst[i]) : "l"(sp + static_cast<int64_t>(t) * p.nsx));
+      }
+      if (++fk == nstages(from.w)) {
+        fk = 0;
+        ++fu;
+        from.next(p);
+      }
+    };
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) fetch(ring[a]);
+    int total = 0;
+    for (int u = 0; u < nu; ++u, at_unit.next(p)) total += nstages(at_unit.w);
+    bool ok = true;
+    for (int c0 = 0; c0 < total && ok; c0 += kAhead) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int c = c0 + a;
+        if (c >= total || !ok) continue;
+        uint32_t b[kTok / 32];
+#pragma unroll
+        for (int i = 0; i < kTok / 32; ++i) b[i] = ring[a][i];
+        fetch(ring[a]);
+        ok = freed(xfree, c, kR.x, 37);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        uint16_t *dst = reinterpret_cast<uint16_t *>(factors + c % kR.x * kFactorBytes);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kTok / 32; ++i) {
+          dst[32 * i + lane] = static_cast<uint16_t>(factor_of(b[i]));
+          top = max(top, b[i]);
+        }
+        const bool large = __any_sync(0xffffffffu, top > kMaxFast);
+        if (lane == 0) *reinterpret_cast<uint32_t *>(dst + kTok) = large ? 1u : 0u;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xfull + 8u * (c % kR.x));
+      }
+    }
   } else {
     // ---------------------------------------------------------------- workers
-    const int wk = warp - 2, tid = threadIdx.x - 64;
+    const int wk = warp - 2;
     const uint32_t quad = static_cast<uint32_t>(warp & 3);
-    const int nh = wk >> 2;                              // which half of the columns
-    const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(nh * NC);
-    constexpr int C = NC % 32 == 0 ? 32 : NC % 16 == 0 ? 16 : 8;
+    const int nq = wk >> 2;                              // which quarter of the columns
+    const int grp = wk >> 3, nh = nq & 1;                // which stages, which half of their tokens
+    const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(nq * NC);
+    constexpr int C = NC % 32 == 0 ? 32 : NC % 16 == 0 ? 16 : NC % 8 == 0 ? 8 : 4;
     float sum[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
-    // this thread's pieces of a stage: 16 features of rows `row` and row + 32
-    const int row = tid >> 3, ch = tid & 7;
-    const uint32_t half = static_cast<uint32_t>(ch >> 2) * (kABytesG / 2);
-    const uint32_t first = static_cast<uint32_t>(ch >> 2);   // the halves write their two 16-byte chunks in opposite order
-    int stage = 0;
-    uint32_t phase = 0;
+    // this lane's row of a transposed load: lanes 0-7 and 8-15 give the rows of
+    // tokens 4 i, 4 i + 1 and 4 i + 2, 4 i + 3 (i < 4) of 16 features, lanes
+    // 16-31 the same of the next 16 features
+    const int tok = 64 * nh + 4 * ((lane & 7) >> 1) + (lane & 1) + 2 * ((lane >> 3) & 1);
+    const int chunk = 2 * static_cast<int>(quad) + (lane >> 4);
+    const uint32_t from_off = static_cast<uint32_t>(tok * 128 + ((chunk ^ (tok & 7)) << 4));
+    int c = 0;
     bool ok = true;
-    int wi = 0;
     auto flush = [&](int k) {   // window number k of this CTA into `sum`
-      const bool got = guard_wait(done0 + 8u * (k & 1), static_cast<uint32_t>(k >> 1) & 1u, ctl, p.guard, 34);
+      const bool got = filled(done0, k, 2, 34);
       if (!__all_sync(0xffffffffu, got)) return false;
       tc_fence_after();
 #pragma unroll
@@ -245,69 +418,72 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       return true;
     };
     int seg0 = 0;   // first window of the current run within one tile
-    for (int64_t u = u0; u < u1 && ok; ++u, ++wi) {
-      const int tile = static_cast<int>(u / p.windows), w = static_cast<int>(u % p.windows);
-      const int mt = tile % p.mtiles, nt = tile / p.mtiles;
+    for (int wi = 0; wi < nu && ok; ++wi, at_unit.next(p)) {
+      const int mt = at_unit.mt, nt = at_unit.nt, w = at_unit.w;
       const int ns = nstages(w);
-      const uint8_t *sp = p.scale + mt;
-      auto scale_at = [&](int t) {
-        return t < p.T ? static_cast<uint32_t>(__ldg(sp + static_cast<int64_t>(t) * p.nsx)) : 127u;
-      };
-      uint32_t b0 = scale_at(w * kWin + row), b1 = scale_at(w * kWin + row + 32);
-      for (int k = 0; k < ns; ++k) {
-        const uint32_t c0 = b0, c1 = b1;
-        if (k + 1 < ns) {
-          b0 = scale_at(w * kWin + (k + 1) * kTok + row);
-          b1 = scale_at(w * kWin + (k + 1) * kTok + row + 32);
-        }
-        const bool got = guard_wait(full0 + 8u * stage, phase, ctl, p.guard, 35);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
-        uint8_t *at = smem + static_cast<size_t>(stage) * p.stage_bytes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int rr = row + 32 * h;
-          const uint32_t byte = h ? c1 : c0;
-          const uint4 raw = *reinterpret_cast<const uint4 *>(at + kABytesG + rr * 128 + ((ch ^ (rr & 7)) << 4));
-          const uint32_t in4[4] = {raw.x, raw.y, raw.z, raw.w};
-          uint2 o[4];
-          // a byte of 0x7f in any sign
-          uint32_t nan = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) nan |= (in4[i] & 0x7f7f7f7fu) + 0x01010101u;
-          if ((nan & 0x80808080u) == 0 && byte <= 134) {
-            const uint32_t e = (byte + 120u) << 7;          // 2^(byte - 7) in bf16
-            const uint32_t up = e | (e << 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = decode4(in4[i], up);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = decode4_any(in4[i], byte);
+      for (int k = 0; k < ns; ++k, ++c) {
+        if ((c & 1) == grp) {
+          bool got = filled(xfull, c, kR.x, 35);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
           }
-          uint8_t *dst = at + half + rr * 128;
-          const uint32_t ca = 2u * (ch & 3);
-          const uint4 lo = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y), hi = make_uint4(o[2].x, o[2].y, o[3].x, o[3].y);
-          const uint32_t x = static_cast<uint32_t>(rr & 7);
-          *reinterpret_cast<uint4 *>(dst + (((ca + first) ^ x) << 4)) = first ? hi : lo;
-          *reinterpret_cast<uint4 *>(dst + (((ca + 1 - first) ^ x) << 4)) = first ? lo : hi;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(conv0 + 8u * stage);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
+          const uint32_t from = x_at + (c % kR.x) * kRawBytes + from_off;
+          const uint8_t *fa = factors + c % kR.x * kFactorBytes;
+          const bool large = *reinterpret_cast<const uint32_t *>(fa + 2 * kTok) != 0;
+          const int op = 2 * c + nh;
+          const uint32_t to = tmem + ((quad * 32u) << 16) + 2 * kN + static_cast<uint32_t>(kOpCols * (op % kR.ops));
+          // this warp's half of the tokens, 32 at a time, as 16 x 16 blocks
+#pragma unroll
+          for (int g2 = 0; g2 < 2; ++g2) {
+            uint32_t raw[2][4], o[2][8];   // o[h]: the 16 columns of feature block h
+            uint32_t top = 0;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) ldmatrix_x4_trans(from + 2048u * (2 * g2 + g), raw[g]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const uint2 up = *reinterpret_cast<const uint2 *>(fa + 2 * (64 * nh + 16 * (2 * g2 + g) + 4 * (lane & 3)));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int h = i / 2, half = i % 2;
+                const Mags m = mags4(raw[g][i]);
+                top = max_mag(top, m);
+                const uint2 d = decode4(raw[g][i], m, half ? up.y : up.x);
+                o[h][4 * g + half] = d.x;
+                o[h][4 * g + 2 + half] = d.y;
+              }
+            }
+            if (g2 == 0) {
+              got = freed(used0, op, kR.ops, 38);
+              if (!__all_sync(0xffffffffu, got)) break;
+              tc_fence_after();
+            }
+            if (!__any_sync(0xffffffffu, large || has_nan(top))) {
+              tmem_st_16x256b_x2(to + 16u * g2, o[0]);
+              tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
+            } else {
+              convert_any(p.scale + mt, p.nsx, p.T, w * p.win + k * kTok + 64 * nh + 32 * g2 + 4 * (lane & 3),
+                          from + 4096u * g2, from + 4096u * g2 + 2048u, to + 16u * g2);
+            }
+          }
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive(xfree + 8u * (c % kR.x));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(conv0 + 8u * (op % kR.ops));
         }
         // the window before this one, once this one keeps the tensor core fed
-        if (k == min(2, ns - 1) && wi > seg0 && !flush(wi - 1)) {
+        if (k == min(1, ns - 1) && wi > seg0 && !flush(wi - 1)) {
           ok = false;
           break;
         }
       }
       if (!ok) break;
-      if (w + 1 == p.windows || u + 1 == u1) {
+      if (w + 1 == p.windows || wi + 1 == nu) {
         // the end of this CTA's run of the tile
         if (!flush(wi)) break;
         const bool whole = w + 1 == p.windows && wi - seg0 + 1 == p.windows;
@@ -317,7 +493,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
           const int f = mt * kTcM + feature_of(m);
 #pragma unroll
           for (int j = 0; j < NC; ++j) {
-            const int n = nh * NC + j, col = nt * p.ncols + n;
+            const int n = nq * NC + j, col = nt * p.ncols + n;
             if (n < p.ncols && col < p.r && f < p.in) p.dA[static_cast<int64_t>(col) * p.in + f] = sum[j];
           }
         } else {
@@ -325,7 +501,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
           float *dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (from_start ? 1 : 0)) * p.ncols * kTcM + m;
 #pragma unroll
           for (int j = 0; j < NC; ++j)
-            if (nh * NC + j < p.ncols) dst[(nh * NC + j) * kTcM] = sum[j];
+            if (nq * NC + j < p.ncols) dst[(nq * NC + j) * kTcM] = sum[j];
         }
 #pragma unroll
         for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
@@ -343,53 +519,75 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
 }
 
 // dA of the tiles that more than one CTA worked on: their parts in CTA order.
-// One block: one tile, 8 of its columns
+// One block: one tile, kJoin of its columns
+constexpr int kJoin = 16;
 __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p, int ctas) {
-  const int chunks = (p.ncols + 7) / 8;
+  __shared__ int owners[2];
+  pdl_wait();
+  const int chunks = (p.ncols + kJoin - 1) / kJoin;
   const int tile = blockIdx.x / chunks;
-  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
-  // the CTA that holds a unit: first_unit(i) <= unit < first_unit(i + 1)
-  auto owner = [&](int64_t unit) {
+  if (threadIdx.x < 2) {
+    // the CTA of the tile's first and of its last unit: first_unit(i) <= unit < first_unit(i + 1)
+    const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
+    const int64_t unit = static_cast<int64_t>(tile + static_cast<int>(threadIdx.x)) * p.windows - threadIdx.x;
     int i = static_cast<int>(unit * ctas / units);
     while (first_unit(units, i + 1, ctas) <= unit) ++i;
-    while (first_unit(units, i, ctas) > unit) --i;
-    return i;
-  };
-  const int i0 = owner(static_cast<int64_t>(tile) * p.windows), i1 = owner(static_cast<int64_t>(tile + 1) * p.windows - 1);
+    owners[threadIdx.x] = i;
+  }
+  __syncthreads();
+  const int i0 = owners[0], i1 = owners[1];
   if (i0 == i1) return;
   const int mt = tile % p.mtiles, nt = tile / p.mtiles;
   const int m = threadIdx.x % kTcM, f = mt * kTcM + feature_of(m);
+  const int n0 = (blockIdx.x % chunks) * kJoin + threadIdx.x / kTcM;
+  const int64_t slot = static_cast<int64_t>(p.ncols) * kTcM;
+  const float *src = p.part + static_cast<int64_t>(n0) * kTcM + m;
+  if (f >= p.in) return;
+  float s[kJoin / 2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int n = (blockIdx.x % chunks) * 8 + 2 * j + threadIdx.x / kTcM, col = nt * p.ncols + n;
-    if (n >= p.ncols || col >= p.r || f >= p.in) continue;
-    const int64_t at = static_cast<int64_t>(n) * kTcM + m, slot = static_cast<int64_t>(p.ncols) * kTcM;
-    float s = p.part[(static_cast<int64_t>(i0) * 2 + 1) * slot + at];
-    for (int i = i0 + 1; i <= i1; ++i) s += p.part[static_cast<int64_t>(i) * 2 * slot + at];
-    p.dA[static_cast<int64_t>(col) * p.in + f] = s;
+  for (int j = 0; j < kJoin / 2; ++j)
+    s[j] = n0 + 2 * j < p.ncols ? src[(static_cast<int64_t>(i0) * 2 + 1) * slot + 2 * j * kTcM] : 0.0f;
+  for (int i = i0 + 1; i <= i1; ++i)
+#pragma unroll
+    for (int j = 0; j < kJoin / 2; ++j)
+      if (n0 + 2 * j < p.ncols) s[j] += src[static_cast<int64_t>(i) * 2 * slot + 2 * j * kTcM];
+#pragma unroll
+  for (int j = 0; j < kJoin / 2; ++j) {
+    const int n = n0 + 2 * j, col = nt * p.ncols + n;
+    if (n < p.ncols && col < p.r) p.dA[static_cast<int64_t>(col) * p.in + f] = s[j];
   }
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// columns of r per tile: as few tiles as hold it at 256 each, of equal width
+// columns of r per tile: as few tiles as hold it at kMaxN each, of equal width
 int tile_columns(int64_t r) {
-  const int64_t tiles = dora::ceil_div(r, 256);
+  const int64_t tiles = dora::ceil_div(r, kMaxN);
   return static_cast<int>(dora::round_up(dora::ceil_div(r, tiles), 16));
 }
 
 template <int NC>
 dora_status launch_grad(const CUtensorMap &mX, const CUtensorMap &mD, GradParams p, int ctas, cudaStream_t cs) {
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + 512;
+  constexpr Rings kR = rings_of(4 * NC);
+  const size_t smem = 1024 + kR.x * (kRawBytes + kFactorBytes) + static_cast<size_t>(kR.d) * p.boxes * kBox + 512;
   lora_grad_kernel<NC><<<static_cast<unsigned>(ctas), kThreadsG, smem, cs>>>(mX, mD, p);
   dora::count_launches(1);
   if (cudaGetLastError() != cudaSuccess) return DORA_ERR_CUDA;
   // no tile is cut when every CTA's run is a whole number of tiles
   const int64_t tiles = static_cast<int64_t>(p.mtiles) * p.ntiles;
   if (tiles % ctas != 0) {
-    const int64_t blocks = tiles * dora::ceil_div(p.ncols, 8);
-    grad_join_kernel<<<static_cast<unsigned>(blocks), 256, 0, cs>>>(p, ctas);
+    // its launch overlaps the end of the first kernel
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * dora::ceil_div(p.ncols, kJoin)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = cs;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, grad_join_kernel, p, ctas) != cudaSuccess) return DORA_ERR_CUDA;
     dora::count_launches(1);
   }
   return dora::launch_status();
@@ -401,7 +599,7 @@ extern "C" size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r) 
   if (bad_size(T, 0) || bad_size(in, 0) || r < 1 || r > kMaxR) return 0;
   if (T == 0 || in == 0) return 256;
   // two parts per CTA, for up to kMaxCtasG CTAs
-  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, tile_columns(r)) * dora::ceil_div(T, kWin);
+  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, tile_columns(r)) * dora::ceil_div(T, kShortWin);
   const int64_t ctas = units < kMaxCtasG ? units : kMaxCtasG;
   return static_cast<size_t>(2 * ctas) * tile_columns(r) * kTcM * sizeof(float);
 }
@@ -427,9 +625,8 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
                                                                                                   : DORA_ERR_CUDA;
   GradParams p = {};
   static const void *const kernels[] = {
-      (const void *)lora_grad_kernel<8>,  (const void *)lora_grad_kernel<16>, (const void *)lora_grad_kernel<32>,
-      (const void *)lora_grad_kernel<48>, (const void *)lora_grad_kernel<64>, (const void *)lora_grad_kernel<96>,
-      (const void *)lora_grad_kernel<128>};
+      (const void *)lora_grad_kernel<4>, (const void *)lora_grad_kernel<8>, (const void *)lora_grad_kernel<16>,
+      (const void *)lora_grad_kernel<32>, (const void *)lora_grad_kernel<48>};
   st = tc_init(device, &p.guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
   if (st != DORA_OK) return st;
   p.T = static_cast<int>(T);
@@ -439,10 +636,10 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   p.boxes = static_cast<int>(dora::ceil_div(p.ncols, 64));
   p.mtiles = static_cast<int>(dora::ceil_div(in, kTcM));
   p.ntiles = static_cast<int>(dora::ceil_div(r, p.ncols));
-  p.windows = static_cast<int>(dora::ceil_div(T, kWin));
-  p.stage_bytes = kABytesG + kRawBytes + p.boxes * kBox;
-  p.stages = static_cast<int>((kSmemMax - 1536) / p.stage_bytes);
-  if (p.stages > kMaxStagesG) p.stages = kMaxStagesG;
+  // short windows spread a small problem more evenly, long ones are read out
+  // half as often: those where every CTA has at least 8 of them
+  p.win = static_cast<int64_t>(p.mtiles) * p.ntiles * dora::ceil_div(T, kLongWin) >= 8 * info.sms ? kLongWin : kShortWin;
+  p.windows = static_cast<int>(dora::ceil_div(T, p.win));
   p.nsx = static_cast<int>(dora::ceil_div(in, kQBlock));
   p.scale = static_cast<const uint8_t *>(xscale);
   p.dA = dA;
@@ -452,12 +649,10 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
   const int sms = info.sms < kMaxCtasG ? info.sms : kMaxCtasG;
   const int ctas = units < sms ? static_cast<int>(units) : sms;
-  const int half = p.ncols / 2;
-  if (half <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
-  if (half <= 16) return launch_grad<16>(mX, mD, p, ctas, cs);
-  if (half <= 32) return launch_grad<32>(mX, mD, p, ctas, cs);
-  if (half <= 48) return launch_grad<48>(mX, mD, p, ctas, cs);
-  if (half <= 64) return launch_grad<64>(mX, mD, p, ctas, cs);
-  if (half <= 96) return launch_grad<96>(mX, mD, p, ctas, cs);
-  return launch_grad<128>(mX, mD, p, ctas, cs);
+  const int quarter = p.ncols / 4;
+  if (quarter <= 4) return launch_grad<4>(mX, mD, p, ctas, cs);
+  if (quarter <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
+  if (quarter <= 16) return launch_grad<16>(mX, mD, p, ctas, cs);
+  if (quarter <= 32) return launch_grad<32>(mX, mD, p, ctas, cs);
+  return launch_grad<48>(mX, mD, p, ctas, cs);
 }

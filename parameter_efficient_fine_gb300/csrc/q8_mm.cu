@@ -162,67 +162,73 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- producer
-      ok = !loads_withheld(p.guard);
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1 && ok; ++kb) {
-        if (!guard_wait(empty0 + 8u * stage, phase ^ 1u, ctl, p.guard, 21)) {
-          ok = false;
-          break;
-        }
-        const uint32_t fb = full0 + 8u * stage;
-        const uint32_t at = smem_u32(smem + static_cast<size_t>(stage) * kStage);
+    // ---------------------------------------------------------------- producer
+    ok = !loads_withheld(p.guard);
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1 && ok; ++kb) {
+      ok = guard_wait(empty0 + 8u * stage, phase ^ 1u, ctl, p.guard, 21);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t fb = full0 + 8u * stage;
+      const uint32_t at = smem_u32(smem) + static_cast<uint32_t>(stage) * kStage;
+      if (elect_one()) {
         mbar_expect_tx(fb, kStage);
         if (TRANS) tma_load_2d(at, &mW, mt * kTcM, kb * kKB, fb);
         else tma_load_2d(at, &mW, kb * kKB, mt * kTcM, fb);
         tma_load_2d(at + kWBytes, &mX, kb * kKB, nt * NT, fb);
-        ++issued;
-        if (++stage == S) {
-          stage = 0;
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok)
+      for (int k = 0; k < S && k < issued; ++k) {   // copies in flight
+        if (--stage < 0) {
+          stage = S - 1;
           phase ^= 1u;
         }
+        wait_drain_ns(full0 + 8u * stage, phase, kWaitNs);
       }
-      if (!ok)
-        for (int k = 0; k < S && k < issued; ++k) {   // copies in flight
-          if (--stage < 0) {
-            stage = S - 1;
-            phase ^= 1u;
-          }
-          wait_drain_ns(full0 + 8u * stage, phase, kWaitNs);
-        }
-    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- MMA issuer
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int grp = kb / 4 - kb0 / 4, slot = grp % kSfSlots;
-        if (kb == kb0 || kb % 4 == 0) {
-          if (!guard_wait(sff0 + 8u * slot, static_cast<uint32_t>(grp / kSfSlots) & 1u, ctl, p.guard, 22)) break;
-        }
-        if (!guard_wait(full0 + 8u * stage, phase, ctl, p.guard, 23)) break;
-        tc_fence_after();
-        const uint32_t at = smem_u32(smem + static_cast<size_t>(stage) * kStage);
-        const uint32_t idesc = idesc_q8(kTcM, NT, static_cast<uint32_t>(kb & 3), TRANS);
-        const uint32_t sf = tmem + kSfCol + 8u * slot;
+    // ---------------------------------------------------------------- MMA issuer
+    int stage = 0;
+    uint32_t phase = 0;
+    bool up = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int grp = kb / 4 - kb0 / 4, slot = grp % kSfSlots;
+      if (kb == kb0 || kb % 4 == 0)
+        up = guard_wait(sff0 + 8u * slot, static_cast<uint32_t>(grp / kSfSlots) & 1u, ctl, p.guard, 22);
+      up = up && guard_wait(full0 + 8u * stage, phase, ctl, p.guard, 23);
+      if (!__all_sync(0xffffffffu, up)) break;
+      tc_fence_after();
+      const uint32_t at = smem_u32(smem) + static_cast<uint32_t>(stage) * kStage;
+      const uint64_t a = sdesc<32>(at), b = sdesc<32>(at + kWBytes);
+      const uint32_t idesc = idesc_q8(kTcM, NT, static_cast<uint32_t>(kb & 3), TRANS);
+      const uint32_t sf = tmem + kSfCol + 8u * slot;
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           // 32 k: 32 bytes along a K-major row; 32 rows of 128 bytes M-major
-          mma_q8(tmem, sdesc<32>(at + (TRANS ? 4096u : 32u) * k), sdesc<32>(at + kWBytes + 32u * k), idesc, sf, sf + 4,
-                 kb != kb0 || k != 0 ? 1u : 0u);
+          // (descriptors count 16 bytes)
+          mma_q8(tmem, a + (TRANS ? 256u : 2u) * k, b + 2u * k, idesc, sf, sf + 4, kb != kb0 || k != 0 ? 1u : 0u);
         mma_commit(empty0 + 8u * stage);
         if (kb % 4 == 3) mma_commit(sfe0 + 8u * slot);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
+      __syncwarp();
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (elect_one()) {
       mma_commit(accf);
       wait_drain_ns(accf, 0, kWaitNs);   // every MMA issued is done before this CTA's memory is given back
     }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------------- scales
     const uint32_t quad = static_cast<uint32_t>(warp & 3);

@@ -24,12 +24,28 @@ struct Guard {
   const unsigned long long *limit_ns;
 };
 
+// bounded wait.  The clock that bounds it is slow to read (hundreds of cycles),
+// so it is started only after a few tries
 __device__ __forceinline__ bool guard_wait(uint32_t bar, uint32_t parity, SharedCtl *ctl, const Guard &g, int code) {
-  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   return wait_bounded_ns(bar, parity, ctl, g.err, code, *reinterpret_cast<const volatile unsigned long long *>(g.limit_ns));
 }
 __device__ __forceinline__ bool loads_withheld(const Guard &g) {
   return *reinterpret_cast<const volatile int *>(g.stall) != 0;
+}
+
+// one lane of a converged warp.  The MMA warp runs its loop as a whole and
+// issues under this, so the operands of its instructions stay warp-uniform
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // C consecutive fp32 columns of this thread's tensor-memory lane
@@ -58,6 +74,18 @@ template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, float (&v
       : "memory");
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // bytes [rows, cols] (cols a multiple of 16) with a [box_rows x 128] box, 128-byte swizzle
