@@ -23,14 +23,14 @@
 // tiles.  A CTA that has a whole tile writes dA; otherwise it writes its part
 // to the workspace and grad_join_kernel adds the parts of a tile in order
 // (bitwise reproducible).
-//   warp 0      x by TMA: 128 tokens x 128 features a stage (16 KB)
+//   warp 0      x by TMA: 128 tokens x 128 features a stage (16 KB), and the
+//               stage's 128 scales as bf16 factors in shared memory
 //   warp 1      tensor memory (two window accumulators, a ring of M operands),
 //               MMA issue
 //   warps 2-17  bytes -> bf16, two groups on alternate stages, a lane quadrant
 //               and half of the tokens a warp; window w - 1 out of tensor
 //               memory while window w runs, a quarter of the columns a warp
-//   warp 18     the stage's 128 scales as bf16 factors in shared memory
-//   warp 19     dxa by TMA: 128 tokens x 64 columns a box (16 KB)
+//   warp 18     dxa by TMA: 128 tokens x 64 columns a box (16 KB)
 // A hand-over through an mbarrier was measured at 230 cycles, and four of them
 // and a load from memory lie on the way of a stage, so each buffer is a ring of
 // its own that is freed as early as it can be: x once it is in registers, dxa
@@ -48,24 +48,35 @@ namespace {
 
 constexpr int kTok = 128;                        // tokens per stage
 constexpr int kShortWin = 256, kLongWin = 512;   // tokens per window
-constexpr int kScaleWarp = 18;
 constexpr int kWorkers = 16;                     // conversion warps, in two groups that take alternate stages
-constexpr int kThreadsG = 128 + 32 * kWorkers;
+constexpr int kThreadsG = 96 + 32 * kWorkers;
 constexpr unsigned kRawBytes = kTok * 128;       // 16 KB of x
 constexpr unsigned kBox = kTok * 128;            // 128 tokens x 64 columns of dxa
 constexpr int kMaxR = 1024;
 constexpr int kMaxN = 192;                       // columns of a tile: two windows and the M operands fill tensor memory
 constexpr int kMaxCtasG = 256;
 // Rings, by the columns of a tile: stages of x and of dxa in shared memory,
-// M operands in tensor memory (32 columns, half a stage of tokens) beside two
-// windows of the tile's columns
+// M operands (64 columns) in tensor memory beside two windows of the tile's
+// columns.  x and the operands in even numbers, as two groups take turns
 struct Rings {
   int x, d, ops;
 };
 __host__ __device__ constexpr Rings rings_of(int columns) {
-  return columns > 128 ? Rings{4, 3, 4} : columns > 64 ? Rings{4, 4, 8} : Rings{8, 4, 8};
+  return columns > 128 ? Rings{4, 3, 2} : columns > 64 ? Rings{4, 4, 4} : Rings{8, 4, 4};
 }
-constexpr int kOpTok = kTok / 2, kOpCols = kOpTok / 2;
+constexpr int kOpCols = kTok / 2;
+// a place in a ring of N
+template <int N> struct At {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int by = 1) {
+    i += by;
+    if (i >= N) {
+      i -= N;
+      phase ^= 1u;
+    }
+  }
+};
 constexpr unsigned kFactorBytes = kTok * 2 + 16; // a stage's factors, and whether one is too large for bf16
 
 struct GradParams {
@@ -205,7 +216,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kR.x; ++s) {
-      mbar_init(xfull + 8u * s, 2);               // the producer (and its bytes), the scale warp
+      mbar_init(xfull + 8u * s, 2);               // the copy (and its bytes), the factors
       mbar_init(xfree + 8u * s, kWorkers / 2);
     }
     for (int s = 0; s < kR.d; ++s) {
@@ -213,7 +224,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       mbar_init(dfree + 8u * s, 1);
     }
     for (int s = 0; s < kR.ops; ++s) {
-      mbar_init(conv0 + 8u * s, kWorkers / 4);
+      mbar_init(conv0 + 8u * s, kWorkers / 2);
       mbar_init(used0 + 8u * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -242,100 +253,23 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
   Place at_unit(p, u0);
   // stages of a window
   auto nstages = [&](int w) { return min(p.win, p.T - w * p.win + kTok - 1) / kTok; };
-  // use number i of a ring of n: wait until its place is filled, or free again
-  auto filled = [&](uint32_t bar, int i, int n, int code) {
-    return guard_wait(bar + 8u * (i % n), static_cast<uint32_t>(i / n) & 1u, ctl, p.guard, code);
-  };
-  auto freed = [&](uint32_t bar, int i, int n, int code) {
-    return guard_wait(bar + 8u * (i % n), (static_cast<uint32_t>(i / n) & 1u) ^ 1u, ctl, p.guard, code);
+
+  // a producer that gives up leaves copies in flight, whose barriers may also
+  // wait for others that have left: they land within microseconds, wait 1 ms
+  auto settle_copies = [] {
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 1000000ull) {
+    }
   };
 
-  if (warp == 0 || warp == kScaleWarp + 1) {
-    // ---------------------------------------------------------------- producers
-    const bool is_x = warp == 0;
-    bool ok = !loads_withheld(p.guard);
-    bool issued = false;
-    int c = 0;
-    for (int u = 0; u < nu && ok; ++u, at_unit.next(p)) {
-      const int f0 = at_unit.mt * kTcM, n0 = at_unit.nt * p.ncols, w = at_unit.w;
-      const int ns = nstages(w);
-      for (int k = 0; k < ns; ++k, ++c) {
-        ok = is_x ? freed(xfree, c, kR.x, 31) : freed(dfree, c, kR.d, 39);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int t0 = w * p.win + k * kTok;
-        if (is_x) {
-          const uint32_t fb = xfull + 8u * (c % kR.x);
-          if (elect_one()) {
-            mbar_expect_tx(fb, kRawBytes);
-            tma_load_2d(x_at + (c % kR.x) * kRawBytes, &mX, f0, t0, fb);
-          }
-        } else {
-          const uint32_t fb = dfull + 8u * (c % kR.d), at = d_at + (c % kR.d) * d_stage;
-          if (elect_one()) {
-            mbar_expect_tx(fb, d_stage);
-#pragma unroll
-            for (int b = 0; b < (kN + 63) / 64; ++b)
-              if (b < p.boxes) tma_load_2d(at + b * kBox, &mD, n0 + 64 * b, t0, fb);
-          }
-        }
-        __syncwarp();
-        issued = true;
-      }
-    }
-    if (!ok && issued) {
-      // copies may be in flight, and their barriers may also wait for a warp
-      // that has left: copies land within microseconds, wait 1 ms
-      const unsigned long long t0 = globaltimer();
-      while (globaltimer() - t0 < 1000000ull) {
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    // bf16, fp32 accumulator, the N side N-major
-    const uint32_t idesc = idesc_bf16(p.ncols) | (1u << 16);
-    bool ok = true;
-    int c = 0;
-    for (int wi = 0; wi < nu && ok; ++wi, at_unit.next(p)) {
-      const int ns = nstages(at_unit.w);
-      const uint32_t d = tmem + static_cast<uint32_t>((wi & 1) * kN);
-      ok = freed(read0, wi, 2, 32);
-      for (int k = 0; k < ns && ok; ++k, ++c) {
-        ok = filled(dfull, c, kR.d, 36);
-        const uint64_t b = mn_desc(d_at + (c % kR.d) * d_stage, kBox);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = 2 * c + h;
-          ok = ok && filled(conv0, i, kR.ops, 33);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = tmem + 2 * kN + static_cast<uint32_t>(kOpCols * (i % kR.ops));
-          if (elect_one()) {
-#pragma unroll
-            for (int j = 0; j < kOpTok / 16; ++j)   // 16 tokens: 8 columns of the M operand, 16 rows of 128 bytes
-              mma_bf16_ta(d, a + 8u * j, b + 128u * (4 * h + j), idesc, k != 0 || h != 0 || j != 0 ? 1u : 0u);
-            mma_commit(used0 + 8u * (i % kR.ops));
-            if (h == 1) mma_commit(dfree + 8u * (c % kR.d));
-            if (h == 1 && k + 1 == ns) mma_commit(done0 + 8u * (wi & 1));
-          }
-          __syncwarp();
-        }
-      }
-    }
-    if (elect_one()) {
-      mma_commit(fin);
-      wait_drain_ns(fin, 0, kWaitNs);
-    }
-    __syncwarp();
-  } else if (warp == kScaleWarp) {
-    // ---------------------------------------------------------------- scales
-    // four tokens a lane, requested kAhead stages before they are needed
-    // (one byte per token and tile: a sector each, often from memory)
+  if (warp == 0) {
+    // ---------------------------------------------------------------- x
+    // the scales, four tokens a lane, are requested kAhead stages before they
+    // are needed (one byte per token and tile: a sector each, often from memory)
     constexpr int kAhead = 3;
     uint32_t ring[kAhead][kTok / 32];
-    Place from = at_unit;   // of the stage that is requested next: stage fk of unit fu
-    int fk = 0, fu = 0;
+    Place from = at_unit;   // of the stage whose scales are requested next: stage fk of unit fu
+    int fk = 0, fu = 0, fns = nstages(from.w);
     auto fetch = [&](uint32_t (&dst)[kTok / 32]) {
       const uint8_t *sp = p.scale + from.mt;
 #pragma unroll
@@ -343,45 +277,123 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
         const int t = from.w * p.win + fk * kTok + 32 * i + lane;
         dst[i] = 127u;
         if (fu < nu && t < p.T)
-          // not moved down to its use by the compiler
+          // volatile: not moved down to its use by the compiler
           asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(dst[i]) : "l"(sp + static_cast<int64_t>(t) * p.nsx));
       }
-      if (++fk == nstages(from.w)) {
+      if (++fk == fns) {
         fk = 0;
         ++fu;
         from.next(p);
+        fns = nstages(from.w);
       }
     };
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) fetch(ring[a]);
-    int total = 0;
-    for (int u = 0; u < nu; ++u, at_unit.next(p)) total += nstages(at_unit.w);
-    bool ok = true;
-    for (int c0 = 0; c0 < total && ok; c0 += kAhead) {
+    bool ok = !loads_withheld(p.guard);
+    bool issued = false;
+    At<kR.x> x;
+    int u = 0, k = 0, ns = nstages(at_unit.w);
+    while (ok && u < nu) {
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        const int c = c0 + a;
-        if (c >= total || !ok) continue;
-        uint32_t b[kTok / 32];
-#pragma unroll
-        for (int i = 0; i < kTok / 32; ++i) b[i] = ring[a][i];
-        fetch(ring[a]);
-        ok = freed(xfree, c, kR.x, 37);
+        if (!ok || u >= nu) break;
+        ok = guard_wait(xfree + 8u * x.i, x.phase ^ 1u, ctl, p.guard, 31);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;
-        uint16_t *dst = reinterpret_cast<uint16_t *>(factors + c % kR.x * kFactorBytes);
+        if (!ok) break;
+        const uint32_t fb = xfull + 8u * x.i;
+        if (elect_one()) {
+          mbar_expect_tx(fb, kRawBytes);
+          tma_load_2d(x_at + x.i * kRawBytes, &mX, at_unit.mt * kTcM, at_unit.w * p.win + k * kTok, fb);
+        }
+        issued = true;
+        uint16_t *dst = reinterpret_cast<uint16_t *>(factors + x.i * kFactorBytes);
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kTok / 32; ++i) {
-          dst[32 * i + lane] = static_cast<uint16_t>(factor_of(b[i]));
-          top = max(top, b[i]);
+          dst[32 * i + lane] = static_cast<uint16_t>(factor_of(ring[a][i]));
+          top = max(top, ring[a][i]);
         }
         const bool large = __any_sync(0xffffffffu, top > kMaxFast);
         if (lane == 0) *reinterpret_cast<uint32_t *>(dst + kTok) = large ? 1u : 0u;
         __syncwarp();
-        if (lane == 0) mbar_arrive(xfull + 8u * (c % kR.x));
+        if (lane == 0) mbar_arrive(fb);
+        fetch(ring[a]);
+        x.next();
+        if (++k == ns) {
+          k = 0;
+          ++u;
+          at_unit.next(p);
+          ns = nstages(at_unit.w);
+        }
       }
     }
+    if (!ok && issued) settle_copies();
+  } else if (warp == 2 + kWorkers) {
+    // ---------------------------------------------------------------- dxa
+    bool ok = !loads_withheld(p.guard);
+    bool issued = false;
+    At<kR.d> d;
+    for (int u = 0; u < nu && ok; ++u, at_unit.next(p)) {
+      const int n0 = at_unit.nt * p.ncols, ns = nstages(at_unit.w);
+      for (int k = 0; k < ns; ++k) {
+        ok = guard_wait(dfree + 8u * d.i, d.phase ^ 1u, ctl, p.guard, 39);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t fb = dfull + 8u * d.i, at = d_at + d.i * d_stage;
+        if (elect_one()) {
+          mbar_expect_tx(fb, d_stage);
+#pragma unroll
+          for (int b = 0; b < (kN + 63) / 64; ++b)
+            if (b < p.boxes) tma_load_2d(at + b * kBox, &mD, n0 + 64 * b, at_unit.w * p.win + k * kTok, fb);
+        }
+        __syncwarp();
+        issued = true;
+        d.next();
+      }
+    }
+    if (!ok && issued) settle_copies();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    // bf16, fp32 accumulator, the N side N-major
+    const uint32_t idesc = idesc_bf16(p.ncols) | (1u << 16);
+    bool ok = true;
+    At<kR.d> ds;
+    At<kR.ops> op;
+    At<2> win;
+    const uint64_t b0 = mn_desc(d_at, kBox);
+    for (int wi = 0; wi < nu && ok; ++wi, at_unit.next(p), win.next()) {
+      const int ns = nstages(at_unit.w);
+      const uint32_t d = tmem + static_cast<uint32_t>(win.i * kN);
+      ok = guard_wait(read0 + 8u * win.i, win.phase ^ 1u, ctl, p.guard, 32);
+      uint32_t acc = 0;
+      for (int k = 0; k < ns; ++k) {
+        ok = ok && guard_wait(dfull + 8u * ds.i, ds.phase, ctl, p.guard, 36) &&
+             guard_wait(conv0 + 8u * op.i, op.phase, ctl, p.guard, 33);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t b = b0 + (ds.i * d_stage >> 4);
+        const uint32_t a = tmem + 2 * kN + static_cast<uint32_t>(kOpCols * op.i);
+        if (elect_one()) {
+          // 16 tokens at a time: 8 columns of the M operand, 16 rows of 128 bytes
+          mma_bf16_ta(d, a, b, idesc, acc);
+#pragma unroll
+          for (int j = 1; j < kTok / 16; ++j) mma_bf16_ta(d, a + 8u * j, b + 128u * j, idesc, 1u);
+          mma_commit(used0 + 8u * op.i);
+          mma_commit(dfree + 8u * ds.i);
+          if (k + 1 == ns) mma_commit(done0 + 8u * win.i);
+        }
+        __syncwarp();
+        acc = 1;
+        ds.next();
+        op.next();
+      }
+    }
+    if (elect_one()) {
+      mma_commit(fin);
+      wait_drain_ns(fin, 0, kWaitNs);
+    }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------------- workers
     const int wk = warp - 2;
@@ -399,114 +411,128 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     const int tok = 64 * nh + 4 * ((lane & 7) >> 1) + (lane & 1) + 2 * ((lane >> 3) & 1);
     const int chunk = 2 * static_cast<int>(quad) + (lane >> 4);
     const uint32_t from_off = static_cast<uint32_t>(tok * 128 + ((chunk ^ (tok & 7)) << 4));
-    int c = 0;
     bool ok = true;
-    auto flush = [&](int k) {   // window number k of this CTA into `sum`
-      const bool got = filled(done0, k, 2, 34);
+    int flushed = 0;         // windows of this CTA that are in `sum` or written out
+    At<2> win;               // the next of them
+    auto flush = [&]() {
+      const bool got = guard_wait(done0 + 8u * win.i, win.phase, ctl, p.guard, 34);
       if (!__all_sync(0xffffffffu, got)) return false;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < NC; c += C) {
         float v[C];
-        tmem_ld<C>(lane_addr + static_cast<uint32_t>((k & 1) * kN + c), v);
+        tmem_ld<C>(lane_addr + static_cast<uint32_t>(win.i * kN + c), v);
 #pragma unroll
         for (int j = 0; j < C; ++j) sum[c + j] += v[j];
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(read0 + 8u * (k & 1));
+      if (lane == 0) mbar_arrive(read0 + 8u * win.i);
+      win.next();
+      ++flushed;
       return true;
     };
-    int seg0 = 0;   // first window of the current run within one tile
-    for (int wi = 0; wi < nu && ok; ++wi, at_unit.next(p)) {
-      const int mt = at_unit.mt, nt = at_unit.nt, w = at_unit.w;
-      const int ns = nstages(w);
-      for (int k = 0; k < ns; ++k, ++c) {
-        if ((c & 1) == grp) {
-          bool got = filled(xfull, c, kR.x, 35);
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
-          const uint32_t from = x_at + (c % kR.x) * kRawBytes + from_off;
-          const uint8_t *fa = factors + c % kR.x * kFactorBytes;
-          const bool large = *reinterpret_cast<const uint32_t *>(fa + 2 * kTok) != 0;
-          const int op = 2 * c + nh;
-          const uint32_t to = tmem + ((quad * 32u) << 16) + 2 * kN + static_cast<uint32_t>(kOpCols * (op % kR.ops));
-          // this warp's half of the tokens, 32 at a time, as 16 x 16 blocks
+    // the stage this warp is at: stage k of ns of the CTA's unit wi
+    int wi = 0, k = grp, ns = nstages(at_unit.w);
+    int seg0 = 0;            // first unit of the run within one tile
+    // the end of the run: the tile's remaining windows up to unit `last`, and
+    // the sum to dA or to the workspace
+    auto finish = [&](const Place &at, int last) {
+      while (flushed <= last)
+        if (!flush()) return false;
+      const bool whole = at.w + 1 == p.windows && last - seg0 + 1 == p.windows;
+      const bool from_start = at.w - (last - seg0) == 0;
+      const int m = static_cast<int>(quad) * 32 + lane;
+      if (whole) {
+        const int f = at.mt * kTcM + feature_of(m);
 #pragma unroll
-          for (int g2 = 0; g2 < 2; ++g2) {
-            uint32_t raw[2][4], o[2][8];   // o[h]: the 16 columns of feature block h
-            uint32_t top = 0;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) ldmatrix_x4_trans(from + 2048u * (2 * g2 + g), raw[g]);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint2 up = *reinterpret_cast<const uint2 *>(fa + 2 * (64 * nh + 16 * (2 * g2 + g) + 4 * (lane & 3)));
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int h = i / 2, half = i % 2;
-                const Mags m = mags4(raw[g][i]);
-                top = max_mag(top, m);
-                const uint2 d = decode4(raw[g][i], m, half ? up.y : up.x);
-                o[h][4 * g + half] = d.x;
-                o[h][4 * g + 2 + half] = d.y;
-              }
-            }
-            if (g2 == 0) {
-              got = freed(used0, op, kR.ops, 38);
-              if (!__all_sync(0xffffffffu, got)) break;
-              tc_fence_after();
-            }
-            if (!__any_sync(0xffffffffu, large || has_nan(top))) {
-              tmem_st_16x256b_x2(to + 16u * g2, o[0]);
-              tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
-            } else {
-              convert_any(p.scale + mt, p.nsx, p.T, w * p.win + k * kTok + 64 * nh + 32 * g2 + 4 * (lane & 3),
-                          from + 4096u * g2, from + 4096u * g2 + 2048u, to + 16u * g2);
-            }
-          }
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive(xfree + 8u * (c % kR.x));
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(conv0 + 8u * (op % kR.ops));
+        for (int j = 0; j < NC; ++j) {
+          const int n = nq * NC + j, col = at.nt * p.ncols + n;
+          if (n < p.ncols && col < p.r && f < p.in) p.dA[static_cast<int64_t>(col) * p.in + f] = sum[j];
         }
-        // the window before this one, once this one keeps the tensor core fed
-        if (k == min(1, ns - 1) && wi > seg0 && !flush(wi - 1)) {
-          ok = false;
-          break;
+      } else {
+        // slot 0: the run began inside the tile; slot 1: at its start
+        float *dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (from_start ? 1 : 0)) * p.ncols * kTcM + m;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          if (nq * NC + j < p.ncols) dst[(nq * NC + j) * kTcM] = sum[j];
+      }
+#pragma unroll
+      for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
+      seg0 = last + 1;
+      return true;
+    };
+    // to the unit that holds stage k (counted from the start of unit wi)
+    auto settle = [&]() {
+      while (k >= ns && wi < nu) {
+        k -= ns;
+        if (at_unit.w + 1 == p.windows || wi + 1 == nu) {
+          if (!finish(at_unit, wi)) return false;
+        }
+        at_unit.next(p);
+        if (++wi < nu) ns = nstages(at_unit.w);
+      }
+      return true;
+    };
+    At<kR.x> x;
+    At<kR.ops> op;
+    x.next(grp);
+    op.next(grp);
+    for (ok = settle(); ok && wi < nu; ok = settle()) {
+      bool got = guard_wait(xfull + 8u * x.i, x.phase, ctl, p.guard, 35);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      const uint32_t from = x_at + x.i * kRawBytes + from_off;
+      const uint8_t *fa = factors + x.i * kFactorBytes;
+      const bool large = *reinterpret_cast<const uint32_t *>(fa + 2 * kTok) != 0;
+      const uint32_t to = tmem + ((quad * 32u) << 16) + 2 * kN + static_cast<uint32_t>(kOpCols * op.i + 32 * nh);
+      // this warp's half of the tokens, 32 at a time, as 16 x 16 blocks
+#pragma unroll
+      for (int g2 = 0; g2 < 2; ++g2) {
+        uint32_t raw[2][4], o[2][8];   // o[h]: the 16 columns of feature block h
+        uint32_t top = 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) ldmatrix_x4_trans(from + 2048u * (2 * g2 + g), raw[g]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint2 up = *reinterpret_cast<const uint2 *>(fa + 2 * (64 * nh + 16 * (2 * g2 + g) + 4 * (lane & 3)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = i / 2, half = i % 2;
+            const Mags m = mags4(raw[g][i]);
+            top = max_mag(top, m);
+            const uint2 d = decode4(raw[g][i], m, half ? up.y : up.x);
+            o[h][4 * g + half] = d.x;
+            o[h][4 * g + 2 + half] = d.y;
+          }
+        }
+        if (g2 == 0) {
+          got = guard_wait(used0 + 8u * op.i, op.phase ^ 1u, ctl, p.guard, 38);
+          ok = __all_sync(0xffffffffu, got);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (!__any_sync(0xffffffffu, large || has_nan(top))) {
+          tmem_st_16x256b_x2(to + 16u * g2, o[0]);
+          tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
+        } else {
+          convert_any(p.scale + at_unit.mt, p.nsx, p.T,
+                      at_unit.w * p.win + k * kTok + 64 * nh + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
+                      from + 4096u * g2 + 2048u, to + 16u * g2);
         }
       }
       if (!ok) break;
-      if (w + 1 == p.windows || wi + 1 == nu) {
-        // the end of this CTA's run of the tile
-        if (!flush(wi)) break;
-        const bool whole = w + 1 == p.windows && wi - seg0 + 1 == p.windows;
-        const bool from_start = w - (wi - seg0) == 0;
-        const int m = static_cast<int>(quad) * 32 + lane;
-        if (whole) {
-          const int f = mt * kTcM + feature_of(m);
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            const int n = nq * NC + j, col = nt * p.ncols + n;
-            if (n < p.ncols && col < p.r && f < p.in) p.dA[static_cast<int64_t>(col) * p.in + f] = sum[j];
-          }
-        } else {
-          // slot 0: the run began inside the tile; slot 1: at its start
-          float *dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (from_start ? 1 : 0)) * p.ncols * kTcM + m;
-#pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (nq * NC + j < p.ncols) dst[(nq * NC + j) * kTcM] = sum[j];
-        }
-#pragma unroll
-        for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
-        seg0 = wi + 1;
-      }
+      if (lane == 0) mbar_arrive(xfree + 8u * x.i);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(conv0 + 8u * op.i);
+      x.next(2);
+      op.next(2);
+      // the windows before this one, now that this one keeps the tensor core fed
+      while (ok && flushed < wi) ok = flush();
+      if (!ok) break;
+      k += 2;
     }
   }
   tc_fence_before();
@@ -519,38 +545,41 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
 }
 
 // dA of the tiles that more than one CTA worked on: their parts in CTA order.
-// One block: one tile, kJoin of its columns
-constexpr int kJoin = 16;
+// One block: one tile, kJoin of its columns; a thread: one feature, kJoin / 2
+// columns, the parts of up to kJoinAt CTAs loaded at a time
+constexpr int kJoin = 8, kJoinAt = 4;
 __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p, int ctas) {
-  __shared__ int owners[2];
-  pdl_wait();
   const int chunks = (p.ncols + kJoin - 1) / kJoin;
   const int tile = blockIdx.x / chunks;
-  if (threadIdx.x < 2) {
-    // the CTA of the tile's first and of its last unit: first_unit(i) <= unit < first_unit(i + 1)
-    const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
-    const int64_t unit = static_cast<int64_t>(tile + static_cast<int>(threadIdx.x)) * p.windows - threadIdx.x;
-    int i = static_cast<int>(unit * ctas / units);
-    while (first_unit(units, i + 1, ctas) <= unit) ++i;
-    owners[threadIdx.x] = i;
-  }
-  __syncthreads();
-  const int i0 = owners[0], i1 = owners[1];
-  if (i0 == i1) return;
+  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
+  // the CTA of a unit: first_unit(i) <= unit < first_unit(i + 1), that is
+  // i = ceil((unit + 1) ctas / units) - 1
+  const int64_t u0 = static_cast<int64_t>(tile) * p.windows, u1 = u0 + p.windows;
+  const int i0 = static_cast<int>(((u0 + 1) * ctas - 1) / units), i1 = static_cast<int>((u1 * ctas - 1) / units);
   const int mt = tile % p.mtiles, nt = tile / p.mtiles;
   const int m = threadIdx.x % kTcM, f = mt * kTcM + feature_of(m);
   const int n0 = (blockIdx.x % chunks) * kJoin + threadIdx.x / kTcM;
   const int64_t slot = static_cast<int64_t>(p.ncols) * kTcM;
   const float *src = p.part + static_cast<int64_t>(n0) * kTcM + m;
-  if (f >= p.in) return;
-  float s[kJoin / 2];
+  pdl_wait();
+  if (i0 == i1 || f >= p.in) return;
+  float s[kJoin / 2] = {};
+  for (int i = i0; i <= i1; i += kJoinAt) {
+    float v[kJoinAt][kJoin / 2];
 #pragma unroll
-  for (int j = 0; j < kJoin / 2; ++j)
-    s[j] = n0 + 2 * j < p.ncols ? src[(static_cast<int64_t>(i0) * 2 + 1) * slot + 2 * j * kTcM] : 0.0f;
-  for (int i = i0 + 1; i <= i1; ++i)
+    for (int b = 0; b < kJoinAt; ++b)
 #pragma unroll
-    for (int j = 0; j < kJoin / 2; ++j)
-      if (n0 + 2 * j < p.ncols) s[j] += src[static_cast<int64_t>(i) * 2 * slot + 2 * j * kTcM];
+      for (int j = 0; j < kJoin / 2; ++j) {
+        v[b][j] = 0.0f;
+        // the first CTA's part is its second (its run of the tile began at the tile's start)
+        if (i + b <= i1 && n0 + 2 * j < p.ncols)
+          v[b][j] = __ldcs(src + (static_cast<int64_t>(i + b) * 2 + (i + b == i0 ? 1 : 0)) * slot + 2 * j * kTcM);
+      }
+#pragma unroll
+    for (int b = 0; b < kJoinAt; ++b)
+#pragma unroll
+      for (int j = 0; j < kJoin / 2; ++j) s[j] += v[b][j];
+  }
 #pragma unroll
   for (int j = 0; j < kJoin / 2; ++j) {
     const int n = n0 + 2 * j, col = nt * p.ncols + n;
