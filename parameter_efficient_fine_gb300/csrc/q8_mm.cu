@@ -27,11 +27,24 @@
 //   warp 1     tensor memory, MMA issue (four 32-wide steps per k block)
 //   warps 2-5  scale words into tensor memory, four k blocks at a time, each
 //              warp its lane quadrant; then the result out of it
+// q8_pair_kernel: for many tokens, tiles of 256 features x 256 tokens on CTA
+// pairs (tcgen05.mma.cta_group::2, M = 256), one pair per two SMs, tile after
+// tile.  Each CTA stages its 128 features and its 128 tokens, 256 k a stage, so
+// an SM loads half of what a single CTA's 128 x 256 tile would; the scale words
+// of all 256 tokens are written in both CTAs.
+//   warp 0      TMA producer (each CTA its own boxes, on the even CTA's barrier)
+//   warp 1      tensor memory, MMA issue (even CTA; eight 32-wide steps a stage)
+//   warps 2-5   scale words into tensor memory
+//   warps 6-13  the result: out of tensor memory into registers as bf16 (the
+//               next tile's MMAs may start), then 32 features a warp and token
+//               straight to memory, 64 contiguous bytes
 // Every wait on a shared-memory barrier is bounded; a wait that gives up
 // records a code in the library's device error word and all roles leave.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "q8.cuh"
@@ -310,6 +323,273 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------------------
+// CTA pairs
+// ---------------------------------------------------------------------------
+constexpr int kPairTok = 256;                        // tokens per tile
+constexpr int kPairFeat = 256;                       // features per tile
+constexpr int kPairKB = 2;                           // k blocks per stage
+constexpr int kPairStages = 3;
+constexpr unsigned kPairBox = kTcM * kKB;            // 16 KB: 128 features or tokens, one k block
+constexpr unsigned kPairStage = 2 * kPairKB * kPairBox;
+constexpr int kPairThreads = 14 * 32;
+constexpr int kPairSfCol = kPairTok, kPairSfStride = 16;   // scale words: 4 columns of W's, 8 of the tokens'
+constexpr int kGroupF = 8;                           // feature tiles per tile-order group (L2 reuse)
+
+__device__ __forceinline__ void mma_q8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+// a place in a ring of N
+template <int N> struct At {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <bool TRANS>
+__global__ void __launch_bounds__(kPairThreads, 1)
+q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const MmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kPairStages * kPairStage);
+  // barriers (a pair uses the even CTA's full, scales full and accumulator
+  // empty): full, empty, scales full and empty, accumulator full and empty, end
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kPairStages, sff0 = empty0 + 8u * kPairStages,
+                 sfe0 = sff0 + 8u * kSfSlots, accf = sfe0 + 8u * kSfSlots, acce = accf + 8, fin = acce + 8;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * kPairStages + 2 * kSfSlots + 3);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(full0 + 8u * s, 1);
+      mbar_init(empty0 + 8u * s, 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(sff0 + 8u * s, 8);     // four warps of either CTA
+      mbar_init(sfe0 + 8u * s, 1);
+    }
+    mbar_init(accf, 1);
+    mbar_init(acce, 16);               // eight warps of either CTA
+    mbar_init(fin, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+    prefetch_map(&mW);
+    prefetch_map(&mX);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers are initialised before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const int pair = static_cast<int>(blockIdx.x / 2), npairs = static_cast<int>(gridDim.x / 2);
+  const int ftiles = p.tiles / p.ntiles, stages = (p.kblocks + kPairKB - 1) / kPairKB, groups = (p.kblocks + 3) / 4;
+  // tile t: groups of kGroupF feature tiles, all token tiles of a group in turn
+  auto place = [&](int t, int *ft, int *tt) {
+    const int per = kGroupF * p.ntiles, g = t / per, f0 = g * kGroupF, gf = min(kGroupF, ftiles - f0), r = t - g * per;
+    *tt = r / gf;
+    *ft = f0 + r - *tt * gf;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    bool ok = !loads_withheld(p.guard);
+    bool issued = false;
+    At<kPairStages> st;
+    for (int t = pair; t < p.tiles && ok; t += npairs) {
+      int ft, tt;
+      place(t, &ft, &tt);
+      const int f0 = ft * kPairFeat + static_cast<int>(rank) * kTcM, t0 = tt * kPairTok + static_cast<int>(rank) * kTcM;
+      for (int s = 0; s < stages; ++s) {
+        ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 41);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t fb = full0 + 8u * st.i, lb = mapa_shared(fb, 0);
+        const uint32_t at = smem_u32(smem) + st.i * kPairStage;
+        if (elect_one()) {
+          // the even CTA's barrier counts both CTAs' bytes
+          if (rank == 0) mbar_expect_tx(fb, 2 * kPairStage);
+#pragma unroll
+          for (int k = 0; k < kPairKB; ++k) {
+            const int kx = (s * kPairKB + k) * kKB;
+            if (TRANS) tma_load_2d_pair(at + k * kPairBox, &mW, f0, kx, lb);
+            else tma_load_2d_pair(at + k * kPairBox, &mW, kx, f0, lb);
+            tma_load_2d_pair(at + (kPairKB + k) * kPairBox, &mX, kx, t0, lb);
+          }
+        }
+        __syncwarp();
+        issued = true;
+        st.next();
+      }
+    }
+    if (!ok && issued) {
+      // copies in flight, whose barrier may never complete after an abort: they
+      // land within microseconds, wait 1 ms
+      const unsigned long long t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      // (a commit arrives on the barrier of this CTA and on the peer's)
+      bool ok = true;
+      At<kPairStages> st;
+      At<kSfSlots> sf;
+      At<1> acc;
+      const uint32_t peer_off = mapa_shared(full0, peer) - full0;   // to the peer's copy of a barrier
+      const uint32_t id0 = idesc_q8(kPairFeat, kPairTok, 0, TRANS);
+      for (int t = pair; t < p.tiles && ok; t += npairs, acc.next()) {
+        ok = guard_wait(acce, acc.phase ^ 1u, ctl, p.guard, 42);
+        for (int s = 0; s < stages; ++s) {
+          const uint32_t half = static_cast<uint32_t>(s & 1);   // which two of the group's four k blocks
+          if (half == 0) ok = ok && guard_wait(sff0 + 8u * sf.i, sf.phase, ctl, p.guard, 43);
+          ok = ok && guard_wait(full0 + 8u * st.i, st.phase, ctl, p.guard, 44);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem) + st.i * kPairStage;
+          const uint64_t a = sdesc<32>(at), b = sdesc<32>(at + kPairKB * kPairBox);
+          const uint32_t sfa = tmem + kPairSfCol + kPairSfStride * sf.i;
+          const bool last = s + 1 == stages;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kPairKB; ++k) {
+              const uint32_t byte = 2 * half + k;
+              const uint32_t idesc = id0 | (byte << 4) | (byte << 29);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_q8_pair(tmem, a + (kPairBox >> 4) * k + (TRANS ? 256u : 2u) * j, b + (kPairBox >> 4) * k + 2u * j,
+                            idesc, sfa, sfa + 4, s != 0 || k != 0 || j != 0 ? 1u : 0u);
+            }
+            mma_commit_pair(empty0 + 8u * st.i);
+            mma_commit_pair(empty0 + 8u * st.i + peer_off);
+            if (half == 1 || last) {
+              mma_commit_pair(sfe0 + 8u * sf.i);
+              mma_commit_pair(sfe0 + 8u * sf.i + peer_off);
+            }
+            if (last) {
+              mma_commit_pair(accf);
+              mma_commit_pair(accf + peer_off);
+            }
+          }
+          __syncwarp();
+          if (half == 1 || last) sf.next();
+          st.next();
+        }
+      }
+      if (elect_one()) {
+        mma_commit_pair(fin);
+        wait_drain_ns(fin, 0, kWaitNs);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 6) {
+    // ---------------------------------------------------------------- scales
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const bool words = p.nsx % 4 == 0 && (reinterpret_cast<uintptr_t>(p.xscale) & 3) == 0;
+    bool ok = true;
+    At<kSfSlots> sf;
+    for (int t = pair; t < p.tiles && ok; t += npairs) {
+      int ft, tt;
+      place(t, &ft, &tt);
+      const int wt = 2 * ft + static_cast<int>(rank);   // 128 features
+      const uint8_t *row = p.xscale + static_cast<int64_t>(tt * kPairTok + lane) * p.nsx;
+      const bool live = wt * kTcM < p.nfeat;
+      for (int g = 0; g < groups; ++g) {
+        uint32_t x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[j] = tt * kPairTok + 32 * j + lane < p.T
+                     ? token_word(row + static_cast<int64_t>(32 * j) * p.nsx, g, p.kblocks, words)
+                     : 0x7f7f7f7fu;
+        const uint32_t w = live ? weight_word<TRANS>(p, wt, g) : 0x7f7f7f7fu;
+        ok = guard_wait(sfe0 + 8u * sf.i, sf.phase ^ 1u, ctl, p.guard, 45);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t to = lane_addr + kPairSfCol + kPairSfStride * sf.i;
+        tmem_st4(to, w, w, w, w);
+        tmem_st8(to + 4, x);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(sff0 + 8u * sf.i, 0));
+        sf.next();
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- result
+    const int e = warp - 6;
+    const uint32_t quad = static_cast<uint32_t>(warp & 3);
+    const int c0 = (e >> 2) * (kPairTok / 2);      // this warp's half of the tokens
+    const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
+    bool ok = true;
+    At<1> acc;
+    for (int t = pair; t < p.tiles && ok; t += npairs, acc.next()) {
+      int ft, tt;
+      place(t, &ft, &tt);
+      ok = guard_wait(accf, acc.phase, ctl, p.guard, 46);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t o[kPairTok / 4];                    // two tokens a register
+#pragma unroll
+      for (int c = 0; c < kPairTok / 2; c += 32) {
+        float v[32];
+        tmem_ld<32>(lane_addr + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[c / 2 + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(acce, 0));
+      const int f = ft * kPairFeat + static_cast<int>(rank) * kTcM + static_cast<int>(quad) * 32 + lane;
+      const int t0 = tt * kPairTok + c0;
+      if (f < p.nfeat) {
+        uint16_t *y = reinterpret_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0) * p.nfeat + f;
+        const int64_t ld = p.nfeat;
+        const int live = p.T - t0;
+#pragma unroll
+        for (int i = 0; i < kPairTok / 4; ++i, y += 2 * ld) {
+          if (2 * i < live) y[0] = static_cast<uint16_t>(o[i]);
+          if (2 * i + 1 < live) y[ld] = static_cast<uint16_t>(o[i] >> 16);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // the even CTA's MMAs, which read this CTA's shared memory and write its
+  // tensor memory, are complete, and both CTAs' results are out
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 size_t split_smem(int nt, int stages) { return 1024 + static_cast<size_t>(stages) * (kWBytes + nt * kKB) + 512; }
@@ -346,8 +626,63 @@ dora_status mm_init(int device, MmParams *p) {
       (const void *)q8_split_kernel<16, false>, (const void *)q8_split_kernel<32, false>,
       (const void *)q8_split_kernel<64, false>, (const void *)q8_split_kernel<128, false>,
       (const void *)q8_split_kernel<16, true>,  (const void *)q8_split_kernel<32, true>,
-      (const void *)q8_split_kernel<64, true>,  (const void *)q8_split_kernel<128, true>};
+      (const void *)q8_split_kernel<64, true>,  (const void *)q8_split_kernel<128, true>,
+      (const void *)q8_pair_kernel<false>,      (const void *)q8_pair_kernel<true>};
   return tc_init(device, &p->guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
+}
+
+constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + 512;
+
+void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int pairs, cudaStream_t cs) {
+  *cfg = cudaLaunchConfig_t{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg->gridDim = dim3(2 * static_cast<unsigned>(pairs));
+  cfg->blockDim = dim3(kPairThreads);
+  cfg->dynamicSmemBytes = kPairSmem;
+  cfg->stream = cs;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// pairs that are resident at once (a pair takes every npairs-th tile, so one
+// that had to wait for another to end would double the time); 0 where the
+// device has no clusters of two
+int resident_pairs(int device, int sms) {
+  static std::mutex mu;
+  static int known[64] = {};   // pairs + 1
+  std::lock_guard<std::mutex> lock(mu);
+  if (device < 0 || device >= 64) return 0;
+  if (known[device] == 0) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    pair_config(&cfg, attr, sms / 2, nullptr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, q8_pair_kernel<false>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[device] = n + 1;
+  }
+  return known[device] - 1;
+}
+
+template <bool TRANS>
+dora_status launch_pairs(const void *q, const void *wq, int64_t out, int64_t in, MmParams p, int pairs,
+                         cudaStream_t cs) {
+  CUtensorMap mW, mX;
+  if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, p.T, p.kdim, 128)) return DORA_ERR_CUDA;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pair_config(&cfg, attr, p.tiles < pairs ? p.tiles : pairs, cs);
+  if (cudaLaunchKernelEx(&cfg, q8_pair_kernel<TRANS>, mW, mX, p) != cudaSuccess) {
+    cudaGetLastError();
+    return DORA_ERR_CUDA;
+  }
+  dora::count_launches(1);
+  return DORA_OK;
 }
 
 // q: the activation's bytes [T, kdim]; features and k are (out, in) or, for dy W, (in, out)
@@ -370,6 +705,14 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   p.xscale = static_cast<const uint8_t *>(scale);
   p.wscale = static_cast<const uint8_t *>(wscale);
   p.y = static_cast<__nv_bfloat16 *>(y);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t pair_tiles = dora::ceil_div(p.nfeat, kPairFeat) * dora::ceil_div(T, kPairTok);
+  const int pairs = resident_pairs(device, info.sms);
+  if (pairs > 0 && pair_tiles >= pairs && pair_tiles <= kMaxDim) {
+    p.ntiles = static_cast<int>(dora::ceil_div(T, kPairTok));
+    p.tiles = static_cast<int>(pair_tiles);
+    return launch_pairs<TRANS>(q, wq, out, in, p, pairs, cs);
+  }
   const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   p.ntiles = static_cast<int>(dora::ceil_div(T, nt));
   const int64_t tiles = dora::ceil_div(p.nfeat, kTcM) * p.ntiles;
@@ -380,7 +723,6 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   while (cluster < kMaxCluster && tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= p.kblocks) cluster *= 2;
   CUtensorMap mW, mX;
   if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, T, p.kdim, nt)) return DORA_ERR_CUDA;
-  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   switch (nt) {
     case 16: return launch_split<16, TRANS>(mW, mX, p, cluster, cs);
     case 32: return launch_split<32, TRANS>(mW, mX, p, cluster, cs);
