@@ -29,11 +29,13 @@
 //              warp its lane quadrant; then the result out of it
 // q8_pair_kernel: for many tokens, tiles of 256 features x 256 tokens on CTA
 // pairs (tcgen05.mma.cta_group::2, M = 256), one pair per two SMs, tile after
-// tile.  Each CTA stages its 128 features and its 128 tokens, 256 k a stage, so
-// an SM loads half of what a single CTA's 128 x 256 tile would; the scale words
-// of all 256 tokens are written in both CTAs.
+// tile.  Each CTA stages its 128 features and its 128 tokens, so an SM loads half
+// of what a single CTA's 128 x 256 tile would; the scale words of all 256
+// tokens are written in both CTAs.
 //   warp 0      TMA producer (each CTA its own boxes, on the even CTA's barrier)
-//   warp 1      tensor memory, MMA issue (even CTA; eight 32-wide steps a stage)
+//   warp 1      tensor memory, MMA issue (even CTA).  A stage is two k blocks: waiting
+//               for one and issuing its MMAs takes this warp about 600 cycles,
+//               more than the 512 that the MMAs of one k block run
 //   warps 2-5   scale words into tensor memory
 //   warps 6-13  the result: out of tensor memory into registers as bf16 (the
 //               next tile's MMAs may start), then 32 features a warp and token
@@ -101,13 +103,25 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// loads that stay where they are written (the compiler would move them down to
+// their use, past the wait that they are to overlap)
+__device__ __forceinline__ uint32_t load_now(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_now(const uint8_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 // the scale bytes of k blocks 4 g .. 4 g + 3 of one row of an activation, a
 // byte each; 1 past the last k block
 __device__ __forceinline__ uint32_t token_word(const uint8_t *row, int g, int kblocks, bool words) {
-  if (words) return __ldg(reinterpret_cast<const uint32_t *>(row) + g);
+  if (words) return load_now(reinterpret_cast<const uint32_t *>(row) + g);
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= static_cast<uint32_t>(4 * g + i < kblocks ? __ldg(row + 4 * g + i) : 127) << (8 * i);
+  for (int i = 0; i < 4; ++i) w |= (4 * g + i < kblocks ? load_now(row + 4 * g + i) : 127u) << (8 * i);
   return w;
 }
 // the same of 128 features of W: along a row of its scales, or down a column
@@ -118,7 +132,7 @@ __device__ __forceinline__ uint32_t weight_word(const MmParams &p, int mt, int g
   for (int i = 0; i < 4; ++i) {
     const int kb = 4 * g + i;
     const int64_t at = TRANS ? static_cast<int64_t>(kb) * p.nsw + mt : static_cast<int64_t>(mt) * p.nsw + kb;
-    w |= static_cast<uint32_t>(kb < p.kblocks ? __ldg(p.wscale + at) : 127) << (8 * i);
+    w |= (kb < p.kblocks ? load_now(p.wscale + at) : 127u) << (8 * i);
   }
   return w;
 }
@@ -349,6 +363,12 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
                "r"(d)
                : "memory");
 }
+// arrive on an mbarrier of the pair where what it hands over is tensor memory
+// only: the tcgen05 fence before it orders that, and a release at cluster scope
+// (a memory fence of about 1500 cycles here) would order nothing more
+__device__ __forceinline__ void mbar_arrive_pair_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // a place in a ring of N
 template <int N> struct At {
   int i = 0;
@@ -461,8 +481,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       for (int t = pair; t < p.tiles && ok; t += npairs, acc.next()) {
         ok = guard_wait(acce, acc.phase ^ 1u, ctl, p.guard, 42);
         for (int s = 0; s < stages; ++s) {
-          const uint32_t half = static_cast<uint32_t>(s & 1);   // which two of the group's four k blocks
-          if (half == 0) ok = ok && guard_wait(sff0 + 8u * sf.i, sf.phase, ctl, p.guard, 43);
+          const bool second = (s & 1) != 0;   // which two of the group's four k blocks
+          if (!second) ok = ok && guard_wait(sff0 + 8u * sf.i, sf.phase, ctl, p.guard, 43);
           ok = ok && guard_wait(full0 + 8u * st.i, st.phase, ctl, p.guard, 44);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -470,20 +490,19 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           const uint32_t at = smem_u32(smem) + st.i * kPairStage;
           const uint64_t a = sdesc<32>(at), b = sdesc<32>(at + kPairKB * kPairBox);
           const uint32_t sfa = tmem + kPairSfCol + kPairSfStride * sf.i;
+          const uint32_t id = second ? id0 | (2u << 4) | (2u << 29) : id0;
           const bool last = s + 1 == stages;
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kPairKB; ++k) {
-              const uint32_t byte = 2 * half + k;
-              const uint32_t idesc = id0 | (byte << 4) | (byte << 29);
+            for (int k = 0; k < kPairKB; ++k)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 mma_q8_pair(tmem, a + (kPairBox >> 4) * k + (TRANS ? 256u : 2u) * j, b + (kPairBox >> 4) * k + 2u * j,
-                            idesc, sfa, sfa + 4, s != 0 || k != 0 || j != 0 ? 1u : 0u);
-            }
+                            id | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa, sfa + 4,
+                            s != 0 || k != 0 || j != 0 ? 1u : 0u);
             mma_commit_pair(empty0 + 8u * st.i);
             mma_commit_pair(empty0 + 8u * st.i + peer_off);
-            if (half == 1 || last) {
+            if (second || last) {
               mma_commit_pair(sfe0 + 8u * sf.i);
               mma_commit_pair(sfe0 + 8u * sf.i + peer_off);
             }
@@ -493,7 +512,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
             }
           }
           __syncwarp();
-          if (half == 1 || last) sf.next();
+          if (second || last) sf.next();
           st.next();
         }
       }
@@ -513,15 +532,17 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       int ft, tt;
       place(t, &ft, &tt);
       const int wt = 2 * ft + static_cast<int>(rank);   // 128 features
-      const uint8_t *row = p.xscale + static_cast<int64_t>(tt * kPairTok + lane) * p.nsx;
       const bool live = wt * kTcM < p.nfeat;
+      const uint8_t *row[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int tok = tt * kPairTok + 32 * j + lane;
+        row[j] = tok < p.T ? p.xscale + static_cast<int64_t>(tok) * p.nsx : nullptr;
+      }
       for (int g = 0; g < groups; ++g) {
         uint32_t x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] = tt * kPairTok + 32 * j + lane < p.T
-                     ? token_word(row + static_cast<int64_t>(32 * j) * p.nsx, g, p.kblocks, words)
-                     : 0x7f7f7f7fu;
+        for (int j = 0; j < 8; ++j) x[j] = row[j] ? token_word(row[j], g, p.kblocks, words) : 0x7f7f7f7fu;
         const uint32_t w = live ? weight_word<TRANS>(p, wt, g) : 0x7f7f7f7fu;
         ok = guard_wait(sfe0 + 8u * sf.i, sf.phase ^ 1u, ctl, p.guard, 45);
         ok = __all_sync(0xffffffffu, ok);
@@ -533,7 +554,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(sff0 + 8u * sf.i, 0));
+        if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(sff0 + 8u * sf.i, 0));
         sf.next();
       }
     }
@@ -562,7 +583,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(acce, 0));
+      if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(acce, 0));
       const int f = ft * kPairFeat + static_cast<int>(rank) * kTcM + static_cast<int>(quad) * 32 + lane;
       const int t0 = tt * kPairTok + c0;
       if (f < p.nfeat) {
