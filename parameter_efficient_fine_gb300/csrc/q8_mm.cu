@@ -27,11 +27,13 @@
 //   warp 1     tensor memory, MMA issue (four 32-wide steps per k block)
 //   warps 2-5  scale words into tensor memory, four k blocks at a time, each
 //              warp its lane quadrant; then the result out of it
-// q8_pair_kernel: for many tokens, tiles of 256 features x 256 tokens on CTA
+// q8_pair_kernel: for many tokens, tiles of 256 features x up to 256 tokens on CTA
 // pairs (tcgen05.mma.cta_group::2, M = 256), one pair per two SMs, tile after
-// tile.  Each CTA stages its 128 features and its 128 tokens, so an SM loads half
-// of what a single CTA's 128 x 256 tile would; the scale words of all 256
-// tokens are written in both CTAs.
+// tile.  Each CTA stages its 128 features and half of the tokens, so an SM loads
+// half of what a single CTA's tile would; the scale words of all tokens of the
+// tile are written in both CTAs.  Up to 224 tokens, two accumulators and the
+// scale words fill tensor memory and a tile's result leaves while the next
+// tile's MMAs run; a tile of more tokens has one accumulator.
 //   warp 0      TMA producer (each CTA its own boxes, on the even CTA's barrier)
 //   warp 1      tensor memory, MMA issue (even CTA).  A stage is two k blocks: waiting
 //               for one and issuing its MMAs takes this warp about 600 cycles,
@@ -66,6 +68,7 @@ struct MmParams {
   int T, nfeat, kdim;               // tokens, features of the result, k
   int kblocks;
   int ntiles, tiles;                // token tiles, all tiles
+  int ntok;                         // tokens per tile (pairs)
   int stages;
   int nsx, nsw;                     // scale bytes per row of x, of W
   const uint8_t *xscale, *wscale;
@@ -339,14 +342,16 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // CTA pairs
 // ---------------------------------------------------------------------------
-constexpr int kPairTok = 256;                        // tokens per tile
+constexpr int kPairTok = 256;                        // most tokens per tile, half of them staged by either CTA
+constexpr int kPairTwo = 224;                        // most tokens of a tile that has two accumulators
 constexpr int kPairFeat = 256;                       // features per tile
 constexpr int kPairKB = 2;                           // k blocks per stage
 constexpr int kPairStages = 3;
-constexpr unsigned kPairBox = kTcM * kKB;            // 16 KB: 128 features or tokens, one k block
-constexpr unsigned kPairStage = 2 * kPairKB * kPairBox;
+constexpr unsigned kPairBox = kTcM * kKB;            // 16 KB: 128 features, one k block
+constexpr unsigned kPairXBox = kPairTok / 2 * kKB;   // room for 128 tokens, one k block (16 KB)
+constexpr unsigned kPairStage = kPairKB * (kPairBox + kPairXBox);
 constexpr int kPairThreads = 14 * 32;
-constexpr int kPairSfCol = kPairTok, kPairSfStride = 16;   // scale words: 4 columns of W's, 8 of the tokens'
+constexpr int kPairSfCol = 2 * kPairTwo, kPairSfStride = 16;   // scale words: 4 columns of W's, 8 of the tokens'
 constexpr int kGroupF = 8;                           // feature tiles per tile-order group (L2 reuse)
 
 __device__ __forceinline__ void mma_q8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
@@ -369,6 +374,19 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
 __device__ __forceinline__ void mbar_arrive_pair_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// the accumulator of a pair's tile: two in turn, or one
+struct Acc {
+  int n, i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Acc(int ntok) : n(ntok > kPairTwo ? 1 : 2) {}
+  __device__ __forceinline__ uint32_t column() const { return static_cast<uint32_t>(i * kPairTwo); }
+  __device__ __forceinline__ void next() {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
 // a place in a ring of N
 template <int N> struct At {
   int i = 0;
@@ -390,8 +408,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   // barriers (a pair uses the even CTA's full, scales full and accumulator
   // empty): full, empty, scales full and empty, accumulator full and empty, end
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kPairStages, sff0 = empty0 + 8u * kPairStages,
-                 sfe0 = sff0 + 8u * kSfSlots, accf = sfe0 + 8u * kSfSlots, acce = accf + 8, fin = acce + 8;
-  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * kPairStages + 2 * kSfSlots + 3);
+                 sfe0 = sff0 + 8u * kSfSlots, accf = sfe0 + 8u * kSfSlots, acce = accf + 16, fin = acce + 16;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * kPairStages + 2 * kSfSlots + 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
   if (threadIdx.x == 0) {
@@ -403,8 +421,10 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       mbar_init(sff0 + 8u * s, 8);     // four warps of either CTA
       mbar_init(sfe0 + 8u * s, 1);
     }
-    mbar_init(accf, 1);
-    mbar_init(acce, 16);               // eight warps of either CTA
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf + 8u * b, 1);
+      mbar_init(acce + 8u * b, 16);    // eight warps of either CTA
+    }
     mbar_init(fin, 1);
     ctl->abort = 0;
     fence_barrier_init();
@@ -438,7 +458,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     for (int t = pair; t < p.tiles && ok; t += npairs) {
       int ft, tt;
       place(t, &ft, &tt);
-      const int f0 = ft * kPairFeat + static_cast<int>(rank) * kTcM, t0 = tt * kPairTok + static_cast<int>(rank) * kTcM;
+      const int f0 = ft * kPairFeat + static_cast<int>(rank) * kTcM, t0 = tt * p.ntok + static_cast<int>(rank) * (p.ntok / 2);
       for (int s = 0; s < stages; ++s) {
         ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 41);
         ok = __all_sync(0xffffffffu, ok);
@@ -447,13 +467,13 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         const uint32_t at = smem_u32(smem) + st.i * kPairStage;
         if (elect_one()) {
           // the even CTA's barrier counts both CTAs' bytes
-          if (rank == 0) mbar_expect_tx(fb, 2 * kPairStage);
+          if (rank == 0) mbar_expect_tx(fb, 2 * kPairKB * (kPairBox + static_cast<uint32_t>(p.ntok / 2) * kKB));
 #pragma unroll
           for (int k = 0; k < kPairKB; ++k) {
             const int kx = (s * kPairKB + k) * kKB;
             if (TRANS) tma_load_2d_pair(at + k * kPairBox, &mW, f0, kx, lb);
             else tma_load_2d_pair(at + k * kPairBox, &mW, kx, f0, lb);
-            tma_load_2d_pair(at + (kPairKB + k) * kPairBox, &mX, kx, t0, lb);
+            tma_load_2d_pair(at + kPairKB * kPairBox + k * kPairXBox, &mX, kx, t0, lb);
           }
         }
         __syncwarp();
@@ -475,11 +495,12 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       bool ok = true;
       At<kPairStages> st;
       At<kSfSlots> sf;
-      At<1> acc;
+      Acc acc(p.ntok);
       const uint32_t peer_off = mapa_shared(full0, peer) - full0;   // to the peer's copy of a barrier
-      const uint32_t id0 = idesc_q8(kPairFeat, kPairTok, 0, TRANS);
+      const uint32_t id0 = idesc_q8(kPairFeat, p.ntok, 0, TRANS);
       for (int t = pair; t < p.tiles && ok; t += npairs, acc.next()) {
-        ok = guard_wait(acce, acc.phase ^ 1u, ctl, p.guard, 42);
+        ok = guard_wait(acce + 8u * acc.i, acc.phase ^ 1u, ctl, p.guard, 42);
+        const uint32_t d = tmem + acc.column();
         for (int s = 0; s < stages; ++s) {
           const bool second = (s & 1) != 0;   // which two of the group's four k blocks
           if (!second) ok = ok && guard_wait(sff0 + 8u * sf.i, sf.phase, ctl, p.guard, 43);
@@ -497,7 +518,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
             for (int k = 0; k < kPairKB; ++k)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mma_q8_pair(tmem, a + (kPairBox >> 4) * k + (TRANS ? 256u : 2u) * j, b + (kPairBox >> 4) * k + 2u * j,
+                mma_q8_pair(d, a + (kPairBox >> 4) * k + (TRANS ? 256u : 2u) * j, b + (kPairXBox >> 4) * k + 2u * j,
                             id | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa, sfa + 4,
                             s != 0 || k != 0 || j != 0 ? 1u : 0u);
             mma_commit_pair(empty0 + 8u * st.i);
@@ -507,8 +528,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
               mma_commit_pair(sfe0 + 8u * sf.i + peer_off);
             }
             if (last) {
-              mma_commit_pair(accf);
-              mma_commit_pair(accf + peer_off);
+              mma_commit_pair(accf + 8u * acc.i);
+              mma_commit_pair(accf + 8u * acc.i + peer_off);
             }
           }
           __syncwarp();
@@ -536,7 +557,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       const uint8_t *row[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int tok = tt * kPairTok + 32 * j + lane;
+        const int tok = tt * p.ntok + 32 * j + lane;
         row[j] = tok < p.T ? p.xscale + static_cast<int64_t>(tok) * p.nsx : nullptr;
       }
       for (int g = 0; g < groups; ++g) {
@@ -562,34 +583,36 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     // ---------------------------------------------------------------- result
     const int e = warp - 6;
     const uint32_t quad = static_cast<uint32_t>(warp & 3);
-    const int c0 = (e >> 2) * (kPairTok / 2);      // this warp's half of the tokens
+    const int half = p.ntok / 2;                   // tokens of this warp, from c0
+    const int c0 = (e >> 2) * half;
     const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
     bool ok = true;
-    At<1> acc;
+    Acc acc(p.ntok);
     for (int t = pair; t < p.tiles && ok; t += npairs, acc.next()) {
       int ft, tt;
       place(t, &ft, &tt);
-      ok = guard_wait(accf, acc.phase, ctl, p.guard, 46);
+      ok = guard_wait(accf + 8u * acc.i, acc.phase, ctl, p.guard, 46);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       uint32_t o[kPairTok / 4];                    // two tokens a register
 #pragma unroll
-      for (int c = 0; c < kPairTok / 2; c += 32) {
-        float v[32];
-        tmem_ld<32>(lane_addr + c, v);
+      for (int c = 0; c < kPairTok / 2; c += 8)
+        if (c < half) {
+          float v[8];
+          tmem_ld<8>(lane_addr + acc.column() + static_cast<uint32_t>(c), v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[c / 2 + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-      }
+          for (int i = 0; i < 4; ++i) o[c / 2 + i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(acce, 0));
+      if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(acce + 8u * acc.i, 0));
       const int f = ft * kPairFeat + static_cast<int>(rank) * kTcM + static_cast<int>(quad) * 32 + lane;
-      const int t0 = tt * kPairTok + c0;
+      const int t0 = tt * p.ntok + c0;
       if (f < p.nfeat) {
         uint16_t *y = reinterpret_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0) * p.nfeat + f;
         const int64_t ld = p.nfeat;
-        const int live = p.T - t0;
+        const int live = min(p.T - t0, half);
 #pragma unroll
         for (int i = 0; i < kPairTok / 4; ++i, y += 2 * ld) {
           if (2 * i < live) y[0] = static_cast<uint16_t>(o[i]);
@@ -694,7 +717,7 @@ template <bool TRANS>
 dora_status launch_pairs(const void *q, const void *wq, int64_t out, int64_t in, MmParams p, int pairs,
                          cudaStream_t cs) {
   CUtensorMap mW, mX;
-  if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, p.T, p.kdim, 128)) return DORA_ERR_CUDA;
+  if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, p.T, p.kdim, p.ntok / 2)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   pair_config(&cfg, attr, p.tiles < pairs ? p.tiles : pairs, cs);
@@ -727,12 +750,28 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   p.wscale = static_cast<const uint8_t *>(wscale);
   p.y = static_cast<__nv_bfloat16 *>(y);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t pair_tiles = dora::ceil_div(p.nfeat, kPairFeat) * dora::ceil_div(T, kPairTok);
   const int pairs = resident_pairs(device, info.sms);
-  if (pairs > 0 && pair_tiles >= pairs && pair_tiles <= kMaxDim) {
-    p.ntiles = static_cast<int>(dora::ceil_div(T, kPairTok));
-    p.tiles = static_cast<int>(pair_tiles);
-    return launch_pairs<TRANS>(q, wq, out, in, p, pairs, cs);
+  if (pairs > 0 && T > 128) {
+    const int64_t ftiles = dora::ceil_div(p.nfeat, kPairFeat);
+    // tokens per tile: the least time over the waves of tiles.  A stage of two
+    // k blocks was measured to take a time in proportion to tokens + 125 (at
+    // 15360 x 8192 x 8192, us a stage: 0.40, 0.48, 0.58, 0.70 with 64, 128, 176
+    // and 224 tokens), and 10 more with one accumulator
+    int64_t best = 0;
+    for (int n = 64; n <= kPairTok; n += 16) {
+      const int64_t waves = dora::ceil_div(ftiles * dora::ceil_div(T, n), pairs);
+      const int64_t cost = waves * (n + 125 + (n > kPairTwo ? 10 : 0));
+      if (best == 0 || cost < best) {
+        best = cost;
+        p.ntok = n;
+      }
+    }
+    p.ntiles = static_cast<int>(dora::ceil_div(T, p.ntok));
+    const int64_t tiles = ftiles * p.ntiles;
+    if (tiles <= kMaxDim) {
+      p.tiles = static_cast<int>(tiles);
+      return launch_pairs<TRANS>(q, wq, out, in, p, pairs, cs);
+    }
   }
   const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   p.ntiles = static_cast<int>(dora::ceil_div(T, nt));

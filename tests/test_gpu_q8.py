@@ -344,6 +344,30 @@ def test_matmul(T, out, inp, trans):
     assert torch.equal(y, run_matmul(*d, trans, 0xff))
 
 
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("T,feat,k", [
+    (2500, 2064, 272),       # odd numbers of everything; a last feature tile of 16, k of 2 blocks and a bit
+    (1120, 4096, 128),       # whole tiles, one k block
+    (1121, 4112, 384),       # one token over, one 16 of features over
+    (7000, 784, 1552),       # few features; k ends inside a group of four blocks
+    (225, 20000, 528),       # two token tiles, the last of one token
+])
+def test_matmul_many_tiles(T, feat, k, trans):
+    """Enough tiles for the kernel on CTA pairs."""
+    out, inp = (k, feat) if trans else (feat, k)
+    h = _matmul_inputs(T, out, inp, trans, T + feat)
+    d = [u8_dev(a) for a in h]
+    y = run_matmul(*d, trans)
+    assert_no_device_error()
+    check_product("y", to_f64(y), *h, trans)
+    assert torch.equal(y, run_matmul(*d, trans, 0xff))
+    h[0][T // 2, 5] = 0x7f
+    z = run_matmul(*[u8_dev(a) for a in h], trans)
+    assert torch.isnan(z[T // 2]).all()
+    z[T // 2] = y[T // 2]
+    assert torch.equal(z, y)
+
+
 def _drawn(k):
     rng = np.random.default_rng(20261206 + k)
     return int(np.exp(rng.uniform(0, np.log(1500)))), 16 * int(rng.integers(1, 120)), 16 * int(rng.integers(1, 120))
