@@ -139,6 +139,10 @@ def _stream(stream) -> int:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
+    # the raw handle where torch gives it: building a Stream object takes 3 us a call
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 

@@ -97,6 +97,12 @@ __device__ __forceinline__ uint32_t idesc_q8(int m, int n, uint32_t byte, bool a
          | (static_cast<uint32_t>(m >> 4) << 24)
          | (byte << 29);                              // A's scale byte
 }
+// a box into L2
+__device__ __forceinline__ void prefetch_box_2d(const CUtensorMap *map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -190,6 +196,15 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / csize);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / csize);
   bool ok = true;
+  // the launch before this one may still run.  Until it has ended nothing is
+  // read or written here, but the first boxes of W are on their way into L2
+  pdl_trigger();
+  if (warp == 0 && elect_one())
+    for (int kb = kb0; kb < kb1 && kb < kb0 + S; ++kb) {
+      if (TRANS) prefetch_box_2d(&mW, mt * kTcM, kb * kKB);
+      else prefetch_box_2d(&mW, kb * kKB, mt * kTcM);
+    }
+  pdl_wait();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -646,17 +661,19 @@ dora_status launch_split(const CUtensorMap &mW, const CUtensorMap &mX, MmParams 
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const size_t smem = split_smem(NT, p.stages);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * cluster));
   cfg.blockDim = dim3(kSplitThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = cs;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kern, mW, mX, p) != cudaSuccess) {
     cudaGetLastError();
     return DORA_ERR_CUDA;
