@@ -246,7 +246,8 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  pdl_trigger();   // grad_join_kernel's launch overlaps this kernel; it waits for its end
+  pdl_trigger();    // grad_join_kernel's launch overlaps this kernel; it waits for its end
+  pdl_wait();       // the set-up above overlaps the end of the launch before
   const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
   const int64_t u0 = first_unit(units, blockIdx.x, gridDim.x);
   const int nu = static_cast<int>(first_unit(units, blockIdx.x + 1, gridDim.x) - u0);
@@ -600,22 +601,27 @@ template <int NC>
 dora_status launch_grad(const CUtensorMap &mX, const CUtensorMap &mD, GradParams p, int ctas, cudaStream_t cs) {
   constexpr Rings kR = rings_of(4 * NC);
   const size_t smem = 1024 + kR.x * (kRawBytes + kFactorBytes) + static_cast<size_t>(kR.d) * p.boxes * kBox + 512;
-  lora_grad_kernel<NC><<<static_cast<unsigned>(ctas), kThreadsG, smem, cs>>>(mX, mD, p);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreadsG);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = cs;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, lora_grad_kernel<NC>, mX, mD, p) != cudaSuccess) {
+    cudaGetLastError();
+    return DORA_ERR_CUDA;
+  }
   dora::count_launches(1);
-  if (cudaGetLastError() != cudaSuccess) return DORA_ERR_CUDA;
   // no tile is cut when every CTA's run is a whole number of tiles
   const int64_t tiles = static_cast<int64_t>(p.mtiles) * p.ntiles;
   if (tiles % ctas != 0) {
-    // its launch overlaps the end of the first kernel
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * dora::ceil_div(p.ncols, kJoin)));
     cfg.blockDim = dim3(256);
-    cfg.stream = cs;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, grad_join_kernel, p, ctas) != cudaSuccess) return DORA_ERR_CUDA;
     dora::count_launches(1);
   }

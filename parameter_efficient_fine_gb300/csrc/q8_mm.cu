@@ -456,6 +456,8 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   cluster_sync();   // both CTAs' barriers are initialised before either signals the other's
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  pdl_trigger();
+  pdl_wait();       // the set-up above overlaps the end of the launch before
   const int pair = static_cast<int>(blockIdx.x / 2), npairs = static_cast<int>(gridDim.x / 2);
   const int ftiles = p.tiles / p.ntiles, stages = (p.kblocks + kPairKB - 1) / kPairKB, groups = (p.kblocks + 3) / 4;
   // tile t: groups of kGroupF feature tiles, all token tiles of a group in turn
@@ -704,8 +706,10 @@ void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int pairs, 
   cfg->blockDim = dim3(kPairThreads);
   cfg->dynamicSmemBytes = kPairSmem;
   cfg->stream = cs;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg->attrs = attr;
-  cfg->numAttrs = 1;
+  cfg->numAttrs = 2;
 }
 
 // pairs that are resident at once (a pair takes every npairs-th tile, so one
@@ -718,7 +722,7 @@ int resident_pairs(int device, int sms) {
   if (device < 0 || device >= 64) return 0;
   if (known[device] == 0) {
     cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     pair_config(&cfg, attr, sms / 2, nullptr);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, q8_pair_kernel<false>, &cfg) != cudaSuccess) {
@@ -736,7 +740,7 @@ dora_status launch_pairs(const void *q, const void *wq, int64_t out, int64_t in,
   CUtensorMap mW, mX;
   if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, p.T, p.kdim, p.ntok / 2)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   pair_config(&cfg, attr, p.tiles < pairs ? p.tiles : pairs, cs);
   if (cudaLaunchKernelEx(&cfg, q8_pair_kernel<TRANS>, mW, mX, p) != cudaSuccess) {
     cudaGetLastError();
