@@ -58,16 +58,33 @@ template <> struct QPiece<1> {
   static __device__ __forceinline__ void dequant(Raw r, float s, float (&v)[1]) { v[0] = dequant2(r, s).x; }
 };
 
-// scale byte of the 128-column block that this thread's VEC values are part
-// of: the maximum over the 128 / VEC neighbouring threads that hold it.  All
-// threads of the warp call it; one past the row's end passes zeros
+// largest `m` over the 128 / VEC neighbouring threads that hold a 128-column
+// block.  All threads of the warp call it
 template <int VEC>
-__device__ __forceinline__ uint32_t block_scale(const float (&v)[VEC]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < VEC; ++k) m = max(m, mag_bits(v[k]));
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
 #pragma unroll
   for (int o = 64 / VEC; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+// scale byte of the 128-column block that this thread's VEC values are part
+// of; one past the row's end passes zeros.  The maximum passes over NaNs but
+// not over infinities: a warp that meets one takes the maximum again without
+// them and turns them into NaNs
+template <int VEC>
+__device__ __forceinline__ uint32_t block_scale(float (&v)[VEC]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) top = fmaxf(top, fabsf(v[k]));
+  uint32_t m = block_max<VEC>(__float_as_uint(top));
+  if (__any_sync(0xffffffffu, m == kInfBits)) [[unlikely]] {
+    m = 0;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      m = max(m, finite_bits(v[k]));
+      v[k] = inf_to_nan(v[k]);
+    }
+    m = block_max<VEC>(m);
+  }
   return scale_byte(m);
 }
 
@@ -82,7 +99,9 @@ q8_fwd_kernel(const Act *__restrict__ base, const Act *__restrict__ lora, const 
               int64_t T, int64_t out, Act *__restrict__ y, uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
   using IO = Io<Act, VEC>;
   using QP = QPiece<VEC>;
-  constexpr int U = 4;               // token rows in flight per thread
+  // token rows in flight per thread (15360 x 8192 bf16: store 66, 62, 63, 68 us
+  // and compose 150, 137, 141, 146 us with 2, 3, 4 and 8)
+  constexpr int U = 3;
   constexpr int kPer = kQBlock / VEC;   // threads per scale
   const int64_t ncg = out / VEC;
   const int64_t cg = (int64_t)blockIdx.x * kBX + threadIdx.x;
@@ -169,7 +188,7 @@ q8_fwd_ragged_kernel(const Act *__restrict__ base, const Act *__restrict__ lora,
         }
       }
     }
-    uint32_t m = max(max(mag_bits(v[0]), mag_bits(v[1])), max(mag_bits(v[2]), mag_bits(v[3])));
+    uint32_t m = max(max(finite_bits(v[0]), finite_bits(v[1])), max(finite_bits(v[2]), finite_bits(v[3])));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t sc = scale_byte(m);
@@ -178,7 +197,7 @@ q8_fwd_ragged_kernel(const Act *__restrict__ base, const Act *__restrict__ lora,
     for (int k = 0; k < 4; ++k) {
       const int64_t c = blk * kQBlock + 32 * k + threadIdx.x;
       if (c < out) {
-        q[t * out + c] = static_cast<uint8_t>(quant2(v[k], 0.0f, inv));
+        q[t * out + c] = static_cast<uint8_t>(quant2(inf_to_nan(v[k]), 0.0f, inv));
         const float yk[1] = {yv[k]};
         if (COMPOSE) IO::store(y, t * out + c, IO::pack(yk));
       }
@@ -203,7 +222,7 @@ q8_store_tile_kernel(const Act *__restrict__ x, int64_t rows, int64_t cols, uint
       const int64_t c = c0 + 32 * k + threadIdx.x;
       float v[1] = {0.0f};
       if (c < cols) IO::unpack(IO::load(x, r * cols + c), v);
-      m = max(m, mag_bits(v[0]));
+      m = max(m, finite_bits(v[0]));
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -220,7 +239,7 @@ q8_store_tile_kernel(const Act *__restrict__ x, int64_t rows, int64_t cols, uint
       if (c < cols) {
         float v[1];
         IO::unpack(IO::load(x, r * cols + c), v);
-        q[r * cols + c] = static_cast<uint8_t>(quant2(v[0], 0.0f, inv));
+        q[r * cols + c] = static_cast<uint8_t>(quant2(inf_to_nan(v[0]), 0.0f, inv));
       }
     }
   if (threadIdx.x == 0 && threadIdx.y == 0) scale[blockIdx.x] = static_cast<uint8_t>(sc);
@@ -235,7 +254,7 @@ q8_load_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale,
                Act *__restrict__ x) {
   using IO = Io<Act, VEC>;
   using QP = QPiece<VEC>;
-  constexpr int U = 4;
+  constexpr int U = 2;   // 15360 x 8192 bf16: 65, 65, 73, 85 us with 1, 2, 4 and 8
   const int64_t cg = (int64_t)blockIdx.x * kBX + threadIdx.x;
   if (cg >= out / VEC) return;
   const int64_t lanes = (int64_t)gridDim.y * kBY;

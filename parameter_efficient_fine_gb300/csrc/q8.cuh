@@ -21,11 +21,12 @@ namespace {
 constexpr int kQBlock = 128;       // columns per scale
 constexpr int kMinScale = 10;      // 2^-117
 
-// bits of |v| for the block maximum; 0 for a NaN or an infinity
-__device__ __forceinline__ uint32_t mag_bits(float v) {
+// bits of |v|; 0 for a NaN or an infinity
+__device__ __forceinline__ uint32_t finite_bits(float v) {
   const uint32_t a = __float_as_uint(v) & 0x7fffffffu;
   return a < 0x7f800000u ? a : 0u;
 }
+constexpr uint32_t kInfBits = 0x7f800000u;
 // scale byte of a block whose largest finite magnitude has the bits `amax`:
 // the exponent rounded up past 1.75, minus 8
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
@@ -35,15 +36,15 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
 __device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// two values / scale as E4M3 bytes (a low, b high).  The sum with 0 * v turns
-// an infinity into NaN, which the saturating conversion keeps
+// two values / scale as E4M3 bytes (a low, b high); a NaN gives 0x7f
 __device__ __forceinline__ uint32_t quant2(float a, float b, float inv) {
-  const float2 u = make_float2(fmaf(a, 0.0f, a * inv), fmaf(b, 0.0f, b * inv));
-  return __nv_cvt_float2_to_fp8x2(u, __NV_SATFINITE, __NV_E4M3);
+  return __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ uint32_t quant4(const float *v, float inv) {
   return quant2(v[0], v[1], inv) | (quant2(v[2], v[3], inv) << 16);
 }
+// an infinity as the NaN that it is stored as (the conversion would saturate it)
+__device__ __forceinline__ float inf_to_nan(float v) { return fmaf(v, 0.0f, v); }
 // two E4M3 bytes (low half of w) times the scale
 __device__ __forceinline__ float2 dequant2(uint32_t w, float s) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);

@@ -1,6 +1,6 @@
 """torch.library registration of the DoRA hot path (integration only).
 
-Seven custom ops; each allocates its outputs (and the library's workspace)
+The custom ops; each allocates its outputs (and the library's workspace)
 with torch and calls the C entry points of the same names on the current CUDA
 stream.  No arithmetic happens here:
 
@@ -11,6 +11,14 @@ stream.  No arithmetic happens here:
   torch.ops.dora.compose_bwd(dy, base, lora, g, norm, s) -> (d_base, d_lora, d_mag)
   torch.ops.dora.norm_factored_bwd(W0, A, B, norm, g, d_mag, s) -> (dA, dB)   (through the norm)
   torch.ops.dora.module(base, lora, W0, A, B, m, s) -> (y, norm, g)           (norm not detached)
+  torch.ops.dora.q8_store(x, block_rows) -> (q, scale)         (x in 8 bits: E4M3, a scale per 128)
+  torch.ops.dora.q8_load(q, scale, block_rows, dtype) -> x
+  torch.ops.dora.compose_q8(base, lora, m, g, norm, s) -> (y, vq, vscale)     (v = base + s lora in 8 bits)
+  torch.ops.dora.compose_bwd_q8(dy, vq, vscale, g, norm, s) -> (d_base, d_lora, d_mag)
+  torch.ops.dora.matmul_q8(xq, xscale, wq, wscale) -> y        (x W^T, both in 8 bits)
+  torch.ops.dora.matmul_q8_t(dyq, dyscale, wq, wscale) -> dx   (dy W)
+  torch.ops.dora.lora_grad_q8(dxa, xq, xscale) -> dA           (dxa^T x)
+  torch.ops.dora.linear_q8(x, wq, wscale, A, B, m, g, norm, s) -> (y, ...)    (the layer on those)
 
 ``compose`` is differentiable in base, lora and m.  It takes m beside g (the
 norm op's output g = m / norm) so that autograd can deliver dL/dm: with the
@@ -26,6 +34,14 @@ lora, A, B and m.  Its backward is one dora_compose_bwd call followed, when A
 or B needs a gradient, by one dora_norm_factored_bwd call on the d_mag it
 returned (dL/dn = -g d_mag); its norm and g outputs are not differentiable.
 
+``compose_q8`` is ``compose`` that keeps one byte an element for its backward
+(v in 8 bits) instead of base and lora.  ``linear_q8`` is the whole layer on a
+frozen weight in 8 bits: x goes into 8 bits once, feeds the base product from
+there and stays there for the gradient of A; what it holds from forward to
+backward is x and v in 8 bits and xa.  It is differentiable in x, A, B and m;
+rounding to 8 bits passes gradients through unchanged, and dy g (the gradient
+of base) is itself rounded to 8 bits for dx.
+
 Inputs must be contiguous, row-major and on one CUDA device (the C ABI's
 layout); m, n0sq, norm and g are float32, the weights float32 (bfloat16 for
 the _bf16 norm and row_sumsq), activations float32 or bfloat16.
@@ -35,12 +51,16 @@ from __future__ import annotations
 import torch
 from torch import Tensor
 
-from . import (dora_compose_bwd, dora_compose_bwd_workspace, dora_compose_fwd, dora_norm_factored,
+from . import (dora_compose_bwd, dora_compose_bwd_q8, dora_compose_bwd_q8_workspace, dora_compose_bwd_workspace,
+               dora_compose_fwd, dora_compose_fwd_q8, dora_lora_grad_q8, dora_lora_grad_q8_workspace, dora_matmul_q8,
+               dora_matmul_q8_t, dora_matmul_q8_t_workspace, dora_matmul_q8_workspace, dora_norm_factored,
                dora_norm_factored_bf16, dora_norm_factored_bf16_workspace, dora_norm_factored_bwd,
-               dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_row_sumsq_bf16)
+               dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_q8_load, dora_q8_store,
+               dora_row_sumsq_bf16)
 
 __all__ = ["norm_factored", "row_sumsq", "norm_factored_bf16", "compose", "compose_bwd", "norm_factored_bwd",
-           "module", "dora_module"]
+           "module", "dora_module", "q8_store", "q8_load", "compose_q8", "compose_bwd_q8", "matmul_q8", "matmul_q8_t",
+           "lora_grad_q8", "linear_q8", "dora_linear_q8"]
 
 
 def _contig(name: str, *ts: Tensor) -> None:
@@ -222,3 +242,197 @@ def dora_module(base: Tensor, lora: Tensor, W0: Tensor, A: Tensor, B: Tensor, m:
         return module(base, lora, W0.detach(), A, B, m, s)[0]
     norm, g = norm_factored(W0.detach(), A.detach(), B.detach(), m.detach(), s)
     return compose(base, lora, m, g, norm, s)
+
+
+# ---------------------------------------------------------------------------
+# 8 bits: E4M3 with a power-of-two scale per 128 columns (include/dora.h)
+# ---------------------------------------------------------------------------
+def _scale_shape(rows: int, cols: int, block_rows: int) -> tuple[int, int]:
+    return -(-rows // block_rows), -(-cols // 128)
+
+
+def _workspace(nbytes: int, like: Tensor) -> Tensor:
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+
+
+@torch.library.custom_op("dora::q8_store", mutates_args=(), device_types="cuda")
+def q8_store(x: Tensor, block_rows: int) -> tuple[Tensor, Tensor]:
+    """x [rows, cols] in 8 bits: (q, scale), a scale per block_rows (1 or 128) x 128 elements."""
+    _contig("q8_store", x)
+    q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    scale = torch.empty(_scale_shape(*x.shape, block_rows), dtype=torch.uint8, device=x.device)
+    dora_q8_store(x, block_rows, q, scale)
+    return q, scale
+
+
+@q8_store.register_fake
+def _q8_store_fake(x, block_rows):
+    return x.new_empty(x.shape, dtype=torch.uint8), x.new_empty(_scale_shape(*x.shape, block_rows), dtype=torch.uint8)
+
+
+@torch.library.custom_op("dora::q8_load", mutates_args=(), device_types="cuda")
+def q8_load(q: Tensor, scale: Tensor, block_rows: int, dtype: torch.dtype) -> Tensor:
+    """The values of an 8-bit form, float32 or bfloat16."""
+    _contig("q8_load", q, scale)
+    x = torch.empty(q.shape, dtype=dtype, device=q.device)
+    dora_q8_load(q, scale, block_rows, x)
+    return x
+
+
+@q8_load.register_fake
+def _q8_load_fake(q, scale, block_rows, dtype):
+    return q.new_empty(q.shape, dtype=dtype)
+
+
+@torch.library.custom_op("dora::compose_bwd_q8", mutates_args=(), device_types="cuda")
+def compose_bwd_q8(dy: Tensor, vq: Tensor, vscale: Tensor, g: Tensor, norm: Tensor,
+                   s: float) -> tuple[Tensor, Tensor, Tensor]:
+    """d_base = g dy, d_lora = s g dy, d_mag = sum_t dy v / norm from the 8-bit v."""
+    _contig("compose_bwd_q8", dy, vq, vscale, g, norm)
+    d_base = torch.empty_like(dy)
+    d_lora = torch.empty_like(dy)
+    d_mag = torch.empty(dy.shape[1], device=dy.device, dtype=torch.float32)
+    dora_compose_bwd_q8(dy, vq, vscale, g, norm, s, d_base, d_lora, d_mag,
+                        _workspace(dora_compose_bwd_q8_workspace(*dy.shape), dy))
+    return d_base, d_lora, d_mag
+
+
+@compose_bwd_q8.register_fake
+def _compose_bwd_q8_fake(dy, vq, vscale, g, norm, s):
+    return torch.empty_like(dy), torch.empty_like(dy), dy.new_empty(dy.shape[1], dtype=torch.float32)
+
+
+@torch.library.custom_op("dora::compose_q8", mutates_args=(), device_types="cuda")
+def compose_q8(base: Tensor, lora: Tensor, m: Tensor, g: Tensor, norm: Tensor,
+               s: float) -> tuple[Tensor, Tensor, Tensor]:
+    """compose, with v = base + s lora kept in 8 bits for the backward: (y, vq, vscale)."""
+    _contig("compose_q8", base, lora, g)
+    y = torch.empty_like(base)
+    vq = torch.empty(base.shape, dtype=torch.uint8, device=base.device)
+    vscale = torch.empty(_scale_shape(*base.shape, 1), dtype=torch.uint8, device=base.device)
+    dora_compose_fwd_q8(base, lora, g, s, y, vq, vscale)
+    return y, vq, vscale
+
+
+@compose_q8.register_fake
+def _compose_q8_fake(base, lora, m, g, norm, s):
+    return (torch.empty_like(base), base.new_empty(base.shape, dtype=torch.uint8),
+            base.new_empty(_scale_shape(*base.shape, 1), dtype=torch.uint8))
+
+
+def _compose_q8_setup(ctx, inputs, output):
+    _, _, _, g, norm, s = inputs
+    _, vq, vscale = output
+    ctx.save_for_backward(vq, vscale, g, norm)
+    ctx.s = s
+    ctx.mark_non_differentiable(vq, vscale)
+
+
+def _compose_q8_backward(ctx, dy, _vq, _vscale):
+    vq, vscale, g, norm = ctx.saved_tensors
+    d_base, d_lora, d_mag = compose_bwd_q8(dy.contiguous(), vq, vscale, g, norm, ctx.s)
+    return d_base, d_lora, d_mag, None, None, None
+
+
+compose_q8.register_autograd(_compose_q8_backward, setup_context=_compose_q8_setup)
+
+
+@torch.library.custom_op("dora::matmul_q8", mutates_args=(), device_types="cuda")
+def matmul_q8(xq: Tensor, xscale: Tensor, wq: Tensor, wscale: Tensor) -> Tensor:
+    """x W^T in bfloat16, x and W in 8 bits (block_rows 1 and 128)."""
+    _contig("matmul_q8", xq, xscale, wq, wscale)
+    T, (out, inp) = xq.shape[0], wq.shape
+    y = torch.empty(T, out, dtype=torch.bfloat16, device=xq.device)
+    dora_matmul_q8(xq, xscale, wq, wscale, y, _workspace(dora_matmul_q8_workspace(T, out, inp), xq))
+    return y
+
+
+@matmul_q8.register_fake
+def _matmul_q8_fake(xq, xscale, wq, wscale):
+    return xq.new_empty(xq.shape[0], wq.shape[0], dtype=torch.bfloat16)
+
+
+@torch.library.custom_op("dora::matmul_q8_t", mutates_args=(), device_types="cuda")
+def matmul_q8_t(dyq: Tensor, dyscale: Tensor, wq: Tensor, wscale: Tensor) -> Tensor:
+    """dy W in bfloat16, dy and the same W in 8 bits."""
+    _contig("matmul_q8_t", dyq, dyscale, wq, wscale)
+    T, (out, inp) = dyq.shape[0], wq.shape
+    dx = torch.empty(T, inp, dtype=torch.bfloat16, device=dyq.device)
+    dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx, _workspace(dora_matmul_q8_t_workspace(T, out, inp), dyq))
+    return dx
+
+
+@matmul_q8_t.register_fake
+def _matmul_q8_t_fake(dyq, dyscale, wq, wscale):
+    return dyq.new_empty(dyq.shape[0], wq.shape[1], dtype=torch.bfloat16)
+
+
+@torch.library.custom_op("dora::lora_grad_q8", mutates_args=(), device_types="cuda")
+def lora_grad_q8(dxa: Tensor, xq: Tensor, xscale: Tensor) -> Tensor:
+    """dA = dxa^T x in float32, dxa bfloat16, x in 8 bits."""
+    _contig("lora_grad_q8", dxa, xq, xscale)
+    (T, r), inp = dxa.shape, xq.shape[1]
+    dA = torch.empty(r, inp, dtype=torch.float32, device=dxa.device)
+    dora_lora_grad_q8(dxa, xq, xscale, dA, _workspace(dora_lora_grad_q8_workspace(T, inp, r), dxa))
+    return dA
+
+
+@lora_grad_q8.register_fake
+def _lora_grad_q8_fake(dxa, xq, xscale):
+    return dxa.new_empty(dxa.shape[1], xq.shape[1], dtype=torch.float32)
+
+
+@torch.library.custom_op("dora::linear_q8", mutates_args=(), device_types="cuda")
+def linear_q8(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Tensor, g: Tensor, norm: Tensor,
+              s: float) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
+    """The layer's output y and what its backward needs: (y, xq, xscale, vq, vscale, xa)."""
+    xq, xscale = q8_store(x, 1)
+    xa = x @ A.to(x.dtype).t()
+    y, vq, vscale = compose_q8(matmul_q8(xq, xscale, wq, wscale), xa @ B.to(x.dtype).t(), m, g, norm, s)
+    return y, xq, xscale, vq, vscale, xa
+
+
+@linear_q8.register_fake
+def _linear_q8_fake(x, wq, wscale, A, B, m, g, norm, s):
+    T, inp = x.shape
+    out = wq.shape[0]
+    u8 = torch.uint8
+    return (x.new_empty(T, out), x.new_empty(T, inp, dtype=u8), x.new_empty(_scale_shape(T, inp, 1), dtype=u8),
+            x.new_empty(T, out, dtype=u8), x.new_empty(_scale_shape(T, out, 1), dtype=u8), x.new_empty(T, A.shape[0]))
+
+
+def _linear_q8_setup(ctx, inputs, output):
+    _, wq, wscale, A, B, _, g, norm, s = inputs
+    _, xq, xscale, vq, vscale, xa = output
+    ctx.save_for_backward(xq, xscale, vq, vscale, xa, wq, wscale, A, B, g, norm)
+    ctx.s = s
+    ctx.mark_non_differentiable(xq, xscale, vq, vscale, xa)
+
+
+def _linear_q8_backward(ctx, dy, *_):
+    xq, xscale, vq, vscale, xa, wq, wscale, A, B, g, norm = ctx.saved_tensors
+    need = ctx.needs_input_grad
+    d_base, d_lora, d_mag = compose_bwd_q8(dy.contiguous(), vq, vscale, g, norm, ctx.s)
+    dx = dA = dB = None
+    if need[4]:
+        dB = (d_lora.t() @ xa).to(B.dtype)
+    if need[0] or need[3]:
+        dxa = d_lora @ B.to(d_lora.dtype)
+        if need[3]:
+            dA = lora_grad_q8(dxa, xq, xscale).to(A.dtype)
+        if need[0]:
+            dx = matmul_q8_t(*q8_store(d_base, 1), wq, wscale) + dxa @ A.to(dxa.dtype)
+    return dx, None, None, dA, dB, d_mag, None, None, None
+
+
+linear_q8.register_autograd(_linear_q8_backward, setup_context=_linear_q8_setup)
+
+
+def dora_linear_q8(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Tensor, g: Tensor, norm: Tensor,
+                   s: float) -> Tensor:
+    """y = g (x W0^T + s x A^T B^T) for a bfloat16 x and a frozen W0 in 8 bits (q8_store(W0, 128)).
+
+    norm and g = m / norm come from one of the norm ops on the values of the
+    8-bit weight (q8_load is exact in bfloat16) and carry no gradient; x, A, B
+    and m do.  in and out are multiples of 16, the rank a multiple of 8."""
+    return linear_q8(x, wq, wscale, A, B, m, g, norm, s)[0]

@@ -163,3 +163,31 @@ def test_wrong_shapes_and_types_are_refused():
         dora.dora_matmul_q8_t(q, sc, w, wsc, x, ws, stream=0)
     with pytest.raises(ValueError, match="expected"):
         dora.dora_lora_grad_q8(torch.zeros(4, 8), q, sc, torch.zeros(8, 256), ws, stream=0)
+
+
+def test_ops_registered_and_fake_shapes():
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    import parameter_efficient_fine_gb300.ops  # noqa: F401  (registers torch.ops.dora.*)
+
+    bf, u8 = torch.bfloat16, torch.uint8
+    with FakeTensorMode():
+        x = torch.empty(8, 272, device="cuda", dtype=bf)
+        q, sc = torch.ops.dora.q8_store(x, 1)
+        assert q.shape == (8, 272) and sc.shape == (8, 3) and q.dtype == sc.dtype == u8
+        wq, wsc = torch.ops.dora.q8_store(torch.empty(144, 272, device="cuda"), 128)
+        assert wq.shape == (144, 272) and wsc.shape == (2, 3)
+        assert torch.ops.dora.q8_load(q, sc, 1, torch.float32).dtype == torch.float32
+        y = torch.ops.dora.matmul_q8(q, sc, wq, wsc)
+        assert y.shape == (8, 144) and y.dtype == bf
+        g = torch.empty(144, device="cuda")
+        z, vq, vsc = torch.ops.dora.compose_q8(y, y, g, g, g, 1.0)
+        assert z.shape == y.shape and vq.shape == y.shape and vsc.shape == (8, 2)
+        db, dl, dm = torch.ops.dora.compose_bwd_q8(y, vq, vsc, g, g, 1.0)
+        assert db.dtype == dl.dtype == bf and dm.shape == (144,) and dm.dtype == torch.float32
+        assert torch.ops.dora.matmul_q8_t(vq, vsc, wq, wsc).shape == (8, 272)
+        dA = torch.ops.dora.lora_grad_q8(torch.empty(8, 16, device="cuda", dtype=bf), q, sc)
+        assert dA.shape == (16, 272) and dA.dtype == torch.float32
+        A, B = torch.empty(16, 272, device="cuda"), torch.empty(144, 16, device="cuda")
+        out = torch.ops.dora.linear_q8(x, wq, wsc, A, B, g, g, g, 1.0)
+        assert out[0].shape == (8, 144) and out[0].dtype == bf and out[5].shape == (8, 16)
