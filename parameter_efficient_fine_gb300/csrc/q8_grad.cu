@@ -27,10 +27,10 @@
 //               stage's 128 scales as bf16 factors in shared memory
 //   warp 1      tensor memory (two window accumulators, a ring of M operands),
 //               MMA issue
-//   warps 2-17  bytes -> bf16, two groups on alternate stages, a lane quadrant
-//               and half of the tokens a warp; window w - 1 out of tensor
-//               memory while window w runs, a quarter of the columns a warp
-//   warp 18     dxa by TMA: 128 tokens x 64 columns a box (16 KB)
+//   warps 2-9   bytes -> bf16, two groups on alternate stages, a lane quadrant a
+//               warp; window w - 1 out of tensor memory while window w runs,
+//               half of the columns a warp
+//   warp 10     dxa by TMA: 128 tokens x 64 columns a box (16 KB)
 // A hand-over through an mbarrier was measured at 230 cycles, and four of them
 // and a load from memory lie on the way of a stage, so each buffer is a ring of
 // its own that is freed as early as it can be: x once it is in registers, dxa
@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kTok = 128;                        // tokens per stage
 constexpr int kShortWin = 256, kLongWin = 512;   // tokens per window
-constexpr int kWorkers = 16;                     // conversion warps, in two groups that take alternate stages
+constexpr int kWorkers = 8;                      // conversion warps, in two groups that take alternate stages
 constexpr int kThreadsG = 96 + 32 * kWorkers;
 constexpr unsigned kRawBytes = kTok * 128;       // 16 KB of x
 constexpr unsigned kBox = kTok * 128;            // 128 tokens x 64 columns of dxa
@@ -192,11 +192,11 @@ __device__ __noinline__ void convert_any(const uint8_t *scale, int nsx, int T, i
   tmem_st_16x256b_x2(to + (16u << 16), o[1]);
 }
 
-// NC: columns of a tile per worker warp (a quarter of the tile's, rounded up)
+// NC: columns of a tile per worker warp (half of the tile's, rounded up)
 template <int NC>
 __global__ void __launch_bounds__(kThreadsG, 1)
 lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mD, const GradParams p) {
-  constexpr int kN = 4 * NC;                             // columns of one window accumulator
+  constexpr int kN = 2 * NC;                             // columns of one window accumulator
   constexpr Rings kR = rings_of(kN);
   constexpr int kUsed = 2 * kN + kOpCols * kR.ops;       // two windows, the M operands
   constexpr int kCols = kUsed <= 256 ? 256 : 512;
@@ -399,9 +399,8 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     // ---------------------------------------------------------------- workers
     const int wk = warp - 2;
     const uint32_t quad = static_cast<uint32_t>(warp & 3);
-    const int nq = wk >> 2;                              // which quarter of the columns
-    const int grp = wk >> 3, nh = nq & 1;                // which stages, which half of their tokens
-    const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(nq * NC);
+    const int grp = wk >> 2;                             // which stages, and which half of the columns
+    const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(grp * NC);
     constexpr int C = NC % 32 == 0 ? 32 : NC % 16 == 0 ? 16 : NC % 8 == 0 ? 8 : 4;
     float sum[NC];
 #pragma unroll
@@ -409,7 +408,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     // this lane's row of a transposed load: lanes 0-7 and 8-15 give the rows of
     // tokens 4 i, 4 i + 1 and 4 i + 2, 4 i + 3 (i < 4) of 16 features, lanes
     // 16-31 the same of the next 16 features
-    const int tok = 64 * nh + 4 * ((lane & 7) >> 1) + (lane & 1) + 2 * ((lane >> 3) & 1);
+    const int tok = 4 * ((lane & 7) >> 1) + (lane & 1) + 2 * ((lane >> 3) & 1);
     const int chunk = 2 * static_cast<int>(quad) + (lane >> 4);
     const uint32_t from_off = static_cast<uint32_t>(tok * 128 + ((chunk ^ (tok & 7)) << 4));
     bool ok = true;
@@ -448,7 +447,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
         const int f = at.mt * kTcM + feature_of(m);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-          const int n = nq * NC + j, col = at.nt * p.ncols + n;
+          const int n = grp * NC + j, col = at.nt * p.ncols + n;
           if (n < p.ncols && col < p.r && f < p.in) p.dA[static_cast<int64_t>(col) * p.in + f] = sum[j];
         }
       } else {
@@ -456,7 +455,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
         float *dst = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (from_start ? 1 : 0)) * p.ncols * kTcM + m;
 #pragma unroll
         for (int j = 0; j < NC; ++j)
-          if (nq * NC + j < p.ncols) dst[(nq * NC + j) * kTcM] = sum[j];
+          if (grp * NC + j < p.ncols) dst[(grp * NC + j) * kTcM] = sum[j];
       }
 #pragma unroll
       for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
@@ -486,17 +485,17 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       const uint32_t from = x_at + x.i * kRawBytes + from_off;
       const uint8_t *fa = factors + x.i * kFactorBytes;
       const bool large = *reinterpret_cast<const uint32_t *>(fa + 2 * kTok) != 0;
-      const uint32_t to = tmem + ((quad * 32u) << 16) + 2 * kN + static_cast<uint32_t>(kOpCols * op.i + 32 * nh);
-      // this warp's half of the tokens, 32 at a time, as 16 x 16 blocks
+      const uint32_t to = tmem + ((quad * 32u) << 16) + 2 * kN + static_cast<uint32_t>(kOpCols * op.i);
+      // 32 tokens at a time, as 16 x 16 blocks
 #pragma unroll
-      for (int g2 = 0; g2 < 2; ++g2) {
+      for (int g2 = 0; g2 < kTok / 32; ++g2) {
         uint32_t raw[2][4], o[2][8];   // o[h]: the 16 columns of feature block h
         uint32_t top = 0;
 #pragma unroll
         for (int g = 0; g < 2; ++g) ldmatrix_x4_trans(from + 2048u * (2 * g2 + g), raw[g]);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint2 up = *reinterpret_cast<const uint2 *>(fa + 2 * (64 * nh + 16 * (2 * g2 + g) + 4 * (lane & 3)));
+          const uint2 up = *reinterpret_cast<const uint2 *>(fa + 2 * (16 * (2 * g2 + g) + 4 * (lane & 3)));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int h = i / 2, half = i % 2;
@@ -518,7 +517,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
           tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
         } else {
           convert_any(p.scale + at_unit.mt, p.nsx, p.T,
-                      at_unit.w * p.win + k * kTok + 64 * nh + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
+                      at_unit.w * p.win + k * kTok + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
                       from + 4096u * g2 + 2048u, to + 16u * g2);
         }
       }
@@ -530,8 +529,10 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       if (lane == 0) mbar_arrive(conv0 + 8u * op.i);
       x.next(2);
       op.next(2);
-      // the windows before this one, now that this one keeps the tensor core fed
-      while (ok && flushed < wi) ok = flush();
+      // the windows before this one, after this warp's last stage of it: their
+      // MMAs are done by then, and the one after it starts no earlier (a tile's
+      // only window without a stage for this warp is its last, which `finish` reads)
+      while (ok && flushed < wi && k + 2 >= ns) ok = flush();
       if (!ok) break;
       k += 2;
     }
@@ -599,7 +600,7 @@ int tile_columns(int64_t r) {
 
 template <int NC>
 dora_status launch_grad(const CUtensorMap &mX, const CUtensorMap &mD, GradParams p, int ctas, cudaStream_t cs) {
-  constexpr Rings kR = rings_of(4 * NC);
+  constexpr Rings kR = rings_of(2 * NC);
   const size_t smem = 1024 + kR.x * (kRawBytes + kFactorBytes) + static_cast<size_t>(kR.d) * p.boxes * kBox + 512;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -660,8 +661,8 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
                                                                                                   : DORA_ERR_CUDA;
   GradParams p = {};
   static const void *const kernels[] = {
-      (const void *)lora_grad_kernel<4>, (const void *)lora_grad_kernel<8>, (const void *)lora_grad_kernel<16>,
-      (const void *)lora_grad_kernel<32>, (const void *)lora_grad_kernel<48>};
+      (const void *)lora_grad_kernel<8>, (const void *)lora_grad_kernel<16>, (const void *)lora_grad_kernel<32>,
+      (const void *)lora_grad_kernel<64>, (const void *)lora_grad_kernel<96>};
   st = tc_init(device, &p.guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
   if (st != DORA_OK) return st;
   p.T = static_cast<int>(T);
@@ -684,10 +685,10 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
   const int sms = info.sms < kMaxCtasG ? info.sms : kMaxCtasG;
   const int ctas = units < sms ? static_cast<int>(units) : sms;
-  const int quarter = p.ncols / 4;
-  if (quarter <= 4) return launch_grad<4>(mX, mD, p, ctas, cs);
-  if (quarter <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
-  if (quarter <= 16) return launch_grad<16>(mX, mD, p, ctas, cs);
-  if (quarter <= 32) return launch_grad<32>(mX, mD, p, ctas, cs);
-  return launch_grad<48>(mX, mD, p, ctas, cs);
+  const int half = p.ncols / 2;
+  if (half <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
+  if (half <= 16) return launch_grad<16>(mX, mD, p, ctas, cs);
+  if (half <= 32) return launch_grad<32>(mX, mD, p, ctas, cs);
+  if (half <= 64) return launch_grad<64>(mX, mD, p, ctas, cs);
+  return launch_grad<96>(mX, mD, p, ctas, cs);
 }
