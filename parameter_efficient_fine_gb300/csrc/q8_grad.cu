@@ -54,15 +54,19 @@ constexpr unsigned kRawBytes = kTok * 128;       // 16 KB of x
 constexpr unsigned kBox = kTok * 128;            // 128 tokens x 64 columns of dxa
 constexpr int kMaxR = 1024;
 constexpr int kMaxN = 192;                       // columns of a tile: two windows and the M operands fill tensor memory
-constexpr int kMaxCtasG = 256;
-// Rings, by the columns of a tile: stages of x and of dxa in shared memory,
-// M operands (64 columns) in tensor memory beside two windows of the tile's
-// columns.  x and the operands in even numbers, as two groups take turns
+constexpr int kMaxCtasG = 512;
+// By the columns of a tile: CTAs per SM; stages of x and of dxa in shared
+// memory; M operands (64 columns) in tensor memory beside two windows of the
+// tile's columns.  x and the operands in even numbers, as two groups take
+// turns.  What limits a stage is the length of the roles' instruction chains,
+// so where a CTA needs half of an SM's memory, two share it (r = 16 at 15360 x
+// 8192: 36.5 us against 42.4 with one CTA and twice the rings; at 64 columns the
+// registers that two CTAs leave do not hold the sums)
 struct Rings {
-  int x, d, ops;
+  int per_sm, x, d, ops;
 };
 __host__ __device__ constexpr Rings rings_of(int columns) {
-  return columns > 128 ? Rings{4, 3, 2} : columns > 64 ? Rings{4, 4, 4} : Rings{8, 4, 4};
+  return columns > 128 ? Rings{1, 4, 3, 2} : columns > 64 ? Rings{1, 4, 4, 4} : columns > 32 ? Rings{1, 8, 4, 4} : Rings{2, 4, 2, 2};
 }
 constexpr int kOpCols = kTok / 2;
 // a place in a ring of N
@@ -194,13 +198,13 @@ __device__ __noinline__ void convert_any(const uint8_t *scale, int nsx, int T, i
 
 // NC: columns of a tile per worker warp (half of the tile's, rounded up)
 template <int NC>
-__global__ void __launch_bounds__(kThreadsG, 1)
+__global__ void __launch_bounds__(kThreadsG, rings_of(2 * NC).per_sm)
 lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mD, const GradParams p) {
   constexpr int kN = 2 * NC;                             // columns of one window accumulator
   constexpr Rings kR = rings_of(kN);
   constexpr int kUsed = 2 * kN + kOpCols * kR.ops;       // two windows, the M operands
   constexpr int kCols = kUsed <= 256 ? 256 : 512;
-  static_assert(kUsed <= 512, "tensor memory");
+  static_assert(kUsed <= 512 / kR.per_sm, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t d_stage = p.boxes * kBox;
@@ -683,8 +687,9 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   CUtensorMap mX, mD;
   if (!map_q8(&mX, xq, T, in, kTok) || !make_map(&mD, dxa, true, T, r, r, kTok, 128)) return DORA_ERR_CUDA;
   const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
-  const int sms = info.sms < kMaxCtasG ? info.sms : kMaxCtasG;
-  const int ctas = units < sms ? static_cast<int>(units) : sms;
+  const int room = info.sms * rings_of(p.ncols).per_sm;
+  const int most = room < kMaxCtasG ? room : kMaxCtasG;
+  const int ctas = units < most ? static_cast<int>(units) : most;
   const int half = p.ncols / 2;
   if (half <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
   if (half <= 16) return launch_grad<16>(mX, mD, p, ctas, cs);

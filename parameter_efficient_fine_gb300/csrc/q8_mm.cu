@@ -162,7 +162,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, sff0 = empty0 + 8u * S, sfe0 = sff0 + 8u * kSfSlots,
                  accf = sfe0 + 8u * kSfSlots;
   SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * S + 2 * kSfSlots + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8u * s, 1);
@@ -425,7 +425,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kPairStages, sff0 = empty0 + 8u * kPairStages,
                  sfe0 = sff0 + 8u * kSfSlots, accf = sfe0 + 8u * kSfSlots, acce = accf + 16, fin = acce + 16;
   SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * kPairStages + 2 * kSfSlots + 5);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {

@@ -36,6 +36,11 @@ __device__ __forceinline__ bool loads_withheld(const Guard &g) {
   return *reinterpret_cast<const volatile int *>(g.stall) != 0;
 }
 
+// this thread's warp, as a value that the compiler knows to be the same in all
+// of its lanes
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+}
 // one lane of a converged warp.  The MMA warp runs its loop as a whole and
 // issues under this, so the operands of its instructions stay warp-uniform
 __device__ __forceinline__ bool elect_one() {
