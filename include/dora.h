@@ -389,7 +389,7 @@ dora_status dora_linear_fwd(const void *x, const void *W0, const void *xa, const
  * [rows, cols], and scale, one byte b per block, standing for 2^(b - 127),
  * [ceil(rows / block_rows), ceil(cols / 128)].  block_rows is 1 (an
  * activation: 128 columns of one row) or 128 (a frozen weight: 128 x 128).
- * An element's value is E4M3(q) 2^(b - 127).
+ * An element's value is E4M3(q) 2^(b - 127), b from 1 to 254.
  *
  * The scale of a block is the smallest power of two that brings its largest
  * finite magnitude to at most 448, and at least 2^-117: every value is then
@@ -451,7 +451,9 @@ dora_status dora_compose_bwd_q8(dora_dtype act, const void *grad_out, const void
                                 void *d_base, void *d_lora, float *d_mag,
                                 void *workspace, size_t workspace_bytes, dora_stream_t stream);
 
-/* Bytes of workspace dora_lora_grad_q8 needs (host arithmetic; 0 for an invalid shape). */
+/* Bytes of workspace dora_lora_grad_q8 needs (host arithmetic; 0 for an invalid
+ * shape): fp32 parts of the tiles of dA that several CTAs work on, at most 1024
+ * parts of 128 features by up to 192 columns. */
 size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r);
 
 /*
@@ -461,14 +463,18 @@ size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r);
  *   xscale uint8 [T, ceil(in / 128)]
  *   dA     float32 [r, in]  16-byte aligned, overwritten
  *   workspace  >= dora_lora_grad_q8_workspace(T, in, r) bytes, 256-byte aligned
- *   Sizes: T, in >= 0 (in == 0 is a no-op, T == 0 writes zeros), 1 <= r <= 1024.
+ *   Sizes: T, in >= 0 (in == 0 is a no-op, T == 0 writes zeros) and below
+ *   2^31 - 1023, 1 <= r <= 1024.
+ * x's values are exact in bf16, so every product is; sums are fp32, in chains
+ * of at most 512 tokens that are added up with ordinary rounding.  One launch,
+ * and one that joins the parts of tiles of dA that several CTAs worked on.
  */
 dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const void *xscale,
                               int64_t T, int64_t in, int64_t r, float *dA,
                               void *workspace, size_t workspace_bytes, dora_stream_t stream);
 
-/* Bytes of workspace dora_matmul_q8 and dora_matmul_q8_t need (host
- * arithmetic; 0 for an invalid shape). */
+/* Bytes of workspace dora_matmul_q8 and dora_matmul_q8_t need: none at any size
+ * (the parts of a tile meet on chip); the pointer may be NULL. */
 size_t dora_matmul_q8_workspace(int64_t T, int64_t out, int64_t in);
 size_t dora_matmul_q8_t_workspace(int64_t T, int64_t out, int64_t in);
 
@@ -478,8 +484,14 @@ size_t dora_matmul_q8_t_workspace(int64_t T, int64_t out, int64_t in);
  *   xq  uint8 [T, in]     xscale  uint8 [T, ceil(in / 128)]
  *   wq  uint8 [out, in]   wscale  uint8 [ceil(out / 128), ceil(in / 128)]  (block_rows = 128)
  *   y   bf16 [T, out];  xq, wq and y 16-byte aligned, out % 16 == 0, in % 16 == 0
- *   workspace  >= dora_matmul_q8_workspace(T, out, in) bytes, 256-byte aligned
- *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1.
+ *   workspace  not used (dora_matmul_q8_workspace)
+ *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1, below 2^31 - 1023.
+ * The tensor core multiplies E4M3 by E4M3 and applies both scales (block-scaled
+ * tcgen05.mma); one launch.  Up to 128 tokens the k range is split over a
+ * cluster of up to 8 CTAs and summed in rank order, above that CTA pairs take
+ * 256 features x 64 to 256 tokens.  The launch is a programmatic dependent one: its set-up
+ * overlaps the launch before it, and it reads and writes nothing of the
+ * caller's before that has completed.
  */
 dora_status dora_matmul_q8(const void *xq, const void *xscale, const void *wq, const void *wscale,
                            int64_t T, int64_t out, int64_t in, void *y,
@@ -512,7 +524,8 @@ uint64_t dora_kernel_launches(void);
 /*
  * Testing hook for the failure path; no counterpart in the paper.  With on != 0
  * the tensor-core kernels of later dora_norm_factored, dora_norm_factored_bwd,
- * dora_compose_lora_fwd and dora_linear_fwd calls on the current device
+ * dora_compose_lora_fwd, dora_linear_fwd, dora_lora_grad_q8, dora_matmul_q8 and
+ * dora_matmul_q8_t calls on the current device
  * withhold all their operand loads, so their bounded waits expire after
  * wait_limit_ns (0 = the default of 2 s): the kernels then record a code in the
  * device error word (see dora_device_error), free their tensor memory and

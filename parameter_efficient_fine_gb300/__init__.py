@@ -392,16 +392,18 @@ def _matmul_q8(name: str, q, scale, wq, wscale, y, workspace, stream, out_side: 
     _same(name, (T, out if out_side else inp), torch.bfloat16, y)
     _dense(name, q, scale, wq, wscale, y)
     st = getattr(load_library(), name)(_ptr(q), _ptr(scale), _ptr(wq), _ptr(wscale), T, out, inp, _ptr(y),
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+                                       _ptr(workspace),
+                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                       _stream(stream))
     _check(name, st)
 
 
-def dora_matmul_q8(xq, xscale, wq, wscale, y, workspace, stream=None) -> None:
+def dora_matmul_q8(xq, xscale, wq, wscale, y, workspace=None, stream=None) -> None:
     """y = x W^T for x and W in 8 bits (see include/dora.h)."""
     _matmul_q8("dora_matmul_q8", xq, xscale, wq, wscale, y, workspace, stream, True)
 
 
-def dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx, workspace, stream=None) -> None:
+def dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx, workspace=None, stream=None) -> None:
     """dx = dy W for dy and the same W in 8 bits (see include/dora.h)."""
     _matmul_q8("dora_matmul_q8_t", dyq, dyscale, wq, wscale, dx, workspace, stream, False)
 

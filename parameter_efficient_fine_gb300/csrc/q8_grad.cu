@@ -555,42 +555,47 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
 // columns, the parts of up to kJoinAt CTAs loaded at a time
 constexpr int kJoin = 8, kJoinAt = 4;
 __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p, int ctas) {
-  const int chunks = (p.ncols + kJoin - 1) / kJoin;
-  const int tile = blockIdx.x / chunks;
-  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
-  // the CTA of a unit: first_unit(i) <= unit < first_unit(i + 1), that is
-  // i = ceil((unit + 1) ctas / units) - 1
-  const int64_t u0 = static_cast<int64_t>(tile) * p.windows, u1 = u0 + p.windows;
-  const int i0 = static_cast<int>(((u0 + 1) * ctas - 1) / units), i1 = static_cast<int>((u1 * ctas - 1) / units);
+  __shared__ int owner[2];
+  const int tile = blockIdx.x;
+  if (threadIdx.x < 2) {
+    // the CTA of the tile's first and of its last unit: first_unit(i) <= unit <
+    // first_unit(i + 1), that is i = ceil((unit + 1) ctas / units) - 1.  Two
+    // threads divide (in every thread the divisions were half of this kernel)
+    const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
+    const int64_t next = static_cast<int64_t>(tile) * p.windows + (threadIdx.x == 0 ? 1 : p.windows);
+    owner[threadIdx.x] = static_cast<int>((next * ctas - 1) / units);
+  }
+  __syncthreads();
+  pdl_wait();
+  const int i0 = owner[0], i1 = owner[1];
   const int mt = tile % p.mtiles, nt = tile / p.mtiles;
   const int m = threadIdx.x % kTcM, f = mt * kTcM + feature_of(m);
-  const int n0 = (blockIdx.x % chunks) * kJoin + threadIdx.x / kTcM;
-  const int64_t slot = static_cast<int64_t>(p.ncols) * kTcM;
-  const float *src = p.part + static_cast<int64_t>(n0) * kTcM + m;
-  pdl_wait();
   if (i0 == i1 || f >= p.in) return;
+  const int n0 = blockIdx.y * kJoin + threadIdx.x / kTcM;
+  const int live = (p.ncols - n0 + 1) / 2;                  // of this thread's columns n0, n0 + 2, ...
+  const int64_t slot = static_cast<int64_t>(p.ncols) * kTcM;
+  // the first CTA's part is its second (its run of the tile began at the tile's
+  // start), the others' their first
+  const float *src = p.part + static_cast<int64_t>(i0) * 2 * slot + n0 * kTcM + m;
   float s[kJoin / 2] = {};
-  for (int i = i0; i <= i1; i += kJoinAt) {
+  for (int i = i0; i <= i1; i += kJoinAt, src += 2 * kJoinAt * slot) {
     float v[kJoinAt][kJoin / 2];
 #pragma unroll
-    for (int b = 0; b < kJoinAt; ++b)
+    for (int b = 0; b < kJoinAt; ++b) {
+      const float *from = src + (2 * b + (b == 0 && i == i0 ? 1 : 0)) * slot;
 #pragma unroll
-      for (int j = 0; j < kJoin / 2; ++j) {
-        v[b][j] = 0.0f;
-        // the first CTA's part is its second (its run of the tile began at the tile's start)
-        if (i + b <= i1 && n0 + 2 * j < p.ncols)
-          v[b][j] = __ldcs(src + (static_cast<int64_t>(i + b) * 2 + (i + b == i0 ? 1 : 0)) * slot + 2 * j * kTcM);
-      }
+      for (int j = 0; j < kJoin / 2; ++j) v[b][j] = i + b <= i1 && j < live ? __ldcs(from + 2 * j * kTcM) : 0.0f;
+    }
 #pragma unroll
     for (int b = 0; b < kJoinAt; ++b)
 #pragma unroll
       for (int j = 0; j < kJoin / 2; ++j) s[j] += v[b][j];
   }
+  const int col = nt * p.ncols + n0;
+  float *dst = p.dA + static_cast<int64_t>(col) * p.in + f;
 #pragma unroll
-  for (int j = 0; j < kJoin / 2; ++j) {
-    const int n = n0 + 2 * j, col = nt * p.ncols + n;
-    if (n < p.ncols && col < p.r) p.dA[static_cast<int64_t>(col) * p.in + f] = s[j];
-  }
+  for (int j = 0; j < kJoin / 2; ++j, dst += 2 * static_cast<int64_t>(p.in))
+    if (j < live && col + 2 * j < p.r) *dst = s[j];
 }
 
 // ---------------------------------------------------------------------------
@@ -624,7 +629,7 @@ dora_status launch_grad(const CUtensorMap &mX, const CUtensorMap &mD, GradParams
   // no tile is cut when every CTA's run is a whole number of tiles
   const int64_t tiles = static_cast<int64_t>(p.mtiles) * p.ntiles;
   if (tiles % ctas != 0) {
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * dora::ceil_div(p.ncols, kJoin)));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(dora::ceil_div(p.ncols, kJoin)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, grad_join_kernel, p, ctas) != cudaSuccess) return DORA_ERR_CUDA;

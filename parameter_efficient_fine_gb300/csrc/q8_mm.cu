@@ -19,8 +19,8 @@
 // (K-major), for dy W it is 128 rows of k x 128 bytes along the features
 // (M-major, the transpose bit of the instruction).
 //
-// q8_split_kernel: one tile of 128 features x NT tokens per cluster of CTAs,
-// which share its k range; each CTA streams its part through a ring of TMA
+// q8_split_kernel: up to 128 tokens, one tile of 128 features x NT of them per
+// cluster of CTAs, which share its k range; each CTA streams its part through a ring of TMA
 // stages, and the parts meet in distributed shared memory, summed in rank
 // order (bitwise reproducible, no workspace).
 //   warp 0     TMA producer: per k block the W box (16 KB) and the token box
@@ -61,13 +61,14 @@ constexpr int kKB = 128;                    // k per block: one 128-byte swizzle
 constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB
 constexpr int kSfSlots = 4;                 // scale words in flight, in groups of four k blocks
 constexpr int kSplitThreads = 192;
+constexpr int kSplitTok = 128;              // most tokens of q8_split_kernel (one tile of them)
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;              // the portable limit
 
 struct MmParams {
   int T, nfeat, kdim;               // tokens, features of the result, k
   int kblocks;
-  int ntiles, tiles;                // token tiles, all tiles
+  int ntiles, tiles;                // token tiles (pairs), all tiles
   int ntok;                         // tokens per tile (pairs)
   int stages;
   int nsx, nsw;                     // scale bytes per row of x, of W
@@ -191,8 +192,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
   uint32_t csize;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
   const uint32_t rank = cluster_ctarank();
-  const int tile = static_cast<int>(blockIdx.x / csize);
-  const int mt = tile / p.ntiles, nt = tile % p.ntiles;
+  const int mt = static_cast<int>(blockIdx.x / csize);
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / csize);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / csize);
   bool ok = true;
@@ -221,7 +221,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
         mbar_expect_tx(fb, kStage);
         if (TRANS) tma_load_2d(at, &mW, mt * kTcM, kb * kKB, fb);
         else tma_load_2d(at, &mW, kb * kKB, mt * kTcM, fb);
-        tma_load_2d(at + kWBytes, &mX, kb * kKB, nt * NT, fb);
+        tma_load_2d(at + kWBytes, &mX, kb * kKB, 0, fb);
       }
       __syncwarp();
       ++issued;
@@ -285,7 +285,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
       w[0] = w[1] = w[2] = w[3] = weight_word<TRANS>(p, mt, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int t = nt * NT + 32 * j + lane;
+        const int t = 32 * j + lane;
         w[4 + j] = 32 * j < NT && t < p.T ? token_word(p.xscale + static_cast<int64_t>(t) * p.nsx, g, p.kblocks, words)
                                           : 0x7f7f7f7fu;
       }
@@ -310,10 +310,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
     const int f = static_cast<int>(quad) * 32 + lane;
-    const int live = min(NT, p.T - nt * NT);
 #pragma unroll
     for (int c = 0; c < NT; c += 16) {
-      if (c < live) {
+      if (c < p.T) {
         float v[16];
         tmem_ld<16>(lane_addr + c, v);
 #pragma unroll
@@ -328,7 +327,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
   {
     // the parts of the cluster in rank order, one rounding to bf16: four
     // features a thread, neighbouring threads on neighbouring features
-    const int live = min(NT, p.T - nt * NT) * 32;
+    const int live = p.T * 32;
     const uint32_t base = smem_u32(smem);
     for (int i = static_cast<int>(rank) * kSplitThreads + threadIdx.x; i < live;
          i += static_cast<int>(csize) * kSplitThreads) {
@@ -340,7 +339,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
         s.z += v.z;
         s.w += v.w;
       }
-      const int t = nt * NT + i / 32, f = mt * kTcM + 4 * (i % 32);
+      const int t = i / 32, f = mt * kTcM + 4 * (i % 32);
       if (f < p.nfeat)
         *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(t) * p.nfeat + f) =
             make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
@@ -771,8 +770,9 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   p.wscale = static_cast<const uint8_t *>(wscale);
   p.y = static_cast<__nv_bfloat16 *>(y);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const int pairs = resident_pairs(device, info.sms);
-  if (pairs > 0 && T > 128) {
+  if (T > kSplitTok) {
+    const int pairs = resident_pairs(device, info.sms);
+    if (pairs == 0) return DORA_ERR_CUDA;
     const int64_t ftiles = dora::ceil_div(p.nfeat, kPairFeat);
     // tokens per tile: the least time over the waves of tiles.  A stage of two
     // k blocks was measured to take a time in proportion to tokens + 125 (at
@@ -789,19 +789,15 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
     }
     p.ntiles = static_cast<int>(dora::ceil_div(T, p.ntok));
     const int64_t tiles = ftiles * p.ntiles;
-    if (tiles <= kMaxDim) {
-      p.tiles = static_cast<int>(tiles);
-      return launch_pairs<TRANS>(q, wq, out, in, p, pairs, cs);
-    }
+    if (tiles > kMaxDim) return DORA_ERR_SHAPE;
+    p.tiles = static_cast<int>(tiles);
+    return launch_pairs<TRANS>(q, wq, out, in, p, pairs, cs);
   }
   const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  p.ntiles = static_cast<int>(dora::ceil_div(T, nt));
-  const int64_t tiles = dora::ceil_div(p.nfeat, kTcM) * p.ntiles;
-  if (tiles * kMaxCluster > kMaxDim) return DORA_ERR_SHAPE;
-  p.tiles = static_cast<int>(tiles);
+  p.tiles = static_cast<int>(dora::ceil_div(p.nfeat, kTcM));
   // the k range over as many CTAs as keep all clusters resident at two CTAs an SM
   int cluster = 1;
-  while (cluster < kMaxCluster && tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= p.kblocks) cluster *= 2;
+  while (cluster < kMaxCluster && p.tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= p.kblocks) cluster *= 2;
   CUtensorMap mW, mX;
   if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, T, p.kdim, nt)) return DORA_ERR_CUDA;
   switch (nt) {
@@ -813,45 +809,35 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
 }
 
 dora_status matmul_check(const void *xq, const void *xscale, const void *wq, const void *wscale, int64_t out,
-                         int64_t in, const void *y, const void *workspace, size_t have, size_t need) {
+                         int64_t in, const void *y) {
   if (!xq || !xscale || !wq || !wscale || !y) return DORA_ERR_NULL;
   // TMA: 16-byte aligned bases and row strides
   if (out % 16 != 0 || in % 16 != 0) return DORA_ERR_ALIGN;
   if (!dora::aligned(xq, 16) || !dora::aligned(wq, 16) || !dora::aligned(y, 16)) return DORA_ERR_ALIGN;
-  if (!workspace || !dora::aligned(workspace, 256) || have < need) return DORA_ERR_WORKSPACE;
   return DORA_OK;
 }
 
 }  // namespace
 
-extern "C" size_t dora_matmul_q8_workspace(int64_t T, int64_t out, int64_t in) {
-  if (bad_size(T, 0) || bad_size(out, 0) || bad_size(in, 1)) return 0;
-  return 256;
-}
-
-extern "C" size_t dora_matmul_q8_t_workspace(int64_t T, int64_t out, int64_t in) {
-  if (bad_size(T, 0) || bad_size(out, 1) || bad_size(in, 0)) return 0;
-  return 256;
-}
+// (both kernels join a tile's parts on chip)
+extern "C" size_t dora_matmul_q8_workspace(int64_t, int64_t, int64_t) { return 0; }
+extern "C" size_t dora_matmul_q8_t_workspace(int64_t, int64_t, int64_t) { return 0; }
 
 extern "C" dora_status dora_matmul_q8(const void *xq, const void *xscale, const void *wq, const void *wscale, int64_t T,
-                                      int64_t out, int64_t in, void *y, void *workspace, size_t workspace_bytes,
-                                      dora_stream_t stream) {
+                                      int64_t out, int64_t in, void *y, void *, size_t, dora_stream_t stream) {
   if (bad_size(T, 0) || bad_size(out, 0) || bad_size(in, 1)) return DORA_ERR_SHAPE;
   if (T == 0 || out == 0) return DORA_OK;
-  const dora_status st = matmul_check(xq, xscale, wq, wscale, out, in, y, workspace, workspace_bytes,
-                                      dora_matmul_q8_workspace(T, out, in));
+  const dora_status st = matmul_check(xq, xscale, wq, wscale, out, in, y);
   if (st != DORA_OK) return st;
   return run_matmul<false>(xq, xscale, wq, wscale, T, out, in, y, stream);
 }
 
 extern "C" dora_status dora_matmul_q8_t(const void *dyq, const void *dyscale, const void *wq, const void *wscale,
-                                        int64_t T, int64_t out, int64_t in, void *dx, void *workspace,
-                                        size_t workspace_bytes, dora_stream_t stream) {
+                                        int64_t T, int64_t out, int64_t in, void *dx, void *, size_t,
+                                        dora_stream_t stream) {
   if (bad_size(T, 0) || bad_size(out, 1) || bad_size(in, 0)) return DORA_ERR_SHAPE;
   if (T == 0 || in == 0) return DORA_OK;
-  const dora_status st = matmul_check(dyq, dyscale, wq, wscale, out, in, dx, workspace, workspace_bytes,
-                                      dora_matmul_q8_t_workspace(T, out, in));
+  const dora_status st = matmul_check(dyq, dyscale, wq, wscale, out, in, dx);
   if (st != DORA_OK) return st;
   return run_matmul<true>(dyq, dyscale, wq, wscale, T, out, in, dx, stream);
 }

@@ -13,7 +13,7 @@
 
 namespace {
 
-constexpr int64_t kMaxDim = (1ll << 31) - 1;
+constexpr int64_t kMaxDim = (1ll << 31) - 1024;   // a tile past it is still an int
 constexpr int kSmemMax = 232448;
 constexpr unsigned long long kWaitNs = 2000000000ull;
 

@@ -53,10 +53,9 @@ from torch import Tensor
 
 from . import (dora_compose_bwd, dora_compose_bwd_q8, dora_compose_bwd_q8_workspace, dora_compose_bwd_workspace,
                dora_compose_fwd, dora_compose_fwd_q8, dora_lora_grad_q8, dora_lora_grad_q8_workspace, dora_matmul_q8,
-               dora_matmul_q8_t, dora_matmul_q8_t_workspace, dora_matmul_q8_workspace, dora_norm_factored,
-               dora_norm_factored_bf16, dora_norm_factored_bf16_workspace, dora_norm_factored_bwd,
-               dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_q8_load, dora_q8_store,
-               dora_row_sumsq_bf16)
+               dora_matmul_q8_t, dora_norm_factored, dora_norm_factored_bf16, dora_norm_factored_bf16_workspace,
+               dora_norm_factored_bwd, dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_q8_load,
+               dora_q8_store, dora_row_sumsq_bf16)
 
 __all__ = ["norm_factored", "row_sumsq", "norm_factored_bf16", "compose", "compose_bwd", "norm_factored_bwd",
            "module", "dora_module", "q8_store", "q8_load", "compose_q8", "compose_bwd_q8", "matmul_q8", "matmul_q8_t",
@@ -341,9 +340,8 @@ compose_q8.register_autograd(_compose_q8_backward, setup_context=_compose_q8_set
 def matmul_q8(xq: Tensor, xscale: Tensor, wq: Tensor, wscale: Tensor) -> Tensor:
     """x W^T in bfloat16, x and W in 8 bits (block_rows 1 and 128)."""
     _contig("matmul_q8", xq, xscale, wq, wscale)
-    T, (out, inp) = xq.shape[0], wq.shape
-    y = torch.empty(T, out, dtype=torch.bfloat16, device=xq.device)
-    dora_matmul_q8(xq, xscale, wq, wscale, y, _workspace(dora_matmul_q8_workspace(T, out, inp), xq))
+    y = torch.empty(xq.shape[0], wq.shape[0], dtype=torch.bfloat16, device=xq.device)
+    dora_matmul_q8(xq, xscale, wq, wscale, y)
     return y
 
 
@@ -356,9 +354,8 @@ def _matmul_q8_fake(xq, xscale, wq, wscale):
 def matmul_q8_t(dyq: Tensor, dyscale: Tensor, wq: Tensor, wscale: Tensor) -> Tensor:
     """dy W in bfloat16, dy and the same W in 8 bits."""
     _contig("matmul_q8_t", dyq, dyscale, wq, wscale)
-    T, (out, inp) = dyq.shape[0], wq.shape
-    dx = torch.empty(T, inp, dtype=torch.bfloat16, device=dyq.device)
-    dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx, _workspace(dora_matmul_q8_t_workspace(T, out, inp), dyq))
+    dx = torch.empty(dyq.shape[0], wq.shape[1], dtype=torch.bfloat16, device=dyq.device)
+    dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx)
     return dx
 
 
