@@ -15,7 +15,7 @@
 // columns is 16 neighbouring threads in bf16 and a whole warp in fp32, and its
 // maximum is a butterfly of shuffles over them; the quantised piece is stored
 // from the same registers.  Rows that are ragged or not 16-byte aligned take
-// a kernel whose warps own one block of 128 columns each.
+// the same kernels with four columns a thread, 32 apart (Piece).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,39 +23,107 @@
 #include "q8.cuh"
 #include "stream.cuh"
 
+#include <type_traits>
+
 namespace {
 
-// the 8-bit piece of VEC elements
-template <int VEC> struct QPiece;
-template <> struct QPiece<8> {
-  using Raw = uint2;
-  static __device__ __forceinline__ Raw quant(const float (&v)[8], float inv) {
-    return make_uint2(quant4(v, inv), quant4(v + 4, inv));
+// What a thread holds of a row.  Vector rows: 16 bytes of it, VEC neighbouring
+// columns from c0, and the matching 8-bit piece.  Ragged rows (any length and
+// alignment): four columns 32 apart, so that a warp's accesses are contiguous
+// and a warp is one block of 128 columns.  `live` is how many of the columns
+// lie inside the row (all or none in a vector row).
+template <typename Act, bool RAGGED> struct Piece;
+
+template <typename Act> struct Piece<Act, false> {
+  static constexpr int VEC = 16 / sizeof(Act);
+  using IO = Io<Act, VEC>;
+  using Raw = typename IO::Raw;
+  using Q = typename std::conditional<VEC == 8, uint2, uint32_t>::type;
+  static __device__ __forceinline__ int64_t first() { return ((int64_t)blockIdx.x * kBX + threadIdx.x) * VEC; }
+  static __device__ __forceinline__ int live(int64_t c0, int64_t cols) { return c0 < cols ? VEC : 0; }
+  static __device__ __forceinline__ int at(int v) { return v; }                          // column c0 + at(v)
+  static __device__ __forceinline__ int in_block(int v) { return threadIdx.x * VEC + v; }  // among the block's
+  static __device__ __forceinline__ Raw load(const Act *p, int64_t e, int n) { return n ? IO::load(p, e) : Raw{}; }
+  static __device__ __forceinline__ void store(Act *p, int64_t e, int n, const float (&v)[VEC]) {
+    if (n) IO::store(p, e, IO::pack(v));
   }
-  static __device__ __forceinline__ void dequant(Raw r, float s, float (&v)[8]) {
-    const uint32_t w[4] = {r.x, r.x >> 16, r.y, r.y >> 16};
+  static __device__ __forceinline__ void unpack(Raw r, float (&v)[VEC]) { IO::unpack(r, v); }
+  static __device__ __forceinline__ Q load_q(const uint8_t *q, int64_t e, int n) {
+    return n ? __ldcs(reinterpret_cast<const Q *>(q + e)) : Q{};
+  }
+  static __device__ __forceinline__ void store_q(uint8_t *q, int64_t e, int n, const float (&v)[VEC], float inv) {
+    if (!n) return;
+    if constexpr (VEC == 8) __stcs(reinterpret_cast<Q *>(q + e), make_uint2(quant4(v, inv), quant4(v + 4, inv)));
+    else __stcs(reinterpret_cast<Q *>(q + e), quant4(v, inv));
+  }
+  static __device__ __forceinline__ void dequant(Q r, float s, float (&v)[VEC]) {
+    uint32_t w[2];
+    if constexpr (VEC == 8) {
+      w[0] = r.x;
+      w[1] = r.y;
+    } else {
+      w[0] = r;
+    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = dequant2(w[k] & 0xffffu, s);
-      v[2 * k] = f.x;
-      v[2 * k + 1] = f.y;
+    for (int k = 0; k < VEC; k += 4) dequant4(w[k / 4], s, v + k);
+  }
+};
+
+template <typename Act> struct Piece<Act, true> {
+  static constexpr int VEC = 4;
+  using IO = Io<Act, 1>;
+  struct Raw {
+    typename IO::Raw v[VEC];
+  };
+  struct Q {
+    uint8_t b[VEC];
+  };
+  static __device__ __forceinline__ int64_t first() { return (int64_t)blockIdx.x * kQBlock + threadIdx.x; }
+  static __device__ __forceinline__ int live(int64_t c0, int64_t cols) {
+    const int64_t n = (cols - c0 + 31) / 32;
+    return n < 0 ? 0 : n > VEC ? VEC : static_cast<int>(n);
+  }
+  static __device__ __forceinline__ int at(int v) { return 32 * v; }
+  static __device__ __forceinline__ int in_block(int v) { return threadIdx.x + 32 * v; }
+  static __device__ __forceinline__ Raw load(const Act *p, int64_t e, int n) {
+    Raw r = {};
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (k < n) r.v[k] = IO::load(p, e + 32 * k);
+    return r;
+  }
+  static __device__ __forceinline__ void store(Act *p, int64_t e, int n, const float (&v)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const float one[1] = {v[k]};
+      if (k < n) IO::store(p, e + 32 * k, IO::pack(one));
     }
   }
-};
-template <> struct QPiece<4> {
-  using Raw = uint32_t;
-  static __device__ __forceinline__ Raw quant(const float (&v)[4], float inv) { return quant4(v, inv); }
-  static __device__ __forceinline__ void dequant(Raw r, float s, float (&v)[4]) {
-    const float2 a = dequant2(r & 0xffffu, s), b = dequant2(r >> 16, s);
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = b.x;
-    v[3] = b.y;
+  static __device__ __forceinline__ void unpack(Raw r, float (&v)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      float one[1];
+      IO::unpack(r.v[k], one);
+      v[k] = one[0];
+    }
   }
-};
-template <> struct QPiece<1> {
-  using Raw = uint8_t;
-  static __device__ __forceinline__ void dequant(Raw r, float s, float (&v)[1]) { v[0] = dequant2(r, s).x; }
+  static __device__ __forceinline__ Q load_q(const uint8_t *q, int64_t e, int n) {
+    Q r = {};
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (k < n) r.b[k] = __ldcs(q + e + 32 * k);
+    return r;
+  }
+  static __device__ __forceinline__ void store_q(uint8_t *q, int64_t e, int n, const float (&v)[VEC], float inv) {
+    const uint32_t w = quant4(v, inv);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (k < n) __stcs(q + e + 32 * k, static_cast<uint8_t>(w >> (8 * k)));
+  }
+  static __device__ __forceinline__ void dequant(Q r, float s, float (&v)[VEC]) {
+    dequant4(r.b[0] | static_cast<uint32_t>(r.b[1]) << 8 | static_cast<uint32_t>(r.b[2]) << 16 |
+                 static_cast<uint32_t>(r.b[3]) << 24, s, v);
+  }
 };
 
 // largest `m` over the 128 / VEC neighbouring threads that hold a 128-column
@@ -93,52 +161,48 @@ __device__ __forceinline__ uint32_t block_scale(float (&v)[VEC]) {
 // ---------------------------------------------------------------------------
 // COMPOSE: y = base + ((g-1) base + g s lora) and the 8-bit form of base + s
 // lora; otherwise the 8-bit form of base alone
-template <typename Act, int VEC, bool COMPOSE>
+template <typename Act, bool RAGGED, bool COMPOSE>
 __global__ void __launch_bounds__(kThreads)
 q8_fwd_kernel(const Act *__restrict__ base, const Act *__restrict__ lora, const float *__restrict__ g, float s,
               int64_t T, int64_t out, Act *__restrict__ y, uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
-  using IO = Io<Act, VEC>;
-  using QP = QPiece<VEC>;
-  // token rows in flight per thread (15360 x 8192 bf16: store 66, 62, 63, 68 us
-  // and compose 150, 137, 141, 146 us with 2, 3, 4 and 8)
-  constexpr int U = 3;
-  constexpr int kPer = kQBlock / VEC;   // threads per scale
-  const int64_t ncg = out / VEC;
-  const int64_t cg = (int64_t)blockIdx.x * kBX + threadIdx.x;
-  const bool active = cg < ncg;      // an idle thread of a ragged row's last warp takes part in the maxima
+  using P = Piece<Act, RAGGED>;
+  constexpr int VEC = P::VEC;
+  // token rows in flight per thread (bf16, 15360 x 8192: store 66, 62, 63, 68 us
+  // and compose 150, 137, 141, 146 us with 2, 3, 4 and 8; 15360 x 8191: store
+  // 94, 128, 128 us and compose 225, 219, 214 us with 1, 2 and 3)
+  constexpr int U = RAGGED ? 1 : 3;
+  const int64_t c0 = P::first();
+  const int live = P::live(c0, out);   // a thread past the row's end takes part in the maxima, with zeros
   const int64_t lanes = (int64_t)gridDim.y * kBY;
-  const int64_t c0 = active ? cg * VEC : 0;
   const int64_t nsc = (out + kQBlock - 1) / kQBlock;
 
   float gm1[VEC], gs[VEC];
   if (COMPOSE) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      const float gv = __ldg(g + c0 + v);
+      const float gv = v < live ? __ldg(g + c0 + P::at(v)) : 0.0f;
       gm1[v] = gv - 1.0f;
       gs[v] = gv * s;
     }
   }
   for (int64_t t = (int64_t)blockIdx.y * kBY + threadIdx.y; t < T; t += U * lanes) {
-    typename IO::Raw rb[U], rl[U];
+    typename P::Raw rb[U], rl[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t tu = t + u * lanes;
-      rb[u] = typename IO::Raw{};
-      if (COMPOSE) rl[u] = typename IO::Raw{};
-      if (active && tu < T) {
-        rb[u] = IO::load(base, tu * out + c0);
-        if (COMPOSE) rl[u] = IO::load(lora, tu * out + c0);
-      }
+      const int n = tu < T ? live : 0;
+      rb[u] = P::load(base, tu * out + c0, n);
+      if (COMPOSE) rl[u] = P::load(lora, tu * out + c0, n);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t tu = t + u * lanes;
+      const int n = tu < T ? live : 0;
       float b[VEC], v[VEC];
-      IO::unpack(rb[u], b);
+      P::unpack(rb[u], b);
       if (COMPOSE) {
         float l[VEC];
-        IO::unpack(rl[u], l);
+        P::unpack(rl[u], l);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
           v[k] = __fadd_rn(b[k], __fmul_rn(s, l[k]));
@@ -149,60 +213,10 @@ q8_fwd_kernel(const Act *__restrict__ base, const Act *__restrict__ lora, const 
         for (int k = 0; k < VEC; ++k) v[k] = b[k];
       }
       const uint32_t sc = block_scale<VEC>(v);
-      if (active && tu < T) {
-        if (COMPOSE) IO::store(y, tu * out + c0, IO::pack(b));
-        __stcs(reinterpret_cast<typename QP::Raw *>(q + tu * out + c0), QP::quant(v, scale_inverse(sc)));
-        if (cg % kPer == 0) scale[tu * nsc + cg / kPer] = static_cast<uint8_t>(sc);
-      }
+      if (COMPOSE) P::store(y, tu * out + c0, n, b);
+      P::store_q(q, tu * out + c0, n, v, scale_inverse(sc));
+      if (n > 0 && c0 % kQBlock == 0) scale[tu * nsc + c0 / kQBlock] = static_cast<uint8_t>(sc);
     }
-  }
-}
-
-// the same for any row length and alignment: a warp takes block blockIdx.x *
-// warps + warp of rows blockIdx.y, blockIdx.y + gridDim.y, ..., four columns a
-// lane, 32 apart
-template <typename Act, bool COMPOSE>
-__global__ void __launch_bounds__(kThreads)
-q8_fwd_ragged_kernel(const Act *__restrict__ base, const Act *__restrict__ lora, const float *__restrict__ g, float s,
-                     int64_t T, int64_t out, Act *__restrict__ y, uint8_t *__restrict__ q,
-                     uint8_t *__restrict__ scale) {
-  using IO = Io<Act, 1>;
-  const int64_t nsc = (out + kQBlock - 1) / kQBlock;
-  const int64_t blk = (int64_t)blockIdx.x * kBY + threadIdx.y;
-  if (blk >= nsc) return;            // a whole warp
-  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
-    float v[4], yv[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t c = blk * kQBlock + 32 * k + threadIdx.x;
-      v[k] = yv[k] = 0.0f;
-      if (c < out) {
-        float b[1], l[1];
-        IO::unpack(IO::load(base, t * out + c), b);
-        v[k] = b[0];
-        if (COMPOSE) {
-          IO::unpack(IO::load(lora, t * out + c), l);
-          const float gv = __ldg(g + c);
-          v[k] = __fadd_rn(b[0], __fmul_rn(s, l[0]));
-          yv[k] = b[0] + fmaf(gv - 1.0f, b[0], gv * s * l[0]);
-        }
-      }
-    }
-    uint32_t m = max(max(finite_bits(v[0]), finite_bits(v[1])), max(finite_bits(v[2]), finite_bits(v[3])));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t sc = scale_byte(m);
-    const float inv = scale_inverse(sc);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t c = blk * kQBlock + 32 * k + threadIdx.x;
-      if (c < out) {
-        q[t * out + c] = static_cast<uint8_t>(quant2(inf_to_nan(v[k]), 0.0f, inv));
-        const float yk[1] = {yv[k]};
-        if (COMPOSE) IO::store(y, t * out + c, IO::pack(yk));
-      }
-    }
-    if (threadIdx.x == 0) scale[t * nsc + blk] = static_cast<uint8_t>(sc);
   }
 }
 
@@ -248,29 +262,32 @@ q8_store_tile_kernel(const Act *__restrict__ x, int64_t rows, int64_t cols, uint
 // ---------------------------------------------------------------------------
 // load
 // ---------------------------------------------------------------------------
-template <typename Act, int VEC>
-__global__ void __launch_bounds__(kThreads)
+// eight blocks an SM: what limits it is how much it has in flight (15360 x 8192
+// f32 127 us with the seven that its registers would leave, 110 with eight;
+// 15360 x 8191 bf16 117 and 99; 15360 x 8192 bf16 66 with either, 5730 GB/s)
+template <typename Act, bool RAGGED>
+__global__ void __launch_bounds__(kThreads, 8)
 q8_load_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, int64_t T, int64_t out, int block_rows,
                Act *__restrict__ x) {
-  using IO = Io<Act, VEC>;
-  using QP = QPiece<VEC>;
-  constexpr int U = 2;   // 15360 x 8192 bf16: 65, 65, 73, 85 us with 1, 2, 4 and 8
-  const int64_t cg = (int64_t)blockIdx.x * kBX + threadIdx.x;
-  if (cg >= out / VEC) return;
+  using P = Piece<Act, RAGGED>;
+  // bf16, 15360 x 8192: 72, 66, 73, 85 us with 1, 2, 4 and 8; 15360 x 8191: 117, 137, 161 us with 1, 2 and 3 (at seven)
+  constexpr int U = RAGGED ? 1 : 2;
+  const int64_t c0 = P::first();
+  const int live = P::live(c0, out);
+  if (live == 0) return;
   const int64_t lanes = (int64_t)gridDim.y * kBY;
-  const int64_t c0 = cg * VEC;
   const int64_t nsc = (out + kQBlock - 1) / kQBlock;
   const uint8_t *sp = scale + c0 / kQBlock;
   for (int64_t t = (int64_t)blockIdx.y * kBY + threadIdx.y; t < T; t += U * lanes) {
-    typename QP::Raw r[U];
+    typename P::Q r[U];
     uint32_t sc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t tu = t + u * lanes;
-      r[u] = typename QP::Raw{};
+      r[u] = typename P::Q{};
       sc[u] = 0;
       if (tu < T) {
-        r[u] = __ldcs(reinterpret_cast<const typename QP::Raw *>(q + tu * out + c0));
+        r[u] = P::load_q(q, tu * out + c0, live);
         sc[u] = __ldg(sp + (block_rows == 1 ? tu : tu / block_rows) * nsc);
       }
     }
@@ -278,9 +295,9 @@ q8_load_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale,
     for (int u = 0; u < U; ++u) {
       const int64_t tu = t + u * lanes;
       if (tu < T) {
-        float v[VEC];
-        QP::dequant(r[u], scale_value(sc[u]), v);
-        IO::store(x, tu * out + c0, IO::pack(v));
+        float v[P::VEC];
+        P::dequant(r[u], scale_value(sc[u]), v);
+        P::store(x, tu * out + c0, live, v);
       }
     }
   }
@@ -289,82 +306,76 @@ q8_load_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale,
 // ---------------------------------------------------------------------------
 // compose backward from the 8-bit v
 // ---------------------------------------------------------------------------
-template <typename Act, int VEC>
+template <typename Act, bool RAGGED>
 __global__ void __launch_bounds__(kThreads)
 q8_compose_bwd_kernel(const Act *__restrict__ dy, const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale,
                       const float *__restrict__ g, float s, int64_t T, int64_t out, Act *__restrict__ d_base,
                       Act *__restrict__ d_lora, float *__restrict__ part) {
-  using IO = Io<Act, VEC>;
-  using QP = QPiece<VEC>;
-  constexpr int U = 2;
+  using P = Piece<Act, RAGGED>;
+  constexpr int VEC = P::VEC;
+  // 15360 x 8192 bf16: 147 us with 2, more with 1, 3 and 4; 15360 x 8191: 236, 240, 209, 280 us with 1, 2, 3 and 4
+  constexpr int U = RAGGED ? 3 : 2;
   __shared__ float red[kBY][kBX * VEC];
 
-  const int64_t ncg = out / VEC;
-  const int64_t cg = (int64_t)blockIdx.x * kBX + threadIdx.x;
-  const bool active = cg < ncg;
+  const int64_t c0 = P::first();
+  const int live = P::live(c0, out);
   const int64_t lanes = (int64_t)gridDim.y * kBY;
-  const int64_t c0 = cg * VEC;
   const int64_t nsc = (out + kQBlock - 1) / kQBlock;
 
   float acc[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) acc[v] = 0.0f;
 
-  if (active) {
+  if (live > 0) {
     float gg[VEC], gs[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      gg[v] = __ldg(g + c0 + v);
+      gg[v] = v < live ? __ldg(g + c0 + P::at(v)) : 0.0f;
       gs[v] = gg[v] * s;
     }
     for (int64_t t = (int64_t)blockIdx.y * kBY + threadIdx.y; t < T; t += U * lanes) {
-      typename IO::Raw rd[U];
-      typename QP::Raw rq[U];
+      typename P::Raw rd[U];
+      typename P::Q rq[U];
       uint32_t sc[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t tu = t + u * lanes;
-        rd[u] = typename IO::Raw{};
-        rq[u] = typename QP::Raw{};
-        sc[u] = 0;
-        if (tu < T) {
-          rd[u] = IO::load(dy, tu * out + c0);
-          rq[u] = __ldcs(reinterpret_cast<const typename QP::Raw *>(q + tu * out + c0));
-          sc[u] = __ldg(scale + tu * nsc + c0 / kQBlock);
-        }
+        const int64_t tu = t + u * lanes, e = tu * out + c0;
+        const int n = tu < T ? live : 0;
+        rd[u] = P::load(dy, e, n);
+        rq[u] = P::load_q(q, e, n);
+        sc[u] = n ? __ldg(scale + tu * nsc + c0 / kQBlock) : 0u;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t tu = t + u * lanes;
-        if (tu < T) {
-          float d[VEC], v[VEC], ob[VEC], ol[VEC];
-          IO::unpack(rd[u], d);
-          QP::dequant(rq[u], scale_value(sc[u]), v);
+        const int64_t tu = t + u * lanes, e = tu * out + c0;
+        const int n = tu < T ? live : 0;
+        float d[VEC], v[VEC], ob[VEC], ol[VEC];
+        P::unpack(rd[u], d);
+        P::dequant(rq[u], scale_value(sc[u]), v);
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            ob[k] = gg[k] * d[k];
-            ol[k] = gs[k] * d[k];
-            acc[k] = fmaf(d[k], v[k], acc[k]);
-          }
-          const int64_t e = tu * out + c0;
-          IO::store(d_base, e, IO::pack(ob));
-          IO::store(d_lora, e, IO::pack(ol));
+        for (int k = 0; k < VEC; ++k) {
+          ob[k] = gg[k] * d[k];
+          ol[k] = gs[k] * d[k];
+          acc[k] = fmaf(d[k], v[k], acc[k]);     // zeros past the last row
         }
+        P::store(d_base, e, n, ob);
+        P::store(d_lora, e, n, ol);
       }
     }
   }
 
   // fixed-order sum of the 8 token lanes of this block
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) red[threadIdx.y][threadIdx.x * VEC + v] = acc[v];
+  for (int v = 0; v < VEC; ++v) red[threadIdx.y][P::in_block(v)] = acc[v];
   __syncthreads();
-  if (threadIdx.y == 0 && active) {
+  if (threadIdx.y == 0) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      float sum = red[0][threadIdx.x * VEC + v];
+      if (v >= live) break;
+      float sum = red[0][P::in_block(v)];
 #pragma unroll
-      for (int k = 1; k < kBY; ++k) sum += red[k][threadIdx.x * VEC + v];
-      part[(int64_t)blockIdx.y * out + c0 + v] = sum;
+      for (int k = 1; k < kBY; ++k) sum += red[k][P::in_block(v)];
+      part[(int64_t)blockIdx.y * out + c0 + P::at(v)] = sum;
     }
   }
 }
@@ -393,55 +404,58 @@ bool q8_vector_ok(int64_t cols, std::initializer_list<const void *> ptrs, const 
   return vector_ok<Act>(cols, ptrs) && dora::aligned(q, 16 / sizeof(Act));
 }
 
-template <typename Act, bool COMPOSE>
+// grid of a kernel of Piece<Act, RAGGED> rows: its blocks hold 32 pieces a row
+template <typename Act, bool RAGGED, auto *KERNEL>
+Grid plan_rows(int64_t T, int64_t out, int device, int sms) {
+  return plan_grid(T, RAGGED ? dora::ceil_div(out, kQBlock) * kBX : out / Piece<Act, RAGGED>::VEC,
+                   (int64_t)sms * resident_blocks<KERNEL>(device));
+}
+
+template <typename Act, bool RAGGED, bool COMPOSE>
 dora_status launch_q8_fwd(const void *base, const void *lora, const float *g, float s, int64_t T, int64_t out, void *y,
                           void *q, void *scale, cudaStream_t stream, int device, int sms) {
-  constexpr int VEC = 16 / sizeof(Act);
-  const Act *b = static_cast<const Act *>(base), *l = static_cast<const Act *>(lora);
-  Act *yo = static_cast<Act *>(y);
-  uint8_t *qo = static_cast<uint8_t *>(q), *so = static_cast<uint8_t *>(scale);
-  const bool vec = COMPOSE ? q8_vector_ok<Act>(out, {base, lora, y}, q) : q8_vector_ok<Act>(out, {base}, q);
-  if (vec) {
-    constexpr auto kern = &q8_fwd_kernel<Act, VEC, COMPOSE>;
-    const Grid gr = plan_grid(T, out / VEC, (int64_t)sms * resident_blocks<kern>(device));
-    kern<<<dim3((unsigned)gr.gx, (unsigned)gr.gy), dim3(kBX, kBY), 0, stream>>>(b, l, g, s, T, out, yo, qo, so);
-  } else {
-    const int64_t gx = dora::ceil_div(dora::ceil_div(out, kQBlock), kBY);
-    const unsigned gy = (unsigned)(T < 65535 ? T : 65535);
-    q8_fwd_ragged_kernel<Act, COMPOSE>
-        <<<dim3((unsigned)gx, gy), dim3(kBX, kBY), 0, stream>>>(b, l, g, s, T, out, yo, qo, so);
-  }
+  constexpr auto kern = &q8_fwd_kernel<Act, RAGGED, COMPOSE>;
+  const Grid gr = plan_rows<Act, RAGGED, kern>(T, out, device, sms);
+  kern<<<dim3((unsigned)gr.gx, (unsigned)gr.gy), dim3(kBX, kBY), 0, stream>>>(
+      static_cast<const Act *>(base), static_cast<const Act *>(lora), g, s, T, out, static_cast<Act *>(y),
+      static_cast<uint8_t *>(q), static_cast<uint8_t *>(scale));
   dora::count_launches(1);
   return dora::launch_status();
 }
+template <typename Act, bool COMPOSE>
+dora_status run_q8_fwd(const void *base, const void *lora, const float *g, float s, int64_t T, int64_t out, void *y,
+                       void *q, void *scale, cudaStream_t stream, int device, int sms) {
+  const bool vec = COMPOSE ? q8_vector_ok<Act>(out, {base, lora, y}, q) : q8_vector_ok<Act>(out, {base}, q);
+  return vec ? launch_q8_fwd<Act, false, COMPOSE>(base, lora, g, s, T, out, y, q, scale, stream, device, sms)
+             : launch_q8_fwd<Act, true, COMPOSE>(base, lora, g, s, T, out, y, q, scale, stream, device, sms);
+}
 
-template <typename Act>
+template <typename Act, bool RAGGED>
 dora_status launch_q8_load(const void *q, const void *scale, int64_t T, int64_t out, int block_rows, void *x,
                            cudaStream_t stream, int device, int sms) {
-  constexpr int VEC = 16 / sizeof(Act);
-  const uint8_t *qi = static_cast<const uint8_t *>(q), *si = static_cast<const uint8_t *>(scale);
-  Act *xo = static_cast<Act *>(x);
-  if (q8_vector_ok<Act>(out, {x}, q)) {
-    constexpr auto kern = &q8_load_kernel<Act, VEC>;
-    const Grid gr = plan_grid(T, out / VEC, (int64_t)sms * resident_blocks<kern>(device));
-    kern<<<dim3((unsigned)gr.gx, (unsigned)gr.gy), dim3(kBX, kBY), 0, stream>>>(qi, si, T, out, block_rows, xo);
-  } else {
-    constexpr auto kern = &q8_load_kernel<Act, 1>;
-    const Grid gr = plan_grid(T, out, (int64_t)sms * resident_blocks<kern>(device));
-    kern<<<dim3((unsigned)gr.gx, (unsigned)gr.gy), dim3(kBX, kBY), 0, stream>>>(qi, si, T, out, block_rows, xo);
-  }
+  constexpr auto kern = &q8_load_kernel<Act, RAGGED>;
+  const Grid gr = plan_rows<Act, RAGGED, kern>(T, out, device, sms);
+  kern<<<dim3((unsigned)gr.gx, (unsigned)gr.gy), dim3(kBX, kBY), 0, stream>>>(
+      static_cast<const uint8_t *>(q), static_cast<const uint8_t *>(scale), T, out, block_rows, static_cast<Act *>(x));
   dora::count_launches(1);
   return dora::launch_status();
 }
+template <typename Act>
+dora_status run_q8_load(const void *q, const void *scale, int64_t T, int64_t out, int block_rows, void *x,
+                        cudaStream_t stream, int device, int sms) {
+  return q8_vector_ok<Act>(out, {x}, q)
+             ? launch_q8_load<Act, false>(q, scale, T, out, block_rows, x, stream, device, sms)
+             : launch_q8_load<Act, true>(q, scale, T, out, block_rows, x, stream, device, sms);
+}
 
-template <typename Act, int VEC>
+template <typename Act, bool RAGGED>
 dora_status launch_q8_bwd(const void *dy, const void *q, const void *scale, const float *g, const float *norm, float s,
                           int64_t T, int64_t out, void *d_base, void *d_lora, float *d_mag, float *part,
                           size_t part_bytes, cudaStream_t stream, int device, int sms) {
-  constexpr auto kern = &q8_compose_bwd_kernel<Act, VEC>;
+  constexpr auto kern = &q8_compose_bwd_kernel<Act, RAGGED>;
   int64_t rows = 0;
   if (T > 0) {
-    const Grid gr = plan_grid(T, out / VEC, (int64_t)sms * resident_blocks<kern>(device));
+    const Grid gr = plan_rows<Act, RAGGED, kern>(T, out, device, sms);
     rows = gr.gy;
     if ((size_t)rows * (size_t)out * sizeof(float) > part_bytes) return DORA_ERR_WORKSPACE;
     kern<<<dim3((unsigned)gr.gx, (unsigned)gr.gy), dim3(kBX, kBY), 0, stream>>>(
@@ -474,10 +488,10 @@ extern "C" dora_status dora_q8_store(dora_dtype act, const void *x, int64_t rows
   if (st != DORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (block_rows == 1)
-    return act == DORA_BF16 ? launch_q8_fwd<__nv_bfloat16, false>(x, nullptr, nullptr, 0.0f, rows, cols, nullptr, q,
-                                                                  scale, cs, device, info.sms)
-                            : launch_q8_fwd<float, false>(x, nullptr, nullptr, 0.0f, rows, cols, nullptr, q, scale, cs,
-                                                          device, info.sms);
+    return act == DORA_BF16 ? run_q8_fwd<__nv_bfloat16, false>(x, nullptr, nullptr, 0.0f, rows, cols, nullptr, q,
+                                                               scale, cs, device, info.sms)
+                            : run_q8_fwd<float, false>(x, nullptr, nullptr, 0.0f, rows, cols, nullptr, q, scale, cs,
+                                                       device, info.sms);
   const int64_t tiles = dora::ceil_div(rows, kQBlock) * dora::ceil_div(cols, kQBlock);
   if (tiles > kMaxDim) return DORA_ERR_SHAPE;
   uint8_t *qo = static_cast<uint8_t *>(q), *so = static_cast<uint8_t *>(scale);
@@ -503,8 +517,8 @@ extern "C" dora_status dora_q8_load(dora_dtype act, const void *q, const void *s
   dora_status st = dora::current_device(&info, &device);
   if (st != DORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return act == DORA_BF16 ? launch_q8_load<__nv_bfloat16>(q, scale, rows, cols, block_rows, x, cs, device, info.sms)
-                          : launch_q8_load<float>(q, scale, rows, cols, block_rows, x, cs, device, info.sms);
+  return act == DORA_BF16 ? run_q8_load<__nv_bfloat16>(q, scale, rows, cols, block_rows, x, cs, device, info.sms)
+                          : run_q8_load<float>(q, scale, rows, cols, block_rows, x, cs, device, info.sms);
 }
 
 extern "C" dora_status dora_compose_fwd_q8(dora_dtype act, const void *base, const void *lora, const float *g, float s,
@@ -523,8 +537,8 @@ extern "C" dora_status dora_compose_fwd_q8(dora_dtype act, const void *base, con
   if (st != DORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   return act == DORA_BF16
-             ? launch_q8_fwd<__nv_bfloat16, true>(base, lora, g, s, T, out, y, q, scale, cs, device, info.sms)
-             : launch_q8_fwd<float, true>(base, lora, g, s, T, out, y, q, scale, cs, device, info.sms);
+             ? run_q8_fwd<__nv_bfloat16, true>(base, lora, g, s, T, out, y, q, scale, cs, device, info.sms)
+             : run_q8_fwd<float, true>(base, lora, g, s, T, out, y, q, scale, cs, device, info.sms);
 }
 
 extern "C" size_t dora_compose_bwd_q8_workspace(int64_t T, int64_t out) {
@@ -555,16 +569,10 @@ extern "C" dora_status dora_compose_bwd_q8(dora_dtype act, const void *grad_out,
   if (st != DORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   float *part = static_cast<float *>(workspace);
-  if (act == DORA_BF16) {
-    if (q8_vector_ok<__nv_bfloat16>(out, {grad_out, d_base, d_lora}, q))
-      return launch_q8_bwd<__nv_bfloat16, 8>(grad_out, q, scale, g, norm, s, T, out, d_base, d_lora, d_mag, part,
-                                             workspace_bytes, cs, device, info.sms);
-    return launch_q8_bwd<__nv_bfloat16, 1>(grad_out, q, scale, g, norm, s, T, out, d_base, d_lora, d_mag, part,
-                                           workspace_bytes, cs, device, info.sms);
-  }
-  if (q8_vector_ok<float>(out, {grad_out, d_base, d_lora}, q))
-    return launch_q8_bwd<float, 4>(grad_out, q, scale, g, norm, s, T, out, d_base, d_lora, d_mag, part,
-                                   workspace_bytes, cs, device, info.sms);
-  return launch_q8_bwd<float, 1>(grad_out, q, scale, g, norm, s, T, out, d_base, d_lora, d_mag, part, workspace_bytes,
-                                 cs, device, info.sms);
+  auto run = act == DORA_BF16
+                 ? (q8_vector_ok<__nv_bfloat16>(out, {grad_out, d_base, d_lora}, q) ? &launch_q8_bwd<__nv_bfloat16, false>
+                                                                                    : &launch_q8_bwd<__nv_bfloat16, true>)
+                 : (q8_vector_ok<float>(out, {grad_out, d_base, d_lora}, q) ? &launch_q8_bwd<float, false>
+                                                                            : &launch_q8_bwd<float, true>);
+  return run(grad_out, q, scale, g, norm, s, T, out, d_base, d_lora, d_mag, part, workspace_bytes, cs, device, info.sms);
 }

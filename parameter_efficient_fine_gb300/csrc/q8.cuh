@@ -51,5 +51,12 @@ __device__ __forceinline__ float2 dequant2(uint32_t w, float s) {
   const float2 f = __half22float2(__half2(h));
   return make_float2(f.x * s, f.y * s);
 }
+__device__ __forceinline__ void dequant4(uint32_t w, float s, float *v) {
+  const float2 a = dequant2(w & 0xffffu, s), b = dequant2(w >> 16, s);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
+}
 
 }  // namespace

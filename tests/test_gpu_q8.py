@@ -132,6 +132,55 @@ def test_unaligned_pointers_take_the_same_values(dtype):
     assert torch.equal(off, back)
 
 
+def shifted(x, by):
+    """x's values in rows that start `by` elements past an aligned address."""
+    flat = torch.empty(x.numel() + by, dtype=x.dtype, device=DEV)
+    flat[by:] = x.reshape(-1)
+    return flat[by:].view(x.shape)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,out", [(1, 512), (2, 256), (3, 17), (40, 130), (70, 384), (301, 1000)])
+@pytest.mark.parametrize("by", [1, 2, 5])
+def test_any_alignment_gives_the_same_bits(T, out, by, dtype):
+    """Every operand at its own odd address against the same values in rows of
+    whole 16-byte pieces, padded with columns that the result does not read."""
+    rng = np.random.default_rng(T + out)
+    wide = -(-out // 128) * 128
+    base, lora, dy = (act(spread(rng, (T, wide)), dtype)[1] for _ in range(3))
+    for x in (base, lora, dy):
+        x[:, out:] = 0                             # leaves a block's scale as it is
+    g, n = f32_dev(rng.uniform(0.5, 1.5, wide)), f32_dev(rng.uniform(0.5, 2.0, wide))
+    y, (q, sc) = torch.empty_like(base), form(T, wide)
+    dora.dora_compose_fwd_q8(base, lora, g, 0.75, y, q, sc)
+    db, dl, dm = torch.empty_like(base), torch.empty_like(base), torch.empty(wide, device=DEV)
+    ws = workspace(dora.dora_compose_bwd_q8_workspace(T, wide))
+    dora.dora_compose_bwd_q8(dy, q, sc, g, n, 0.75, db, dl, dm, ws)
+    ref = (y, q, db, dl)
+
+    cut = [x[:, :out].contiguous() for x in (base, lora, dy)]
+    b2, l2, dy2 = (shifted(x, by + k) for k, x in enumerate(cut))
+    g2, n2 = g[:out].contiguous(), n[:out].contiguous()
+    y2, q2 = shifted(torch.empty_like(cut[0]), by), shifted(torch.empty(T, out, dtype=U8, device=DEV), 2 * by + 1)
+    sc2 = torch.empty_like(sc)
+    dora.dora_compose_fwd_q8(b2, l2, g2, 0.75, y2, q2, sc2)
+    db2, dl2 = (shifted(torch.empty_like(cut[0]), by + k) for k in (2, 1))
+    dm2 = torch.empty(out, device=DEV)
+    ws = workspace(dora.dora_compose_bwd_q8_workspace(T, out))
+    dora.dora_compose_bwd_q8(dy2, q2, sc2, g2, n2, 0.75, db2, dl2, dm2, ws)
+    for a, b in zip(ref, (y2, q2, db2, dl2)):
+        assert torch.equal(a[:, :out], b)
+    assert torch.equal(sc, sc2)
+    v = torch.from_numpy(q8.q8_decode(q2.cpu().numpy(), sc2.cpu().numpy())).to(DEV)
+    size = (dy2.double().abs() * v.abs()).sum(0) / n2.double()
+    exact = (dy2.double() * v).sum(0) / n2.double()
+    assert ((dm2.double() - exact).abs() <= 2.0 ** -24 * (T + 16) * size).all()
+    back, back2 = torch.empty_like(base), shifted(torch.empty_like(cut[0]), by + 3)
+    dora.dora_q8_load(q, sc, 1, back)
+    dora.dora_q8_load(q2, sc2, 1, back2)
+    assert torch.equal(back[:, :out], back2)
+
+
 def test_offsets_past_32_bits():
     rows, cols = 300000, 14400                     # 4.3e9 elements
     x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
