@@ -14,7 +14,12 @@
 // compose.cu: a thread holds one 16-byte piece of a row, so a block of 128
 // columns is 16 neighbouring threads in bf16 and a whole warp in fp32, and its
 // maximum is a butterfly of shuffles over them; the quantised piece is stored
-// from the same registers.  Rows that are ragged or not 16-byte aligned take
+// from the same registers.  At 15360 x 8192, in us and as a fraction of the
+// 6800 GB/s of a plain copy (bytes that have to move / time):
+//            store       load        forward     backward (with the d_mag sum)
+//   bf16    64  0.87    66  0.85    135  0.96    140  0.92
+//   f32    100  0.92   109  0.85    243  0.99    269  0.89
+// A call on a few rows costs its launch, about 6 us (the backward's two, 12).  Rows that are ragged or not 16-byte aligned take
 // the same kernels with four columns a thread, 32 apart (Piece).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -167,10 +172,11 @@ q8_fwd_kernel(const Act *__restrict__ base, const Act *__restrict__ lora, const 
               int64_t T, int64_t out, Act *__restrict__ y, uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
   using P = Piece<Act, RAGGED>;
   constexpr int VEC = P::VEC;
-  // token rows in flight per thread (bf16, 15360 x 8192: store 66, 62, 63, 68 us
-  // and compose 150, 137, 141, 146 us with 2, 3, 4 and 8; 15360 x 8191: store
-  // 94, 128, 128 us and compose 225, 219, 214 us with 1, 2 and 3)
-  constexpr int U = RAGGED ? 1 : 3;
+  // token rows in flight per thread (15360 x 8192 bf16: store 66, 62, 63, 68 us
+  // and compose 150, 137, 141, 146 us with 2, 3, 4 and 8; f32: compose 243, 267,
+  // 264 us with 1, 2 and 3; 15360 x 8191 bf16: store 94, 128, 128 us and compose
+  // 225, 219, 214 us with 1, 2 and 3)
+  constexpr int U = RAGGED || (COMPOSE && VEC == 4) ? 1 : 3;
   const int64_t c0 = P::first();
   const int live = P::live(c0, out);   // a thread past the row's end takes part in the maxima, with zeros
   const int64_t lanes = (int64_t)gridDim.y * kBY;
@@ -220,43 +226,56 @@ q8_fwd_kernel(const Act *__restrict__ base, const Act *__restrict__ lora, const 
   }
 }
 
-// a 128 x 128 block with one scale per thread block (a frozen weight, once)
-template <typename Act>
+// a 128 x 128 block with one scale per thread block (a frozen weight, once),
+// held in registers between its maximum and its bytes: one read of x
+template <typename Act, bool RAGGED>
 __global__ void __launch_bounds__(kThreads)
 q8_store_tile_kernel(const Act *__restrict__ x, int64_t rows, int64_t cols, uint8_t *__restrict__ q,
                      uint8_t *__restrict__ scale) {
-  using IO = Io<Act, 1>;
-  __shared__ uint32_t wmax[kBY];
+  using P = Piece<Act, RAGGED>;
+  constexpr int kAcross = kQBlock / P::VEC, kDown = kThreads / kAcross, kPasses = kQBlock / kDown;
+  __shared__ uint32_t wmax[kThreads / 32];
   const int64_t nsc = (cols + kQBlock - 1) / kQBlock;
-  const int64_t r0 = (int64_t)(blockIdx.x / nsc) * kQBlock, c0 = (int64_t)(blockIdx.x % nsc) * kQBlock;
+  const int tid = threadIdx.x, at = tid % kAcross;
+  const int64_t c0 = (int64_t)(blockIdx.x % nsc) * kQBlock + (RAGGED ? at : at * P::VEC);
+  const int64_t r0 = (int64_t)(blockIdx.x / nsc) * kQBlock + tid / kAcross;
+  const int live = P::live(c0, cols);
+  // past the last row the last row again, and past the row's end its first
+  // piece, which change no maximum.  Loads without conditions all go out at
+  // once (8192 x 8192 f32: 69 us, 4870 GB/s; 147 us with a condition on each)
+  const int64_t from = live > 0 ? c0 : c0 - at * (RAGGED ? 1 : P::VEC);
+  const int load_live = RAGGED && live > 0 ? live : RAGGED ? 1 : P::VEC;
+  typename P::Raw raw[kPasses];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int64_t r = r0 + k * kDown;
+    raw[k] = P::load(x, (r < rows ? r : rows - 1) * cols + from, load_live);
+  }
   uint32_t m = 0;
-  for (int64_t r = r0 + threadIdx.y; r < min(r0 + kQBlock, rows); r += kBY)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t c = c0 + 32 * k + threadIdx.x;
-      float v[1] = {0.0f};
-      if (c < cols) IO::unpack(IO::load(x, r * cols + c), v);
-      m = max(m, finite_bits(v[0]));
-    }
+  for (int k = 0; k < kPasses; ++k) {
+    float v[P::VEC];
+    P::unpack(raw[k], v);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (threadIdx.x == 0) wmax[threadIdx.y] = m;
+    for (int i = 0; i < P::VEC; ++i) m = max(m, finite_bits(v[i]));
+  }
+  m = block_max<4>(m);               // of the warp
+  if (tid % 32 == 0) wmax[tid / 32] = m;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kBY; ++k) m = max(m, wmax[k]);
+  for (int k = 0; k < kThreads / 32; ++k) m = max(m, wmax[k]);
   const uint32_t sc = scale_byte(m);
   const float inv = scale_inverse(sc);
-  for (int64_t r = r0 + threadIdx.y; r < min(r0 + kQBlock, rows); r += kBY)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t c = c0 + 32 * k + threadIdx.x;
-      if (c < cols) {
-        float v[1];
-        IO::unpack(IO::load(x, r * cols + c), v);
-        q[r * cols + c] = static_cast<uint8_t>(quant2(inf_to_nan(v[0]), 0.0f, inv));
-      }
-    }
-  if (threadIdx.x == 0 && threadIdx.y == 0) scale[blockIdx.x] = static_cast<uint8_t>(sc);
+  for (int k = 0; k < kPasses; ++k) {
+    const int64_t r = r0 + k * kDown;
+    float v[P::VEC];
+    P::unpack(raw[k], v);
+#pragma unroll
+    for (int i = 0; i < P::VEC; ++i) v[i] = inf_to_nan(v[i]);
+    P::store_q(q, r * cols + c0, r < rows ? live : 0, v, inv);
+  }
+  if (tid == 0) scale[blockIdx.x] = static_cast<uint8_t>(sc);
 }
 
 // ---------------------------------------------------------------------------
@@ -430,6 +449,16 @@ dora_status run_q8_fwd(const void *base, const void *lora, const float *g, float
              : launch_q8_fwd<Act, true, COMPOSE>(base, lora, g, s, T, out, y, q, scale, stream, device, sms);
 }
 
+template <typename Act>
+dora_status run_q8_store_tile(const void *x, int64_t rows, int64_t cols, int64_t tiles, void *q, void *scale,
+                              cudaStream_t stream) {
+  const auto kern = q8_vector_ok<Act>(cols, {x}, q) ? &q8_store_tile_kernel<Act, false> : &q8_store_tile_kernel<Act, true>;
+  kern<<<(unsigned)tiles, kThreads, 0, stream>>>(static_cast<const Act *>(x), rows, cols, static_cast<uint8_t *>(q),
+                                                 static_cast<uint8_t *>(scale));
+  dora::count_launches(1);
+  return dora::launch_status();
+}
+
 template <typename Act, bool RAGGED>
 dora_status launch_q8_load(const void *q, const void *scale, int64_t T, int64_t out, int block_rows, void *x,
                            cudaStream_t stream, int device, int sms) {
@@ -494,15 +523,8 @@ extern "C" dora_status dora_q8_store(dora_dtype act, const void *x, int64_t rows
                                                        device, info.sms);
   const int64_t tiles = dora::ceil_div(rows, kQBlock) * dora::ceil_div(cols, kQBlock);
   if (tiles > kMaxDim) return DORA_ERR_SHAPE;
-  uint8_t *qo = static_cast<uint8_t *>(q), *so = static_cast<uint8_t *>(scale);
-  if (act == DORA_BF16)
-    q8_store_tile_kernel<__nv_bfloat16><<<(unsigned)tiles, dim3(kBX, kBY), 0, cs>>>(
-        static_cast<const __nv_bfloat16 *>(x), rows, cols, qo, so);
-  else
-    q8_store_tile_kernel<float>
-        <<<(unsigned)tiles, dim3(kBX, kBY), 0, cs>>>(static_cast<const float *>(x), rows, cols, qo, so);
-  dora::count_launches(1);
-  return dora::launch_status();
+  return act == DORA_BF16 ? run_q8_store_tile<__nv_bfloat16>(x, rows, cols, tiles, q, scale, cs)
+                          : run_q8_store_tile<float>(x, rows, cols, tiles, q, scale, cs);
 }
 
 extern "C" dora_status dora_q8_load(dora_dtype act, const void *q, const void *scale, int64_t rows, int64_t cols,
