@@ -14,13 +14,12 @@
 // first) it moved six times that and was the limit.
 //
 // The tensor core's fp32 sum rounds toward zero, so its error grows with the
-// length of a chain of MMAs.  A window of 256 or 512 tokens is one chain (16
-// or 32 MMAs of k = 16); the windows are added up in registers with ordinary
-// rounding.
+// length of a chain of MMAs.  A window of 512 tokens is one chain (32 MMAs of
+// k = 16); the windows are added up in registers with ordinary rounding.
 //
 // Work: a tile of the result is 128 features x N columns of r; its windows
-// are units, and each CTA (one per SM) takes an equal run of units over all
-// tiles.  A CTA that has a whole tile writes dA; otherwise it writes its part
+// are units, and each CTA (one or two an SM) takes an equal run of units over
+// all tiles.  A CTA that has a whole tile writes dA; otherwise it writes its part
 // to the workspace and grad_join_kernel adds the parts of a tile in order
 // (bitwise reproducible).
 //   warp 0      x by TMA: 128 tokens x 128 features a stage (16 KB), and the
@@ -31,6 +30,12 @@
 //               warp; window w - 1 out of tensor memory while window w runs,
 //               half of the columns a warp
 //   warp 10     dxa by TMA: 128 tokens x 64 columns a box (16 KB)
+// What bounds it: the work is 2 T in r bf16 operations and T in bytes of x, and
+// it reaches about half of either rate, as the roles' chains of instructions
+// and hand-overs set the time of a stage.  15360 x 8192, us, and what reading x
+// or the products (at 1886 TFLOP/s) would take: r = 16 36 (19, x), r = 128 48
+// (20, x), r = 384 96 (51, products), r = 768 178 (103).  At r = 384 the tensor
+// pipe is active in 37% of the cycles, the issue slots in 44%, the ALU in 39%.
 // A hand-over through an mbarrier was measured at 230 cycles, and four of them
 // and a load from memory lie on the way of a stage, so each buffer is a ring of
 // its own that is freed as early as it can be: x once it is in registers, dxa
@@ -47,7 +52,11 @@
 namespace {
 
 constexpr int kTok = 128;                        // tokens per stage
-constexpr int kShortWin = 256, kLongWin = 512;   // tokens per window
+// Tokens per window.  Longer ones are read out and joined less often, but the
+// sum's error grows with them: 15360 x 8192, r = 384: 102, 96, 92 us and 1.4,
+// 1.6, 2.9e-7 of dA's norm with 256, 512, 1024; 16384 x 256, r = 256: 21 and 14
+// us with 256 and 512
+constexpr int kWin = 512;
 constexpr int kWorkers = 8;                      // conversion warps, in two groups that take alternate stages
 constexpr int kThreadsG = 96 + 32 * kWorkers;
 constexpr unsigned kRawBytes = kTok * 128;       // 16 KB of x
@@ -86,7 +95,6 @@ constexpr unsigned kFactorBytes = kTok * 2 + 16; // a stage's factors, and wheth
 struct GradParams {
   int T, in, r;
   int mtiles, ntiles, windows;     // tiles are m fastest; windows per tile
-  int win;                         // tokens per window
   int ncols;                       // columns of r per tile (N of the MMA)
   int boxes;                       // dxa boxes per stage
   int nsx;
@@ -257,7 +265,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
   const int nu = static_cast<int>(first_unit(units, blockIdx.x + 1, gridDim.x) - u0);
   Place at_unit(p, u0);
   // stages of a window
-  auto nstages = [&](int w) { return min(p.win, p.T - w * p.win + kTok - 1) / kTok; };
+  auto nstages = [&](int w) { return min(kWin, p.T - w * kWin + kTok - 1) / kTok; };
 
   // a producer that gives up leaves copies in flight, whose barriers may also
   // wait for others that have left: they land within microseconds, wait 1 ms
@@ -279,7 +287,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       const uint8_t *sp = p.scale + from.mt;
 #pragma unroll
       for (int i = 0; i < kTok / 32; ++i) {
-        const int t = from.w * p.win + fk * kTok + 32 * i + lane;
+        const int t = from.w * kWin + fk * kTok + 32 * i + lane;
         dst[i] = 127u;
         if (fu < nu && t < p.T)
           // volatile: not moved down to its use by the compiler
@@ -308,7 +316,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
         const uint32_t fb = xfull + 8u * x.i;
         if (elect_one()) {
           mbar_expect_tx(fb, kRawBytes);
-          tma_load_2d(x_at + x.i * kRawBytes, &mX, at_unit.mt * kTcM, at_unit.w * p.win + k * kTok, fb);
+          tma_load_2d(x_at + x.i * kRawBytes, &mX, at_unit.mt * kTcM, at_unit.w * kWin + k * kTok, fb);
         }
         issued = true;
         uint16_t *dst = reinterpret_cast<uint16_t *>(factors + x.i * kFactorBytes);
@@ -349,7 +357,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
           mbar_expect_tx(fb, d_stage);
 #pragma unroll
           for (int b = 0; b < (kN + 63) / 64; ++b)
-            if (b < p.boxes) tma_load_2d(at + b * kBox, &mD, n0 + 64 * b, at_unit.w * p.win + k * kTok, fb);
+            if (b < p.boxes) tma_load_2d(at + b * kBox, &mD, n0 + 64 * b, at_unit.w * kWin + k * kTok, fb);
         }
         __syncwarp();
         issued = true;
@@ -521,7 +529,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
           tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
         } else {
           convert_any(p.scale + at_unit.mt, p.nsx, p.T,
-                      at_unit.w * p.win + k * kTok + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
+                      at_unit.w * kWin + k * kTok + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
                       from + 4096u * g2 + 2048u, to + 16u * g2);
         }
       }
@@ -644,7 +652,7 @@ extern "C" size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r) 
   if (bad_size(T, 0) || bad_size(in, 0) || r < 1 || r > kMaxR) return 0;
   if (T == 0 || in == 0) return 256;
   // two parts per CTA, for up to kMaxCtasG CTAs
-  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, tile_columns(r)) * dora::ceil_div(T, kShortWin);
+  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, tile_columns(r)) * dora::ceil_div(T, kWin);
   const int64_t ctas = units < kMaxCtasG ? units : kMaxCtasG;
   return static_cast<size_t>(2 * ctas) * tile_columns(r) * kTcM * sizeof(float);
 }
@@ -681,10 +689,7 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   p.boxes = static_cast<int>(dora::ceil_div(p.ncols, 64));
   p.mtiles = static_cast<int>(dora::ceil_div(in, kTcM));
   p.ntiles = static_cast<int>(dora::ceil_div(r, p.ncols));
-  // short windows spread a small problem more evenly, long ones are read out
-  // half as often: those where every CTA has at least 8 of them
-  p.win = static_cast<int64_t>(p.mtiles) * p.ntiles * dora::ceil_div(T, kLongWin) >= 8 * info.sms ? kLongWin : kShortWin;
-  p.windows = static_cast<int>(dora::ceil_div(T, p.win));
+  p.windows = static_cast<int>(dora::ceil_div(T, kWin));
   p.nsx = static_cast<int>(dora::ceil_div(in, kQBlock));
   p.scale = static_cast<const uint8_t *>(xscale);
   p.dA = dA;

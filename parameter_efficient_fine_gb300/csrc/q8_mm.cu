@@ -20,9 +20,15 @@
 // (M-major, the transpose bit of the instruction).
 //
 // q8_split_kernel: up to 128 tokens, one tile of 128 features x NT of them per
-// cluster of CTAs, which share its k range; each CTA streams its part through a ring of TMA
-// stages, and the parts meet in distributed shared memory, summed in rank
-// order (bitwise reproducible, no workspace).
+// cluster of CTAs, which share its k range; each CTA streams its part through
+// a ring of TMA stages, and the parts meet in distributed shared memory,
+// summed in rank order (bitwise reproducible, no workspace).  It has to read W
+// once and is bound by that and by what lies around it: the launch, the first
+// loads' latency and the joining of the parts are 3 us of the 13.0 that 1 x
+// 8192 x 8192 takes (9.9 to read W at the copy bandwidth; 5150 GB/s), so its
+// set-up and the first boxes of W into L2 overlap the end of the launch
+// before.  37 x 14336 x 4096: 13.5 us (8.8); 128 x 8192 x 8192: 18.3 (10.3),
+// where the token box is as large as W's.
 //   warp 0     TMA producer: per k block the W box (16 KB) and the token box
 //   warp 1     tensor memory, MMA issue (four 32-wide steps per k block)
 //   warps 2-5  scale words into tensor memory, four k blocks at a time, each
@@ -33,7 +39,11 @@
 // half of what a single CTA's tile would; the scale words of all tokens of the
 // tile are written in both CTAs.  Up to 224 tokens, two accumulators and the
 // scale words fill tensor memory and a tile's result leaves while the next
-// tile's MMAs run; a tile of more tokens has one accumulator.
+// tile's MMAs run; a tile of more tokens has one accumulator.  It is bound by
+// the tensor cores: their pipe is active in 83% of the cycles (8192^3), and
+// over longer calls the power limit lowers the clock (15360 x 8192 x 8192: 650
+// us, 3.16 PFLOP/s; 8192 x 4096 x 4096: 89-100 us; 512 x 8192 x 8192: 27 us).
+// dy W takes as long as x W^T.
 //   warp 0      TMA producer (each CTA its own boxes, on the even CTA's barrier)
 //   warp 1      tensor memory, MMA issue (even CTA).  A stage is two k blocks: waiting
 //               for one and issuing its MMAs takes this warp about 600 cycles,
@@ -366,7 +376,10 @@ constexpr unsigned kPairXBox = kPairTok / 2 * kKB;   // room for 128 tokens, one
 constexpr unsigned kPairStage = kPairKB * (kPairBox + kPairXBox);
 constexpr int kPairThreads = 14 * 32;
 constexpr int kPairSfCol = 2 * kPairTwo, kPairSfStride = 16;   // scale words: 4 columns of W's, 8 of the tokens'
-constexpr int kGroupF = 8;                           // feature tiles per tile-order group (L2 reuse)
+// feature tiles per tile-order group, for reuse in L2 (15360 x 8192 x 8192: 701,
+// 676, 629, 628 us with 2, 4, 8, 16, 671 with one group; 8192 x 14336 x 4096: 327
+// to 333 with each, 341 with one group)
+constexpr int kGroupF = 8;
 
 __device__ __forceinline__ void mma_q8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                             uint32_t sfb, uint32_t acc) {
@@ -770,6 +783,10 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   p.wscale = static_cast<const uint8_t *>(wscale);
   p.y = static_cast<__nv_bfloat16 *>(y);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  // up to 128 tokens W is read by all SMs at once, its k range split where there
+  // are few tiles; the pairs, one tile of 256 features each, would leave most
+  // of them idle (us split / on pairs: 128 x 8192 x 8192 18.6 / 20.4, 70 x 4096 x
+  // 14336 16.0 / 27.9, 64 x 8192 x 8192 15.8 / 20.2, 128 x 14336 x 4096 17.2 / 15.8)
   if (T > kSplitTok) {
     const int pairs = resident_pairs(device, info.sms);
     if (pairs == 0) return DORA_ERR_CUDA;
@@ -796,6 +813,8 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   const int nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   p.tiles = static_cast<int>(dora::ceil_div(p.nfeat, kTcM));
   // the k range over as many CTAs as keep all clusters resident at two CTAs an SM
+  // (us with clusters of up to 1, 2, 4, 8: 1 x 8192 x 8192 20.0, 14.6, 13.2, 13.2;
+  // 37 x 4096 x 14336 33.8, 22.1, 15.7, 14.3; 1 x 1024 x 8192 18.3, 11.3, 8.0, 7.9)
   int cluster = 1;
   while (cluster < kMaxCluster && p.tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= p.kblocks) cluster *= 2;
   CUtensorMap mW, mX;
