@@ -124,15 +124,15 @@ def load_library():
 
 
 def _ptr(x) -> int:
+    if getattr(x, "is_cuda", False):
+        return x.data_ptr()
     if x is None:
         return 0
     if isinstance(x, int):
         return x
     # every pointer of the C ABI is a device pointer: a host tensor would hand
     # a host address to the kernels
-    if not getattr(x, "is_cuda", False):
-        raise ValueError(f"libdora takes CUDA tensors (device memory); got one on {getattr(x, 'device', type(x))}")
-    return x.data_ptr()
+    raise ValueError(f"libdora takes CUDA tensors (device memory); got one on {getattr(x, 'device', type(x))}")
 
 
 def _stream(stream) -> int:
@@ -288,8 +288,8 @@ def _q8(name: str, rows: int, cols: int, block_rows: int, q, scale) -> None:
     """The shapes of an 8-bit form; the C ABI sees only the matrix's."""
     if q.element_size() != 1 or scale.element_size() != 1:
         raise TypeError(f"{name}: the 8-bit form is bytes, got {q.dtype} and {scale.dtype}")
-    want = (-(-rows // block_rows), -(-cols // 128)) if block_rows in (1, 128) else None
-    if tuple(q.shape) != (rows, cols) or (want and tuple(scale.shape) != want):
+    want = (-(-rows // block_rows), -(-cols // 128)) if block_rows == 1 or block_rows == 128 else None
+    if q.shape != (rows, cols) or (want and scale.shape != want):
         raise ValueError(f"{name}: 8-bit form of [{rows}, {cols}] with {block_rows} rows a scale: "
                          f"got q {tuple(q.shape)}, scale {tuple(scale.shape)}")
 
@@ -302,7 +302,7 @@ def _dense(name: str, *ts) -> None:
 
 def _same(name: str, shape, dtype, *ts) -> None:
     for t in ts:
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        if t.shape != shape or t.dtype != dtype:
             raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
 
 
