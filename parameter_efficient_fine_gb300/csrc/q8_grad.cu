@@ -17,11 +17,12 @@
 // length of a chain of MMAs.  A window of 512 tokens is one chain (32 MMAs of
 // k = 16); the windows are added up in registers with ordinary rounding.
 //
-// Work: a tile of the result is 128 features x N columns of r; its windows
-// are units, and each CTA (one or two an SM) takes an equal run of units over
-// all tiles.  A CTA that has a whole tile writes dA; otherwise it writes its part
-// to the workspace and grad_join_kernel adds the parts of a tile in order
-// (bitwise reproducible).
+// Work: a tile of the result is 128 features x N columns of r; its stages of
+// 128 tokens are units, and each CTA (one or two an SM) takes an equal run of
+// units over all tiles, in windows of up to four.  (Runs of whole windows left up
+// to a sixth of the CTAs idle at the end: r = 16 36.4 us, now 34.4.)  A CTA that
+// has a whole tile writes dA; otherwise it writes its part to the workspace and
+// grad_join_kernel adds the parts of a tile in order (bitwise reproducible).
 //   warp 0      x by TMA: 128 tokens x 128 features a stage (16 KB), and the
 //               stage's 128 scales as bf16 factors in shared memory
 //   warp 1      tensor memory (two window accumulators, a ring of M operands),
@@ -33,8 +34,8 @@
 // What bounds it: the work is 2 T in r bf16 operations and T in bytes of x, and
 // it reaches about half of either rate, as the roles' chains of instructions
 // and hand-overs set the time of a stage.  15360 x 8192, us, and what reading x
-// or the products (at 1886 TFLOP/s) would take: r = 16 36 (19, x), r = 128 48
-// (20, x), r = 384 96 (51, products), r = 768 178 (103).  At r = 384 the tensor
+// or the products (at 1886 TFLOP/s) would take: r = 16 33 (19, x), r = 128 47
+// (20, x), r = 384 95 (51, products), r = 768 177 (103).  At r = 384 the tensor
 // pipe is active in 37% of the cycles, the issue slots in 44%, the ALU in 39%.
 // A hand-over through an mbarrier was measured at 230 cycles, and four of them
 // and a load from memory lie on the way of a stage, so each buffer is a ring of
@@ -69,8 +70,8 @@ constexpr int kMaxCtasG = 512;
 // tile's columns.  x and the operands in even numbers, as two groups take
 // turns.  What limits a stage is the length of the roles' instruction chains,
 // so where a CTA needs half of an SM's memory, two share it (r = 16 at 15360 x
-// 8192: 36.5 us against 42.4 with one CTA and twice the rings; at 64 columns the
-// registers that two CTAs leave do not hold the sums)
+// 8192, with runs of whole windows: 36.5 us against 42.4 with one CTA and twice
+// the rings; at 64 columns the registers that two CTAs leave do not hold the sums)
 struct Rings {
   int per_sm, x, d, ops;
 };
@@ -94,7 +95,7 @@ constexpr unsigned kFactorBytes = kTok * 2 + 16; // a stage's factors, and wheth
 
 struct GradParams {
   int T, in, r;
-  int mtiles, ntiles, windows;     // tiles are m fastest; windows per tile
+  int mtiles, ntiles, stages;      // tiles are m fastest; stages (of kTok tokens) per tile
   int ncols;                       // columns of r per tile (N of the MMA)
   int boxes;                       // dxa boxes per stage
   int nsx;
@@ -107,19 +108,25 @@ struct GradParams {
 // first unit of CTA i of n
 __host__ __device__ __forceinline__ int64_t first_unit(int64_t units, int i, int n) { return units * i / n; }
 
-// a unit's place: window w of tile (mt, nt).  Counted up unit by unit, as a
-// 64-bit division in every role's loop costs more than a stage of work
+// a unit's place: stage k of tile (mt, nt).  Counted up, as a 64-bit division
+// in every role's loop costs more than a stage of work
 struct Place {
-  int mt, nt, w;
+  int mt, nt, k;
   __device__ __forceinline__ Place(const GradParams &p, int64_t u) {
-    const int tile = static_cast<int>(u / p.windows);
-    w = static_cast<int>(u - static_cast<int64_t>(tile) * p.windows);
+    const int tile = static_cast<int>(u / p.stages);
+    k = static_cast<int>(u - static_cast<int64_t>(tile) * p.stages);
     nt = tile / p.mtiles;
     mt = tile - nt * p.mtiles;
   }
-  __device__ __forceinline__ void next(const GradParams &p) {
-    if (++w == p.windows) {
-      w = 0;
+  // stages of the window that begins here: up to the tile's end and the run's
+  __device__ __forceinline__ int window(const GradParams &p, int left) const {
+    return min(min(kWin / kTok, p.stages - k), left);
+  }
+  // n stages on, which do not pass the tile's end
+  __device__ __forceinline__ void next(const GradParams &p, int n) {
+    k += n;
+    if (k == p.stages) {
+      k = 0;
       if (++mt == p.mtiles) {
         mt = 0;
         ++nt;
@@ -260,12 +267,10 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
   const uint32_t tmem = ctl->tmem_base;
   pdl_trigger();    // grad_join_kernel's launch overlaps this kernel; it waits for its end
   pdl_wait();       // the set-up above overlaps the end of the launch before
-  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
+  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.stages;
   const int64_t u0 = first_unit(units, blockIdx.x, gridDim.x);
-  const int nu = static_cast<int>(first_unit(units, blockIdx.x + 1, gridDim.x) - u0);
-  Place at_unit(p, u0);
-  // stages of a window
-  auto nstages = [&](int w) { return min(kWin, p.T - w * kWin + kTok - 1) / kTok; };
+  int left = static_cast<int>(first_unit(units, blockIdx.x + 1, gridDim.x) - u0);   // of the run, in each role
+  Place at(p, u0);
 
   // a producer that gives up leaves copies in flight, whose barriers may also
   // wait for others that have left: they land within microseconds, wait 1 ms
@@ -281,42 +286,37 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     // are needed (one byte per token and tile: a sector each, often from memory)
     constexpr int kAhead = 3;
     uint32_t ring[kAhead][kTok / 32];
-    Place from = at_unit;   // of the stage whose scales are requested next: stage fk of unit fu
-    int fk = 0, fu = 0, fns = nstages(from.w);
+    Place from = at;        // of the stage whose scales are requested next
+    int from_left = left;
     auto fetch = [&](uint32_t (&dst)[kTok / 32]) {
       const uint8_t *sp = p.scale + from.mt;
 #pragma unroll
       for (int i = 0; i < kTok / 32; ++i) {
-        const int t = from.w * kWin + fk * kTok + 32 * i + lane;
+        const int t = from.k * kTok + 32 * i + lane;
         dst[i] = 127u;
-        if (fu < nu && t < p.T)
+        if (from_left > 0 && t < p.T)
           // volatile: not moved down to its use by the compiler
           asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(dst[i]) : "l"(sp + static_cast<int64_t>(t) * p.nsx));
       }
-      if (++fk == fns) {
-        fk = 0;
-        ++fu;
-        from.next(p);
-        fns = nstages(from.w);
-      }
+      --from_left;
+      from.next(p, 1);
     };
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) fetch(ring[a]);
     bool ok = !loads_withheld(p.guard);
     bool issued = false;
     At<kR.x> x;
-    int u = 0, k = 0, ns = nstages(at_unit.w);
-    while (ok && u < nu) {
+    while (ok && left > 0) {
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        if (!ok || u >= nu) break;
+        if (!ok || left == 0) break;
         ok = guard_wait(xfree + 8u * x.i, x.phase ^ 1u, ctl, p.guard, 31);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t fb = xfull + 8u * x.i;
         if (elect_one()) {
           mbar_expect_tx(fb, kRawBytes);
-          tma_load_2d(x_at + x.i * kRawBytes, &mX, at_unit.mt * kTcM, at_unit.w * kWin + k * kTok, fb);
+          tma_load_2d(x_at + x.i * kRawBytes, &mX, at.mt * kTcM, at.k * kTok, fb);
         }
         issued = true;
         uint16_t *dst = reinterpret_cast<uint16_t *>(factors + x.i * kFactorBytes);
@@ -332,12 +332,8 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
         if (lane == 0) mbar_arrive(fb);
         fetch(ring[a]);
         x.next();
-        if (++k == ns) {
-          k = 0;
-          ++u;
-          at_unit.next(p);
-          ns = nstages(at_unit.w);
-        }
+        --left;
+        at.next(p, 1);
       }
     }
     if (!ok && issued) settle_copies();
@@ -346,23 +342,20 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     bool ok = !loads_withheld(p.guard);
     bool issued = false;
     At<kR.d> d;
-    for (int u = 0; u < nu && ok; ++u, at_unit.next(p)) {
-      const int n0 = at_unit.nt * p.ncols, ns = nstages(at_unit.w);
-      for (int k = 0; k < ns; ++k) {
-        ok = guard_wait(dfree + 8u * d.i, d.phase ^ 1u, ctl, p.guard, 39);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t fb = dfull + 8u * d.i, at = d_at + d.i * d_stage;
-        if (elect_one()) {
-          mbar_expect_tx(fb, d_stage);
+    for (; left > 0 && ok; --left, at.next(p, 1)) {
+      ok = guard_wait(dfree + 8u * d.i, d.phase ^ 1u, ctl, p.guard, 39);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t fb = dfull + 8u * d.i, to = d_at + d.i * d_stage;
+      if (elect_one()) {
+        mbar_expect_tx(fb, d_stage);
 #pragma unroll
-          for (int b = 0; b < (kN + 63) / 64; ++b)
-            if (b < p.boxes) tma_load_2d(at + b * kBox, &mD, n0 + 64 * b, at_unit.w * kWin + k * kTok, fb);
-        }
-        __syncwarp();
-        issued = true;
-        d.next();
+        for (int b = 0; b < (kN + 63) / 64; ++b)
+          if (b < p.boxes) tma_load_2d(to + b * kBox, &mD, at.nt * p.ncols + 64 * b, at.k * kTok, fb);
       }
+      __syncwarp();
+      issued = true;
+      d.next();
     }
     if (!ok && issued) settle_copies();
   } else if (warp == 1) {
@@ -374,8 +367,8 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     At<kR.ops> op;
     At<2> win;
     const uint64_t b0 = mn_desc(d_at, kBox);
-    for (int wi = 0; wi < nu && ok; ++wi, at_unit.next(p), win.next()) {
-      const int ns = nstages(at_unit.w);
+    while (left > 0 && ok) {
+      const int ns = at.window(p, left);
       const uint32_t d = tmem + static_cast<uint32_t>(win.i * kN);
       ok = guard_wait(read0 + 8u * win.i, win.phase ^ 1u, ctl, p.guard, 32);
       uint32_t acc = 0;
@@ -401,6 +394,9 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
         ds.next();
         op.next();
       }
+      left -= ns;
+      at.next(p, ns);
+      win.next();
     }
     if (elect_one()) {
       mma_commit(fin);
@@ -444,18 +440,17 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       ++flushed;
       return true;
     };
-    // the stage this warp is at: stage k of ns of the CTA's unit wi
-    int wi = 0, k = grp, ns = nstages(at_unit.w);
-    int seg0 = 0;            // first unit of the run within one tile
-    // the end of the run: the tile's remaining windows up to unit `last`, and
-    // the sum to dA or to the workspace
-    auto finish = [&](const Place &at, int last) {
-      while (flushed <= last)
+    // the stage this warp is at: stage k of the ns of the CTA's window wi, which
+    // begins at `at`
+    int wi = 0, k = grp, ns = at.window(p, left);
+    bool from_start = at.k == 0;   // the run's part of this tile begins at the tile's start
+    // the end of that part: its remaining windows, up to window wi, and the sum
+    // to dA or to the workspace
+    auto finish = [&](bool at_end) {
+      while (flushed <= wi)
         if (!flush()) return false;
-      const bool whole = at.w + 1 == p.windows && last - seg0 + 1 == p.windows;
-      const bool from_start = at.w - (last - seg0) == 0;
       const int m = static_cast<int>(quad) * 32 + lane;
-      if (whole) {
+      if (from_start && at_end) {
         const int f = at.mt * kTcM + feature_of(m);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
@@ -471,18 +466,21 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       }
 #pragma unroll
       for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
-      seg0 = last + 1;
+      from_start = true;
       return true;
     };
-    // to the unit that holds stage k (counted from the start of unit wi)
+    // to the window that holds stage k (counted from the start of window wi)
     auto settle = [&]() {
-      while (k >= ns && wi < nu) {
-        k -= ns;
-        if (at_unit.w + 1 == p.windows || wi + 1 == nu) {
-          if (!finish(at_unit, wi)) return false;
+      while (k >= ns && left > 0) {
+        const bool at_end = at.k + ns == p.stages;
+        if (at_end || ns == left) {
+          if (!finish(at_end)) return false;
         }
-        at_unit.next(p);
-        if (++wi < nu) ns = nstages(at_unit.w);
+        k -= ns;
+        left -= ns;
+        at.next(p, ns);
+        ++wi;
+        ns = at.window(p, left);
       }
       return true;
     };
@@ -490,7 +488,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     At<kR.ops> op;
     x.next(grp);
     op.next(grp);
-    for (ok = settle(); ok && wi < nu; ok = settle()) {
+    for (ok = settle(); ok && left > 0; ok = settle()) {
       bool got = guard_wait(xfull + 8u * x.i, x.phase, ctl, p.guard, 35);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
@@ -528,8 +526,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
           tmem_st_16x256b_x2(to + 16u * g2, o[0]);
           tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
         } else {
-          convert_any(p.scale + at_unit.mt, p.nsx, p.T,
-                      at_unit.w * kWin + k * kTok + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
+          convert_any(p.scale + at.mt, p.nsx, p.T, (at.k + k) * kTok + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
                       from + 4096u * g2 + 2048u, to + 16u * g2);
         }
       }
@@ -542,8 +539,9 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       x.next(2);
       op.next(2);
       // the windows before this one, after this warp's last stage of it: their
-      // MMAs are done by then, and the one after it starts no earlier (a tile's
-      // only window without a stage for this warp is its last, which `finish` reads)
+      // MMAs are done by then, and the one after it starts no earlier (a window
+      // without a stage for this warp is the last of its tile or of the run,
+      // which `finish` reads)
       while (ok && flushed < wi && k + 2 >= ns) ok = flush();
       if (!ok) break;
       k += 2;
@@ -560,17 +558,22 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
 
 // dA of the tiles that more than one CTA worked on: their parts in CTA order.
 // One block: one tile, kJoin of its columns; a thread: one feature, kJoin / 2
-// columns, the parts of up to kJoinAt CTAs loaded at a time
-constexpr int kJoin = 8, kJoinAt = 4;
-__global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p, int ctas) {
+// columns, the parts of AT CTAs loaded at a time.  Many at a time where a tile
+// has more than four parts, whose loads are all that it waits for, else two, as
+// a load that is not needed costs its instructions (us with 2 and 16 at a time,
+// the gradient's kernel included: 8192 x 4096, r = 64 20.0, 18.3; 16384 x 1024,
+// r = 128 18.9, 13.6; 15360 x 8192, r = 384 94.8, 104.5; 2048 x 2048, r = 384 12.6,
+// 13.8)
+constexpr int kJoin = 8;
+template <int AT> __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p, int ctas) {
   __shared__ int owner[2];
   const int tile = blockIdx.x;
   if (threadIdx.x < 2) {
     // the CTA of the tile's first and of its last unit: first_unit(i) <= unit <
     // first_unit(i + 1), that is i = ceil((unit + 1) ctas / units) - 1.  Two
     // threads divide (in every thread the divisions were half of this kernel)
-    const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
-    const int64_t next = static_cast<int64_t>(tile) * p.windows + (threadIdx.x == 0 ? 1 : p.windows);
+    const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.stages;
+    const int64_t next = static_cast<int64_t>(tile) * p.stages + (threadIdx.x == 0 ? 1 : p.stages);
     owner[threadIdx.x] = static_cast<int>((next * ctas - 1) / units);
   }
   __syncthreads();
@@ -586,16 +589,16 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p, int 
   // start), the others' their first
   const float *src = p.part + static_cast<int64_t>(i0) * 2 * slot + n0 * kTcM + m;
   float s[kJoin / 2] = {};
-  for (int i = i0; i <= i1; i += kJoinAt, src += 2 * kJoinAt * slot) {
-    float v[kJoinAt][kJoin / 2];
+  for (int i = i0; i <= i1; i += AT, src += 2 * AT * slot) {
+    float v[AT][kJoin / 2];
 #pragma unroll
-    for (int b = 0; b < kJoinAt; ++b) {
+    for (int b = 0; b < AT; ++b) {
       const float *from = src + (2 * b + (b == 0 && i == i0 ? 1 : 0)) * slot;
 #pragma unroll
       for (int j = 0; j < kJoin / 2; ++j) v[b][j] = i + b <= i1 && j < live ? __ldcs(from + 2 * j * kTcM) : 0.0f;
     }
 #pragma unroll
-    for (int b = 0; b < kJoinAt; ++b)
+    for (int b = 0; b < AT; ++b)
 #pragma unroll
       for (int j = 0; j < kJoin / 2; ++j) s[j] += v[b][j];
   }
@@ -640,7 +643,8 @@ dora_status launch_grad(const CUtensorMap &mX, const CUtensorMap &mD, GradParams
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(dora::ceil_div(p.ncols, kJoin)));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, grad_join_kernel, p, ctas) != cudaSuccess) return DORA_ERR_CUDA;
+    const auto join = ctas > 4 * tiles ? &grad_join_kernel<16> : &grad_join_kernel<2>;
+    if (cudaLaunchKernelEx(&cfg, join, p, ctas) != cudaSuccess) return DORA_ERR_CUDA;
     dora::count_launches(1);
   }
   return dora::launch_status();
@@ -652,7 +656,7 @@ extern "C" size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r) 
   if (bad_size(T, 0) || bad_size(in, 0) || r < 1 || r > kMaxR) return 0;
   if (T == 0 || in == 0) return 256;
   // two parts per CTA, for up to kMaxCtasG CTAs
-  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, tile_columns(r)) * dora::ceil_div(T, kWin);
+  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, tile_columns(r)) * dora::ceil_div(T, kTok);
   const int64_t ctas = units < kMaxCtasG ? units : kMaxCtasG;
   return static_cast<size_t>(2 * ctas) * tile_columns(r) * kTcM * sizeof(float);
 }
@@ -689,17 +693,21 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   p.boxes = static_cast<int>(dora::ceil_div(p.ncols, 64));
   p.mtiles = static_cast<int>(dora::ceil_div(in, kTcM));
   p.ntiles = static_cast<int>(dora::ceil_div(r, p.ncols));
-  p.windows = static_cast<int>(dora::ceil_div(T, kWin));
+  p.stages = static_cast<int>(dora::ceil_div(T, kTok));
   p.nsx = static_cast<int>(dora::ceil_div(in, kQBlock));
   p.scale = static_cast<const uint8_t *>(xscale);
   p.dA = dA;
   p.part = static_cast<float *>(workspace);
   CUtensorMap mX, mD;
   if (!map_q8(&mX, xq, T, in, kTok) || !make_map(&mD, dxa, true, T, r, r, kTok, 128)) return DORA_ERR_CUDA;
-  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.windows;
+  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.stages;
   const int room = info.sms * rings_of(p.ncols).per_sm;
   const int most = room < kMaxCtasG ? room : kMaxCtasG;
-  const int ctas = units < most ? static_cast<int>(units) : most;
+  // at least four stages a CTA, where there are as many: the parts have to be
+  // joined (us with 1, 2, 4, 8 stages: 16384 x 256, r = 256 20, 20, 13, 13; 16384 x
+  // 128, r = 16 18, 13, 10, 11; 256 x 512, r = 16 8.4, 6.6, 6.7, 10.4)
+  const int64_t runs = dora::ceil_div(units, kWin / kTok);
+  const int ctas = runs < most ? static_cast<int>(runs) : most;
   const int half = p.ncols / 2;
   if (half <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
   if (half <= 16) return launch_grad<16>(mX, mD, p, ctas, cs);

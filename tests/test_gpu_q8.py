@@ -308,6 +308,29 @@ def test_lora_grad(T, inp, r):
     assert torch.equal(dA, run_grad(qd, scd, dd, 0xff))
 
 
+@pytest.mark.parametrize("T,inp,r", [
+    (20000, 144, 24), (9000, 528, 72), (2700, 4112, 200), (5000, 2064, 392), (16300, 1040, 16), (3000, 8192, 136),
+])
+def test_lora_grad_of_cut_runs(T, inp, r):
+    """Sizes at which a CTA's run of 128 tokens begins and ends inside a tile, at
+    any place of a window, and a tile has up to dozens of parts; twice the same bits."""
+    rng = np.random.default_rng(T + inp + r)
+    dxa = torch.from_numpy(rng.standard_normal((T, r))).to(DEV).bfloat16()
+    q, sc = store(torch.from_numpy(rng.standard_normal((T, inp))).to(DEV).bfloat16())
+    ws = workspace(dora.dora_lora_grad_q8_workspace(T, inp, r))
+    got = [torch.full((r, inp), float("nan"), device=DEV) for _ in range(2)]
+    for dA in got:
+        dora.dora_lora_grad_q8(dxa, q, sc, dA, ws)
+    x = torch.empty(T, inp, device=DEV)
+    dora.dora_q8_load(q, sc, 1, x)
+    assert_no_device_error()
+    ref = dxa.double().t() @ x.double()
+    size = dxa.double().abs().t() @ x.double().abs()
+    err = (got[0].double() - ref).abs()
+    assert (err <= 2.0 ** -23 * (T + 64) * size).all() and err.norm() <= 1e-6 * ref.norm()
+    assert torch.equal(got[0], got[1])
+
+
 def test_lora_grad_without_tokens():
     dA = run_grad(torch.empty(0, 144, dtype=U8, device=DEV), torch.empty(0, 2, dtype=U8, device=DEV),
                   torch.empty(0, 24, dtype=torch.bfloat16, device=DEV))
