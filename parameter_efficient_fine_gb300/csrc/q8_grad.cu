@@ -496,22 +496,34 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       const uint8_t *fa = factors + x.i * kFactorBytes;
       const bool large = *reinterpret_cast<const uint32_t *>(fa + 2 * kTok) != 0;
       const uint32_t to = tmem + ((quad * 32u) << 16) + 2 * kN + static_cast<uint32_t>(kOpCols * op.i);
-      // 32 tokens at a time, as 16 x 16 blocks
-#pragma unroll
-      for (int g2 = 0; g2 < kTok / 32; ++g2) {
-        uint32_t raw[2][4], o[2][8];   // o[h]: the 16 columns of feature block h
-        uint32_t top = 0;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) ldmatrix_x4_trans(from + 2048u * (2 * g2 + g), raw[g]);
+      // 32 tokens at a time, as 16 x 16 blocks, the next ones' loads before
+      // these ones' arithmetic.  NaN bytes are looked for once, at the end
+      struct Block {
+        uint32_t raw[2][4];
+        uint2 up[2];
+      } blk[2];
+      auto load_block = [&](int g2, Block &b) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint2 up = *reinterpret_cast<const uint2 *>(fa + 2 * (16 * (2 * g2 + g) + 4 * (lane & 3)));
+          ldmatrix_x4_trans(from + 2048u * (2 * g2 + g), b.raw[g]);
+          b.up[g] = *reinterpret_cast<const uint2 *>(fa + 2 * (16 * (2 * g2 + g) + 4 * (lane & 3)));
+        }
+      };
+      uint32_t top = 0;
+      load_block(0, blk[0]);
+#pragma unroll
+      for (int g2 = 0; g2 < kTok / 32; ++g2) {
+        if (g2 + 1 < kTok / 32) load_block(g2 + 1, blk[(g2 + 1) % 2]);
+        const Block &b = blk[g2 % 2];
+        uint32_t o[2][8];              // o[h]: the 16 columns of feature block h
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int h = i / 2, half = i % 2;
-            const Mags m = mags4(raw[g][i]);
+            const Mags m = mags4(b.raw[g][i]);
             top = max_mag(top, m);
-            const uint2 d = decode4(raw[g][i], m, half ? up.y : up.x);
+            const uint2 d = decode4(b.raw[g][i], m, half ? b.up[g].y : b.up[g].x);
             o[h][4 * g + half] = d.x;
             o[h][4 * g + 2 + half] = d.y;
           }
@@ -522,15 +534,17 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
           if (!ok) break;
           tc_fence_after();
         }
-        if (!__any_sync(0xffffffffu, large || has_nan(top))) {
-          tmem_st_16x256b_x2(to + 16u * g2, o[0]);
-          tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
-        } else {
-          convert_any(p.scale + at.mt, p.nsx, p.T, (at.k + k) * kTok + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
-                      from + 4096u * g2 + 2048u, to + 16u * g2);
-        }
+        tmem_st_16x256b_x2(to + 16u * g2, o[0]);
+        tmem_st_16x256b_x2(to + 16u * g2 + (16u << 16), o[1]);
       }
       if (!ok) break;
+      if (__any_sync(0xffffffffu, large || has_nan(top))) [[unlikely]] {
+        tmem_wait_st();                // what was written is written again
+#pragma unroll 1
+        for (int g2 = 0; g2 < kTok / 32; ++g2)
+          convert_any(p.scale + at.mt, p.nsx, p.T, (at.k + k) * kTok + 32 * g2 + 4 * (lane & 3), from + 4096u * g2,
+                      from + 4096u * g2 + 2048u, to + 16u * g2);
+      }
       if (lane == 0) mbar_arrive(xfree + 8u * x.i);
       tmem_wait_st();
       tc_fence_before();
