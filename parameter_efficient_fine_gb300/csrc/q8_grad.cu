@@ -32,11 +32,12 @@
 //               half of the columns a warp
 //   warp 10     dxa by TMA: 128 tokens x 64 columns a box (16 KB)
 // What bounds it: the work is 2 T in r bf16 operations and T in bytes of x, and
-// it reaches about half of either rate, as the roles' chains of instructions
-// and hand-overs set the time of a stage.  15360 x 8192, us, and what reading x
-// or the products (at 1886 TFLOP/s) would take: r = 16 33 (19, x), r = 128 47
-// (20, x), r = 384 95 (51, products), r = 768 177 (103).  At r = 384 the tensor
-// pipe is active in 37% of the cycles, the issue slots in 44%, the ALU in 39%.
+// it reaches about half of either rate, as the conversion warps' chains of
+// instructions and the hand-overs set the time of a stage.  15360 x 8192, us, and
+// what reading x or the products (at 1886 TFLOP/s) would take: r = 16 29 (19, x),
+// r = 128 43 (20, x), r = 384 93 (51, products), r = 768 174 (103).  With every
+// operand in L2 these are 28, 41 and 83: it is not the memory.  At r = 384 the
+// tensor pipe is active in 37% of the cycles, the issue slots in 44%.
 // A hand-over through an mbarrier was measured at 230 cycles, and four of them
 // and a load from memory lie on the way of a stage, so each buffer is a ring of
 // its own that is freed as early as it can be: x once it is in registers, dxa
@@ -60,6 +61,10 @@ constexpr int kTok = 128;                        // tokens per stage
 constexpr int kWin = 512;
 constexpr int kWorkers = 8;                      // conversion warps, in two groups that take alternate stages
 constexpr int kThreadsG = 96 + 32 * kWorkers;
+// a box's 128-byte rows are fetched alone: their neighbours belong to CTAs that
+// are at other tokens (15360 x 8192, us: r = 16 29.2 against 31.6 with 256 bytes
+// at a time, r = 128 43.0 against 46.9)
+constexpr CUtensorMapL2promotion kPromote = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
 constexpr unsigned kRawBytes = kTok * 128;       // 16 KB of x
 constexpr unsigned kBox = kTok * 128;            // 128 tokens x 64 columns of dxa
 constexpr int kMaxR = 1024;
@@ -713,7 +718,7 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   p.dA = dA;
   p.part = static_cast<float *>(workspace);
   CUtensorMap mX, mD;
-  if (!map_q8(&mX, xq, T, in, kTok) || !make_map(&mD, dxa, true, T, r, r, kTok, 128)) return DORA_ERR_CUDA;
+  if (!map_q8(&mX, xq, T, in, kTok, kPromote) || !make_map(&mD, dxa, true, T, r, r, kTok, 128)) return DORA_ERR_CUDA;
   const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.stages;
   const int room = info.sms * rings_of(p.ncols).per_sm;
   const int most = room < kMaxCtasG ? room : kMaxCtasG;

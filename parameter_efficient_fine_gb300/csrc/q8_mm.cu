@@ -87,6 +87,10 @@ struct MmParams {
   Guard guard;
 };
 
+// a box's 128-byte rows are fetched with their neighbours' (128 x 8192 x 8192:
+// 18.6 us, 19.0 without)
+constexpr CUtensorMapL2promotion kPromote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+
 // D (+)= A B with a power-of-two scale per row of A and per row of B, E4M3
 // operands in shared memory, scale words in tensor memory
 __device__ __forceinline__ void mma_q8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
@@ -750,7 +754,8 @@ template <bool TRANS>
 dora_status launch_pairs(const void *q, const void *wq, int64_t out, int64_t in, MmParams p, int pairs,
                          cudaStream_t cs) {
   CUtensorMap mW, mX;
-  if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, p.T, p.kdim, p.ntok / 2)) return DORA_ERR_CUDA;
+  if (!map_q8(&mW, wq, out, in, 128, kPromote) || !map_q8(&mX, q, p.T, p.kdim, p.ntok / 2, kPromote))
+    return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   pair_config(&cfg, attr, p.tiles < pairs ? p.tiles : pairs, cs);
@@ -818,7 +823,7 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   int cluster = 1;
   while (cluster < kMaxCluster && p.tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= p.kblocks) cluster *= 2;
   CUtensorMap mW, mX;
-  if (!map_q8(&mW, wq, out, in, 128) || !map_q8(&mX, q, T, p.kdim, nt)) return DORA_ERR_CUDA;
+  if (!map_q8(&mW, wq, out, in, 128, kPromote) || !map_q8(&mX, q, T, p.kdim, nt, kPromote)) return DORA_ERR_CUDA;
   switch (nt) {
     case 16: return launch_split<16, TRANS>(mW, mX, p, cluster, cs);
     case 32: return launch_split<32, TRANS>(mW, mX, p, cluster, cs);

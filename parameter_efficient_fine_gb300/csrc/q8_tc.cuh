@@ -93,8 +93,10 @@ template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, float (&v
   for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// bytes [rows, cols] (cols a multiple of 16) with a [box_rows x 128] box, 128-byte swizzle
-inline bool map_q8(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows) {
+// bytes [rows, cols] (cols a multiple of 16) with a [box_rows x 128] box, 128-byte
+// swizzle; `promotion` is how much a fetch from memory brings into L2
+inline bool map_q8(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows,
+                   CUtensorMapL2promotion promotion) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -102,7 +104,7 @@ inline bool map_q8(CUtensorMap *map, const void *base, int64_t rows, int64_t col
   cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
