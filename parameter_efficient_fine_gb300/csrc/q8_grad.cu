@@ -35,8 +35,8 @@
 // it reaches about half of either rate, as the conversion warps' chains of
 // instructions and the hand-overs set the time of a stage.  15360 x 8192, us, and
 // what reading x or the products (at 1886 TFLOP/s) would take: r = 16 29 (19, x),
-// r = 128 43 (20, x), r = 384 93 (51, products), r = 768 174 (103).  With every
-// operand in L2 these are 28, 41 and 83: it is not the memory.  At r = 384 the
+// r = 128 43 (20, x), r = 384 90 (51, products), r = 768 166 (103).  With every
+// operand in L2 the first two are 28 and 41: it is not the memory.  At r = 384 the
 // tensor pipe is active in 37% of the cycles, the issue slots in 44%.
 // A hand-over through an mbarrier was measured at 230 cycles, and four of them
 // and a load from memory lie on the way of a stage, so each buffer is a ring of
@@ -73,10 +73,11 @@ constexpr int kMaxCtasG = 512;
 // By the columns of a tile: CTAs per SM; stages of x and of dxa in shared
 // memory; M operands (64 columns) in tensor memory beside two windows of the
 // tile's columns.  x and the operands in even numbers, as two groups take
-// turns.  What limits a stage is the length of the roles' instruction chains,
-// so where a CTA needs half of an SM's memory, two share it (r = 16 at 15360 x
-// 8192, with runs of whole windows: 36.5 us against 42.4 with one CTA and twice
-// the rings; at 64 columns the registers that two CTAs leave do not hold the sums)
+// turns, and no fewer of dxa than of operands (the kernel says why).  What limits
+// a stage is the length of the roles' instruction chains, so where a CTA needs
+// half of an SM's memory, two share it (r = 16 at 15360 x 8192, with runs of
+// whole windows: 36.5 us against 42.4 with one CTA and twice the rings; at 64
+// columns the registers that two CTAs leave do not hold the sums)
 struct Rings {
   int per_sm, x, d, ops;
 };
@@ -225,6 +226,18 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
   constexpr int kUsed = 2 * kN + kOpCols * kR.ops;       // two windows, the M operands
   constexpr int kCols = kUsed <= 256 ? 256 : 512;
   static_assert(kUsed <= 512 / kR.per_sm, "tensor memory");
+  // a wait tells a barrier's phase from the one before, not from the one before
+  // that, so whoever waits for use c of a slot must know that use c - 1 is over:
+  // a group's own earlier stage for x and the operands, the end of an earlier
+  // MMA for dxa (which stage c's operand slot was waited for)
+  static_assert(kR.x % 2 == 0 && kR.ops % 2 == 0 && kR.d >= kR.ops, "phases");
+  // Who waits for a stage's dxa: the MMA warp, or, for wide tiles, one of the
+  // warps that hand it the operand.  A wait takes the MMA warp 150 cycles or
+  // more, in which it issues nothing, and the others' chains are shorter than a
+  // wide tile's MMAs (15360 x 8192, us, MMA warp / other: r = 768 174 / 166, r = 384
+  // 92.8 / 89.7, r = 192 54.1 / 51.8; r = 128 43.0 / 43.2, r = 64 39.1 / 40.1, r = 16
+  // 29.2 / 30.1)
+  constexpr bool kRelay = kN > 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t d_stage = p.boxes * kBox;
@@ -378,8 +391,8 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
       ok = guard_wait(read0 + 8u * win.i, win.phase ^ 1u, ctl, p.guard, 32);
       uint32_t acc = 0;
       for (int k = 0; k < ns; ++k) {
-        ok = ok && guard_wait(dfull + 8u * ds.i, ds.phase, ctl, p.guard, 36) &&
-             guard_wait(conv0 + 8u * op.i, op.phase, ctl, p.guard, 33);
+        if (!kRelay) ok = ok && guard_wait(dfull + 8u * ds.i, ds.phase, ctl, p.guard, 36);
+        ok = ok && guard_wait(conv0 + 8u * op.i, op.phase, ctl, p.guard, 33);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -491,8 +504,10 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     };
     At<kR.x> x;
     At<kR.ops> op;
+    At<kR.d> ds;
     x.next(grp);
     op.next(grp);
+    ds.next(grp);
     for (ok = settle(); ok && left > 0; ok = settle()) {
       bool got = guard_wait(xfull + 8u * x.i, x.phase, ctl, p.guard, 35);
       ok = __all_sync(0xffffffffu, got);
@@ -551,12 +566,18 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
                       from + 4096u * g2 + 2048u, to + 16u * g2);
       }
       if (lane == 0) mbar_arrive(xfree + 8u * x.i);
+      if (kRelay && (wk & 3) == 0) {
+        got = guard_wait(dfull + 8u * ds.i, ds.phase, ctl, p.guard, 36);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(conv0 + 8u * op.i);
       x.next(2);
       op.next(2);
+      ds.next(2);
       // the windows before this one, after this warp's last stage of it: their
       // MMAs are done by then, and the one after it starts no earlier (a window
       // without a stage for this warp is the last of its tile or of the run,
