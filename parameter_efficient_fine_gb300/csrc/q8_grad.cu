@@ -743,10 +743,11 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.stages;
   const int room = info.sms * rings_of(p.ncols).per_sm;
   const int most = room < kMaxCtasG ? room : kMaxCtasG;
-  // at least four stages a CTA, where there are as many: the parts have to be
+  // at least four stages a CTA, or a tile's where it has fewer: parts have to be
   // joined (us with 1, 2, 4, 8 stages: 16384 x 256, r = 256 20, 20, 13, 13; 16384 x
-  // 128, r = 16 18, 13, 10, 11; 256 x 512, r = 16 8.4, 6.6, 6.7, 10.4)
-  const int64_t runs = dora::ceil_div(units, kWin / kTok);
+  // 128, r = 16 18, 13, 10, 11; 256 x 512, r = 16 8.4, 6.6, 6.7, 10.4; 100 x 4096,
+  // r = 192, a stage a tile, 7.6 with one and 16.6 with four)
+  const int64_t runs = dora::ceil_div(units, p.stages < kWin / kTok ? p.stages : kWin / kTok);
   const int ctas = runs < most ? static_cast<int>(runs) : most;
   const int half = p.ncols / 2;
   if (half <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
