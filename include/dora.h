@@ -452,8 +452,8 @@ dora_status dora_compose_bwd_q8(dora_dtype act, const void *grad_out, const void
                                 void *workspace, size_t workspace_bytes, dora_stream_t stream);
 
 /* Bytes of workspace dora_lora_grad_q8 needs (host arithmetic; 0 for an invalid
- * shape): fp32 parts of the tiles of dA that several CTAs work on, at most 1024
- * parts of 128 features by up to 192 columns. */
+ * shape): fp32 parts of the tiles of dA that several CTAs work on, at most 512
+ * parts of 128 features by up to 192 columns (50 MB; 1024 up to 32 columns). */
 size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r);
 
 /*

@@ -69,7 +69,7 @@ constexpr unsigned kRawBytes = kTok * 128;       // 16 KB of x
 constexpr unsigned kBox = kTok * 128;            // 128 tokens x 64 columns of dxa
 constexpr int kMaxR = 1024;
 constexpr int kMaxN = 192;                       // columns of a tile: two windows and the M operands fill tensor memory
-constexpr int kMaxCtasG = 512;
+constexpr int kMaxSMs = 256;                     // workspace bound: any device up to this size
 // By the columns of a tile: CTAs per SM; stages of x and of dxa in shared
 // memory; M operands (64 columns) in tensor memory beside two windows of the
 // tile's columns.  x and the operands in even numbers, as two groups take
@@ -658,6 +658,19 @@ int tile_columns(int64_t r) {
   return static_cast<int>(dora::round_up(dora::ceil_div(r, tiles), 16));
 }
 
+// CTAs: at least four stages each, or a tile's where it has fewer, as parts
+// have to be joined (us with 1, 2, 4, 8 stages: 16384 x 256, r = 256 20, 20, 13,
+// 13; 16384 x 128, r = 16 18, 13, 10, 11; 256 x 512, r = 16 8.4, 6.6, 6.7, 10.4; 100 x
+// 4096, r = 192, a stage a tile, 6.9 with one and 16.6 with four)
+int64_t grad_ctas(int64_t T, int64_t in, int64_t r, int sms) {
+  const int cols = tile_columns(r);
+  const int64_t stages = dora::ceil_div(T, kTok);
+  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, cols) * stages;
+  const int64_t runs = dora::ceil_div(units, stages < kWin / kTok ? stages : kWin / kTok);
+  const int64_t room = static_cast<int64_t>(sms < kMaxSMs ? sms : kMaxSMs) * rings_of(cols).per_sm;
+  return runs < room ? runs : room;
+}
+
 template <int NC>
 dora_status launch_grad(const CUtensorMap &mX, const CUtensorMap &mD, GradParams p, int ctas, cudaStream_t cs) {
   constexpr Rings kR = rings_of(2 * NC);
@@ -695,10 +708,8 @@ dora_status launch_grad(const CUtensorMap &mX, const CUtensorMap &mD, GradParams
 extern "C" size_t dora_lora_grad_q8_workspace(int64_t T, int64_t in, int64_t r) {
   if (bad_size(T, 0) || bad_size(in, 0) || r < 1 || r > kMaxR) return 0;
   if (T == 0 || in == 0) return 256;
-  // two parts per CTA, for up to kMaxCtasG CTAs
-  const int64_t units = dora::ceil_div(in, kTcM) * dora::ceil_div(r, tile_columns(r)) * dora::ceil_div(T, kTok);
-  const int64_t ctas = units < kMaxCtasG ? units : kMaxCtasG;
-  return static_cast<size_t>(2 * ctas) * tile_columns(r) * kTcM * sizeof(float);
+  // two parts per CTA
+  return static_cast<size_t>(2 * grad_ctas(T, in, r, kMaxSMs)) * tile_columns(r) * kTcM * sizeof(float);
 }
 
 extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const void *xscale, int64_t T, int64_t in,
@@ -740,15 +751,7 @@ extern "C" dora_status dora_lora_grad_q8(const void *dxa, const void *xq, const 
   p.part = static_cast<float *>(workspace);
   CUtensorMap mX, mD;
   if (!map_q8(&mX, xq, T, in, kTok, kPromote) || !make_map(&mD, dxa, true, T, r, r, kTok, 128)) return DORA_ERR_CUDA;
-  const int64_t units = static_cast<int64_t>(p.mtiles) * p.ntiles * p.stages;
-  const int room = info.sms * rings_of(p.ncols).per_sm;
-  const int most = room < kMaxCtasG ? room : kMaxCtasG;
-  // at least four stages a CTA, or a tile's where it has fewer: parts have to be
-  // joined (us with 1, 2, 4, 8 stages: 16384 x 256, r = 256 20, 20, 13, 13; 16384 x
-  // 128, r = 16 18, 13, 10, 11; 256 x 512, r = 16 8.4, 6.6, 6.7, 10.4; 100 x 4096,
-  // r = 192, a stage a tile, 7.6 with one and 16.6 with four)
-  const int64_t runs = dora::ceil_div(units, p.stages < kWin / kTok ? p.stages : kWin / kTok);
-  const int ctas = runs < most ? static_cast<int>(runs) : most;
+  const int ctas = static_cast<int>(grad_ctas(T, in, r, info.sms));
   const int half = p.ncols / 2;
   if (half <= 8) return launch_grad<8>(mX, mD, p, ctas, cs);
   if (half <= 16) return launch_grad<16>(mX, mD, p, ctas, cs);
