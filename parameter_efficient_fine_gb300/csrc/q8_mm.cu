@@ -42,7 +42,7 @@
 // tile's MMAs run; a tile of more tokens has one accumulator.  It is bound by
 // the tensor cores: their pipe is active in 83% of the cycles (8192^3), and
 // over longer calls the power limit lowers the clock (15360 x 8192 x 8192: 650
-// us, 3.16 PFLOP/s; 8192 x 4096 x 4096: 89-100 us; 512 x 8192 x 8192: 27 us).
+// us, 3.16 PFLOP/s; 8192 x 4096 x 4096: 94 us; 512 x 8192 x 8192: 27 us).
 // dy W takes as long as x W^T.
 //   warp 0      TMA producer (each CTA its own boxes, on the even CTA's barrier)
 //   warp 1      tensor memory, MMA issue (even CTA).  A stage is two k blocks: waiting
@@ -374,10 +374,10 @@ constexpr int kPairTok = 256;                        // most tokens per tile, ha
 constexpr int kPairTwo = 224;                        // most tokens of a tile that has two accumulators
 constexpr int kPairFeat = 256;                       // features per tile
 constexpr int kPairKB = 2;                           // k blocks per stage
-constexpr int kPairStages = 3;
 constexpr unsigned kPairBox = kTcM * kKB;            // 16 KB: 128 features, one k block
-constexpr unsigned kPairXBox = kPairTok / 2 * kKB;   // room for 128 tokens, one k block (16 KB)
-constexpr unsigned kPairStage = kPairKB * (kPairBox + kPairXBox);
+// half of the tile's tokens, one k block
+__host__ __device__ constexpr unsigned pair_xbox(int ntok) { return static_cast<unsigned>(ntok / 2 * kKB); }
+__host__ __device__ constexpr unsigned pair_stage(int ntok) { return kPairKB * (kPairBox + pair_xbox(ntok)); }
 constexpr int kPairThreads = 14 * 32;
 constexpr int kPairSfCol = 2 * kPairTwo, kPairSfStride = 16;   // scale words: 4 columns of W's, 8 of the tokens'
 // feature tiles per tile-order group, for reuse in L2 (15360 x 8192 x 8192: 701,
@@ -418,12 +418,13 @@ struct Acc {
     }
   }
 };
-// a place in a ring of N
-template <int N> struct At {
-  int i = 0;
+// a place in a ring of n
+struct Ring {
+  int n, i = 0;
   uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int size) : n(size) {}
   __device__ __forceinline__ void next() {
-    if (++i == N) {
+    if (++i == n) {
       i = 0;
       phase ^= 1u;
     }
@@ -435,16 +436,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const MmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kPairStages * kPairStage);
+  const int S = p.stages;
+  const uint32_t xbox = pair_xbox(p.ntok), stage_bytes = pair_stage(p.ntok);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * stage_bytes);
   // barriers (a pair uses the even CTA's full, scales full and accumulator
   // empty): full, empty, scales full and empty, accumulator full and empty, end
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kPairStages, sff0 = empty0 + 8u * kPairStages,
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, sff0 = empty0 + 8u * S,
                  sfe0 = sff0 + 8u * kSfSlots, accf = sfe0 + 8u * kSfSlots, acce = accf + 16, fin = acce + 16;
-  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * kPairStages + 2 * kSfSlots + 5);
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * S + 2 * kSfSlots + 5);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8u * s, 1);
       mbar_init(empty0 + 8u * s, 1);
     }
@@ -487,7 +490,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     // ---------------------------------------------------------------- producer
     bool ok = !loads_withheld(p.guard);
     bool issued = false;
-    At<kPairStages> st;
+    Ring st(S);
     for (int t = pair; t < p.tiles && ok; t += npairs) {
       int ft, tt;
       place(t, &ft, &tt);
@@ -497,16 +500,16 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t fb = full0 + 8u * st.i, lb = mapa_shared(fb, 0);
-        const uint32_t at = smem_u32(smem) + st.i * kPairStage;
+        const uint32_t at = smem_u32(smem) + st.i * stage_bytes;
         if (elect_one()) {
           // the even CTA's barrier counts both CTAs' bytes
-          if (rank == 0) mbar_expect_tx(fb, 2 * kPairKB * (kPairBox + static_cast<uint32_t>(p.ntok / 2) * kKB));
+          if (rank == 0) mbar_expect_tx(fb, 2 * stage_bytes);
 #pragma unroll
           for (int k = 0; k < kPairKB; ++k) {
             const int kx = (s * kPairKB + k) * kKB;
             if (TRANS) tma_load_2d_pair(at + k * kPairBox, &mW, f0, kx, lb);
             else tma_load_2d_pair(at + k * kPairBox, &mW, kx, f0, lb);
-            tma_load_2d_pair(at + kPairKB * kPairBox + k * kPairXBox, &mX, kx, t0, lb);
+            tma_load_2d_pair(at + kPairKB * kPairBox + k * xbox, &mX, kx, t0, lb);
           }
         }
         __syncwarp();
@@ -526,8 +529,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       // ---------------------------------------------------------------- MMA issuer
       // (a commit arrives on the barrier of this CTA and on the peer's)
       bool ok = true;
-      At<kPairStages> st;
-      At<kSfSlots> sf;
+      Ring st(S), sf(kSfSlots);
       Acc acc(p.ntok);
       const uint32_t peer_off = mapa_shared(full0, peer) - full0;   // to the peer's copy of a barrier
       const uint32_t id0 = idesc_q8(kPairFeat, p.ntok, 0, TRANS);
@@ -541,7 +543,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = smem_u32(smem) + st.i * kPairStage;
+          const uint32_t at = smem_u32(smem) + st.i * stage_bytes;
           const uint64_t a = sdesc<32>(at), b = sdesc<32>(at + kPairKB * kPairBox);
           const uint32_t sfa = tmem + kPairSfCol + kPairSfStride * sf.i;
           const uint32_t id = second ? id0 | (2u << 4) | (2u << 29) : id0;
@@ -551,7 +553,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
             for (int k = 0; k < kPairKB; ++k)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mma_q8_pair(d, a + (kPairBox >> 4) * k + (TRANS ? 256u : 2u) * j, b + (kPairXBox >> 4) * k + 2u * j,
+                mma_q8_pair(d, a + (kPairBox >> 4) * k + (TRANS ? 256u : 2u) * j, b + (xbox >> 4) * k + 2u * j,
                             id | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29), sfa, sfa + 4,
                             s != 0 || k != 0 || j != 0 ? 1u : 0u);
             mma_commit_pair(empty0 + 8u * st.i);
@@ -581,7 +583,7 @@ q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool words = p.nsx % 4 == 0 && (reinterpret_cast<uintptr_t>(p.xscale) & 3) == 0;
     bool ok = true;
-    At<kSfSlots> sf;
+    Ring sf(kSfSlots);
     for (int t = pair; t < p.tiles && ok; t += npairs) {
       int ft, tt;
       place(t, &ft, &tt);
@@ -710,9 +712,14 @@ dora_status mm_init(int device, MmParams *p) {
   return tc_init(device, &p->guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
 }
 
-constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + 512;
+// as many stages as fit: the loads' latency over them is what a narrow tile's
+// stage takes (64 tokens: five of 40 KB; 256: three of 64 KB.  200 x 8192 x 8192,
+// in tiles of 112: 19.1 us with four, 21.4 with three)
+constexpr int pair_stages(int ntok) { return static_cast<int>((kSmemMax - 1024 - 512) / pair_stage(ntok)); }
+constexpr size_t pair_smem(int ntok) { return 1024 + pair_stages(ntok) * pair_stage(ntok) + 512; }
+static_assert(2 * pair_stages(64) + 2 * kSfSlots + 5 <= 56, "barriers and control words");
 
-void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int pairs, cudaStream_t cs) {
+void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ntok, int pairs, cudaStream_t cs) {
   *cfg = cudaLaunchConfig_t{};
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -720,7 +727,7 @@ void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int pairs, 
   attr[0].val.clusterDim.z = 1;
   cfg->gridDim = dim3(2 * static_cast<unsigned>(pairs));
   cfg->blockDim = dim3(kPairThreads);
-  cfg->dynamicSmemBytes = kPairSmem;
+  cfg->dynamicSmemBytes = pair_smem(ntok);
   cfg->stream = cs;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -739,7 +746,7 @@ int resident_pairs(int device, int sms) {
   if (known[device] == 0) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    pair_config(&cfg, attr, sms / 2, nullptr);
+    pair_config(&cfg, attr, kPairTok, sms / 2, nullptr);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, q8_pair_kernel<false>, &cfg) != cudaSuccess) {
       cudaGetLastError();
@@ -758,7 +765,7 @@ dora_status launch_pairs(const void *q, const void *wq, int64_t out, int64_t in,
     return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  pair_config(&cfg, attr, p.tiles < pairs ? p.tiles : pairs, cs);
+  pair_config(&cfg, attr, p.ntok, p.tiles < pairs ? p.tiles : pairs, cs);
   if (cudaLaunchKernelEx(&cfg, q8_pair_kernel<TRANS>, mW, mX, p) != cudaSuccess) {
     cudaGetLastError();
     return DORA_ERR_CUDA;
@@ -796,19 +803,21 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
     const int pairs = resident_pairs(device, info.sms);
     if (pairs == 0) return DORA_ERR_CUDA;
     const int64_t ftiles = dora::ceil_div(p.nfeat, kPairFeat);
-    // tokens per tile: the least time over the waves of tiles.  A stage of two
-    // k blocks was measured to take a time in proportion to tokens + 125 (at
-    // 15360 x 8192 x 8192, us a stage: 0.40, 0.48, 0.58, 0.70 with 64, 128, 176
-    // and 224 tokens), and 10 more with one accumulator
+    // tokens per tile: the least time over the waves of tiles, a stage of two k
+    // blocks taken as n + 100, and 20 more with one accumulator (15360 x 8192 x 8192,
+    // us a stage: 0.37, 0.45, 0.54, 0.59, 0.67, 0.79 with 64, 128, 176, 192, 224,
+    // 256 tokens; with 125 and 10, which prefer wider tiles: 5000 x 14336 x 4096
+    // 210 us against 192, 8192 x 4096 x 4096 99 against 94, others the same)
     int64_t best = 0;
     for (int n = 64; n <= kPairTok; n += 16) {
       const int64_t waves = dora::ceil_div(ftiles * dora::ceil_div(T, n), pairs);
-      const int64_t cost = waves * (n + 125 + (n > kPairTwo ? 10 : 0));
+      const int64_t cost = waves * (n + 100 + (n > kPairTwo ? 20 : 0));
       if (best == 0 || cost < best) {
         best = cost;
         p.ntok = n;
       }
     }
+    p.stages = pair_stages(p.ntok);
     p.ntiles = static_cast<int>(dora::ceil_div(T, p.ntok));
     const int64_t tiles = ftiles * p.ntiles;
     if (tiles > kMaxDim) return DORA_ERR_SHAPE;
