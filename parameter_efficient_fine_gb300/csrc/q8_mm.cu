@@ -796,9 +796,10 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   p.y = static_cast<__nv_bfloat16 *>(y);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   // up to 128 tokens W is read by all SMs at once, its k range split where there
-  // are few tiles; the pairs, one tile of 256 features each, would leave most
-  // of them idle (us split / on pairs: 128 x 8192 x 8192 18.6 / 20.4, 70 x 4096 x
-  // 14336 16.0 / 27.9, 64 x 8192 x 8192 15.8 / 20.2, 128 x 14336 x 4096 17.2 / 15.8)
+  // are few tiles; the pairs, one tile of 256 features each, leave many of them
+  // idle where a weight has few features (us split / on pairs: 70 x 4096 x 14336
+  // 15.9 / 24.6, 128 x 4096 x 14336 18.4 / 24.8, 70 x 8192 x 8192 16.1 / 17.1, 128 x 8192 x
+  // 8192 18.6 / 17.3, 128 x 14336 x 4096 17.2 / 15.0)
   if (T > kSplitTok) {
     const int pairs = resident_pairs(device, info.sms);
     if (pairs == 0) return DORA_ERR_CUDA;
