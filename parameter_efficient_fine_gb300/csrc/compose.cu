@@ -181,8 +181,8 @@ compose_bwd_kernel(const Act *__restrict__ dy, const Act *__restrict__ base,
 template <typename Act, int VEC>
 dora_status launch_fwd(const void *base, const void *lora, const float *g, float s, int64_t T,
                        int64_t out, void *y, cudaStream_t stream, int device, int sms) {
-  auto kern = compose_fwd_kernel<Act, VEC>;
-  const int bps = blocks_per_sm(kern, device);
+  constexpr auto kern = &compose_fwd_kernel<Act, VEC>;
+  const int bps = resident_blocks<kern>(device);
   Grid gr = plan_grid(T, out / VEC, (int64_t)sms * bps);
   kern<<<dim3((unsigned)gr.gx, (unsigned)gr.gy), dim3(kBX, kBY), 0, stream>>>(
       static_cast<const Act *>(base), static_cast<const Act *>(lora), g, s, T, out, static_cast<Act *>(y));
@@ -195,8 +195,8 @@ dora_status launch_bwd(const void *dy, const void *base, const void *lora, const
                        const float *norm, float s, int64_t T, int64_t out, void *d_base, void *d_lora,
                        float *d_mag, float *part, size_t part_bytes, cudaStream_t stream, int device,
                        int sms) {
-  auto kern = compose_bwd_kernel<Act, VEC>;
-  const int bps = blocks_per_sm(kern, device);
+  constexpr auto kern = &compose_bwd_kernel<Act, VEC>;
+  const int bps = resident_blocks<kern>(device);
   int64_t rows = 0;
   if (T > 0) {
     Grid gr = plan_grid(T, out / VEC, (int64_t)sms * bps);
@@ -325,8 +325,8 @@ template <typename Act, int VEC>
 dora_status launch_bwd_noalloc(const void *dy, const void *base, const void *lora, const float *g,
                                const float *norm, float s, int64_t T, int64_t out, void *d_base, void *d_lora,
                                float *d_mag, float *part, cudaStream_t stream, int device, int sms) {
-  auto kern = compose_bwd_kernel<Act, VEC>;
-  const int bps = blocks_per_sm(kern, device);
+  constexpr auto kern = &compose_bwd_kernel<Act, VEC>;
+  const int bps = resident_blocks<kern>(device);
   int64_t rows = 0;
   if (T > 0) {
     const Grid gr = plan_grid(T, out / VEC, (int64_t)sms * bps);

@@ -402,21 +402,6 @@ q8_compose_bwd_kernel(const Act *__restrict__ dy, const uint8_t *__restrict__ q,
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// resident blocks per SM of one kernel (each kernel has its own cache)
-template <auto *KERNEL>
-int resident_blocks(int device) {
-  static std::mutex mu;
-  static int cache[64] = {};
-  if (device < 0 || device >= 64) return 1;
-  std::lock_guard<std::mutex> lock(mu);
-  if (cache[device] == 0) {
-    int b = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, KERNEL, kThreads, 0) != cudaSuccess || b <= 0) b = 1;
-    cache[device] = b;
-  }
-  return cache[device];
-}
-
 // 16-byte pieces of the rows of `act` and the matching pieces of their 8-bit form
 template <typename Act>
 bool q8_vector_ok(int64_t cols, std::initializer_list<const void *> ptrs, const void *q) {

@@ -111,15 +111,18 @@ dmag_reduce_kernel(const float *__restrict__ part, int64_t rows, int64_t out,
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <typename K>
-int blocks_per_sm(K kernel, int device) {
+// resident blocks per SM of one kernel.  The kernel is the template's argument,
+// not its type: the forms of a kernel for whole pieces and for ragged rows
+// have one type and each its own number
+template <auto *KERNEL>
+int resident_blocks(int device) {
   static std::mutex mu;
   static int cache[64] = {};
-  std::lock_guard<std::mutex> lock(mu);
   if (device < 0 || device >= 64) return 1;
+  std::lock_guard<std::mutex> lock(mu);
   if (cache[device] == 0) {
     int b = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, kThreads, 0) != cudaSuccess || b <= 0) b = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, KERNEL, kThreads, 0) != cudaSuccess || b <= 0) b = 1;
     cache[device] = b;
   }
   return cache[device];
