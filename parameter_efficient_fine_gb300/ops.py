@@ -379,10 +379,31 @@ def _lora_grad_q8_fake(dxa, xq, xscale):
     return dxa.new_empty(dxa.shape[1], xq.shape[1], dtype=torch.float32)
 
 
+def _linear_q8_check(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, g: Tensor) -> None:
+    """What the layer's forward takes; the same eagerly and while it is traced."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"dora::linear_q8: x is bfloat16, got {x.dtype}")
+    if wq.element_size() != 1 or wscale.element_size() != 1:
+        raise TypeError(f"dora::linear_q8: the 8-bit weight is bytes, got {wq.dtype} and {wscale.dtype}")
+    if x.dim() != 2 or wq.dim() != 2 or A.dim() != 2:
+        raise ValueError(f"dora::linear_q8: x [T, in], wq [out, in] and A [r, in] are matrices, got {tuple(x.shape)}, "
+                         f"{tuple(wq.shape)}, {tuple(A.shape)}")
+    (out, inp), r = wq.shape, A.shape[0]
+    if out % 16 or inp % 16:
+        raise ValueError(f"dora::linear_q8: in and out are multiples of 16, got {inp} and {out}")
+    for name, t, want in (("x", x, (x.shape[0], inp)), ("wscale", wscale, _scale_shape(out, inp, 128)),
+                          ("A", A, (r, inp)), ("B", B, (out, r)), ("g", g, (out,))):
+        if t.shape != want:
+            raise ValueError(f"dora::linear_q8: {name} is {want} for a weight [{out}, {inp}] and rank {r}, got {tuple(t.shape)}")
+    if g.dtype != torch.float32:
+        raise ValueError(f"dora::linear_q8: g is float32, got {g.dtype}")
+
+
 @torch.library.custom_op("dora::linear_q8", mutates_args=(), device_types="cuda")
 def linear_q8(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Tensor, g: Tensor, norm: Tensor,
               s: float) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
     """The layer's output y and what its backward needs: (y, xq, xscale, vq, vscale, xa)."""
+    _linear_q8_check(x, wq, wscale, A, B, g)
     xq, xscale = q8_store(x, 1)
     xa = x @ A.to(x.dtype).t()
     y, vq, vscale = compose_q8(matmul_q8(xq, xscale, wq, wscale), xa @ B.to(x.dtype).t(), m, g, norm, s)
@@ -391,6 +412,7 @@ def linear_q8(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Te
 
 @linear_q8.register_fake
 def _linear_q8_fake(x, wq, wscale, A, B, m, g, norm, s):
+    _linear_q8_check(x, wq, wscale, A, B, g)
     T, inp = x.shape
     out = wq.shape[0]
     u8 = torch.uint8
@@ -399,8 +421,16 @@ def _linear_q8_fake(x, wq, wscale, A, B, m, g, norm, s):
 
 
 def _linear_q8_setup(ctx, inputs, output):
-    _, wq, wscale, A, B, _, g, norm, s = inputs
+    _, wq, wscale, A, B, m, g, norm, s = inputs
     _, xq, xscale, vq, vscale, xa = output
+    # what the backward alone needs is refused by the call that leads to it
+    r, (out,) = A.shape[0], g.shape
+    if ctx.needs_input_grad[3] and (r % 8 or not 1 <= r <= 1024):
+        raise ValueError(f"dora::linear_q8: a gradient of A takes a rank of 8, 16, ... 1024, got {r}")
+    if ctx.needs_input_grad[5] and m.shape != (out,):
+        raise ValueError(f"dora::linear_q8: m is ({out},), got {tuple(m.shape)}")
+    if norm.shape != (out,) or norm.dtype != torch.float32:
+        raise ValueError(f"dora::linear_q8: norm is ({out},) of float32, got {tuple(norm.shape)} of {norm.dtype}")
     ctx.save_for_backward(xq, xscale, vq, vscale, xa, wq, wscale, A, B, g, norm)
     ctx.s = s
     ctx.mark_non_differentiable(xq, xscale, vq, vscale, xa)
@@ -431,5 +461,6 @@ def dora_linear_q8(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, 
 
     norm and g = m / norm come from one of the norm ops on the values of the
     8-bit weight (q8_load is exact in bfloat16) and carry no gradient; x, A, B
-    and m do.  in and out are multiples of 16, the rank a multiple of 8."""
+    and m do.  in and out are multiples of 16; where A takes a gradient, the rank
+    is a multiple of 8 up to 1024.  What does not fit is refused by this call."""
     return linear_q8(x, wq, wscale, A, B, m, g, norm, s)[0]
