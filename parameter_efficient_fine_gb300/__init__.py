@@ -288,8 +288,9 @@ def _q8(name: str, rows: int, cols: int, block_rows: int, q, scale) -> None:
     """The shapes of an 8-bit form; the C ABI sees only the matrix's."""
     if q.element_size() != 1 or scale.element_size() != 1:
         raise TypeError(f"{name}: the 8-bit form is bytes, got {q.dtype} and {scale.dtype}")
-    want = (-(-rows // block_rows), -(-cols // 128)) if block_rows == 1 or block_rows == 128 else None
-    if q.shape != (rows, cols) or (want and scale.shape != want):
+    if block_rows != 1 and block_rows != 128:      # the C int would take it modulo 2^32
+        raise ValueError(f"{name}: 1 or 128 rows a scale, got {block_rows}")
+    if q.shape != (rows, cols) or scale.shape != (-(-rows // block_rows), -(-cols // 128)):
         raise ValueError(f"{name}: 8-bit form of [{rows}, {cols}] with {block_rows} rows a scale: "
                          f"got q {tuple(q.shape)}, scale {tuple(scale.shape)}")
 

@@ -247,6 +247,8 @@ def dora_module(base: Tensor, lora: Tensor, W0: Tensor, A: Tensor, B: Tensor, m:
 # 8 bits: E4M3 with a power-of-two scale per 128 columns (include/dora.h)
 # ---------------------------------------------------------------------------
 def _scale_shape(rows: int, cols: int, block_rows: int) -> tuple[int, int]:
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError(f"dora: an 8-bit form has 1 or 128 rows a scale, got {block_rows}")
     return -(-rows // block_rows), -(-cols // 128)
 
 
