@@ -350,7 +350,7 @@ def dora_compose_bwd_q8(grad_out, q, scale, g, norm, s: float, d_base, d_lora, d
     _same("dora_compose_bwd_q8", grad_out.shape, grad_out.dtype, d_base, d_lora)
     _same("dora_compose_bwd_q8", (out,), torch.float32, g, norm, d_mag)
     _q8("dora_compose_bwd_q8", T, out, 1, q, scale)
-    _dense("dora_compose_bwd_q8", grad_out, q, scale, g, norm, d_base, d_lora, d_mag)
+    _dense("dora_compose_bwd_q8", grad_out, q, scale, g, norm, d_base, d_lora, d_mag, workspace)
     st = load_library().dora_compose_bwd_q8(
         _act(grad_out), _ptr(grad_out), _ptr(q), _ptr(scale), _ptr(g), _ptr(norm), float(s), T, out,
         _ptr(d_base), _ptr(d_lora), _ptr(d_mag), _ptr(workspace),
@@ -370,7 +370,7 @@ def dora_lora_grad_q8(dxa, xq, xscale, dA, workspace, stream=None) -> None:
     _same("dora_lora_grad_q8", (T, r), torch.bfloat16, dxa)
     _same("dora_lora_grad_q8", (r, inp), torch.float32, dA)
     _q8("dora_lora_grad_q8", T, inp, 1, xq, xscale)
-    _dense("dora_lora_grad_q8", dxa, xq, xscale, dA)
+    _dense("dora_lora_grad_q8", dxa, xq, xscale, dA, workspace)
     st = load_library().dora_lora_grad_q8(_ptr(dxa), _ptr(xq), _ptr(xscale), T, inp, r, _ptr(dA), _ptr(workspace),
                                           workspace.numel() * workspace.element_size(), _stream(stream))
     _check("dora_lora_grad_q8", st)
