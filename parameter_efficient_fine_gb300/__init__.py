@@ -135,24 +135,34 @@ def _ptr(x) -> int:
     raise ValueError(f"libdora takes CUDA tensors (device memory); got one on {getattr(x, 'device', type(x))}")
 
 
-def _stream(stream) -> int:
+_raw_stream = None   # torch's lookup of a device's current stream, as a raw handle
+_ACTS = {}           # torch dtype -> dora_dtype
+
+
+def _stream(stream, device=None) -> int:
+    global _raw_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    # the raw handle where torch gives it: building a Stream object takes 3 us a call
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        import torch
+        # the raw handle where torch gives it: building a Stream object takes 3 us a call
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    return _raw_stream(device)
 
 
 def _act(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return DORA_F32
-    if t.dtype == torch.bfloat16:
-        return DORA_BF16
-    raise TypeError(f"activation dtype {t.dtype} not supported (float32 or bfloat16)")
+    act = _ACTS.get(t.dtype)
+    if act is None:
+        import torch
+        _ACTS.update({torch.float32: DORA_F32, torch.bfloat16: DORA_BF16})
+        act = _ACTS.get(t.dtype)
+    if act is None:
+        raise TypeError(f"activation dtype {t.dtype} not supported (float32 or bfloat16)")
+    return act
 
 
 def _check(name: str, st: int) -> None:
@@ -295,10 +305,22 @@ def _q8(name: str, rows: int, cols: int, block_rows: int, q, scale) -> None:
                          f"got q {tuple(q.shape)}, scale {tuple(scale.shape)}")
 
 
-def _dense(name: str, *ts) -> None:
+def _addresses(name: str, stream, *ts) -> list[int]:
+    """Device addresses of a call's tensors, which are dense and in the memory of
+    the current device, as the kernels run there; then the stream's handle."""
+    here = None
     for t in ts:
         if not t.is_contiguous():
             raise ValueError(f"{name}: tensors must be contiguous (row-major)")
+        if t.get_device() != here:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError(f"libdora takes CUDA tensors (device memory); got one on {t.device}")
+            import torch
+            here = torch.cuda.current_device()
+            if d != here:
+                raise ValueError(f"{name}: a tensor on cuda:{d}, but the current device is cuda:{here}")
+    return [t.data_ptr() for t in ts] + [_stream(stream, here)]
 
 
 def _same(name: str, shape, dtype, *ts) -> None:
@@ -312,8 +334,9 @@ def dora_q8_store(x, block_rows: int, q, scale, stream=None) -> None:
     128) x 128 elements (see include/dora.h)."""
     rows, cols = x.shape
     _q8("dora_q8_store", rows, cols, block_rows, q, scale)
-    _dense("dora_q8_store", x, q, scale)
-    st = load_library().dora_q8_store(_act(x), _ptr(x), rows, cols, block_rows, _ptr(q), _ptr(scale), _stream(stream))
+    act = _act(x)
+    px, pq, psc, cs = _addresses("dora_q8_store", stream, x, q, scale)
+    st = load_library().dora_q8_store(act, px, rows, cols, block_rows, pq, psc, cs)
     _check("dora_q8_store", st)
 
 
@@ -321,8 +344,9 @@ def dora_q8_load(q, scale, block_rows: int, x, stream=None) -> None:
     """The values of an 8-bit form into x (see include/dora.h)."""
     rows, cols = x.shape
     _q8("dora_q8_load", rows, cols, block_rows, q, scale)
-    _dense("dora_q8_load", x, q, scale)
-    st = load_library().dora_q8_load(_act(x), _ptr(q), _ptr(scale), rows, cols, block_rows, _ptr(x), _stream(stream))
+    act = _act(x)
+    px, pq, psc, cs = _addresses("dora_q8_load", stream, x, q, scale)
+    st = load_library().dora_q8_load(act, pq, psc, rows, cols, block_rows, px, cs)
     _check("dora_q8_load", st)
 
 
@@ -333,9 +357,9 @@ def dora_compose_fwd_q8(base, lora, g, s: float, y, q, scale, stream=None) -> No
     _same("dora_compose_fwd_q8", base.shape, base.dtype, lora, y)
     _same("dora_compose_fwd_q8", (out,), torch.float32, g)
     _q8("dora_compose_fwd_q8", T, out, 1, q, scale)
-    _dense("dora_compose_fwd_q8", base, lora, g, y, q, scale)
-    st = load_library().dora_compose_fwd_q8(_act(base), _ptr(base), _ptr(lora), _ptr(g), float(s), T, out, _ptr(y),
-                                            _ptr(q), _ptr(scale), _stream(stream))
+    act = _act(base)
+    pb, pl, pg, py, pq, psc, cs = _addresses("dora_compose_fwd_q8", stream, base, lora, g, y, q, scale)
+    st = load_library().dora_compose_fwd_q8(act, pb, pl, pg, float(s), T, out, py, pq, psc, cs)
     _check("dora_compose_fwd_q8", st)
 
 
@@ -350,11 +374,11 @@ def dora_compose_bwd_q8(grad_out, q, scale, g, norm, s: float, d_base, d_lora, d
     _same("dora_compose_bwd_q8", grad_out.shape, grad_out.dtype, d_base, d_lora)
     _same("dora_compose_bwd_q8", (out,), torch.float32, g, norm, d_mag)
     _q8("dora_compose_bwd_q8", T, out, 1, q, scale)
-    _dense("dora_compose_bwd_q8", grad_out, q, scale, g, norm, d_base, d_lora, d_mag, workspace)
-    st = load_library().dora_compose_bwd_q8(
-        _act(grad_out), _ptr(grad_out), _ptr(q), _ptr(scale), _ptr(g), _ptr(norm), float(s), T, out,
-        _ptr(d_base), _ptr(d_lora), _ptr(d_mag), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+    act = _act(grad_out)
+    pws, pd, pq, psc, pg, pn, pdb, pdl, pdm, cs = _addresses("dora_compose_bwd_q8", stream, workspace, grad_out, q, scale,
+                                                             g, norm, d_base, d_lora, d_mag)
+    st = load_library().dora_compose_bwd_q8(act, pd, pq, psc, pg, pn, float(s), T, out, pdb, pdl, pdm, pws,
+                                            workspace.numel() * workspace.element_size(), cs)
     _check("dora_compose_bwd_q8", st)
 
 
@@ -370,9 +394,9 @@ def dora_lora_grad_q8(dxa, xq, xscale, dA, workspace, stream=None) -> None:
     _same("dora_lora_grad_q8", (T, r), torch.bfloat16, dxa)
     _same("dora_lora_grad_q8", (r, inp), torch.float32, dA)
     _q8("dora_lora_grad_q8", T, inp, 1, xq, xscale)
-    _dense("dora_lora_grad_q8", dxa, xq, xscale, dA, workspace)
-    st = load_library().dora_lora_grad_q8(_ptr(dxa), _ptr(xq), _ptr(xscale), T, inp, r, _ptr(dA), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _stream(stream))
+    pws, pd, pq, psc, pa, cs = _addresses("dora_lora_grad_q8", stream, workspace, dxa, xq, xscale, dA)
+    st = load_library().dora_lora_grad_q8(pd, pq, psc, T, inp, r, pa, pws,
+                                          workspace.numel() * workspace.element_size(), cs)
     _check("dora_lora_grad_q8", st)
 
 
@@ -391,11 +415,10 @@ def _matmul_q8(name: str, q, scale, wq, wscale, y, workspace, stream, out_side: 
     _q8(name, T, inp if out_side else out, 1, q, scale)
     _q8(name, out, inp, 128, wq, wscale)
     _same(name, (T, out if out_side else inp), torch.bfloat16, y)
-    _dense(name, q, scale, wq, wscale, y)
-    st = getattr(load_library(), name)(_ptr(q), _ptr(scale), _ptr(wq), _ptr(wscale), T, out, inp, _ptr(y),
-                                       _ptr(workspace),
+    pq, psc, pw, pwsc, py, cs = _addresses(name, stream, q, scale, wq, wscale, y)
+    st = getattr(load_library(), name)(pq, psc, pw, pwsc, T, out, inp, py, _ptr(workspace),
                                        0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                       _stream(stream))
+                                       cs)
     _check(name, st)
 
 
