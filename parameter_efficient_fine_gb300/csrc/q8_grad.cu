@@ -427,7 +427,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
     const uint32_t quad = static_cast<uint32_t>(warp & 3);
     const int grp = wk >> 2;                             // which stages, and which half of the columns
     const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(grp * NC);
-    constexpr int C = NC % 32 == 0 ? 32 : NC % 16 == 0 ? 16 : NC % 8 == 0 ? 8 : 4;
+    constexpr int C = NC % 32 == 0 ? 32 : NC % 16 == 0 ? 16 : 8;
     float sum[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) sum[j] = 0.0f;

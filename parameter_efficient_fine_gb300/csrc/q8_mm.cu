@@ -72,7 +72,6 @@ constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB
 constexpr int kSfSlots = 4;                 // scale words in flight, in groups of four k blocks
 constexpr int kSplitThreads = 192;
 constexpr int kSplitTok = 128;              // most tokens of q8_split_kernel (one tile of them)
-constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;              // the portable limit
 
 struct MmParams {
@@ -207,6 +206,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
   const uint32_t rank = cluster_ctarank();
   const int mt = static_cast<int>(blockIdx.x / csize);
+  // at least one k block: a cluster has no more CTAs than there are
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / csize);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / csize);
   bool ok = true;
@@ -293,7 +293,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
     const uint32_t quad = static_cast<uint32_t>(warp & 3);
     const uint32_t lane_addr = tmem + ((quad * 32u) << 16);
     const bool words = p.nsx % 4 == 0 && (reinterpret_cast<uintptr_t>(p.xscale) & 3) == 0;
-    const int g0 = kb0 / 4, g1 = kb1 > kb0 ? (kb1 - 1) / 4 + 1 : g0;
+    const int g0 = kb0 / 4, g1 = (kb1 - 1) / 4 + 1;
     for (int g = g0; g < g1; ++g) {
       uint32_t w[8];
       w[0] = w[1] = w[2] = w[3] = weight_word<TRANS>(p, mt, g);
@@ -320,7 +320,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
     // into shared memory as [token][feature]: the stages are free once the
     // last MMA is done
     const bool got = guard_wait(accf, 0, ctl, p.guard, 25);
-    ok = __all_sync(0xffffffffu, got) && ok && kb1 > kb0;
+    ok = __all_sync(0xffffffffu, got) && ok;
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
     const int f = static_cast<int>(quad) * 32 + lane;
@@ -677,9 +677,10 @@ template <int NT, bool TRANS>
 dora_status launch_split(const CUtensorMap &mW, const CUtensorMap &mX, MmParams p, int cluster, cudaStream_t cs) {
   constexpr auto kern = &q8_split_kernel<NT, TRANS>;
   // two CTAs an SM: half of the shared memory each
-  p.stages = static_cast<int>((kSmemMax / 2 - 2048) / (kWBytes + NT * kKB));
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const size_t smem = split_smem(NT, p.stages);
+  constexpr int stages = static_cast<int>((kSmemMax / 2 - 2048) / (kWBytes + NT * kKB));
+  static_assert(2 * stages + 2 * kSfSlots + 1 <= 56, "barriers and control words");
+  p.stages = stages;
+  const size_t smem = split_smem(NT, stages);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

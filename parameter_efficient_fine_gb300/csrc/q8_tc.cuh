@@ -81,18 +81,6 @@ template <> __device__ __forceinline__ void tmem_ld<8>(uint32_t taddr, float (&v
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-template <> __device__ __forceinline__ void tmem_ld<4>(uint32_t taddr, float (&v)[4]) {
-  uint32_t r[4];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // bytes [rows, cols] (cols a multiple of 16) with a [box_rows x 128] box, 128-byte
 // swizzle; `promotion` is how much a fetch from memory brings into L2
 inline bool map_q8(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows,
