@@ -17,10 +17,11 @@
 // from the same registers.  At 15360 x 8192, in us and as a fraction of the
 // 6800 GB/s of a plain copy (bytes that have to move / time):
 //            store       load        forward     backward (with the d_mag sum)
-//   bf16    64  0.87    66  0.85    135  0.96    140  0.92
-//   f32    100  0.92   109  0.85    243  0.99    269  0.89
-// A call on a few rows costs its launch, about 6 us (the backward's two, 12).  Rows that are ragged or not 16-byte aligned take
-// the same kernels with four columns a thread, 32 apart (Piece).
+//   bf16    64  0.87    66  0.85    136  0.95    142  0.91
+//   f32    101  0.92   109  0.85    248  0.97    269  0.90
+// A call on a few rows costs its launch, 5 to 7 us (the backward's two, 10).
+// Rows that are ragged or not 16-byte aligned take the same kernels with four
+// columns a thread, 32 apart (Piece).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -20,7 +20,7 @@
 // Work: a tile of the result is 128 features x N columns of r; its stages of
 // 128 tokens are units, and each CTA (one or two an SM) takes an equal run of
 // units over all tiles, in windows of up to four.  (Runs of whole windows left up
-// to a sixth of the CTAs idle at the end: r = 16 36.4 us, now 34.4.)  A CTA that
+// to a sixth of the CTAs idle at the end: 6% more time at r = 16.)  A CTA that
 // has a whole tile writes dA; otherwise it writes its part to the workspace and
 // grad_join_kernel adds the parts of a tile in order (bitwise reproducible).
 //   warp 0      x by TMA: 128 tokens x 128 features a stage (16 KB), and the
@@ -55,9 +55,11 @@ namespace {
 
 constexpr int kTok = 128;                        // tokens per stage
 // Tokens per window.  Longer ones are read out and joined less often, but the
-// sum's error grows with them: 15360 x 8192, r = 384: 102, 96, 92 us and 1.4,
-// 1.6, 2.9e-7 of dA's norm with 256, 512, 1024; 16384 x 256, r = 256: 21 and 14
-// us with 256 and 512
+// sum's error grows with them (parts of dA's norm; an fp32 product's is 1.8e-7 at
+// the first size, 1.1e-7 at the last).
+// 256, 512, 1024, in us and 1e-7: 15360 x 8192, r = 384 98 1.4, 90 1.6, 88 2.9;
+// r = 16 30.4 1.1, 29.2 1.5, 29.1 2.8; 8192 x 4096, r = 64 17.2 1.0, 16.6 1.4, 16.4
+// 2.5
 constexpr int kWin = 512;
 constexpr int kWorkers = 8;                      // conversion warps, in two groups that take alternate stages
 constexpr int kThreadsG = 96 + 32 * kWorkers;
@@ -601,9 +603,9 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__
 // columns, the parts of AT CTAs loaded at a time.  Many at a time where a tile
 // has more than four parts, whose loads are all that it waits for, else two, as
 // a load that is not needed costs its instructions (us with 2 and 16 at a time,
-// the gradient's kernel included: 8192 x 4096, r = 64 20.0, 18.3; 16384 x 1024,
-// r = 128 18.9, 13.6; 15360 x 8192, r = 384 94.8, 104.5; 2048 x 2048, r = 384 12.6,
-// 13.8)
+// the gradient's kernel included: 8192 x 4096, r = 64 18.3, 16.6; 16384 x 1024,
+// r = 128 18.8, 13.5; 15360 x 8192, r = 384 89.4, 98.6; 2048 x 2048, r = 384 12.1,
+// 13.3)
 constexpr int kJoin = 8;
 template <int AT> __global__ void __launch_bounds__(256) grad_join_kernel(const GradParams p, int ctas) {
   __shared__ int owner[2];
@@ -659,9 +661,9 @@ int tile_columns(int64_t r) {
 }
 
 // CTAs: at least four stages each, or a tile's where it has fewer, as parts
-// have to be joined (us with 1, 2, 4, 8 stages: 16384 x 256, r = 256 20, 20, 13,
-// 13; 16384 x 128, r = 16 18, 13, 10, 11; 256 x 512, r = 16 8.4, 6.6, 6.7, 10.4; 100 x
-// 4096, r = 192, a stage a tile, 6.9 with one and 16.6 with four)
+// have to be joined (us with 1, 2, 4, 8 stages: 16384 x 256, r = 256 11.9, 12.0,
+// 10.9, 11.2; 16384 x 128, r = 16 10.4, 8.5, 8.5, 9.0; 256 x 512, r = 16 8.5, 6.8, 6.8,
+// 6.8; 100 x 4096, r = 192, a stage a tile, 6.8 with one and 16.7 with four)
 int64_t grad_ctas(int64_t T, int64_t in, int64_t r, int sms) {
   const int cols = tile_columns(r);
   const int64_t stages = dora::ceil_div(T, kTok);

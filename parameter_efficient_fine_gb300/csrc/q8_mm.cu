@@ -24,11 +24,11 @@
 // a ring of TMA stages, and the parts meet in distributed shared memory,
 // summed in rank order (bitwise reproducible, no workspace).  It has to read W
 // once and is bound by that and by what lies around it: the launch, the first
-// loads' latency and the joining of the parts are 3 us of the 13.0 that 1 x
-// 8192 x 8192 takes (9.9 to read W at the copy bandwidth; 5150 GB/s), so its
+// loads' latency and the joining of the parts are 3 us of the 13.2 that 1 x
+// 8192 x 8192 takes (9.9 to read W at the copy bandwidth; 5100 GB/s), so its
 // set-up and the first boxes of W into L2 overlap the end of the launch
-// before.  37 x 14336 x 4096: 13.5 us (8.8); 128 x 8192 x 8192: 18.3 (10.3),
-// where the token box is as large as W's.
+// before.  37 x 14336 x 4096: 13.7 us (8.8); 128 x 8192 x 8192: 18.6 (10.3),
+// where the token box is as large as W's.  dy W: 13.6, 14.2, 18.7.
 //   warp 0     TMA producer: per k block the W box (16 KB) and the token box
 //   warp 1     tensor memory, MMA issue (four 32-wide steps per k block)
 //   warps 2-5  scale words into tensor memory, four k blocks at a time, each
@@ -41,9 +41,11 @@
 // scale words fill tensor memory and a tile's result leaves while the next
 // tile's MMAs run; a tile of more tokens has one accumulator.  It is bound by
 // the tensor cores: their pipe is active in 83% of the cycles (8192^3), and
-// over longer calls the power limit lowers the clock (15360 x 8192 x 8192: 650
-// us, 3.16 PFLOP/s; 8192 x 4096 x 4096: 94 us; 512 x 8192 x 8192: 27 us).
-// dy W takes as long as x W^T.
+// over longer calls the power limit lowers the clock (15360 x 8192 x 8192: 605
+// to 660 us, 3.1 to 3.4 PFLOP/s; 8192 x 4096 x 4096: 94 to 98 us; 512 x 8192 x 8192:
+// 27 us; dy W 655 to 695 and 28 us).  A pair walks all of k alone, so a call of few
+// tiles takes as long as one tile does: 129 x 256 x 14336 24 us, 129 x 4096 x 14336 29,
+// 200 x 8192 x 8192 19 (10.6 to read and write).
 //   warp 0      TMA producer (each CTA its own boxes, on the even CTA's barrier)
 //   warp 1      tensor memory, MMA issue (even CTA).  A stage is two k blocks: waiting
 //               for one and issuing its MMAs takes this warp about 600 cycles,
@@ -799,8 +801,11 @@ dora_status run_matmul(const void *q, const void *scale, const void *wq, const v
   // up to 128 tokens W is read by all SMs at once, its k range split where there
   // are few tiles; the pairs, one tile of 256 features each, leave many of them
   // idle where a weight has few features (us split / on pairs: 70 x 4096 x 14336
-  // 15.9 / 24.6, 128 x 4096 x 14336 18.4 / 24.8, 70 x 8192 x 8192 16.1 / 17.1, 128 x 8192 x
-  // 8192 18.6 / 17.3, 128 x 14336 x 4096 17.2 / 15.0)
+  // 16.0 / 24.6, 128 x 4096 x 14336 18.5 / 24.7, 70 x 8192 x 8192 16.2 / 17.2).  128 is
+  // the most that the split kernel takes, not where the two are even: that lies
+  // lower for a wide weight (128 x 8192 x 8192 18.6 / 17.5, 70 x 14336 x 4096 15.1 / 14.2,
+  // 128 x 14336 x 4096 17.2 / 14.8) and higher for a narrow one (128 x 256 x 14336 10.0 on
+  // the split kernel, 129 on pairs 23.9)
   if (T > kSplitTok) {
     const int pairs = resident_pairs(device, info.sms);
     if (pairs == 0) return DORA_ERR_CUDA;

@@ -2,7 +2,8 @@
 
 The custom ops; each allocates its outputs (and the library's workspace)
 with torch and calls the C entry points of the same names on the current CUDA
-stream.  No arithmetic happens here:
+stream.  No arithmetic happens here but the low-rank products of linear_q8 and
+of its backward, which are torch's:
 
   torch.ops.dora.norm_factored(W0, A, B, m, s) -> (norm, g)
   torch.ops.dora.row_sumsq(W0) -> n0sq                       (bf16 W0: ||W0_i||^2, once)
@@ -407,6 +408,9 @@ def linear_q8(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Te
     """The layer's output y and what its backward needs: (y, xq, xscale, vq, vscale, xa)."""
     _linear_q8_check(x, wq, wscale, A, B, g)
     xq, xscale = q8_store(x, 1)
+    # the low-rank products run in x's bfloat16, fp32 A and B rounded to it (2^-8,
+    # below what the 8-bit base product next to them carries, 2^-4).  v is kept
+    # also where no backward will read it: one form of the call
     xa = x @ A.to(x.dtype).t()
     y, vq, vscale = compose_q8(matmul_q8(xq, xscale, wq, wscale), xa @ B.to(x.dtype).t(), m, g, norm, s)
     return y, xq, xscale, vq, vscale, xa
@@ -443,6 +447,9 @@ def _linear_q8_backward(ctx, dy, *_):
     need = ctx.needs_input_grad
     d_base, d_lora, d_mag = compose_bwd_q8(dy.contiguous(), vq, vscale, g, norm, ctx.s)
     dx = dA = dB = None
+    # dB and dxa leave their products in bfloat16, as under autocast, and dx is
+    # the bfloat16 sum of two such results; dA, from the library's own product,
+    # is fp32 until it takes A's type
     if need[4]:
         dB = (d_lora.t() @ xa).to(B.dtype)
     if need[0] or need[3]:
