@@ -508,6 +508,128 @@ dora_status dora_matmul_q8_t(const void *dyq, const void *dyscale, const void *w
                              void *workspace, size_t workspace_bytes, dora_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* (f) a frozen weight in 4 bits                                             */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The 4-bit form of a matrix [rows, cols], cols a multiple of 32: q, one E2M1
+ * value per element (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign bit), two a byte with
+ * the even column in the low half [rows, cols / 2], and scale, one byte b per 32
+ * columns of a row, standing for 2^(b - 127) [rows, cols / 32].  An element's
+ * value is E2M1(q) 2^(b - 127), b from 0 to 254; b = 255 makes its group NaN.
+ * This is the layout of a microscaling (MX) FP4 matrix stored row by row.
+ *
+ * The scale that a store gives a group is the smallest power of two that brings
+ * its largest magnitude to at most 6, and at least 2^-125: every value is then
+ * exact in bf16, and rounding (nearest even) happens once, in E2M1.  E2M1 has no
+ * NaN: a group that holds a NaN or an infinity is stored as zeros with b = 255.
+ * A stack of matrices of one width is stored as one matrix of all their rows.
+ */
+
+/*
+ * x into the 4-bit form, one pass.
+ *   act    DORA_F32 or DORA_BF16: dtype of x
+ *   x      [rows, cols] of `act`, 16-byte aligned
+ *   q      uint8 [rows, cols / 2]  out, 16-byte aligned
+ *   scale  uint8 [rows, cols / 32]  out
+ *   Sizes: rows, cols >= 0 (either 0 is a no-op), < 2^31, cols % 32 == 0.
+ */
+dora_status dora_q4_store(dora_dtype act, const void *x, int64_t rows, int64_t cols,
+                          void *q, void *scale, dora_stream_t stream);
+
+/* The values of a 4-bit form: x[i,j] = E2M1(q[i,j]) 2^(b - 127), one pass; exact in
+ * either `act`, but infinite from 2^128 on (b = 253 and 254).  Arguments and sizes
+ * as dora_q4_store (x is written). */
+dora_status dora_q4_load(dora_dtype act, const void *q, const void *scale, int64_t rows, int64_t cols,
+                         void *x, dora_stream_t stream);
+
+/* Bytes of workspace dora_matmul_q4 and dora_matmul_q4_t need: none at any size; the
+ * pointer may be NULL. */
+size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts);
+size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t experts);
+
+/*
+ * y = x W^T for a bf16 x and a frozen W in 4 bits; fp32 accumulation, y rounded
+ * once to bf16.  With experts, W is a stack of them, the rows of x are sorted by
+ * expert, and rows offsets[e] to offsets[e + 1] meet W[e]; rows of y that no
+ * expert has are left as they were.
+ *   x        bf16 [T, in]     y  bf16 [T, out]
+ *   offsets  int32 [experts + 1] on the device (dora_expert_sort), not falling; or
+ *            NULL with experts == 1: all rows.  Values are clamped to 0 .. T.
+ *   wq       uint8 [experts, out, in / 2]   wscale  uint8 [experts, out, in / 32]
+ *   x, wq and y 16-byte aligned, in % 32 == 0, out % 16 == 0
+ *   workspace  not used (dora_matmul_q4_workspace)
+ *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1, below 2^31 - 1023,
+ *   1 <= experts <= 4096.
+ * The launch is a programmatic dependent one: its set-up overlaps the launch before
+ * it, and it reads and writes nothing of the caller's before that has completed.
+ */
+dora_status dora_matmul_q4(const void *x, const int32_t *offsets, const void *wq, const void *wscale,
+                           int64_t T, int64_t out, int64_t in, int64_t experts, void *y,
+                           void *workspace, size_t workspace_bytes, dora_stream_t stream);
+
+/*
+ * dx = dy W for the same stored W (no transposed copy): dy bf16 [T, out], dx bf16
+ * [T, in].  The rest as dora_matmul_q4.
+ *   Sizes: T, in >= 0 (either 0 is a no-op), out >= 1.
+ */
+dora_status dora_matmul_q4_t(const void *dy, const int32_t *offsets, const void *wq, const void *wscale,
+                             int64_t T, int64_t out, int64_t in, int64_t experts, void *dx,
+                             void *workspace, size_t workspace_bytes, dora_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* (g) tokens sorted by expert and back                                      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The T * k entries of expert [T, k] (entry i = t * k + j) sorted by expert, stably:
+ *   order    int32 [T * k]       the entry at each sorted row
+ *   inverse  int32 [T, k]        the sorted row of each entry
+ *   offsets  int32 [experts + 1] the rows of expert e are offsets[e] to offsets[e + 1]
+ * An entry outside [0, experts) goes to no expert: its row comes at or behind
+ * offsets[experts], after all that do.  An expert may be named twice by a token.
+ *   index_bytes  4 or 8: expert is int32 or int64
+ *   Sizes: T >= 0, k >= 1, T * k < 2^31 - 1024, 1 <= experts <= 4096.
+ */
+dora_status dora_expert_sort(int index_bytes, const void *expert, int64_t T, int64_t k, int64_t experts,
+                             int32_t *order, int32_t *inverse, int32_t *offsets, dora_stream_t stream);
+
+/*
+ * xs[inverse[t,j]] = x[t] for every entry that has an expert: the tokens' rows sorted
+ * by expert.  The other rows of xs are left as they were.  Its gradient is
+ * dora_expert_return without weights.
+ *   act  DORA_F32 or DORA_BF16: dtype of x [T, cols] and xs [T * k, cols]
+ *   inverse, offsets  of dora_expert_sort.  An entry of inverse is a row of xs where
+ *        it lies in 0 .. min(offsets[experts], T * k), else it has no expert.
+ *   Sizes: T, cols >= 0 (either 0 is a no-op), cols < 2^31; the rest as dora_expert_sort.
+ *   Any element alignment; 128-bit accesses where rows are whole 16-byte pieces.
+ */
+dora_status dora_expert_send(dora_dtype act, const void *x, const int32_t *inverse, const int32_t *offsets,
+                             int64_t T, int64_t k, int64_t cols, int64_t experts, void *xs,
+                             dora_stream_t stream);
+
+/*
+ * y[t] = sum_j weight[t,j] ys[inverse[t,j]] over the entries that have an expert, in
+ * fp32 and in the order of j, rounded once; 0 where none has.
+ *   ys  [T * k, cols] and y [T, cols] of `act`;  weight  float32 [T, k], or NULL:
+ *   every one 1.  The rest as dora_expert_send.
+ */
+dora_status dora_expert_return(dora_dtype act, const void *ys, const int32_t *inverse, const int32_t *offsets,
+                               const float *weight, int64_t T, int64_t k, int64_t cols, int64_t experts,
+                               void *y, dora_stream_t stream);
+
+/*
+ * The gradient of dora_expert_return: d_ys[inverse[t,j]] = weight[t,j] dy[t] and
+ * d_weight[t,j] = <dy[t], ys[inverse[t,j]]> (fp32, fixed order; 0 for an entry that has
+ * no expert).  Rows of d_ys that no expert has are left as they were.
+ *   dy [T, cols], ys and d_ys [T * k, cols] of `act`;  weight, d_weight  float32 [T, k]
+ */
+dora_status dora_expert_return_bwd(dora_dtype act, const void *dy, const void *ys, const int32_t *inverse,
+                                   const int32_t *offsets, const float *weight, int64_t T, int64_t k,
+                                   int64_t cols, int64_t experts, void *d_ys, float *d_weight,
+                                   dora_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 
@@ -524,8 +646,8 @@ uint64_t dora_kernel_launches(void);
 /*
  * Testing hook for the failure path; no counterpart in the paper.  With on != 0
  * the tensor-core kernels of later dora_norm_factored, dora_norm_factored_bwd,
- * dora_compose_lora_fwd, dora_linear_fwd, dora_lora_grad_q8, dora_matmul_q8 and
- * dora_matmul_q8_t calls on the current device
+ * dora_compose_lora_fwd, dora_linear_fwd, dora_lora_grad_q8, dora_matmul_q8,
+ * dora_matmul_q8_t, dora_matmul_q4 and dora_matmul_q4_t calls on the current device
  * withhold all their operand loads, so their bounded waits expire after
  * wait_limit_ns (0 = the default of 2 s): the kernels then record a code in the
  * device error word (see dora_device_error), free their tensor memory and

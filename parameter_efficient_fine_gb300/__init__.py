@@ -42,6 +42,16 @@ __all__ = [
     "dora_matmul_q8",
     "dora_matmul_q8_t_workspace",
     "dora_matmul_q8_t",
+    "dora_q4_store",
+    "dora_q4_load",
+    "dora_matmul_q4_workspace",
+    "dora_matmul_q4",
+    "dora_matmul_q4_t_workspace",
+    "dora_matmul_q4_t",
+    "dora_expert_sort",
+    "dora_expert_send",
+    "dora_expert_return",
+    "dora_expert_return_bwd",
     "dora_device_error",
     "dora_kernel_launches",
     "dora_test_stall_loads",
@@ -91,6 +101,16 @@ _SIGNATURES = {
     "dora_matmul_q8": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
     "dora_matmul_q8_t_workspace": (_sz, [_i64, _i64, _i64]),
     "dora_matmul_q8_t": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "dora_q4_store": (_int, [_int, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "dora_q4_load": (_int, [_int, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "dora_matmul_q4_workspace": (_sz, [_i64, _i64, _i64, _i64]),
+    "dora_matmul_q4": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "dora_matmul_q4_t_workspace": (_sz, [_i64, _i64, _i64, _i64]),
+    "dora_matmul_q4_t": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "dora_expert_sort": (_int, [_int, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "dora_expert_send": (_int, [_int, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
+    "dora_expert_return": (_int, [_int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
+    "dora_expert_return_bwd": (_int, [_int, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp]),
     "dora_device_error": (_int, [ctypes.POINTER(_int)]),
     "dora_kernel_launches": (ctypes.c_uint64, []),
     "dora_test_stall_loads": (_int, [_int, ctypes.c_uint64]),
@@ -430,6 +450,150 @@ def dora_matmul_q8(xq, xscale, wq, wscale, y, workspace=None, stream=None) -> No
 def dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx, workspace=None, stream=None) -> None:
     """dx = dy W for dy and the same W in 8 bits (see include/dora.h)."""
     _matmul_q8("dora_matmul_q8_t", dyq, dyscale, wq, wscale, dx, workspace, stream, False)
+
+
+def _q4(name: str, lead, cols: int, q, scale) -> None:
+    """The shapes of a 4-bit form of [*lead, cols]; the C ABI sees only the matrix's."""
+    if q.element_size() != 1 or scale.element_size() != 1:
+        raise TypeError(f"{name}: the 4-bit form is bytes, got {q.dtype} and {scale.dtype}")
+    if cols % 32:
+        raise ValueError(f"{name}: the 4-bit form has rows of whole groups of 32 columns, got {cols}")
+    if q.shape != (*lead, cols // 2) or scale.shape != (*lead, cols // 32):
+        raise ValueError(f"{name}: 4-bit form of {[*lead, cols]}: got q {tuple(q.shape)}, scale {tuple(scale.shape)}")
+
+
+def _q4_rows(name: str, x, q, scale) -> tuple[int, int]:
+    """Rows and columns of a matrix or of a stack of them; the form of either is checked."""
+    if x.dim() < 2:
+        raise ValueError(f"{name}: a matrix or a stack of them, got {tuple(x.shape)}")
+    cols = x.shape[-1]
+    _q4(name, x.shape[:-1], cols, q, scale)
+    return x.shape[:-1].numel(), cols
+
+
+def dora_q4_store(x, q, scale, stream=None) -> None:
+    """x [..., rows, cols] into its 4-bit form: two E2M1 values a byte and a scale per
+    32 columns of a row (see include/dora.h)."""
+    rows, cols = _q4_rows("dora_q4_store", x, q, scale)
+    act = _act(x)
+    px, pq, psc, cs = _addresses("dora_q4_store", stream, x, q, scale)
+    _check("dora_q4_store", load_library().dora_q4_store(act, px, rows, cols, pq, psc, cs))
+
+
+def dora_q4_load(q, scale, x, stream=None) -> None:
+    """The values of a 4-bit form into x (see include/dora.h)."""
+    rows, cols = _q4_rows("dora_q4_load", x, q, scale)
+    act = _act(x)
+    px, pq, psc, cs = _addresses("dora_q4_load", stream, x, q, scale)
+    _check("dora_q4_load", load_library().dora_q4_load(act, pq, psc, rows, cols, px, cs))
+
+
+def dora_matmul_q4_workspace(T: int, out: int, inp: int, experts: int = 1) -> int:
+    return int(load_library().dora_matmul_q4_workspace(T, out, inp, experts))
+
+
+def dora_matmul_q4_t_workspace(T: int, out: int, inp: int, experts: int = 1) -> int:
+    return int(load_library().dora_matmul_q4_t_workspace(T, out, inp, experts))
+
+
+def _matmul_q4(name: str, x, wq, wscale, y, offsets, workspace, stream, out_side: bool) -> None:
+    import torch
+    if wq.dim() != (2 if offsets is None else 3):
+        raise ValueError(f"{name}: a weight [out, in / 2], or with offsets a stack [experts, out, in / 2], "
+                         f"got {tuple(wq.shape)}")
+    out, inp = wq.shape[-2], 2 * wq.shape[-1]
+    experts = 1 if offsets is None else wq.shape[0]
+    _q4(name, wq.shape[:-1], inp, wq, wscale)
+    T = x.shape[0]
+    _same(name, (T, inp if out_side else out), torch.bfloat16, x)
+    _same(name, (T, out if out_side else inp), torch.bfloat16, y)
+    ts = [x, wq, wscale, y]
+    if offsets is not None:
+        _same(name, (experts + 1,), torch.int32, offsets)
+        ts.append(offsets)
+    if workspace is not None:
+        ts.append(workspace)
+    px, pw, psc, py, *more, cs = _addresses(name, stream, *ts)
+    poff = more.pop(0) if offsets is not None else 0
+    st = getattr(load_library(), name)(px, poff, pw, psc, T, out, inp, experts, py, more[0] if more else 0,
+                                       0 if workspace is None else workspace.numel() * workspace.element_size(), cs)
+    _check(name, st)
+
+
+def dora_matmul_q4(x, wq, wscale, y, offsets=None, workspace=None, stream=None) -> None:
+    """y = x W^T for a bfloat16 x and W in 4 bits; with offsets, W is a stack and rows
+    offsets[e] to offsets[e + 1] of x meet W[e] (see include/dora.h)."""
+    _matmul_q4("dora_matmul_q4", x, wq, wscale, y, offsets, workspace, stream, True)
+
+
+def dora_matmul_q4_t(dy, wq, wscale, dx, offsets=None, workspace=None, stream=None) -> None:
+    """dx = dy W for the same W (see include/dora.h)."""
+    _matmul_q4("dora_matmul_q4_t", dy, wq, wscale, dx, offsets, workspace, stream, False)
+
+
+def dora_expert_sort(expert, experts: int, order, inverse, offsets, stream=None) -> None:
+    """The entries of expert [T, k] sorted by expert, stably: order, its inverse and
+    where each expert's begin (see include/dora.h)."""
+    import torch
+    if expert.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"dora_expert_sort: expert is int32 or int64, got {expert.dtype}")
+    if not 1 <= experts <= 4096:
+        raise ValueError(f"dora_expert_sort: 1 to 4096 experts, got {experts}")
+    T, k = expert.shape
+    _same("dora_expert_sort", (T * k,), torch.int32, order)
+    _same("dora_expert_sort", (T, k), torch.int32, inverse)
+    _same("dora_expert_sort", (experts + 1,), torch.int32, offsets)
+    pe, po, pi, pf, cs = _addresses("dora_expert_sort", stream, expert, order, inverse, offsets)
+    _check("dora_expert_sort", load_library().dora_expert_sort(expert.element_size(), pe, T, k, experts, po, pi, pf, cs))
+
+
+def _routed(name: str, x, xs, inverse, offsets) -> tuple[int, int, int, int]:
+    """T, k, cols and the number of experts of tokens x [T, cols] and their rows xs [T k, cols]."""
+    import torch
+    T, k = inverse.shape
+    cols, experts = x.shape[1], offsets.numel() - 1
+    if offsets.dim() != 1 or not 1 <= experts <= 4096:
+        raise ValueError(f"{name}: offsets are [experts + 1], 1 to 4096 experts, got {tuple(offsets.shape)}")
+    _same(name, (T, k), torch.int32, inverse)
+    _same(name, (experts + 1,), torch.int32, offsets)
+    _same(name, (T, cols), x.dtype, x)
+    _same(name, (T * k, cols), x.dtype, xs)
+    return T, k, cols, experts
+
+
+def dora_expert_send(x, inverse, offsets, xs, stream=None) -> None:
+    """xs[inverse[t, j]] = x[t], the tokens' rows sorted by expert (see include/dora.h)."""
+    T, k, cols, experts = _routed("dora_expert_send", x, xs, inverse, offsets)
+    act = _act(x)
+    px, ps, pi, pf, cs = _addresses("dora_expert_send", stream, x, xs, inverse, offsets)
+    _check("dora_expert_send", load_library().dora_expert_send(act, px, pi, pf, T, k, cols, experts, ps, cs))
+
+
+def dora_expert_return(ys, inverse, offsets, weight, y, stream=None) -> None:
+    """y[t] = sum_j weight[t, j] ys[inverse[t, j]]; weight None: every one 1 (see include/dora.h)."""
+    import torch
+    T, k, cols, experts = _routed("dora_expert_return", y, ys, inverse, offsets)
+    act = _act(y)
+    ts = [ys, y, inverse, offsets]
+    if weight is not None:
+        _same("dora_expert_return", (T, k), torch.float32, weight)
+        ts.append(weight)
+    ps, py, pi, pf, *pw, cs = _addresses("dora_expert_return", stream, *ts)
+    _check("dora_expert_return",
+           load_library().dora_expert_return(act, ps, pi, pf, pw[0] if pw else 0, T, k, cols, experts, py, cs))
+
+
+def dora_expert_return_bwd(dy, ys, inverse, offsets, weight, d_ys, d_weight, stream=None) -> None:
+    """d_ys[inverse[t, j]] = weight[t, j] dy[t], d_weight[t, j] = <dy[t], ys[inverse[t, j]]> (see include/dora.h)."""
+    import torch
+    T, k, cols, experts = _routed("dora_expert_return_bwd", dy, ys, inverse, offsets)
+    _same("dora_expert_return_bwd", (T * k, cols), dy.dtype, d_ys)
+    _same("dora_expert_return_bwd", (T, k), torch.float32, weight, d_weight)
+    act = _act(dy)
+    pd, ps, pi, pf, pw, pds, pdw, cs = _addresses("dora_expert_return_bwd", stream, dy, ys, inverse, offsets, weight,
+                                                  d_ys, d_weight)
+    _check("dora_expert_return_bwd",
+           load_library().dora_expert_return_bwd(act, pd, ps, pi, pf, pw, T, k, cols, experts, pds, pdw, cs))
 
 
 def dora_device_error() -> int:

@@ -1,0 +1,567 @@
+// Products with a weight in 4 bits (see q4.cuh for the form) on the tensor cores
+// of GB300 (sm_103a), in bf16.
+//
+//   dora_matmul_q4     y  = x W^T      x [T, in], W [out, in]
+//   dora_matmul_q4_t   dx = dy W       dy [T, out], the same W
+//
+// With experts, W is a stack and the rows of x are sorted by expert: rows
+// offsets[e] to offsets[e + 1] meet W[e].
+//
+// The features are the M side, the tokens the N side.  A block of W, 128 rows of
+// it by 128 columns, arrives as it is stored (8 KB), is turned into bf16 by
+// conversion warps and lies in shared memory as two panels of 128 rows x 64
+// columns, 128 bytes a row, swizzled.  For x W^T its rows are features and the
+// panels K-major, for dy W its rows are k and the panels M-major: one conversion
+// serves both, and only the descriptors differ.
+//
+// CTA pairs (tcgen05.mma.cta_group::2): tiles of 256 features by up to 256 tokens,
+// each CTA converting its 128 features and staging half of the tokens.
+//   warp 0       TMA: blocks of W into a ring of their own, tokens into the stages
+//   warp 1       tensor memory, MMA issue (even CTA)
+//   warps 2-9    conversion: a row and a panel each thread
+//   warps 10-17  the result
+// Every wait on a shared-memory barrier is bounded; a wait that gives up records
+// a code in the library's device error word and all roles leave.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "q4.cuh"
+#include "q8_tc.cuh"
+#include "tc_ptx.cuh"
+
+namespace {
+
+constexpr int kKB = 128;                              // k per stage, and the side of a block of W
+constexpr int kTileF = 256;                           // features per tile
+constexpr int kTileT = 256;                           // most tokens per tile
+constexpr int kRaw = 4;                               // blocks of W in flight
+constexpr unsigned kRawBytes = 128 * kKB / 2;         // 8 KB
+constexpr unsigned kPanel = 128 * 128;                // 16 KB: 128 rows of 64 bf16
+constexpr int kConvWarps = 8, kOutWarps = 8;
+constexpr int kThreadsMm = 32 * (2 + kConvWarps + kOutWarps);
+constexpr int64_t kMaxExperts = 4096;
+// half of the tile's tokens, 64 k
+__host__ __device__ constexpr unsigned tok_box(int ntok) { return static_cast<unsigned>(ntok / 2 * 128); }
+__host__ __device__ constexpr unsigned stage_size(int ntok) { return 2 * (kPanel + tok_box(ntok)); }
+
+struct Q4Params {
+  int T, out, in;
+  int nfeat, kdim;                  // features of the result, k
+  int experts;
+  const int *offsets;               // null: one weight, all rows
+  int ntok, stages;                 // tokens per tile, ring
+  int ftiles;
+  int64_t tiles;                    // no more than these
+  const uint8_t *scale;
+  __nv_bfloat16 *y;
+  Guard guard;
+};
+
+// feature tiles per tile-order group, for reuse in L2
+constexpr int kGroupF = 8;
+
+// what a tile works on
+struct Tile {
+  int e, ft;                        // expert, feature tile
+  int t0, t1;                       // its tokens
+};
+
+// Tile `t`, or false past the last.  All lanes of the warp call it.  Experts: the
+// tokens' tiles of all experts in order, the feature tiles of each in turn.
+__device__ __forceinline__ bool find_tile(const Q4Params &p, int64_t t, Tile *o) {
+  if (!p.offsets) {
+    const int ntiles = (p.T + p.ntok - 1) / p.ntok;
+    if (t >= static_cast<int64_t>(ntiles) * p.ftiles) return false;
+    const int per = kGroupF * ntiles, g = static_cast<int>(t / per), f0 = g * kGroupF, gf = min(kGroupF, p.ftiles - f0),
+              r = static_cast<int>(t - static_cast<int64_t>(g) * per), tt = r / gf;
+    o->e = 0;
+    o->ft = f0 + r - tt * gf;
+    o->t0 = tt * p.ntok;
+    o->t1 = min(p.T, o->t0 + p.ntok);
+    return true;
+  }
+  const int lane = threadIdx.x & 31;
+  const int64_t tt = t / p.ftiles;
+  int64_t before = 0;                                  // token tiles of the experts before this 32
+  for (int e0 = 0; e0 < p.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int a = 0, b = 0;
+    if (e < p.experts) {
+      a = min(max(p.offsets[e], 0), p.T);
+      b = min(max(p.offsets[e + 1], a), p.T);
+    }
+    const int own = (b - a + p.ntok - 1) / p.ntok;
+    int upto = own;                                    // tiles of this 32, up to and with this expert's
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > tt);
+    if (past) {
+      const int who = __ffs(past) - 1;
+      const int first = __shfl_sync(0xffffffffu, upto - own, who);
+      a = __shfl_sync(0xffffffffu, a, who);
+      b = __shfl_sync(0xffffffffu, b, who);
+      o->e = e0 + who;
+      o->ft = static_cast<int>(t - tt * p.ftiles);
+      o->t0 = a + static_cast<int>(tt - before - first) * p.ntok;
+      o->t1 = min(b, o->t0 + p.ntok);
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+// a place in a ring of n
+struct Ring {
+  int n, i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int size) : n(size) {}
+  __device__ __forceinline__ void next() {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// arrive on an mbarrier of the pair where what it hands over is tensor memory
+// only, which the tcgen05 fence before it orders
+__device__ __forceinline__ void mbar_arrive_pair_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// this thread's writes to shared memory before the tensor core's reads
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t *v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+// loads that stay where they are written (the compiler would move them down to
+// their use, past the wait that they are to overlap)
+__device__ __forceinline__ uint32_t load_now(const uint8_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_now16(const uint8_t *p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
+// M-major panels: 64 features a row of 128 bytes, k down the rows, the panel of the
+// next 64 features kPanel further
+__device__ __forceinline__ uint64_t sdesc_mmajor(uint32_t saddr) {
+  return (sdesc<32>(saddr) & ~(static_cast<uint64_t>(0x3fff) << 16)) | (static_cast<uint64_t>(kPanel >> 4) << 16);
+}
+
+template <bool TRANS>
+__global__ void __launch_bounds__(kThreadsMm, 1)
+q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = p.stages;
+  const uint32_t xbox = tok_box(p.ntok), stage_bytes = stage_size(p.ntok);
+  uint8_t *raw = smem + S * stage_bytes;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(raw + kRaw * kRawBytes);
+  // barriers (a pair uses the even CTA's full and accumulator empty): tokens full,
+  // W converted, empty; raw full and empty; accumulator full and empty; end
+  const uint32_t tfull0 = smem_u32(bars), wfull0 = tfull0 + 8u * S, empty0 = wfull0 + 8u * S, rfull0 = empty0 + 8u * S,
+                 rempty0 = rfull0 + 8u * kRaw, accf = rempty0 + 8u * kRaw, acce = accf + 16, fin = acce + 16;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 3 * S + 2 * kRaw + 5);
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(tfull0 + 8u * s, 1);
+      mbar_init(wfull0 + 8u * s, 2 * kConvWarps);
+      mbar_init(empty0 + 8u * s, 1);
+    }
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(rfull0 + 8u * s, 1);
+      mbar_init(rempty0 + 8u * s, kConvWarps);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf + 8u * b, 1);
+      mbar_init(acce + 8u * b, 2 * kOutWarps);
+    }
+    mbar_init(fin, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+    prefetch_map(&mW);
+    prefetch_map(&mX);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers are initialised before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  pdl_trigger();
+  pdl_wait();       // the set-up above overlaps the end of the launch before
+  const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+  const int kstages = (p.kdim + kKB - 1) / kKB;
+  Tile o;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    bool ok = !loads_withheld(p.guard);
+    bool issued = false;
+    Ring st(S), rw(kRaw);
+    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+      const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128, t0 = o.t0 + static_cast<int>(rank) * (p.ntok / 2);
+      for (int s = 0; s < kstages; ++s) {
+        ok = guard_wait(rempty0 + 8u * rw.i, rw.phase ^ 1u, ctl, p.guard, 61);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t fb = rfull0 + 8u * rw.i, at = smem_u32(raw) + rw.i * kRawBytes;
+          mbar_expect_tx(fb, kRawBytes);
+          // coordinates in bytes along a row of W
+          if (TRANS) tma_load_3d(at, &mW, f0 / 2, s * kKB, o.e, fb);
+          else tma_load_3d(at, &mW, s * (kKB / 2), f0, o.e, fb);
+        }
+        __syncwarp();
+        issued = true;
+        rw.next();
+        ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 62);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t fb = tfull0 + 8u * st.i, lb = mapa_shared(fb, 0);
+          const uint32_t at = smem_u32(smem) + st.i * stage_bytes + 2 * kPanel;
+          // the even CTA's barrier counts both CTAs' bytes
+          if (rank == 0) mbar_expect_tx(fb, 4 * xbox);
+          tma_load_2d_pair(at, &mX, s * kKB, t0, lb);
+          tma_load_2d_pair(at + xbox, &mX, s * kKB + 64, t0, lb);
+        }
+        __syncwarp();
+        st.next();
+      }
+    }
+    if (!ok && issued) {
+      // copies in flight, whose barrier may never complete after an abort: they
+      // land within microseconds, wait 1 ms
+      const unsigned long long c0 = globaltimer();
+      while (globaltimer() - c0 < 1000000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      // (a commit arrives on the barrier of this CTA and on the peer's)
+      bool ok = true;
+      Ring st(S), acc(2);
+      const uint32_t peer_off = mapa_shared(tfull0, peer) - tfull0;   // to the peer's copy of a barrier
+      const uint32_t id = idesc_bf16_pair(p.ntok) | (TRANS ? 1u << 15 : 0u);
+      for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
+        ok = guard_wait(acce + 8u * acc.i, acc.phase ^ 1u, ctl, p.guard, 63);
+        const uint32_t d = tmem + static_cast<uint32_t>(acc.i) * kTileT;
+        for (int s = 0; s < kstages; ++s) {
+          ok = ok && guard_wait(tfull0 + 8u * st.i, st.phase, ctl, p.guard, 64);
+          ok = ok && guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 65);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem) + st.i * stage_bytes;
+          const uint64_t a = TRANS ? sdesc_mmajor(at) : sdesc<32>(at), b = sdesc<32>(at + 2 * kPanel);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              // 16 k: 32 bytes along a K-major row, or 16 rows of an M-major panel
+              mma_bf16_ss_pair(d, TRANS ? a + 128u * k : a + (kPanel >> 4) * (k / 4) + 2u * (k % 4),
+                               b + (xbox >> 4) * (k / 4) + 2u * (k % 4), id, s != 0 || k != 0 ? 1u : 0u);
+            mma_commit_pair(empty0 + 8u * st.i);
+            mma_commit_pair(empty0 + 8u * st.i + peer_off);
+            if (s + 1 == kstages) {
+              mma_commit_pair(accf + 8u * acc.i);
+              mma_commit_pair(accf + 8u * acc.i + peer_off);
+            }
+          }
+          __syncwarp();
+          st.next();
+        }
+      }
+      if (elect_one()) {
+        mma_commit_pair(fin);
+        wait_drain_ns(fin, 0, kWaitNs);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 2 + kConvWarps) {
+    // ---------------------------------------------------------------- conversion
+    const int panel = (warp - 2) / 4, r = ((warp - 2) % 4) * 32 + lane;
+    const int G = p.in / kQ4Group;
+    const bool words = G % 2 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 1) == 0;
+    const uint32_t from = smem_u32(raw) + static_cast<uint32_t>(r) * 64u, to = smem_u32(smem) + panel * kPanel + r * 128u;
+    const uint32_t c0 = static_cast<uint32_t>((2 * panel) ^ ((r >> 1) & 3)) * 16u,
+                   c1 = static_cast<uint32_t>((2 * panel + 1) ^ ((r >> 1) & 3)) * 16u;
+    bool ok = true;
+    Ring st(S), rw(kRaw);
+    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+      const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
+      // the two scale bytes of this thread's part of block s
+      auto scales = [&](int s) -> uint32_t {
+        const int row = TRANS ? s * kKB + r : f0 + r, g = (TRANS ? f0 : s * kKB) / kQ4Group + 2 * panel;
+        if (row >= p.out || g >= G) return 0x7f7fu;
+        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + row) * G + g;
+        if (words) return load_now16(at);
+        return load_now(at) | (g + 1 < G ? load_now(at + 1) : 127u) << 8;
+      };
+      uint32_t sc[kRaw];
+#pragma unroll
+      for (int u = 0; u < kRaw; ++u) sc[u] = u < kstages ? scales(u) : 0u;
+      for (int s0 = 0; s0 < kstages && ok; s0 += kRaw) {
+#pragma unroll
+        for (int u = 0; u < kRaw; ++u) {
+          const int s = s0 + u;
+          if (s >= kstages || !ok) break;
+          const uint32_t b = sc[u];
+          if (s + kRaw < kstages) sc[u] = scales(s + kRaw);
+          ok = guard_wait(rfull0 + 8u * rw.i, rw.phase, ctl, p.guard, 66);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint4 w0 = lds128(from + rw.i * kRawBytes + c0), w1 = lds128(from + rw.i * kRawBytes + c1);
+          uint32_t v[2][16];
+          q4_bf16x32(w0, b & 255u, v[0]);
+          q4_bf16x32(w1, b >> 8, v[1]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(rempty0 + 8u * rw.i);
+          ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 67);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t dst = to + st.i * stage_bytes;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) sts128(dst + static_cast<uint32_t>((c ^ (r & 7)) * 16), &v[c / 4][(c % 4) * 4]);
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(wfull0 + 8u * st.i, 0));
+          rw.next();
+          st.next();
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- result
+    const int e = warp - 2 - kConvWarps;
+    const uint32_t quad = static_cast<uint32_t>(warp & 3);
+    const int half = p.ntok / 2;                   // tokens of this warp, from c0
+    const int c0 = (e >> 2) * half;
+    const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
+    bool ok = true;
+    Ring acc(2);
+    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
+      ok = guard_wait(accf + 8u * acc.i, acc.phase, ctl, p.guard, 68);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[kTileT / 4];                      // two tokens a register
+#pragma unroll
+      for (int c = 0; c < kTileT / 2; c += 8)
+        if (c < half) {
+          float f[8];
+          tmem_ld<8>(lane_addr + acc.i * kTileT + static_cast<uint32_t>(c), f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[c / 2 + i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(acce + 8u * acc.i, 0));
+      const int f = o.ft * kTileF + static_cast<int>(rank) * 128 + static_cast<int>(quad) * 32 + lane;
+      const int t0 = o.t0 + c0;
+      if (f < p.nfeat) {
+        uint16_t *y = reinterpret_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0) * p.nfeat + f;
+        const int64_t ld = p.nfeat;
+        const int live = min(o.t1 - t0, half);
+#pragma unroll
+        for (int i = 0; i < kTileT / 4; ++i, y += 2 * ld) {
+          if (2 * i < live) y[0] = static_cast<uint16_t>(v[i]);
+          if (2 * i + 1 < live) y[ld] = static_cast<uint16_t>(v[i] >> 16);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // the even CTA's MMAs, which read this CTA's shared memory and write its
+  // tensor memory, are complete, and both CTAs' results are out
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr size_t kFixed = 1024 + kRaw * kRawBytes + 512;
+constexpr int pair_stages(int ntok) {
+  const int s = static_cast<int>((kSmemMax - kFixed) / stage_size(ntok));
+  return s < 6 ? s : 6;
+}
+constexpr size_t pair_smem(int ntok) { return kFixed + static_cast<size_t>(pair_stages(ntok)) * stage_size(ntok); }
+static_assert(pair_stages(kTileT) >= 3 && 8 * (3 * 6 + 2 * kRaw + 5) + sizeof(SharedCtl) <= 512,
+              "ring, barriers and control words");
+
+void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ntok, int64_t pairs, cudaStream_t cs) {
+  *cfg = cudaLaunchConfig_t{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->gridDim = dim3(2 * static_cast<unsigned>(pairs));
+  cfg->blockDim = dim3(kThreadsMm);
+  cfg->dynamicSmemBytes = pair_smem(ntok);
+  cfg->stream = cs;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+// pairs that are resident at once; 0 where the device has no clusters of two
+int resident_pairs(int device, int sms) {
+  static std::mutex mu;
+  static int known[64] = {};   // pairs + 1
+  std::lock_guard<std::mutex> lock(mu);
+  if (device < 0 || device >= 64) return 0;
+  if (known[device] == 0) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    pair_config(&cfg, attr, kTileT, sms / 2, nullptr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, q4_pair_kernel<false>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[device] = n + 1;
+  }
+  return known[device] - 1;
+}
+
+dora_status mm_init(int device, Q4Params *p) {
+  static const void *const kernels[] = {(const void *)q4_pair_kernel<false>, (const void *)q4_pair_kernel<true>};
+  return tc_init(device, &p->guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
+}
+
+// the stack of weights [experts, out, in / 2 bytes] in boxes of 128 rows x 64 bytes, 64-byte swizzle
+bool map_w(CUtensorMap *map, const void *base, int64_t experts, int64_t out, int64_t in) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(out), static_cast<cuuint64_t>(experts)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(in / 2) * static_cast<cuuint64_t>(out)};
+  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool TRANS>
+dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T, int64_t out,
+                       int64_t in, int64_t experts, void *y, dora_stream_t stream) {
+  dora::DeviceInfo info;
+  int device = 0;
+  dora_status st = dora::current_device(&info, &device);
+  if (st != DORA_OK) return st;
+  Q4Params p = {};
+  st = mm_init(device, &p);
+  if (st != DORA_OK) return st;
+  p.T = static_cast<int>(T);
+  p.out = static_cast<int>(out);
+  p.in = static_cast<int>(in);
+  p.nfeat = static_cast<int>(TRANS ? in : out);
+  p.kdim = static_cast<int>(TRANS ? out : in);
+  p.experts = static_cast<int>(experts);
+  p.offsets = offsets;
+  p.scale = static_cast<const uint8_t *>(wscale);
+  p.y = static_cast<__nv_bfloat16 *>(y);
+  const int pairs = resident_pairs(device, info.sms);
+  if (pairs == 0) return DORA_ERR_CUDA;
+  p.ftiles = static_cast<int>(dora::ceil_div(p.nfeat, kTileF));
+  // tokens per tile: the least time over the waves of tiles.  Experts: as if their
+  // loads were even
+  const int64_t groups = offsets ? (experts < T ? experts : T) : 1, per = dora::ceil_div(T, groups);
+  int64_t best = 0;
+  for (int n = 32; n <= kTileT; n += 32) {
+    const int64_t waves = dora::ceil_div(p.ftiles * groups * dora::ceil_div(per, n), pairs);
+    const int64_t cost = waves * (n + 100);
+    if (best == 0 || cost < best) {
+      best = cost;
+      p.ntok = n;
+    }
+  }
+  p.stages = pair_stages(p.ntok);
+  p.tiles = p.ftiles * (offsets ? T / p.ntok + groups : dora::ceil_div(T, p.ntok));
+  CUtensorMap mW, mX;
+  if (!map_w(&mW, wq, experts, out, in) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.ntok / 2, 128)) return DORA_ERR_CUDA;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  pair_config(&cfg, attr, p.ntok, p.tiles < pairs ? p.tiles : pairs, reinterpret_cast<cudaStream_t>(stream));
+  if (cudaLaunchKernelEx(&cfg, q4_pair_kernel<TRANS>, mW, mX, p) != cudaSuccess) {
+    cudaGetLastError();
+    return DORA_ERR_CUDA;
+  }
+  dora::count_launches(1);
+  return DORA_OK;
+}
+
+dora_status check(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T, int64_t out,
+                  int64_t in, int64_t experts, const void *y) {
+  if (bad_size(T, 0) || bad_size(out, 0) || bad_size(in, 0) || experts < 1 || experts > kMaxExperts) return DORA_ERR_SHAPE;
+  if (!offsets && experts != 1) return DORA_ERR_NULL;
+  if (in % kQ4Group != 0) return DORA_ERR_SHAPE;
+  if (T == 0 || out == 0 || in == 0) return DORA_OK;
+  if (!x || !wq || !wscale || !y) return DORA_ERR_NULL;
+  // TMA: 16-byte aligned bases and row strides
+  if (out % 16 != 0) return DORA_ERR_ALIGN;
+  if (!dora::aligned(x, 16) || !dora::aligned(wq, 16) || !dora::aligned(y, 16) || !dora::aligned(offsets, 4))
+    return DORA_ERR_ALIGN;
+  return DORA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t dora_matmul_q4_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
+extern "C" size_t dora_matmul_q4_t_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+extern "C" dora_status dora_matmul_q4(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
+                                      int64_t out, int64_t in, int64_t experts, void *y, void *, size_t,
+                                      dora_stream_t stream) {
+  if (in < 1) return DORA_ERR_SHAPE;
+  const dora_status st = check(x, offsets, wq, wscale, T, out, in, experts, y);
+  if (st != DORA_OK || T == 0 || out == 0) return st;
+  return run_matmul<false>(x, offsets, wq, wscale, T, out, in, experts, y, stream);
+}
+
+extern "C" dora_status dora_matmul_q4_t(const void *dy, const int32_t *offsets, const void *wq, const void *wscale,
+                                        int64_t T, int64_t out, int64_t in, int64_t experts, void *dx, void *, size_t,
+                                        dora_stream_t stream) {
+  if (out < 1) return DORA_ERR_SHAPE;
+  const dora_status st = check(dy, offsets, wq, wscale, T, out, in, experts, dx);
+  if (st != DORA_OK || T == 0 || in == 0) return st;
+  return run_matmul<true>(dy, offsets, wq, wscale, T, out, in, experts, dx, stream);
+}

@@ -1,0 +1,376 @@
+// Tokens sorted by expert and back, with their gradients, for GB300 (sm_103a).
+//
+//   dora_expert_sort        expert[T, k] -> order, inverse, offsets
+//   dora_expert_send        xs[inverse[t, j]] = x[t]
+//   dora_expert_return      y[t] = sum_j weight[t, j] ys[inverse[t, j]]
+//   dora_expert_return_bwd  d_ys[inverse[t, j]] = weight[t, j] dy[t],
+//                           d_weight[t, j] = <dy[t], ys[inverse[t, j]]>
+//
+// The gradient of send is return without weights.  An entry whose expert is
+// outside [0, experts) goes to no expert: its row lies behind the last expert's,
+// where nothing is read or written, its weight counts for nothing and gets the
+// gradient 0.  All of them are stable and add in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "stream.cuh"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// the sort: one block per expert, and one for the entries of none.  Block e
+// counts the entries of lower experts, which is where its rows start, and of its
+// own in every warp's stretch of the input, and then numbers its own in order.
+// No block waits for another; the input is read from L2.
+// ---------------------------------------------------------------------------
+constexpr int kSortWarps = 32;
+
+template <typename Idx>
+__device__ __forceinline__ int bin_of(Idx v, int experts) {
+  return v >= 0 && v < experts ? static_cast<int>(v) : experts;
+}
+
+template <typename Idx>
+__global__ void __launch_bounds__(32 * kSortWarps)
+expert_sort_kernel(const Idx *__restrict__ expert, int n, int experts, int *__restrict__ order,
+                   int *__restrict__ inverse, int *__restrict__ offsets) {
+  __shared__ int below[kSortWarps], own[kSortWarps];
+  const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // each warp a stretch of whole 32s
+  const int64_t per = (static_cast<int64_t>(n) + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32;
+  const int64_t i0 = per * warp, i1 = i0 + per < n ? i0 + per : n;
+  int lt = 0, eq = 0;
+#pragma unroll 4
+  for (int64_t i = i0 + lane; i < i1; i += 32) {
+    const int b = bin_of(expert[i], experts);
+    lt += b < e;
+    eq += b == e;
+  }
+  lt = __reduce_add_sync(0xffffffffu, lt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    below[warp] = lt;
+    own[warp] = eq;
+  }
+  __syncthreads();
+  const int start = __reduce_add_sync(0xffffffffu, below[lane]);
+  int at = start + __reduce_add_sync(0xffffffffu, lane < warp ? own[lane] : 0);
+  if (threadIdx.x == 0) offsets[e] = start;
+#pragma unroll 4
+  for (int64_t i = i0; i < i1; i += 32) {
+    const bool mine = i + lane < i1 && bin_of(expert[i + lane], experts) == e;
+    const uint32_t all = __ballot_sync(0xffffffffu, mine);
+    if (mine) {
+      const int p = at + __popc(all & ((1u << lane) - 1));
+      order[p] = static_cast<int>(i) + lane;
+      inverse[i + lane] = p;
+    }
+    at += __popc(all);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows there and back.  The threads of a token hold VEC columns each and walk
+// its row; a block holds kThreads / tpt tokens.
+// ---------------------------------------------------------------------------
+struct RouteParams {
+  int64_t T, cols;
+  int k, tpt;                  // rows a token has, threads a token has
+  uint32_t rows;               // T k
+  const int *inverse;          // [T, k]
+  const int *end;              // rows that belong to an expert
+};
+// no row past the T k of the arrays, whatever the offsets say
+__device__ __forceinline__ uint32_t rows_sent(const RouteParams &p) {
+  return min(static_cast<uint32_t>(max(*p.end, 0)), p.rows);
+}
+
+template <typename Act, int VEC>
+__global__ void __launch_bounds__(kThreads)
+expert_send_kernel(const Act *__restrict__ x, const RouteParams p, Act *__restrict__ xs) {
+  using IO = Io<Act, VEC>;
+  const int per = kThreads / p.tpt, c0 = static_cast<int>(threadIdx.x % p.tpt) * VEC;
+  const uint32_t end = rows_sent(p);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / p.tpt; t < p.T;
+       t += static_cast<int64_t>(gridDim.x) * per) {
+    const int *row = p.inverse + t * p.k;
+    for (int64_t c = c0; c < p.cols; c += static_cast<int64_t>(p.tpt) * VEC) {
+      const typename IO::Raw v = IO::load(x, t * p.cols + c);
+      for (int j = 0; j < p.k; ++j) {
+        const uint32_t r = static_cast<uint32_t>(row[j]);
+        if (r < end) IO::store(xs, static_cast<int64_t>(r) * p.cols + c, v);
+      }
+    }
+  }
+}
+
+template <typename Act, int VEC>
+__global__ void __launch_bounds__(kThreads)
+expert_return_kernel(const Act *__restrict__ ys, const float *__restrict__ weight, const RouteParams p,
+                     Act *__restrict__ y) {
+  using IO = Io<Act, VEC>;
+  constexpr int kAhead = 4;
+  const int per = kThreads / p.tpt, c0 = static_cast<int>(threadIdx.x % p.tpt) * VEC;
+  const uint32_t end = rows_sent(p);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / p.tpt; t < p.T;
+       t += static_cast<int64_t>(gridDim.x) * per) {
+    const int *row = p.inverse + t * p.k;
+    for (int64_t c = c0; c < p.cols; c += static_cast<int64_t>(p.tpt) * VEC) {
+      float acc[VEC] = {};
+      for (int j = 0; j < p.k; j += kAhead) {
+        typename IO::Raw raw[kAhead];
+        bool live[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const uint32_t r = j + a < p.k ? static_cast<uint32_t>(row[j + a]) : 0xffffffffu;
+          live[a] = r < end;
+          raw[a] = live[a] ? IO::load(ys, static_cast<int64_t>(r) * p.cols + c) : typename IO::Raw{};
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          if (!live[a]) continue;
+          const float w = weight ? weight[t * p.k + j + a] : 1.0f;
+          float v[VEC];
+          IO::unpack(raw[a], v);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+        }
+      }
+      IO::store(y, t * p.cols + c, IO::pack(acc));
+    }
+  }
+}
+
+template <typename Act, int VEC>
+__global__ void __launch_bounds__(kThreads)
+expert_return_bwd_kernel(const Act *__restrict__ dy, const Act *__restrict__ ys, const float *__restrict__ weight,
+                         const RouteParams p, Act *__restrict__ d_ys, float *__restrict__ d_weight) {
+  using IO = Io<Act, VEC>;
+  constexpr int kAhead = 4;
+  __shared__ float part[kAhead][kThreads / 32];
+  const int per = kThreads / p.tpt, c0 = static_cast<int>(threadIdx.x % p.tpt) * VEC;
+  const uint32_t end = rows_sent(p);
+  // every thread takes part in the sums, whether its token exists or not
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * per; t0 < p.T; t0 += static_cast<int64_t>(gridDim.x) * per) {
+    const int64_t t = t0 + threadIdx.x / p.tpt;
+    const bool in = t < p.T;
+    for (int j = 0; j < p.k; j += kAhead) {
+      uint32_t r[kAhead];
+      float w[kAhead], dot[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const bool has = in && j + a < p.k;
+        r[a] = has ? static_cast<uint32_t>(p.inverse[t * p.k + j + a]) : 0xffffffffu;
+        w[a] = has ? weight[t * p.k + j + a] : 0.0f;
+        dot[a] = 0.0f;
+      }
+      if (in)
+        for (int64_t c = c0; c < p.cols; c += static_cast<int64_t>(p.tpt) * VEC) {
+          const typename IO::Raw draw = IO::load(dy, t * p.cols + c);
+          typename IO::Raw raw[kAhead];
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a)
+            raw[a] = r[a] < end ? IO::load(ys, static_cast<int64_t>(r[a]) * p.cols + c) : typename IO::Raw{};
+          float d[VEC];
+          IO::unpack(draw, d);
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a) {
+            if (r[a] >= end) continue;
+            float v[VEC], o[VEC];
+            IO::unpack(raw[a], v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              dot[a] = fmaf(d[i], v[i], dot[a]);
+              o[i] = w[a] * d[i];
+            }
+            IO::store(d_ys, static_cast<int64_t>(r[a]) * p.cols + c, IO::pack(o));
+          }
+        }
+      // the token's threads: within a warp, then its warps in order
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        for (int o = min(p.tpt, 32) / 2; o > 0; o >>= 1) dot[a] += __shfl_xor_sync(0xffffffffu, dot[a], o);
+      const int lead = threadIdx.x % p.tpt;
+      if (p.tpt > 32) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+          if (threadIdx.x % 32 == 0) part[a][threadIdx.x / 32] = dot[a];
+        __syncthreads();
+        if (lead == 0)
+#pragma unroll
+          for (int a = 0; a < kAhead; ++a) {
+            float s = 0.0f;
+            for (int v = 0; v < p.tpt / 32; ++v) s += part[a][threadIdx.x / 32 + v];
+            dot[a] = s;
+          }
+        __syncthreads();
+      }
+      if (lead == 0)
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+          if (in && j + a < p.k) d_weight[t * p.k + j + a] = r[a] < end ? dot[a] : 0.0f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxExperts = 4096;
+
+bool bad_rows(int64_t T, int64_t k, int64_t cols, int64_t experts) {
+  return T < 0 || k < 1 || cols < 0 || experts < 1 || experts > kMaxExperts || cols >= (1ll << 31) ||
+         T >= (1ll << 31) || k >= (1ll << 31) || T * k >= (1ll << 31) - 1024;
+}
+
+// as many threads a token as its row has pieces, up to the block
+unsigned plan(RouteParams *p, int vec, int resident, int sms) {
+  const int64_t pieces = dora::ceil_div(p->cols, vec);
+  p->tpt = 1;
+  while (p->tpt < kThreads && p->tpt < pieces) p->tpt *= 2;
+  const int64_t all = dora::ceil_div(p->T, kThreads / p->tpt), most = static_cast<int64_t>(sms) * resident;
+  return static_cast<unsigned>(all < most ? all : most);
+}
+
+template <typename Act>
+dora_status run_send(const void *x, RouteParams p, void *xs, int device, int sms, cudaStream_t cs) {
+  constexpr int V = 16 / sizeof(Act);
+  if (vector_ok<Act>(p.cols, {x, xs})) {
+    const unsigned g = plan(&p, V, resident_blocks<expert_send_kernel<Act, V>>(device), sms);
+    expert_send_kernel<Act, V><<<g, kThreads, 0, cs>>>(static_cast<const Act *>(x), p, static_cast<Act *>(xs));
+  } else {
+    const unsigned g = plan(&p, 1, resident_blocks<expert_send_kernel<Act, 1>>(device), sms);
+    expert_send_kernel<Act, 1><<<g, kThreads, 0, cs>>>(static_cast<const Act *>(x), p, static_cast<Act *>(xs));
+  }
+  dora::count_launches(1);
+  return dora::launch_status();
+}
+
+template <typename Act>
+dora_status run_return(const void *ys, const float *w, RouteParams p, void *y, int device, int sms, cudaStream_t cs) {
+  constexpr int V = 16 / sizeof(Act);
+  if (vector_ok<Act>(p.cols, {ys, y})) {
+    const unsigned g = plan(&p, V, resident_blocks<expert_return_kernel<Act, V>>(device), sms);
+    expert_return_kernel<Act, V><<<g, kThreads, 0, cs>>>(static_cast<const Act *>(ys), w, p, static_cast<Act *>(y));
+  } else {
+    const unsigned g = plan(&p, 1, resident_blocks<expert_return_kernel<Act, 1>>(device), sms);
+    expert_return_kernel<Act, 1><<<g, kThreads, 0, cs>>>(static_cast<const Act *>(ys), w, p, static_cast<Act *>(y));
+  }
+  dora::count_launches(1);
+  return dora::launch_status();
+}
+
+template <typename Act>
+dora_status run_return_bwd(const void *dy, const void *ys, const float *w, RouteParams p, void *d_ys, float *dw,
+                           int device, int sms, cudaStream_t cs) {
+  constexpr int V = 16 / sizeof(Act);
+  const auto *pd = static_cast<const Act *>(dy), *py = static_cast<const Act *>(ys);
+  if (vector_ok<Act>(p.cols, {dy, ys, d_ys})) {
+    const unsigned g = plan(&p, V, resident_blocks<expert_return_bwd_kernel<Act, V>>(device), sms);
+    expert_return_bwd_kernel<Act, V><<<g, kThreads, 0, cs>>>(pd, py, w, p, static_cast<Act *>(d_ys), dw);
+  } else {
+    const unsigned g = plan(&p, 1, resident_blocks<expert_return_bwd_kernel<Act, 1>>(device), sms);
+    expert_return_bwd_kernel<Act, 1><<<g, kThreads, 0, cs>>>(pd, py, w, p, static_cast<Act *>(d_ys), dw);
+  }
+  dora::count_launches(1);
+  return dora::launch_status();
+}
+
+RouteParams params(const int32_t *inverse, const int32_t *offsets, int64_t T, int64_t k, int64_t cols, int64_t experts) {
+  RouteParams p = {};
+  p.T = T;
+  p.cols = cols;
+  p.k = static_cast<int>(k);
+  p.rows = static_cast<uint32_t>(T * k);
+  p.inverse = inverse;
+  p.end = offsets + experts;
+  return p;
+}
+
+bool bad_elem(dora_dtype act, const void *p) { return !dora::aligned(p, act == DORA_BF16 ? 2 : 4); }
+
+}  // namespace
+
+extern "C" dora_status dora_expert_sort(int index_bytes, const void *expert, int64_t T, int64_t k, int64_t experts,
+                                        int32_t *order, int32_t *inverse, int32_t *offsets, dora_stream_t stream) {
+  if (index_bytes != 4 && index_bytes != 8) return DORA_ERR_DTYPE;
+  if (bad_rows(T, k, 0, experts)) return DORA_ERR_SHAPE;
+  if (!offsets || (T > 0 && (!expert || !order || !inverse))) return DORA_ERR_NULL;
+  if (!dora::aligned(expert, index_bytes) || !dora::aligned(order, 4) || !dora::aligned(inverse, 4) ||
+      !dora::aligned(offsets, 4))
+    return DORA_ERR_ALIGN;
+  dora::DeviceInfo info;
+  const dora_status st = dora::current_device(&info, nullptr);
+  if (st != DORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int n = static_cast<int>(T * k), E = static_cast<int>(experts);
+  if (index_bytes == 4)
+    expert_sort_kernel<int32_t><<<E + 1, 32 * kSortWarps, 0, cs>>>(static_cast<const int32_t *>(expert), n, E, order,
+                                                                   inverse, offsets);
+  else
+    expert_sort_kernel<int64_t><<<E + 1, 32 * kSortWarps, 0, cs>>>(static_cast<const int64_t *>(expert), n, E, order,
+                                                                   inverse, offsets);
+  dora::count_launches(1);
+  return dora::launch_status();
+}
+
+extern "C" dora_status dora_expert_send(dora_dtype act, const void *x, const int32_t *inverse, const int32_t *offsets,
+                                        int64_t T, int64_t k, int64_t cols, int64_t experts, void *xs,
+                                        dora_stream_t stream) {
+  if (!valid_dtype(act)) return DORA_ERR_DTYPE;
+  if (bad_rows(T, k, cols, experts)) return DORA_ERR_SHAPE;
+  if (T == 0 || cols == 0) return DORA_OK;
+  if (!x || !inverse || !offsets || !xs) return DORA_ERR_NULL;
+  if (bad_elem(act, x) || bad_elem(act, xs) || !dora::aligned(inverse, 4) || !dora::aligned(offsets, 4))
+    return DORA_ERR_ALIGN;
+  dora::DeviceInfo info;
+  int device = 0;
+  const dora_status st = dora::current_device(&info, &device);
+  if (st != DORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const RouteParams p = params(inverse, offsets, T, k, cols, experts);
+  return act == DORA_BF16 ? run_send<__nv_bfloat16>(x, p, xs, device, info.sms, cs)
+                          : run_send<float>(x, p, xs, device, info.sms, cs);
+}
+
+extern "C" dora_status dora_expert_return(dora_dtype act, const void *ys, const int32_t *inverse, const int32_t *offsets,
+                                          const float *weight, int64_t T, int64_t k, int64_t cols, int64_t experts,
+                                          void *y, dora_stream_t stream) {
+  if (!valid_dtype(act)) return DORA_ERR_DTYPE;
+  if (bad_rows(T, k, cols, experts)) return DORA_ERR_SHAPE;
+  if (T == 0 || cols == 0) return DORA_OK;
+  if (!ys || !inverse || !offsets || !y) return DORA_ERR_NULL;
+  if (bad_elem(act, ys) || bad_elem(act, y) || !dora::aligned(inverse, 4) || !dora::aligned(offsets, 4) ||
+      !dora::aligned(weight, 4))
+    return DORA_ERR_ALIGN;
+  dora::DeviceInfo info;
+  int device = 0;
+  const dora_status st = dora::current_device(&info, &device);
+  if (st != DORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const RouteParams p = params(inverse, offsets, T, k, cols, experts);
+  return act == DORA_BF16 ? run_return<__nv_bfloat16>(ys, weight, p, y, device, info.sms, cs)
+                          : run_return<float>(ys, weight, p, y, device, info.sms, cs);
+}
+
+extern "C" dora_status dora_expert_return_bwd(dora_dtype act, const void *dy, const void *ys, const int32_t *inverse,
+                                              const int32_t *offsets, const float *weight, int64_t T, int64_t k,
+                                              int64_t cols, int64_t experts, void *d_ys, float *d_weight,
+                                              dora_stream_t stream) {
+  if (!valid_dtype(act)) return DORA_ERR_DTYPE;
+  if (bad_rows(T, k, cols, experts)) return DORA_ERR_SHAPE;
+  if (T == 0) return DORA_OK;
+  if (!inverse || !offsets || !weight || !d_weight || (cols > 0 && (!dy || !ys || !d_ys))) return DORA_ERR_NULL;
+  if (bad_elem(act, dy) || bad_elem(act, ys) || bad_elem(act, d_ys) || !dora::aligned(inverse, 4) ||
+      !dora::aligned(offsets, 4) || !dora::aligned(weight, 4) || !dora::aligned(d_weight, 4))
+    return DORA_ERR_ALIGN;
+  dora::DeviceInfo info;
+  int device = 0;
+  const dora_status st = dora::current_device(&info, &device);
+  if (st != DORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const RouteParams p = params(inverse, offsets, T, k, cols, experts);
+  return act == DORA_BF16 ? run_return_bwd<__nv_bfloat16>(dy, ys, weight, p, d_ys, d_weight, device, info.sms, cs)
+                          : run_return_bwd<float>(dy, ys, weight, p, d_ys, d_weight, device, info.sms, cs);
+}
