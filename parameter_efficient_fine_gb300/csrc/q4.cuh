@@ -74,7 +74,7 @@ __device__ __forceinline__ void q4_bf16x8(uint32_t w, uint32_t factor, uint32_t 
   out[3] = q4_mul2(((hi << 4) & 0x80008000u) | ((hi >> 2) & 0x01c001c0u), factor);
 }
 // a group's 32 values
-__device__ __forceinline__ void q4_bf16x32(uint4 w, uint32_t byte, uint32_t (&out)[16]) {
+__device__ __forceinline__ void q4_bf16x32(uint4 w, uint32_t byte, uint32_t *out) {
   const uint32_t f = q4_factor(byte);
   q4_bf16x8(w.x, f, out);
   q4_bf16x8(w.y, f, out + 4);

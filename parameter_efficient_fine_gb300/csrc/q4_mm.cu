@@ -8,18 +8,20 @@
 // offsets[e] to offsets[e + 1] meet W[e].
 //
 // The features are the M side, the tokens the N side.  A block of W, 128 rows of
-// it by 128 columns, arrives as it is stored (8 KB), is turned into bf16 by
-// conversion warps and lies in shared memory as two panels of 128 rows x 64
-// columns, 128 bytes a row, swizzled.  For x W^T its rows are features and the
-// panels K-major, for dy W its rows are k and the panels M-major: one conversion
-// serves both, and only the descriptors differ.
+// it by 128 columns, arrives as it is stored (8 KB) and is turned into bf16 by
+// conversion warps, 64 k at a time.  For x W^T its rows are features: they go to
+// tensor memory, a lane each, from where the tensor core takes them as its A
+// operand.  For dy W its rows are k: they go to shared memory as two panels of 64
+// rows x 64 features, 128 bytes a row, swizzled, read M-major.  Neither makes a
+// transposed copy.
 //
 // CTA pairs (tcgen05.mma.cta_group::2): tiles of 256 features by up to 256 tokens,
 // each CTA converting its 128 features and staging half of the tokens.
-//   warp 0       TMA: blocks of W into a ring of their own, tokens into the stages
+//   warp 0       TMA: tokens into the stages
 //   warp 1       tensor memory, MMA issue (even CTA)
-//   warps 2-9    conversion: a row and a panel each thread
-//   warps 10-17  the result
+//   warp 2       TMA: blocks of W into a ring of their own
+//   warps 3-10   conversion, two groups, each one half of every block's k
+//   warps 11-18  the result
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -35,25 +37,37 @@
 
 namespace {
 
-constexpr int kKB = 128;                              // k per stage, and the side of a block of W
+constexpr int kKB = 128;                              // the side of a block of W
+constexpr int kKS = 64;                               // k per stage
 constexpr int kTileF = 256;                           // features per tile
 constexpr int kTileT = 256;                           // most tokens per tile
-constexpr int kRaw = 4;                               // blocks of W in flight
 constexpr unsigned kRawBytes = 128 * kKB / 2;         // 8 KB
-constexpr unsigned kPanel = 128 * 128;                // 16 KB: 128 rows of 64 bf16
-constexpr int kConvWarps = 8, kOutWarps = 8;
-constexpr int kThreadsMm = 32 * (2 + kConvWarps + kOutWarps);
+constexpr unsigned kPanel = kKS * 128;                // 8 KB: 64 rows of 64 bf16
+constexpr int kGroups = 2, kGroupWarps = 4;           // conversion
+constexpr int kConvWarps = kGroups * kGroupWarps, kOutWarps = 8;
+constexpr int kConv0 = 3, kOut0 = kConv0 + kConvWarps;
+constexpr int kThreadsMm = 32 * (kOut0 + kOutWarps);
+constexpr int kAhead = 4;                             // blocks whose scales are on their way
+constexpr uint32_t kACol = 256;                       // x W^T: first column of the converted W
 constexpr int64_t kMaxExperts = 4096;
 // half of the tile's tokens, 64 k
 __host__ __device__ constexpr unsigned tok_box(int ntok) { return static_cast<unsigned>(ntok / 2 * 128); }
-__host__ __device__ constexpr unsigned stage_size(int ntok) { return 2 * (kPanel + tok_box(ntok)); }
+template <bool TRANS> __host__ __device__ constexpr unsigned stage_size(int ntok) {
+  return (TRANS ? 2 * kPanel : 0) + tok_box(ntok);
+}
+// stages and blocks of W in flight.  x W^T: a stage is 32 columns of tensor memory,
+// of which the accumulator leaves 256
+template <bool TRANS> constexpr int kStages = TRANS ? 6 : 8;
+template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 8;
+// a group converts every kGroups-th stage, so it visits every use of its slots in turn
+static_assert(kStages<false> % kGroups == 0 && kStages<true> % kGroups == 0, "slots of a group");
 
 struct Q4Params {
   int T, out, in;
   int nfeat, kdim;                  // features of the result, k
   int experts;
   const int *offsets;               // null: one weight, all rows
-  int ntok, stages;                 // tokens per tile, ring
+  int ntok;                         // tokens per tile
   int ftiles;
   int64_t tiles;                    // no more than these
   const uint8_t *scale;
@@ -166,6 +180,47 @@ __device__ __forceinline__ uint32_t load_now16(const uint8_t *p) {
   return v;
 }
 
+// D (+)= A B over the pair, A of each CTA in its tensor memory
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// 32 consecutive 32-bit columns of this thread's tensor-memory lane
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+// arrive on an mbarrier of the pair after writes to this CTA's shared memory, which
+// the tensor core of this SM reads; they are ordered before it by fence_async_proxy
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// the accumulators: for x W^T the converted W leaves 256 columns, two of 128 tokens
+// or one of more
+struct Acc {
+  int n, stride, i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Acc(bool trans, int ntok) : n(trans || ntok <= 128 ? 2 : 1), stride(trans ? 256 : 128) {}
+  __device__ __forceinline__ uint32_t column() const { return static_cast<uint32_t>(i * stride); }
+  __device__ __forceinline__ void next() {
+    if (++i == n) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 // M-major panels: 64 features a row of 128 bytes, k down the rows, the panel of the
 // next 64 features kPanel further
 __device__ __forceinline__ uint64_t sdesc_mmajor(uint32_t saddr) {
@@ -175,26 +230,26 @@ __device__ __forceinline__ uint64_t sdesc_mmajor(uint32_t saddr) {
 template <bool TRANS>
 __global__ void __launch_bounds__(kThreadsMm, 1)
 q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p) {
+  constexpr int S = kStages<TRANS>, R = kRaw<TRANS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int S = p.stages;
-  const uint32_t xbox = tok_box(p.ntok), stage_bytes = stage_size(p.ntok);
+  const uint32_t xbox = tok_box(p.ntok), stage_bytes = stage_size<TRANS>(p.ntok);
   uint8_t *raw = smem + S * stage_bytes;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(raw + kRaw * kRawBytes);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(raw + R * kRawBytes);
   // barriers (a pair uses the even CTA's full and accumulator empty): tokens full,
   // W converted, empty; raw full and empty; accumulator full and empty; end
   const uint32_t tfull0 = smem_u32(bars), wfull0 = tfull0 + 8u * S, empty0 = wfull0 + 8u * S, rfull0 = empty0 + 8u * S,
-                 rempty0 = rfull0 + 8u * kRaw, accf = rempty0 + 8u * kRaw, acce = accf + 16, fin = acce + 16;
-  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 3 * S + 2 * kRaw + 5);
+                 rempty0 = rfull0 + 8u * R, accf = rempty0 + 8u * R, acce = accf + 16, fin = acce + 16;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 3 * S + 2 * R + 5);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(tfull0 + 8u * s, 1);
-      mbar_init(wfull0 + 8u * s, 2 * kConvWarps);
+      mbar_init(wfull0 + 8u * s, 2 * kGroupWarps);
       mbar_init(empty0 + 8u * s, 1);
     }
-    for (int s = 0; s < kRaw; ++s) {
+    for (int s = 0; s < R; ++s) {
       mbar_init(rfull0 + 8u * s, 1);
       mbar_init(rempty0 + 8u * s, kConvWarps);
     }
@@ -221,17 +276,45 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   pdl_trigger();
   pdl_wait();       // the set-up above overlaps the end of the launch before
   const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
-  const int kstages = (p.kdim + kKB - 1) / kKB;
+  const int blocks = (p.kdim + kKB - 1) / kKB;     // of W, two stages each
   Tile o;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    bool ok = !loads_withheld(p.guard);
-    bool issued = false;
-    Ring st(S), rw(kRaw);
+    // ---------------------------------------------------------------- tokens
+    bool ok = !loads_withheld(p.guard), issued = false;
+    Ring st(S);
     for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
-      const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128, t0 = o.t0 + static_cast<int>(rank) * (p.ntok / 2);
-      for (int s = 0; s < kstages; ++s) {
+      const int t0 = o.t0 + static_cast<int>(rank) * (p.ntok / 2);
+      for (int s = 0; s < 2 * blocks; ++s) {
+        ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 62);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t fb = tfull0 + 8u * st.i;
+          // the even CTA's barrier counts both CTAs' bytes
+          if (rank == 0) mbar_expect_tx(fb, 2 * xbox);
+          tma_load_2d_pair(smem_u32(smem) + (st.i + 1) * stage_bytes - xbox, &mX, s * kKS, t0, mapa_shared(fb, 0));
+        }
+        __syncwarp();
+        issued = true;
+        st.next();
+      }
+    }
+    if (!ok && issued) {
+      // copies in flight, whose barrier may never complete after an abort: they
+      // land within microseconds, wait 1 ms
+      const unsigned long long c0 = globaltimer();
+      while (globaltimer() - c0 < 1000000ull) {
+      }
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- blocks of W
+    bool ok = !loads_withheld(p.guard);
+    int issued = 0;
+    Ring rw(R);
+    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+      const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
+      for (int s = 0; s < blocks; ++s) {
         ok = guard_wait(rempty0 + 8u * rw.i, rw.phase ^ 1u, ctl, p.guard, 61);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -243,58 +326,49 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           else tma_load_3d(at, &mW, s * (kKB / 2), f0, o.e, fb);
         }
         __syncwarp();
-        issued = true;
+        ++issued;
         rw.next();
-        ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 62);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (elect_one()) {
-          const uint32_t fb = tfull0 + 8u * st.i, lb = mapa_shared(fb, 0);
-          const uint32_t at = smem_u32(smem) + st.i * stage_bytes + 2 * kPanel;
-          // the even CTA's barrier counts both CTAs' bytes
-          if (rank == 0) mbar_expect_tx(fb, 4 * xbox);
-          tma_load_2d_pair(at, &mX, s * kKB, t0, lb);
-          tma_load_2d_pair(at + xbox, &mX, s * kKB + 64, t0, lb);
+      }
+    }
+    if (!ok)
+      for (int k = 0; k < R && k < issued; ++k) {   // copies in flight
+        if (--rw.i < 0) {
+          rw.i = R - 1;
+          rw.phase ^= 1u;
         }
-        __syncwarp();
-        st.next();
+        wait_drain_ns(rfull0 + 8u * rw.i, rw.phase, kWaitNs);
       }
-    }
-    if (!ok && issued) {
-      // copies in flight, whose barrier may never complete after an abort: they
-      // land within microseconds, wait 1 ms
-      const unsigned long long c0 = globaltimer();
-      while (globaltimer() - c0 < 1000000ull) {
-      }
-    }
   } else if (warp == 1) {
     if (rank == 0) {
       // ---------------------------------------------------------------- MMA issuer
       // (a commit arrives on the barrier of this CTA and on the peer's)
       bool ok = true;
-      Ring st(S), acc(2);
+      Ring st(S);
+      Acc acc(TRANS, p.ntok);
       const uint32_t peer_off = mapa_shared(tfull0, peer) - tfull0;   // to the peer's copy of a barrier
       const uint32_t id = idesc_bf16_pair(p.ntok) | (TRANS ? 1u << 15 : 0u);
       for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
         ok = guard_wait(acce + 8u * acc.i, acc.phase ^ 1u, ctl, p.guard, 63);
-        const uint32_t d = tmem + static_cast<uint32_t>(acc.i) * kTileT;
-        for (int s = 0; s < kstages; ++s) {
+        const uint32_t d = tmem + acc.column();
+        for (int s = 0; s < 2 * blocks; ++s) {
           ok = ok && guard_wait(tfull0 + 8u * st.i, st.phase, ctl, p.guard, 64);
           ok = ok && guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 65);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = smem_u32(smem) + st.i * stage_bytes;
-          const uint64_t a = TRANS ? sdesc_mmajor(at) : sdesc<32>(at), b = sdesc<32>(at + 2 * kPanel);
+          const uint64_t b = sdesc<32>(at + stage_bytes - xbox);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              // 16 k: 32 bytes along a K-major row, or 16 rows of an M-major panel
-              mma_bf16_ss_pair(d, TRANS ? a + 128u * k : a + (kPanel >> 4) * (k / 4) + 2u * (k % 4),
-                               b + (xbox >> 4) * (k / 4) + 2u * (k % 4), id, s != 0 || k != 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t more = s != 0 || k != 0 ? 1u : 0u;
+              // 16 k: 32 bytes along a K-major row, 16 rows of an M-major panel, 8 columns
+              if (TRANS) mma_bf16_ss_pair(d, sdesc_mmajor(at) + 128u * k, b + 2u * k, id, more);
+              else mma_bf16_ts_pair(d, tmem + kACol + 32u * st.i + 8u * k, b + 2u * k, id, more);
+            }
             mma_commit_pair(empty0 + 8u * st.i);
             mma_commit_pair(empty0 + 8u * st.i + peer_off);
-            if (s + 1 == kstages) {
+            if (s + 1 == 2 * blocks) {
               mma_commit_pair(accf + 8u * acc.i);
               mma_commit_pair(accf + 8u * acc.i + peer_off);
             }
@@ -309,68 +383,82 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       }
       __syncwarp();
     }
-  } else if (warp < 2 + kConvWarps) {
+  } else if (warp < kOut0) {
     // ---------------------------------------------------------------- conversion
-    const int panel = (warp - 2) / 4, r = ((warp - 2) % 4) * 32 + lane;
+    // group g: the g-th half of every block's k, 64 values a thread
+    const int g = (warp - kConv0) / kGroupWarps, i = (warp & 3) * 32 + lane;
+    const int r = TRANS ? kKS * g + (i & 63) : i, panel = TRANS ? i >> 6 : g;    // row of the block, half of it
     const int G = p.in / kQ4Group;
     const bool words = G % 2 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 1) == 0;
-    const uint32_t from = smem_u32(raw) + static_cast<uint32_t>(r) * 64u, to = smem_u32(smem) + panel * kPanel + r * 128u;
-    const uint32_t c0 = static_cast<uint32_t>((2 * panel) ^ ((r >> 1) & 3)) * 16u,
-                   c1 = static_cast<uint32_t>((2 * panel + 1) ^ ((r >> 1) & 3)) * 16u;
+    const uint32_t from = smem_u32(raw) + static_cast<uint32_t>(r) * 64u;
+    const uint32_t c0 = static_cast<uint32_t>((2 * panel) ^ ((r >> 1) & 3)) * 16u, c1 = c0 ^ 16u;
+    const uint32_t to = TRANS ? smem_u32(smem) + panel * kPanel + (i & 63) * 128u
+                              : tmem + kACol + (static_cast<uint32_t>(warp & 3) * 32u << 16);
     bool ok = true;
-    Ring st(S), rw(kRaw);
+    Ring st(S), rw(R);
+    if (g == 1) st.next();
     for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
       // the two scale bytes of this thread's part of block s
       auto scales = [&](int s) -> uint32_t {
-        const int row = TRANS ? s * kKB + r : f0 + r, g = (TRANS ? f0 : s * kKB) / kQ4Group + 2 * panel;
-        if (row >= p.out || g >= G) return 0x7f7fu;
-        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + row) * G + g;
+        const int row = TRANS ? s * kKB + r : f0 + r, q = (TRANS ? f0 : s * kKB) / kQ4Group + 2 * panel;
+        if (row >= p.out || q >= G) return 0x7f7fu;
+        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + row) * G + q;
         if (words) return load_now16(at);
-        return load_now(at) | (g + 1 < G ? load_now(at + 1) : 127u) << 8;
+        return load_now(at) | (q + 1 < G ? load_now(at + 1) : 127u) << 8;
       };
-      uint32_t sc[kRaw];
+      uint32_t sc[kAhead];
 #pragma unroll
-      for (int u = 0; u < kRaw; ++u) sc[u] = u < kstages ? scales(u) : 0u;
-      for (int s0 = 0; s0 < kstages && ok; s0 += kRaw) {
+      for (int u = 0; u < kAhead; ++u) sc[u] = u < blocks ? scales(u) : 0u;
+      for (int s0 = 0; s0 < blocks && ok; s0 += kAhead) {
 #pragma unroll
-        for (int u = 0; u < kRaw; ++u) {
+        for (int u = 0; u < kAhead; ++u) {
           const int s = s0 + u;
-          if (s >= kstages || !ok) break;
+          if (s >= blocks || !ok) break;
           const uint32_t b = sc[u];
-          if (s + kRaw < kstages) sc[u] = scales(s + kRaw);
+          if (s + kAhead < blocks) sc[u] = scales(s + kAhead);
           ok = guard_wait(rfull0 + 8u * rw.i, rw.phase, ctl, p.guard, 66);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint4 w0 = lds128(from + rw.i * kRawBytes + c0), w1 = lds128(from + rw.i * kRawBytes + c1);
-          uint32_t v[2][16];
-          q4_bf16x32(w0, b & 255u, v[0]);
-          q4_bf16x32(w1, b >> 8, v[1]);
+          uint32_t v[32];
+          q4_bf16x32(w0, b & 255u, v);
+          q4_bf16x32(w1, b >> 8, v + 16);
           __syncwarp();
           if (lane == 0) mbar_arrive(rempty0 + 8u * rw.i);
           ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 67);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint32_t dst = to + st.i * stage_bytes;
+          if (TRANS) {
+            const uint32_t dst = to + st.i * stage_bytes;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) sts128(dst + static_cast<uint32_t>((c ^ (r & 7)) * 16), &v[c / 4][(c % 4) * 4]);
-          fence_async_proxy();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(wfull0 + 8u * st.i, 0));
+            for (int c = 0; c < 8; ++c) sts128(dst + static_cast<uint32_t>((c ^ (r & 7)) * 16), v + 4 * c);
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(mapa_shared(wfull0 + 8u * st.i, 0));
+          } else {
+            tc_fence_after();
+            tmem_st32(to + 32u * st.i, v);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(wfull0 + 8u * st.i, 0));
+          }
           rw.next();
+          st.next();
           st.next();
         }
       }
     }
   } else {
     // ---------------------------------------------------------------- result
-    const int e = warp - 2 - kConvWarps;
+    const int e = warp - kOut0;
     const uint32_t quad = static_cast<uint32_t>(warp & 3);
     const int half = p.ntok / 2;                   // tokens of this warp, from c0
     const int c0 = (e >> 2) * half;
     const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
     bool ok = true;
-    Ring acc(2);
+    Acc acc(TRANS, p.ntok);
     for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
       ok = guard_wait(accf + 8u * acc.i, acc.phase, ctl, p.guard, 68);
       ok = __all_sync(0xffffffffu, ok);
@@ -381,7 +469,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       for (int c = 0; c < kTileT / 2; c += 8)
         if (c < half) {
           float f[8];
-          tmem_ld<8>(lane_addr + acc.i * kTileT + static_cast<uint32_t>(c), f);
+          tmem_ld<8>(lane_addr + acc.column() + static_cast<uint32_t>(c), f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[c / 2 + i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
         }
@@ -417,15 +505,15 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-constexpr size_t kFixed = 1024 + kRaw * kRawBytes + 512;
-constexpr int pair_stages(int ntok) {
-  const int s = static_cast<int>((kSmemMax - kFixed) / stage_size(ntok));
-  return s < 6 ? s : 6;
+template <bool TRANS> constexpr size_t pair_smem(int ntok) {
+  return 1024 + kRaw<TRANS> * kRawBytes + 512 + kStages<TRANS> * static_cast<size_t>(stage_size<TRANS>(ntok));
 }
-constexpr size_t pair_smem(int ntok) { return kFixed + static_cast<size_t>(pair_stages(ntok)) * stage_size(ntok); }
-static_assert(pair_stages(kTileT) >= 3 && 8 * (3 * 6 + 2 * kRaw + 5) + sizeof(SharedCtl) <= 512,
-              "ring, barriers and control words");
+template <bool TRANS> constexpr bool fits() {
+  return pair_smem<TRANS>(kTileT) <= kSmemMax && 8 * (3 * kStages<TRANS> + 2 * kRaw<TRANS> + 5) + sizeof(SharedCtl) <= 512;
+}
+static_assert(fits<false>() && fits<true>(), "rings, barriers and control words");
 
+template <bool TRANS>
 void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ntok, int64_t pairs, cudaStream_t cs) {
   *cfg = cudaLaunchConfig_t{};
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -436,7 +524,7 @@ void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ntok, i
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg->gridDim = dim3(2 * static_cast<unsigned>(pairs));
   cfg->blockDim = dim3(kThreadsMm);
-  cfg->dynamicSmemBytes = pair_smem(ntok);
+  cfg->dynamicSmemBytes = pair_smem<TRANS>(ntok);
   cfg->stream = cs;
   cfg->attrs = attr;
   cfg->numAttrs = 2;
@@ -451,7 +539,7 @@ int resident_pairs(int device, int sms) {
   if (known[device] == 0) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    pair_config(&cfg, attr, kTileT, sms / 2, nullptr);
+    pair_config<false>(&cfg, attr, kTileT, sms / 2, nullptr);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, q4_pair_kernel<false>, &cfg) != cudaSuccess) {
       cudaGetLastError();
@@ -514,13 +602,12 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
       p.ntok = n;
     }
   }
-  p.stages = pair_stages(p.ntok);
   p.tiles = p.ftiles * (offsets ? T / p.ntok + groups : dora::ceil_div(T, p.ntok));
   CUtensorMap mW, mX;
   if (!map_w(&mW, wq, experts, out, in) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.ntok / 2, 128)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  pair_config(&cfg, attr, p.ntok, p.tiles < pairs ? p.tiles : pairs, reinterpret_cast<cudaStream_t>(stream));
+  pair_config<TRANS>(&cfg, attr, p.ntok, p.tiles < pairs ? p.tiles : pairs, reinterpret_cast<cudaStream_t>(stream));
   if (cudaLaunchKernelEx(&cfg, q4_pair_kernel<TRANS>, mW, mX, p) != cudaSuccess) {
     cudaGetLastError();
     return DORA_ERR_CUDA;
