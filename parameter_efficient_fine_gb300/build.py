@@ -19,8 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libdora.so")
 SOURCES = ("abi.cu", "compose.cu", "norm.cu", "fused.cu", "q8.cu", "q8_mm.cu", "q8_grad.cu",
-           "q4.cu", "q4_mm.cu", "route.cu")
-HEADERS = ("common.cuh", "tc_ptx.cuh", "stream.cuh", "q8.cuh", "q8_tc.cuh", "q4.cuh")
+           "q4.cu", "q4_mm.cu", "q4_few.cu", "route.cu")
+HEADERS = ("common.cuh", "tc_ptx.cuh", "stream.cuh", "q8.cuh", "q8_tc.cuh", "q4.cuh", "q4_mm.cuh")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,0 +1,410 @@
+// x W^T of few tokens with a weight in 4 bits (see q4.cuh for the form) on the
+// tensor cores of GB300 (sm_103a), without turning W into anything.
+//
+// tcgen05.mma kind::mxf8f6f4 takes E2M1 beside E4M3 and multiplies every 32 k of a
+// row of either operand by a power of two, which is W's form.  x, a bf16, becomes
+// two E4M3 pieces with a scale per 32 columns: h = E4M3(x / s), s the power of two
+// that brings the group's largest magnitude to at most 448, and E4M3((x / s - h) 16)
+// with the scale s / 16.  8 bits less the 4 of h leave 4, so x / s is their sum
+// exactly down to 2^-6, and within 2^-14 below: an error of at most 2^-21 of the
+// group's largest magnitude, as the fp32 sum itself makes.
+//
+// The features are the M side, the tokens' pieces the N side (NT first pieces, NT
+// second ones).  A tile of 128 features and up to NT tokens is a cluster of CTAs
+// that share its k range and meet in distributed shared memory, summed in rank
+// order.
+//   warps 0-3   x into pieces, scale words into tensor memory (each warp its lane
+//               quadrant); then the result out of it
+//   warp 4      tensor memory, MMA issue (four 32-wide steps per 128 k)
+//   warps 5-6   W: 16 values, 8 bytes, to every 16 bytes of shared memory, the
+//               layout that the tensor core takes 4-bit values in
+// Every wait on a shared-memory barrier is bounded; a wait that gives up records
+// a code in the library's device error word and all roles leave.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "q4.cuh"
+#include "q4_mm.cuh"
+#include "q8.cuh"
+#include "q8_tc.cuh"
+#include "tc_ptx.cuh"
+
+namespace {
+
+constexpr int kKB = 128;                    // k per stage
+constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB of shared memory, 8 of W
+constexpr int kTokWarps = 4, kMmaWarp = 4, kWWarps = 2;
+constexpr int kFewThreads = 32 * (kTokWarps + 1 + kWWarps);
+constexpr int kMaxCluster = 8;              // the portable limit
+constexpr int kFewCols = 128, kSfCol = 64, kSfStride = 8;   // tensor memory: scale words, 4 columns of W's and 2 of x's a stage
+
+template <int NT> constexpr unsigned kXBytes = 2 * NT * kKB;
+template <int NT> constexpr unsigned kStage = kWBytes + kXBytes<NT>;
+// two CTAs an SM: half of the shared memory each
+template <int NT> constexpr int kFewStages = static_cast<int>((kSmemMax / 2 - 3072) / kStage<NT>) < 6
+                                                 ? static_cast<int>((kSmemMax / 2 - 3072) / kStage<NT>) : 6;
+
+// the 4 W scale bytes of 128 k from column k, a byte each; 1 past the last
+__device__ __forceinline__ uint32_t scale_word(const uint8_t *row, int g, int groups, bool words) {
+  if (words) return load_now(reinterpret_cast<const uint32_t *>(row + g));
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= (g + i < groups ? load_now(row + g + i) : 127u) << (8 * i);
+  return w;
+}
+__device__ __forceinline__ uint2 load_now2(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+// 8 bytes into shared memory, zeros where `bytes` is 0
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// barrier 1 of `THREADS` threads, and whether `v` holds in all of them
+template <int THREADS> __device__ __forceinline__ bool all_of(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.b32 a, %1, 0;\n\t"
+      "bar.red.and.pred b, 1, %2, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(THREADS)
+      : "memory");
+  return r != 0;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p, const __nv_bfloat16 *x, const uint8_t *wq) {
+  constexpr int S = kFewStages<NT>, N = 2 * NT;
+  constexpr int kMine = NT / kTokWarps;     // tokens a warp splits
+  constexpr int kXCols = (N + 31) / 32;
+  static_assert(NT % 8 == 0 && kXCols <= 2 && S * kSfStride + kSfCol <= kFewCols, "tensor memory");
+  static_assert(NT * kTcM * 4 <= S * kStage<NT>, "the parts lie in the stages");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint32_t *words = reinterpret_cast<uint32_t *>(smem + S * kStage<NT>);   // x's scale words, [S][N]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(words + S * N);
+  const uint32_t wfull0 = smem_u32(bars), xfull0 = wfull0 + 8u * S, empty0 = xfull0 + 8u * S, accf = empty0 + 8u * S;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 3 * S + 1);
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(wfull0 + 8u * s, kWWarps);
+      mbar_init(xfull0 + 8u * s, kTokWarps);
+      mbar_init(empty0 + 8u * s, 1);
+    }
+    mbar_init(accf, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_alloc(smem_u32(&ctl->tmem_base), kFewCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  uint32_t csize;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const uint32_t rank = cluster_ctarank();
+  pdl_trigger();
+  pdl_wait();       // the set-up above overlaps the end of the launch before
+
+  Tile o = {};
+  const bool work = find_tile(p, blockIdx.x / csize, &o);   // all of a cluster alike
+  const int blocks = (p.kdim + kKB - 1) / kKB;
+  // at least one block: a cluster has no more CTAs than there are
+  const int kb0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / csize);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / csize);
+  const int ntok = o.t1 - o.t0, f0 = o.ft * kTcM;
+  bool ok = true;
+
+  if (!work) {
+    // no tile for this cluster
+  } else if (warp > kMmaWarp) {
+    // ---------------------------------------------------------------- W
+    const int i = threadIdx.x - 32 * (kMmaWarp + 1), r = i / 8, c = i % 8;   // first row, piece of 16 values
+    const int64_t ld = p.in / 2;
+    const uint8_t *src = wq + (static_cast<int64_t>(o.e) * p.out + f0 + r) * ld + 8 * c;
+    const uint32_t dst = smem_u32(smem) + r * 128u + static_cast<uint32_t>((c ^ r) * 16);
+    const int live = p.out - f0 - r;                                         // rows from r that exist
+    ok = !loads_withheld(p.guard);
+    Ring st(S), done(S);
+    for (int kb = kb0; kb < kb1 && ok; ++kb) {
+      ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 71);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const bool in = kb * kKB + 16 * c < p.in;
+#pragma unroll
+      for (int j = 0; j < kTcM / 8; ++j) {
+        const bool has = in && 8 * j < live;
+        copy8(dst + st.i * kStage<NT> + j * 1024u, has ? src + 8 * j * ld + kb * (kKB / 2) : wq, has ? 8u : 0u);
+      }
+      copy_commit();
+      st.next();
+      if (kb - kb0 >= S - 1) {
+        // the oldest of S stages is here
+        copy_wait<S - 1>();
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(wfull0 + 8u * done.i);
+        done.next();
+      }
+    }
+    copy_wait<0>();
+    fence_async_proxy();
+    __syncwarp();
+    if (lane == 0)
+      while (done.i != st.i || done.phase != st.phase) {
+        mbar_arrive(wfull0 + 8u * done.i);
+        done.next();
+      }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- MMA issuer
+    Ring st(S);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = guard_wait(xfull0 + 8u * st.i, st.phase, ctl, p.guard, 72);
+      ok = ok && guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 73);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t at = smem_u32(smem) + st.i * kStage<NT>;
+      const uint64_t a = sdesc<32>(at), b = sdesc<32>(at + kWBytes);
+      const uint32_t sf = tmem + kSfCol + kSfStride * st.i;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_q8(tmem, a + 2u * k, b + 2u * k, idesc_q8(kTcM, N, k, false) | 5u << 7 /* A: E2M1 */, sf, sf + 4,
+                 kb != kb0 || k != 0 ? 1u : 0u);
+        mma_commit(empty0 + 8u * st.i);
+      }
+      __syncwarp();
+      st.next();
+    }
+    if (elect_one()) {
+      mma_commit(accf);
+      wait_drain_ns(accf, 0, kWaitNs);   // every MMA issued is done before this CTA's memory is given back
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- x and the scales
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp) * 32u << 16);
+    const int G = p.in / kQ4Group;
+    const bool quads = G % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3) == 0;
+    const uint8_t *srow[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int f = f0 + 32 * j + lane;
+      srow[j] = f < p.out ? p.scale + (static_cast<int64_t>(o.e) * p.out + f) * G : nullptr;
+    }
+    struct Next {
+      uint32_t s[4];
+      uint2 x[kMine];
+    };
+    auto fetch = [&](int kb, Next *n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n->s[j] = srow[j] ? scale_word(srow[j], 4 * kb, G, quads) : 0x7f7f7f7fu;
+      const int k = kb * kKB + 4 * lane;
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int t = warp + kTokWarps * j;
+        n->x[j] = t < ntok && k < p.in ? load_now2(x + static_cast<int64_t>(o.t0 + t) * p.in + k) : make_uint2(0, 0);
+      }
+    };
+    constexpr int kDeep = 2;                 // blocks of x and scales on their way
+    Next nx[kDeep];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u)
+      if (kb0 + u < kb1) fetch(kb0 + u, &nx[u]);
+    Ring st(S);
+    for (int k0 = kb0; k0 < kb1 && ok; k0 += kDeep) {
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        const int kb = k0 + u;
+        if (kb >= kb1 || !ok) break;
+        const Next cur = nx[u];
+        if (kb + kDeep < kb1) fetch(kb + kDeep, &nx[u]);
+        uint32_t h[kMine], l[kMine], sb[kMine];
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          float v[4] = {__uint_as_float(cur.x[j].x << 16), __uint_as_float(cur.x[j].x & 0xffff0000u),
+                        __uint_as_float(cur.x[j].y << 16), __uint_as_float(cur.x[j].y & 0xffff0000u)};
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = max(m, finite_bits(v[i]));
+          // the group's 8 lanes
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          sb[j] = scale_byte(m);
+          const float inv = scale_inverse(sb[j]);
+          float f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = inf_to_nan(v[i]) * inv;
+          h[j] = quant4(v, 1.0f);
+          dequant4(h[j], 1.0f, f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = v[i] - f[i];
+          l[j] = quant4(f, 16.0f);
+        }
+        ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 74);
+        uint8_t *xs = smem + st.i * kStage<NT> + kWBytes;
+        uint8_t *ws = reinterpret_cast<uint8_t *>(words + st.i * N);
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          if (!ok) break;
+          const int t = warp + kTokWarps * j, at = (((lane >> 2) ^ (t & 7)) * 16) + (lane & 3) * 4;
+          *reinterpret_cast<uint32_t *>(xs + t * 128 + at) = h[j];
+          *reinterpret_cast<uint32_t *>(xs + (NT + t) * 128 + at) = l[j];      // NT % 8 == 0: the same swizzle
+          if ((lane & 7) == 0) {
+            ws[4 * t + (lane >> 3)] = static_cast<uint8_t>(sb[j]);
+            ws[4 * (NT + t) + (lane >> 3)] = static_cast<uint8_t>(sb[j] - 4u);
+          }
+        }
+        fence_async_proxy();
+        // all scale words are there; the four warps go on or leave together
+        ok = all_of<32 * kTokWarps>(ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sf = lane_addr + kSfCol + kSfStride * st.i;
+        const uint32_t w0 = N >= 32 || lane < N ? words[st.i * N + lane] : 0x7f7f7f7fu;
+        const uint32_t w1 = kXCols > 1 ? words[st.i * N + 32 + lane] : 0x7f7f7f7fu;
+        const uint32_t all[8] = {cur.s[0], cur.s[1], cur.s[2], cur.s[3], w0, w1, 0u, 0u};
+        tmem_st8(sf, all);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xfull0 + 8u * st.i);
+        st.next();
+      }
+    }
+    // ---------------------------------------------------------------- result
+    // into shared memory as [token][feature]: the stages are free once the
+    // last MMA is done
+    const bool got = guard_wait(accf, 0, ctl, p.guard, 75);
+    ok = __all_sync(0xffffffffu, got) && ok;
+    tc_fence_after();
+    float *part = reinterpret_cast<float *>(smem);
+    const int f = warp * 32 + lane;
+#pragma unroll
+    for (int c = 0; c < NT; c += 8) {
+      if (c < ntok) {
+        float a[8], b[8];
+        tmem_ld<8>(lane_addr + c, a);
+        tmem_ld<8>(lane_addr + NT + c, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[(c + i) * kTcM + f] = ok ? a[i] + b[i] : 0.0f;
+      }
+    }
+  }
+  tc_fence_before();
+  if (csize > 1) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  if (work) {
+    // the parts of the cluster in rank order, one rounding to bf16: four
+    // features a thread, neighbouring threads on neighbouring features
+    const int quads = ntok * 32;
+    const uint32_t base = smem_u32(smem);
+    for (int i = static_cast<int>(rank) * kFewThreads + threadIdx.x; i < quads; i += static_cast<int>(csize) * kFewThreads) {
+      float4 s = ld_cluster_f32x4(mapa_shared(base + 16u * i, 0));
+      for (uint32_t c = 1; c < csize; ++c) {
+        const float4 v = ld_cluster_f32x4(mapa_shared(base + 16u * i, c));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      const int t = o.t0 + i / 32, f = f0 + 4 * (i % 32);
+      if (f < p.nfeat)
+        *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(t) * p.nfeat + f) =
+            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  }
+  if (csize > 1) cluster_sync();   // no CTA leaves while another reads its part
+  else __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tmem, kFewCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int NT>
+dora_status launch(const void *x, const void *wq, Q4Params p, int cluster, cudaStream_t cs) {
+  constexpr auto kern = &q4_few_kernel<NT>;
+  constexpr size_t smem = 1024 + kFewStages<NT> * (kStage<NT> + 8 * NT) + 8 * (3 * kFewStages<NT> + 1) + sizeof(SharedCtl);
+  static_assert(2 * (smem + 1024) <= kSmemMax + 1024, "two CTAs an SM");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * cluster));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = cs;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, p, static_cast<const __nv_bfloat16 *>(x), static_cast<const uint8_t *>(wq)) != cudaSuccess) {
+    cudaGetLastError();
+    return DORA_ERR_CUDA;
+  }
+  dora::count_launches(1);
+  return DORA_OK;
+}
+
+}  // namespace
+
+namespace dora {
+
+dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
+                          int64_t out, int64_t in, int64_t experts, void *y, cudaStream_t cs) {
+  DeviceInfo info;
+  int device = 0;
+  dora_status st = current_device(&info, &device);
+  if (st != DORA_OK) return st;
+  static const void *const kernels[] = {(const void *)q4_few_kernel<8>, (const void *)q4_few_kernel<16>,
+                                        (const void *)q4_few_kernel<32>};
+  Q4Params p = {};
+  st = tc_init(device, &p.guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
+  if (st != DORA_OK) return st;
+  p.T = static_cast<int>(T);
+  p.out = static_cast<int>(out);
+  p.in = static_cast<int>(in);
+  p.nfeat = p.out;
+  p.kdim = p.in;
+  p.experts = static_cast<int>(experts);
+  p.offsets = offsets;
+  p.scale = static_cast<const uint8_t *>(wscale);
+  p.y = static_cast<__nv_bfloat16 *>(y);
+  const int64_t groups = offsets ? (experts < T ? experts : T) : 1, per = ceil_div(T, groups);
+  p.ntok = per <= 8 ? 8 : per <= 16 ? 16 : 32;
+  p.ftiles = static_cast<int>(ceil_div(out, kTcM));
+  p.tiles = p.ftiles * (offsets ? T / p.ntok + groups : ceil_div(T, p.ntok));
+  // the k range over as many CTAs as keep all clusters resident at two CTAs an SM
+  int cluster = 1;
+  const int64_t blocks = ceil_div(in, kKB);
+  while (cluster < kMaxCluster && p.tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= blocks) cluster *= 2;
+  if (p.tiles * cluster > kMaxDim) return DORA_ERR_SHAPE;
+  switch (p.ntok) {
+    case 8: return launch<8>(x, wq, p, cluster, cs);
+    case 16: return launch<16>(x, wq, p, cluster, cs);
+  }
+  return launch<32>(x, wq, p, cluster, cs);
+}
+
+}  // namespace dora

@@ -32,6 +32,7 @@
 
 #include "common.cuh"
 #include "q4.cuh"
+#include "q4_mm.cuh"
 #include "q8_tc.cuh"
 #include "tc_ptx.cuh"
 
@@ -47,9 +48,9 @@ constexpr int kGroups = 2, kGroupWarps = 4;           // conversion
 constexpr int kConvWarps = kGroups * kGroupWarps, kOutWarps = 8;
 constexpr int kConv0 = 3, kOut0 = kConv0 + kConvWarps;
 constexpr int kThreadsMm = 32 * (kOut0 + kOutWarps);
+constexpr int kFewTok = 32;                           // tokens, or tokens an expert, of q4_few.cu
 constexpr int kAhead = 4;                             // blocks whose scales are on their way
 constexpr uint32_t kACol = 256;                       // x W^T: first column of the converted W
-constexpr int64_t kMaxExperts = 4096;
 // half of the tile's tokens, 64 k
 __host__ __device__ constexpr unsigned tok_box(int ntok) { return static_cast<unsigned>(ntok / 2 * 128); }
 template <bool TRANS> __host__ __device__ constexpr unsigned stage_size(int ntok) {
@@ -62,89 +63,6 @@ template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 8;
 // a group converts every kGroups-th stage, so it visits every use of its slots in turn
 static_assert(kStages<false> % kGroups == 0 && kStages<true> % kGroups == 0, "slots of a group");
 
-struct Q4Params {
-  int T, out, in;
-  int nfeat, kdim;                  // features of the result, k
-  int experts;
-  const int *offsets;               // null: one weight, all rows
-  int ntok;                         // tokens per tile
-  int ftiles;
-  int64_t tiles;                    // no more than these
-  const uint8_t *scale;
-  __nv_bfloat16 *y;
-  Guard guard;
-};
-
-// feature tiles per tile-order group, for reuse in L2
-constexpr int kGroupF = 8;
-
-// what a tile works on
-struct Tile {
-  int e, ft;                        // expert, feature tile
-  int t0, t1;                       // its tokens
-};
-
-// Tile `t`, or false past the last.  All lanes of the warp call it.  Experts: the
-// tokens' tiles of all experts in order, the feature tiles of each in turn.
-__device__ __forceinline__ bool find_tile(const Q4Params &p, int64_t t, Tile *o) {
-  if (!p.offsets) {
-    const int ntiles = (p.T + p.ntok - 1) / p.ntok;
-    if (t >= static_cast<int64_t>(ntiles) * p.ftiles) return false;
-    const int per = kGroupF * ntiles, g = static_cast<int>(t / per), f0 = g * kGroupF, gf = min(kGroupF, p.ftiles - f0),
-              r = static_cast<int>(t - static_cast<int64_t>(g) * per), tt = r / gf;
-    o->e = 0;
-    o->ft = f0 + r - tt * gf;
-    o->t0 = tt * p.ntok;
-    o->t1 = min(p.T, o->t0 + p.ntok);
-    return true;
-  }
-  const int lane = threadIdx.x & 31;
-  const int64_t tt = t / p.ftiles;
-  int64_t before = 0;                                  // token tiles of the experts before this 32
-  for (int e0 = 0; e0 < p.experts; e0 += 32) {
-    const int e = e0 + lane;
-    int a = 0, b = 0;
-    if (e < p.experts) {
-      a = min(max(p.offsets[e], 0), p.T);
-      b = min(max(p.offsets[e + 1], a), p.T);
-    }
-    const int own = (b - a + p.ntok - 1) / p.ntok;
-    int upto = own;                                    // tiles of this 32, up to and with this expert's
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += v;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > tt);
-    if (past) {
-      const int who = __ffs(past) - 1;
-      const int first = __shfl_sync(0xffffffffu, upto - own, who);
-      a = __shfl_sync(0xffffffffu, a, who);
-      b = __shfl_sync(0xffffffffu, b, who);
-      o->e = e0 + who;
-      o->ft = static_cast<int>(t - tt * p.ftiles);
-      o->t0 = a + static_cast<int>(tt - before - first) * p.ntok;
-      o->t1 = min(b, o->t0 + p.ntok);
-      return true;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return false;
-}
-
-// a place in a ring of n
-struct Ring {
-  int n, i = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ explicit Ring(int size) : n(size) {}
-  __device__ __forceinline__ void next() {
-    if (++i == n) {
-      i = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -152,13 +70,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// arrive on an mbarrier of the pair where what it hands over is tensor memory
-// only, which the tcgen05 fence before it orders
-__device__ __forceinline__ void mbar_arrive_pair_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// this thread's writes to shared memory before the tensor core's reads
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -166,13 +77,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t *v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-}
-// loads that stay where they are written (the compiler would move them down to
-// their use, past the wait that they are to overlap)
-__device__ __forceinline__ uint32_t load_now(const uint8_t *p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
 }
 __device__ __forceinline__ uint32_t load_now16(const uint8_t *p) {
   uint16_t v;
@@ -641,6 +545,8 @@ extern "C" dora_status dora_matmul_q4(const void *x, const int32_t *offsets, con
   if (in < 1) return DORA_ERR_SHAPE;
   const dora_status st = check(x, offsets, wq, wscale, T, out, in, experts, y);
   if (st != DORA_OK || T == 0 || out == 0) return st;
+  if (T <= kFewTok * (offsets && experts < T ? experts : 1))
+    return dora::matmul_q4_few(x, offsets, wq, wscale, T, out, in, experts, y, reinterpret_cast<cudaStream_t>(stream));
   return run_matmul<false>(x, offsets, wq, wscale, T, out, in, experts, y, stream);
 }
 

@@ -1,0 +1,100 @@
+// What the two kernels of a product with a 4-bit weight share: the call's
+// parameters and the tiles of it.  Each translation unit gets its own internal copy
+// (anonymous namespace).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "q4.cuh"
+#include "q8_tc.cuh"
+
+namespace {
+
+constexpr int64_t kMaxExperts = 4096;
+
+struct Q4Params {
+  int T, out, in;
+  int nfeat, kdim;                  // features of the result, k
+  int experts;
+  const int *offsets;               // null: one weight, all rows
+  int ntok;                         // tokens per tile
+  int ftiles;
+  int64_t tiles;                    // no more than these
+  const uint8_t *scale;
+  __nv_bfloat16 *y;
+  Guard guard;
+};
+
+// feature tiles per tile-order group, for reuse in L2
+constexpr int kGroupF = 8;
+
+// what a tile works on
+struct Tile {
+  int e, ft;                        // expert, feature tile
+  int t0, t1;                       // its tokens
+};
+
+// Tile `t`, or false past the last.  All lanes of the warp call it.  Experts: the
+// tokens' tiles of all experts in order, the feature tiles of each in turn.
+__device__ __forceinline__ bool find_tile(const Q4Params &p, int64_t t, Tile *o) {
+  if (!p.offsets) {
+    const int ntiles = (p.T + p.ntok - 1) / p.ntok;
+    if (t >= static_cast<int64_t>(ntiles) * p.ftiles) return false;
+    const int per = kGroupF * ntiles, g = static_cast<int>(t / per), f0 = g * kGroupF, gf = min(kGroupF, p.ftiles - f0),
+              r = static_cast<int>(t - static_cast<int64_t>(g) * per), tt = r / gf;
+    o->e = 0;
+    o->ft = f0 + r - tt * gf;
+    o->t0 = tt * p.ntok;
+    o->t1 = min(p.T, o->t0 + p.ntok);
+    return true;
+  }
+  const int lane = threadIdx.x & 31;
+  const int64_t tt = t / p.ftiles;
+  int64_t before = 0;                                  // token tiles of the experts before this 32
+  for (int e0 = 0; e0 < p.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int a = 0, b = 0;
+    if (e < p.experts) {
+      a = min(max(p.offsets[e], 0), p.T);
+      b = min(max(p.offsets[e + 1], a), p.T);
+    }
+    const int own = (b - a + p.ntok - 1) / p.ntok;
+    int upto = own;                                    // tiles of this 32, up to and with this expert's
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > tt);
+    if (past) {
+      const int who = __ffs(past) - 1;
+      const int first = __shfl_sync(0xffffffffu, upto - own, who);
+      a = __shfl_sync(0xffffffffu, a, who);
+      b = __shfl_sync(0xffffffffu, b, who);
+      o->e = e0 + who;
+      o->ft = static_cast<int>(t - tt * p.ftiles);
+      o->t0 = a + static_cast<int>(tt - before - first) * p.ntok;
+      o->t1 = min(b, o->t0 + p.ntok);
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+// this thread's writes to shared memory before the tensor core's reads
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+}  // namespace
+
+namespace dora {
+
+// x W^T of few tokens (q4_few.cu), one launch
+dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
+                          int64_t out, int64_t in, int64_t experts, void *y, cudaStream_t cs);
+
+}  // namespace dora

@@ -92,53 +92,11 @@ struct MmParams {
 // 18.6 us, 19.0 without)
 constexpr CUtensorMapL2promotion kPromote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
 
-// D (+)= A B with a power-of-two scale per row of A and per row of B, E4M3
-// operands in shared memory, scale words in tensor memory
-__device__ __forceinline__ void mma_q8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                       uint32_t sfb, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-      : "memory");
-}
-// instruction descriptor: E4M3 x E4M3, E8M0 scales, fp32 accumulator, M = m,
-// N = n, `byte` of the scale words on both sides, A transposed (M-major) or not
-__device__ __forceinline__ uint32_t idesc_q8(int m, int n, uint32_t byte, bool a_mmajor) {
-  return (byte << 4)                                  // B's scale byte
-         | (a_mmajor ? 1u << 15 : 0u)
-         | (static_cast<uint32_t>(n >> 3) << 17)
-         | (1u << 23)                                 // E8M0 scales
-         | (static_cast<uint32_t>(m >> 4) << 24)
-         | (byte << 29);                              // A's scale byte
-}
 // a box into L2
 __device__ __forceinline__ void prefetch_box_2d(const CUtensorMap *map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y)
                : "memory");
-}
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-// loads that stay where they are written (the compiler would move them down to
-// their use, past the wait that they are to overlap)
-__device__ __forceinline__ uint32_t load_now(const uint32_t *p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t load_now(const uint8_t *p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
 }
 // the scale bytes of k blocks 4 g .. 4 g + 3 of one row of an activation, a
 // byte each; 1 past the last k block
@@ -396,17 +354,6 @@ __device__ __forceinline__ void mma_q8_pair(uint32_t d, uint64_t adesc, uint64_t
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
-}
-// arrive on an mbarrier of the pair where what it hands over is tensor memory
-// only: the tcgen05 fence before it orders that, and a release at cluster scope
-// (a memory fence of about 1500 cycles here) would order nothing more
-__device__ __forceinline__ void mbar_arrive_pair_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
 // the accumulator of a pair's tile: two in turn, or one
 struct Acc {
   int n, i = 0;
@@ -420,19 +367,6 @@ struct Acc {
     }
   }
 };
-// a place in a ring of n
-struct Ring {
-  int n, i = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ explicit Ring(int size) : n(size) {}
-  __device__ __forceinline__ void next() {
-    if (++i == n) {
-      i = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
 template <bool TRANS>
 __global__ void __launch_bounds__(kPairThreads, 1)
 q8_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const MmParams p) {
