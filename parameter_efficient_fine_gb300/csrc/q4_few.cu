@@ -13,11 +13,13 @@
 // second ones).  A tile of 128 features and up to NT tokens is a cluster of CTAs
 // that share its k range and meet in distributed shared memory, summed in rank
 // order.
-//   warps 0-3   x into pieces, scale words into tensor memory (each warp its lane
-//               quadrant); then the result out of it
-//   warp 4      tensor memory, MMA issue (four 32-wide steps per 128 k)
-//   warps 5-6   W: 16 values, 8 bytes, to every 16 bytes of shared memory, the
-//               layout that the tensor core takes 4-bit values in
+//   warps 0-7   x into pieces, in place, scale words into tensor memory (each warp
+//               its lane quadrant), two groups of four taking turns; then the
+//               result out of it
+//   warp 8      tensor memory, MMA issue (four 32-wide steps per 128 k)
+//   warps 9-10  asynchronous copies of W, its scales and x.  W: 16 values, 8 bytes,
+//               to every 16 bytes of shared memory, the layout that the tensor core
+//               takes 4-bit values in
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -35,47 +37,44 @@ namespace {
 
 constexpr int kKB = 128;                    // k per stage
 constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB of shared memory, 8 of W
-constexpr int kTokWarps = 4, kMmaWarp = 4, kWWarps = 2;
-constexpr int kFewThreads = 32 * (kTokWarps + 1 + kWWarps);
+constexpr int kGroups = 2, kTokWarps = 4;   // turns, warps of each
+constexpr int kMmaWarp = kGroups * kTokWarps, kWWarps = 2;
+constexpr int kFewThreads = 32 * (kMmaWarp + 1 + kWWarps);
 constexpr int kMaxCluster = 8;              // the portable limit
 constexpr int kFewCols = 128, kSfCol = 64, kSfStride = 8;   // tensor memory: scale words, 4 columns of W's and 2 of x's a stage
 
 template <int NT> constexpr unsigned kXBytes = 2 * NT * kKB;
 template <int NT> constexpr unsigned kStage = kWBytes + kXBytes<NT>;
-// two CTAs an SM: half of the shared memory each
-template <int NT> constexpr int kFewStages = static_cast<int>((kSmemMax / 2 - 3072) / kStage<NT>) < 6
-                                                 ? static_cast<int>((kSmemMax / 2 - 3072) / kStage<NT>) : 6;
+// two CTAs an SM: half of the shared memory each.  Each group visits every use of its slots
+template <int NT> constexpr int kFewStages = NT == 8 ? 6 : 4;
+static_assert(kFewStages<8> % kGroups == 0 && kFewStages<32> % kGroups == 0, "slots of a group");
 
-// the 4 W scale bytes of 128 k from column k, a byte each; 1 past the last
-__device__ __forceinline__ uint32_t scale_word(const uint8_t *row, int g, int groups, bool words) {
-  if (words) return load_now(reinterpret_cast<const uint32_t *>(row + g));
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (g + i < groups ? load_now(row + g + i) : 127u) << (8 * i);
-  return w;
+// 4, 8 or 16 bytes into shared memory, zeros where `bytes` is 0
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ uint2 load_now2(const void *p) {
-  uint2 v;
-  asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// 8 bytes into shared memory, zeros where `bytes` is 0
 __device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// an arrival on `bar` once this thread's copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// barrier 1 of `THREADS` threads, and whether `v` holds in all of them
-template <int THREADS> __device__ __forceinline__ bool all_of(bool v) {
+// barrier `id` of `THREADS` threads, and whether `v` holds in all of them
+template <int THREADS> __device__ __forceinline__ bool all_of(int id, bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred a, b;\n\t"
       "setp.ne.b32 a, %1, 0;\n\t"
-      "bar.red.and.pred b, 1, %2, a;\n\t"
+      "bar.red.and.pred b, %2, %3, a;\n\t"
       "selp.u32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "n"(THREADS)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "n"(THREADS)
       : "memory");
   return r != 0;
 }
@@ -89,14 +88,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
   static_assert(NT * kTcM * 4 <= S * kStage<NT>, "the parts lie in the stages");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint32_t *words = reinterpret_cast<uint32_t *>(smem + S * kStage<NT>);   // x's scale words, [S][N]
+  uint32_t *wscale = reinterpret_cast<uint32_t *>(smem + S * kStage<NT>);  // W's scale words, [S][128]
+  uint32_t *words = wscale + S * kTcM;                                     // x's, [S][N]
   uint64_t *bars = reinterpret_cast<uint64_t *>(words + S * N);
   const uint32_t wfull0 = smem_u32(bars), xfull0 = wfull0 + 8u * S, empty0 = xfull0 + 8u * S, accf = empty0 + 8u * S;
   SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 3 * S + 1);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(wfull0 + 8u * s, kWWarps);
+      mbar_init(wfull0 + 8u * s, 33 * kWWarps);   // every thread's copies, every warp
       mbar_init(xfull0 + 8u * s, kTokWarps);
       mbar_init(empty0 + 8u * s, 1);
     }
@@ -137,8 +137,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
     const uint8_t *src = wq + (static_cast<int64_t>(o.e) * p.out + f0 + r) * ld + 8 * c;
     const uint32_t dst = smem_u32(smem) + r * 128u + static_cast<uint32_t>((c ^ r) * 16);
     const int live = p.out - f0 - r;                                         // rows from r that exist
+    const int G = p.in / kQ4Group;
+    const bool words4 = G % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3) == 0;
     ok = !loads_withheld(p.guard);
-    Ring st(S), done(S);
+    Ring st(S);
     for (int kb = kb0; kb < kb1 && ok; ++kb) {
       ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 71);
       ok = __all_sync(0xffffffffu, ok);
@@ -149,31 +151,45 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
         const bool has = in && 8 * j < live;
         copy8(dst + st.i * kStage<NT> + j * 1024u, has ? src + 8 * j * ld + kb * (kKB / 2) : wq, has ? 8u : 0u);
       }
-      copy_commit();
+      // x as it is: the 256 bytes of token t where its two pieces go, rows t and NT + t
+      const uint32_t xs = smem_u32(smem) + st.i * kStage<NT> + kWBytes;
+#pragma unroll
+      for (int j = 0; j < NT / 4; ++j) {
+        const int t = 4 * j + i / 16, d = i % 16, k = kb * kKB + 8 * d;
+        const bool has = t < ntok && k < p.in;
+        copy16(xs + static_cast<uint32_t>(t + (d >= 8 ? NT : 0)) * 128u + static_cast<uint32_t>(d & 7) * 16u,
+               has ? x + static_cast<int64_t>(o.t0 + t) * p.in + k : x, has ? 16u : 0u);
+      }
+      const uint32_t sc = smem_u32(wscale + st.i * kTcM);
+#pragma unroll
+      for (int j = 0; j < kTcM / (32 * kWWarps); ++j) {
+        const int f = 32 * kWWarps * j + i;
+        const bool has = f0 + f < p.out;
+        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + f0 + f) * G + 4 * kb;
+        if (words4) {
+          copy4(sc + 4u * f, has ? at : p.scale, has ? 4u : 0u);
+        } else {
+          uint32_t w = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w |= (has && 4 * kb + q < G ? load_now(at + q) : 127u) << (8 * q);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 4u * f), "r"(w) : "memory");
+        }
+      }
+      // the stage is full when the copies of all producing threads have landed and
+      // their plain stores are out.  The threads that wait for it order both before
+      // the tensor core's reads: a proxy fence here would wait for the copies
+      copies_arrive(wfull0 + 8u * st.i);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wfull0 + 8u * st.i);
       st.next();
-      if (kb - kb0 >= S - 1) {
-        // the oldest of S stages is here
-        copy_wait<S - 1>();
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(wfull0 + 8u * done.i);
-        done.next();
-      }
     }
-    copy_wait<0>();
-    fence_async_proxy();
-    __syncwarp();
-    if (lane == 0)
-      while (done.i != st.i || done.phase != st.phase) {
-        mbar_arrive(wfull0 + 8u * done.i);
-        done.next();
-      }
+    copies_wait();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer
     Ring st(S);
     for (int kb = kb0; kb < kb1; ++kb) {
+      // after x's pieces come W, whose copies the pieces waited for
       ok = guard_wait(xfull0 + 8u * st.i, st.phase, ctl, p.guard, 72);
-      ok = ok && guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 73);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t at = smem_u32(smem) + st.i * kStage<NT>;
@@ -196,95 +212,62 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- x and the scales
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp) * 32u << 16);
-    const int G = p.in / kQ4Group;
-    const bool quads = G % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3) == 0;
-    const uint8_t *srow[4];
+    const int group = warp / kTokWarps, own = warp % kTokWarps;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(own) * 32u << 16);
+    Ring st(S);
+    if (group == 1) st.next();
+    for (int kb = kb0 + group; kb < kb1; kb += kGroups, st.next(), st.next()) {
+      ok = guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 74);
+      uint8_t *xs = smem + st.i * kStage<NT> + kWBytes;
+      uint8_t *ws = reinterpret_cast<uint8_t *>(words + st.i * N);
+      uint2 raw[kMine];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int f = f0 + 32 * j + lane;
-      srow[j] = f < p.out ? p.scale + (static_cast<int64_t>(o.e) * p.out + f) * G : nullptr;
-    }
-    struct Next {
-      uint32_t s[4];
-      uint2 x[kMine];
-    };
-    auto fetch = [&](int kb, Next *n) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) n->s[j] = srow[j] ? scale_word(srow[j], 4 * kb, G, quads) : 0x7f7f7f7fu;
-      const int k = kb * kKB + 4 * lane;
+      for (int j = 0; j < kMine; ++j)
+        raw[j] = *reinterpret_cast<const uint2 *>(xs + (own + kTokWarps * j + (lane >= 16 ? NT : 0)) * 128 + (lane & 15) * 8);
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
-        const int t = warp + kTokWarps * j;
-        n->x[j] = t < ntok && k < p.in ? load_now2(x + static_cast<int64_t>(o.t0 + t) * p.in + k) : make_uint2(0, 0);
-      }
-    };
-    constexpr int kDeep = 2;                 // blocks of x and scales on their way
-    Next nx[kDeep];
+        float v[4] = {__uint_as_float(raw[j].x << 16), __uint_as_float(raw[j].x & 0xffff0000u),
+                      __uint_as_float(raw[j].y << 16), __uint_as_float(raw[j].y & 0xffff0000u)};
+        uint32_t m = 0;
 #pragma unroll
-    for (int u = 0; u < kDeep; ++u)
-      if (kb0 + u < kb1) fetch(kb0 + u, &nx[u]);
-    Ring st(S);
-    for (int k0 = kb0; k0 < kb1 && ok; k0 += kDeep) {
+        for (int i = 0; i < 4; ++i) m = max(m, finite_bits(v[i]));
+        // the group's 8 lanes
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        const uint32_t b = scale_byte(m);
+        const float inv = scale_inverse(b);
+        float f[4];
 #pragma unroll
-      for (int u = 0; u < kDeep; ++u) {
-        const int kb = k0 + u;
-        if (kb >= kb1 || !ok) break;
-        const Next cur = nx[u];
-        if (kb + kDeep < kb1) fetch(kb + kDeep, &nx[u]);
-        uint32_t h[kMine], l[kMine], sb[kMine];
+        for (int i = 0; i < 4; ++i) v[i] = inf_to_nan(v[i]) * inv;
+        const uint32_t h = quant4(v, 1.0f);
+        dequant4(h, 1.0f, f);
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          float v[4] = {__uint_as_float(cur.x[j].x << 16), __uint_as_float(cur.x[j].x & 0xffff0000u),
-                        __uint_as_float(cur.x[j].y << 16), __uint_as_float(cur.x[j].y & 0xffff0000u)};
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, finite_bits(v[i]));
-          // the group's 8 lanes
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          sb[j] = scale_byte(m);
-          const float inv = scale_inverse(sb[j]);
-          float f[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = inf_to_nan(v[i]) * inv;
-          h[j] = quant4(v, 1.0f);
-          dequant4(h[j], 1.0f, f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = v[i] - f[i];
-          l[j] = quant4(f, 16.0f);
+        for (int i = 0; i < 4; ++i) f[i] = v[i] - f[i];
+        const uint32_t l = quant4(f, 16.0f);
+        const int t = own + kTokWarps * j, at = ((lane >> 2) ^ (t & 7)) * 16 + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t *>(xs + t * 128 + at) = h;
+        *reinterpret_cast<uint32_t *>(xs + (NT + t) * 128 + at) = l;      // NT % 8 == 0: the same swizzle
+        if ((lane & 7) == 0) {
+          ws[4 * t + (lane >> 3)] = static_cast<uint8_t>(b);
+          ws[4 * (NT + t) + (lane >> 3)] = static_cast<uint8_t>(b - 4u);
         }
-        ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 74);
-        uint8_t *xs = smem + st.i * kStage<NT> + kWBytes;
-        uint8_t *ws = reinterpret_cast<uint8_t *>(words + st.i * N);
-#pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          if (!ok) break;
-          const int t = warp + kTokWarps * j, at = (((lane >> 2) ^ (t & 7)) * 16) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t *>(xs + t * 128 + at) = h[j];
-          *reinterpret_cast<uint32_t *>(xs + (NT + t) * 128 + at) = l[j];      // NT % 8 == 0: the same swizzle
-          if ((lane & 7) == 0) {
-            ws[4 * t + (lane >> 3)] = static_cast<uint8_t>(sb[j]);
-            ws[4 * (NT + t) + (lane >> 3)] = static_cast<uint8_t>(sb[j] - 4u);
-          }
-        }
-        fence_async_proxy();
-        // all scale words are there; the four warps go on or leave together
-        ok = all_of<32 * kTokWarps>(ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sf = lane_addr + kSfCol + kSfStride * st.i;
-        const uint32_t w0 = N >= 32 || lane < N ? words[st.i * N + lane] : 0x7f7f7f7fu;
-        const uint32_t w1 = kXCols > 1 ? words[st.i * N + 32 + lane] : 0x7f7f7f7fu;
-        const uint32_t all[8] = {cur.s[0], cur.s[1], cur.s[2], cur.s[3], w0, w1, 0u, 0u};
-        tmem_st8(sf, all);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(xfull0 + 8u * st.i);
-        st.next();
       }
+      fence_async_proxy();
+      // all scale words are there; the four warps go on or leave together
+      ok = all_of<32 * kTokWarps>(1 + group, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t *sw = wscale + st.i * kTcM + lane;
+      const uint32_t w0 = N >= 32 || lane < N ? words[st.i * N + lane] : 0x7f7f7f7fu;
+      const uint32_t w1 = kXCols > 1 ? words[st.i * N + 32 + lane] : 0x7f7f7f7fu;
+      const uint32_t all[8] = {sw[0], sw[32], sw[64], sw[96], w0, w1, 0u, 0u};
+      tmem_st8(lane_addr + kSfCol + kSfStride * st.i, all);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xfull0 + 8u * st.i);
     }
     // ---------------------------------------------------------------- result
     // into shared memory as [token][feature]: the stages are free once the
@@ -293,10 +276,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
     ok = __all_sync(0xffffffffu, got) && ok;
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
-    const int f = warp * 32 + lane;
+    const int f = own * 32 + lane;
 #pragma unroll
     for (int c = 0; c < NT; c += 8) {
-      if (c < ntok) {
+      if (c < ntok && (c / 8) % kGroups == group) {
         float a[8], b[8];
         tmem_ld<8>(lane_addr + c, a);
         tmem_ld<8>(lane_addr + NT + c, b);
@@ -343,8 +326,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
 template <int NT>
 dora_status launch(const void *x, const void *wq, Q4Params p, int cluster, cudaStream_t cs) {
   constexpr auto kern = &q4_few_kernel<NT>;
-  constexpr size_t smem = 1024 + kFewStages<NT> * (kStage<NT> + 8 * NT) + 8 * (3 * kFewStages<NT> + 1) + sizeof(SharedCtl);
-  static_assert(2 * (smem + 1024) <= kSmemMax + 1024, "two CTAs an SM");
+  constexpr size_t smem = 1024 + kFewStages<NT> * (kStage<NT> + 4 * kTcM + 8 * NT) + 8 * (3 * kFewStages<NT> + 1) + sizeof(SharedCtl);
+  static_assert(2 * (smem + 1024) <= kSmemMax + 1024, "two CTAs an SM, each with 1 KB of the system's");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
