@@ -17,9 +17,10 @@
 //               its lane quadrant), two groups of four taking turns; then the
 //               result out of it
 //   warp 8      tensor memory, MMA issue (four 32-wide steps per 128 k)
-//   warps 9-10  asynchronous copies of W, its scales and x.  W: 16 values, 8 bytes,
-//               to every 16 bytes of shared memory, the layout that the tensor core
-//               takes 4-bit values in
+//   warps 9-10  copies of W, its scales and x.  W: 16 values, 8 bytes, to every 16
+//               bytes of shared memory, the layout that the tensor core takes 4-bit
+//               values in.  TMA does that (BOX) where rows are whole blocks of 128;
+//               other rows come by asynchronous copies of 8 bytes
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -79,8 +80,10 @@ template <int THREADS> __device__ __forceinline__ bool all_of(int id, bool v) {
   return r != 0;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p, const __nv_bfloat16 *x, const uint8_t *wq) {
+template <int NT, bool BOX>
+__global__ void __launch_bounds__(kFewThreads, 2)
+q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p,
+              const __nv_bfloat16 *x, const uint8_t *wq) {
   constexpr int S = kFewStages<NT>, N = 2 * NT;
   constexpr int kMine = NT / kTokWarps;     // tokens a warp splits
   constexpr int kXCols = (N + 31) / 32;
@@ -96,14 +99,19 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
   const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(wfull0 + 8u * s, 33 * kWWarps);   // every thread's copies, every warp
+      mbar_init(wfull0 + 8u * s, 33 * kWWarps + (BOX ? 1 : 0));   // every thread's copies, every warp; boxes
       mbar_init(xfull0 + 8u * s, kTokWarps);
       mbar_init(empty0 + 8u * s, 1);
     }
     mbar_init(accf, 1);
     ctl->abort = 0;
     fence_barrier_init();
+    if (BOX) {
+      prefetch_map(&mW);
+      prefetch_map(&mX);
+    }
   }
+  for (int i = threadIdx.x; i < S * N; i += kFewThreads) words[i] = 0x7f7f7f7fu;
   if (warp == kMmaWarp) {
     __syncwarp();
     tmem_alloc(smem_u32(&ctl->tmem_base), kFewCols);
@@ -132,11 +140,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
     // no tile for this cluster
   } else if (warp > kMmaWarp) {
     // ---------------------------------------------------------------- W
-    const int i = threadIdx.x - 32 * (kMmaWarp + 1), r = i / 8, c = i % 8;   // first row, piece of 16 values
-    const int64_t ld = p.in / 2;
-    const uint8_t *src = wq + (static_cast<int64_t>(o.e) * p.out + f0 + r) * ld + 8 * c;
-    const uint32_t dst = smem_u32(smem) + r * 128u + static_cast<uint32_t>((c ^ r) * 16);
-    const int live = p.out - f0 - r;                                         // rows from r that exist
+    const int i = threadIdx.x - 32 * (kMmaWarp + 1);
     const int G = p.in / kQ4Group;
     const bool words4 = G % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3) == 0;
     ok = !loads_withheld(p.guard);
@@ -145,33 +149,45 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
       ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 71);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const bool in = kb * kKB + 16 * c < p.in;
-#pragma unroll
-      for (int j = 0; j < kTcM / 8; ++j) {
-        const bool has = in && 8 * j < live;
-        copy8(dst + st.i * kStage<NT> + j * 1024u, has ? src + 8 * j * ld + kb * (kKB / 2) : wq, has ? 8u : 0u);
-      }
+      const uint32_t at = smem_u32(smem) + st.i * kStage<NT>, xs = at + kWBytes;
       // x as it is: the 256 bytes of token t where its two pieces go, rows t and NT + t
-      const uint32_t xs = smem_u32(smem) + st.i * kStage<NT> + kWBytes;
+      if (BOX) {
+        if (warp == kMmaWarp + 1 && elect_one()) {
+          const uint32_t fb = wfull0 + 8u * st.i;
+          mbar_expect_tx(fb, kWBytes / 2 + kXBytes<NT>);      // a box counts the bytes it reads
+          tma_load_3d(at, &mW, kb * kKB, f0, o.e, fb);
+          tma_load_2d(xs, &mX, kb * kKB, o.t0, fb);
+          tma_load_2d(xs + NT * 128u, &mX, kb * kKB + 64, o.t0, fb);
+        }
+        __syncwarp();
+      } else {
+        const int r = i / 8, c = i % 8;                       // first row, piece of 16 values
+        const int64_t ld = p.in / 2;
+        const uint8_t *src = wq + (static_cast<int64_t>(o.e) * p.out + f0 + r) * ld + kb * (kKB / 2) + 8 * c;
+        const uint32_t dst = at + r * 128u + static_cast<uint32_t>((c ^ r) * 16);
+        const int live = kb * kKB + 16 * c < p.in ? p.out - f0 - r : 0;      // rows from r that exist
 #pragma unroll
-      for (int j = 0; j < NT / 4; ++j) {
-        const int t = 4 * j + i / 16, d = i % 16, k = kb * kKB + 8 * d;
-        const bool has = t < ntok && k < p.in;
-        copy16(xs + static_cast<uint32_t>(t + (d >= 8 ? NT : 0)) * 128u + static_cast<uint32_t>(d & 7) * 16u,
-               has ? x + static_cast<int64_t>(o.t0 + t) * p.in + k : x, has ? 16u : 0u);
+        for (int j = 0; j < kTcM / 8; ++j) copy8(dst + j * 1024u, 8 * j < live ? src + 8 * j * ld : wq, 8 * j < live ? 8u : 0u);
+#pragma unroll
+        for (int j = 0; j < NT / 4; ++j) {
+          const int t = 4 * j + i / 16, d = i % 16, k = kb * kKB + 8 * d;
+          const bool has = t < ntok && k < p.in;
+          copy16(xs + static_cast<uint32_t>(t + (d >= 8 ? NT : 0)) * 128u + static_cast<uint32_t>(d & 7) * 16u,
+                 has ? x + static_cast<int64_t>(o.t0 + t) * p.in + k : x, has ? 16u : 0u);
+        }
       }
       const uint32_t sc = smem_u32(wscale + st.i * kTcM);
 #pragma unroll
       for (int j = 0; j < kTcM / (32 * kWWarps); ++j) {
         const int f = 32 * kWWarps * j + i;
         const bool has = f0 + f < p.out;
-        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + f0 + f) * G + 4 * kb;
+        const uint8_t *row = p.scale + (static_cast<int64_t>(o.e) * p.out + f0 + f) * G + 4 * kb;
         if (words4) {
-          copy4(sc + 4u * f, has ? at : p.scale, has ? 4u : 0u);
+          copy4(sc + 4u * f, has ? row : p.scale, has ? 4u : 0u);
         } else {
           uint32_t w = 0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) w |= (has && 4 * kb + q < G ? load_now(at + q) : 127u) << (8 * q);
+          for (int q = 0; q < 4; ++q) w |= (has && 4 * kb + q < G ? load_now(row + q) : 127u) << (8 * q);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 4u * f), "r"(w) : "memory");
         }
       }
@@ -184,6 +200,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
       st.next();
     }
     copies_wait();
+    if (BOX && !ok && warp == kMmaWarp + 1) {
+      // boxes in flight, whose barrier may never complete after an abort: they land
+      // within microseconds, wait 1 ms
+      const unsigned long long c0 = globaltimer();
+      while (globaltimer() - c0 < 1000000ull) {
+      }
+    }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuer
     Ring st(S);
@@ -216,6 +239,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(own) * 32u << 16);
     Ring st(S);
     if (group == 1) st.next();
+    // a place without a token keeps what it holds: its column of the result is not read
+    const int mine = own < ntok ? (ntok - own + kTokWarps - 1) / kTokWarps : 0;
     for (int kb = kb0 + group; kb < kb1; kb += kGroups, st.next(), st.next()) {
       ok = guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 74);
       uint8_t *xs = smem + st.i * kStage<NT> + kWBytes;
@@ -227,6 +252,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
+        if (j >= mine) break;
         float v[4] = {__uint_as_float(raw[j].x << 16), __uint_as_float(raw[j].x & 0xffff0000u),
                       __uint_as_float(raw[j].y << 16), __uint_as_float(raw[j].y & 0xffff0000u)};
         uint32_t m = 0;
@@ -323,9 +349,36 @@ __global__ void __launch_bounds__(kFewThreads, 2) q4_few_kernel(const Q4Params p
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int NT>
+// a stack of weights [experts, out, in] in boxes of 128 x 128 values, 8 bytes of every 16 of the result
+bool map_w4(CUtensorMap *map, const void *base, int64_t experts, int64_t out, int64_t in) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(in), static_cast<cuuint64_t>(out), static_cast<cuuint64_t>(experts)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(in / 2) * static_cast<cuuint64_t>(out)};
+  cuuint32_t box[3] = {kKB, kTcM, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// x [T, in] in boxes of NT rows x 64 columns, unswizzled
+bool map_x(CUtensorMap *map, const void *base, int64_t T, int64_t in, int nt) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(in), static_cast<cuuint64_t>(T)};
+  cuuint64_t strides[1] = {2 * static_cast<cuuint64_t>(in)};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(nt)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, bool BOX>
 dora_status launch(const void *x, const void *wq, Q4Params p, int cluster, cudaStream_t cs) {
-  constexpr auto kern = &q4_few_kernel<NT>;
+  constexpr auto kern = &q4_few_kernel<NT, BOX>;
+  CUtensorMap mW = {}, mX = {};
+  if (BOX && (!map_w4(&mW, wq, p.experts, p.out, p.in) || !map_x(&mX, x, p.T, p.in, NT))) return DORA_ERR_CUDA;
   constexpr size_t smem = 1024 + kFewStages<NT> * (kStage<NT> + 4 * kTcM + 8 * NT) + 8 * (3 * kFewStages<NT> + 1) + sizeof(SharedCtl);
   static_assert(2 * (smem + 1024) <= kSmemMax + 1024, "two CTAs an SM, each with 1 KB of the system's");
   cudaLaunchConfig_t cfg = {};
@@ -342,7 +395,7 @@ dora_status launch(const void *x, const void *wq, Q4Params p, int cluster, cudaS
   cfg.stream = cs;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, p, static_cast<const __nv_bfloat16 *>(x), static_cast<const uint8_t *>(wq)) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, mW, mX, p, static_cast<const __nv_bfloat16 *>(x), static_cast<const uint8_t *>(wq)) != cudaSuccess) {
     cudaGetLastError();
     return DORA_ERR_CUDA;
   }
@@ -360,8 +413,9 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   int device = 0;
   dora_status st = current_device(&info, &device);
   if (st != DORA_OK) return st;
-  static const void *const kernels[] = {(const void *)q4_few_kernel<8>, (const void *)q4_few_kernel<16>,
-                                        (const void *)q4_few_kernel<32>};
+  static const void *const kernels[] = {
+      (const void *)q4_few_kernel<8, false>,  (const void *)q4_few_kernel<8, true>,  (const void *)q4_few_kernel<16, false>,
+      (const void *)q4_few_kernel<16, true>, (const void *)q4_few_kernel<32, false>, (const void *)q4_few_kernel<32, true>};
   Q4Params p = {};
   st = tc_init(device, &p.guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
   if (st != DORA_OK) return st;
@@ -383,11 +437,13 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   const int64_t blocks = ceil_div(in, kKB);
   while (cluster < kMaxCluster && p.tiles * cluster * 2 <= 2 * info.sms && cluster * 2 <= blocks) cluster *= 2;
   if (p.tiles * cluster > kMaxDim) return DORA_ERR_SHAPE;
+  // boxes of 4-bit values take whole blocks of 128 and 32-byte rows
+  const bool box = in % kKB == 0 && aligned(wq, 32);
   switch (p.ntok) {
-    case 8: return launch<8>(x, wq, p, cluster, cs);
-    case 16: return launch<16>(x, wq, p, cluster, cs);
+    case 8: return box ? launch<8, true>(x, wq, p, cluster, cs) : launch<8, false>(x, wq, p, cluster, cs);
+    case 16: return box ? launch<16, true>(x, wq, p, cluster, cs) : launch<16, false>(x, wq, p, cluster, cs);
   }
-  return launch<32>(x, wq, p, cluster, cs);
+  return box ? launch<32, true>(x, wq, p, cluster, cs) : launch<32, false>(x, wq, p, cluster, cs);
 }
 
 }  // namespace dora

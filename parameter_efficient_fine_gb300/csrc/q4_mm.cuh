@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "q4.cuh"
 #include "q8_tc.cuh"
+#include "tc_ptx.cuh"
 
 namespace {
 
@@ -86,6 +87,13 @@ __device__ __forceinline__ bool find_tile(const Q4Params &p, int64_t t, Tile *o)
   return false;
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 // this thread's writes to shared memory before the tensor core's reads
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
