@@ -48,7 +48,6 @@ constexpr int kGroups = 2, kGroupWarps = 4;           // conversion
 constexpr int kConvWarps = kGroups * kGroupWarps, kOutWarps = 8;
 constexpr int kConv0 = 3, kOut0 = kConv0 + kConvWarps;
 constexpr int kThreadsMm = 32 * (kOut0 + kOutWarps);
-constexpr int kFewTok = 32;                           // tokens, or tokens an expert, of q4_few.cu
 constexpr int kAhead = 4;                             // blocks whose scales are on their way
 constexpr uint32_t kACol = 256;                       // x W^T: first column of the converted W
 // half of the tile's tokens, 64 k
@@ -172,7 +171,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   const uint32_t tmem = ctl->tmem_base;
   pdl_trigger();
   pdl_wait();       // the set-up above overlaps the end of the launch before
-  const int64_t pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+  const int pair = static_cast<int>(blockIdx.x / 2), npairs = static_cast<int>(gridDim.x / 2);
   const int blocks = (p.kdim + kKB - 1) / kKB;     // of W, two stages each
   Tile o;
 
@@ -180,7 +179,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     // ---------------------------------------------------------------- tokens
     bool ok = !loads_withheld(p.guard), issued = false;
     Ring st(S);
-    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
       const int t0 = o.t0 + static_cast<int>(rank) * (p.ntok / 2);
       for (int s = 0; s < 2 * blocks; ++s) {
         ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 62);
@@ -209,7 +208,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     bool ok = !loads_withheld(p.guard);
     int issued = 0;
     Ring rw(R);
-    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
       for (int s = 0; s < blocks; ++s) {
         ok = guard_wait(rempty0 + 8u * rw.i, rw.phase ^ 1u, ctl, p.guard, 61);
@@ -244,7 +243,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       Acc acc(TRANS, p.ntok);
       const uint32_t peer_off = mapa_shared(tfull0, peer) - tfull0;   // to the peer's copy of a barrier
       const uint32_t id = idesc_bf16_pair(p.ntok) | (TRANS ? 1u << 15 : 0u);
-      for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
+      for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
         ok = guard_wait(acce + 8u * acc.i, acc.phase ^ 1u, ctl, p.guard, 63);
         const uint32_t d = tmem + acc.column();
         for (int s = 0; s < 2 * blocks; ++s) {
@@ -294,7 +293,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     bool ok = true;
     Ring st(S), rw(R);
     if (g == 1) st.next();
-    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
       // the two scale bytes of this thread's part of block s
       auto scales = [&](int s) -> uint32_t {
@@ -356,7 +355,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
     bool ok = true;
     Acc acc(TRANS, p.ntok);
-    for (int64_t t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
+    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
       ok = guard_wait(accf + 8u * acc.i, acc.phase, ctl, p.guard, 68);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -499,7 +498,9 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
       p.ntok = n;
     }
   }
-  p.tiles = p.ftiles * (offsets ? T / p.ntok + groups : dora::ceil_div(T, p.ntok));
+  const int64_t tiles = p.ftiles * (offsets ? T / p.ntok + groups : dora::ceil_div(T, p.ntok));
+  if (tiles > kMaxDim) return DORA_ERR_SHAPE;
+  p.tiles = static_cast<int>(tiles);
   CUtensorMap mW, mX;
   if (!map_w(&mW, wq, experts, out, in) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.ntok / 2, 128)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
@@ -529,17 +530,29 @@ dora_status check(const void *x, const int32_t *offsets, const void *wq, const v
 
 }  // namespace
 
-extern "C" size_t dora_matmul_q4_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
+// few tokens a weight: q4_few.cu, where W is read as it is.  Rows that are no whole
+// blocks of 128 reach it by small copies, which fall behind sooner
+static bool few(int64_t T, int64_t in, int64_t experts) {
+  return dora::q4_per(T, experts) <= (in % kKB == 0 ? dora::kQ4Few : 16);
+}
+
+extern "C" size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {
+  if (bad_size(T, 1) || bad_size(out, 1) || bad_size(in, 1) || experts < 1 || experts > kMaxExperts) return 0;
+  return few(T, in, experts) ? dora::q4_few_workspace(T, in, dora::q4_per(T, experts)) : 0;
+}
 extern "C" size_t dora_matmul_q4_t_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
 
 extern "C" dora_status dora_matmul_q4(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
-                                      int64_t out, int64_t in, int64_t experts, void *y, void *, size_t,
-                                      dora_stream_t stream) {
+                                      int64_t out, int64_t in, int64_t experts, void *y, void *workspace,
+                                      size_t workspace_bytes, dora_stream_t stream) {
   if (in < 1) return DORA_ERR_SHAPE;
   const dora_status st = check(x, offsets, wq, wscale, T, out, in, experts, y);
   if (st != DORA_OK || T == 0 || out == 0) return st;
-  if (T <= kFewTok * (offsets && experts < T ? experts : 1))
-    return dora::matmul_q4_few(x, offsets, wq, wscale, T, out, in, experts, y, reinterpret_cast<cudaStream_t>(stream));
+  const size_t need = dora_matmul_q4_workspace(T, out, in, experts);
+  if (need > 0 && (!workspace || !dora::aligned(workspace, 256) || workspace_bytes < need)) return DORA_ERR_WORKSPACE;
+  if (few(T, in, experts))
+    return dora::matmul_q4_few(x, offsets, wq, wscale, T, out, in, experts, y, workspace,
+                               reinterpret_cast<cudaStream_t>(stream));
   return run_matmul<false>(x, offsets, wq, wscale, T, out, in, experts, y, stream);
 }
 

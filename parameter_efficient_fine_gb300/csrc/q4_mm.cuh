@@ -24,7 +24,7 @@ struct Q4Params {
   const int *offsets;               // null: one weight, all rows
   int ntok;                         // tokens per tile
   int ftiles;
-  int64_t tiles;                    // no more than these
+  int tiles;                        // no more than these
   const uint8_t *scale;
   __nv_bfloat16 *y;
   Guard guard;
@@ -41,12 +41,11 @@ struct Tile {
 
 // Tile `t`, or false past the last.  All lanes of the warp call it.  Experts: the
 // tokens' tiles of all experts in order, the feature tiles of each in turn.
-__device__ __forceinline__ bool find_tile(const Q4Params &p, int64_t t, Tile *o) {
+__device__ __forceinline__ bool find_tile(const Q4Params &p, int t, Tile *o) {
   if (!p.offsets) {
-    const int ntiles = (p.T + p.ntok - 1) / p.ntok;
-    if (t >= static_cast<int64_t>(ntiles) * p.ftiles) return false;
-    const int per = kGroupF * ntiles, g = static_cast<int>(t / per), f0 = g * kGroupF, gf = min(kGroupF, p.ftiles - f0),
-              r = static_cast<int>(t - static_cast<int64_t>(g) * per), tt = r / gf;
+    if (t >= p.tiles) return false;
+    const int ntiles = p.tiles / p.ftiles, per = kGroupF * ntiles, g = t / per, f0 = g * kGroupF,
+              gf = min(kGroupF, p.ftiles - f0), r = t - g * per, tt = r / gf;
     o->e = 0;
     o->ft = f0 + r - tt * gf;
     o->t0 = tt * p.ntok;
@@ -54,7 +53,7 @@ __device__ __forceinline__ bool find_tile(const Q4Params &p, int64_t t, Tile *o)
     return true;
   }
   const int lane = threadIdx.x & 31;
-  const int64_t tt = t / p.ftiles;
+  const int tt = t / p.ftiles;
   int64_t before = 0;                                  // token tiles of the experts before this 32
   for (int e0 = 0; e0 < p.experts; e0 += 32) {
     const int e = e0 + lane;
@@ -64,20 +63,20 @@ __device__ __forceinline__ bool find_tile(const Q4Params &p, int64_t t, Tile *o)
       b = min(max(p.offsets[e + 1], a), p.T);
     }
     const int own = (b - a + p.ntok - 1) / p.ntok;
-    int upto = own;                                    // tiles of this 32, up to and with this expert's
+    int64_t upto = own;                                // tiles of this 32, up to and with this expert's
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += v;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, before + upto > tt);
     if (past) {
       const int who = __ffs(past) - 1;
-      const int first = __shfl_sync(0xffffffffu, upto - own, who);
+      const int64_t first = __shfl_sync(0xffffffffu, upto - own, who);
       a = __shfl_sync(0xffffffffu, a, who);
       b = __shfl_sync(0xffffffffu, b, who);
       o->e = e0 + who;
-      o->ft = static_cast<int>(t - tt * p.ftiles);
+      o->ft = t - tt * p.ftiles;
       o->t0 = a + static_cast<int>(tt - before - first) * p.ntok;
       o->t1 = min(b, o->t0 + p.ntok);
       return true;
@@ -101,8 +100,11 @@ __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.
 
 namespace dora {
 
-// x W^T of few tokens (q4_few.cu), one launch
+// x W^T of few tokens (q4_few.cu): `per` of them a weight
+constexpr int64_t kQ4Few = 128;
+inline int64_t q4_per(int64_t T, int64_t experts) { return experts < T ? ceil_div(T, experts) : 1; }
+size_t q4_few_workspace(int64_t T, int64_t in, int64_t per);
 dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
-                          int64_t out, int64_t in, int64_t experts, void *y, cudaStream_t cs);
+                          int64_t out, int64_t in, int64_t experts, void *y, void *workspace, cudaStream_t cs);
 
 }  // namespace dora

@@ -133,10 +133,20 @@ def sum_bound(x, wq, ws, K, t, offsets=None):
     return bound
 
 
+def product(x, wq, ws, y, t, offsets=None):
+    """The call with a guarded workspace of just the size that it names."""
+    out, inp = wq.shape[-2], 2 * wq.shape[-1]
+    size = dora.dora_matmul_q4_t_workspace if t else dora.dora_matmul_q4_workspace
+    n = size(x.shape[0], out, inp, 1 if offsets is None else wq.shape[0])
+    b = Guarded(n)
+    (dora.dora_matmul_q4_t if t else dora.dora_matmul_q4)(x, wq, ws, y, offsets, b.view(U8, (n,)))
+    b.check("workspace")
+
+
 def run(x, wq, ws, t, offsets=None, fill=float("nan")):
     n = 2 * wq.shape[-1] if t else wq.shape[-2]
     y = torch.full((x.shape[0], n), fill, dtype=BF16, device=DEV)
-    (dora.dora_matmul_q4_t if t else dora.dora_matmul_q4)(x, wq, ws, y, offsets)
+    product(x, wq, ws, y, t, offsets)
     return y
 
 
@@ -156,7 +166,7 @@ def check_product(x, h, wq, ws, t, offsets=None):
 @pytest.mark.parametrize("T,out,inp", [
     (1, 16, 32), (1, 512, 512), (1, 1040, 2080), (2, 272, 1120), (3, 4096, 256), (7, 128, 128), (8, 256, 4096),
     (9, 48, 160), (16, 400, 640), (17, 256, 256), (31, 528, 992), (33, 64, 96), (40, 2048, 512), (64, 272, 384), (65, 272, 544),
-    (100, 1040, 2080), (129, 256, 1024), (200, 144, 8192), (257, 512, 160), (300, 784, 288), (1000, 272, 736)])
+    (100, 1040, 2080), (100, 400, 1152), (128, 4096, 128), (129, 256, 1024), (200, 144, 8192), (257, 512, 160), (300, 784, 288), (1000, 272, 736)])
 def test_products(T, out, inp, t):
     rng = np.random.default_rng(T * 31 + out + inp)
     wq, ws = weight(rng, out, inp)
@@ -166,7 +176,7 @@ def test_products(T, out, inp, t):
 
 EXPERTS = [
     ([0, 1], 64, 96), ([0, 0, 3, 3, 4, 4], 272, 544), ([0, 5, 5, 40, 41, 300], 144, 160), ([0] * 40 + [2, 2, 9, 9], 256, 384),
-    ([0, 700, 701, 701], 400, 256), ([0, 8, 16, 24, 32, 40, 48, 56, 64], 512, 1024), (list(range(0, 78, 2)), 48, 2080)]
+    ([0, 700, 701, 701], 400, 256), ([0, 30, 30, 100, 130], 272, 640), ([0, 1, 300, 301], 144, 384), ([0, 8, 16, 24, 32, 40, 48, 56, 64], 512, 1024), (list(range(0, 78, 2)), 48, 2080)]
 
 
 @pytest.mark.parametrize("t", [False, True], ids=["xWt", "dyW"])
@@ -189,8 +199,7 @@ def test_offsets_past_the_rows_stay_inside(offsets, t):
     _, x = act(spread(rng, (T, out if t else inp)))
     yb = Guarded(T * n * 2)
     y = yb.view(BF16, (T, n))
-    (dora.dora_matmul_q4_t if t else dora.dora_matmul_q4)(x, u8_dev(wq), u8_dev(ws), y,
-                                                         torch.tensor(offsets, dtype=torch.int32, device=DEV))
+    product(x, u8_dev(wq), u8_dev(ws), y, t, torch.tensor(offsets, dtype=torch.int32, device=DEV))
     torch.cuda.synchronize()
     yb.check("y")
     assert_no_device_error()
@@ -257,7 +266,7 @@ def test_same_bits_again_and_nothing_else_written(T, t):
     for _ in range(3):
         yb = Guarded(T * n * 2)
         y = yb.view(BF16, (T, n))
-        (dora.dora_matmul_q4_t if t else dora.dora_matmul_q4)(x, wq, ws, y)
+        product(x, wq, ws, y, t)
         torch.cuda.synchronize()
         yb.check("y")
         assert torch.equal(y.view(torch.int16), first.view(torch.int16))
