@@ -557,7 +557,7 @@ size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t ex
  *   offsets  int32 [experts + 1] on the device (dora_expert_sort), not falling; or
  *            NULL with experts == 1: all rows.  Values are clamped to 0 .. T.
  *   wq       uint8 [experts, out, in / 2]   wscale  uint8 [experts, out, in / 32]
- *   x, wq and y 16-byte aligned, in % 32 == 0, out % 16 == 0
+ *   x, wq, wscale and y 16-byte aligned, in % 32 == 0, out % 16 == 0
  *   workspace  not used (dora_matmul_q4_workspace)
  *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1, below 2^31 - 1023,
  *   1 <= experts <= 4096.

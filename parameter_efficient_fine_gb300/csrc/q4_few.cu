@@ -13,21 +13,25 @@
 // second ones).  A tile of 128 features and up to NT tokens is a cluster of CTAs
 // that share its k range and meet in distributed shared memory, summed in rank
 // order.
-//   first warps  scale words into tensor memory, each warp its lane quadrant; then
-//                the result out of it.  Up to 8 tokens they also make the pieces of
-//                x, in place, three groups of four warps taking turns; more tokens
-//                are split by a launch of its own before (q4_split_kernel), while
-//                this one's first blocks of W are already on their way
-//   next warp    tensor memory, MMA issue (four 32-wide steps per 128 k)
-//   last two     copies of W, its scales and x.  W: 16 values, 8 bytes, to every 16
-//                bytes of shared memory, the layout that the tensor core takes 4-bit
-//                values in.  TMA does that (BOX) where rows are whole blocks of 128;
-//                other rows come by asynchronous copies of 8 bytes
+//   workers      up to 8 tokens: x of a block of 128 k into pieces, in place, each
+//                warp the blocks of its own in turn; then the result out of tensor
+//                memory.  More tokens are split by a launch of its own before
+//                (q4_split_kernel), while this one's first blocks of W are already
+//                on their way
+//   next warp    tensor memory, scale words into it, MMA issue (four 32-wide steps per
+//                block)
+//   next warp    copies of W and of its scales
+//   last warp    copies of x or its pieces
+// The tensor core takes 4-bit values 16 to every 16 bytes of shared memory, in 8 of
+// them.  TMA lays W out like that where its rows are whole blocks of 128 (BOX); else
+// a block arrives as it is stored, in the half of its place, and a worker spreads it.
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "q4.cuh"
@@ -40,38 +44,38 @@ namespace {
 
 constexpr int kKB = 128;                    // k per stage
 constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB of shared memory, 8 of W
-constexpr int kQuads = 4, kCopyWarps = 2;   // warps of a group, of copies
-constexpr int kMaxCluster = 8;              // the portable limit
+constexpr int kMaxClusterLog = 3;           // 8 CTAs, the portable limit
+constexpr int kAheadL2 = 6;                 // blocks asked into L2 while the launch before ends
+constexpr unsigned kSfBytes = kTcM * 4;     // scale words of 128 rows
 
 // what a kernel of up to NT tokens a tile is made of
-template <int NT> struct Few {
+template <int NT, bool BOX> struct Few {
   static constexpr bool kSplit = NT > 8;                        // x comes in pieces
   static constexpr int N = 2 * NT;                              // rows of pieces
-  static constexpr int kGroups = kSplit ? 1 : 3;                // turns
-  static constexpr int kStages = NT == 8 ? 6 : NT == 16 ? 5 : NT == 64 ? 3 : 4;
   static constexpr int kPerSm = NT == 128 ? 1 : 2;              // CTAs, limited by shared memory
-  static constexpr int kMma = kGroups * kQuads, kCopy = kMma + 1, kThreads = 32 * (kCopy + kCopyWarps);
-  static constexpr unsigned kXBytes = N * kKB, kStage = kWBytes + kXBytes;
-  // tensor memory: the result, then 4 columns of W's scale words and one per 32 rows of x's for each stage
-  static constexpr int kXCols = (N + 31) / 32, kSfCol = N < 64 ? 64 : N, kSfStride = kXCols > 4 ? 16 : 8;
+  static constexpr int kStages = NT <= 16 ? 5 : NT == 64 ? 3 : 4;   // blocks of W
+  static constexpr int kXStages = NT == 8 ? 10 : kStages;       // blocks of x
+  static constexpr int kWorkers = kStages < 4 ? 4 : kStages;
+  static constexpr int kMma = kWorkers, kCopyW = kMma + 1, kCopyX = kMma + 2, kThreads = 32 * (kMma + 3);
+  static constexpr unsigned kXSf = (N + 127) / 128 * kSfBytes;  // scale words of a block of pieces
+  static constexpr unsigned kXBytes = N * kKB;
+  // tensor memory: the result, then 4 columns of W's scale words and 4 per 128 rows of x's for each stage
+  static constexpr int kSfCol = N < 64 ? 64 : N, kSfStride = 4 + static_cast<int>(kXSf / kSfBytes) * 4;
   static constexpr int kCols = NT == 128 ? 512 : NT == 64 ? 256 : 128;
-  static constexpr int kWords = kSplit ? NT : N;                // scale words of x in shared memory, a stage
-  static constexpr size_t kSmem = 1024 + kStages * (kStage + 4 * (kTcM + kWords)) + 8 * (4 * kStages + 1) + sizeof(SharedCtl);
-  // each group visits every use of its slots
-  static_assert(kStages % kGroups == 0 && kSfCol + kSfStride * kStages <= kCols && kPerSm * kCols <= 512, "stages, tensor memory");
+  static constexpr int kBars = 3 * kStages + 3 * kXStages + 1;
+  static constexpr size_t kSmem = 1024 + kStages * (kWBytes + kSfBytes) + kXStages * (kXBytes + kXSf) + 8 * kBars +
+                                  sizeof(SharedCtl);
+  // a wait goes by the parity of a phase, so a worker's slots are its own: it visits
+  // every use of them in turn
+  static_assert(kXStages % kStages == 0 && kStages <= kWorkers, "slots of a worker");
+  static_assert(kSfCol + kSfStride * kStages <= kCols && kPerSm * kCols <= 512, "tensor memory");
   static_assert(kPerSm * (kSmem + 1024) <= kSmemMax + 1024, "shared memory, with 1 KB of the system's a CTA");
-  static_assert(NT * kTcM * 4 <= kStages * kStage, "the parts lie in the stages");
+  static_assert(NT * kTcM * 4 <= kStages * kWBytes + kXStages * kXBytes, "the parts lie in the blocks");
 };
 
-// 4, 8 or 16 bytes into shared memory, zeros where `bytes` is 0
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global.L2::256B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 4 bytes into shared memory
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // an arrival on `bar` once this thread's copies so far have landed
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
@@ -79,20 +83,15 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// barrier `id` of `THREADS` threads, and whether `v` holds in all of them
-template <int THREADS> __device__ __forceinline__ bool all_of(int id, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\t"
-      "setp.ne.b32 a, %1, 0;\n\t"
-      "bar.red.and.pred b, %2, %3, a;\n\t"
-      "selp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "n"(THREADS)
-      : "memory");
-  return r != 0;
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// The scale words of 128 rows, 512 bytes, into 4 columns of tensor memory, the same in
+// each lane quadrant: row 32 j + l at byte 16 l + 4 j comes to lane l, column j
+__device__ __forceinline__ uint32_t sf_at(int row) { return static_cast<uint32_t>((row % 32) * 16 + (row / 32) % 4 * 4 + row / 128 * 512); }
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+  // 8 rows of 16 bytes, the next 8 128 bytes on; no swizzle
+  const uint64_t d = ((saddr & 0x3FFFFu) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
-
 // Two pieces of four values of a group of 32 that 8 neighbouring lanes hold, and the
 // first one's scale byte; the second's is 4 less
 __device__ __forceinline__ void split4(uint2 raw, uint32_t *h, uint32_t *l, uint32_t *byte) {
@@ -116,17 +115,17 @@ __device__ __forceinline__ void split4(uint2 raw, uint32_t *h, uint32_t *l, uint
   *l = quant4(f, 16.0f);
 }
 
-// x [T, in] into pieces: first ones [T, in], second ones [T, in], then the scale words of
-// the first ones [T, blocks], a byte per 32 columns; the second ones' bytes are 4 less
+// x [T, in] into pieces: first ones [T, in], second ones [T, in], then their scale words
+// [blocks, 2, T], a byte per 32 columns
 constexpr int kSplitThreads = 256;
 __global__ void __launch_bounds__(kSplitThreads)
 q4_split_kernel(const __nv_bfloat16 *__restrict__ x, int T, int in, uint8_t *__restrict__ pieces) {
   pdl_trigger();
-  const int blocks = (in + kKB - 1) / kKB, c = 4 * static_cast<int>(blockIdx.x * kSplitThreads + threadIdx.x);
+  const int c = 4 * static_cast<int>(blockIdx.x * kSplitThreads + threadIdx.x);
   const int64_t all = static_cast<int64_t>(T) * in;
-  uint8_t *words = pieces + 2 * all;
+  uint32_t *words = reinterpret_cast<uint32_t *>(pieces + 2 * all);
   for (int t = blockIdx.y; t < T; t += gridDim.y) {
-    // a warp holds 128 columns: all of a block's scale bytes, any past the row
+    // a warp holds a block of 128 columns; any scale past the row
     const int64_t at = static_cast<int64_t>(t) * in + c;
     uint32_t h, l, b;
     split4(c < in ? __ldg(reinterpret_cast<const uint2 *>(x + at)) : make_uint2(0, 0), &h, &l, &b);
@@ -134,43 +133,53 @@ q4_split_kernel(const __nv_bfloat16 *__restrict__ x, int T, int in, uint8_t *__r
       *reinterpret_cast<uint32_t *>(pieces + at) = h;
       *reinterpret_cast<uint32_t *>(pieces + all + at) = l;
     }
-    if ((threadIdx.x & 7) == 0 && c < blocks * kKB) words[static_cast<int64_t>(t) * blocks * 4 + c / 32] = static_cast<uint8_t>(b);
+    b |= __shfl_down_sync(0xffffffffu, b, 8) << 8;      // lanes 0 and 16 hold two bytes,
+    b |= __shfl_down_sync(0xffffffffu, b, 16) << 16;    // lane 0 four
+    if ((threadIdx.x & 31) == 0 && c < in) {
+      uint32_t *at = words + 2 * static_cast<int64_t>(c / kKB) * T + t;
+      at[0] = b;
+      at[T] = b - 0x04040404u;
+    }
   }
 }
 
 template <int NT, bool BOX>
-__global__ void __launch_bounds__(Few<NT>::kThreads, Few<NT>::kPerSm)
+__global__ void __launch_bounds__(Few<NT, BOX>::kThreads, Few<NT, BOX>::kPerSm)
 q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p,
-              const __nv_bfloat16 *x, const uint8_t *wq, const uint32_t *xwords) {
-  using F = Few<NT>;
-  constexpr int S = F::kStages, N = F::N;
+              const uint8_t *wq, const uint32_t *xwords) {
+  using F = Few<NT, BOX>;
+  constexpr int S = F::kStages, XS = F::kXStages, N = F::N;
   constexpr bool PRE = F::kSplit;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint32_t *wscale = reinterpret_cast<uint32_t *>(smem + S * F::kStage);  // W's scale words, [S][128]
-  uint32_t *words = wscale + S * kTcM;                                    // x's, [S][kWords]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(words + S * F::kWords);
-  // barriers of a stage: W (and pieces), scales (and x), scale words in tensor memory, empty; the result
-  const uint32_t wfull0 = smem_u32(bars), sfull0 = wfull0 + 8u * S, xfull0 = sfull0 + 8u * S, empty0 = xfull0 + 8u * S,
-                 accf = empty0 + 8u * S;
-  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 4 * S + 1);
+  uint8_t *xs0 = smem + S * kWBytes;                         // x's pieces, [XS]
+  uint8_t *wsf0 = xs0 + XS * F::kXBytes, *xsf0 = wsf0 + S * kSfBytes;   // scale words, as sf_at says
+  uint64_t *bars = reinterpret_cast<uint64_t *>(xsf0 + XS * F::kXSf);
+  // barriers: of a block of W here, spread (!BOX), empty; of a block of x here, split, empty; the result
+  const uint32_t wfull0 = smem_u32(bars), wready0 = wfull0 + 8u * S, wempty0 = wready0 + 8u * S, xfull0 = wempty0 + 8u * S,
+                 xready0 = xfull0 + 8u * XS, xempty0 = xready0 + 8u * XS, accf = xempty0 + 8u * XS;
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + F::kBars);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      // boxes; every thread's copies of W
-      mbar_init(wfull0 + 8u * s, (BOX || PRE ? 1 : 0) + (BOX ? 0 : 32 * kCopyWarps));
-      // every thread's copies, every warp's plain stores; boxes of x
-      mbar_init(sfull0 + 8u * s, 33 * kCopyWarps + (BOX && !PRE ? 1 : 0));
-      mbar_init(xfull0 + 8u * s, kQuads);
-      mbar_init(empty0 + 8u * s, 1);
+      mbar_init(wfull0 + 8u * s, BOX ? 33 : 1);              // the box; every lane's copies of scale words
+      mbar_init(wready0 + 8u * s, 1);
+      mbar_init(wempty0 + 8u * s, 1);
+    }
+    for (int s = 0; s < XS; ++s) {
+      mbar_init(xfull0 + 8u * s, PRE ? 33 : 1);
+      mbar_init(xready0 + 8u * s, 1);
+      mbar_init(xempty0 + 8u * s, 1);
     }
     mbar_init(accf, 1);
     ctl->abort = 0;
     fence_barrier_init();
-    if (BOX) prefetch_map(&mW);
-    if (BOX || PRE) prefetch_map(&mX);
+    prefetch_map(&mW);
+    prefetch_map(&mX);
   }
-  for (int i = threadIdx.x; i < S * F::kWords; i += F::kThreads) words[i] = 0x7f7f7f7fu;
+  // scale words that nothing writes: of rows without a token or a feature
+  for (int i = threadIdx.x; i < static_cast<int>((S * kSfBytes + XS * F::kXSf) / 4); i += F::kThreads)
+    reinterpret_cast<uint32_t *>(wsf0)[i] = 0x7f7f7f7fu;
   if (warp == F::kMma) {
     __syncwarp();
     tmem_alloc(smem_u32(&ctl->tmem_base), F::kCols);
@@ -182,142 +191,130 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
   const uint32_t tmem = ctl->tmem_base;
   uint32_t csize;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
-  const uint32_t rank = cluster_ctarank();
-  // Without pieces the launch before this one may still run: nothing is read or
-  // written before it has ended.  With pieces it is q4_split_kernel, which itself
-  // started after all launches before it had ended: only what it writes is waited for
-  pdl_trigger();
-  if (!PRE) pdl_wait();
-
-  Tile o = {};
-  const bool work = find_tile(p, static_cast<int>(blockIdx.x / csize), &o);   // all of a cluster alike
+  const uint32_t rank = cluster_ctarank(), clog = 31u - __clz(csize);      // a power of two
+  const int tile = static_cast<int>(blockIdx.x >> clog);
   const uint32_t blocks = static_cast<uint32_t>((p.kdim + kKB - 1) / kKB);
-  // at least one block: a cluster has no more CTAs than there are
-  const int kb0 = static_cast<int>(blocks * rank / csize), kb1 = static_cast<int>(blocks * (rank + 1) / csize);
-  const int ntok = o.t1 - o.t0, f0 = o.ft * kTcM;
+  // blocks kb0 to kb0 + nb of k, at least one: a cluster has no more CTAs than there are
+  const int kb0 = static_cast<int>((blocks * rank) >> clog), nb = static_cast<int>((blocks * (rank + 1)) >> clog) - kb0;
+  // Without pieces the launch before this one may still run: nothing is read or
+  // written before it has ended, but the first blocks of W are on their way into L2
+  // (by lines: TMA takes rows of a box one by one, and that is what bounds this
+  // kernel).  With pieces it is q4_split_kernel, which itself started after all
+  // launches before it had ended: only what it writes is waited for
+  pdl_trigger();
+  if (!PRE) {
+    if (!p.offsets)
+      for (int f = threadIdx.x; f < kTcM && tile * kTcM + f < p.out; f += F::kThreads) {
+        const uint8_t *row = wq + static_cast<int64_t>(tile * kTcM + f) * (p.in / 2) + kb0 * (kKB / 2);
+        for (int c = 0; c < min(nb, kAheadL2) * (kKB / 2); c += 128) prefetch_line(row + c);
+      }
+    pdl_wait();
+  }
+  Tile o = {0, tile, 0, p.T};       // one weight: all tokens are one tile
+  const bool work = !p.offsets || find_tile(p, tile, &o);                  // all of a cluster alike
+  const int ntok = o.t1 - o.t0, f0 = o.ft * kTcM, G = p.in / kQ4Group;
+  // W's scales of row f, block kb0 + b
+  auto scale_at = [&](int f, int b) { return (static_cast<int64_t>(o.e) * p.out + f0 + f) * G + 4 * (kb0 + b); };
   bool ok = true;
 
   if (!work) {
     // no tile for this cluster
-  } else if (warp >= F::kCopy) {
-    // ---------------------------------------------------------------- copies
-    const int i = threadIdx.x - 32 * F::kCopy;
-    const bool boxes = warp == F::kCopy;               // this warp issues them
-    const int G = p.in / kQ4Group;
-    const bool words4 = G % 4 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3) == 0;
-    // what the boxes of a stage count on wfull: those of W count the bytes that they read
-    constexpr uint32_t tx = (BOX ? kWBytes / 2 : 0) + (PRE ? F::kXBytes : 0);
+  } else if (warp == F::kCopyW) {
+    // ---------------------------------------------------------------- W and its scales
     ok = !loads_withheld(p.guard);
-    int ahead = 0;                                     // blocks of W asked for before the pieces
-    if (BOX && PRE && ok) {
-      ahead = min(S, kb1 - kb0);
-      if (boxes && elect_one())
-        for (int s = 0; s < ahead; ++s) {
-          mbar_expect_tx(wfull0 + 8u * s, tx);
-          tma_load_3d(smem_u32(smem) + s * F::kStage, &mW, (kb0 + s) * kKB, f0, o.e, wfull0 + 8u * s);
-        }
-      __syncwarp();
-    }
-    if (PRE) pdl_wait();
+    bool issued = false;
     Ring st(S);
-    for (int kb = kb0; kb < kb1 && ok; ++kb) {
-      ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 71);
+    for (int b = 0; b < nb && ok; ++b, st.next()) {
+      ok = guard_wait(wempty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 71);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t at = smem_u32(smem) + st.i * F::kStage, xs = at + kWBytes;
-      const uint32_t wb = wfull0 + 8u * st.i, sb = sfull0 + 8u * st.i;
-      if ((BOX || PRE) && boxes && elect_one()) {
-        if (kb - kb0 >= ahead) {
-          mbar_expect_tx(wb, tx);
-          if (BOX) tma_load_3d(at, &mW, kb * kKB, f0, o.e, wb);
-        }
-        if (PRE) {
-          tma_load_2d(xs, &mX, kb * kKB, o.t0, wb);
-          tma_load_2d(xs + NT * kKB, &mX, kb * kKB, p.T + o.t0, wb);
-        } else {
-          // x as it is: the 256 bytes of token t where its two pieces go, rows t and NT + t
-          mbar_expect_tx(sb, F::kXBytes);
-          tma_load_2d(xs, &mX, kb * kKB, o.t0, sb);
-          tma_load_2d(xs + NT * kKB, &mX, kb * kKB + 64, o.t0, sb);
-        }
+      const uint32_t full = wfull0 + 8u * st.i, at = smem_u32(smem) + st.i * kWBytes;
+      if (elect_one()) {
+        // a box counts the bytes that it reads
+        mbar_expect_tx(full, kWBytes / 2);
+        if (BOX) tma_load_3d(at, &mW, (kb0 + b) * kKB, f0, o.e, full);
+        else tma_load_3d(at, &mW, (kb0 + b) * (kKB / 2), f0, o.e, full);
       }
       __syncwarp();
-      if (!BOX && !PRE) {
+      issued = true;
+      if (BOX) {
 #pragma unroll
-        for (int j = 0; j < NT / 4; ++j) {
-          const int t = 4 * j + i / 16, d = i % 16, k = kb * kKB + 8 * d;
-          const bool has = t < ntok && k < p.in;
-          copy16(xs + static_cast<uint32_t>(t + (d >= 8 ? NT : 0)) * 128u + static_cast<uint32_t>(d & 7) * 16u,
-                 has ? x + static_cast<int64_t>(o.t0 + t) * p.in + k : x, has ? 16u : 0u);
+        for (int j = 0; j < kTcM / 32; ++j) {
+          const int f = 32 * j + lane;
+          if (f0 + f < p.out) copy4(smem_u32(wsf0) + st.i * kSfBytes + sf_at(f), p.scale + scale_at(f, b));
         }
+        copies_arrive(full);
       }
-      if (PRE) {
-        const uint32_t to = smem_u32(words + st.i * F::kWords);
-        for (int t = i; t < ntok; t += 32 * kCopyWarps)
-          copy4(to + 4u * t, xwords + static_cast<int64_t>(o.t0 + t) * blocks + kb, 4u);
-      }
-      const uint32_t sc = smem_u32(wscale + st.i * kTcM);
-#pragma unroll
-      for (int j = 0; j < kTcM / (32 * kCopyWarps); ++j) {
-        const int f = 32 * kCopyWarps * j + i;
-        const bool has = f0 + f < p.out;
-        const uint8_t *row = p.scale + (static_cast<int64_t>(o.e) * p.out + f0 + f) * G + 4 * kb;
-        if (words4) {
-          copy4(sc + 4u * f, has ? row : p.scale, has ? 4u : 0u);
-        } else {
-          uint32_t w = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) w |= (has && 4 * kb + q < G ? load_now(row + q) : 127u) << (8 * q);
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 4u * f), "r"(w) : "memory");
-        }
-      }
-      // full when the copies of all these threads have landed and their plain stores
-      // are out.  The threads that wait for it order both before the tensor core's
-      // reads: a proxy fence here would wait for the copies
-      copies_arrive(sb);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sb);
-      if (!BOX) {
-        const int r = i / 8, c = i % 8;                       // first row, piece of 16 values
-        const int64_t ld = p.in / 2;
-        const uint8_t *src = wq + (static_cast<int64_t>(o.e) * p.out + f0 + r) * ld + kb * (kKB / 2) + 8 * c;
-        const uint32_t dst = at + r * 128u + static_cast<uint32_t>((c ^ r) * 16);
-        const int live = kb * kKB + 16 * c < p.in ? p.out - f0 - r : 0;      // rows from r that exist
-#pragma unroll
-        for (int j = 0; j < kTcM / 8; ++j) copy8(dst + j * 1024u, 8 * j < live ? src + 8 * j * ld : wq, 8 * j < live ? 8u : 0u);
-        copies_arrive(wb);
-      }
-      st.next();
     }
     copies_wait();
-    if ((BOX || PRE) && !ok && boxes) {
-      // boxes in flight, whose barrier may never complete after an abort: they land
+    if (!ok && issued) {
+      // boxes in flight, whose barrier nobody may wait for after an abort: they land
       // within microseconds, wait 1 ms
+      const unsigned long long c0 = globaltimer();
+      while (globaltimer() - c0 < 1000000ull) {
+      }
+    }
+  } else if (warp == F::kCopyX) {
+    // ---------------------------------------------------------------- x or its pieces
+    ok = !loads_withheld(p.guard);
+    bool issued = false;
+    if (PRE) pdl_wait();
+    Ring st(XS);
+    for (int b = 0; b < nb && ok; ++b, st.next()) {
+      ok = guard_wait(xempty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 72);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t xs = smem_u32(xs0) + st.i * F::kXBytes, full = xfull0 + 8u * st.i;
+      const int k = (kb0 + b) * kKB;
+      if (elect_one()) {
+        mbar_expect_tx(full, F::kXBytes);
+        // x as it is: the 256 bytes of token t where its two pieces go, rows t and NT + t
+        tma_load_2d(xs, &mX, k, o.t0, full);
+        tma_load_2d(xs + NT * kKB, &mX, PRE ? k : k + 64, PRE ? p.T + o.t0 : o.t0, full);
+      }
+      __syncwarp();
+      issued = true;
+      if (PRE) {
+        const uint32_t to = smem_u32(xsf0) + st.i * F::kXSf;
+        const uint32_t *from = xwords + 2 * static_cast<int64_t>(kb0 + b) * p.T + o.t0;
+        for (int t = lane; t < ntok; t += 32) {
+          copy4(to + sf_at(t), from + t);
+          copy4(to + sf_at(NT + t), from + p.T + t);
+        }
+        copies_arrive(full);
+      }
+    }
+    copies_wait();
+    if (!ok && issued) {
       const unsigned long long c0 = globaltimer();
       while (globaltimer() - c0 < 1000000ull) {
       }
     }
   } else if (warp == F::kMma) {
     // ---------------------------------------------------------------- MMA issuer
-    Ring st(S);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      ok = guard_wait(xfull0 + 8u * st.i, st.phase, ctl, p.guard, 72);
-      ok = ok && guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 73);
+    Ring st(S), xt(XS);
+    for (int b = 0; b < nb; ++b, st.next(), xt.next()) {
+      ok = guard_wait((PRE ? xfull0 : xready0) + 8u * xt.i, xt.phase, ctl, p.guard, 73);
+      ok = ok && guard_wait((BOX ? wfull0 : wready0) + 8u * st.i, st.phase, ctl, p.guard, 74);
       if (!__all_sync(0xffffffffu, ok)) break;
-      if (!BOX) fence_async_proxy();
+      // scale words came by copies that the tensor core's reads are not ordered after
+      fence_async_proxy();
       tc_fence_after();
-      const uint32_t at = smem_u32(smem) + st.i * F::kStage;
-      const uint64_t a = sdesc<32>(at), b = sdesc<32>(at + kWBytes);
+      const uint64_t da = sdesc<32>(smem_u32(smem) + st.i * kWBytes), db = sdesc<32>(smem_u32(xs0) + xt.i * F::kXBytes);
       const uint32_t sf = tmem + F::kSfCol + F::kSfStride * st.i;
       if (elect_one()) {
+        // (a copy runs before the MMAs that this thread issues after it)
+        copy_scales(sf, smem_u32(wsf0) + st.i * kSfBytes);
+#pragma unroll
+        for (unsigned q = 0; q < F::kXSf; q += kSfBytes) copy_scales(sf + 4 + 4 * (q / kSfBytes), smem_u32(xsf0) + xt.i * F::kXSf + q);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_q8(tmem, a + 2u * k, b + 2u * k, idesc_q8(kTcM, N, k, false) | 5u << 7 /* A: E2M1 */, sf, sf + 4,
-                 kb != kb0 || k != 0 ? 1u : 0u);
-        mma_commit(empty0 + 8u * st.i);
+          mma_q8(tmem, da + 2u * k, db + 2u * k, idesc_q8(kTcM, N, k, false) | 5u << 7 /* A: E2M1 */, sf, sf + 4,
+                 b != 0 || k != 0 ? 1u : 0u);
+        mma_commit(wempty0 + 8u * st.i);
+        mma_commit(xempty0 + 8u * xt.i);
       }
       __syncwarp();
-      st.next();
     }
     if (elect_one()) {
       mma_commit(accf);
@@ -325,76 +322,112 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
     }
     __syncwarp();
   } else {
-    // ---------------------------------------------------------------- scales (and x)
-    const int group = warp / kQuads, own = warp % kQuads;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(own) * 32u << 16);
-    Ring st(S);
-    for (int i = 0; i < group; ++i) st.next();
-    for (int kb = kb0 + group; kb < kb1; kb += F::kGroups) {
-      ok = guard_wait(sfull0 + 8u * st.i, st.phase, ctl, p.guard, 74);
-      if constexpr (!PRE) {
-        // a place without a token keeps what it holds: its column of the result is not read
-        uint8_t *xs = smem + st.i * F::kStage + kWBytes;
-        uint8_t *ws = reinterpret_cast<uint8_t *>(words + st.i * N);
+    // ---------------------------------------------------------------- workers
+    // blocks warp, warp + S, ...; none where there is nothing to do with them
+    if (warp < S && (!PRE || !BOX)) {
+      Ring st(S), xt(XS);
+      for (int i = 0; i < warp; ++i) {
+        st.next();
+        xt.next();
+      }
+      // !BOX: the two aligned words that hold the scale bytes of rows 32 j + lane
+      uint32_t sw[4][2];
+      auto fetch = [&](int b) {
 #pragma unroll
-        for (int j = 0; j < NT / kQuads; ++j) {
-          const int t = own + kQuads * j, at = ((lane >> 2) ^ (t & 7)) * 16 + (lane & 3) * 4;
-          if (t >= ntok) break;
-          const uint2 raw = *reinterpret_cast<const uint2 *>(xs + (t + (lane >= 16 ? NT : 0)) * 128 + (lane & 15) * 8);
-          __syncwarp();
-          uint32_t h, l, b;
-          split4(raw, &h, &l, &b);
-          *reinterpret_cast<uint32_t *>(xs + t * 128 + at) = h;
-          *reinterpret_cast<uint32_t *>(xs + (NT + t) * 128 + at) = l;      // NT % 8 == 0: the same swizzle
-          if ((lane & 7) == 0) {
-            ws[4 * t + (lane >> 3)] = static_cast<uint8_t>(b);
-            ws[4 * (NT + t) + (lane >> 3)] = static_cast<uint8_t>(b - 4u);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const int f = 32 * j + lane;
+          const int64_t at = scale_at(f, b), from = at & ~int64_t(3);
+          const bool has = b < nb && f0 + f < p.out;
+          sw[j][0] = has ? load_now(reinterpret_cast<const uint32_t *>(p.scale + from)) : 0u;
+          // the scales end on 16 bytes
+          sw[j][1] = has && at != from && from + 4 < static_cast<int64_t>(p.experts) * p.out * G
+                         ? load_now(reinterpret_cast<const uint32_t *>(p.scale + from + 4)) : 0u;
         }
-        fence_async_proxy();
-        // all scale words are there; the four warps go on or leave together
-        ok = all_of<32 * kQuads>(1 + group, ok);
-      } else {
-        ok = __all_sync(0xffffffffu, ok);
+      };
+      if (!BOX) fetch(warp);
+      for (int b = warp; b < nb; b += S) {
+        if constexpr (!PRE) {
+          ok = guard_wait(xfull0 + 8u * xt.i, xt.phase, ctl, p.guard, 75);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          // a place without a token keeps what it holds: its column of the result is not read
+          uint8_t *xs = xs0 + xt.i * F::kXBytes, *sf = xsf0 + xt.i * F::kXSf;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t >= ntok) break;
+            const int to = ((lane >> 2) ^ (t & 7)) * 16 + (lane & 3) * 4;
+            const uint2 v = *reinterpret_cast<const uint2 *>(xs + (t + (lane >= 16 ? NT : 0)) * 128 + (lane & 15) * 8);
+            __syncwarp();
+            uint32_t h, l, sb;
+            split4(v, &h, &l, &sb);
+            *reinterpret_cast<uint32_t *>(xs + t * 128 + to) = h;
+            *reinterpret_cast<uint32_t *>(xs + (NT + t) * 128 + to) = l;      // NT % 8 == 0: the same swizzle
+            if ((lane & 7) == 0) {
+              sf[sf_at(t) + (lane >> 3)] = static_cast<uint8_t>(sb);
+              sf[sf_at(NT + t) + (lane >> 3)] = static_cast<uint8_t>(sb - 4u);
+            }
+          }
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(xready0 + 8u * xt.i);
+        }
+        if constexpr (!BOX) {
+          ok = guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 76);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          // 64 bytes of each of 128 rows, 64-byte swizzle; lane l has rows l, l + 32, ...
+          uint8_t *at = smem + st.i * kWBytes;
+          uint4 w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int f = 32 * (j / 4) + lane;
+            w[j] = *reinterpret_cast<const uint4 *>(at + f * 64 + (((j % 4) ^ ((f >> 1) & 3)) * 16));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            // 32 values: 8 bytes to each of chunks 2 c and 2 c + 1 of the row
+            const int f = 32 * (j / 4) + lane, c = j % 4;
+            *reinterpret_cast<uint2 *>(at + f * 128 + (((2 * c) ^ (f & 7)) * 16)) = make_uint2(w[j].x, w[j].y);
+            *reinterpret_cast<uint2 *>(at + f * 128 + (((2 * c + 1) ^ (f & 7)) * 16)) = make_uint2(w[j].z, w[j].w);
+          }
+          // past the last group of a row lies the next row's first
+          const int left = G - 4 * (kb0 + b);
+          const uint32_t none = left < 4 ? 0xffffffffu << (8 * left) : 0u;
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = (__funnelshift_r(sw[j][0], sw[j][1], 8 * static_cast<uint32_t>(scale_at(32 * j + lane, b) & 3)) & ~none) |
+                   (0x7f7f7f7fu & none);
+          *reinterpret_cast<uint4 *>(wsf0 + st.i * kSfBytes + 16 * lane) = make_uint4(v[0], v[1], v[2], v[3]);
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(wready0 + 8u * st.i);
+          fetch(b + S);
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          st.next();
+          xt.next();
+        }
       }
-      if (!ok) break;
-      uint32_t all[F::kSfStride] = {};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) all[j] = wscale[st.i * kTcM + 32 * j + lane];
-#pragma unroll
-      for (int j = 0; j < F::kXCols; ++j) {
-        const int n = 32 * j + lane;
-        if (PRE) all[4 + j] = n < NT ? words[st.i * NT + n] : words[st.i * NT + n - NT] - 0x04040404u;
-        else if (n < N) all[4 + j] = words[st.i * N + n];
-      }
-      tc_fence_after();
-      const uint32_t to = lane_addr + F::kSfCol + F::kSfStride * st.i;
-      const uint32_t lo[8] = {all[0], all[1], all[2], all[3], all[4], all[5], all[6], all[7]};
-      tmem_st8(to, lo);
-      if constexpr (F::kSfStride > 8) tmem_st4(to + 8, all[8], all[9], all[10], all[11]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(xfull0 + 8u * st.i);
-#pragma unroll
-      for (int i = 0; i < F::kGroups; ++i) st.next();
     }
     // ---------------------------------------------------------------- result
-    // into shared memory as [token][feature]: the stages are free once the
-    // last MMA is done
-    const bool got = guard_wait(accf, 0, ctl, p.guard, 75);
-    ok = __all_sync(0xffffffffu, got) && ok;
-    tc_fence_after();
-    float *part = reinterpret_cast<float *>(smem);
-    const int f = own * 32 + lane;
+    if (warp < 4) {
+      // into shared memory as [token][feature]: the blocks are free once the last MMA
+      // is done
+      const bool got = guard_wait(accf, 0, ctl, p.guard, 77);
+      ok = __all_sync(0xffffffffu, got) && ok;
+      tc_fence_after();
+      const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp) * 32u << 16);
+      float *part = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int c = 0; c < NT; c += 8) {
-      if (c < ntok && (c / 8) % F::kGroups == group) {
-        float a[8], b[8];
-        tmem_ld<8>(lane_addr + c, a);
-        tmem_ld<8>(lane_addr + NT + c, b);
+      for (int c = 0; c < NT; c += 8) {
+        if (c < ntok) {
+          float a[8], d[8];
+          tmem_ld<8>(lane_addr + c, a);
+          tmem_ld<8>(lane_addr + NT + c, d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[(c + i) * kTcM + f] = ok ? a[i] + b[i] : 0.0f;
+          for (int i = 0; i < 8; ++i) part[(c + i) * kTcM + 32 * warp + lane] = ok ? a[i] + d[i] : 0.0f;
+        }
       }
     }
   }
@@ -436,18 +469,6 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// a stack of weights [experts, out, in] in boxes of 128 x 128 values, 8 bytes of every 16 of the result
-bool map_w4(CUtensorMap *map, const void *base, int64_t experts, int64_t out, int64_t in) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(in), static_cast<cuuint64_t>(out), static_cast<cuuint64_t>(experts)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(in / 2) * static_cast<cuuint64_t>(out)};
-  cuuint32_t box[3] = {kKB, kTcM, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 // x [T, in] in boxes of NT rows x 64 columns, unswizzled
 bool map_x(CUtensorMap *map, const void *base, int64_t T, int64_t in, int nt) {
   EncodeTiledFn fn = encode_fn();
@@ -461,38 +482,93 @@ bool map_x(CUtensorMap *map, const void *base, int64_t T, int64_t in, int nt) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// a stack of weights [experts, out, in] in boxes of 128 x 128 values, 8 bytes of every 16 of the result
+bool map_w4(CUtensorMap *map, const void *base, int64_t experts, int64_t out, int64_t in) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(in), static_cast<cuuint64_t>(out), static_cast<cuuint64_t>(experts)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(in / 2) * static_cast<cuuint64_t>(out)};
+  cuuint32_t box[3] = {kKB, kTcM, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int NT, bool BOX>
-dora_status launch(const void *x, const void *wq, const Q4Params &p, int cluster, void *workspace, cudaStream_t cs) {
-  using F = Few<NT>;
-  CUtensorMap mW = {}, mX = {};
-  const int64_t all = static_cast<int64_t>(p.T) * p.in;
-  uint8_t *pieces = static_cast<uint8_t *>(workspace);
-  if (BOX && !map_w4(&mW, wq, p.experts, p.out, p.in)) return DORA_ERR_CUDA;
-  if (F::kSplit) {
-    if (!map_q8(&mX, pieces, 2 * static_cast<int64_t>(p.T), p.in, NT, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)) return DORA_ERR_CUDA;
-    const dim3 grid(static_cast<unsigned>(dora::ceil_div(p.in, 4 * kSplitThreads)), p.T < 65535 ? p.T : 65535);
-    q4_split_kernel<<<grid, kSplitThreads, 0, cs>>>(static_cast<const __nv_bfloat16 *>(x), p.T, p.in, pieces);
-    if (dora::launch_status() != DORA_OK) return DORA_ERR_CUDA;
-    dora::count_launches(1);
-  } else if (BOX && !map_x(&mX, x, p.T, p.in, NT)) {
-    return DORA_ERR_CUDA;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
+void few_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int64_t tiles, int cluster, cudaStream_t cs) {
+  using F = Few<NT, BOX>;
+  *cfg = cudaLaunchConfig_t{};
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * cluster));
-  cfg.blockDim = dim3(F::kThreads);
-  cfg.dynamicSmemBytes = F::kSmem;
-  cfg.stream = cs;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, q4_few_kernel<NT, BOX>, mW, mX, p, static_cast<const __nv_bfloat16 *>(x),
-                         static_cast<const uint8_t *>(wq), reinterpret_cast<const uint32_t *>(pieces + 2 * all)) != cudaSuccess) {
+  cfg->gridDim = dim3(static_cast<unsigned>(tiles * cluster));
+  cfg->blockDim = dim3(F::kThreads);
+  cfg->dynamicSmemBytes = F::kSmem;
+  cfg->stream = cs;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+// clusters of 2^`log` CTAs that are resident at once
+template <int NT, bool BOX> int resident_clusters(int device, int log) {
+  using F = Few<NT, BOX>;
+  static std::mutex mu;
+  static int known[64][4] = {};   // clusters + 1
+  std::lock_guard<std::mutex> lock(mu);
+  if (device < 0 || device >= 64) return 0;
+  int &k = known[device][log];
+  if (k == 0) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    few_config<NT, BOX>(&cfg, attr, 1, 1 << log, nullptr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, q4_few_kernel<NT, BOX>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    // the query counts one CTA an SM of these kernels, two run
+    int one = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&one, q4_few_kernel<NT, BOX>, F::kThreads, F::kSmem) != cudaSuccess || one < 1) one = 1;
+    k = n * F::kPerSm / one + 1;
+  }
+  return k - 1;
+}
+
+template <int NT, bool BOX>
+dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, int device, cudaStream_t cs) {
+  using F = Few<NT, BOX>;
+  const int64_t groups = p.offsets ? (p.experts < p.T ? p.experts : p.T) : 1;
+  const int64_t tiles = p.ftiles * (p.offsets ? p.T / NT + groups : 1);
+  // the k range over as many CTAs as keep all clusters resident
+  int log = 0;
+  const int64_t blocks = dora::ceil_div(p.in, kKB);
+  while (log < kMaxClusterLog && (2 << log) <= blocks && tiles <= resident_clusters<NT, BOX>(device, log + 1)) ++log;
+  if (tiles << log > kMaxDim) return DORA_ERR_SHAPE;
+  p.ntok = NT;
+  p.tiles = static_cast<int>(tiles);
+  CUtensorMap mW, mX;
+  const int64_t all = static_cast<int64_t>(p.T) * p.in;
+  uint8_t *pieces = static_cast<uint8_t *>(workspace);
+  if (!(BOX ? map_w4(&mW, wq, p.experts, p.out, p.in) : map_w(&mW, wq, p.experts, p.out, p.in, 64))) return DORA_ERR_CUDA;
+  if (F::kSplit) {
+    if (!map_q8(&mX, pieces, 2 * static_cast<int64_t>(p.T), p.in, NT, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)) return DORA_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(dora::ceil_div(p.in, 4 * kSplitThreads)), p.T < 65535 ? p.T : 65535);
+    q4_split_kernel<<<grid, kSplitThreads, 0, cs>>>(static_cast<const __nv_bfloat16 *>(x), p.T, p.in, pieces);
+    if (dora::launch_status() != DORA_OK) return DORA_ERR_CUDA;
+    dora::count_launches(1);
+  } else if (!map_x(&mX, x, p.T, p.in, NT)) {
+    return DORA_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  few_config<NT, BOX>(&cfg, attr, tiles, 1 << log, cs);
+  if (cudaLaunchKernelEx(&cfg, q4_few_kernel<NT, BOX>, mW, mX, p, static_cast<const uint8_t *>(wq),
+                         reinterpret_cast<const uint32_t *>(pieces + 2 * all)) !=
+      cudaSuccess) {
     cudaGetLastError();
     return DORA_ERR_CUDA;
   }
@@ -501,19 +577,10 @@ dora_status launch(const void *x, const void *wq, const Q4Params &p, int cluster
 }
 
 template <int NT>
-dora_status launch_few(const void *x, const void *wq, Q4Params p, void *workspace, int sms, cudaStream_t cs) {
-  const int64_t groups = p.offsets ? (p.experts < p.T ? p.experts : p.T) : 1;
-  const int64_t tiles = p.ftiles * (p.offsets ? p.T / NT + groups : dora::ceil_div(p.T, NT));
-  // the k range over as many CTAs as keep all clusters resident
-  int cluster = 1;
-  const int64_t blocks = dora::ceil_div(p.in, kKB);
-  while (cluster < kMaxCluster && tiles * cluster * 2 <= Few<NT>::kPerSm * sms && cluster * 2 <= blocks) cluster *= 2;
-  if (tiles * cluster > kMaxDim) return DORA_ERR_SHAPE;
-  p.ntok = NT;
-  p.tiles = static_cast<int>(tiles);
+dora_status launch(const void *x, const void *wq, const Q4Params &p, void *workspace, int device, cudaStream_t cs) {
   // boxes of 4-bit values take whole blocks of 128 and 32-byte rows
-  return p.in % kKB == 0 && dora::aligned(wq, 32) ? launch<NT, true>(x, wq, p, cluster, workspace, cs)
-                                                  : launch<NT, false>(x, wq, p, cluster, workspace, cs);
+  return p.in % kKB == 0 && dora::aligned(wq, 32) ? launch<NT, true>(x, wq, p, workspace, device, cs)
+                                                  : launch<NT, false>(x, wq, p, workspace, device, cs);
 }
 
 }  // namespace
@@ -521,7 +588,7 @@ dora_status launch_few(const void *x, const void *wq, Q4Params p, void *workspac
 namespace dora {
 
 size_t q4_few_workspace(int64_t T, int64_t in, int64_t per) {
-  return per <= 8 ? 0 : static_cast<size_t>(2 * T * in + T * 4 * ceil_div(in, kKB));
+  return per <= 8 ? 0 : static_cast<size_t>(2 * T * in + 8 * T * ceil_div(in, kKB));
 }
 
 dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
@@ -549,11 +616,11 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   p.y = static_cast<__nv_bfloat16 *>(y);
   p.ftiles = static_cast<int>(ceil_div(out, kTcM));
   const int64_t per = offsets ? q4_per(T, experts) : T;
-  if (per <= 8) return launch_few<8>(x, wq, p, workspace, info.sms, cs);
-  if (per <= 16) return launch_few<16>(x, wq, p, workspace, info.sms, cs);
-  if (per <= 32) return launch_few<32>(x, wq, p, workspace, info.sms, cs);
-  if (per <= 64) return launch_few<64>(x, wq, p, workspace, info.sms, cs);
-  return launch_few<128>(x, wq, p, workspace, info.sms, cs);
+  if (per <= 8) return launch<8>(x, wq, p, workspace, device, cs);
+  if (per <= 16) return launch<16>(x, wq, p, workspace, device, cs);
+  if (per <= 32) return launch<32>(x, wq, p, workspace, device, cs);
+  if (per <= 64) return launch<64>(x, wq, p, workspace, device, cs);
+  return launch<128>(x, wq, p, workspace, device, cs);
 }
 
 }  // namespace dora

@@ -451,19 +451,6 @@ dora_status mm_init(int device, Q4Params *p) {
   return tc_init(device, &p->guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
 }
 
-// the stack of weights [experts, out, in / 2 bytes] in boxes of 128 rows x 64 bytes, 64-byte swizzle
-bool map_w(CUtensorMap *map, const void *base, int64_t experts, int64_t out, int64_t in) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(out), static_cast<cuuint64_t>(experts)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(in / 2) * static_cast<cuuint64_t>(out)};
-  cuuint32_t box[3] = {64, 128, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool TRANS>
 dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T, int64_t out,
                        int64_t in, int64_t experts, void *y, dora_stream_t stream) {
@@ -502,7 +489,7 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
   if (tiles > kMaxDim) return DORA_ERR_SHAPE;
   p.tiles = static_cast<int>(tiles);
   CUtensorMap mW, mX;
-  if (!map_w(&mW, wq, experts, out, in) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.ntok / 2, 128)) return DORA_ERR_CUDA;
+  if (!map_w(&mW, wq, experts, out, in, 64) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.ntok / 2, 128)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   pair_config<TRANS>(&cfg, attr, p.ntok, p.tiles < pairs ? p.tiles : pairs, reinterpret_cast<cudaStream_t>(stream));
@@ -523,22 +510,20 @@ dora_status check(const void *x, const int32_t *offsets, const void *wq, const v
   if (!x || !wq || !wscale || !y) return DORA_ERR_NULL;
   // TMA: 16-byte aligned bases and row strides
   if (out % 16 != 0) return DORA_ERR_ALIGN;
-  if (!dora::aligned(x, 16) || !dora::aligned(wq, 16) || !dora::aligned(y, 16) || !dora::aligned(offsets, 4))
+  if (!dora::aligned(x, 16) || !dora::aligned(wq, 16) || !dora::aligned(y, 16) || !dora::aligned(wscale, 16) ||
+      !dora::aligned(offsets, 4))
     return DORA_ERR_ALIGN;
   return DORA_OK;
 }
 
 }  // namespace
 
-// few tokens a weight: q4_few.cu, where W is read as it is.  Rows that are no whole
-// blocks of 128 reach it by small copies, which fall behind sooner
-static bool few(int64_t T, int64_t in, int64_t experts) {
-  return dora::q4_per(T, experts) <= (in % kKB == 0 ? dora::kQ4Few : 16);
-}
+// few tokens a weight: q4_few.cu, where W is read as it is
+static bool few(int64_t T, int64_t experts) { return dora::q4_per(T, experts) <= dora::kQ4Few; }
 
 extern "C" size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {
   if (bad_size(T, 1) || bad_size(out, 1) || bad_size(in, 1) || experts < 1 || experts > kMaxExperts) return 0;
-  return few(T, in, experts) ? dora::q4_few_workspace(T, in, dora::q4_per(T, experts)) : 0;
+  return few(T, experts) ? dora::q4_few_workspace(T, in, dora::q4_per(T, experts)) : 0;
 }
 extern "C" size_t dora_matmul_q4_t_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
 
@@ -550,7 +535,7 @@ extern "C" dora_status dora_matmul_q4(const void *x, const int32_t *offsets, con
   if (st != DORA_OK || T == 0 || out == 0) return st;
   const size_t need = dora_matmul_q4_workspace(T, out, in, experts);
   if (need > 0 && (!workspace || !dora::aligned(workspace, 256) || workspace_bytes < need)) return DORA_ERR_WORKSPACE;
-  if (few(T, in, experts))
+  if (few(T, experts))
     return dora::matmul_q4_few(x, offsets, wq, wscale, T, out, in, experts, y, workspace,
                                reinterpret_cast<cudaStream_t>(stream));
   return run_matmul<false>(x, offsets, wq, wscale, T, out, in, experts, y, stream);
