@@ -156,6 +156,8 @@ def _ptr(x) -> int:
 
 
 _raw_stream = None   # torch's lookup of a device's current stream, as a raw handle
+_cuda = None         # torch.cuda, once torch is here
+_TYPES = ()          # torch's bfloat16, float32, int32, once torch is here
 _ACTS = {}           # torch dtype -> dora_dtype
 
 
@@ -172,6 +174,15 @@ def _stream(stream, device=None) -> int:
         import torch
         device = torch.cuda.current_device()
     return _raw_stream(device)
+
+
+def _types():
+    """torch.bfloat16, torch.float32, torch.int32.  An import statement in each call would
+    take as long as all its comparisons."""
+    global _TYPES
+    import torch
+    _TYPES = (torch.bfloat16, torch.float32, torch.int32)
+    return _TYPES
 
 
 def _act(t) -> int:
@@ -328,16 +339,19 @@ def _q8(name: str, rows: int, cols: int, block_rows: int, q, scale) -> None:
 def _addresses(name: str, stream, *ts) -> list[int]:
     """Device addresses of a call's tensors, which are dense and in the memory of
     the current device, as the kernels run there; then the stream's handle."""
+    global _cuda
     here = None
     for t in ts:
         if not t.is_contiguous():
             raise ValueError(f"{name}: tensors must be contiguous (row-major)")
-        if t.get_device() != here:
-            d = t.get_device()
+        d = t.get_device()
+        if d != here:
             if d < 0:
                 raise ValueError(f"libdora takes CUDA tensors (device memory); got one on {t.device}")
-            import torch
-            here = torch.cuda.current_device()
+            if _cuda is None:
+                import torch
+                _cuda = torch.cuda
+            here = _cuda.current_device()
             if d != here:
                 raise ValueError(f"{name}: a tensor on cuda:{d}, but the current device is cuda:{here}")
     return [t.data_ptr() for t in ts] + [_stream(stream, here)]
@@ -452,40 +466,37 @@ def dora_matmul_q8_t(dyq, dyscale, wq, wscale, dx, workspace=None, stream=None) 
     _matmul_q8("dora_matmul_q8_t", dyq, dyscale, wq, wscale, dx, workspace, stream, False)
 
 
-def _q4(name: str, lead, cols: int, q, scale) -> None:
-    """The shapes of a 4-bit form of [*lead, cols]; the C ABI sees only the matrix's."""
+def _q4(name: str, shape, q, scale) -> None:
+    """The shapes of a 4-bit form of a matrix or of a stack of them; the C ABI sees only
+    the matrix's."""
     if q.element_size() != 1 or scale.element_size() != 1:
         raise TypeError(f"{name}: the 4-bit form is bytes, got {q.dtype} and {scale.dtype}")
+    *lead, cols = shape
+    if not lead:
+        raise ValueError(f"{name}: a matrix or a stack of them, got {tuple(shape)}")
     if cols % 32:
         raise ValueError(f"{name}: the 4-bit form has rows of whole groups of 32 columns, got {cols}")
     if q.shape != (*lead, cols // 2) or scale.shape != (*lead, cols // 32):
-        raise ValueError(f"{name}: 4-bit form of {[*lead, cols]}: got q {tuple(q.shape)}, scale {tuple(scale.shape)}")
-
-
-def _q4_rows(name: str, x, q, scale) -> tuple[int, int]:
-    """Rows and columns of a matrix or of a stack of them; the form of either is checked."""
-    if x.dim() < 2:
-        raise ValueError(f"{name}: a matrix or a stack of them, got {tuple(x.shape)}")
-    cols = x.shape[-1]
-    _q4(name, x.shape[:-1], cols, q, scale)
-    return x.shape[:-1].numel(), cols
+        raise ValueError(f"{name}: 4-bit form of {list(shape)}: got q {tuple(q.shape)}, scale {tuple(scale.shape)}")
 
 
 def dora_q4_store(x, q, scale, stream=None) -> None:
     """x [..., rows, cols] into its 4-bit form: two E2M1 values a byte and a scale per
     32 columns of a row (see include/dora.h)."""
-    rows, cols = _q4_rows("dora_q4_store", x, q, scale)
+    shape = x.shape
+    _q4("dora_q4_store", shape, q, scale)
     act = _act(x)
     px, pq, psc, cs = _addresses("dora_q4_store", stream, x, q, scale)
-    _check("dora_q4_store", load_library().dora_q4_store(act, px, rows, cols, pq, psc, cs))
+    _check("dora_q4_store", load_library().dora_q4_store(act, px, shape[:-1].numel(), shape[-1], pq, psc, cs))
 
 
 def dora_q4_load(q, scale, x, stream=None) -> None:
     """The values of a 4-bit form into x (see include/dora.h)."""
-    rows, cols = _q4_rows("dora_q4_load", x, q, scale)
+    shape = x.shape
+    _q4("dora_q4_load", shape, q, scale)
     act = _act(x)
     px, pq, psc, cs = _addresses("dora_q4_load", stream, x, q, scale)
-    _check("dora_q4_load", load_library().dora_q4_load(act, pq, psc, rows, cols, px, cs))
+    _check("dora_q4_load", load_library().dora_q4_load(act, pq, psc, shape[:-1].numel(), shape[-1], px, cs))
 
 
 def dora_matmul_q4_workspace(T: int, out: int, inp: int, experts: int = 1) -> int:
@@ -497,27 +508,31 @@ def dora_matmul_q4_t_workspace(T: int, out: int, inp: int, experts: int = 1) -> 
 
 
 def _matmul_q4(name: str, x, wq, wscale, y, offsets, workspace, stream, out_side: bool) -> None:
-    import torch
-    if wq.dim() != (2 if offsets is None else 3):
-        raise ValueError(f"{name}: a weight [out, in / 2], or with offsets a stack [experts, out, in / 2], "
-                         f"got {tuple(wq.shape)}")
-    out, inp = wq.shape[-2], 2 * wq.shape[-1]
-    experts = 1 if offsets is None else wq.shape[0]
-    _q4(name, wq.shape[:-1], inp, wq, wscale)
-    T = x.shape[0]
-    _same(name, (T, inp if out_side else out), torch.bfloat16, x)
-    _same(name, (T, out if out_side else inp), torch.bfloat16, y)
+    bf16, _, i32 = _TYPES or _types()
+    xs, ws = x.shape, wq.shape
+    if len(ws) != (2 if offsets is None else 3):
+        raise ValueError(f"{name}: a weight [out, in / 2], or with offsets a stack [experts, out, in / 2], got {tuple(ws)}")
+    T, out, inp = xs[0], ws[-2], 2 * ws[-1]
+    k, n = (inp, out) if out_side else (out, inp)
+    if inp % 32 or wscale.shape != (*ws[:-1], inp // 32) or wq.element_size() != 1 or wscale.element_size() != 1:
+        _q4(name, (*ws[:-1], inp), wq, wscale)
+    if xs != (T, k) or x.dtype != bf16 or y.shape != (T, n) or y.dtype != bf16:
+        _same(name, (T, k), bf16, x)
+        _same(name, (T, n), bf16, y)
+    experts, nbytes = 1, 0
     ts = [x, wq, wscale, y]
     if offsets is not None:
-        _same(name, (experts + 1,), torch.int32, offsets)
+        experts = ws[0]
+        _same(name, (experts + 1,), i32, offsets)
         ts.append(offsets)
     if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
         ts.append(workspace)
     px, pw, psc, py, *more, cs = _addresses(name, stream, *ts)
     poff = more.pop(0) if offsets is not None else 0
-    st = getattr(load_library(), name)(px, poff, pw, psc, T, out, inp, experts, py, more[0] if more else 0,
-                                       0 if workspace is None else workspace.numel() * workspace.element_size(), cs)
-    _check(name, st)
+    st = getattr(load_library(), name)(px, poff, pw, psc, T, out, inp, experts, py, more[0] if more else 0, nbytes, cs)
+    if st:
+        _check(name, st)
 
 
 def dora_matmul_q4(x, wq, wscale, y, offsets=None, workspace=None, stream=None) -> None:
@@ -534,30 +549,34 @@ def dora_matmul_q4_t(dy, wq, wscale, dx, offsets=None, workspace=None, stream=No
 def dora_expert_sort(expert, experts: int, order, inverse, offsets, stream=None) -> None:
     """The entries of expert [T, k] sorted by expert, stably: order, its inverse and
     where each expert's begin (see include/dora.h)."""
-    import torch
-    if expert.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"dora_expert_sort: expert is int32 or int64, got {expert.dtype}")
+    i32 = (_TYPES or _types())[2]
+    if expert.dtype != i32:
+        import torch
+        if expert.dtype != torch.int64:
+            raise TypeError(f"dora_expert_sort: expert is int32 or int64, got {expert.dtype}")
     if not 1 <= experts <= 4096:
         raise ValueError(f"dora_expert_sort: 1 to 4096 experts, got {experts}")
     T, k = expert.shape
-    _same("dora_expert_sort", (T * k,), torch.int32, order)
-    _same("dora_expert_sort", (T, k), torch.int32, inverse)
-    _same("dora_expert_sort", (experts + 1,), torch.int32, offsets)
+    _same("dora_expert_sort", (T * k,), i32, order)
+    _same("dora_expert_sort", (T, k), i32, inverse)
+    _same("dora_expert_sort", (experts + 1,), i32, offsets)
     pe, po, pi, pf, cs = _addresses("dora_expert_sort", stream, expert, order, inverse, offsets)
     _check("dora_expert_sort", load_library().dora_expert_sort(expert.element_size(), pe, T, k, experts, po, pi, pf, cs))
 
 
 def _routed(name: str, x, xs, inverse, offsets) -> tuple[int, int, int, int]:
     """T, k, cols and the number of experts of tokens x [T, cols] and their rows xs [T k, cols]."""
-    import torch
+    i32 = (_TYPES or _types())[2]
     T, k = inverse.shape
-    cols, experts = x.shape[1], offsets.numel() - 1
-    if offsets.dim() != 1 or not 1 <= experts <= 4096:
-        raise ValueError(f"{name}: offsets are [experts + 1], 1 to 4096 experts, got {tuple(offsets.shape)}")
-    _same(name, (T, k), torch.int32, inverse)
-    _same(name, (experts + 1,), torch.int32, offsets)
-    _same(name, (T, cols), x.dtype, x)
-    _same(name, (T * k, cols), x.dtype, xs)
+    cols, so = x.shape[1], offsets.shape
+    experts = so[0] - 1
+    if len(so) != 1 or not 1 <= experts <= 4096:
+        raise ValueError(f"{name}: offsets are [experts + 1], 1 to 4096 experts, got {tuple(so)}")
+    if inverse.dtype != i32 or offsets.dtype != i32 or x.shape != (T, cols) or xs.shape != (T * k, cols) or xs.dtype != x.dtype:
+        _same(name, (T, k), i32, inverse)
+        _same(name, (experts + 1,), i32, offsets)
+        _same(name, (T, cols), x.dtype, x)
+        _same(name, (T * k, cols), x.dtype, xs)
     return T, k, cols, experts
 
 
@@ -571,12 +590,11 @@ def dora_expert_send(x, inverse, offsets, xs, stream=None) -> None:
 
 def dora_expert_return(ys, inverse, offsets, weight, y, stream=None) -> None:
     """y[t] = sum_j weight[t, j] ys[inverse[t, j]]; weight None: every one 1 (see include/dora.h)."""
-    import torch
     T, k, cols, experts = _routed("dora_expert_return", y, ys, inverse, offsets)
     act = _act(y)
     ts = [ys, y, inverse, offsets]
     if weight is not None:
-        _same("dora_expert_return", (T, k), torch.float32, weight)
+        _same("dora_expert_return", (T, k), _TYPES[1], weight)
         ts.append(weight)
     ps, py, pi, pf, *pw, cs = _addresses("dora_expert_return", stream, *ts)
     _check("dora_expert_return",
@@ -585,10 +603,9 @@ def dora_expert_return(ys, inverse, offsets, weight, y, stream=None) -> None:
 
 def dora_expert_return_bwd(dy, ys, inverse, offsets, weight, d_ys, d_weight, stream=None) -> None:
     """d_ys[inverse[t, j]] = weight[t, j] dy[t], d_weight[t, j] = <dy[t], ys[inverse[t, j]]> (see include/dora.h)."""
-    import torch
     T, k, cols, experts = _routed("dora_expert_return_bwd", dy, ys, inverse, offsets)
     _same("dora_expert_return_bwd", (T * k, cols), dy.dtype, d_ys)
-    _same("dora_expert_return_bwd", (T, k), torch.float32, weight, d_weight)
+    _same("dora_expert_return_bwd", (T, k), _TYPES[1], weight, d_weight)
     act = _act(dy)
     pd, ps, pi, pf, pw, pds, pdw, cs = _addresses("dora_expert_return_bwd", stream, dy, ys, inverse, offsets, weight,
                                                   d_ys, d_weight)
