@@ -435,6 +435,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
   // before the split has ended
   if (PRE) pdl_wait();
   tc_fence_before();
+  __syncwarp();   // the cluster's barrier takes whole warps
   if (csize > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
@@ -458,6 +459,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
             make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
     }
   }
+  __syncwarp();
   if (csize > 1) cluster_sync();   // no CTA leaves while another reads its part
   else __syncthreads();
   if (warp == F::kMma) {

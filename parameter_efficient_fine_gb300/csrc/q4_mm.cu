@@ -20,8 +20,8 @@
 //   warp 0       TMA: tokens into the stages
 //   warp 1       tensor memory, MMA issue (even CTA)
 //   warp 2       TMA: blocks of W into a ring of their own
-//   warps 3-10   conversion, two groups, each one half of every block's k
-//   warps 11-18  the result
+//   warps 3-14   conversion, three groups taking turns at the stages
+//   warps 15-22  the result
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -44,7 +44,7 @@ constexpr int kTileF = 256;                           // features per tile
 constexpr int kTileT = 256;                           // most tokens per tile
 constexpr unsigned kRawBytes = 128 * kKB / 2;         // 8 KB
 constexpr unsigned kPanel = kKS * 128;                // 8 KB: 64 rows of 64 bf16
-constexpr int kGroups = 2, kGroupWarps = 4;           // conversion
+constexpr int kGroups = 3, kGroupWarps = 4;           // conversion
 constexpr int kConvWarps = kGroups * kGroupWarps, kOutWarps = 8;
 constexpr int kConv0 = 3, kOut0 = kConv0 + kConvWarps;
 constexpr int kThreadsMm = 32 * (kOut0 + kOutWarps);
@@ -57,10 +57,12 @@ template <bool TRANS> __host__ __device__ constexpr unsigned stage_size(int ntok
 }
 // stages and blocks of W in flight.  x W^T: a stage is 32 columns of tensor memory,
 // of which the accumulator leaves 256
-template <bool TRANS> constexpr int kStages = TRANS ? 6 : 8;
-template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 8;
-// a group converts every kGroups-th stage, so it visits every use of its slots in turn
-static_assert(kStages<false> % kGroups == 0 && kStages<true> % kGroups == 0, "slots of a group");
+constexpr int kStages = 6;
+template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 6;
+// a wait goes by the parity of a phase, so a group visits every use of the slots that
+// it visits: with three groups taking turns at the stages, two to a block, each comes
+// to two of any three consecutive blocks
+static_assert(kGroups == 3 && kStages % 3 == 0 && kRaw<false> % 3 == 0 && kRaw<true> % 3 == 0, "slots of a group");
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -126,28 +128,27 @@ __device__ __forceinline__ uint64_t sdesc_mmajor(uint32_t saddr) {
 template <bool TRANS>
 __global__ void __launch_bounds__(kThreadsMm, 1)
 q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p) {
-  constexpr int S = kStages<TRANS>, R = kRaw<TRANS>;
+  constexpr int S = kStages, R = kRaw<TRANS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t xbox = tok_box(p.ntok), stage_bytes = stage_size<TRANS>(p.ntok);
   uint8_t *raw = smem + S * stage_bytes;
   uint64_t *bars = reinterpret_cast<uint64_t *>(raw + R * kRawBytes);
-  // barriers (a pair uses the even CTA's full and accumulator empty): tokens full,
+  // barriers (a pair uses the even CTA's full and accumulator empty): tokens here and
   // W converted, empty; raw full and empty; accumulator full and empty; end
-  const uint32_t tfull0 = smem_u32(bars), wfull0 = tfull0 + 8u * S, empty0 = wfull0 + 8u * S, rfull0 = empty0 + 8u * S,
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, rfull0 = empty0 + 8u * S,
                  rempty0 = rfull0 + 8u * R, accf = rempty0 + 8u * R, acce = accf + 16, fin = acce + 16;
-  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 3 * S + 2 * R + 5);
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * S + 2 * R + 5);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(tfull0 + 8u * s, 1);
-      mbar_init(wfull0 + 8u * s, 2 * kGroupWarps);
+      mbar_init(full0 + 8u * s, 1 + 2 * kGroupWarps);   // the copies; a group of either CTA
       mbar_init(empty0 + 8u * s, 1);
     }
     for (int s = 0; s < R; ++s) {
       mbar_init(rfull0 + 8u * s, 1);
-      mbar_init(rempty0 + 8u * s, kConvWarps);
+      mbar_init(rempty0 + 8u * s, 2 * kGroupWarps);     // two stages
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf + 8u * b, 1);
@@ -186,7 +187,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t fb = tfull0 + 8u * st.i;
+          const uint32_t fb = full0 + 8u * st.i;
           // the even CTA's barrier counts both CTAs' bytes
           if (rank == 0) mbar_expect_tx(fb, 2 * xbox);
           tma_load_2d_pair(smem_u32(smem) + (st.i + 1) * stage_bytes - xbox, &mX, s * kKS, t0, mapa_shared(fb, 0));
@@ -241,14 +242,13 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       bool ok = true;
       Ring st(S);
       Acc acc(TRANS, p.ntok);
-      const uint32_t peer_off = mapa_shared(tfull0, peer) - tfull0;   // to the peer's copy of a barrier
+      const uint32_t peer_off = mapa_shared(full0, peer) - full0;   // to the peer's copy of a barrier
       const uint32_t id = idesc_bf16_pair(p.ntok) | (TRANS ? 1u << 15 : 0u);
       for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
         ok = guard_wait(acce + 8u * acc.i, acc.phase ^ 1u, ctl, p.guard, 63);
         const uint32_t d = tmem + acc.column();
         for (int s = 0; s < 2 * blocks; ++s) {
-          ok = ok && guard_wait(tfull0 + 8u * st.i, st.phase, ctl, p.guard, 64);
-          ok = ok && guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 65);
+          ok = ok && guard_wait(full0 + 8u * st.i, st.phase, ctl, p.guard, 64);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -281,68 +281,72 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     }
   } else if (warp < kOut0) {
     // ---------------------------------------------------------------- conversion
-    // group g: the g-th half of every block's k, 64 values a thread
+    // 64 values a thread: a row of the block, a half of it
     const int g = (warp - kConv0) / kGroupWarps, i = (warp & 3) * 32 + lane;
-    const int r = TRANS ? kKS * g + (i & 63) : i, panel = TRANS ? i >> 6 : g;    // row of the block, half of it
     const int G = p.in / kQ4Group;
     const bool words = G % 2 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 1) == 0;
-    const uint32_t from = smem_u32(raw) + static_cast<uint32_t>(r) * 64u;
-    const uint32_t c0 = static_cast<uint32_t>((2 * panel) ^ ((r >> 1) & 3)) * 16u, c1 = c0 ^ 16u;
-    const uint32_t to = TRANS ? smem_u32(smem) + panel * kPanel + (i & 63) * 128u
+    const uint32_t to = TRANS ? smem_u32(smem) + (i >> 6) * kPanel + (i & 63) * 128u
                               : tmem + kACol + (static_cast<uint32_t>(warp & 3) * 32u << 16);
     bool ok = true;
-    Ring st(S), rw(R);
-    if (g == 1) st.next();
-    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+    int u = g;                                     // stage, counted over all tiles
+    for (int t = pair, u0 = 0; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, u0 += 2 * blocks) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
-      // the two scale bytes of this thread's part of block s
-      auto scales = [&](int s) -> uint32_t {
-        const int row = TRANS ? s * kKB + r : f0 + r, q = (TRANS ? f0 : s * kKB) / kQ4Group + 2 * panel;
-        if (row >= p.out || q >= G) return 0x7f7fu;
-        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + row) * G + q;
+      // stage q of the tile is half h = q % 2 of the k of block q / 2.  Row of the block
+      // and half of its columns: features x k, or k x features
+      auto row = [&](int q) { return TRANS ? kKS * (q & 1) + (i & 63) : i; };
+      auto half = [&](int q) { return TRANS ? i >> 6 : q & 1; };
+      // the two scale bytes of this thread's part
+      auto scales = [&](int q) -> uint32_t {
+        const int f = TRANS ? (q >> 1) * kKB + row(q) : f0 + row(q), c = (TRANS ? f0 : (q >> 1) * kKB) / kQ4Group + 2 * half(q);
+        if (q >= 2 * blocks || f >= p.out || c >= G) return 0x7f7fu;
+        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + f) * G + c;
         if (words) return load_now16(at);
-        return load_now(at) | (q + 1 < G ? load_now(at + 1) : 127u) << 8;
+        return load_now(at) | (c + 1 < G ? load_now(at + 1) : 127u) << 8;
       };
+      const int q0 = u - u0;                       // this group's first stage of the tile
       uint32_t sc[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) sc[u] = u < blocks ? scales(u) : 0u;
-      for (int s0 = 0; s0 < blocks && ok; s0 += kAhead) {
+      for (int k = 0; k < kAhead; ++k) sc[k] = scales(q0 + k * kGroups);
+      for (int qa = q0; qa < 2 * blocks && ok; qa += kAhead * kGroups) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int s = s0 + u;
-          if (s >= blocks || !ok) break;
-          const uint32_t b = sc[u];
-          if (s + kAhead < blocks) sc[u] = scales(s + kAhead);
-          ok = guard_wait(rfull0 + 8u * rw.i, rw.phase, ctl, p.guard, 66);
+        for (int k = 0; k < kAhead; ++k) {
+          const int q = qa + k * kGroups;
+          if (q >= 2 * blocks || !ok) break;
+          const uint32_t b = sc[k];
+          sc[k] = scales(q + kAhead * kGroups);
+          const int slot = (u >> 1) % R, stage = u % S;
+          const uint32_t rphase = static_cast<uint32_t>((u >> 1) / R) & 1u, sphase = static_cast<uint32_t>(u / S) & 1u;
+          ok = guard_wait(rfull0 + 8u * slot, rphase, ctl, p.guard, 66);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint4 w0 = lds128(from + rw.i * kRawBytes + c0), w1 = lds128(from + rw.i * kRawBytes + c1);
+          const int r = row(q);
+          const uint32_t from = smem_u32(raw) + slot * kRawBytes + static_cast<uint32_t>(r) * 64u,
+                         c0 = static_cast<uint32_t>((2 * half(q)) ^ ((r >> 1) & 3)) * 16u;
+          const uint4 w0 = lds128(from + c0), w1 = lds128(from + (c0 ^ 16u));
           uint32_t v[32];
           q4_bf16x32(w0, b & 255u, v);
           q4_bf16x32(w1, b >> 8, v + 16);
           __syncwarp();
-          if (lane == 0) mbar_arrive(rempty0 + 8u * rw.i);
-          ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 67);
+          if (lane == 0) mbar_arrive(rempty0 + 8u * slot);
+          ok = guard_wait(empty0 + 8u * stage, sphase ^ 1u, ctl, p.guard, 67);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (TRANS) {
-            const uint32_t dst = to + st.i * stage_bytes;
+            const uint32_t dst = to + stage * stage_bytes;
 #pragma unroll
             for (int c = 0; c < 8; ++c) sts128(dst + static_cast<uint32_t>((c ^ (r & 7)) * 16), v + 4 * c);
             fence_async_proxy();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(mapa_shared(wfull0 + 8u * st.i, 0));
+            if (lane == 0) mbar_arrive_pair(mapa_shared(full0 + 8u * stage, 0));
           } else {
             tc_fence_after();
-            tmem_st32(to + 32u * st.i, v);
+            tmem_st32(to + 32u * stage, v);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(wfull0 + 8u * st.i, 0));
+            if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(full0 + 8u * stage, 0));
           }
-          rw.next();
-          st.next();
-          st.next();
+          u += kGroups;
         }
       }
     }
@@ -388,6 +392,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   }
   tc_fence_before();
   __syncthreads();
+  __syncwarp();   // the cluster's barrier takes whole warps
   // the even CTA's MMAs, which read this CTA's shared memory and write its
   // tensor memory, are complete, and both CTAs' results are out
   cluster_sync();
@@ -402,10 +407,10 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 // host side
 // ---------------------------------------------------------------------------
 template <bool TRANS> constexpr size_t pair_smem(int ntok) {
-  return 1024 + kRaw<TRANS> * kRawBytes + 512 + kStages<TRANS> * static_cast<size_t>(stage_size<TRANS>(ntok));
+  return 1024 + kRaw<TRANS> * kRawBytes + 512 + kStages * static_cast<size_t>(stage_size<TRANS>(ntok));
 }
 template <bool TRANS> constexpr bool fits() {
-  return pair_smem<TRANS>(kTileT) <= kSmemMax && 8 * (3 * kStages<TRANS> + 2 * kRaw<TRANS> + 5) + sizeof(SharedCtl) <= 512;
+  return pair_smem<TRANS>(kTileT) <= kSmemMax && 8 * (2 * kStages + 2 * kRaw<TRANS> + 5) + sizeof(SharedCtl) <= 512;
 }
 static_assert(fits<false>() && fits<true>(), "rings, barriers and control words");
 
