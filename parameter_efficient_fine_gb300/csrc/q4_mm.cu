@@ -125,6 +125,18 @@ __device__ __forceinline__ uint64_t sdesc_mmajor(uint32_t saddr) {
   return (sdesc<32>(saddr) & ~(static_cast<uint64_t>(0x3fff) << 16)) | (static_cast<uint64_t>(kPanel >> 4) << 16);
 }
 
+// A tile, or a part of its k where the tiles are few: blocks b0 to b0 + nb
+struct Unit : Tile {
+  int part, b0, nb;
+};
+__device__ __forceinline__ bool find_unit(const Q4Params &p, int u, Unit *o) {
+  const int t = p.parts > 1 ? u / p.parts : u, blocks = (p.kdim + kKB - 1) / kKB;
+  o->part = u - t * p.parts;
+  o->b0 = blocks * o->part / p.parts;
+  o->nb = blocks * (o->part + 1) / p.parts - o->b0;
+  return t < p.tiles && find_tile(p, t, o);
+}
+
 template <bool TRANS>
 __global__ void __launch_bounds__(kThreadsMm, 1)
 q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p) {
@@ -173,16 +185,15 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   pdl_trigger();
   pdl_wait();       // the set-up above overlaps the end of the launch before
   const int pair = static_cast<int>(blockIdx.x / 2), npairs = static_cast<int>(gridDim.x / 2);
-  const int blocks = (p.kdim + kKB - 1) / kKB;     // of W, two stages each
-  Tile o;
+  Unit o;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- tokens
     bool ok = !loads_withheld(p.guard), issued = false;
     Ring st(S);
-    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+    for (int t = pair; ok && find_unit(p, t, &o); t += npairs) {
       const int t0 = o.t0 + static_cast<int>(rank) * (p.ntok / 2);
-      for (int s = 0; s < 2 * blocks; ++s) {
+      for (int s = 2 * o.b0; s < 2 * (o.b0 + o.nb); ++s) {
         ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 62);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -209,9 +220,9 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     bool ok = !loads_withheld(p.guard);
     int issued = 0;
     Ring rw(R);
-    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs) {
+    for (int t = pair; ok && find_unit(p, t, &o); t += npairs) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
-      for (int s = 0; s < blocks; ++s) {
+      for (int s = o.b0; s < o.b0 + o.nb; ++s) {
         ok = guard_wait(rempty0 + 8u * rw.i, rw.phase ^ 1u, ctl, p.guard, 61);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -244,32 +255,42 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       Acc acc(TRANS, p.ntok);
       const uint32_t peer_off = mapa_shared(full0, peer) - full0;   // to the peer's copy of a barrier
       const uint32_t id = idesc_bf16_pair(p.ntok) | (TRANS ? 1u << 15 : 0u);
-      for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
+      for (int t = pair; ok && find_unit(p, t, &o); t += npairs, acc.next()) {
         ok = guard_wait(acce + 8u * acc.i, acc.phase ^ 1u, ctl, p.guard, 63);
         const uint32_t d = tmem + acc.column();
-        for (int s = 0; s < 2 * blocks; ++s) {
+        for (int s = 0; s < o.nb; ++s) {
+          // both stages of a block at once: a wait between two stages' MMAs costs this
+          // warp more than a wait behind another
+          Ring nx = st;
+          nx.next();
           ok = ok && guard_wait(full0 + 8u * st.i, st.phase, ctl, p.guard, 64);
+          ok = ok && guard_wait(full0 + 8u * nx.i, nx.phase, ctl, p.guard, 65);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = smem_u32(smem) + st.i * stage_bytes;
-          const uint64_t b = sdesc<32>(at + stage_bytes - xbox);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t more = s != 0 || k != 0 ? 1u : 0u;
-              // 16 k: 32 bytes along a K-major row, 16 rows of an M-major panel, 8 columns
-              if (TRANS) mma_bf16_ss_pair(d, sdesc_mmajor(at) + 128u * k, b + 2u * k, id, more);
-              else mma_bf16_ts_pair(d, tmem + kACol + 32u * st.i + 8u * k, b + 2u * k, id, more);
+            for (int h = 0; h < 2; ++h) {
+              const int i = h ? nx.i : st.i;
+              const uint32_t at = smem_u32(smem) + i * stage_bytes;
+              const uint64_t b = sdesc<32>(at + stage_bytes - xbox);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t more = s != 0 || h != 0 || k != 0 ? 1u : 0u;
+                // 16 k: 32 bytes along a K-major row, 16 rows of an M-major panel, 8 columns
+                if (TRANS) mma_bf16_ss_pair(d, sdesc_mmajor(at) + 128u * k, b + 2u * k, id, more);
+                else mma_bf16_ts_pair(d, tmem + kACol + 32u * i + 8u * k, b + 2u * k, id, more);
+              }
+              mma_commit_pair(empty0 + 8u * i);
+              mma_commit_pair(empty0 + 8u * i + peer_off);
             }
-            mma_commit_pair(empty0 + 8u * st.i);
-            mma_commit_pair(empty0 + 8u * st.i + peer_off);
-            if (s + 1 == 2 * blocks) {
+            if (s + 1 == o.nb) {
               mma_commit_pair(accf + 8u * acc.i);
               mma_commit_pair(accf + 8u * acc.i + peer_off);
             }
           }
           __syncwarp();
+          st.next();
           st.next();
         }
       }
@@ -289,29 +310,30 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
                               : tmem + kACol + (static_cast<uint32_t>(warp & 3) * 32u << 16);
     bool ok = true;
     int u = g;                                     // stage, counted over all tiles
-    for (int t = pair, u0 = 0; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, u0 += 2 * blocks) {
+    for (int t = pair, u0 = 0; ok && find_unit(p, t, &o); t += npairs, u0 += 2 * o.nb) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
-      // stage q of the tile is half h = q % 2 of the k of block q / 2.  Row of the block
+      // stage q of the unit is half h = q % 2 of the k of its block q / 2.  Row of the block
       // and half of its columns: features x k, or k x features
       auto row = [&](int q) { return TRANS ? kKS * (q & 1) + (i & 63) : i; };
       auto half = [&](int q) { return TRANS ? i >> 6 : q & 1; };
       // the two scale bytes of this thread's part
       auto scales = [&](int q) -> uint32_t {
-        const int f = TRANS ? (q >> 1) * kKB + row(q) : f0 + row(q), c = (TRANS ? f0 : (q >> 1) * kKB) / kQ4Group + 2 * half(q);
-        if (q >= 2 * blocks || f >= p.out || c >= G) return 0x7f7fu;
+        const int k = (o.b0 + (q >> 1)) * kKB;
+        const int f = TRANS ? k + row(q) : f0 + row(q), c = (TRANS ? f0 : k) / kQ4Group + 2 * half(q);
+        if (q >= 2 * o.nb || f >= p.out || c >= G) return 0x7f7fu;
         const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + f) * G + c;
         if (words) return load_now16(at);
         return load_now(at) | (c + 1 < G ? load_now(at + 1) : 127u) << 8;
       };
-      const int q0 = u - u0;                       // this group's first stage of the tile
+      const int q0 = u - u0;                       // this group's first stage of the unit
       uint32_t sc[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) sc[k] = scales(q0 + k * kGroups);
-      for (int qa = q0; qa < 2 * blocks && ok; qa += kAhead * kGroups) {
+      for (int qa = q0; qa < 2 * o.nb && ok; qa += kAhead * kGroups) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const int q = qa + k * kGroups;
-          if (q >= 2 * blocks || !ok) break;
+          if (q >= 2 * o.nb || !ok) break;
           const uint32_t b = sc[k];
           sc[k] = scales(q + kAhead * kGroups);
           const int slot = (u >> 1) % R, stage = u % S;
@@ -359,34 +381,59 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
     bool ok = true;
     Acc acc(TRANS, p.ntok);
-    for (int t = pair; ok && t < p.tiles && find_tile(p, t, &o); t += npairs, acc.next()) {
+    for (int t = pair; ok && find_unit(p, t, &o); t += npairs, acc.next()) {
       ok = guard_wait(accf + 8u * acc.i, acc.phase, ctl, p.guard, 68);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t v[kTileT / 4];                      // two tokens a register
-#pragma unroll
-      for (int c = 0; c < kTileT / 2; c += 8)
-        if (c < half) {
-          float f[8];
-          tmem_ld<8>(lane_addr + acc.column() + static_cast<uint32_t>(c), f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[c / 2 + i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-        }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(acce + 8u * acc.i, 0));
       const int f = o.ft * kTileF + static_cast<int>(rank) * 128 + static_cast<int>(quad) * 32 + lane;
-      const int t0 = o.t0 + c0;
-      if (f < p.nfeat) {
-        uint16_t *y = reinterpret_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0) * p.nfeat + f;
-        const int64_t ld = p.nfeat;
-        const int live = min(o.t1 - t0, half);
+      const int t0 = o.t0 + c0, live = min(o.t1 - t0, half);
+      const int64_t ld = p.nfeat;
+      if (p.parts > 1) {
+        float *to = p.partial + (static_cast<int64_t>(o.part) * p.T + t0) * ld + f;
+#pragma unroll 1
+        for (int c = 0; c < half; c += 16, to += 16 * ld) {
+          float w[16];
+          tmem_ld<16>(lane_addr + acc.column() + static_cast<uint32_t>(c), w);
+          if (f < p.nfeat)
 #pragma unroll
-        for (int i = 0; i < kTileT / 4; ++i, y += 2 * ld) {
-          if (2 * i < live) y[0] = static_cast<uint16_t>(v[i]);
-          if (2 * i + 1 < live) y[ld] = static_cast<uint16_t>(v[i] >> 16);
+            for (int i = 0; i < 16; ++i)
+              if (c + i < live) to[i * ld] = w[i];
+          __syncwarp();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(acce + 8u * acc.i, 0));
+        continue;
+      }
+      // in two goes, for which there are registers
+      const int quarter = half / 2;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[kTileT / 8];                    // two tokens a register
+#pragma unroll
+        for (int c = 0; c < kTileT / 4; c += 8)
+          if (c < quarter) {
+            float w[8];
+            tmem_ld<8>(lane_addr + acc.column() + static_cast<uint32_t>(h * quarter + c), w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[c / 2 + i] = pack_bf16x2(w[2 * i], w[2 * i + 1]);
+          }
+        if (h == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(acce + 8u * acc.i, 0));
+        }
+        if (f < p.nfeat) {
+          uint16_t *y = reinterpret_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0 + h * quarter) * ld + f;
+          const int n = min(live - h * quarter, quarter);
+#pragma unroll
+          for (int i = 0; i < kTileT / 8; ++i, y += 2 * ld) {
+            if (2 * i < n) y[0] = static_cast<uint16_t>(v[i]);
+            if (2 * i + 1 < n) y[ld] = static_cast<uint16_t>(v[i] >> 16);
+          }
+        }
+        __syncwarp();
       }
     }
   }
@@ -403,9 +450,65 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   }
 }
 
+// the sum of a tile's parts in their order, rounded once; rows that no expert has are
+// left as they are
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
+q4_join_kernel(const float4 *__restrict__ parts, int n, int T, int quads, const int *__restrict__ offsets, int experts,
+               uint2 *__restrict__ y) {
+  pdl_trigger();
+  pdl_wait();
+  const int a = offsets ? min(max(offsets[0], 0), T) : 0, b = offsets ? min(max(offsets[experts], a), T) : T;
+  const int64_t all = static_cast<int64_t>(T) * quads, end = static_cast<int64_t>(b) * quads;
+  for (int64_t i = static_cast<int64_t>(a) * quads + blockIdx.x * kJoinThreads + threadIdx.x; i < end;
+       i += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
+    float4 s = parts[i];
+    for (int k = 1; k < n; ++k) {
+      const float4 v = parts[k * all + i];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    y[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+// Tokens per tile and parts of k: the least time, in us, of the waves of units over
+// the pairs that a GB300 holds, a fixed number so that the workspace is the same
+// everywhere.  A block of k takes a pair about as long with 32 tokens as with 256;
+// parts cost their way through memory and a launch.  Experts: half a tile more each
+// than their tokens fill, and of two plans alike the wider tiles, which even loads
+// suit
+struct Plan {
+  int ntok, parts;
+};
+Plan plan(bool trans, int64_t T, int64_t nfeat, int64_t kdim, int64_t experts) {
+  constexpr int kPairs = 76;
+  const int64_t groups = experts < T ? experts : T, ftiles = dora::ceil_div(nfeat, kTileF), blocks = dora::ceil_div(kdim, kKB);
+  Plan best = {kTileT, 1};
+  double least = 0;
+  for (int n = 32; n <= kTileT; n += 32)
+    for (int parts = 1; parts <= 8; ++parts) {
+      if (parts > 1 && blocks < 4 * parts) break;
+      const int64_t tiles = ftiles * (experts > 1 ? (T + groups * n / 2) / n + 1 : dora::ceil_div(T, n));
+      const double block = (trans ? 0.68 : 0.6) + (experts > 1 ? -0.0001 : 0.0003) * n;
+      double cost = static_cast<double>(dora::ceil_div(tiles * parts, kPairs)) * (dora::ceil_div(blocks, parts) * block + 1.5);
+      if (parts > 1) cost += 2.5 + static_cast<double>(parts) * T * nfeat * 8 / 5e6;
+      if (least == 0 || cost < least) {
+        least = cost;
+        best = {n, parts};
+      }
+    }
+  return best;
+}
+size_t parts_bytes(const Plan &pl, int64_t T, int64_t nfeat) {
+  return pl.parts > 1 ? static_cast<size_t>(pl.parts) * T * nfeat * 4 : 0;
+}
+
 template <bool TRANS> constexpr size_t pair_smem(int ntok) {
   return 1024 + kRaw<TRANS> * kRawBytes + 512 + kStages * static_cast<size_t>(stage_size<TRANS>(ntok));
 }
@@ -458,7 +561,7 @@ dora_status mm_init(int device, Q4Params *p) {
 
 template <bool TRANS>
 dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T, int64_t out,
-                       int64_t in, int64_t experts, void *y, dora_stream_t stream) {
+                       int64_t in, int64_t experts, void *y, void *workspace, dora_stream_t stream) {
   dora::DeviceInfo info;
   int device = 0;
   dora_status st = dora::current_device(&info, &device);
@@ -478,27 +581,36 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
   const int pairs = resident_pairs(device, info.sms);
   if (pairs == 0) return DORA_ERR_CUDA;
   p.ftiles = static_cast<int>(dora::ceil_div(p.nfeat, kTileF));
-  // tokens per tile: the least time over the waves of tiles.  Experts: as if their
-  // loads were even
-  const int64_t groups = offsets ? (experts < T ? experts : T) : 1, per = dora::ceil_div(T, groups);
-  int64_t best = 0;
-  for (int n = 32; n <= kTileT; n += 32) {
-    const int64_t waves = dora::ceil_div(p.ftiles * groups * dora::ceil_div(per, n), pairs);
-    const int64_t cost = waves * (n + 100);
-    if (best == 0 || cost < best) {
-      best = cost;
-      p.ntok = n;
-    }
-  }
-  const int64_t tiles = p.ftiles * (offsets ? T / p.ntok + groups : dora::ceil_div(T, p.ntok));
-  if (tiles > kMaxDim) return DORA_ERR_SHAPE;
+  const Plan pl = plan(TRANS, T, p.nfeat, p.kdim, experts);
+  p.ntok = pl.ntok;
+  p.parts = pl.parts;
+  p.partial = static_cast<float *>(workspace);
+  const int64_t tiles = p.ftiles * (offsets ? T / p.ntok + (experts < T ? experts : T) : dora::ceil_div(T, p.ntok));
+  if (tiles * p.parts > kMaxDim) return DORA_ERR_SHAPE;
   p.tiles = static_cast<int>(tiles);
+  const int64_t units = tiles * p.parts;
   CUtensorMap mW, mX;
   if (!map_w(&mW, wq, experts, out, in, 64) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.ntok / 2, 128)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  pair_config<TRANS>(&cfg, attr, p.ntok, p.tiles < pairs ? p.tiles : pairs, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  pair_config<TRANS>(&cfg, attr, p.ntok, units < pairs ? units : pairs, cs);
   if (cudaLaunchKernelEx(&cfg, q4_pair_kernel<TRANS>, mW, mX, p) != cudaSuccess) {
+    cudaGetLastError();
+    return DORA_ERR_CUDA;
+  }
+  dora::count_launches(1);
+  if (p.parts == 1) return DORA_OK;
+  const int quads = p.nfeat / 4;
+  const int64_t all = dora::ceil_div(T * quads, kJoinThreads), most = 8 * static_cast<int64_t>(info.sms);
+  cudaLaunchConfig_t jc = {};
+  jc.gridDim = dim3(static_cast<unsigned>(all < most ? all : most));
+  jc.blockDim = dim3(kJoinThreads);
+  jc.stream = cs;
+  jc.attrs = attr + 1;   // a programmatic dependent launch
+  jc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&jc, q4_join_kernel, static_cast<const float4 *>(workspace), p.parts, p.T, quads, offsets, p.experts,
+                         static_cast<uint2 *>(y)) != cudaSuccess) {
     cudaGetLastError();
     return DORA_ERR_CUDA;
   }
@@ -523,14 +635,27 @@ dora_status check(const void *x, const int32_t *offsets, const void *wq, const v
 
 }  // namespace
 
-// few tokens a weight: q4_few.cu, where W is read as it is
-static bool few(int64_t T, int64_t experts) { return dora::q4_per(T, experts) <= dora::kQ4Few; }
+// few tokens a weight: q4_few.cu, where W is read as it is.  64, or 128 where a tile a
+// pair is all that the pairs would have
+static bool few(int64_t T, int64_t out, int64_t experts) {
+  const int64_t per = dora::q4_per(T, experts), groups = experts < T ? experts : T;
+  return per <= dora::kQ4Few / 2 || (per <= dora::kQ4Few && dora::ceil_div(out, kTileF) * groups <= 76);
+}
+static bool bad_call(int64_t T, int64_t out, int64_t in, int64_t experts) {
+  return bad_size(T, 1) || bad_size(out, 1) || bad_size(in, 1) || experts < 1 || experts > kMaxExperts;
+}
 
 extern "C" size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {
-  if (bad_size(T, 1) || bad_size(out, 1) || bad_size(in, 1) || experts < 1 || experts > kMaxExperts) return 0;
-  return few(T, experts) ? dora::q4_few_workspace(T, in, dora::q4_per(T, experts)) : 0;
+  if (bad_call(T, out, in, experts)) return 0;
+  if (few(T, out, experts)) return dora::q4_few_workspace(T, in, dora::q4_per(T, experts));
+  return parts_bytes(plan(false, T, out, in, experts), T, out);
 }
-extern "C" size_t dora_matmul_q4_t_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
+extern "C" size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {
+  return bad_call(T, out, in, experts) ? 0 : parts_bytes(plan(true, T, in, out, experts), T, in);
+}
+static bool short_of(size_t need, const void *workspace, size_t bytes) {
+  return need > 0 && (!workspace || !dora::aligned(workspace, 256) || bytes < need);
+}
 
 extern "C" dora_status dora_matmul_q4(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
                                       int64_t out, int64_t in, int64_t experts, void *y, void *workspace,
@@ -538,19 +663,19 @@ extern "C" dora_status dora_matmul_q4(const void *x, const int32_t *offsets, con
   if (in < 1) return DORA_ERR_SHAPE;
   const dora_status st = check(x, offsets, wq, wscale, T, out, in, experts, y);
   if (st != DORA_OK || T == 0 || out == 0) return st;
-  const size_t need = dora_matmul_q4_workspace(T, out, in, experts);
-  if (need > 0 && (!workspace || !dora::aligned(workspace, 256) || workspace_bytes < need)) return DORA_ERR_WORKSPACE;
-  if (few(T, experts))
+  if (short_of(dora_matmul_q4_workspace(T, out, in, experts), workspace, workspace_bytes)) return DORA_ERR_WORKSPACE;
+  if (few(T, out, experts))
     return dora::matmul_q4_few(x, offsets, wq, wscale, T, out, in, experts, y, workspace,
                                reinterpret_cast<cudaStream_t>(stream));
-  return run_matmul<false>(x, offsets, wq, wscale, T, out, in, experts, y, stream);
+  return run_matmul<false>(x, offsets, wq, wscale, T, out, in, experts, y, workspace, stream);
 }
 
 extern "C" dora_status dora_matmul_q4_t(const void *dy, const int32_t *offsets, const void *wq, const void *wscale,
-                                        int64_t T, int64_t out, int64_t in, int64_t experts, void *dx, void *, size_t,
-                                        dora_stream_t stream) {
+                                        int64_t T, int64_t out, int64_t in, int64_t experts, void *dx, void *workspace,
+                                        size_t workspace_bytes, dora_stream_t stream) {
   if (out < 1) return DORA_ERR_SHAPE;
   const dora_status st = check(dy, offsets, wq, wscale, T, out, in, experts, dx);
   if (st != DORA_OK || T == 0 || in == 0) return st;
-  return run_matmul<true>(dy, offsets, wq, wscale, T, out, in, experts, dx, stream);
+  if (short_of(dora_matmul_q4_t_workspace(T, out, in, experts), workspace, workspace_bytes)) return DORA_ERR_WORKSPACE;
+  return run_matmul<true>(dy, offsets, wq, wscale, T, out, in, experts, dx, workspace, stream);
 }

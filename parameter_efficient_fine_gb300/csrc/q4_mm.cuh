@@ -23,10 +23,11 @@ struct Q4Params {
   int experts;
   const int *offsets;               // null: one weight, all rows
   int ntok;                         // tokens per tile
-  int ftiles;
+  int ftiles, parts;                // feature tiles; parts that k is cut into
   int tiles;                        // no more than these
   const uint8_t *scale;
   __nv_bfloat16 *y;
+  float *partial;                   // results of the parts [parts, T, nfeat]
   Guard guard;
 };
 
