@@ -629,6 +629,14 @@ dora_status dora_expert_return_bwd(dora_dtype act, const void *dy, const void *y
                                    int64_t cols, int64_t experts, void *d_ys, float *d_weight,
                                    dora_stream_t stream);
 
+/*
+ * Zeros in the rows of x [rows, cols] (of `act`) that no expert has: those before
+ * offsets[0] and from offsets[experts] on, for callers who read them.
+ *   Sizes: rows >= 0 (0 is a no-op), below 2^31 - 1024; the rest as dora_expert_send.
+ */
+dora_status dora_expert_clear(dora_dtype act, void *x, const int32_t *offsets, int64_t rows, int64_t cols,
+                              int64_t experts, dora_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* diagnostics                                                               */
 /* ------------------------------------------------------------------------ */

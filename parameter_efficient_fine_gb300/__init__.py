@@ -52,6 +52,7 @@ __all__ = [
     "dora_expert_send",
     "dora_expert_return",
     "dora_expert_return_bwd",
+    "dora_expert_clear",
     "dora_device_error",
     "dora_kernel_launches",
     "dora_test_stall_loads",
@@ -110,6 +111,7 @@ _SIGNATURES = {
     "dora_expert_sort": (_int, [_int, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "dora_expert_send": (_int, [_int, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
     "dora_expert_return": (_int, [_int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
+    "dora_expert_clear": (_int, [_int, _vp, _vp, _i64, _i64, _i64, _vp]),
     "dora_expert_return_bwd": (_int, [_int, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp]),
     "dora_device_error": (_int, [ctypes.POINTER(_int)]),
     "dora_kernel_launches": (ctypes.c_uint64, []),
@@ -611,6 +613,18 @@ def dora_expert_return_bwd(dy, ys, inverse, offsets, weight, d_ys, d_weight, str
                                                   d_ys, d_weight)
     _check("dora_expert_return_bwd",
            load_library().dora_expert_return_bwd(act, pd, ps, pi, pf, pw, T, k, cols, experts, pds, pdw, cs))
+
+
+def dora_expert_clear(x, offsets, stream=None) -> None:
+    """Zeros in the rows of x [rows, cols] that no expert has (see include/dora.h)."""
+    rows, cols = x.shape
+    experts = offsets.shape[0] - 1
+    _same("dora_expert_clear", (experts + 1,), (_TYPES or _types())[2], offsets)
+    if not 1 <= experts <= 4096:
+        raise ValueError(f"dora_expert_clear: offsets are [experts + 1], 1 to 4096 experts, got {tuple(offsets.shape)}")
+    act = _act(x)
+    px, pf, cs = _addresses("dora_expert_clear", stream, x, offsets)
+    _check("dora_expert_clear", load_library().dora_expert_clear(act, px, pf, rows, cols, experts, cs))
 
 
 def dora_device_error() -> int:

@@ -5,6 +5,7 @@
 //   dora_expert_return      y[t] = sum_j weight[t, j] ys[inverse[t, j]]
 //   dora_expert_return_bwd  d_ys[inverse[t, j]] = weight[t, j] dy[t],
 //                           d_weight[t, j] = <dy[t], ys[inverse[t, j]]>
+//   dora_expert_clear       zeros in the rows that no expert has
 //
 // The gradient of send is return without weights.  An entry whose expert is
 // outside [0, experts) goes to no expert: its row lies behind the last expert's,
@@ -214,6 +215,18 @@ expert_return_bwd_kernel(const Act *__restrict__ dy, const Act *__restrict__ ys,
   }
 }
 
+// rows [rows, cols] of no expert: before the first's and behind the last's.  `Word`
+// divides a row
+template <typename Word>
+__global__ void __launch_bounds__(kThreads)
+expert_clear_kernel(Word *__restrict__ x, int64_t rows, int64_t words, const int *__restrict__ offsets, int experts) {
+  const int64_t first = min(static_cast<int64_t>(max(offsets[0], 0)), rows),
+                end = min(max(static_cast<int64_t>(offsets[experts]), first), rows);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads, i0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  for (int64_t i = i0; i < first * words; i += step) x[i] = Word{};
+  for (int64_t i = end * words + i0; i < rows * words; i += step) x[i] = Word{};
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -373,4 +386,28 @@ extern "C" dora_status dora_expert_return_bwd(dora_dtype act, const void *dy, co
   const RouteParams p = params(inverse, offsets, T, k, cols, experts);
   return act == DORA_BF16 ? run_return_bwd<__nv_bfloat16>(dy, ys, weight, p, d_ys, d_weight, device, info.sms, cs)
                           : run_return_bwd<float>(dy, ys, weight, p, d_ys, d_weight, device, info.sms, cs);
+}
+
+extern "C" dora_status dora_expert_clear(dora_dtype act, void *x, const int32_t *offsets, int64_t rows, int64_t cols,
+                                         int64_t experts, dora_stream_t stream) {
+  if (!valid_dtype(act)) return DORA_ERR_DTYPE;
+  if (bad_rows(rows, 1, cols, experts)) return DORA_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return DORA_OK;
+  if (!x || !offsets) return DORA_ERR_NULL;
+  if (bad_elem(act, x) || !dora::aligned(offsets, 4)) return DORA_ERR_ALIGN;
+  dora::DeviceInfo info;
+  const dora_status st = dora::current_device(&info, nullptr);
+  if (st != DORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t bytes = cols * (act == DORA_BF16 ? 2 : 4);
+  const bool wide = bytes % 16 == 0 && dora::aligned(x, 16);
+  const int64_t words = wide ? bytes / 16 : bytes / 2, all = dora::ceil_div(rows * words, kThreads), most = 4 * info.sms;
+  const unsigned grid = static_cast<unsigned>(all < most ? all : most);
+  if (wide)
+    expert_clear_kernel<uint4><<<grid, kThreads, 0, cs>>>(static_cast<uint4 *>(x), rows, words, offsets, static_cast<int>(experts));
+  else
+    expert_clear_kernel<uint16_t><<<grid, kThreads, 0, cs>>>(static_cast<uint16_t *>(x), rows, words, offsets,
+                                                             static_cast<int>(experts));
+  dora::count_launches(1);
+  return dora::launch_status();
 }

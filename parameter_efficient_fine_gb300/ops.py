@@ -3,7 +3,7 @@
 The custom ops; each allocates its outputs (and the library's workspace)
 with torch and calls the C entry points of the same names on the current CUDA
 stream.  No arithmetic happens here but the low-rank products of linear_q8 and
-of its backward, which are torch's:
+linear_q4 and of their backward, which are torch's:
 
   torch.ops.dora.norm_factored(W0, A, B, m, s) -> (norm, g)
   torch.ops.dora.row_sumsq(W0) -> n0sq                       (bf16 W0: ||W0_i||^2, once)
@@ -20,6 +20,15 @@ of its backward, which are torch's:
   torch.ops.dora.matmul_q8_t(dyq, dyscale, wq, wscale) -> dx   (dy W)
   torch.ops.dora.lora_grad_q8(dxa, xq, xscale) -> dA           (dxa^T x)
   torch.ops.dora.linear_q8(x, wq, wscale, A, B, m, g, norm, s) -> (y, ...)    (the layer on those)
+  torch.ops.dora.q4_store(x) -> (q, scale)                     (x in 4 bits: E2M1, a scale per 32)
+  torch.ops.dora.q4_load(q, scale, dtype) -> x
+  torch.ops.dora.matmul_q4(x, wq, wscale, offsets) -> y        (x W^T, W in 4 bits, or by expert)
+  torch.ops.dora.matmul_q4_t(dy, wq, wscale, offsets) -> dx    (dy W)
+  torch.ops.dora.linear_q4(x, wq, wscale, A, B, m, g, norm, s) -> (y, ...)    (the layer on those)
+  torch.ops.dora.expert_sort(expert, experts) -> (order, inverse, offsets)
+  torch.ops.dora.expert_send(x, inverse, offsets) -> xs        (tokens' rows by expert)
+  torch.ops.dora.expert_return(ys, inverse, offsets, weight) -> y             (their weighted sums)
+  torch.ops.dora.expert_return_bwd(dy, ys, inverse, offsets, weight) -> (d_ys, d_weight)
 
 ``compose`` is differentiable in base, lora and m.  It takes m beside g (the
 norm op's output g = m / norm) so that autograd can deliver dL/dm: with the
@@ -43,24 +52,35 @@ backward is x and v in 8 bits and xa.  It is differentiable in x, A, B and m;
 rounding to 8 bits passes gradients through unchanged, and dy g (the gradient
 of base) is itself rounded to 8 bits for dx.
 
+``matmul_q4`` is differentiable in x (its gradient is matmul_q4_t),
+``expert_send`` in x and ``expert_return`` in ys and weight.  Rows of their
+outputs that no expert has are 0.  ``linear_q4`` is ``linear_q8`` on a frozen
+weight in 4 bits: its products take x and dy g as they are, in bfloat16; x and
+v are kept in 8 bits as there.
+
 Inputs must be contiguous, row-major and on one CUDA device (the C ABI's
 layout); m, n0sq, norm and g are float32, the weights float32 (bfloat16 for
 the _bf16 norm and row_sumsq), activations float32 or bfloat16.
 """
 from __future__ import annotations
 
+from typing import Optional
+
 import torch
 from torch import Tensor
 
 from . import (dora_compose_bwd, dora_compose_bwd_q8, dora_compose_bwd_q8_workspace, dora_compose_bwd_workspace,
-               dora_compose_fwd, dora_compose_fwd_q8, dora_lora_grad_q8, dora_lora_grad_q8_workspace, dora_matmul_q8,
-               dora_matmul_q8_t, dora_norm_factored, dora_norm_factored_bf16, dora_norm_factored_bf16_workspace,
-               dora_norm_factored_bwd, dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_q8_load,
-               dora_q8_store, dora_row_sumsq_bf16)
+               dora_compose_fwd, dora_compose_fwd_q8, dora_expert_clear, dora_expert_return, dora_expert_return_bwd, dora_expert_send,
+               dora_expert_sort, dora_lora_grad_q8, dora_lora_grad_q8_workspace, dora_matmul_q4, dora_matmul_q4_t,
+               dora_matmul_q4_t_workspace, dora_matmul_q4_workspace, dora_matmul_q8, dora_matmul_q8_t,
+               dora_norm_factored, dora_norm_factored_bf16, dora_norm_factored_bf16_workspace,
+               dora_norm_factored_bwd, dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_q4_load,
+               dora_q4_store, dora_q8_load, dora_q8_store, dora_row_sumsq_bf16)
 
 __all__ = ["norm_factored", "row_sumsq", "norm_factored_bf16", "compose", "compose_bwd", "norm_factored_bwd",
            "module", "dora_module", "q8_store", "q8_load", "compose_q8", "compose_bwd_q8", "matmul_q8", "matmul_q8_t",
-           "lora_grad_q8", "linear_q8", "dora_linear_q8"]
+           "lora_grad_q8", "linear_q8", "dora_linear_q8", "q4_store", "q4_load", "matmul_q4", "matmul_q4_t", "linear_q4",
+           "dora_linear_q4", "expert_sort", "expert_send", "expert_return", "expert_return_bwd", "experts_q4"]
 
 
 def _contig(name: str, *ts: Tensor) -> None:
@@ -473,3 +493,302 @@ def dora_linear_q8(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, 
     and m do.  in and out are multiples of 16; where A takes a gradient, the rank
     is a multiple of 8 up to 1024.  What does not fit is refused by this call."""
     return linear_q8(x, wq, wscale, A, B, m, g, norm, s)[0]
+
+
+# ---------------------------------------------------------------------------
+# 4 bits: E2M1 with a power-of-two scale per 32 columns (include/dora.h)
+# ---------------------------------------------------------------------------
+def _q4_shapes(x: Tensor) -> tuple[list[int], list[int]]:
+    *lead, cols = x.shape
+    if not lead or cols % 32:
+        raise ValueError(f"dora: a 4-bit form has rows of whole groups of 32 columns, got {tuple(x.shape)}")
+    return [*lead, cols // 2], [*lead, cols // 32]
+
+
+@torch.library.custom_op("dora::q4_store", mutates_args=(), device_types="cuda")
+def q4_store(x: Tensor) -> tuple[Tensor, Tensor]:
+    """x [..., rows, cols] in 4 bits: (q, scale), a scale per 32 columns of a row."""
+    _contig("q4_store", x)
+    q, scale = (torch.empty(s, dtype=torch.uint8, device=x.device) for s in _q4_shapes(x))
+    dora_q4_store(x, q, scale)
+    return q, scale
+
+
+@q4_store.register_fake
+def _q4_store_fake(x):
+    q, scale = _q4_shapes(x)
+    return x.new_empty(q, dtype=torch.uint8), x.new_empty(scale, dtype=torch.uint8)
+
+
+@torch.library.custom_op("dora::q4_load", mutates_args=(), device_types="cuda")
+def q4_load(q: Tensor, scale: Tensor, dtype: torch.dtype) -> Tensor:
+    """The values of a 4-bit form, float32 or bfloat16."""
+    _contig("q4_load", q, scale)
+    x = torch.empty((*q.shape[:-1], 2 * q.shape[-1]), dtype=dtype, device=q.device)
+    dora_q4_load(q, scale, x)
+    return x
+
+
+@q4_load.register_fake
+def _q4_load_fake(q, scale, dtype):
+    return q.new_empty((*q.shape[:-1], 2 * q.shape[-1]), dtype=dtype)
+
+
+@torch.library.custom_op("dora::matmul_q4", mutates_args=(), device_types="cuda")
+def matmul_q4(x: Tensor, wq: Tensor, wscale: Tensor, offsets: Optional[Tensor] = None) -> Tensor:
+    """x W^T for a bfloat16 x and W in 4 bits; with offsets (expert_sort) W is a stack and
+    x's rows are sorted by expert."""
+    _contig("matmul_q4", x, wq, wscale)
+    out, inp = wq.shape[-2], 2 * wq.shape[-1]
+    y = torch.empty(x.shape[0], out, dtype=torch.bfloat16, device=x.device)
+    n = dora_matmul_q4_workspace(x.shape[0], out, inp, 1 if offsets is None else wq.shape[0])
+    dora_matmul_q4(x, wq, wscale, y, offsets, _workspace(n, x) if n else None)
+    if offsets is not None:
+        dora_expert_clear(y, offsets)
+    return y
+
+
+@matmul_q4.register_fake
+def _matmul_q4_fake(x, wq, wscale, offsets=None):
+    return x.new_empty(x.shape[0], wq.shape[-2], dtype=torch.bfloat16)
+
+
+@torch.library.custom_op("dora::matmul_q4_t", mutates_args=(), device_types="cuda")
+def matmul_q4_t(dy: Tensor, wq: Tensor, wscale: Tensor, offsets: Optional[Tensor] = None) -> Tensor:
+    """dy W for a bfloat16 dy and the same W."""
+    _contig("matmul_q4_t", dy, wq, wscale)
+    out, inp = wq.shape[-2], 2 * wq.shape[-1]
+    dx = torch.empty(dy.shape[0], inp, dtype=torch.bfloat16, device=dy.device)
+    n = dora_matmul_q4_t_workspace(dy.shape[0], out, inp, 1 if offsets is None else wq.shape[0])
+    dora_matmul_q4_t(dy, wq, wscale, dx, offsets, _workspace(n, dy) if n else None)
+    if offsets is not None:
+        dora_expert_clear(dx, offsets)
+    return dx
+
+
+@matmul_q4_t.register_fake
+def _matmul_q4_t_fake(dy, wq, wscale, offsets=None):
+    return dy.new_empty(dy.shape[0], 2 * wq.shape[-1], dtype=torch.bfloat16)
+
+
+def _matmul_q4_setup(ctx, inputs, output):
+    _, wq, wscale, offsets = inputs
+    ctx.save_for_backward(wq, wscale, offsets)
+
+
+def _matmul_q4_backward(ctx, dy):
+    return matmul_q4_t(dy.contiguous(), *ctx.saved_tensors), None, None, None
+
+
+matmul_q4.register_autograd(_matmul_q4_backward, setup_context=_matmul_q4_setup)
+
+
+def _linear_q4_check(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, g: Tensor) -> None:
+    """What the layer's forward takes; the same eagerly and while it is traced."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"dora::linear_q4: x is bfloat16, got {x.dtype}")
+    if wq.element_size() != 1 or wscale.element_size() != 1:
+        raise TypeError(f"dora::linear_q4: the 4-bit weight is bytes, got {wq.dtype} and {wscale.dtype}")
+    if x.dim() != 2 or wq.dim() != 2 or A.dim() != 2:
+        raise ValueError(f"dora::linear_q4: x [T, in], wq [out, in / 2] and A [r, in] are matrices, got {tuple(x.shape)}, "
+                         f"{tuple(wq.shape)}, {tuple(A.shape)}")
+    out, inp, r = wq.shape[0], 2 * wq.shape[1], A.shape[0]
+    if out % 16 or inp % 32:
+        raise ValueError(f"dora::linear_q4: in is a multiple of 32 and out of 16, got {inp} and {out}")
+    for name, t, want in (("x", x, (x.shape[0], inp)), ("wscale", wscale, (out, inp // 32)), ("A", A, (r, inp)),
+                          ("B", B, (out, r)), ("g", g, (out,))):
+        if t.shape != want:
+            raise ValueError(f"dora::linear_q4: {name} is {want} for a weight [{out}, {inp}] and rank {r}, got {tuple(t.shape)}")
+    if g.dtype != torch.float32:
+        raise ValueError(f"dora::linear_q4: g is float32, got {g.dtype}")
+
+
+@torch.library.custom_op("dora::linear_q4", mutates_args=(), device_types="cuda")
+def linear_q4(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Tensor, g: Tensor, norm: Tensor,
+              s: float) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
+    """The layer's output y and what its backward needs: (y, xq, xscale, vq, vscale, xa)."""
+    _linear_q4_check(x, wq, wscale, A, B, g)
+    xq, xscale = q8_store(x, 1)
+    xa = x @ A.to(x.dtype).t()
+    y, vq, vscale = compose_q8(matmul_q4(x, wq, wscale), xa @ B.to(x.dtype).t(), m, g, norm, s)
+    return y, xq, xscale, vq, vscale, xa
+
+
+@linear_q4.register_fake
+def _linear_q4_fake(x, wq, wscale, A, B, m, g, norm, s):
+    _linear_q4_check(x, wq, wscale, A, B, g)
+    T, inp = x.shape
+    out = wq.shape[0]
+    u8 = torch.uint8
+    return (x.new_empty(T, out), x.new_empty(T, inp, dtype=u8), x.new_empty(_scale_shape(T, inp, 1), dtype=u8),
+            x.new_empty(T, out, dtype=u8), x.new_empty(_scale_shape(T, out, 1), dtype=u8), x.new_empty(T, A.shape[0]))
+
+
+def _linear_q4_setup(ctx, inputs, output):
+    _, wq, wscale, A, B, m, g, norm, s = inputs
+    _, xq, xscale, vq, vscale, xa = output
+    # what the backward alone needs is refused by the call that leads to it
+    r, (out,) = A.shape[0], g.shape
+    if ctx.needs_input_grad[3] and (r % 8 or not 1 <= r <= 1024):
+        raise ValueError(f"dora::linear_q4: a gradient of A takes a rank of 8, 16, ... 1024, got {r}")
+    if ctx.needs_input_grad[5] and m.shape != (out,):
+        raise ValueError(f"dora::linear_q4: m is ({out},), got {tuple(m.shape)}")
+    if norm.shape != (out,) or norm.dtype != torch.float32:
+        raise ValueError(f"dora::linear_q4: norm is ({out},) of float32, got {tuple(norm.shape)} of {norm.dtype}")
+    ctx.save_for_backward(xq, xscale, vq, vscale, xa, wq, wscale, A, B, g, norm)
+    ctx.s = s
+    ctx.mark_non_differentiable(xq, xscale, vq, vscale, xa)
+
+
+def _linear_q4_backward(ctx, dy, *_):
+    xq, xscale, vq, vscale, xa, wq, wscale, A, B, g, norm = ctx.saved_tensors
+    need = ctx.needs_input_grad
+    d_base, d_lora, d_mag = compose_bwd_q8(dy.contiguous(), vq, vscale, g, norm, ctx.s)
+    dx = dA = dB = None
+    # dB and dxa leave their products in bfloat16, as in linear_q8; dx is the bfloat16
+    # sum of two such results
+    if need[4]:
+        dB = (d_lora.t() @ xa).to(B.dtype)
+    if need[0] or need[3]:
+        dxa = d_lora @ B.to(d_lora.dtype)
+        if need[3]:
+            dA = lora_grad_q8(dxa, xq, xscale).to(A.dtype)
+        if need[0]:
+            dx = matmul_q4_t(d_base, wq, wscale) + dxa @ A.to(dxa.dtype)
+    return dx, None, None, dA, dB, d_mag, None, None, None
+
+
+linear_q4.register_autograd(_linear_q4_backward, setup_context=_linear_q4_setup)
+
+
+def dora_linear_q4(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Tensor, g: Tensor, norm: Tensor,
+                   s: float) -> Tensor:
+    """y = g (x W0^T + s x A^T B^T) for a bfloat16 x and a frozen W0 in 4 bits (q4_store(W0)).
+
+    norm and g = m / norm come from one of the norm ops on the values of the 4-bit
+    weight (q4_load is exact in bfloat16) and carry no gradient; x, A, B and m do.  in is
+    a multiple of 32 and out of 16; where A takes a gradient, the rank is a multiple of 8
+    up to 1024.  Where nothing takes a gradient, nothing is kept for one: serving a token
+    is the products and a compose."""
+    if not (torch.is_grad_enabled() and any(t.requires_grad for t in (x, A, B, m))):
+        _linear_q4_check(x, wq, wscale, A, B, g)
+        lora = (x @ A.to(x.dtype).t()) @ B.to(x.dtype).t()
+        return compose(matmul_q4(x, wq, wscale), lora, m, g, norm, s)
+    return linear_q4(x, wq, wscale, A, B, m, g, norm, s)[0]
+
+
+# ---------------------------------------------------------------------------
+# tokens sorted by expert and back
+# ---------------------------------------------------------------------------
+@torch.library.custom_op("dora::expert_sort", mutates_args=(), device_types="cuda")
+def expert_sort(expert: Tensor, experts: int) -> tuple[Tensor, Tensor, Tensor]:
+    """The entries of expert [T, k] (int32 or int64) sorted by expert, stably: (order
+    [T k], inverse [T, k], offsets [experts + 1]), int32.  An entry outside
+    [0, experts) goes to no expert, behind all that do."""
+    _contig("expert_sort", expert)
+    T, k = expert.shape
+    i32 = dict(dtype=torch.int32, device=expert.device)
+    order, inverse, offsets = torch.empty(T * k, **i32), torch.empty(T, k, **i32), torch.empty(experts + 1, **i32)
+    dora_expert_sort(expert, experts, order, inverse, offsets)
+    return order, inverse, offsets
+
+
+@expert_sort.register_fake
+def _expert_sort_fake(expert, experts):
+    T, k = expert.shape
+    i32 = torch.int32
+    return expert.new_empty(T * k, dtype=i32), expert.new_empty(T, k, dtype=i32), expert.new_empty(experts + 1, dtype=i32)
+
+
+@torch.library.custom_op("dora::expert_return", mutates_args=(), device_types="cuda")
+def expert_return(ys: Tensor, inverse: Tensor, offsets: Tensor, weight: Optional[Tensor] = None) -> Tensor:
+    """y[t] = sum_j weight[t, j] ys[inverse[t, j]] over the entries that have an expert;
+    without weights the plain sum."""
+    _contig("expert_return", ys, inverse, offsets)
+    y = torch.empty(inverse.shape[0], ys.shape[1], dtype=ys.dtype, device=ys.device)
+    dora_expert_return(ys, inverse, offsets, None if weight is None else weight.contiguous(), y)
+    return y
+
+
+@expert_return.register_fake
+def _expert_return_fake(ys, inverse, offsets, weight=None):
+    return ys.new_empty(inverse.shape[0], ys.shape[1])
+
+
+@torch.library.custom_op("dora::expert_send", mutates_args=(), device_types="cuda")
+def expert_send(x: Tensor, inverse: Tensor, offsets: Tensor) -> Tensor:
+    """xs[inverse[t, j]] = x[t], the tokens' rows sorted by expert."""
+    _contig("expert_send", x, inverse, offsets)
+    xs = torch.empty(inverse.numel(), x.shape[1], dtype=x.dtype, device=x.device)
+    dora_expert_send(x, inverse, offsets, xs)
+    dora_expert_clear(xs, offsets)
+    return xs
+
+
+@expert_send.register_fake
+def _expert_send_fake(x, inverse, offsets):
+    return x.new_empty(inverse.numel(), x.shape[1])
+
+
+def _expert_send_setup(ctx, inputs, output):
+    ctx.save_for_backward(inputs[1], inputs[2])
+
+
+def _expert_send_backward(ctx, d_xs):
+    return expert_return(d_xs.contiguous(), *ctx.saved_tensors), None, None
+
+
+expert_send.register_autograd(_expert_send_backward, setup_context=_expert_send_setup)
+
+
+@torch.library.custom_op("dora::expert_return_bwd", mutates_args=(), device_types="cuda")
+def expert_return_bwd(dy: Tensor, ys: Tensor, inverse: Tensor, offsets: Tensor, weight: Tensor) -> tuple[Tensor, Tensor]:
+    """d_ys[inverse[t, j]] = weight[t, j] dy[t], d_weight[t, j] = <dy[t], ys[inverse[t, j]]>."""
+    _contig("expert_return_bwd", dy, ys, inverse, offsets, weight)
+    d_ys, d_weight = torch.empty_like(ys), torch.empty_like(weight)
+    dora_expert_return_bwd(dy, ys, inverse, offsets, weight, d_ys, d_weight)
+    dora_expert_clear(d_ys, offsets)
+    return d_ys, d_weight
+
+
+@expert_return_bwd.register_fake
+def _expert_return_bwd_fake(dy, ys, inverse, offsets, weight):
+    return torch.empty_like(ys), torch.empty_like(weight)
+
+
+def _expert_return_setup(ctx, inputs, output):
+    ys, inverse, offsets, weight = inputs
+    # without weights the gradient of ys is the sending of dy
+    ctx.save_for_backward(None if weight is None else ys, inverse, offsets, weight)
+
+
+def _expert_return_backward(ctx, dy):
+    ys, inverse, offsets, weight = ctx.saved_tensors
+    if weight is None:
+        return expert_send(dy.contiguous(), inverse, offsets), None, None, None
+    d_ys, d_weight = expert_return_bwd(dy.contiguous(), ys, inverse, offsets, weight.contiguous())
+    return d_ys, None, None, d_weight
+
+
+expert_return.register_autograd(_expert_return_backward, setup_context=_expert_return_setup)
+
+
+def experts_q4(x: Tensor, expert: Tensor, weight: Tensor, wq: Tensor, wscale: Tensor) -> Tensor:
+    """y[t] = sum_j weight[t, j] W[expert[t, j]] x[t] for frozen experts W [experts, out, in] in
+    4 bits (q4_store of the stack), x bfloat16 [T, in], expert and weight [T, k].
+
+    Differentiable in x and weight.  Experts of more than one product (gate, up and down
+    with an activation between) sort and send once:
+
+        _, inverse, offsets = expert_sort(expert, experts)
+        xs = expert_send(x, inverse, offsets)
+        hs = act(matmul_q4(xs, gate_q, gate_scale, offsets)) * matmul_q4(xs, up_q, up_scale, offsets)
+        y = expert_return(matmul_q4(hs, down_q, down_scale, offsets), inverse, offsets, weight)"""
+    if wq.dim() != 3:
+        raise ValueError(f"dora::experts_q4: a stack of weights [experts, out, in / 2], got {tuple(wq.shape)}")
+    if expert.dim() != 2 or expert.shape[0] != x.shape[0] or weight.shape != expert.shape:
+        raise ValueError(f"dora::experts_q4: expert and weight are [T, k] for x [T, in], got {tuple(expert.shape)}, "
+                         f"{tuple(weight.shape)}, {tuple(x.shape)}")
+    _, inverse, offsets = expert_sort(expert, wq.shape[0])
+    ys = matmul_q4(expert_send(x, inverse, offsets), wq, wscale, offsets)
+    return expert_return(ys, inverse, offsets, weight.float())

@@ -166,7 +166,7 @@ def check_product(x, h, wq, ws, t, offsets=None):
 @pytest.mark.parametrize("T,out,inp", [
     (1, 16, 32), (1, 512, 512), (1, 1040, 2080), (2, 272, 1120), (3, 4096, 256), (7, 128, 128), (8, 256, 4096),
     (9, 48, 160), (16, 400, 640), (17, 256, 256), (31, 528, 992), (33, 64, 96), (40, 2048, 512), (64, 272, 384), (65, 272, 544),
-    (100, 1040, 2080), (100, 400, 1152), (128, 4096, 128), (129, 256, 1024), (200, 144, 8192), (257, 512, 160), (300, 784, 288), (1000, 272, 736)])
+    (100, 1040, 2080), (100, 400, 1152), (128, 4096, 128), (129, 256, 1024), (200, 144, 8192), (257, 512, 160), (70, 4096, 160), (150, 160, 4096), (300, 784, 288), (1000, 272, 736)])
 def test_products(T, out, inp, t):
     rng = np.random.default_rng(T * 31 + out + inp)
     wq, ws = weight(rng, out, inp)
