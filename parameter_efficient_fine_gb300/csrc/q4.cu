@@ -12,6 +12,8 @@
 #include "q4.cuh"
 #include "stream.cuh"
 
+#include <type_traits>
+
 namespace {
 
 constexpr int kPer = 8;            // elements a thread holds
@@ -25,9 +27,6 @@ template <> struct Eight<__nv_bfloat16> {
   };
   static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p, int64_t e) { return {IO::load(p, e)}; }
   static __device__ __forceinline__ void unpack(const Raw &r, float (&v)[8]) { IO::unpack(r.a, v); }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, int64_t e, const float (&v)[8]) {
-    IO::store(p, e, IO::pack(v));
-  }
 };
 template <> struct Eight<float> {
   using IO = Io<float, 4>;
@@ -38,10 +37,6 @@ template <> struct Eight<float> {
   static __device__ __forceinline__ void unpack(const Raw &r, float (&v)[8]) {
     v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
     v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
-  }
-  static __device__ __forceinline__ void store(float *p, int64_t e, const float (&v)[8]) {
-    IO::store(p, e, make_float4(v[0], v[1], v[2], v[3]));
-    IO::store(p, e + 4, make_float4(v[4], v[5], v[6], v[7]));
   }
 };
 
@@ -81,31 +76,35 @@ q4_store_kernel(const Act *__restrict__ x, int64_t pieces, uint32_t *__restrict_
   }
 }
 
+// A load writes pieces of 16 bytes: 8 elements of bf16, 4 of fp32 (of 8, a thread's two
+// stores would each leave gaps: 14336 x 4096 63.9 us)
 template <typename Act>
 __global__ void __launch_bounds__(kThreads)
-q4_load_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ scale, int64_t pieces, Act *__restrict__ x) {
-  using E = Eight<Act>;
+q4_load_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, int64_t pieces, Act *__restrict__ x) {
+  constexpr int V = 16 / sizeof(Act), kFlight = 2 * kRows;
+  using IO = Io<Act, V>;
+  using Q = typename std::conditional<V == 8, uint32_t, uint16_t>::type;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads; base < pieces; base += kRows * step) {
-    uint32_t w[kRows], b[kRows];
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads; base < pieces; base += kFlight * step) {
+    uint32_t w[kFlight], b[kFlight];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < kFlight; ++r) {
       const int64_t i = base + r * step + threadIdx.x;
-      w[r] = i < pieces ? __ldcs(q + i) : 0u;
-      b[r] = i < pieces ? scale[i / 4] : 0u;
+      w[r] = i < pieces ? __ldcs(reinterpret_cast<const Q *>(q) + i) : 0u;
+      b[r] = i < pieces ? scale[i / (kQ4Group / V)] : 0u;
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < kFlight; ++r) {
       const int64_t i = base + r * step + threadIdx.x;
       const float s = q4_scale(b[r]);
-      float v[kPer];
+      float v[V];
 #pragma unroll
-      for (int k = 0; k < kPer; k += 2) {
+      for (int k = 0; k < V; k += 2) {
         const float2 f = q4_value2((w[r] >> (4 * k)) & 0xffu);
         v[k] = f.x * s;
         v[k + 1] = f.y * s;
       }
-      if (i < pieces) E::store(x, i * kPer, v);
+      if (i < pieces) IO::store(x, i * V, IO::pack(v));
     }
   }
 }
@@ -158,16 +157,18 @@ extern "C" dora_status dora_q4_load(dora_dtype act, const void *q, const void *s
   int device = 0;
   st = dora::current_device(&info, &device);
   if (st != DORA_OK) return st;
-  const int64_t pieces = rows * (cols / kPer);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  auto *pq = static_cast<const uint32_t *>(q);
+  auto *pq = static_cast<const uint8_t *>(q);
   auto *ps = static_cast<const uint8_t *>(scale);
-  if (act == DORA_BF16)
+  if (act == DORA_BF16) {
+    const int64_t pieces = rows * (cols / 8);
     q4_load_kernel<__nv_bfloat16><<<blocks<q4_load_kernel<__nv_bfloat16>>(pieces, device, info.sms), kThreads, 0, cs>>>(
         pq, ps, pieces, static_cast<__nv_bfloat16 *>(x));
-  else
+  } else {
+    const int64_t pieces = rows * (cols / 4);
     q4_load_kernel<float><<<blocks<q4_load_kernel<float>>(pieces, device, info.sms), kThreads, 0, cs>>>(
         pq, ps, pieces, static_cast<float *>(x));
+  }
   dora::count_launches(1);
   return dora::launch_status();
 }

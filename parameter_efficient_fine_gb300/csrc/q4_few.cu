@@ -349,21 +349,29 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
         if constexpr (!PRE) {
           ok = guard_wait(xfull0 + 8u * xt.i, xt.phase, ctl, p.guard, 75);
           if (!__all_sync(0xffffffffu, ok)) break;
-          // a place without a token keeps what it holds: its column of the result is not read
+          // a place without a token holds anything: its column of the result is not read
           uint8_t *xs = xs0 + xt.i * F::kXBytes, *sf = xsf0 + xt.i * F::kXSf;
+          // four at a time, whose steps hide one another's latencies
+          constexpr int kAtOnce = 4;
+#pragma unroll 1
+          for (int t0 = 0; t0 < ntok; t0 += kAtOnce) {
+            uint2 v[kAtOnce];
+            uint32_t h[kAtOnce], l[kAtOnce], sb[kAtOnce];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (t >= ntok) break;
-            const int to = ((lane >> 2) ^ (t & 7)) * 16 + (lane & 3) * 4;
-            const uint2 v = *reinterpret_cast<const uint2 *>(xs + (t + (lane >= 16 ? NT : 0)) * 128 + (lane & 15) * 8);
+            for (int j = 0; j < kAtOnce; ++j)
+              v[j] = *reinterpret_cast<const uint2 *>(xs + (t0 + j + (lane >= 16 ? NT : 0)) * 128 + (lane & 15) * 8);
             __syncwarp();
-            uint32_t h, l, sb;
-            split4(v, &h, &l, &sb);
-            *reinterpret_cast<uint32_t *>(xs + t * 128 + to) = h;
-            *reinterpret_cast<uint32_t *>(xs + (NT + t) * 128 + to) = l;      // NT % 8 == 0: the same swizzle
-            if ((lane & 7) == 0) {
-              sf[sf_at(t) + (lane >> 3)] = static_cast<uint8_t>(sb);
-              sf[sf_at(NT + t) + (lane >> 3)] = static_cast<uint8_t>(sb - 4u);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) split4(v[j], &h[j], &l[j], &sb[j]);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              const int t = t0 + j, to = ((lane >> 2) ^ (t & 7)) * 16 + (lane & 3) * 4;
+              *reinterpret_cast<uint32_t *>(xs + t * 128 + to) = h[j];
+              *reinterpret_cast<uint32_t *>(xs + (NT + t) * 128 + to) = l[j];      // NT % 8 == 0: the same swizzle
+              if ((lane & 7) == 0) {
+                sf[sf_at(t) + (lane >> 3)] = static_cast<uint8_t>(sb[j]);
+                sf[sf_at(NT + t) + (lane >> 3)] = static_cast<uint8_t>(sb[j] - 4u);
+              }
             }
           }
           fence_async_proxy();

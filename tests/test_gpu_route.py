@@ -42,7 +42,8 @@ def entries(rng, T, k, E, kind):
     return e
 
 
-CASES = [(1, 1, 1), (1, 8, 64), (3, 2, 2), (17, 3, 5), (63, 6, 60), (128, 8, 300), (1000, 4, 33), (5000, 7, 16), (333, 1, 4096)]
+CASES = [(1, 1, 1), (1, 8, 64), (3, 2, 2), (17, 3, 5), (63, 6, 60), (128, 8, 300), (1000, 4, 33), (5000, 7, 16), (333, 1, 4096), (4097, 1, 3), (8192, 8, 64),
+         (20001, 2, 1024), (5000, 1, 1025), (16384, 3, 200)]
 
 
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
