@@ -44,10 +44,11 @@ constexpr int kTileF = 256;                           // features per tile
 constexpr int kTileT = 256;                           // most tokens per tile
 constexpr unsigned kRawBytes = 128 * kKB / 2;         // 8 KB
 constexpr unsigned kPanel = kKS * 128;                // 8 KB: 64 rows of 64 bf16
-constexpr int kGroups = 3, kGroupWarps = 4;           // conversion
-constexpr int kConvWarps = kGroups * kGroupWarps, kOutWarps = 8;
-constexpr int kConv0 = 3, kOut0 = kConv0 + kConvWarps;
-constexpr int kThreadsMm = 32 * (kOut0 + kOutWarps);
+constexpr int kGroupWarps = 4, kOutWarps = 8;
+template <bool TRANS> constexpr int kGroups = TRANS ? 3 : 4;   // of conversion warps
+constexpr int kConv0 = 3;
+template <bool TRANS> constexpr int kOut0 = kConv0 + kGroups<TRANS> * kGroupWarps;
+template <bool TRANS> constexpr int kThreadsMm = 32 * (kOut0<TRANS> + kOutWarps);
 constexpr int kAhead = 4;                             // blocks whose scales are on their way
 constexpr uint32_t kACol = 256;                       // x W^T: first column of the converted W
 // half of the tile's tokens, 64 k
@@ -57,12 +58,17 @@ template <bool TRANS> __host__ __device__ constexpr unsigned stage_size(int ntok
 }
 // stages and blocks of W in flight.  x W^T: a stage is 32 columns of tensor memory,
 // of which the accumulator leaves 256
-constexpr int kStages = 6;
+template <bool TRANS> constexpr int kStages = TRANS ? 6 : 8;
 template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 6;
 // a wait goes by the parity of a phase, so a group visits every use of the slots that
-// it visits: with three groups taking turns at the stages, two to a block, each comes
-// to two of any three consecutive blocks
-static_assert(kGroups == 3 && kStages % 3 == 0 && kRaw<false> % 3 == 0 && kRaw<true> % 3 == 0, "slots of a group");
+// it visits: of the stages if the groups divide them, of the blocks of W, two stages
+// each, if it comes to every one in turn (of three groups, each to two of any three
+// consecutive blocks; of four, to every second)
+template <bool TRANS> constexpr bool turns_ok() {
+  return kStages<TRANS> % kGroups<TRANS> == 0 &&
+         (kGroups<TRANS> == 3 ? kRaw<TRANS> % 3 == 0 : kGroups<TRANS> == 4 && kRaw<TRANS> % 2 == 0);
+}
+static_assert(turns_ok<false>() && turns_ok<true>(), "slots of a group");
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -104,6 +110,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// once all MMAs of the pair issued so far are done, arrive on a barrier of either CTA,
+// at the same place in both
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\t"
+      "mov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
+      : "memory");
+}
 // the accumulators: for x W^T the converted W leaves 256 columns, two of 128 tokens
 // or one of more
 struct Acc {
@@ -127,6 +142,7 @@ __device__ __forceinline__ uint64_t sdesc_mmajor(uint32_t saddr) {
 
 // A tile, or a part of its k where the tiles are few: blocks b0 to b0 + nb
 struct Unit : Tile {
+  int n;                            // tokens that its MMAs take: its own, in steps of 32
   int part, b0, nb;
 };
 __device__ __forceinline__ bool find_unit(const Q4Params &p, int u, Unit *o) {
@@ -134,13 +150,15 @@ __device__ __forceinline__ bool find_unit(const Q4Params &p, int u, Unit *o) {
   o->part = u - t * p.parts;
   o->b0 = blocks * o->part / p.parts;
   o->nb = blocks * (o->part + 1) / p.parts - o->b0;
-  return t < p.tiles && find_tile(p, t, o);
+  if (t >= p.tiles || !find_tile(p, t, o)) return false;
+  o->n = (o->t1 - o->t0 + 31) & ~31;
+  return true;
 }
 
 template <bool TRANS>
-__global__ void __launch_bounds__(kThreadsMm, 1)
+__global__ void __launch_bounds__(kThreadsMm<TRANS>, 1)
 q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p) {
-  constexpr int S = kStages, R = kRaw<TRANS>;
+  constexpr int S = kStages<TRANS>, B = S / 2, R = kRaw<TRANS>, NG = kGroups<TRANS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t xbox = tok_box(p.ntok), stage_bytes = stage_size<TRANS>(p.ntok);
@@ -148,14 +166,14 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   uint64_t *bars = reinterpret_cast<uint64_t *>(raw + R * kRawBytes);
   // barriers (a pair uses the even CTA's full and accumulator empty): tokens here and
   // W converted, empty; raw full and empty; accumulator full and empty; end
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, rfull0 = empty0 + 8u * S,
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * B, rfull0 = empty0 + 8u * B,
                  rempty0 = rfull0 + 8u * R, accf = rempty0 + 8u * R, acce = accf + 16, fin = acce + 16;
-  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * S + 2 * R + 5);
+  SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + 2 * B + 2 * R + 5);
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
+  const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full0 + 8u * s, 1 + 2 * kGroupWarps);   // the copies; a group of either CTA
+    for (int s = 0; s < B; ++s) {
+      mbar_init(full0 + 8u * s, 1 + 4 * kGroupWarps);   // the copies; two groups of either CTA
       mbar_init(empty0 + 8u * s, 1);
     }
     for (int s = 0; s < R; ++s) {
@@ -190,18 +208,22 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   if (warp == 0) {
     // ---------------------------------------------------------------- tokens
     bool ok = !loads_withheld(p.guard), issued = false;
-    Ring st(S);
+    Ring st(B);
     for (int t = pair; ok && find_unit(p, t, &o); t += npairs) {
-      const int t0 = o.t0 + static_cast<int>(rank) * (p.ntok / 2);
-      for (int s = 2 * o.b0; s < 2 * (o.b0 + o.nb); ++s) {
+      const int t0 = o.t0 + static_cast<int>(rank) * (o.n / 2), boxes = o.n / 2 > p.xrows ? 2 : 1;
+      for (int s = o.b0; s < o.b0 + o.nb; ++s) {
         ok = guard_wait(empty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 62);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t fb = full0 + 8u * st.i;
+          const uint32_t fb = full0 + 8u * st.i, at = smem_u32(smem) + (2 * st.i + 1) * stage_bytes - xbox;
           // the even CTA's barrier counts both CTAs' bytes
-          if (rank == 0) mbar_expect_tx(fb, 2 * xbox);
-          tma_load_2d_pair(smem_u32(smem) + (st.i + 1) * stage_bytes - xbox, &mX, s * kKS, t0, mapa_shared(fb, 0));
+          if (rank == 0) mbar_expect_tx(fb, static_cast<uint32_t>(4 * boxes * p.xrows) * 128u);
+          for (int b = 0; b < boxes; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_2d_pair(at + h * stage_bytes + static_cast<uint32_t>(b * p.xrows) * 128u, &mX, s * kKB + h * kKS,
+                               t0 + b * p.xrows, mapa_shared(fb, 0));
         }
         __syncwarp();
         issued = true;
@@ -251,27 +273,20 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       // ---------------------------------------------------------------- MMA issuer
       // (a commit arrives on the barrier of this CTA and on the peer's)
       bool ok = true;
-      Ring st(S);
+      Ring st(B);
       Acc acc(TRANS, p.ntok);
-      const uint32_t peer_off = mapa_shared(full0, peer) - full0;   // to the peer's copy of a barrier
-      const uint32_t id = idesc_bf16_pair(p.ntok) | (TRANS ? 1u << 15 : 0u);
       for (int t = pair; ok && find_unit(p, t, &o); t += npairs, acc.next()) {
         ok = guard_wait(acce + 8u * acc.i, acc.phase ^ 1u, ctl, p.guard, 63);
-        const uint32_t d = tmem + acc.column();
+        const uint32_t d = tmem + acc.column(), id = idesc_bf16_pair(o.n) | (TRANS ? 1u << 15 : 0u);
         for (int s = 0; s < o.nb; ++s) {
-          // both stages of a block at once: a wait between two stages' MMAs costs this
-          // warp more than a wait behind another
-          Ring nx = st;
-          nx.next();
           ok = ok && guard_wait(full0 + 8u * st.i, st.phase, ctl, p.guard, 64);
-          ok = ok && guard_wait(full0 + 8u * nx.i, nx.phase, ctl, p.guard, 65);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int i = h ? nx.i : st.i;
+              const int i = 2 * st.i + h;
               const uint32_t at = smem_u32(smem) + i * stage_bytes;
               const uint64_t b = sdesc<32>(at + stage_bytes - xbox);
 #pragma unroll
@@ -281,16 +296,13 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
                 if (TRANS) mma_bf16_ss_pair(d, sdesc_mmajor(at) + 128u * k, b + 2u * k, id, more);
                 else mma_bf16_ts_pair(d, tmem + kACol + 32u * i + 8u * k, b + 2u * k, id, more);
               }
-              mma_commit_pair(empty0 + 8u * i);
-              mma_commit_pair(empty0 + 8u * i + peer_off);
             }
+            mma_commit_both(empty0 + 8u * st.i);
             if (s + 1 == o.nb) {
-              mma_commit_pair(accf + 8u * acc.i);
-              mma_commit_pair(accf + 8u * acc.i + peer_off);
+              mma_commit_both(accf + 8u * acc.i);
             }
           }
           __syncwarp();
-          st.next();
           st.next();
         }
       }
@@ -300,7 +312,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       }
       __syncwarp();
     }
-  } else if (warp < kOut0) {
+  } else if (warp < kOut0<TRANS>) {
     // ---------------------------------------------------------------- conversion
     // 64 values a thread: a row of the block, a half of it
     const int g = (warp - kConv0) / kGroupWarps, i = (warp & 3) * 32 + lane;
@@ -328,15 +340,15 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       const int q0 = u - u0;                       // this group's first stage of the unit
       uint32_t sc[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) sc[k] = scales(q0 + k * kGroups);
-      for (int qa = q0; qa < 2 * o.nb && ok; qa += kAhead * kGroups) {
+      for (int k = 0; k < kAhead; ++k) sc[k] = scales(q0 + k * NG);
+      for (int qa = q0; qa < 2 * o.nb && ok; qa += kAhead * NG) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const int q = qa + k * kGroups;
+          const int q = qa + k * NG;
           if (q >= 2 * o.nb || !ok) break;
           const uint32_t b = sc[k];
-          sc[k] = scales(q + kAhead * kGroups);
-          const int slot = (u >> 1) % R, stage = u % S;
+          sc[k] = scales(q + kAhead * NG);
+          const int slot = (u >> 1) % R, stage = u % S, blk = stage >> 1;
           const uint32_t rphase = static_cast<uint32_t>((u >> 1) / R) & 1u, sphase = static_cast<uint32_t>(u / S) & 1u;
           ok = guard_wait(rfull0 + 8u * slot, rphase, ctl, p.guard, 66);
           ok = __all_sync(0xffffffffu, ok);
@@ -350,7 +362,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           q4_bf16x32(w1, b >> 8, v + 16);
           __syncwarp();
           if (lane == 0) mbar_arrive(rempty0 + 8u * slot);
-          ok = guard_wait(empty0 + 8u * stage, sphase ^ 1u, ctl, p.guard, 67);
+          ok = guard_wait(empty0 + 8u * blk, sphase ^ 1u, ctl, p.guard, 67);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (TRANS) {
@@ -359,26 +371,23 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
             for (int c = 0; c < 8; ++c) sts128(dst + static_cast<uint32_t>((c ^ (r & 7)) * 16), v + 4 * c);
             fence_async_proxy();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(mapa_shared(full0 + 8u * stage, 0));
+            if (lane == 0) mbar_arrive_pair(mapa_shared(full0 + 8u * blk, 0));
           } else {
             tc_fence_after();
             tmem_st32(to + 32u * stage, v);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(full0 + 8u * stage, 0));
+            if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(full0 + 8u * blk, 0));
           }
-          u += kGroups;
+          u += NG;
         }
       }
     }
   } else {
     // ---------------------------------------------------------------- result
-    const int e = warp - kOut0;
+    const int e = warp - kOut0<TRANS>;
     const uint32_t quad = static_cast<uint32_t>(warp & 3);
-    const int half = p.ntok / 2;                   // tokens of this warp, from c0
-    const int c0 = (e >> 2) * half;
-    const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
     bool ok = true;
     Acc acc(TRANS, p.ntok);
     for (int t = pair; ok && find_unit(p, t, &o); t += npairs, acc.next()) {
@@ -386,6 +395,8 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      const int half = o.n / 2, c0 = (e >> 2) * half;   // tokens of this warp
+      const uint32_t lane_addr = tmem + ((quad * 32u) << 16) + static_cast<uint32_t>(c0);
       const int f = o.ft * kTileF + static_cast<int>(rank) * 128 + static_cast<int>(quad) * 32 + lane;
       const int t0 = o.t0 + c0, live = min(o.t1 - t0, half);
       const int64_t ld = p.nfeat;
@@ -510,10 +521,10 @@ size_t parts_bytes(const Plan &pl, int64_t T, int64_t nfeat) {
 }
 
 template <bool TRANS> constexpr size_t pair_smem(int ntok) {
-  return 1024 + kRaw<TRANS> * kRawBytes + 512 + kStages * static_cast<size_t>(stage_size<TRANS>(ntok));
+  return 1024 + kRaw<TRANS> * kRawBytes + 512 + kStages<TRANS> * static_cast<size_t>(stage_size<TRANS>(ntok));
 }
 template <bool TRANS> constexpr bool fits() {
-  return pair_smem<TRANS>(kTileT) <= kSmemMax && 8 * (2 * kStages + 2 * kRaw<TRANS> + 5) + sizeof(SharedCtl) <= 512;
+  return pair_smem<TRANS>(kTileT) <= kSmemMax && 8 * (kStages<TRANS> + 2 * kRaw<TRANS> + 5) + sizeof(SharedCtl) <= 512;
 }
 static_assert(fits<false>() && fits<true>(), "rings, barriers and control words");
 
@@ -527,7 +538,7 @@ void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int ntok, i
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg->gridDim = dim3(2 * static_cast<unsigned>(pairs));
-  cfg->blockDim = dim3(kThreadsMm);
+  cfg->blockDim = dim3(kThreadsMm<TRANS>);
   cfg->dynamicSmemBytes = pair_smem<TRANS>(ntok);
   cfg->stream = cs;
   cfg->attrs = attr;
@@ -583,6 +594,7 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
   p.ftiles = static_cast<int>(dora::ceil_div(p.nfeat, kTileF));
   const Plan pl = plan(TRANS, T, p.nfeat, p.kdim, experts);
   p.ntok = pl.ntok;
+  p.xrows = p.ntok / 2 <= 64 ? p.ntok / 2 : p.ntok / 4;
   p.parts = pl.parts;
   p.partial = static_cast<float *>(workspace);
   const int64_t tiles = p.ftiles * (offsets ? T / p.ntok + (experts < T ? experts : T) : dora::ceil_div(T, p.ntok));
@@ -590,7 +602,7 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
   p.tiles = static_cast<int>(tiles);
   const int64_t units = tiles * p.parts;
   CUtensorMap mW, mX;
-  if (!map_w(&mW, wq, experts, out, in, 64) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.ntok / 2, 128)) return DORA_ERR_CUDA;
+  if (!map_w(&mW, wq, experts, out, in, 64) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.xrows, 128)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

@@ -23,6 +23,7 @@ struct Q4Params {
   int experts;
   const int *offsets;               // null: one weight, all rows
   int ntok;                         // tokens per tile
+  int xrows;                        // rows of a box of x (q4_mm.cu)
   int ftiles, parts;                // feature tiles; parts that k is cut into
   int tiles;                        // no more than these
   const uint8_t *scale;
