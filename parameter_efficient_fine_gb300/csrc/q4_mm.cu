@@ -49,7 +49,7 @@ template <bool TRANS> constexpr int kGroups = TRANS ? 3 : 4;   // of conversion 
 constexpr int kConv0 = 3;
 template <bool TRANS> constexpr int kOut0 = kConv0 + kGroups<TRANS> * kGroupWarps;
 template <bool TRANS> constexpr int kThreadsMm = 32 * (kOut0<TRANS> + kOutWarps);
-constexpr int kAhead = 4;                             // blocks whose scales are on their way
+constexpr int kAhead = 2;                             // blocks whose scales are on their way
 constexpr uint32_t kACol = 256;                       // x W^T: first column of the converted W
 // half of the tile's tokens, 64 k
 __host__ __device__ constexpr unsigned tok_box(int ntok) { return static_cast<unsigned>(ntok / 2 * 128); }
@@ -59,14 +59,11 @@ template <bool TRANS> __host__ __device__ constexpr unsigned stage_size(int ntok
 // stages and blocks of W in flight.  x W^T: a stage is 32 columns of tensor memory,
 // of which the accumulator leaves 256
 template <bool TRANS> constexpr int kStages = TRANS ? 6 : 8;
-template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 6;
+template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 8;
 // a wait goes by the parity of a phase, so a group visits every use of the slots that
-// it visits: of the stages if the groups divide them, of the blocks of W, two stages
-// each, if it comes to every one in turn (of three groups, each to two of any three
-// consecutive blocks; of four, to every second)
+// it visits
 template <bool TRANS> constexpr bool turns_ok() {
-  return kStages<TRANS> % kGroups<TRANS> == 0 &&
-         (kGroups<TRANS> == 3 ? kRaw<TRANS> % 3 == 0 : kGroups<TRANS> == 4 && kRaw<TRANS> % 2 == 0);
+  return kStages<TRANS> / 2 % kGroups<TRANS> == 0 && kRaw<TRANS> % kGroups<TRANS> == 0;
 }
 static_assert(turns_ok<false>() && turns_ok<true>(), "slots of a group");
 
@@ -78,12 +75,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t *v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
-__device__ __forceinline__ uint32_t load_now16(const uint8_t *p) {
-  uint16_t v;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
-}
-
 // D (+)= A B over the pair, A of each CTA in its tensor memory
 __device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -173,12 +164,12 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < B; ++s) {
-      mbar_init(full0 + 8u * s, 1 + 4 * kGroupWarps);   // the copies; two groups of either CTA
+      mbar_init(full0 + 8u * s, 1 + 2 * kGroupWarps);   // the copies; a group of either CTA
       mbar_init(empty0 + 8u * s, 1);
     }
     for (int s = 0; s < R; ++s) {
       mbar_init(rfull0 + 8u * s, 1);
-      mbar_init(rempty0 + 8u * s, 2 * kGroupWarps);     // two stages
+      mbar_init(rempty0 + 8u * s, kGroupWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf + 8u * b, 1);
@@ -314,67 +305,74 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     }
   } else if (warp < kOut0<TRANS>) {
     // ---------------------------------------------------------------- conversion
-    // 64 values a thread: a row of the block, a half of it
+    // a thread has a row of the block: of x W^T a feature, of dy W a k
     const int g = (warp - kConv0) / kGroupWarps, i = (warp & 3) * 32 + lane;
     const int G = p.in / kQ4Group;
-    const bool words = G % 2 == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 1) == 0;
-    const uint32_t to = TRANS ? smem_u32(smem) + (i >> 6) * kPanel + (i & 63) * 128u
+    const bool words = G % 4 == 0;                 // the scales of a block's row are a word
+    const uint32_t to = TRANS ? smem_u32(smem) + (i >> 6) * stage_bytes + (i & 63) * 128u
                               : tmem + kACol + (static_cast<uint32_t>(warp & 3) * 32u << 16);
+    const uint32_t from = smem_u32(raw) + static_cast<uint32_t>(i) * 64u, swz = static_cast<uint32_t>((i >> 1) & 3) * 16u;
     bool ok = true;
-    int u = g;                                     // stage, counted over all tiles
-    for (int t = pair, u0 = 0; ok && find_unit(p, t, &o); t += npairs, u0 += 2 * o.nb) {
+    int u = g;                                     // block, counted over all tiles
+    for (int t = pair, u0 = 0; ok && find_unit(p, t, &o); t += npairs, u0 += o.nb) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
-      // stage q of the unit is half h = q % 2 of the k of its block q / 2.  Row of the block
-      // and half of its columns: features x k, or k x features
-      auto row = [&](int q) { return TRANS ? kKS * (q & 1) + (i & 63) : i; };
-      auto half = [&](int q) { return TRANS ? i >> 6 : q & 1; };
-      // the two scale bytes of this thread's part
+      // scales of this thread's row of block q of the unit
+      const int64_t row0 = static_cast<int64_t>(o.e) * p.out + i + (TRANS ? o.b0 * kKB : f0);
       auto scales = [&](int q) -> uint32_t {
-        const int k = (o.b0 + (q >> 1)) * kKB;
-        const int f = TRANS ? k + row(q) : f0 + row(q), c = (TRANS ? f0 : k) / kQ4Group + 2 * half(q);
-        if (q >= 2 * o.nb || f >= p.out || c >= G) return 0x7f7fu;
-        const uint8_t *at = p.scale + (static_cast<int64_t>(o.e) * p.out + f) * G + c;
-        if (words) return load_now16(at);
-        return load_now(at) | (c + 1 < G ? load_now(at + 1) : 127u) << 8;
+        const int k = (o.b0 + q) * kKB, f = i + (TRANS ? k : f0), c = (TRANS ? f0 : k) / kQ4Group;
+        if (q >= o.nb || f >= p.out || c >= G) return 0x7f7f7f7fu;
+        const uint8_t *at = p.scale + (row0 + (TRANS ? q * kKB : 0)) * G + c;
+        if (words) return load_now(reinterpret_cast<const uint32_t *>(at));
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w |= (c + j < G ? load_now(at + j) : 127u) << (8 * j);
+        return w;
       };
-      const int q0 = u - u0;                       // this group's first stage of the unit
+      const int q0 = u - u0;                       // this group's first block of the unit
       uint32_t sc[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) sc[k] = scales(q0 + k * NG);
-      for (int qa = q0; qa < 2 * o.nb && ok; qa += kAhead * NG) {
+      for (int qa = q0; qa < o.nb && ok; qa += kAhead * NG) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const int q = qa + k * NG;
-          if (q >= 2 * o.nb || !ok) break;
+          if (q >= o.nb || !ok) break;
           const uint32_t b = sc[k];
           sc[k] = scales(q + kAhead * NG);
-          const int slot = (u >> 1) % R, stage = u % S, blk = stage >> 1;
-          const uint32_t rphase = static_cast<uint32_t>((u >> 1) / R) & 1u, sphase = static_cast<uint32_t>(u / S) & 1u;
-          ok = guard_wait(rfull0 + 8u * slot, rphase, ctl, p.guard, 66);
+          const int slot = u % R, blk = u % B;
+          ok = guard_wait(rfull0 + 8u * slot, static_cast<uint32_t>(u / R) & 1u, ctl, p.guard, 66);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const int r = row(q);
-          const uint32_t from = smem_u32(raw) + slot * kRawBytes + static_cast<uint32_t>(r) * 64u,
-                         c0 = static_cast<uint32_t>((2 * half(q)) ^ ((r >> 1) & 3)) * 16u;
-          const uint4 w0 = lds128(from + c0), w1 = lds128(from + (c0 ^ 16u));
-          uint32_t v[32];
-          q4_bf16x32(w0, b & 255u, v);
-          q4_bf16x32(w1, b >> 8, v + 16);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(rempty0 + 8u * slot);
-          ok = guard_wait(empty0 + 8u * blk, sphase ^ 1u, ctl, p.guard, 67);
-          ok = __all_sync(0xffffffffu, ok);
+          const uint32_t at = from + slot * kRawBytes;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            const uint4 w0 = lds128(at + ((h * 32u) ^ swz)), w1 = lds128(at + ((h * 32u + 16u) ^ swz));
+            q4_bf16x32(w0, b >> (16 * h) & 255u, v);
+            q4_bf16x32(w1, b >> (16 * h + 8) & 255u, v + 16);
+            if (h == 0) {
+              ok = guard_wait(empty0 + 8u * blk, (static_cast<uint32_t>(u / B) & 1u) ^ 1u, ctl, p.guard, 67);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+            } else {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(rempty0 + 8u * slot);
+            }
+            if (TRANS) {
+              const uint32_t dst = to + 2 * blk * stage_bytes + h * kPanel;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) sts128(dst + static_cast<uint32_t>((c ^ (i & 7)) * 16), v + 4 * c);
+            } else {
+              tmem_st32(to + 32u * (2 * blk + h), v);
+            }
+          }
           if (!ok) break;
           if (TRANS) {
-            const uint32_t dst = to + stage * stage_bytes;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) sts128(dst + static_cast<uint32_t>((c ^ (r & 7)) * 16), v + 4 * c);
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(mapa_shared(full0 + 8u * blk, 0));
           } else {
-            tc_fence_after();
-            tmem_st32(to + 32u * stage, v);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
