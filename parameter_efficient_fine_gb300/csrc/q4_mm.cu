@@ -61,9 +61,9 @@ template <bool TRANS> __host__ __device__ constexpr unsigned stage_size(int ntok
 template <bool TRANS> constexpr int kStages = TRANS ? 6 : 8;
 template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 8;
 // a wait goes by the parity of a phase, so a group visits every use of the slots that
-// it visits
+// it visits: it has a slot of the ring of blocks, and one or two of that of W
 template <bool TRANS> constexpr bool turns_ok() {
-  return kStages<TRANS> / 2 % kGroups<TRANS> == 0 && kRaw<TRANS> % kGroups<TRANS> == 0;
+  return kStages<TRANS> == 2 * kGroups<TRANS> && (kRaw<TRANS> == kGroups<TRANS> || kRaw<TRANS> == 2 * kGroups<TRANS>);
 }
 static_assert(turns_ok<false>() && turns_ok<true>(), "slots of a group");
 
@@ -314,6 +314,10 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     const uint32_t from = smem_u32(raw) + static_cast<uint32_t>(i) * 64u, swz = static_cast<uint32_t>((i >> 1) & 3) * 16u;
     bool ok = true;
     int u = g;                                     // block, counted over all tiles
+    const int blk = g;                             // its slot, in the ring of W `slot`
+    int slot = g;
+    uint32_t rphase = 0, ephase = 1;
+    const uint32_t full = mapa_shared(full0 + 8u * blk, 0);
     for (int t = pair, u0 = 0; ok && find_unit(p, t, &o); t += npairs, u0 += o.nb) {
       const int f0 = o.ft * kTileF + static_cast<int>(rank) * 128;
       // scales of this thread's row of block q of the unit
@@ -339,8 +343,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           if (q >= o.nb || !ok) break;
           const uint32_t b = sc[k];
           sc[k] = scales(q + kAhead * NG);
-          const int slot = u % R, blk = u % B;
-          ok = guard_wait(rfull0 + 8u * slot, static_cast<uint32_t>(u / R) & 1u, ctl, p.guard, 66);
+          ok = guard_wait(rfull0 + 8u * slot, rphase, ctl, p.guard, 66);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t at = from + slot * kRawBytes;
@@ -351,7 +354,7 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
             q4_bf16x32(w0, b >> (16 * h) & 255u, v);
             q4_bf16x32(w1, b >> (16 * h + 8) & 255u, v + 16);
             if (h == 0) {
-              ok = guard_wait(empty0 + 8u * blk, (static_cast<uint32_t>(u / B) & 1u) ^ 1u, ctl, p.guard, 67);
+              ok = guard_wait(empty0 + 8u * blk, ephase, ctl, p.guard, 67);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();
@@ -371,14 +374,21 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           if (TRANS) {
             fence_async_proxy();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(mapa_shared(full0 + 8u * blk, 0));
+            if (lane == 0) mbar_arrive_pair(full);
           } else {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair_relaxed(mapa_shared(full0 + 8u * blk, 0));
+            if (lane == 0) mbar_arrive_pair_relaxed(full);
           }
           u += NG;
+          ephase ^= 1u;
+          if (R > NG && slot < NG) {
+            slot += NG;
+          } else {
+            slot = g;
+            rphase ^= 1u;
+          }
         }
       }
     }
