@@ -52,16 +52,16 @@ constexpr unsigned kSfBytes = kTcM * 4;     // scale words of 128 rows
 template <int NT, bool BOX> struct Few {
   static constexpr bool kSplit = NT > 8;                        // x comes in pieces
   static constexpr int N = 2 * NT;                              // rows of pieces
-  static constexpr int kPerSm = NT == 128 ? 1 : 2;              // CTAs, limited by shared memory
+  static constexpr int kPerSm = 2;                              // CTAs, limited by shared memory
   static constexpr int kStages = NT <= 16 ? 5 : NT == 64 ? 3 : 4;   // blocks of W
   static constexpr int kXStages = NT == 8 ? 10 : kStages;       // blocks of x
   static constexpr int kWorkers = kStages < 4 ? 4 : kStages;
   static constexpr int kMma = kWorkers, kCopyW = kMma + 1, kCopyX = kMma + 2, kThreads = 32 * (kMma + 3);
-  static constexpr unsigned kXSf = (N + 127) / 128 * kSfBytes;  // scale words of a block of pieces
+  static constexpr unsigned kXSf = kSfBytes;                    // scale words of a block of pieces
   static constexpr unsigned kXBytes = N * kKB;
-  // tensor memory: the result, then 4 columns of W's scale words and 4 per 128 rows of x's for each stage
-  static constexpr int kSfCol = N < 64 ? 64 : N, kSfStride = 4 + static_cast<int>(kXSf / kSfBytes) * 4;
-  static constexpr int kCols = NT == 128 ? 512 : NT == 64 ? 256 : 128;
+  // tensor memory: the result, then 4 columns of W's scale words and 4 of x's for each stage
+  static constexpr int kSfCol = N < 64 ? 64 : N, kSfStride = 8;
+  static constexpr int kCols = NT == 64 ? 256 : 128;
   static constexpr int kBars = 3 * kStages + 3 * kXStages + 1;
   static constexpr size_t kSmem = 1024 + kStages * (kWBytes + kSfBytes) + kXStages * (kXBytes + kXSf) + 8 * kBars +
                                   sizeof(SharedCtl);
@@ -86,7 +86,7 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 __device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // The scale words of 128 rows, 512 bytes, into 4 columns of tensor memory, the same in
 // each lane quadrant: row 32 j + l at byte 16 l + 4 j comes to lane l, column j
-__device__ __forceinline__ uint32_t sf_at(int row) { return static_cast<uint32_t>((row % 32) * 16 + (row / 32) % 4 * 4 + row / 128 * 512); }
+__device__ __forceinline__ uint32_t sf_at(int row) { return static_cast<uint32_t>((row % 32) * 16 + row / 32 * 4); }
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
   // 8 rows of 16 bytes, the next 8 128 bytes on; no swizzle
   const uint64_t d = ((saddr & 0x3FFFFu) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
@@ -305,8 +305,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       if (elect_one()) {
         // (a copy runs before the MMAs that this thread issues after it)
         copy_scales(sf, smem_u32(wsf0) + st.i * kSfBytes);
-#pragma unroll
-        for (unsigned q = 0; q < F::kXSf; q += kSfBytes) copy_scales(sf + 4 + 4 * (q / kSfBytes), smem_u32(xsf0) + xt.i * F::kXSf + q);
+        copy_scales(sf + 4, smem_u32(xsf0) + xt.i * F::kXSf);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_q8(tmem, da + 2u * k, db + 2u * k, idesc_q8(kTcM, N, k, false) | 5u << 7 /* A: E2M1 */, sf, sf + 4,
@@ -610,8 +609,7 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   static const void *const kernels[] = {
       (const void *)q4_few_kernel<8, false>,  (const void *)q4_few_kernel<8, true>,   (const void *)q4_few_kernel<16, false>,
       (const void *)q4_few_kernel<16, true>,  (const void *)q4_few_kernel<32, false>, (const void *)q4_few_kernel<32, true>,
-      (const void *)q4_few_kernel<64, false>, (const void *)q4_few_kernel<64, true>,  (const void *)q4_few_kernel<128, false>,
-      (const void *)q4_few_kernel<128, true>};
+      (const void *)q4_few_kernel<64, false>, (const void *)q4_few_kernel<64, true>};
   Q4Params p = {};
   st = tc_init(device, &p.guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
   if (st != DORA_OK) return st;
@@ -629,8 +627,7 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   if (per <= 8) return launch<8>(x, wq, p, workspace, device, cs);
   if (per <= 16) return launch<16>(x, wq, p, workspace, device, cs);
   if (per <= 32) return launch<32>(x, wq, p, workspace, device, cs);
-  if (per <= 64) return launch<64>(x, wq, p, workspace, device, cs);
-  return launch<128>(x, wq, p, workspace, device, cs);
+  return launch<64>(x, wq, p, workspace, device, cs);
 }
 
 }  // namespace dora

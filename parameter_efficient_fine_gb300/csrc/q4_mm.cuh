@@ -116,8 +116,10 @@ inline bool map_w(CUtensorMap *map, const void *base, int64_t experts, int64_t o
 
 namespace dora {
 
-// x W^T of few tokens (q4_few.cu): `per` of them a weight
-constexpr int64_t kQ4Few = 128;
+// x W^T of few tokens (q4_few.cu): up to so many a weight (us, that kernel / pairs: 64 x 8192 x 8192
+// 17.4 / 20.2, 70 21.8 / 20.6, 128 23.5 / 22.0; at 32 experts of 2048 x 4096, 32 tokens each
+// 45.6 / 62.8, 64 55 / 63, 16 experts of 128 50.7 / 35.0)
+constexpr int64_t kQ4Few = 64;
 inline int64_t q4_per(int64_t T, int64_t experts) { return experts < T ? ceil_div(T, experts) : 1; }
 size_t q4_few_workspace(int64_t T, int64_t in, int64_t per);
 dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
