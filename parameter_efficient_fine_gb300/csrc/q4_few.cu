@@ -56,7 +56,7 @@ template <int NT, bool BOX> struct Few {
   static constexpr int kStages = NT <= 16 ? 5 : NT == 64 ? 3 : 4;   // blocks of W
   static constexpr int kXStages = NT == 8 ? 10 : kStages;       // blocks of x
   static constexpr int kWorkers = kStages < 4 ? 4 : kStages;
-  static constexpr int kMma = kWorkers, kCopyW = kMma + 1, kCopyX = kMma + 2, kThreads = 32 * (kMma + 3);
+  static constexpr int kMma = kWorkers, kCopyW = kMma + 1, kCopyX = kMma + 2, kScale = kMma + 3, kThreads = 32 * (kMma + 3 + (BOX ? 1 : 0));
   static constexpr unsigned kXSf = kSfBytes;                    // scale words of a block of pieces
   static constexpr unsigned kXBytes = N * kKB;
   // tensor memory: the result, then 4 columns of W's scale words and 4 of x's for each stage
@@ -84,6 +84,11 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ uint4 load_now16(const uint8_t *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 // The scale words of 128 rows, 512 bytes, into 4 columns of tensor memory, the same in
 // each lane quadrant: row 32 j + l at byte 16 l + 4 j comes to lane l, column j
 __device__ __forceinline__ uint32_t sf_at(int row) { return static_cast<uint32_t>((row % 32) * 16 + row / 32 * 4); }
@@ -162,7 +167,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
   const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(wfull0 + 8u * s, BOX ? 33 : 1);              // the box; every lane's copies of scale words
+      mbar_init(wfull0 + 8u * s, BOX ? 2 : 1);               // the box; the scale words
       mbar_init(wready0 + 8u * s, 1);
       mbar_init(wempty0 + 8u * s, 1);
     }
@@ -207,6 +212,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       for (int f = threadIdx.x; f < kTcM && tile * kTcM + f < p.out; f += F::kThreads) {
         const uint8_t *row = wq + static_cast<int64_t>(tile * kTcM + f) * (p.in / 2) + kb0 * (kKB / 2);
         for (int c = 0; c < min(nb, kAheadL2) * (kKB / 2); c += 128) prefetch_line(row + c);
+        prefetch_line(p.scale + static_cast<int64_t>(tile * kTcM + f) * (p.in / kQ4Group) + 4 * kb0);
       }
     pdl_wait();
   }
@@ -237,21 +243,55 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       }
       __syncwarp();
       issued = true;
-      if (BOX) {
-#pragma unroll
-        for (int j = 0; j < kTcM / 32; ++j) {
-          const int f = 32 * j + lane;
-          if (f0 + f < p.out) copy4(smem_u32(wsf0) + st.i * kSfBytes + sf_at(f), p.scale + scale_at(f, b));
-        }
-        copies_arrive(full);
-      }
     }
-    copies_wait();
     if (!ok && issued) {
       // boxes in flight, whose barrier nobody may wait for after an abort: they land
       // within microseconds, wait 1 ms
       const unsigned long long c0 = globaltimer();
       while (globaltimer() - c0 < 1000000ull) {
+      }
+    }
+  } else if (BOX && warp == F::kScale) {
+    // ---------------------------------------------------------------- W's scales
+    // lane l has rows l, l + 32, ...: 16 bytes of each, four blocks, are on their way
+    // while the four before go block by block to where sf_at says
+    const bool wide = G % 16 == 0 && kb0 % 4 == 0;
+    uint4 next[4];
+    auto fetch = [&](int b) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool has = f0 + 32 * j + lane < p.out;
+        const uint8_t *at = p.scale + scale_at(32 * j + lane, b);
+        if (wide) {
+          next[j] = has && b < nb ? load_now16(at) : make_uint4(0, 0, 0, 0);
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = has && b + i < nb ? load_now(reinterpret_cast<const uint32_t *>(at) + i) : 0u;
+          next[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    };
+    fetch(0);
+    Ring st(S);
+    for (int b0 = 0; b0 < nb && ok; b0 += 4) {
+      uint4 now[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) now[j] = next[j];
+      fetch(b0 + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (b0 + i >= nb) break;
+        ok = guard_wait(wempty0 + 8u * st.i, st.phase ^ 1u, ctl, p.guard, 79);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        auto word = [&](const uint4 &v) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+        *reinterpret_cast<uint4 *>(wsf0 + st.i * kSfBytes + 16 * lane) =
+            make_uint4(word(now[0]), word(now[1]), word(now[2]), word(now[3]));
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(wfull0 + 8u * st.i);
+        st.next();
       }
     }
   } else if (warp == F::kCopyX) {
@@ -297,8 +337,8 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       ok = guard_wait((PRE ? xfull0 : xready0) + 8u * xt.i, xt.phase, ctl, p.guard, 73);
       ok = ok && guard_wait((BOX ? wfull0 : wready0) + 8u * st.i, st.phase, ctl, p.guard, 74);
       if (!__all_sync(0xffffffffu, ok)) break;
-      // scale words came by copies that the tensor core's reads are not ordered after
-      fence_async_proxy();
+      // x's scale words came by copies that the tensor core's reads are not ordered after
+      if (PRE) fence_async_proxy();
       tc_fence_after();
       const uint64_t da = sdesc<32>(smem_u32(smem) + st.i * kWBytes), db = sdesc<32>(smem_u32(xs0) + xt.i * F::kXBytes);
       const uint32_t sf = tmem + F::kSfCol + F::kSfStride * st.i;
