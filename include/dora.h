@@ -543,8 +543,11 @@ dora_status dora_q4_store(dora_dtype act, const void *x, int64_t rows, int64_t c
 dora_status dora_q4_load(dora_dtype act, const void *q, const void *scale, int64_t rows, int64_t cols,
                          void *x, dora_stream_t stream);
 
-/* Bytes of workspace dora_matmul_q4 and dora_matmul_q4_t need: none at any size; the
- * pointer may be NULL. */
+/* Bytes of workspace dora_matmul_q4 and dora_matmul_q4_t need, by the sizes alone: for
+ * x W^T of 9 to 64 tokens a weight (T / experts, rounded up) 2 T in + 8 T ceil(in / 128),
+ * for x in pieces; for others, where k is cut in parts to fill the device, 4 T out (dy W:
+ * 4 T in) a part; else 0, and the pointer may be NULL.  Nothing in it is kept from one
+ * call to the next; calls that run at once need one each. */
 size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts);
 size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t experts);
 
@@ -558,11 +561,16 @@ size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t ex
  *            NULL with experts == 1: all rows.  Values are clamped to 0 .. T.
  *   wq       uint8 [experts, out, in / 2]   wscale  uint8 [experts, out, in / 32]
  *   x, wq, wscale and y 16-byte aligned, in % 32 == 0, out % 16 == 0
- *   workspace  not used (dora_matmul_q4_workspace)
+ *   workspace  dora_matmul_q4_workspace bytes, 256-byte aligned
  *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1, below 2^31 - 1023,
  *   1 <= experts <= 4096.
- * The launch is a programmatic dependent one: its set-up overlaps the launch before
- * it, and it reads and writes nothing of the caller's before that has completed.
+ * Up to 64 tokens a weight, x enters as two 8-bit pieces and is off by at most 2^-21 of
+ * the largest magnitude among its 32 neighbours of a scale, and an infinity in it counts
+ * as NaN; above, W enters as bf16, which is exact.  Parts are summed in a fixed order:
+ * the same call gives the same bits.
+ * One launch, or two where there is a workspace.  They are programmatic dependent ones:
+ * their set-up overlaps the launch before them, and they read (but for lines of W asked
+ * into L2) and write nothing of the caller's before that has completed.
  */
 dora_status dora_matmul_q4(const void *x, const int32_t *offsets, const void *wq, const void *wscale,
                            int64_t T, int64_t out, int64_t in, int64_t experts, void *y,

@@ -17,14 +17,22 @@
 //                warp the blocks of its own in turn; then the result out of tensor
 //                memory.  More tokens are split by a launch of its own before
 //                (q4_split_kernel), while this one's first blocks of W are already
-//                on their way
+//                on their way (8 x 8192 x 8192 12.8 us, 9 13.8)
 //   next warp    tensor memory, scale words into it, MMA issue (four 32-wide steps per
 //                block)
-//   next warp    copies of W and of its scales
-//   last warp    copies of x or its pieces
+//   next warps   copies of W; copies of x or its pieces; W's scale words (BOX)
 // The tensor core takes 4-bit values 16 to every 16 bytes of shared memory, in 8 of
 // them.  TMA lays W out like that where its rows are whole blocks of 128 (BOX); else
-// a block arrives as it is stored, in the half of its place, and a worker spreads it.
+// a block arrives as it is stored, in the half of its place, and a worker spreads it
+// (1 x 8192 x 8192 11.2 us, 8224 columns 14.7).  From boxes of 256 k, whose rows are
+// twice as long, all of W spread by workers took 13.6.
+// W's scales go through registers, 16 bytes of a row at a time (13.0 us with a copy of
+// 4 bytes a row and block straight to their place).
+//
+// What bounds it: reading W, in boxes of 64-byte rows, which TMA takes one by one, at
+// 3.8 TB/s, after a launch and the first loads' latency, 3.6 us.  1 x 8192 x 8192 11.2
+// us (5.3 to read it at the copy bandwidth), 1 x 14336 x 4096 10.6 (4.7), 37 of them 14.4,
+// 64 x 8192 x 8192 15.9, 8 tokens at as many experts of 2048 x 4096 11.3, 512 at 32 38.7 (22).
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -45,7 +53,8 @@ namespace {
 constexpr int kKB = 128;                    // k per stage
 constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB of shared memory, 8 of W
 constexpr int kMaxClusterLog = 3;           // 8 CTAs, the portable limit
-constexpr int kAheadL2 = 6;                 // blocks asked into L2 while the launch before ends
+// blocks asked into L2 while the launch before ends (1 x 8192 x 8192: 0 0.5 us more, 16 1.5)
+constexpr int kAheadL2 = 6;
 constexpr unsigned kSfBytes = kTcM * 4;     // scale words of 128 rows
 
 // what a kernel of up to NT tokens a tile is made of

@@ -9,7 +9,7 @@
 //
 // The features are the M side, the tokens the N side.  A block of W, 128 rows of
 // it by 128 columns, arrives as it is stored (8 KB) and is turned into bf16 by
-// conversion warps, 64 k at a time.  For x W^T its rows are features: they go to
+// conversion warps.  For x W^T its rows are features: they go to
 // tensor memory, a lane each, from where the tensor core takes them as its A
 // operand.  For dy W its rows are k: they go to shared memory as two panels of 64
 // rows x 64 features, 128 bytes a row, swizzled, read M-major.  Neither makes a
@@ -20,8 +20,21 @@
 //   warp 0       TMA: tokens into the stages
 //   warp 1       tensor memory, MMA issue (even CTA)
 //   warp 2       TMA: blocks of W into a ring of their own
-//   warps 3-14   conversion, three groups taking turns at the stages
-//   warps 15-22  the result
+//   then         conversion, four groups of four warps taking turns at the blocks (dy W:
+//                three, which is what shared memory holds)
+//   last 8       the result
+// A tile's MMAs and copies are as wide as its own tokens are, in steps of 32: a tile of
+// an expert is seldom full, and one 256 wide saves converting W twice (4096 tokens at 32
+// experts of 2048 x 4096: 76 us, 96 with all tiles' MMAs 256 wide).
+//
+// What bounds it: with 256 tokens, the MMAs, 0.56 us a block of 128 k, and over longer
+// calls the power limit (8192 x 4096 x 4096 144 to 147 us, 1.9 PFLOP/s; 15360 x 8192 x
+// 8192 1135; 512 x 8192 x 8192 43); of dy W they read both operands from shared memory
+// and take 0.66 (15360 x 8192 x 8192 1225 us, 1.68 PFLOP/s; 512 45 to 47).  With up to
+// about 200 the conversion's integer instructions, 0.48 us a block whatever the tokens
+// (128 x 38912 x 4096 35 us; 700 x 8192 x 8192 62; 4096 tokens at 32 experts of 2048 x
+// 4096 66 to 71, dy W 80).  Its groups take whole blocks: with half blocks, whose waits and
+// addresses count twice, the last three were 40, 70 and 77 us, and dy W 512 53.
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -498,8 +511,10 @@ q4_join_kernel(const float4 *__restrict__ parts, int n, int T, int quads, const 
 // ---------------------------------------------------------------------------
 // Tokens per tile and parts of k: the least time, in us, of the waves of units over
 // the pairs that a GB300 holds, a fixed number so that the workspace is the same
-// everywhere.  A block of k takes a pair about as long with 32 tokens as with 256;
-// parts cost their way through memory and a launch.  Experts: half a tile more each
+// everywhere.  A block of k is counted alike for all tokens; parts cost their way through
+// memory and a launch.  What it picks is within 3% of the best of all widths and parts
+// (129 x 8192 x 8192: 160 tokens in 2 parts 22.8 us, in 1 about 30, in 4 26; 200 x 4096 x
+// 4096: 15.0, 14.8; dy W 4096 at 32 experts: 80.9, 78.1; 64 at 64: 146, 140).  Experts: half a tile more each
 // than their tokens fill, and of two plans alike the wider tiles, which even loads
 // suit
 struct Plan {

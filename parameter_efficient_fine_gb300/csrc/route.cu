@@ -25,8 +25,8 @@ namespace {
 // and each of its warps a stretch of the input.  A cluster counts the entries of lower
 // experts, which is where its rows start, and its own in every stretch, and then
 // numbers its own in order.  No cluster waits for another; the input is read from L2.
-// It is bound by its instructions, about 20 an entry, expert and lane: with one CTA an
-// expert 65536 entries of 64 experts took 16 us.
+// It is bound by its instructions, about 20 an entry, expert and lane: 65536 entries of
+// 64 experts 10 us (one CTA an expert 16), 378 of 60 4.
 // ---------------------------------------------------------------------------
 constexpr int kSortWarps = 32;
 constexpr int kMaxSortCtas = 8;
@@ -102,7 +102,9 @@ expert_sort_kernel(const Idx *__restrict__ expert, int n, int experts, int many,
 
 // ---------------------------------------------------------------------------
 // rows there and back.  The threads of a token hold VEC columns each and walk
-// its row; a block holds kThreads / tpt tokens.
+// its row; a block holds kThreads / tpt tokens.  Bound by memory: 8192 tokens at 8 experts
+// each, 4096 columns of bf16, send 103 us, return 91, its gradient 176 (at the copy
+// bandwidth 90, 90 and 171).
 // ---------------------------------------------------------------------------
 struct RouteParams {
   int64_t T, cols;
