@@ -6,7 +6,7 @@
 // matrix, in memory order, is 16 bytes of q and one of scale.  A thread holds 8
 // neighbouring elements, four threads a group, whose maximum is two shuffles.  Both
 // are bound by memory: 14336 x 4096 store 42 us from fp32 and 27 from bf16, load 45 and
-// 27 (at the copy bandwidth 40 and 22); 512 x 512 2.5, a launch.
+// 27 (at the copy bandwidth 40 and 22); 512 x 512 2, a launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

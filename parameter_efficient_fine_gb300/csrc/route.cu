@@ -26,7 +26,7 @@ namespace {
 // experts, which is where its rows start, and its own in every stretch, and then
 // numbers its own in order.  No cluster waits for another; the input is read from L2.
 // It is bound by its instructions, about 20 an entry, expert and lane: 65536 entries of
-// 64 experts 10 us (one CTA an expert 16), 378 of 60 4.
+// 64 experts 10 us (one CTA an expert 16), 378 of 60 2.
 // ---------------------------------------------------------------------------
 constexpr int kSortWarps = 32;
 constexpr int kMaxSortCtas = 8;
