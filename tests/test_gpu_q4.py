@@ -174,6 +174,28 @@ def test_products(T, out, inp, t):
     check_product(x, h, wq, ws, t)
 
 
+@pytest.mark.parametrize("T,out,inp", [(1, 272, 4608), (5, 144, 8320), (40, 272, 4608), (64, 528, 2560)])
+def test_parts_of_k_that_start_anywhere(T, out, inp):
+    """Few tokens: CTAs whose first block of k is no multiple of four, and rows of scales
+    that are no multiple of 16 bytes."""
+    rng = np.random.default_rng(T + inp)
+    wq, ws = weight(rng, out, inp)
+    h, x = act(spread(rng, (T, inp)))
+    check_product(x, h, wq, ws, False)
+
+
+@pytest.mark.parametrize("t", [False, True], ids=["xWt", "dyW"])
+def test_tiles_of_every_width_in_turn(t):
+    """More tiles than the device holds pairs of CTAs, each a few blocks of k that the
+    conversion groups do not divide, their tokens from one to a full tile."""
+    rng = np.random.default_rng(11)
+    offsets = np.cumsum([0, 1, 33, 64, 65, 97, 129, 160, 0, 191, 224, 256]).tolist()
+    out, inp = (544, 4096) if t else (4096, 544)
+    wq, ws = weight(rng, out, inp, len(offsets) - 1)
+    h, x = act(spread(rng, (offsets[-1], out if t else inp)))
+    check_product(x, h, wq, ws, t, offsets)
+
+
 EXPERTS = [
     ([0, 1], 64, 96), ([0, 0, 3, 3, 4, 4], 272, 544), ([0, 5, 5, 40, 41, 300], 144, 160), ([0] * 40 + [2, 2, 9, 9], 256, 384),
     ([0, 700, 701, 701], 400, 256), ([0, 30, 30, 100, 130], 272, 640), ([0, 1, 300, 301], 144, 384), ([0, 8, 16, 24, 32, 40, 48, 56, 64], 512, 1024), (list(range(0, 78, 2)), 48, 2080)]
