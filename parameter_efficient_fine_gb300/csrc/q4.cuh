@@ -49,48 +49,49 @@ __device__ __forceinline__ float2 q4_value2(uint32_t byte) {
 }
 
 // ---------------------------------------------------------------------------
-// Values as bf16, for the tensor cores.  The eight magnitudes of a group, scaled, are
-// a table of eight bf16, kept as their low and their high bytes; a byte permute looks
-// up four values' bytes at once, by three bits each.  The sign bits are put on the
-// high bytes before the two are laced: 15 integer instructions for 8 values, where
-// shifting each pair's fields into place and multiplying takes 19 and 4 products.
+// Values as bf16, for the tensor cores.  The three magnitude bits at bits 8-6 of a
+// bf16 are the value times 2^-126, its subnormal range included, so one
+// multiplication by 2^(b - 1) scales it.  That factor is a bf16 up to b = 128;
+// above, 2^127 and a second factor.  A nibble times 2^12 + 2^6 has its sign at bit
+// 15 and its magnitude at bits 8-6, and two of them 16 bits apart do not meet: for
+// 8 values 11 instructions of the integer pipe, which bounds the conversion, and 8
+// of the other.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t q4_twice(uint32_t bf16) { return bf16 * 0x10001u; }
+__device__ __forceinline__ uint32_t q4_factor(uint32_t byte) {
+  return q4_twice(byte == kQ4Nan ? 0x7fc0u : (min(byte, 128u) + 126u) << 7);
+}
 __device__ __forceinline__ uint32_t q4_mul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-struct Q4Table {
-  uint32_t lo[2], hi[2];
-};
-// the magnitudes times 2^(b - 127), a subnormal bf16 for b = 0
-__device__ __forceinline__ Q4Table q4_table(uint32_t byte) {
-  const uint32_t f = q4_twice(byte == kQ4Nan ? 0x7fc0u : byte == 0 ? 0x40u : byte << 7);
-  // 0, 0.5 | 1, 1.5 | 2, 3 | 4, 6
-  const uint32_t v0 = q4_mul2(0x3f000000u, f), v1 = q4_mul2(0x3fc03f80u, f), v2 = q4_mul2(0x40404000u, f),
-                 v3 = q4_mul2(0x40c04080u, f);
-  return {{__byte_perm(v0, v1, 0x6420), __byte_perm(v2, v3, 0x6420)}, {__byte_perm(v0, v1, 0x7531), __byte_perm(v2, v3, 0x7531)}};
+// bytes of a and b by `selector`'s four-bit fields; 8 on a field whose byte is below 128 gives zero
+__device__ __forceinline__ uint32_t q4_prmt(uint32_t a, uint32_t b, uint32_t selector) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(selector));
+  return d;
 }
 // the eight values of four bytes, in order, two a register
-__device__ __forceinline__ void q4_bf16x8(uint32_t w, const Q4Table &t, uint32_t *out) {
-  const uint32_t m = w & 0x77777777u, m1 = m >> 16, up = w << 4;
-  // the sign of value i at bit 7 of byte i: the even ones' come up by four bits
-  const uint32_t s0 = __byte_perm(w, up, 0x1504), s1 = __byte_perm(w, up, 0x3726);
-  const uint32_t h0 = __byte_perm(t.hi[0], t.hi[1], m) | (s0 & 0x80808080u), h1 = __byte_perm(t.hi[0], t.hi[1], m1) | (s1 & 0x80808080u);
-  const uint32_t l0 = __byte_perm(t.lo[0], t.lo[1], m), l1 = __byte_perm(t.lo[0], t.lo[1], m1);
-  out[0] = __byte_perm(l0, h0, 0x5140);
-  out[1] = __byte_perm(l0, h0, 0x7362);
-  out[2] = __byte_perm(l1, h1, 0x5140);
-  out[3] = __byte_perm(l1, h1, 0x7362);
+__device__ __forceinline__ void q4_bf16x8(uint32_t w, uint32_t factor, uint32_t *out) {
+  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+  out[0] = q4_mul2(q4_prmt(even, odd, 0xc480) * 0x1040u & 0x81c081c0u, factor);
+  out[1] = q4_mul2(q4_prmt(even, odd, 0xd591) * 0x1040u & 0x81c081c0u, factor);
+  out[2] = q4_mul2(q4_prmt(even, odd, 0xe6a2) * 0x1040u & 0x81c081c0u, factor);
+  out[3] = q4_mul2(q4_prmt(even, odd, 0xf7b3) * 0x1040u & 0x81c081c0u, factor);
 }
 // a group's 32 values
 __device__ __forceinline__ void q4_bf16x32(uint4 w, uint32_t byte, uint32_t *out) {
-  const Q4Table t = q4_table(byte);
-  q4_bf16x8(w.x, t, out);
-  q4_bf16x8(w.y, t, out + 4);
-  q4_bf16x8(w.z, t, out + 8);
-  q4_bf16x8(w.w, t, out + 12);
+  const uint32_t f = q4_factor(byte);
+  q4_bf16x8(w.x, f, out);
+  q4_bf16x8(w.y, f, out + 4);
+  q4_bf16x8(w.z, f, out + 8);
+  q4_bf16x8(w.w, f, out + 12);
+  if (byte > 128 && byte != kQ4Nan) {
+    const uint32_t g = q4_twice((byte - 1u) << 7);     // 2^(b - 128)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) out[i] = q4_mul2(out[i], g);
+  }
 }
 
 }  // namespace
