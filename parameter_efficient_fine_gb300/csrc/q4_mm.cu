@@ -72,11 +72,15 @@ template <bool TRANS> __host__ __device__ constexpr unsigned stage_size(int ntok
 // stages and blocks of W in flight.  x W^T: a stage is 32 columns of tensor memory,
 // of which the accumulator leaves 256
 template <bool TRANS> constexpr int kStages = TRANS ? 6 : 8;
-template <bool TRANS> constexpr int kRaw = TRANS ? 3 : 8;
+// dy W: six blocks of W where the stages leave room, which hides their copies' latency
+// where few tokens leave little else to do (129 x 8192 x 8192 26.8 us, 30.8 with three)
+template <bool TRANS> constexpr int raw_slots(int ntok) { return !TRANS ? 8 : ntok <= 192 ? 6 : 3; }
 // a wait goes by the parity of a phase, so a group visits every use of the slots that
 // it visits: it has a slot of the ring of blocks, and one or two of that of W
 template <bool TRANS> constexpr bool turns_ok() {
-  return kStages<TRANS> == 2 * kGroups<TRANS> && (kRaw<TRANS> == kGroups<TRANS> || kRaw<TRANS> == 2 * kGroups<TRANS>);
+  for (int n = 32; n <= kTileT; n += 32)
+    if (raw_slots<TRANS>(n) != kGroups<TRANS> && raw_slots<TRANS>(n) != 2 * kGroups<TRANS>) return false;
+  return kStages<TRANS> == 2 * kGroups<TRANS>;
 }
 static_assert(turns_ok<false>() && turns_ok<true>(), "slots of a group");
 
@@ -159,10 +163,10 @@ __device__ __forceinline__ bool find_unit(const Q4Params &p, int u, Unit *o) {
   return true;
 }
 
-template <bool TRANS>
+template <bool TRANS, int R>
 __global__ void __launch_bounds__(kThreadsMm<TRANS>, 1)
 q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p) {
-  constexpr int S = kStages<TRANS>, B = S / 2, R = kRaw<TRANS>, NG = kGroups<TRANS>;
+  constexpr int S = kStages<TRANS>, B = S / 2, NG = kGroups<TRANS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t xbox = tok_box(p.ntok), stage_bytes = stage_size<TRANS>(p.ntok);
@@ -544,10 +548,12 @@ size_t parts_bytes(const Plan &pl, int64_t T, int64_t nfeat) {
 }
 
 template <bool TRANS> constexpr size_t pair_smem(int ntok) {
-  return 1024 + kRaw<TRANS> * kRawBytes + 512 + kStages<TRANS> * static_cast<size_t>(stage_size<TRANS>(ntok));
+  return 1024 + raw_slots<TRANS>(ntok) * kRawBytes + 512 + kStages<TRANS> * static_cast<size_t>(stage_size<TRANS>(ntok));
 }
 template <bool TRANS> constexpr bool fits() {
-  return pair_smem<TRANS>(kTileT) <= kSmemMax && 8 * (kStages<TRANS> + 2 * kRaw<TRANS> + 5) + sizeof(SharedCtl) <= 512;
+  for (int n = 32; n <= kTileT; n += 32)
+    if (pair_smem<TRANS>(n) > kSmemMax || 8 * (kStages<TRANS> + 2 * raw_slots<TRANS>(n) + 5) + sizeof(SharedCtl) > 512) return false;
+  return true;
 }
 static_assert(fits<false>() && fits<true>(), "rings, barriers and control words");
 
@@ -579,7 +585,7 @@ int resident_pairs(int device, int sms) {
     cudaLaunchAttribute attr[2];
     pair_config<false>(&cfg, attr, kTileT, sms / 2, nullptr);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, q4_pair_kernel<false>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, q4_pair_kernel<false, raw_slots<false>(kTileT)>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -589,7 +595,8 @@ int resident_pairs(int device, int sms) {
 }
 
 dora_status mm_init(int device, Q4Params *p) {
-  static const void *const kernels[] = {(const void *)q4_pair_kernel<false>, (const void *)q4_pair_kernel<true>};
+  static const void *const kernels[] = {(const void *)q4_pair_kernel<false, 8>, (const void *)q4_pair_kernel<true, 3>,
+                                        (const void *)q4_pair_kernel<true, 6>};
   return tc_init(device, &p->guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
 }
 
@@ -630,7 +637,9 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
   cudaLaunchAttribute attr[2];
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   pair_config<TRANS>(&cfg, attr, p.ntok, units < pairs ? units : pairs, cs);
-  if (cudaLaunchKernelEx(&cfg, q4_pair_kernel<TRANS>, mW, mX, p) != cudaSuccess) {
+  constexpr int kMost = raw_slots<TRANS>(kTileT), kFew = raw_slots<TRANS>(32);
+  if ((raw_slots<TRANS>(p.ntok) == kFew ? cudaLaunchKernelEx(&cfg, q4_pair_kernel<TRANS, kFew>, mW, mX, p)
+                                        : cudaLaunchKernelEx(&cfg, q4_pair_kernel<TRANS, kMost>, mW, mX, p)) != cudaSuccess) {
     cudaGetLastError();
     return DORA_ERR_CUDA;
   }
