@@ -30,17 +30,19 @@
 // What bounds it: with 256 tokens, the MMAs, 0.56 us a block of 128 k, and over longer
 // calls the power limit (8192 x 4096 x 4096 144 to 147 us, 1.9 PFLOP/s; 15360 x 8192 x
 // 8192 1135; 512 x 8192 x 8192 43); of dy W they read both operands from shared memory
-// and take 0.66 (15360 x 8192 x 8192 1225 us, 1.68 PFLOP/s; 512 45 to 47).  With up to
-// about 200 the conversion's integer instructions, 0.48 us a block whatever the tokens
-// (128 x 38912 x 4096 35 us; 700 x 8192 x 8192 62; 4096 tokens at 32 experts of 2048 x
-// 4096 66 to 71, dy W 80).  Its groups take whole blocks: with half blocks, whose waits and
-// addresses count twice, the last three were 40, 70 and 77 us, and dy W 512 53.
+// and take a little more (15360 x 8192 x 8192 1150 us, 1.8 PFLOP/s; 512 44).  With up to
+// 192 the conversion and its hand-overs, about 0.46 us a block whatever the tokens
+// (128 x 38912 x 4096 33.6 us; 700 x 8192 x 8192 61; 4096 tokens at 32 experts of 2048 x
+// 4096 63 to 68, dy W 74 to 85).  Its groups take whole blocks: with half blocks, whose
+// waits and addresses count twice, and looked-up values the last were 40, 70, 77 and 95,
+// and dy W 512 53.
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -515,12 +517,15 @@ q4_join_kernel(const float4 *__restrict__ parts, int n, int T, int quads, const 
 // ---------------------------------------------------------------------------
 // Tokens per tile and parts of k: the least time, in us, of the waves of units over
 // the pairs that a GB300 holds, a fixed number so that the workspace is the same
-// everywhere.  A block of k is counted alike for all tokens; parts cost their way through
-// memory and a launch.  What it picks is within 3% of the best of all widths and parts
-// (129 x 8192 x 8192: 160 tokens in 2 parts 22.8 us, in 1 about 30, in 4 26; 200 x 4096 x
-// 4096: 15.0, 14.8; dy W 4096 at 32 experts: 80.9, 78.1; 64 at 64: 146, 140).  Experts: half a tile more each
-// than their tokens fill, and of two plans alike the wider tiles, which even loads
-// suit
+// everywhere.  A block of k takes the conversion's time, above 192 tokens the MMAs'
+// (or, of dy W, the copies' with half of the slots); parts cost their way through memory
+// and a launch.  Experts: a tile at least, half a tile more than their tokens fill where
+// they fill more, and of two plans alike the wider tiles, which even loads suit.
+// One weight: within 2% of the best of all widths and parts but for the smallest (129 x
+// 8192 x 8192: 160 tokens in 2 parts 22.4 us, in 3 29.4, in 4 25.7; 129 x 1024 x 1024 8.2,
+// 7.1).  Experts depend on the loads: 4096 uneven ones at 32 of 2048 x 4096 68 us by 192
+// tokens, 71.5 by 256, 76 by 160, 87 by 128; dy W 85, 92, 103, 109; 5000 at 48 of 512 x
+// 4096, dy W, 65 by 192, 60 by 256.
 struct Plan {
   int ntok, parts;
 };
@@ -532,8 +537,12 @@ Plan plan(bool trans, int64_t T, int64_t nfeat, int64_t kdim, int64_t experts) {
   for (int n = 32; n <= kTileT; n += 32)
     for (int parts = 1; parts <= 8; ++parts) {
       if (parts > 1 && blocks < 4 * parts) break;
-      const int64_t tiles = ftiles * (experts > 1 ? (T + groups * n / 2) / n + 1 : dora::ceil_div(T, n));
-      const double block = (trans ? 0.68 : 0.6) + (experts > 1 ? -0.0001 : 0.0003) * n;
+      int64_t tiles = ftiles * dora::ceil_div(T, n);
+      if (experts > 1) {
+        const double fill = static_cast<double>(T) / static_cast<double>(groups * n);
+        tiles = ftiles * static_cast<int64_t>(groups * std::max(1.0, fill + 0.5 * std::min(fill, 1.0)) + 0.5);
+      }
+      const double block = (trans ? (n > 192 ? 0.64 : 0.57) : (n > 192 ? 0.56 : 0.5)) + (experts > 1 ? -0.0001 : 0.0001) * n;
       double cost = static_cast<double>(dora::ceil_div(tiles * parts, kPairs)) * (dora::ceil_div(blocks, parts) * block + 1.5);
       if (parts > 1) cost += 2.5 + static_cast<double>(parts) * T * nfeat * 8 / 5e6;
       if (least == 0 || cost < least) {
