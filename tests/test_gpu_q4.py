@@ -311,3 +311,42 @@ def test_error_of_a_row_is_what_rounding_leaves(T, t):
     ref = (q4.matmul_q4_t if t else q4.matmul_q4)(act_to_f64(h), wq, ws)
     err = np.linalg.norm(y - ref, axis=1) / np.linalg.norm(ref, axis=1)
     assert err.max() <= 1.1 * 2.0 ** -9, err.max()
+
+
+@pytest.mark.parametrize("t", [False, True], ids=["xWt", "dyW"])
+@pytest.mark.parametrize("T", [7, 4700])
+def test_a_stack_past_32_bits(T, t):
+    """More than 2^32 values, 2^31 bytes, the tokens at the first and the last expert: a
+    row's error as above."""
+    E, n = 66, 8192
+    torch.manual_seed(T)
+    wq = torch.randint(0, 256, (E, n, n // 2), dtype=U8, device=DEV)
+    ws = torch.randint(110, 118, (E, n, n // 32), dtype=U8, device=DEV)
+    offsets = torch.full((E + 1,), 3, dtype=torch.int32, device=DEV)
+    offsets[0], offsets[E] = 0, T
+    x = torch.randn(T, n, device=DEV).to(BF16)
+    y = run(x, wq, ws, t, offsets)
+    assert_no_device_error()
+    W = torch.empty(n, n, device=DEV)
+    for e, rows in ((0, slice(0, 3)), (E - 1, slice(3, None, 1 + T // 50))):
+        dora.dora_q4_load(wq[e], ws[e], W)
+        ref = x[rows].double() @ (W if t else W.t()).double()
+        err = (y[rows].double() - ref).norm(dim=1) / ref.norm(dim=1)
+        assert err.max() <= 1.1 * 2.0 ** -9, (e, err.max())
+
+
+def test_a_result_past_32_bits():
+    T, out, inp = 70000, 32768, 64
+    torch.manual_seed(1)
+    wq = torch.randint(0, 256, (out, inp // 2), dtype=U8, device=DEV)
+    ws = torch.randint(110, 118, (out, inp // 32), dtype=U8, device=DEV)
+    x = torch.randn(T, inp, device=DEV).to(BF16)
+    y = run(x, wq, ws, False)
+    assert_no_device_error()
+    W = torch.empty(out, inp, device=DEV)
+    dora.dora_q4_load(wq, ws, W)
+    rows = slice(0, None, 1021)
+    ref = x[rows].double() @ W.t().double()
+    err = (y[rows].double() - ref).norm(dim=1) / ref.norm(dim=1)
+    assert err.max() <= 1.1 * 2.0 ** -9, err.max()
+    assert not y.isnan().any()

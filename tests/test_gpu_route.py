@@ -143,3 +143,30 @@ def test_unaligned_rows_take_the_same_values():
     dora.dora_expert_send(x, inverse, offsets, a)
     dora.dora_expert_send(shifted, inverse, offsets, b)
     assert torch.equal(a, b)
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 elements of sorted rows; the last tokens' against torch."""
+    T, k, E, cols = 70000, 8, 16, 4096
+    torch.manual_seed(2)
+    expert = torch.randint(0, E, (T, k), dtype=I32, device=DEV)
+    _, inverse, offsets = sort(expert, E)
+    x = torch.randn(T, cols, device=DEV).to(torch.bfloat16)
+    xs = torch.empty(T * k, cols, dtype=torch.bfloat16, device=DEV)
+    dora.dora_expert_send(x, inverse, offsets, xs)
+    some = torch.cat([torch.arange(0, T, 997), torch.arange(T - 5, T)]).to(DEV)
+    at = inverse[some].long()
+    assert torch.equal(xs[at], x[some][:, None].expand(-1, k, -1))
+    assert int(at.max()) * cols > 2 ** 31
+    w = torch.rand(T, k, device=DEV)
+    y = torch.empty_like(x)
+    dora.dora_expert_return(xs, inverse, offsets, w, y)
+    d, dw = torch.empty_like(xs), torch.empty_like(w)
+    dora.dora_expert_return_bwd(x, xs, inverse, offsets, w, d, dw)
+    rows, ws, xd = xs[at].double(), w[some].double(), x[some].double()
+    ref, mag = (ws[:, :, None] * rows).sum(1), (ws[:, :, None] * rows.abs()).sum(1)
+    assert ((y[some].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * 2 * k * 2.0 ** -24 * mag).all()
+    ref = ws[:, :, None] * xd[:, None]
+    assert ((d[at].double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -23) * ref.abs()).all()
+    ref, mag = (rows * xd[:, None]).sum(-1), (rows * xd[:, None]).abs().sum(-1)
+    assert ((dw[some].double() - ref).abs() <= 2 * cols * 2.0 ** -24 * mag).all()
