@@ -501,6 +501,8 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
     const int quads = ntok * 32;
     const uint32_t base = smem_u32(smem);
     for (int i = static_cast<int>(rank) * F::kThreads + threadIdx.x; i < quads; i += static_cast<int>(csize) * F::kThreads) {
+      const int t = o.t0 + i / 32, f = f0 + 4 * (i % 32);
+      if (f >= p.nfeat) continue;   // nothing is read that no store waits for
       float4 s = ld_cluster_f32x4(mapa_shared(base + 16u * i, 0));
       for (uint32_t c = 1; c < csize; ++c) {
         const float4 v = ld_cluster_f32x4(mapa_shared(base + 16u * i, c));
@@ -509,10 +511,8 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
         s.z += v.z;
         s.w += v.w;
       }
-      const int t = o.t0 + i / 32, f = f0 + 4 * (i % 32);
-      if (f < p.nfeat)
-        *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(t) * p.nfeat + f) =
-            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      *reinterpret_cast<uint2 *>(p.y + static_cast<int64_t>(t) * p.nfeat + f) =
+          make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
     }
   }
   __syncwarp();

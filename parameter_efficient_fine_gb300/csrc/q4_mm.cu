@@ -377,9 +377,6 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();
-            } else {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(rempty0 + 8u * slot);
             }
             if (TRANS) {
               const uint32_t dst = to + 2 * blk * stage_bytes + h * kPanel;
@@ -390,6 +387,10 @@ q4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
             }
           }
           if (!ok) break;
+          // W's slot only now, behind stores that take what was loaded from it: an arrival
+          // right after the loads does not wait for them, and the next copy overtook some
+          __syncwarp();
+          if (lane == 0) mbar_arrive(rempty0 + 8u * slot);
           if (TRANS) {
             fence_async_proxy();
             __syncwarp();

@@ -295,6 +295,24 @@ def test_same_bits_again_and_nothing_else_written(T, t):
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("T,out,inp,t", [(600, 1024, 8192, False), (129, 4096, 8192, False), (1000, 4096, 4096, True),
+                                         (600, 4096, 1024, True), (5, 1040, 8192, False), (50, 1040, 8224, False)])
+def test_many_calls_give_the_same_bits(T, out, inp, t):
+    """Long rings of copies, conversions and products, over and over with other work
+    between: a slot that was given back too early would show as another result."""
+    torch.manual_seed(T)
+    wq = torch.randint(0, 256, (out, inp // 2), dtype=U8, device=DEV)
+    ws = torch.randint(115, 125, (out, inp // 32), dtype=U8, device=DEV)
+    x = torch.randn(T, out if t else inp, device=DEV).to(BF16)
+    big = torch.empty(200 << 20, dtype=U8, device=DEV)
+    first = run(x, wq, ws, t)
+    for i in range(60):
+        if i % 3 == 0:
+            big.fill_(i)                                 # out of L2
+        assert torch.equal(run(x, wq, ws, t), first), i
+    assert_no_device_error()
+
+
 @pytest.mark.parametrize("t", [False, True], ids=["xWt", "dyW"])
 @pytest.mark.parametrize("T", [1, 24, 600])
 def test_error_of_a_row_is_what_rounding_leaves(T, t):
