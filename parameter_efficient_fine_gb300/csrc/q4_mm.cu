@@ -42,7 +42,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -520,13 +520,15 @@ q4_join_kernel(const float4 *__restrict__ parts, int n, int T, int quads, const 
 // the pairs that a GB300 holds, a fixed number so that the workspace is the same
 // everywhere.  A block of k takes the conversion's time, above 192 tokens the MMAs'
 // (or, of dy W, the copies' with half of the slots); parts cost their way through memory
-// and a launch.  Experts: a tile at least, half a tile more than their tokens fill where
-// they fill more, and of two plans alike the wider tiles, which even loads suit.
+// and a launch.
 // One weight: within 2% of the best of all widths and parts but for the smallest (129 x
 // 8192 x 8192: 160 tokens in 2 parts 22.4 us, in 3 29.4, in 4 25.7; 129 x 1024 x 1024 8.2,
-// 7.1).  Experts depend on the loads: 4096 uneven ones at 32 of 2048 x 4096 68 us by 192
-// tokens, 71.5 by 256, 76 by 160, 87 by 128; dy W 85, 92, 103, 109; 5000 at 48 of 512 x
-// 4096, dy W, 65 by 192, 60 by 256.
+// 7.1).  Experts: the host does not know their loads, which are taken as squares of
+// even numbers, up to three times the mean; so an expert has a (k + 1)th tile in 1 -
+// sqrt(k n / most) of the cases, and a last wave behind others counts half.  Over four draws of such
+// loads, us by 256 tokens and by 192: 4096 at 32 of 2048 x 4096 72-74, 78-80; 1001 at 8
+// of 1040 x 2080 16.1, 14.1; dy W 13-19, 17; 8192 at 64 of 1024 x 2048 47-49, 49-50; dy W
+// 58-59, 62.
 struct Plan {
   int ntok, parts;
 };
@@ -538,13 +540,19 @@ Plan plan(bool trans, int64_t T, int64_t nfeat, int64_t kdim, int64_t experts) {
   for (int n = 32; n <= kTileT; n += 32)
     for (int parts = 1; parts <= 8; ++parts) {
       if (parts > 1 && blocks < 4 * parts) break;
-      int64_t tiles = ftiles * dora::ceil_div(T, n);
+      double waves, block;
       if (experts > 1) {
-        const double fill = static_cast<double>(T) / static_cast<double>(groups * n);
-        tiles = ftiles * static_cast<int64_t>(groups * std::max(1.0, fill + 0.5 * std::min(fill, 1.0)) + 0.5);
+        const double most = 3.0 * static_cast<double>(T) / static_cast<double>(groups * n);
+        double tiles = 0;
+        for (int k = 0; k < most; ++k) tiles += 1 - std::sqrt(k / most);
+        waves = tiles * static_cast<double>(groups * ftiles * parts) / kPairs;
+        waves = waves < 1 ? 1 : (waves + std::ceil(waves)) / 2;
+        block = trans ? (n > 192 ? 0.59 : 0.57) : (n > 192 ? 0.52 : 0.5);
+      } else {
+        waves = static_cast<double>(dora::ceil_div(ftiles * dora::ceil_div(T, n) * parts, kPairs));
+        block = (trans ? (n > 192 ? 0.64 : 0.57) : (n > 192 ? 0.56 : 0.5)) + 0.0001 * n;
       }
-      const double block = (trans ? (n > 192 ? 0.64 : 0.57) : (n > 192 ? 0.56 : 0.5)) + (experts > 1 ? -0.0001 : 0.0001) * n;
-      double cost = static_cast<double>(dora::ceil_div(tiles * parts, kPairs)) * (dora::ceil_div(blocks, parts) * block + 1.5);
+      double cost = waves * (dora::ceil_div(blocks, parts) * block + 1.5);
       if (parts > 1) cost += 2.5 + static_cast<double>(parts) * T * nfeat * 8 / 5e6;
       if (least == 0 || cost < least) {
         least = cost;
