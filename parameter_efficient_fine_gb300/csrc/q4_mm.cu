@@ -28,14 +28,14 @@
 // experts of 2048 x 4096: 76 us, 96 with all tiles' MMAs 256 wide).
 //
 // What bounds it: with 256 tokens, the MMAs, 0.56 us a block of 128 k, and over longer
-// calls the power limit (8192 x 4096 x 4096 144 to 147 us, 1.9 PFLOP/s; 15360 x 8192 x
-// 8192 1135; 512 x 8192 x 8192 43); of dy W they read both operands from shared memory
-// and take a little more (15360 x 8192 x 8192 1150 us, 1.8 PFLOP/s; 512 44).  With up to
-// 192 the conversion and its hand-overs, about 0.46 us a block whatever the tokens
-// (128 x 38912 x 4096 33.6 us; 700 x 8192 x 8192 61; 4096 tokens at 32 experts of 2048 x
-// 4096 63 to 68, dy W 74 to 85).  Its groups take whole blocks: with half blocks, whose
-// waits and addresses count twice, and looked-up values the last were 40, 70, 77 and 95,
-// and dy W 512 53.
+// calls the power limit (8192 x 4096 x 4096 143 to 147 us, 1.9 PFLOP/s; 15360 x 8192 x
+// 8192 1127; 512 x 8192 x 8192 42); of dy W they read both operands from shared memory
+// and take a little more (15360 x 8192 x 8192 1145 to 1170 us, 1.8 PFLOP/s; 512 44).  With
+// up to 192 the conversion and its hand-overs, about 0.46 us a block whatever the tokens
+// (128 x 38912 x 4096 34 us; 700 x 8192 x 8192 61; 4096 tokens evenly at 32 experts of
+// 2048 x 4096 64, unevenly 74, dy W 77 and 86 to 95).  Its groups take whole blocks, with
+// half the waits and addresses of half blocks (with those, and values by a table, 128 x
+// 38912 x 4096 took 40, 700 70, dy W 512 53).
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -525,10 +525,10 @@ q4_join_kernel(const float4 *__restrict__ parts, int n, int T, int quads, const 
 // 8192 x 8192: 160 tokens in 2 parts 22.4 us, in 3 29.4, in 4 25.7; 129 x 1024 x 1024 8.2,
 // 7.1).  Experts: the host does not know their loads, which are taken as squares of
 // even numbers, up to three times the mean; so an expert has a (k + 1)th tile in 1 -
-// sqrt(k n / most) of the cases, and a last wave behind others counts half.  Over four draws of such
-// loads, us by 256 tokens and by 192: 4096 at 32 of 2048 x 4096 72-74, 78-80; 1001 at 8
-// of 1040 x 2080 16.1, 14.1; dy W 13-19, 17; 8192 at 64 of 1024 x 2048 47-49, 49-50; dy W
-// 58-59, 62.
+// sqrt(k n / most) of the cases, and a last wave behind others counts half.  Over four
+// draws of such loads, us by 256 tokens and by 192: 4096 at 32 of 2048 x 4096 72-74,
+// 78-80; 1001 at 8 of 1040 x 2080 16.1, 14.1; dy W 13-19, 17; 8192 at 64 of 1024 x 2048
+// 47-49, 49-50; dy W 58-59, 62.
 struct Plan {
   int ntok, parts;
 };

@@ -117,8 +117,8 @@ inline bool map_w(CUtensorMap *map, const void *base, int64_t experts, int64_t o
 namespace dora {
 
 // x W^T of few tokens (q4_few.cu): up to so many a weight (us, that kernel / pairs: 64 x 8192 x 8192
-// 17.4 / 20.2, 70 21.8 / 20.6, 128 23.5 / 22.0; at 32 experts of 2048 x 4096, 32 tokens each
-// 45.6 / 62.8, 64 55 / 63, 16 experts of 128 50.7 / 35.0)
+// 15.9 / 19.6; at 32 experts of 2048 x 4096, 32 tokens each 41.7 / 59.4, 64 52.5 / 60.5.  With 128 in
+// a tile it took 23.5 for 128 x 8192 x 8192 and 50.7 for 2048 tokens at 16 experts, pairs 21.5 and 35)
 constexpr int64_t kQ4Few = 64;
 inline int64_t q4_per(int64_t T, int64_t experts) { return experts < T ? ceil_div(T, experts) : 1; }
 size_t q4_few_workspace(int64_t T, int64_t in, int64_t per);
