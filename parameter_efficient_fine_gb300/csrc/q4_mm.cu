@@ -537,28 +537,31 @@ Plan plan(bool trans, int64_t T, int64_t nfeat, int64_t kdim, int64_t experts) {
   const int64_t groups = experts < T ? experts : T, ftiles = dora::ceil_div(nfeat, kTileF), blocks = dora::ceil_div(kdim, kKB);
   Plan best = {kTileT, 1};
   double least = 0;
-  for (int n = 32; n <= kTileT; n += 32)
+  for (int n = 32; n <= kTileT; n += 32) {
+    double tiles = static_cast<double>(ftiles * dora::ceil_div(T, n));
+    if (experts > 1) {
+      const double most = 3.0 * static_cast<double>(T) / static_cast<double>(groups * n);
+      double own = 0;
+      if (most > 6) own = most / 3 + 0.5;          // what the sum tends to (6: 2.58)
+      else
+        for (int k = 0; k < most; ++k) own += 1 - std::sqrt(k / most);
+      tiles = own * static_cast<double>(groups * ftiles);
+    }
+    const bool wide = n > 192;
+    const double block = experts > 1 ? (trans ? (wide ? 0.59 : 0.57) : (wide ? 0.52 : 0.5))
+                                     : (trans ? (wide ? 0.64 : 0.57) : (wide ? 0.56 : 0.5)) + 0.0001 * n;
     for (int parts = 1; parts <= 8; ++parts) {
-      if (parts > 1 && blocks < 4 * parts) break;
-      double waves, block;
-      if (experts > 1) {
-        const double most = 3.0 * static_cast<double>(T) / static_cast<double>(groups * n);
-        double tiles = 0;
-        for (int k = 0; k < most; ++k) tiles += 1 - std::sqrt(k / most);
-        waves = tiles * static_cast<double>(groups * ftiles * parts) / kPairs;
-        waves = waves < 1 ? 1 : (waves + std::ceil(waves)) / 2;
-        block = trans ? (n > 192 ? 0.59 : 0.57) : (n > 192 ? 0.52 : 0.5);
-      } else {
-        waves = static_cast<double>(dora::ceil_div(ftiles * dora::ceil_div(T, n) * parts, kPairs));
-        block = (trans ? (n > 192 ? 0.64 : 0.57) : (n > 192 ? 0.56 : 0.5)) + 0.0001 * n;
-      }
-      double cost = waves * (dora::ceil_div(blocks, parts) * block + 1.5);
+      if (parts > 1 && (blocks < 4 * parts || tiles * (parts - 1) > 4 * kPairs)) break;   // enough without
+      double waves = std::ceil(tiles * parts / kPairs);
+      if (experts > 1 && waves > 1) waves = (waves + tiles * parts / kPairs) / 2;
+      double cost = waves * (static_cast<double>(dora::ceil_div(blocks, parts)) * block + 1.5);
       if (parts > 1) cost += 2.5 + static_cast<double>(parts) * T * nfeat * 8 / 5e6;
       if (least == 0 || cost < least) {
         least = cost;
         best = {n, parts};
       }
     }
+  }
   return best;
 }
 size_t parts_bytes(const Plan &pl, int64_t T, int64_t nfeat) {
