@@ -571,7 +571,8 @@ void few_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int64_t tile
   cfg->numAttrs = 2;
 }
 
-// clusters of 2^`log` CTAs that are resident at once
+// clusters of 2^`log` CTAs that are resident at once, at least: the query counts one CTA an
+// SM of these kernels where two run, and twice that leaves out what remains of each group of SMs
 template <int NT, bool BOX> int resident_clusters(int device, int log) {
   using F = Few<NT, BOX>;
   static std::mutex mu;
@@ -588,7 +589,6 @@ template <int NT, bool BOX> int resident_clusters(int device, int log) {
       cudaGetLastError();
       n = 0;
     }
-    // the query counts one CTA an SM of these kernels, two run
     int one = 1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&one, q4_few_kernel<NT, BOX>, F::kThreads, F::kSmem) != cudaSuccess || one < 1) one = 1;
     k = n * F::kPerSm / one + 1;
@@ -597,14 +597,20 @@ template <int NT, bool BOX> int resident_clusters(int device, int log) {
 }
 
 template <int NT, bool BOX>
-dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, int device, cudaStream_t cs) {
+dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, int device, int sms, cudaStream_t cs) {
   using F = Few<NT, BOX>;
   const int64_t groups = p.offsets ? (p.experts < p.T ? p.experts : p.T) : 1;
   const int64_t tiles = p.ftiles * (p.offsets ? p.T / NT + groups : 1);
-  // the k range over as many CTAs as keep all clusters resident
+  // the k range over as many CTAs as keep all clusters resident.  Up to 27 CTAs on 16 SMs
+  // were, as clusters of 8 too: 1 x 4096 x 14336 11.1 us, by the query's count 15.5.  With x
+  // in pieces the joins of so many take more than they give unless each has 8 blocks (64 x
+  // 4096 x 4096 10.2, 9.2; 37 x 4096 x 14336 15.1, 18.3)
   int log = 0;
   const int64_t blocks = dora::ceil_div(p.in, kKB);
-  while (log < kMaxClusterLog && (2 << log) <= blocks && tiles <= resident_clusters<NT, BOX>(device, log + 1)) ++log;
+  while (log < kMaxClusterLog && (2 << log) <= blocks &&
+         (tiles <= resident_clusters<NT, BOX>(device, log + 1) ||
+          (tiles << (log + 1) <= sms * 27 / 16 && (!F::kSplit || 16 << log <= blocks))))
+    ++log;
   if (tiles << log > kMaxDim) return DORA_ERR_SHAPE;
   p.ntok = NT;
   p.tiles = static_cast<int>(tiles);
@@ -635,10 +641,10 @@ dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, i
 }
 
 template <int NT>
-dora_status launch(const void *x, const void *wq, const Q4Params &p, void *workspace, int device, cudaStream_t cs) {
+dora_status launch(const void *x, const void *wq, const Q4Params &p, void *workspace, int device, int sms, cudaStream_t cs) {
   // boxes of 4-bit values take whole blocks of 128 and 32-byte rows
-  return p.in % kKB == 0 && dora::aligned(wq, 32) ? launch<NT, true>(x, wq, p, workspace, device, cs)
-                                                  : launch<NT, false>(x, wq, p, workspace, device, cs);
+  return p.in % kKB == 0 && dora::aligned(wq, 32) ? launch<NT, true>(x, wq, p, workspace, device, sms, cs)
+                                                  : launch<NT, false>(x, wq, p, workspace, device, sms, cs);
 }
 
 }  // namespace
@@ -673,10 +679,10 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   p.y = static_cast<__nv_bfloat16 *>(y);
   p.ftiles = static_cast<int>(ceil_div(out, kTcM));
   const int64_t per = offsets ? q4_per(T, experts) : T;
-  if (per <= 8) return launch<8>(x, wq, p, workspace, device, cs);
-  if (per <= 16) return launch<16>(x, wq, p, workspace, device, cs);
-  if (per <= 32) return launch<32>(x, wq, p, workspace, device, cs);
-  return launch<64>(x, wq, p, workspace, device, cs);
+  if (per <= 8) return launch<8>(x, wq, p, workspace, device, info.sms, cs);
+  if (per <= 16) return launch<16>(x, wq, p, workspace, device, info.sms, cs);
+  if (per <= 32) return launch<32>(x, wq, p, workspace, device, info.sms, cs);
+  return launch<64>(x, wq, p, workspace, device, info.sms, cs);
 }
 
 }  // namespace dora
