@@ -32,7 +32,7 @@
 // What bounds it: reading W, in boxes of 64-byte rows, which TMA takes one by one, at
 // 3.8 TB/s, after a launch and the first loads' latency, 3.6 us.  1 x 8192 x 8192 11.2
 // us (5.3 to read it at the copy bandwidth), 1 x 14336 x 4096 10.6 (4.7), 37 of them 14.4,
-// 64 x 8192 x 8192 15.9, 8 tokens at as many experts of 2048 x 4096 11.3, 512 at 32 38.7 (22).
+// 4096 x 14336 11.1, 64 x 8192 x 8192 16.0, 8 tokens at as many experts of 2048 x 4096 11.3, 512 at 32 38.7 (22).
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -600,7 +600,8 @@ template <int NT, bool BOX>
 dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, int device, int sms, cudaStream_t cs) {
   using F = Few<NT, BOX>;
   const int64_t groups = p.offsets ? (p.experts < p.T ? p.experts : p.T) : 1;
-  const int64_t tiles = p.ftiles * (p.offsets ? p.T / NT + groups : 1);
+  // an expert of n tokens has (n - 1) / NT + 1
+  const int64_t tiles = p.ftiles * (p.offsets ? (p.T - groups) / NT + groups : 1);
   // the k range over as many CTAs as keep all clusters resident.  Up to 27 CTAs on 16 SMs
   // were, as clusters of 8 too: 1 x 4096 x 14336 11.1 us, by the query's count 15.5.  With x
   // in pieces the joins of so many take more than they give unless each has 8 blocks (64 x

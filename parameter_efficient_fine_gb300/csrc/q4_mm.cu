@@ -648,7 +648,9 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
   p.xrows = p.ntok / 2 <= 64 ? p.ntok / 2 : p.ntok / 4;
   p.parts = pl.parts;
   p.partial = static_cast<float *>(workspace);
-  const int64_t tiles = p.ftiles * (offsets ? T / p.ntok + (experts < T ? experts : T) : dora::ceil_div(T, p.ntok));
+  // an expert of n tokens has (n - 1) / ntok + 1
+  const int64_t groups = experts < T ? experts : T;
+  const int64_t tiles = p.ftiles * (offsets ? (T - groups) / p.ntok + groups : dora::ceil_div(T, p.ntok));
   if (tiles * p.parts > kMaxDim) return DORA_ERR_SHAPE;
   p.tiles = static_cast<int>(tiles);
   const int64_t units = tiles * p.parts;
