@@ -544,8 +544,8 @@ dora_status dora_q4_load(dora_dtype act, const void *q, const void *scale, int64
                          void *x, dora_stream_t stream);
 
 /* Bytes of workspace dora_matmul_q4 and dora_matmul_q4_t need, by the sizes alone: for
- * x W^T of 9 to 64 tokens a weight (T / experts, rounded up) 2 T in + 8 T ceil(in / 128),
- * for x in pieces; for others, where k is cut in parts to fill the device, 4 T out (dy W:
+ * x W^T of 9 to 64 tokens (of 5 to 64 an expert: T / experts, rounded up) 2 T in +
+ * 8 T ceil(in / 128), for x in pieces; for others, where k is cut in parts to fill the device, 4 T out (dy W:
  * 4 T in) a part; else 0, and the pointer may be NULL.  Nothing in it is kept from one
  * call to the next; calls that run at once need one each. */
 size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts);

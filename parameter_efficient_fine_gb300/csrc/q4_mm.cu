@@ -710,7 +710,7 @@ static bool bad_call(int64_t T, int64_t out, int64_t in, int64_t experts) {
 
 extern "C" size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {
   if (bad_call(T, out, in, experts)) return 0;
-  if (few(T, experts)) return dora::q4_few_workspace(T, in, dora::q4_per(T, experts));
+  if (few(T, experts)) return dora::q4_few_workspace(T, in, experts);
   return parts_bytes(plan(false, T, out, in, experts), T, out);
 }
 extern "C" size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {

@@ -121,7 +121,7 @@ namespace dora {
 // a tile it took 23.5 for 128 x 8192 x 8192 and 50.7 for 2048 tokens at 16 experts, pairs 21.5 and 35)
 constexpr int64_t kQ4Few = 64;
 inline int64_t q4_per(int64_t T, int64_t experts) { return experts < T ? ceil_div(T, experts) : 1; }
-size_t q4_few_workspace(int64_t T, int64_t in, int64_t per);
+size_t q4_few_workspace(int64_t T, int64_t in, int64_t experts);
 dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
                           int64_t out, int64_t in, int64_t experts, void *y, void *workspace, cudaStream_t cs);
 
