@@ -198,7 +198,10 @@ def test_tiles_of_every_width_in_turn(t):
 
 EXPERTS = [
     ([0, 1], 64, 96), ([0, 0, 3, 3, 4, 4], 272, 544), ([0, 5, 5, 40, 41, 300], 144, 160), ([0] * 40 + [2, 2, 9, 9], 256, 384),
-    ([0, 700, 701, 701], 400, 256), ([0, 30, 30, 100, 130], 272, 640), ([0, 1, 300, 301], 144, 384), ([0, 8, 16, 24, 32, 40, 48, 56, 64], 512, 1024), (list(range(0, 78, 2)), 48, 2080)]
+    ([0, 700, 701, 701], 400, 256), ([0, 30, 30, 100, 130], 272, 640), ([0, 1, 300, 301], 144, 384), ([0, 8, 16, 24, 32, 40, 48, 56, 64], 512, 1024), (list(range(0, 78, 2)), 48, 2080),
+    # few tokens, some experts with more than a tile holds
+    ([0, 0, 1, 3, 43, 46, 46, 63, 72], 272, 384), ([0, 30, 31, 33, 36, 38], 144, 1024), ([0, 0, 0, 0, 150, 160], 272, 544),
+    ([0, 0, 20, 20, 20, 20], 528, 4096)]
 
 
 @pytest.mark.parametrize("t", [False, True], ids=["xWt", "dyW"])

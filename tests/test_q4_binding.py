@@ -141,6 +141,8 @@ def test_workspaces():
     w, wt = dora.dora_matmul_q4_workspace, dora.dora_matmul_q4_t_workspace
     assert w(1, 8192, 8192) == w(8, 8192, 8192) == 0 and w(15360, 8192, 8192) == wt(15360, 8192, 8192) == 0
     assert w(9, 64, 128) == 2 * 9 * 128 + 8 * 9                # pieces of x and their scale words
+    # experts: tiles for twice the mean
+    assert w(32, 64, 128, 8) == 0 and w(40, 64, 128, 8) == w(33, 64, 128, 8) // 33 * 40 == 2 * 40 * 128 + 8 * 40
     for bad in ((0, 64, 128, 1), (9, 0, 128, 1), (9, 64, 0, 1), (9, 64, 128, 0), (9, 64, 128, 5000)):
         assert w(*bad) == wt(*bad) == 0
     # never more than eight parts of the result
