@@ -544,8 +544,8 @@ dora_status dora_q4_load(dora_dtype act, const void *q, const void *scale, int64
                          void *x, dora_stream_t stream);
 
 /* Bytes of workspace dora_matmul_q4 and dora_matmul_q4_t need, by the sizes alone: for
- * x W^T of 9 to 64 tokens (of 5 to 64 an expert: T / experts, rounded up) 2 T in +
- * 8 T ceil(in / 128), for x in pieces; for others, where k is cut in parts to fill the device, 4 T out (dy W:
+ * x W^T of 9 to 32 tokens (of 5 to 16 an expert: T / experts, rounded up; where in is no
+ * multiple of 128, to 16 and to 8) 2 T in + 8 T ceil(in / 128), for x in pieces; for others, where k is cut in parts to fill the device, 4 T out (dy W:
  * 4 T in) a part; else 0, and the pointer may be NULL.  Nothing in it is kept from one
  * call to the next; calls that run at once need one each. */
 size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts);
@@ -564,10 +564,11 @@ size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t ex
  *   workspace  dora_matmul_q4_workspace bytes, 256-byte aligned
  *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1, below 2^31 - 1023,
  *   1 <= experts <= 4096.
- * Up to 64 tokens a weight, x enters as two 8-bit pieces and is off by at most 2^-21 of
- * the largest magnitude among its 32 neighbours of a scale, and an infinity in it counts
- * as NaN; above, W enters as bf16, which is exact.  Parts are summed in a fixed order:
- * the same call gives the same bits.
+ * Both operands enter as they are, infinities and the smallest numbers too, however many
+ * tokens there are; a result below 2^-126 may be flushed to zero.  Parts are summed in a
+ * fixed order: the same call gives the same bits.  Of few tokens x enters as 8-bit
+ * pieces, up to four; where those do not hold 32 neighbouring values (an infinity, values
+ * more than 2^36 apart), the call is slower.
  * One launch, or two where there is a workspace.  They are programmatic dependent ones:
  * their set-up overlaps the launch before them, and they read (but for lines of W asked
  * into L2) and write nothing of the caller's before that has completed.

@@ -5,34 +5,43 @@
 // row of either operand by a power of two, which is W's form.  x, a bf16, becomes
 // two E4M3 pieces with a scale per 32 columns: h = E4M3(x / s), s the power of two
 // that brings the group's largest magnitude to at most 448, and E4M3((x / s - h) 16)
-// with the scale s / 16.  8 bits less the 4 of h leave 4, so x / s is their sum
-// exactly down to 2^-6, and within 2^-14 below: an error of at most 2^-21 of the
-// group's largest magnitude, as the fp32 sum itself makes.
+// with the scale s / 16.  8 bits less the 4 of h leave 4, so x / s is their sum exactly
+// where it is a multiple of 2^-13: always from 2^-6 on, 2^-14 of the largest magnitude.
+// Of 32 normal values one is below that with low bits set in 0.3% of the cases, beside
+// one 24 times louder in 4%.  What the two pieces leave of such a group is at most 2^-14
+// and becomes two more, 2^22 finer.  A group that those do not hold either (an
+// infinity, values more than 2^36 apart) is added at the end in fp32 (add_rest).  So x
+// counts as it is, whatever its neighbours and however many tokens there are.
 //
 // The features are the M side, the tokens' pieces the N side (NT first pieces, NT
-// second ones).  A tile of 128 features and up to NT tokens is a cluster of CTAs
-// that share its k range and meet in distributed shared memory, summed in rank
+// second ones; in blocks that have such a group, third and fourth ones by MMAs of their
+// own into the same sums).  A tile of 128 features and up to NT tokens is a cluster of
+// CTAs that share its k range and meet in distributed shared memory, summed in rank
 // order.
 //   workers      up to 8 tokens: x of a block of 128 k into pieces, in place, each
-//                warp the blocks of its own in turn; then the result out of tensor
-//                memory.  More tokens are split by a launch of its own before
-//                (q4_split_kernel), while this one's first blocks of W are already
-//                on their way (8 x 8192 x 8192 12.8 us, 9 13.8)
+//                warp the blocks of its own in turn.  More tokens are split by a launch
+//                of its own before (q4_split_kernel), while this one's first blocks of W
+//                are already on their way (8 x 8192 x 8192 14.4 us, 9 13.9).  Third and
+//                fourth pieces of either, from x in memory, one block in five of a
+//                token's, half of 32 tokens'.  Then the result out of tensor memory
 //   next warp    tensor memory, scale words into it, MMA issue (four 32-wide steps per
 //                block)
 //   next warps   copies of W; copies of x or its pieces; W's scale words (BOX)
 // The tensor core takes 4-bit values 16 to every 16 bytes of shared memory, in 8 of
 // them.  TMA lays W out like that where its rows are whole blocks of 128 (BOX); else
 // a block arrives as it is stored, in the half of its place, and a worker spreads it
-// (1 x 8192 x 8192 11.2 us, 8224 columns 14.7).  From boxes of 256 k, whose rows are
-// twice as long, all of W spread by workers took 13.6.
-// W's scales go through registers, 16 bytes of a row at a time (13.0 us with a copy of
-// 4 bytes a row and block straight to their place).
+// (1 x 8192 x 8192 11.6 us, 8224 columns 15.3).  From boxes of 256 k, whose rows are
+// twice as long, all of W spread by workers took 2.4 us more than boxes of 128 do.
+// W's scales go through registers, 16 bytes of a row at a time (1.8 us less than a copy
+// of 4 bytes a row and block straight to their place).
 //
-// What bounds it: reading W, in boxes of 64-byte rows, which TMA takes one by one, at
-// 3.8 TB/s, after a launch and the first loads' latency, 3.6 us.  1 x 8192 x 8192 11.2
-// us (5.3 to read it at the copy bandwidth), 1 x 14336 x 4096 10.6 (4.7), 37 of them 14.4,
-// 4096 x 14336 11.1, 64 x 8192 x 8192 16.0, 8 tokens at as many experts of 2048 x 4096 11.3, 512 at 32 38.7 (22).
+// What bounds it: reading W, in boxes of 64-byte rows, which TMA takes one by one: 4.4 us
+// for a launch and the first loads, then 4.9 TB/s (1 x 8192 x 8192 11.6 us, 16384 x 8192
+// 18.7, 32768 x 8192 33.1; 14336 x 4096 10.9, 4096 x 14336 11.5; at the copy bandwidth the
+// first takes 5.3).  Of more tokens also the workers: 16 x 8192 x 8192 15.1, 32 16.9, where
+// values of one binade, which two pieces always hold, take 13.6 and 14.5.  8 tokens at as many
+// experts of 2048 x 4096 11.9, 512 at 32 45 (22).  x whose groups no pieces hold is slow: where
+// all are such, 1 x 8192 x 8192 75 us, 8 290, 32 1150.
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
 // a code in the library's device error word and all roles leave.
 #include <cuda.h>
@@ -53,31 +62,31 @@ namespace {
 constexpr int kKB = 128;                    // k per stage
 constexpr unsigned kWBytes = kTcM * kKB;    // 16 KB of shared memory, 8 of W
 constexpr int kMaxClusterLog = 3;           // 8 CTAs, the portable limit
-// blocks asked into L2 while the launch before ends (1 x 8192 x 8192: 0 0.5 us more, 16 1.5)
+// blocks asked into L2 while the launch before ends (1 x 8192 x 8192: 0 0.3 us more, 16 1.3)
 constexpr int kAheadL2 = 6;
 constexpr unsigned kSfBytes = kTcM * 4;     // scale words of 128 rows
 
 // what a kernel of up to NT tokens a tile is made of
 template <int NT, bool BOX> struct Few {
   static constexpr bool kSplit = NT > 8;                        // x comes in pieces
-  static constexpr int N = 2 * NT;                              // rows of pieces
+  static constexpr int N = 2 * NT;                              // rows of first and second pieces
   static constexpr int kPerSm = 2;                              // CTAs, limited by shared memory
-  static constexpr int kStages = NT <= 16 ? 5 : NT == 64 ? 3 : 4;   // blocks of W
-  static constexpr int kXStages = NT == 8 ? 10 : kStages;       // blocks of x
+  static constexpr int kStages = NT == 32 ? 3 : 4;              // blocks of W
+  static constexpr int kXStages = NT == 8 ? 8 : kStages;        // blocks of x
   static constexpr int kWorkers = kStages < 4 ? 4 : kStages;
   static constexpr int kMma = kWorkers, kCopyW = kMma + 1, kCopyX = kMma + 2, kScale = kMma + 3, kThreads = 32 * (kMma + 3 + (BOX ? 1 : 0));
-  static constexpr unsigned kXSf = kSfBytes;                    // scale words of a block of pieces
-  static constexpr unsigned kXBytes = N * kKB;
-  // tensor memory: the result, then 4 columns of W's scale words and 4 of x's for each stage
-  static constexpr int kSfCol = N < 64 ? 64 : N, kSfStride = 8;
-  static constexpr int kCols = NT == 64 ? 256 : 128;
+  static constexpr unsigned kXSf = 2 * kSfBytes;                // scale words of a block: first and second pieces, third and fourth
+  static constexpr unsigned kXBytes = 2 * N * kKB;              // first and second pieces, third and fourth
+  // tensor memory: the result, then 4 columns of W's scale words and 8 of x's for each stage
+  static constexpr int kSfCol = 64, kSfStride = 12, kCols = 128;
+  static constexpr int kLeftWords = 8;                          // a bit a block, of 256 in turn
   static constexpr int kBars = 3 * kStages + 3 * kXStages + 1;
   static constexpr size_t kSmem = 1024 + kStages * (kWBytes + kSfBytes) + kXStages * (kXBytes + kXSf) + 8 * kBars +
-                                  sizeof(SharedCtl);
+                                  sizeof(SharedCtl) + 4 * (kXStages + kLeftWords);
   // a wait goes by the parity of a phase, so a worker's slots are its own: it visits
   // every use of them in turn
   static_assert(kXStages % kStages == 0 && kStages <= kWorkers, "slots of a worker");
-  static_assert(kSfCol + kSfStride * kStages <= kCols && kPerSm * kCols <= 512, "tensor memory");
+  static_assert(N <= kSfCol && kSfCol + kSfStride * kStages <= kCols && kPerSm * kCols <= 512, "tensor memory");
   static_assert(kPerSm * (kSmem + 1024) <= kSmemMax + 1024, "shared memory, with 1 KB of the system's a CTA");
   static_assert(NT * kTcM * 4 <= kStages * kWBytes + kXStages * kXBytes, "the parts lie in the blocks");
 };
@@ -106,9 +115,13 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
   const uint64_t d = ((saddr & 0x3FFFFu) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
+// whether two pieces hold a value of a group over its scale: whether it is a multiple of
+// 2^-13, the step of fp32 from 1024 to 2048 (a NaN is none)
+__device__ __forceinline__ bool held(float v) { return __fsub_rn(__fadd_rn(v, 1536.0f), 1536.0f) == v; }
 // Two pieces of four values of a group of 32 that 8 neighbouring lanes hold, and the
-// first one's scale byte; the second's is 4 less
-__device__ __forceinline__ void split4(uint2 raw, uint32_t *h, uint32_t *l, uint32_t *byte) {
+// first one's scale byte; the second's is 4 less.  Returns which of the warp's four
+// groups the pieces do not hold, 1 in the byte of each
+__device__ __forceinline__ uint32_t split4(uint2 raw, uint32_t *h, uint32_t *l, uint32_t *byte) {
   float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
                 __uint_as_float(raw.y & 0xffff0000u)};
   uint32_t m = 0;
@@ -120,17 +133,44 @@ __device__ __forceinline__ void split4(uint2 raw, uint32_t *h, uint32_t *l, uint
   *byte = scale_byte(m);
   const float inv = scale_inverse(*byte);
   float f[4];
+  bool all = true;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = inf_to_nan(v[i]) * inv;
+  for (int i = 0; i < 4; ++i) {
+    v[i] = inf_to_nan(v[i]) * inv;
+    all = all && held(v[i]);
+  }
   *h = quant4(v, 1.0f);
   dequant4(*h, 1.0f, f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = v[i] - f[i];
   *l = quant4(f, 16.0f);
+  uint32_t left = __ballot_sync(0xffffffffu, !all);
+  left |= left >> 4;
+  left |= left >> 2;
+  return (left | left >> 1) & 0x01010101u;
 }
 
-// x [T, in] into pieces: first ones [T, in], second ones [T, in], then their scale words
-// [blocks, 2, T], a byte per 32 columns
+// A group, a value a lane: what split4's pieces leave of it in two more, with scale bytes
+// 22 and 26 less than the first's.  False where they do not hold it
+__device__ __forceinline__ bool split_rest(float v, uint32_t *h, uint32_t *l, uint32_t *byte) {
+  *byte = scale_byte(__reduce_max_sync(0xffffffffu, finite_bits(v)));
+  // (a NaN is one in the first piece already, an infinity is held by none)
+  float r = v == v ? inf_to_nan(v) * scale_inverse(*byte) : 0.0f;
+  auto less = [](float x, uint32_t piece) { return x - dequant2(piece, 1.0f).x; };
+  r = less(r, quant2(r, 0.0f, 1.0f)) * 16.0f;
+  r = less(r, quant2(r, 0.0f, 1.0f)) * 262144.0f;
+  *h = quant2(r, 0.0f, 1.0f) & 255u;
+  r = less(r, *h) * 16.0f;
+  *l = quant2(r, 0.0f, 1.0f) & 255u;
+  return __all_sync(0xffffffffu, less(r, *l) == 0.0f) && *byte >= 26u;
+}
+// this lane's column of a group of x
+__device__ __forceinline__ float load_bf16(const __nv_bfloat16 *p) {
+  return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short *>(p))) << 16);
+}
+
+// x [T, in] into pieces: first ones [T, in], second ones [T, in], then [blocks, 2, T] words, a byte
+// per 32 columns: scales of the first; 1 where the two do not hold the group
 constexpr int kSplitThreads = 256;
 __global__ void __launch_bounds__(kSplitThreads)
 q4_split_kernel(const __nv_bfloat16 *__restrict__ x, int T, int in, uint8_t *__restrict__ pieces) {
@@ -142,7 +182,7 @@ q4_split_kernel(const __nv_bfloat16 *__restrict__ x, int T, int in, uint8_t *__r
     // a warp holds a block of 128 columns; any scale past the row
     const int64_t at = static_cast<int64_t>(t) * in + c;
     uint32_t h, l, b;
-    split4(c < in ? __ldg(reinterpret_cast<const uint2 *>(x + at)) : make_uint2(0, 0), &h, &l, &b);
+    const uint32_t left = split4(c < in ? __ldg(reinterpret_cast<const uint2 *>(x + at)) : make_uint2(0, 0), &h, &l, &b);
     if (c < in) {
       *reinterpret_cast<uint32_t *>(pieces + at) = h;
       *reinterpret_cast<uint32_t *>(pieces + all + at) = l;
@@ -152,7 +192,49 @@ q4_split_kernel(const __nv_bfloat16 *__restrict__ x, int T, int in, uint8_t *__r
     if ((threadIdx.x & 31) == 0 && c < in) {
       uint32_t *at = words + 2 * static_cast<int64_t>(c / kKB) * T + t;
       at[0] = b;
-      at[T] = b - 0x04040404u;
+      at[T] = left;
+    }
+  }
+}
+
+// The groups of x that no pieces hold, in blocks that `bits` names, added to the tile's result
+// [token][feature] in fp32 and in the order of k, from W and x as they are; a thread has
+// feature f of the tile.  It is slow, as every group of such a block is looked at, and seldom called.
+__device__ __forceinline__ void add_rest(const Q4Params &p, const uint8_t *wq, const __nv_bfloat16 *x, const Tile &o, int f0,
+                                         int f, int kb0, int nb, const uint32_t *bits, float *part) {
+  constexpr int kAtOnce = 4;
+  const int lane = threadIdx.x & 31, G = p.in / kQ4Group;
+  const bool has = f0 + f < p.out;
+  const int64_t row = static_cast<int64_t>(o.e) * p.out + f0 + f;
+#pragma unroll 1
+  for (int b = 0; b < nb; ++b) {
+    if ((bits[b / 32 % 8] >> (b % 32) & 1u) == 0) continue;
+#pragma unroll 1
+    for (int g = 4 * (kb0 + b); g < min(4 * (kb0 + b) + 4, G); ++g) {
+      const uint4 q = has ? __ldcg(reinterpret_cast<const uint4 *>(wq + row * (p.in / 2) + g * (kQ4Group / 2))) : make_uint4(0, 0, 0, 0);
+      const float s = q4_scale(has ? __ldcg(p.scale + row * G + g) : 0u);
+      const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll 1
+      for (int t0 = o.t0; t0 < o.t1; t0 += kAtOnce) {
+        float v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+          v[i] = t0 + i < o.t1 ? load_bf16(x + static_cast<int64_t>(t0 + i) * p.in + g * kQ4Group + lane) : 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < min(kAtOnce, o.t1 - t0); ++i) {
+          const float xv = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
+          uint32_t h, l, byte;
+          if (split_rest(xv, &h, &l, &byte) || __all_sync(0xffffffffu, held(inf_to_nan(xv) * scale_inverse(byte)))) continue;
+          float sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < kQ4Group; j += 2) {
+            const float2 c = q4_value2(words[j / 8] >> (4 * (j % 8)) & 0xffu);
+            sum = fmaf(__shfl_sync(0xffffffffu, xv, j), c.x * s, sum);
+            sum = fmaf(__shfl_sync(0xffffffffu, xv, j + 1), c.y * s, sum);
+          }
+          part[(t0 + i - o.t0) * kTcM + f] += sum;
+        }
+      }
     }
   }
 }
@@ -160,7 +242,7 @@ q4_split_kernel(const __nv_bfloat16 *__restrict__ x, int T, int in, uint8_t *__r
 template <int NT, bool BOX>
 __global__ void __launch_bounds__(Few<NT, BOX>::kThreads, Few<NT, BOX>::kPerSm)
 q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const Q4Params p,
-              const uint8_t *wq, const uint32_t *xwords) {
+              const uint8_t *wq, const __nv_bfloat16 *x, const uint32_t *xwords) {
   using F = Few<NT, BOX>;
   constexpr int S = F::kStages, XS = F::kXStages, N = F::N;
   constexpr bool PRE = F::kSplit;
@@ -173,6 +255,9 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
   const uint32_t wfull0 = smem_u32(bars), wready0 = wfull0 + 8u * S, wempty0 = wready0 + 8u * S, xfull0 = wempty0 + 8u * S,
                  xready0 = xfull0 + 8u * XS, xempty0 = xready0 + 8u * XS, accf = xempty0 + 8u * XS;
   SharedCtl *ctl = reinterpret_cast<SharedCtl *>(bars + F::kBars);
+  // which blocks of x have third and fourth pieces [XS]; which have groups that no pieces hold
+  volatile uint32_t *wide = reinterpret_cast<uint32_t *>(ctl + 1);
+  uint32_t *left_out = reinterpret_cast<uint32_t *>(ctl + 1) + XS;
   const int warp = warp_index(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -187,6 +272,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
     }
     mbar_init(accf, 1);
     ctl->abort = 0;
+    for (int i = 0; i < F::kLeftWords; ++i) left_out[i] = 0;
     fence_barrier_init();
     prefetch_map(&mW);
     prefetch_map(&mX);
@@ -316,7 +402,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       const uint32_t xs = smem_u32(xs0) + st.i * F::kXBytes, full = xfull0 + 8u * st.i;
       const int k = (kb0 + b) * kKB;
       if (elect_one()) {
-        mbar_expect_tx(full, F::kXBytes);
+        mbar_expect_tx(full, N * kKB);
         // x as it is: the 256 bytes of token t where its two pieces go, rows t and NT + t
         tma_load_2d(xs, &mX, k, o.t0, full);
         tma_load_2d(xs + NT * kKB, &mX, PRE ? k : k + 64, PRE ? p.T + o.t0 : o.t0, full);
@@ -326,10 +412,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       if (PRE) {
         const uint32_t to = smem_u32(xsf0) + st.i * F::kXSf;
         const uint32_t *from = xwords + 2 * static_cast<int64_t>(kb0 + b) * p.T + o.t0;
-        for (int t = lane; t < ntok; t += 32) {
-          copy4(to + sf_at(t), from + t);
-          copy4(to + sf_at(NT + t), from + p.T + t);
-        }
+        for (int t = lane; t < ntok; t += 32) copy4(to + sf_at(t), from + t);
         copies_arrive(full);
       }
     }
@@ -343,7 +426,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
     // ---------------------------------------------------------------- MMA issuer
     Ring st(S), xt(XS);
     for (int b = 0; b < nb; ++b, st.next(), xt.next()) {
-      ok = guard_wait((PRE ? xfull0 : xready0) + 8u * xt.i, xt.phase, ctl, p.guard, 73);
+      ok = guard_wait(xready0 + 8u * xt.i, xt.phase, ctl, p.guard, 73);
       ok = ok && guard_wait((BOX ? wfull0 : wready0) + 8u * st.i, st.phase, ctl, p.guard, 74);
       if (!__all_sync(0xffffffffu, ok)) break;
       // x's scale words came by copies that the tensor core's reads are not ordered after
@@ -351,6 +434,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       tc_fence_after();
       const uint64_t da = sdesc<32>(smem_u32(smem) + st.i * kWBytes), db = sdesc<32>(smem_u32(xs0) + xt.i * F::kXBytes);
       const uint32_t sf = tmem + F::kSfCol + F::kSfStride * st.i;
+      const bool more = wide[xt.i] != 0;
       if (elect_one()) {
         // (a copy runs before the MMAs that this thread issues after it)
         copy_scales(sf, smem_u32(wsf0) + st.i * kSfBytes);
@@ -359,6 +443,12 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
         for (int k = 0; k < 4; ++k)
           mma_q8(tmem, da + 2u * k, db + 2u * k, idesc_q8(kTcM, N, k, false) | 5u << 7 /* A: E2M1 */, sf, sf + 4,
                  b != 0 || k != 0 ? 1u : 0u);
+        if (more) {
+          copy_scales(sf + 8, smem_u32(xsf0) + xt.i * F::kXSf + kSfBytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_q8(tmem, da + 2u * k, db + (N * kKB >> 4) + 2u * k, idesc_q8(kTcM, N, k, false) | 5u << 7, sf, sf + 8, 1u);
+        }
         mma_commit(wempty0 + 8u * st.i);
         mma_commit(xempty0 + 8u * xt.i);
       }
@@ -371,8 +461,8 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- workers
-    // blocks warp, warp + S, ...; none where there is nothing to do with them
-    if (warp < S && (!PRE || !BOX)) {
+    // blocks warp, warp + S, ...
+    if (warp < S) {
       Ring st(S), xt(XS);
       for (int i = 0; i < warp; ++i) {
         st.next();
@@ -393,14 +483,91 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
         }
       };
       if (!BOX) fetch(warp);
+      constexpr int kAtOnce = 4;                     // tokens, or groups left over, worked on together
+      // PRE: a byte of a token's word says whether the two pieces leave something of a group
+      auto mark = [&](int b) { return b < nb && lane < ntok ? __ldcg(xwords + (2 * static_cast<int64_t>(kb0 + b) + 1) * p.T + o.t0 + lane) : 0u; };
+      uint32_t marks = 0;
+      if (PRE) {
+        pdl_wait();
+        marks = mark(warp);
+      }
       for (int b = warp; b < nb; b += S) {
-        if constexpr (!PRE) {
-          ok = guard_wait(xfull0 + 8u * xt.i, xt.phase, ctl, p.guard, 75);
-          if (!__all_sync(0xffffffffu, ok)) break;
+        uint8_t *xs = xs0 + xt.i * F::kXBytes, *sf = xsf0 + xt.i * F::kXSf;
+        uint32_t over[4] = {}, rest[4] = {};         // of each group, tokens of which the two pieces leave something; the four too
+        // third and fourth pieces, zeros but for these groups.  x comes from memory once more.  PRE:
+        // while the first two are on their way, once the MMAs of the block before here are done
+        auto more_pieces = [&]() {
+          const __nv_bfloat16 *from = x + static_cast<int64_t>(o.t0) * p.in + (kb0 + b) * kKB + lane;
+          uint8_t *sf2 = sf + kSfBytes;
+          bool first = true;
+#pragma unroll 1
+          while ((over[0] | over[1] | over[2] | over[3]) != 0) {
+            int at[kAtOnce];                         // group and token
+            float v[kAtOnce];
+            uint32_t h[kAtOnce], l[kAtOnce], byte[kAtOnce];
+            bool all[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              const int g = over[0] != 0 ? 0 : over[1] != 0 ? 1 : over[2] != 0 ? 2 : 3;
+              const uint32_t m = over[0] != 0 ? over[0] : over[1] != 0 ? over[1] : over[2] != 0 ? over[2] : over[3];
+              at[j] = m != 0 ? 32 * g + __ffs(m) - 1 : -1;
+              v[j] = m != 0 ? load_bf16(from + static_cast<int64_t>(at[j] & 31) * p.in + g * kQ4Group) : 0.0f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (i == g) over[i] &= over[i] - 1;
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) all[j] = split_rest(v[j], &h[j], &l[j], &byte[j]);
+            if (first) {
+              if (PRE) {
+                ok = guard_wait(xempty0 + 8u * xt.i, xt.phase ^ 1u, ctl, p.guard, 78);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+              }
+              for (int i = lane; i < N * kKB / 16; i += 32) reinterpret_cast<uint4 *>(xs + N * kKB)[i] = make_uint4(0, 0, 0, 0);
+              __syncwarp();
+              first = false;
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              if (at[j] < 0) break;
+              const int g = at[j] >> 5, t = at[j] & 31, to = ((2 * g + (lane >> 4)) ^ (t & 7)) * 16 + (lane & 15);
+              if (all[j]) {
+                xs[(N + t) * kKB + to] = static_cast<uint8_t>(h[j]);
+                xs[(N + NT + t) * kKB + to] = static_cast<uint8_t>(l[j]);
+                if (lane == 0) {
+                  sf2[sf_at(t) + g] = static_cast<uint8_t>(byte[j] - 22u);
+                  sf2[sf_at(NT + t) + g] = static_cast<uint8_t>(byte[j] - 26u);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (i == g) rest[i] |= 1u << t;
+              }
+            }
+          }
+        };
+        bool more = false;
+        if constexpr (PRE) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) over[g] = __ballot_sync(0xffffffffu, (marks >> (8 * g) & 255u) != 0);
+          marks = mark(b + S);
+          more = (over[0] | over[1] | over[2] | over[3]) != 0;
+          if (more) {
+            more_pieces();
+            if (!ok) break;
+          }
+        }
+        ok = guard_wait(xfull0 + 8u * xt.i, xt.phase, ctl, p.guard, 75);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if constexpr (PRE) {
+          // the second pieces' scales
+          if (lane < ntok)
+            *reinterpret_cast<uint32_t *>(sf + sf_at(NT + lane)) = *reinterpret_cast<const uint32_t *>(sf + sf_at(lane)) - 0x04040404u;
+        } else {
           // a place without a token holds anything: its column of the result is not read
-          uint8_t *xs = xs0 + xt.i * F::kXBytes, *sf = xsf0 + xt.i * F::kXSf;
+          uint32_t groups = 0;
           // four at a time, whose steps hide one another's latencies
-          constexpr int kAtOnce = 4;
 #pragma unroll 1
           for (int t0 = 0; t0 < ntok; t0 += kAtOnce) {
             uint2 v[kAtOnce];
@@ -410,7 +577,10 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
               v[j] = *reinterpret_cast<const uint2 *>(xs + (t0 + j + (lane >= 16 ? NT : 0)) * 128 + (lane & 15) * 8);
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) split4(v[j], &h[j], &l[j], &sb[j]);
+            for (int j = 0; j < kAtOnce; ++j) {
+              const uint32_t left = split4(v[j], &h[j], &l[j], &sb[j]);
+              if (t0 + j < ntok) groups |= left << (t0 + j);
+            }
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
               const int t = t0 + j, to = ((lane >> 2) ^ (t & 7)) * 16 + (lane & 3) * 4;
@@ -422,10 +592,30 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
               }
             }
           }
-          fence_async_proxy();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(xready0 + 8u * xt.i);
+          more = groups != 0;
+          if (more) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) over[g] = groups >> (8 * g) & 255u;
+            more_pieces();
+          }
         }
+        if (more && (rest[0] | rest[1] | rest[2] | rest[3]) != 0) {
+          // groups that no pieces hold: zeros (add_rest)
+          __syncwarp();
+#pragma unroll 1
+          for (int g = 0; g < 4; ++g)
+#pragma unroll 1
+            for (uint32_t m = g == 0 ? rest[0] : g == 1 ? rest[1] : g == 2 ? rest[2] : rest[3]; m != 0; m &= m - 1) {
+              const int t = __ffs(m) - 1, to = ((2 * g + (lane >> 4)) ^ (t & 7)) * 16 + (lane & 15);
+              xs[t * kKB + to] = 0;
+              xs[(NT + t) * kKB + to] = 0;
+            }
+          if (lane == 0) atomicOr(left_out + b / 32 % F::kLeftWords, 1u << (b % 32));
+        }
+        if (lane == 0) wide[xt.i] = more ? 1u : 0u;
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xready0 + 8u * xt.i);
         if constexpr (!BOX) {
           ok = guard_wait(wfull0 + 8u * st.i, st.phase, ctl, p.guard, 76);
           if (!__all_sync(0xffffffffu, ok)) break;
@@ -467,6 +657,7 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
       }
     }
     // ---------------------------------------------------------------- result
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * F::kWorkers) : "memory");   // all workers' words of left_out
     if (warp < 4) {
       // into shared memory as [token][feature]: the blocks are free once the last MMA
       // is done
@@ -485,6 +676,10 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
           for (int i = 0; i < 8; ++i) part[(c + i) * kTcM + 32 * warp + lane] = ok ? a[i] + d[i] : 0.0f;
         }
       }
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < F::kLeftWords; ++i) any |= left_out[i];
+      if (any != 0 && ok) add_rest(p, wq, x, o, f0, 32 * warp + lane, kb0, nb, left_out, part);
     }
   }
   // the pieces are written, whoever reads them: no launch after this one comes
@@ -603,14 +798,14 @@ dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, i
   // an expert of n tokens has (n - 1) / NT + 1
   const int64_t tiles = p.ftiles * (p.offsets ? (p.T - groups) / NT + groups : 1);
   // the k range over as many CTAs as keep all clusters resident.  Up to 27 CTAs on 16 SMs
-  // were, as clusters of 8 too: 1 x 4096 x 14336 11.1 us, by the query's count 15.5.  With x
-  // in pieces the joins of so many take more than they give unless each has 8 blocks (64 x
-  // 4096 x 4096 10.2, 9.2; 37 x 4096 x 14336 15.1, 18.3)
+  // were, as clusters of 8 too, where the query counts fewer: that matters for 29 to 32 tiles
+  // (1 x 4096 x 4096 6.4 us, by the query alone 7.3; 4096 x 8192 8.3, 10.8; 4096 x 14336 11.4,
+  // 16.3, 32 tokens 17.5, 20.9), for other sizes both choose alike (20 and 28 tiles, 48 and 64)
   int log = 0;
   const int64_t blocks = dora::ceil_div(p.in, kKB);
   while (log < kMaxClusterLog && (2 << log) <= blocks &&
          (tiles <= resident_clusters<NT, BOX>(device, log + 1) ||
-          (tiles << (log + 1) <= sms * 27 / 16 && (!F::kSplit || 16 << log <= blocks))))
+          tiles << (log + 1) <= sms * 27 / 16))
     ++log;
   if (tiles << log > kMaxDim) return DORA_ERR_SHAPE;
   p.ntok = NT;
@@ -632,6 +827,7 @@ dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, i
   cudaLaunchAttribute attr[2];
   few_config<NT, BOX>(&cfg, attr, tiles, 1 << log, cs);
   if (cudaLaunchKernelEx(&cfg, q4_few_kernel<NT, BOX>, mW, mX, p, static_cast<const uint8_t *>(wq),
+                         static_cast<const __nv_bfloat16 *>(x),
                          reinterpret_cast<const uint32_t *>(pieces + 2 * all)) !=
       cudaSuccess) {
     cudaGetLastError();
@@ -652,15 +848,8 @@ dora_status launch(const void *x, const void *wq, const Q4Params &p, void *works
 
 namespace dora {
 
-// the tokens that a tile is made for.  Experts: twice their mean, for uneven loads, whose
-// second tile of an expert would read its weight again (squares of even numbers up to
-// three times the mean, 32 experts of 2048 x 4096, us by twice the mean and by the mean:
-// 256 tokens 36, 55; 512 38.4, 51.7; 1024 44.7, 56.2; even loads 36.9, 40.2; 38.8, 38.9;
-// 45.1, 42.0)
-static int64_t tokens(int64_t T, int64_t experts) { return (experts > 1 ? 2 : 1) * q4_per(T, experts); }
-
 size_t q4_few_workspace(int64_t T, int64_t in, int64_t experts) {
-  return tokens(T, experts) <= 8 ? 0 : static_cast<size_t>(2 * T * in + 8 * T * ceil_div(in, kKB));
+  return q4_tile(T, experts) <= 8 ? 0 : static_cast<size_t>(2 * T * in + 8 * T * ceil_div(in, kKB));
 }
 
 dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
@@ -671,8 +860,7 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   if (st != DORA_OK) return st;
   static const void *const kernels[] = {
       (const void *)q4_few_kernel<8, false>,  (const void *)q4_few_kernel<8, true>,   (const void *)q4_few_kernel<16, false>,
-      (const void *)q4_few_kernel<16, true>,  (const void *)q4_few_kernel<32, false>, (const void *)q4_few_kernel<32, true>,
-      (const void *)q4_few_kernel<64, false>, (const void *)q4_few_kernel<64, true>};
+      (const void *)q4_few_kernel<16, true>,  (const void *)q4_few_kernel<32, false>, (const void *)q4_few_kernel<32, true>};
   Q4Params p = {};
   st = tc_init(device, &p.guard, kernels, sizeof(kernels) / sizeof(kernels[0]));
   if (st != DORA_OK) return st;
@@ -686,11 +874,10 @@ dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq,
   p.scale = static_cast<const uint8_t *>(wscale);
   p.y = static_cast<__nv_bfloat16 *>(y);
   p.ftiles = static_cast<int>(ceil_div(out, kTcM));
-  const int64_t n = tokens(T, experts);
+  const int64_t n = q4_tile(T, experts);
   if (n <= 8) return launch<8>(x, wq, p, workspace, device, info.sms, cs);
   if (n <= 16) return launch<16>(x, wq, p, workspace, device, info.sms, cs);
-  if (n <= 32) return launch<32>(x, wq, p, workspace, device, info.sms, cs);
-  return launch<64>(x, wq, p, workspace, device, info.sms, cs);
+  return launch<32>(x, wq, p, workspace, device, info.sms, cs);
 }
 
 }  // namespace dora

@@ -702,15 +702,13 @@ dora_status check(const void *x, const int32_t *offsets, const void *wq, const v
 
 }  // namespace
 
-// few tokens a weight: q4_few.cu, where W is read as it is
-static bool few(int64_t T, int64_t experts) { return dora::q4_per(T, experts) <= dora::kQ4Few; }
 static bool bad_call(int64_t T, int64_t out, int64_t in, int64_t experts) {
   return bad_size(T, 1) || bad_size(out, 1) || bad_size(in, 1) || experts < 1 || experts > kMaxExperts;
 }
 
 extern "C" size_t dora_matmul_q4_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {
   if (bad_call(T, out, in, experts)) return 0;
-  if (few(T, experts)) return dora::q4_few_workspace(T, in, experts);
+  if (dora::q4_few(T, in, experts)) return dora::q4_few_workspace(T, in, experts);
   return parts_bytes(plan(false, T, out, in, experts), T, out);
 }
 extern "C" size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t experts) {
@@ -727,7 +725,7 @@ extern "C" dora_status dora_matmul_q4(const void *x, const int32_t *offsets, con
   const dora_status st = check(x, offsets, wq, wscale, T, out, in, experts, y);
   if (st != DORA_OK || T == 0 || out == 0) return st;
   if (short_of(dora_matmul_q4_workspace(T, out, in, experts), workspace, workspace_bytes)) return DORA_ERR_WORKSPACE;
-  if (few(T, experts))
+  if (dora::q4_few(T, in, experts))                 // few tokens a weight, W read as it is
     return dora::matmul_q4_few(x, offsets, wq, wscale, T, out, in, experts, y, workspace,
                                reinterpret_cast<cudaStream_t>(stream));
   return run_matmul<false>(x, offsets, wq, wscale, T, out, in, experts, y, workspace, stream);

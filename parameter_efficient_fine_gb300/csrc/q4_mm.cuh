@@ -116,11 +116,20 @@ inline bool map_w(CUtensorMap *map, const void *base, int64_t experts, int64_t o
 
 namespace dora {
 
-// x W^T of few tokens (q4_few.cu): up to so many a weight (us, that kernel / pairs: 64 x 8192 x 8192
-// 15.9 / 19.6; at 32 experts of 2048 x 4096, 32 tokens each 41.7 / 59.4, 64 52.5 / 60.5.  With 128 in
-// a tile it took 23.5 for 128 x 8192 x 8192 and 50.7 for 2048 tokens at 16 experts, pairs 21.5 and 35)
-constexpr int64_t kQ4Few = 64;
-inline int64_t q4_per(int64_t T, int64_t experts) { return experts < T ? ceil_div(T, experts) : 1; }
+// The tokens that a tile of q4_few.cu is made for.  Experts: twice their mean, for uneven loads,
+// whose second tile of an expert would read its weight again (32 experts of 2048 x 4096, us
+// by twice the mean and by the mean; uneven: squares of even numbers, up to three times the mean: 256
+// tokens 40, 62; 512 47, 59; even loads 40, 48; 47, 45; one expert with half of the tokens 49, 62; 59, 58)
+inline int64_t q4_tile(int64_t T, int64_t experts) {
+  const int64_t per = experts < T ? ceil_div(T, experts) : 1;
+  return (experts > 1 ? 2 : 1) * per;
+}
+// x W^T by q4_few.cu: where a tile is made for so many at most; where rows of W are no whole blocks of
+// 128, for half (us, that kernel / pairs: 32 x 8192 x 8192 17 / 19, 32 x 14336 x 4096 16.4 / 18.1, 32 x 4096 x
+// 4096 10.8 / 9.6, 512 tokens at 32 experts of 2048 x 4096 47 / 59, 768 at 32, tiles of 32, 65 / 59; with 64 in a
+// tile, whose third and fourth pieces leave room for one CTA an SM, 37 x 14336 x 4096 21.9 / 18.2, 64 x 8192 x 8192 25 / 19.5.
+// 8224 columns: 16 tokens 18.7 / 20.1, 20 22.6 / 20.2; 16 x 1024 x 4128 9.1 / 8.1)
+inline bool q4_few(int64_t T, int64_t in, int64_t experts) { return q4_tile(T, experts) <= (in % 128 == 0 ? 32 : 16); }
 size_t q4_few_workspace(int64_t T, int64_t in, int64_t experts);
 dora_status matmul_q4_few(const void *x, const int32_t *offsets, const void *wq, const void *wscale, int64_t T,
                           int64_t out, int64_t in, int64_t experts, void *y, void *workspace, cudaStream_t cs);

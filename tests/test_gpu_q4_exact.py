@@ -1,0 +1,159 @@
+"""x enters the products with a 4-bit weight as it is, however many tokens there are.
+
+A row of W with one value that is not zero picks a column of x: every other product is
+zero, so y is that column's value times W's, rounded once to bf16 (half a step, so the
+same bits as the 64-bit product rounded), whatever else the row of x holds.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q4_oracle as q4
+from parameter_efficient_fine_gb300 import workloads as wl
+
+from gpu_util import DEV, act_to_dev, act_to_f64, assert_no_device_error, check_bound, to_f64
+from test_gpu_q4 import BF16, run, u8_dev, weight
+
+pytestmark = pytest.mark.gpu
+
+TOKENS = [1, 3, 8, 9, 16, 17, 32, 40, 64, 65, 200]       # every kernel and tile, and both sides of their limits
+WIDTHS = [384, 416, 2080]                                # rows of whole blocks of 128, and not
+
+
+def bits(v):
+    """float64 values rounded to bf16, as bits."""
+    return wl.f32_to_bf16_bits(v.astype(np.float32))
+
+
+def picks(rng, out, inp, byte=127):
+    """A weight whose row f has one value that is not zero, and (column, value) of each."""
+    col, code = rng.integers(0, inp, out), rng.integers(1, 8, out) + 8 * rng.integers(0, 2, out)
+    c = np.zeros((out, inp), np.uint8)
+    c[np.arange(out), col] = code
+    wq, ws = c[:, 0::2] | c[:, 1::2] << 4, np.full((out, inp // 32), byte, np.uint8)
+    return wq, ws, col, q4.e2m1_table()[code] * 2.0 ** (byte - 127)
+
+
+def same_values(got, want):
+    """Equal, but that a result below the smallest normal number may be flushed."""
+    tiny = np.abs(want) < 2.0 ** -126
+    assert np.array_equal(got[~tiny], want[~tiny])
+    assert np.all(np.abs(got[tiny]) <= 2.0 ** -126)
+
+
+def rounded(v):
+    """float64 values as the bf16 that they round to, widened again."""
+    return act_to_f64(bits(v))
+
+
+@pytest.mark.parametrize("inp", WIDTHS)
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("least", [-8, -14, -17, -24, -40, -100])
+def test_a_column_comes_out_as_it_is(T, inp, least):
+    """Values of any mantissa from 2^least to 1, neighbours of very different size."""
+    rng = np.random.default_rng(T * 7 + inp - least)
+    wq, ws, col, w = picks(rng, 528, inp)
+    x = act_to_f64(bits(rng.choice([-1.0, 1.0], (T, inp)) * 2.0 ** rng.uniform(least, 0, (T, inp))))
+    y = to_f64(run(act_to_dev(bits(x)), u8_dev(wq), u8_dev(ws), False))
+    same_values(y, rounded(x[:, col] * w))
+    assert_no_device_error()
+
+
+@pytest.mark.parametrize("inp", WIDTHS)
+@pytest.mark.parametrize("T", TOKENS)
+def test_every_finite_value_among_any_others(T, inp):
+    rng = np.random.default_rng(T + inp)
+    wq, ws, col, w = picks(rng, 528, inp)
+    pattern = rng.integers(0, 1 << 16, (T, inp)).astype(np.uint16)
+    pattern[(pattern & 0x7f80) == 0x7f80] = 0
+    x = act_to_f64(pattern)
+    y = to_f64(run(act_to_dev(pattern), u8_dev(wq), u8_dev(ws), False))
+    with np.errstate(over="ignore"):
+        same_values(y, rounded(x[:, col] * w))
+    assert_no_device_error()
+
+
+@pytest.mark.parametrize("inp", [384, 416])
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("top", [-126, -118, -110, -105])
+def test_small_groups_beside_a_large_scale(T, inp, top):
+    """Groups whose largest magnitude is near the smallest number, times a W that brings the
+    result back: nothing of x is lost below."""
+    rng = np.random.default_rng(T + top + inp)
+    wq, ws, col, w = picks(rng, 272, inp, byte=227)
+    # whole numbers of 2^-133, the smallest bf16
+    k = rng.integers(-(1 << 7), 1 << 7, (T, inp)) * 2.0 ** rng.integers(0, top + 127, (T, inp))
+    x = k * 2.0 ** -133
+    x = act_to_f64(bits(x))
+    y = to_f64(run(act_to_dev(bits(x)), u8_dev(wq), u8_dev(ws), False))
+    same_values(y, rounded(x[:, col] * w))
+
+
+@pytest.mark.parametrize("loud", [1e3, 1e5, 1e6, 1e12, 1e30])
+@pytest.mark.parametrize("T,inp", [(1, 2048), (5, 2080), (8, 2048), (12, 2048), (30, 2080), (64, 2048), (64, 2080), (100, 2048)])
+def test_loud_columns_beside_zeros_of_the_weight(T, inp, loud):
+    """Sums: columns that are far louder meet zeros of W, so the result is the others' alone."""
+    rng = np.random.default_rng(T + inp)
+    wq, ws = weight(rng, 272, inp)
+    x = rng.standard_normal((T, inp))
+    cols = np.arange(0, inp, 96) + 6
+    x[:, cols] *= loud
+    wq[:, cols // 2] &= 0xf0                           # even columns lie in the low half
+    h = bits(x)
+    v = act_to_f64(h)
+    y = to_f64(run(act_to_dev(h), u8_dev(wq), u8_dev(ws), False))
+    ref = q4.matmul_q4(v, wq, ws)
+    sums = 2.0 ** -23 * (inp + 64) * q4.matmul_q4(np.abs(v), wq & 0x77, ws)
+    check_bound("y", y, ref, (1 + 2.0 ** -8) * sums + 2.0 ** -8 * np.abs(ref))
+
+
+@pytest.mark.parametrize("t", [False, True], ids=["xWt", "dyW"])
+@pytest.mark.parametrize("inp", [384, 416])
+@pytest.mark.parametrize("T", TOKENS)
+def test_infinities_are_added_as_the_formula_says(T, inp, t):
+    """inf times a value is inf of that sign, times zero NaN; two of different signs NaN."""
+    rng = np.random.default_rng(T + inp)
+    wq, ws = weight(rng, 272, inp)
+    x = rng.standard_normal((T, 272 if t else inp))
+    x[0, 5] = np.inf
+    if T > 2:
+        x[1, [7, 70]] = np.inf, -np.inf
+        x[T - 1, 33] = -np.inf
+    h = bits(x)
+    y = to_f64(run(act_to_dev(h), u8_dev(wq), u8_dev(ws), t))
+    v, W = act_to_f64(h), q4.q4_decode(wq, ws)
+    with np.errstate(invalid="ignore"):
+        ref = sum(v[:, k, None] * (W if t else W.T)[k][None] for k in range(v.shape[1]))
+    bad = ~np.isfinite(ref)
+    assert np.array_equal(y[bad], ref[bad], equal_nan=True)
+    assert np.isfinite(y[~bad]).all() and (~bad).any() == (T > 3)
+    assert_no_device_error()
+
+
+@pytest.mark.parametrize("inp", [384, 416])
+@pytest.mark.parametrize("T", TOKENS)
+def test_a_nan_reaches_its_own_row_and_no_other(T, inp):
+    rng = np.random.default_rng(T + inp)
+    wq, ws = weight(rng, 272, inp)
+    x = rng.standard_normal((T, inp))
+    x[T // 2, 40] = np.nan
+    y = to_f64(run(act_to_dev(bits(x)), u8_dev(wq), u8_dev(ws), False))
+    rest = np.arange(T) != T // 2
+    assert np.isnan(y[T // 2]).all() and np.isfinite(y[rest]).all()
+
+
+EXPERTS = [[0, 3, 3, 8, 9], [0, 5, 30, 31, 60], [0, 64, 100, 100, 180], [0, 0, 70, 71, 200], [0, 200, 300, 400, 700]]
+
+
+@pytest.mark.parametrize("inp", [384, 416])
+@pytest.mark.parametrize("offsets", EXPERTS, ids=[str(i) for i in range(len(EXPERTS))])
+def test_columns_of_experts_come_out_as_they_are(offsets, inp):
+    rng = np.random.default_rng(offsets[-1] + inp)
+    E, T, out = len(offsets) - 1, offsets[-1], 272
+    wq, ws, col, w = picks(rng, E * out, inp)
+    x = act_to_f64(bits(rng.choice([-1.0, 1.0], (T, inp)) * 2.0 ** rng.uniform(-40, 0, (T, inp))))
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    y = to_f64(run(act_to_dev(bits(x)), u8_dev(wq.reshape(E, out, -1)), u8_dev(ws.reshape(E, out, -1)), False, off))
+    for e in range(E):
+        rows, f = slice(offsets[e], offsets[e + 1]), slice(e * out, (e + 1) * out)
+        same_values(y[rows], rounded(x[rows][:, col[f]] * w[f]))
