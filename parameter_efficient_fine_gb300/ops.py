@@ -583,7 +583,8 @@ def _matmul_q4_backward(ctx, dy):
 matmul_q4.register_autograd(_matmul_q4_backward, setup_context=_matmul_q4_setup)
 
 
-def _linear_q4_check(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, g: Tensor) -> None:
+def _linear_q4_check(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Tensor,
+                     g: Tensor, norm: Tensor) -> None:
     """What the layer's forward takes; the same eagerly and while it is traced."""
     if x.dtype != torch.bfloat16:
         raise TypeError(f"dora::linear_q4: x is bfloat16, got {x.dtype}")
@@ -596,18 +597,19 @@ def _linear_q4_check(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor
     if out % 16 or inp % 32:
         raise ValueError(f"dora::linear_q4: in is a multiple of 32 and out of 16, got {inp} and {out}")
     for name, t, want in (("x", x, (x.shape[0], inp)), ("wscale", wscale, (out, inp // 32)), ("A", A, (r, inp)),
-                          ("B", B, (out, r)), ("g", g, (out,))):
+                          ("B", B, (out, r)), ("m", m, (out,)), ("g", g, (out,)), ("norm", norm, (out,))):
         if t.shape != want:
             raise ValueError(f"dora::linear_q4: {name} is {want} for a weight [{out}, {inp}] and rank {r}, got {tuple(t.shape)}")
-    if g.dtype != torch.float32:
-        raise ValueError(f"dora::linear_q4: g is float32, got {g.dtype}")
+    for name, t in (("g", g), ("norm", norm)):
+        if t.dtype != torch.float32:
+            raise ValueError(f"dora::linear_q4: {name} is float32, got {t.dtype}")
 
 
 @torch.library.custom_op("dora::linear_q4", mutates_args=(), device_types="cuda")
 def linear_q4(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Tensor, g: Tensor, norm: Tensor,
               s: float) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
     """The layer's output y and what its backward needs: (y, xq, xscale, vq, vscale, xa)."""
-    _linear_q4_check(x, wq, wscale, A, B, g)
+    _linear_q4_check(x, wq, wscale, A, B, m, g, norm)
     xq, xscale = q8_store(x, 1)
     xa = x @ A.to(x.dtype).t()
     y, vq, vscale = compose_q8(matmul_q4(x, wq, wscale), xa @ B.to(x.dtype).t(), m, g, norm, s)
@@ -616,7 +618,7 @@ def linear_q4(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, m: Te
 
 @linear_q4.register_fake
 def _linear_q4_fake(x, wq, wscale, A, B, m, g, norm, s):
-    _linear_q4_check(x, wq, wscale, A, B, g)
+    _linear_q4_check(x, wq, wscale, A, B, m, g, norm)
     T, inp = x.shape
     out = wq.shape[0]
     u8 = torch.uint8
@@ -625,16 +627,12 @@ def _linear_q4_fake(x, wq, wscale, A, B, m, g, norm, s):
 
 
 def _linear_q4_setup(ctx, inputs, output):
-    _, wq, wscale, A, B, m, g, norm, s = inputs
+    _, wq, wscale, A, B, _, g, norm, s = inputs
     _, xq, xscale, vq, vscale, xa = output
     # what the backward alone needs is refused by the call that leads to it
-    r, (out,) = A.shape[0], g.shape
+    r = A.shape[0]
     if ctx.needs_input_grad[3] and (r % 8 or not 1 <= r <= 1024):
         raise ValueError(f"dora::linear_q4: a gradient of A takes a rank of 8, 16, ... 1024, got {r}")
-    if ctx.needs_input_grad[5] and m.shape != (out,):
-        raise ValueError(f"dora::linear_q4: m is ({out},), got {tuple(m.shape)}")
-    if norm.shape != (out,) or norm.dtype != torch.float32:
-        raise ValueError(f"dora::linear_q4: norm is ({out},) of float32, got {tuple(norm.shape)} of {norm.dtype}")
     ctx.save_for_backward(xq, xscale, vq, vscale, xa, wq, wscale, A, B, g, norm)
     ctx.s = s
     ctx.mark_non_differentiable(xq, xscale, vq, vscale, xa)
@@ -671,7 +669,7 @@ def dora_linear_q4(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, 
     up to 1024.  Where nothing takes a gradient, nothing is kept for one: serving a token
     is the products and a compose."""
     if not (torch.is_grad_enabled() and any(t.requires_grad for t in (x, A, B, m))):
-        _linear_q4_check(x, wq, wscale, A, B, g)
+        _linear_q4_check(x, wq, wscale, A, B, m, g, norm)
         lora = (x @ A.to(x.dtype).t()) @ B.to(x.dtype).t()
         return compose(matmul_q4(x, wq, wscale), lora, m, g, norm, s)
     return linear_q4(x, wq, wscale, A, B, m, g, norm, s)[0]
