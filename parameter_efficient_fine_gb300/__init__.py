@@ -509,23 +509,32 @@ def dora_matmul_q4_t_workspace(T: int, out: int, inp: int, experts: int = 1) -> 
     return int(load_library().dora_matmul_q4_t_workspace(T, out, inp, experts))
 
 
-def _matmul_q4(name: str, x, wq, wscale, y, offsets, workspace, stream, out_side: bool) -> None:
+def _matmul_q4_sizes(name: str, x, wq, wscale, offsets, out_side: bool) -> tuple[int, int, int, int, int]:
+    """T, out, in, the result's columns and the number of experts of a product's operands."""
     bf16, _, i32 = _TYPES or _types()
     xs, ws = x.shape, wq.shape
     if len(ws) != (2 if offsets is None else 3):
         raise ValueError(f"{name}: a weight [out, in / 2], or with offsets a stack [experts, out, in / 2], got {tuple(ws)}")
+    if len(xs) != 2:
+        raise ValueError(f"{name}: rows [T, {'in' if out_side else 'out'}], got {tuple(xs)}")
     T, out, inp = xs[0], ws[-2], 2 * ws[-1]
     k, n = (inp, out) if out_side else (out, inp)
     if inp % 32 or wscale.shape != (*ws[:-1], inp // 32) or wq.element_size() != 1 or wscale.element_size() != 1:
         _q4(name, (*ws[:-1], inp), wq, wscale)
-    if xs != (T, k) or x.dtype != bf16 or y.shape != (T, n) or y.dtype != bf16:
+    if xs[1] != k or x.dtype != bf16:
         _same(name, (T, k), bf16, x)
-        _same(name, (T, n), bf16, y)
-    experts, nbytes = 1, 0
+    if offsets is None:
+        return T, out, inp, n, 1
+    _same(name, (ws[0] + 1,), i32, offsets)
+    return T, out, inp, n, ws[0]
+
+
+def _matmul_q4(name: str, x, wq, wscale, y, offsets, workspace, stream, out_side: bool) -> None:
+    T, out, inp, n, experts = _matmul_q4_sizes(name, x, wq, wscale, offsets, out_side)
+    _same(name, (T, n), _TYPES[0], y)
+    nbytes = 0
     ts = [x, wq, wscale, y]
     if offsets is not None:
-        experts = ws[0]
-        _same(name, (experts + 1,), i32, offsets)
         ts.append(offsets)
     if workspace is not None:
         nbytes = workspace.numel() * workspace.element_size()
@@ -548,9 +557,7 @@ def dora_matmul_q4_t(dy, wq, wscale, dx, offsets=None, workspace=None, stream=No
     _matmul_q4("dora_matmul_q4_t", dy, wq, wscale, dx, offsets, workspace, stream, False)
 
 
-def dora_expert_sort(expert, experts: int, order, inverse, offsets, stream=None) -> None:
-    """The entries of expert [T, k] sorted by expert, stably: order, its inverse and
-    where each expert's begin (see include/dora.h)."""
+def _expert_sort_sizes(expert, experts: int) -> tuple[int, int]:
     i32 = (_TYPES or _types())[2]
     if expert.dtype != i32:
         import torch
@@ -558,7 +565,16 @@ def dora_expert_sort(expert, experts: int, order, inverse, offsets, stream=None)
             raise TypeError(f"dora_expert_sort: expert is int32 or int64, got {expert.dtype}")
     if not 1 <= experts <= 4096:
         raise ValueError(f"dora_expert_sort: 1 to 4096 experts, got {experts}")
-    T, k = expert.shape
+    if len(expert.shape) != 2:
+        raise ValueError(f"dora_expert_sort: expert is [T, k], got {tuple(expert.shape)}")
+    return expert.shape
+
+
+def dora_expert_sort(expert, experts: int, order, inverse, offsets, stream=None) -> None:
+    """The entries of expert [T, k] sorted by expert, stably: order, its inverse and
+    where each expert's begin (see include/dora.h)."""
+    T, k = _expert_sort_sizes(expert, experts)
+    i32 = _TYPES[2]
     _same("dora_expert_sort", (T * k,), i32, order)
     _same("dora_expert_sort", (T, k), i32, inverse)
     _same("dora_expert_sort", (experts + 1,), i32, offsets)
@@ -569,6 +585,8 @@ def dora_expert_sort(expert, experts: int, order, inverse, offsets, stream=None)
 def _routed(name: str, x, xs, inverse, offsets) -> tuple[int, int, int, int]:
     """T, k, cols and the number of experts of tokens x [T, cols] and their rows xs [T k, cols]."""
     i32 = (_TYPES or _types())[2]
+    if len(inverse.shape) != 2 or len(x.shape) != 2:
+        raise ValueError(f"{name}: tokens [T, cols] and inverse [T, k], got {tuple(x.shape)} and {tuple(inverse.shape)}")
     T, k = inverse.shape
     cols, so = x.shape[1], offsets.shape
     experts = so[0] - 1

@@ -69,7 +69,7 @@ from typing import Optional
 import torch
 from torch import Tensor
 
-from . import (dora_compose_bwd, dora_compose_bwd_q8, dora_compose_bwd_q8_workspace, dora_compose_bwd_workspace,
+from . import (_act, _expert_sort_sizes, _matmul_q4_sizes, _q4, _routed, _same, dora_compose_bwd, dora_compose_bwd_q8, dora_compose_bwd_q8_workspace, dora_compose_bwd_workspace,
                dora_compose_fwd, dora_compose_fwd_q8, dora_expert_clear, dora_expert_return, dora_expert_return_bwd, dora_expert_send,
                dora_expert_sort, dora_lora_grad_q8, dora_lora_grad_q8_workspace, dora_matmul_q4, dora_matmul_q4_t,
                dora_matmul_q4_t_workspace, dora_matmul_q4_workspace, dora_matmul_q8, dora_matmul_q8_t,
@@ -516,6 +516,7 @@ def q4_store(x: Tensor) -> tuple[Tensor, Tensor]:
 
 @q4_store.register_fake
 def _q4_store_fake(x):
+    _act(x)
     q, scale = _q4_shapes(x)
     return x.new_empty(q, dtype=torch.uint8), x.new_empty(scale, dtype=torch.uint8)
 
@@ -531,7 +532,10 @@ def q4_load(q: Tensor, scale: Tensor, dtype: torch.dtype) -> Tensor:
 
 @q4_load.register_fake
 def _q4_load_fake(q, scale, dtype):
-    return q.new_empty((*q.shape[:-1], 2 * q.shape[-1]), dtype=dtype)
+    x = q.new_empty((*q.shape[:-1], 2 * q.shape[-1]), dtype=dtype)
+    _q4("dora_q4_load", x.shape, q, scale)
+    _act(x)
+    return x
 
 
 @torch.library.custom_op("dora::matmul_q4", mutates_args=(), device_types="cuda")
@@ -539,27 +543,37 @@ def matmul_q4(x: Tensor, wq: Tensor, wscale: Tensor, offsets: Optional[Tensor] =
     """x W^T for a bfloat16 x and W in 4 bits; with offsets (expert_sort) W is a stack and
     x's rows are sorted by expert."""
     _contig("matmul_q4", x, wq, wscale)
-    out, inp = wq.shape[-2], 2 * wq.shape[-1]
-    y = torch.empty(x.shape[0], out, dtype=torch.bfloat16, device=x.device)
-    n = dora_matmul_q4_workspace(x.shape[0], out, inp, 1 if offsets is None else wq.shape[0])
+    T, out, inp, cols, experts = _matmul_q4_sizes("dora_matmul_q4", x, wq, wscale, offsets, True)
+    y = torch.empty(T, cols, dtype=torch.bfloat16, device=x.device)
+    n = dora_matmul_q4_workspace(T, out, inp, experts)
     dora_matmul_q4(x, wq, wscale, y, offsets, _workspace(n, x) if n else None)
     if offsets is not None:
         dora_expert_clear(y, offsets)
     return y
 
 
+def _matmul_q4_traced(name, x, wq, wscale, offsets, out_side):
+    T, out, _, cols, experts = _matmul_q4_sizes(name, x, wq, wscale, offsets, out_side)
+    # what the library itself refuses
+    if T and out % 16:
+        raise ValueError(f"{name}: out is a multiple of 16, got {out}")
+    if not 1 <= experts <= 4096:
+        raise ValueError(f"{name}: 1 to 4096 experts, got {experts}")
+    return x.new_empty(T, cols, dtype=torch.bfloat16)
+
+
 @matmul_q4.register_fake
 def _matmul_q4_fake(x, wq, wscale, offsets=None):
-    return x.new_empty(x.shape[0], wq.shape[-2], dtype=torch.bfloat16)
+    return _matmul_q4_traced("dora_matmul_q4", x, wq, wscale, offsets, True)
 
 
 @torch.library.custom_op("dora::matmul_q4_t", mutates_args=(), device_types="cuda")
 def matmul_q4_t(dy: Tensor, wq: Tensor, wscale: Tensor, offsets: Optional[Tensor] = None) -> Tensor:
     """dy W for a bfloat16 dy and the same W."""
     _contig("matmul_q4_t", dy, wq, wscale)
-    out, inp = wq.shape[-2], 2 * wq.shape[-1]
-    dx = torch.empty(dy.shape[0], inp, dtype=torch.bfloat16, device=dy.device)
-    n = dora_matmul_q4_t_workspace(dy.shape[0], out, inp, 1 if offsets is None else wq.shape[0])
+    T, out, inp, cols, experts = _matmul_q4_sizes("dora_matmul_q4_t", dy, wq, wscale, offsets, False)
+    dx = torch.empty(T, cols, dtype=torch.bfloat16, device=dy.device)
+    n = dora_matmul_q4_t_workspace(T, out, inp, experts)
     dora_matmul_q4_t(dy, wq, wscale, dx, offsets, _workspace(n, dy) if n else None)
     if offsets is not None:
         dora_expert_clear(dx, offsets)
@@ -568,7 +582,7 @@ def matmul_q4_t(dy: Tensor, wq: Tensor, wscale: Tensor, offsets: Optional[Tensor
 
 @matmul_q4_t.register_fake
 def _matmul_q4_t_fake(dy, wq, wscale, offsets=None):
-    return dy.new_empty(dy.shape[0], 2 * wq.shape[-1], dtype=torch.bfloat16)
+    return _matmul_q4_traced("dora_matmul_q4_t", dy, wq, wscale, offsets, False)
 
 
 def _matmul_q4_setup(ctx, inputs, output):
@@ -684,7 +698,7 @@ def expert_sort(expert: Tensor, experts: int) -> tuple[Tensor, Tensor, Tensor]:
     [T k], inverse [T, k], offsets [experts + 1]), int32.  An entry outside
     [0, experts) goes to no expert, behind all that do."""
     _contig("expert_sort", expert)
-    T, k = expert.shape
+    T, k = _expert_sort_sizes(expert, experts)
     i32 = dict(dtype=torch.int32, device=expert.device)
     order, inverse, offsets = torch.empty(T * k, **i32), torch.empty(T, k, **i32), torch.empty(experts + 1, **i32)
     dora_expert_sort(expert, experts, order, inverse, offsets)
@@ -693,7 +707,7 @@ def expert_sort(expert: Tensor, experts: int) -> tuple[Tensor, Tensor, Tensor]:
 
 @expert_sort.register_fake
 def _expert_sort_fake(expert, experts):
-    T, k = expert.shape
+    T, k = _expert_sort_sizes(expert, experts)
     i32 = torch.int32
     return expert.new_empty(T * k, dtype=i32), expert.new_empty(T, k, dtype=i32), expert.new_empty(experts + 1, dtype=i32)
 
@@ -710,7 +724,12 @@ def expert_return(ys: Tensor, inverse: Tensor, offsets: Tensor, weight: Optional
 
 @expert_return.register_fake
 def _expert_return_fake(ys, inverse, offsets, weight=None):
-    return ys.new_empty(inverse.shape[0], ys.shape[1])
+    y = ys.new_empty(inverse.shape[0], *ys.shape[1:])
+    T, k, _, _ = _routed("dora_expert_return", y, ys, inverse, offsets)
+    if weight is not None:
+        _same("dora_expert_return", (T, k), torch.float32, weight)
+    _act(ys)
+    return y
 
 
 @torch.library.custom_op("dora::expert_send", mutates_args=(), device_types="cuda")
@@ -725,7 +744,10 @@ def expert_send(x: Tensor, inverse: Tensor, offsets: Tensor) -> Tensor:
 
 @expert_send.register_fake
 def _expert_send_fake(x, inverse, offsets):
-    return x.new_empty(inverse.numel(), x.shape[1])
+    xs = x.new_empty(inverse.numel(), *x.shape[1:])
+    _routed("dora_expert_send", x, xs, inverse, offsets)
+    _act(x)
+    return xs
 
 
 def _expert_send_setup(ctx, inputs, output):
@@ -751,6 +773,9 @@ def expert_return_bwd(dy: Tensor, ys: Tensor, inverse: Tensor, offsets: Tensor, 
 
 @expert_return_bwd.register_fake
 def _expert_return_bwd_fake(dy, ys, inverse, offsets, weight):
+    T, k, _, _ = _routed("dora_expert_return_bwd", dy, ys, inverse, offsets)
+    _same("dora_expert_return_bwd", (T, k), torch.float32, weight)
+    _act(dy)
     return torch.empty_like(ys), torch.empty_like(weight)
 
 
