@@ -813,7 +813,7 @@ dora_status launch(const void *x, const void *wq, Q4Params p, void *workspace, i
   CUtensorMap mW, mX;
   const int64_t all = static_cast<int64_t>(p.T) * p.in;
   uint8_t *pieces = static_cast<uint8_t *>(workspace);
-  if (!(BOX ? map_w4(&mW, wq, p.experts, p.out, p.in) : map_w(&mW, wq, p.experts, p.out, p.in, 64))) return DORA_ERR_CUDA;
+  if (!(BOX ? map_w4(&mW, wq, p.experts, p.out, p.in) : map_w(&mW, wq, p.experts, p.out, p.in))) return DORA_ERR_CUDA;
   if (F::kSplit) {
     if (!map_q8(&mX, pieces, 2 * static_cast<int64_t>(p.T), p.in, NT, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)) return DORA_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>(dora::ceil_div(p.in, 4 * kSplitThreads)), p.T < 65535 ? p.T : 65535);

@@ -655,7 +655,7 @@ dora_status run_matmul(const void *x, const int32_t *offsets, const void *wq, co
   p.tiles = static_cast<int>(tiles);
   const int64_t units = tiles * p.parts;
   CUtensorMap mW, mX;
-  if (!map_w(&mW, wq, experts, out, in, 64) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.xrows, 128)) return DORA_ERR_CUDA;
+  if (!map_w(&mW, wq, experts, out, in) || !make_map(&mX, x, true, T, p.kdim, p.kdim, p.xrows, 128)) return DORA_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

@@ -98,17 +98,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 // this thread's writes to shared memory before the tensor core's reads
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// the stack of weights [experts, out, in / 2 bytes] in boxes of 128 rows x `bytes` (64 or 128), that swizzle
-inline bool map_w(CUtensorMap *map, const void *base, int64_t experts, int64_t out, int64_t in,
-                  unsigned bytes) {
+// the stack of weights [experts, out, in / 2 bytes] in boxes of 128 rows x 64 bytes, 64-byte swizzle
+inline bool map_w(CUtensorMap *map, const void *base, int64_t experts, int64_t out, int64_t in) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(out), static_cast<cuuint64_t>(experts)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(in / 2), static_cast<cuuint64_t>(in / 2) * static_cast<cuuint64_t>(out)};
-  cuuint32_t box[3] = {bytes, 128, 1};
+  cuuint32_t box[3] = {64, 128, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
