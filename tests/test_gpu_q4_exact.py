@@ -157,3 +157,38 @@ def test_columns_of_experts_come_out_as_they_are(offsets, inp):
     for e in range(E):
         rows, f = slice(offsets[e], offsets[e + 1]), slice(e * out, (e + 1) * out)
         same_values(y[rows], rounded(x[rows][:, col[f]] * w[f]))
+
+
+@pytest.mark.parametrize("T,experts", [(1, 0), (8, 0), (9, 0), (16, 0), (20, 0), (32, 0), (33, 0), (200, 0), (6, 3), (20, 3), (40, 3), (200, 3)])
+def test_a_weight_that_starts_16_bytes_into_its_memory(T, experts):
+    """16-byte alignment is what the products ask for; rows of whole blocks of 128 take
+    another way into shared memory where W is on 32 bytes."""
+    rng = np.random.default_rng(T + experts)
+    E, out, inp = max(experts, 1), 272, 512
+    wq, ws, col, w = picks(rng, E * out, inp)
+    x = act_to_f64(bits(rng.choice([-1.0, 1.0], (T, inp)) * 2.0 ** rng.uniform(-20, 0, (T, inp))))
+    shape = (E, out) if experts else (out,)
+    offsets = np.linspace(0, T, E + 1).astype(int)
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV) if experts else None
+    d = act_to_dev(bits(x))
+    plain = u8_dev(wq).reshape(*shape, -1)
+    raw = torch.zeros(wq.size + 32, dtype=torch.uint8, device=DEV)
+    moved = raw[16:16 + wq.size].view(plain.shape)
+    moved.copy_(plain)
+    assert moved.data_ptr() % 32 == 16
+    scales = u8_dev(ws).reshape(*shape, -1)
+    y = to_f64(run(d, moved, scales, False, off))
+    for e in range(E):
+        rows, f = slice(offsets[e], offsets[e + 1]), slice(e * out, (e + 1) * out)
+        same_values(y[rows], rounded(x[rows][:, col[f]] * w[f]))
+    # sums: the same within what sums of either order leave
+    wq, ws = weight(rng, out, inp, experts or None)
+    h = bits(rng.standard_normal((T, inp)))
+    moved.copy_(u8_dev(wq))
+    y = to_f64(run(act_to_dev(h), moved, u8_dev(ws), False, off))
+    v = act_to_f64(h)
+    offs = offsets.tolist() if experts else None
+    ref = q4.matmul_q4(v, wq, ws, offs)
+    sums = 2.0 ** -23 * (inp + 64) * q4.matmul_q4(np.abs(v), wq & 0x77, ws, offs)
+    check_bound("y", y, ref, (1 + 2.0 ** -8) * sums + 2.0 ** -8 * np.abs(ref))
+    assert_no_device_error()
