@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import q4_oracle as q4
-from parameter_efficient_fine_gb300 import workloads as wl
+from parameter_efficient_fine_gb300 import ops, workloads as wl
 
 from gpu_util import DEV, act_to_dev, act_to_f64, assert_no_device_error, check_bound, to_f64
 from test_gpu_q4 import BF16, run, u8_dev, weight
@@ -192,3 +192,80 @@ def test_a_weight_that_starts_16_bytes_into_its_memory(T, experts):
     sums = 2.0 ** -23 * (inp + 64) * q4.matmul_q4(np.abs(v), wq & 0x77, ws, offs)
     check_bound("y", y, ref, (1 + 2.0 ** -8) * sums + 2.0 ** -8 * np.abs(ref))
     assert_no_device_error()
+
+
+@pytest.mark.parametrize("T", [2, 8, 20])
+def test_long_rows(T):
+    """More blocks of k a CTA than it has bits for: 262, groups that no pieces hold among them."""
+    rng = np.random.default_rng(T)
+    inp = 128 * 2100
+    x = rng.standard_normal((T, inp))
+    odd = rng.choice(inp // 32, 60, replace=False)
+    odd[:4] = 0, 1024, 2100 * 4 - 1, 1028             # the first and the last; blocks that share a bit
+    for t in range(T):
+        x[t, 32 * odd + rng.integers(0, 32, 60)] *= 2.0 ** rng.integers(20, 90, 60)
+    x = act_to_f64(bits(x))
+    wq, ws, col, w = picks(rng, 144, inp)
+    wq[:] = 0
+    col[:120] = 32 * odd[rng.integers(0, 60, 120)] + rng.integers(0, 32, 120)
+    code = rng.integers(1, 8, 144)
+    wq[np.arange(144), col // 2] = code << (4 * (col % 2))
+    w = q4.e2m1_table()[code]
+    y = to_f64(run(act_to_dev(bits(x)), u8_dev(wq), u8_dev(ws), False))
+    same_values(y, rounded(x[:, col] * w))
+    assert_no_device_error()
+
+
+def loud(seed, T, inp):
+    """Hidden states with loud columns, and a few values that are far louder."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(T, inp, generator=gen, device=DEV)
+    x *= torch.where(torch.rand(inp, generator=gen, device=DEV) < 0.01, 24.0, 1.0)
+    return torch.where(torch.rand(T, inp, generator=gen, device=DEV) < 2e-5, x * 2.0 ** 50, x).to(BF16)
+
+
+@pytest.mark.parametrize("T,inp", [(1, 4096), (8, 4096), (8, 4128), (13, 4096), (30, 4096)])
+def test_replayed_calls_and_calls_at_once(T, inp):
+    """The same bits from a captured call with other inputs, and from calls on several streams,
+    each with its own workspace."""
+    rng = np.random.default_rng(T)
+    wq, ws = (u8_dev(v) for v in weight(rng, 1040, inp))
+    xs = [loud(i, T, inp) for i in range(4)]
+    want = [ops.matmul_q4(x, wq, ws) for x in xs]
+    torch.cuda.synchronize()
+    x = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ops.matmul_q4(x, wq, ws)
+    for i in (1, 2, 3, 0):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        got = []
+        for a, st in zip(xs, streams):
+            with torch.cuda.stream(st):
+                got.append(ops.matmul_q4(a, wq, ws))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert_no_device_error()
+
+
+@pytest.mark.parametrize("T", [1, 8, 12, 30])
+def test_a_chain_of_calls_reads_what_the_one_before_wrote(T):
+    """Launches that overlap the end of the one before: x of each call is the result of the last,
+    read once more from memory for its finer pieces."""
+    rng = np.random.default_rng(T)
+    wq, ws = (u8_dev(v) for v in weight(rng, 1024, 1024))
+    big = loud(9, T, 1024)
+    want = None
+    for _ in range(20):
+        y = big
+        for i in range(8):
+            y = ops.matmul_q4(y, wq, ws)
+            if want is None:
+                torch.cuda.synchronize()
+        want = y if want is None else want
+        assert torch.equal(y, want)
