@@ -565,8 +565,10 @@ size_t dora_matmul_q4_t_workspace(int64_t T, int64_t out, int64_t in, int64_t ex
  *   Sizes: T, out >= 0 (either 0 is a no-op), in >= 1, below 2^31 - 1023,
  *   1 <= experts <= 4096.
  * Both operands enter as they are, infinities and the smallest numbers too, however many
- * tokens there are; a result below 2^-126 may be flushed to zero.  Parts are summed in a
- * fixed order: the same call gives the same bits.  Of few tokens x enters as 8-bit
+ * tokens there are; a result below 2^-126 may be flushed to zero.  A value of W from 2^128
+ * on (b = 253 and 254) is infinite where W enters as bf16: in dy W, and in x W^T of more
+ * tokens than x enters in pieces for.  Parts are summed in a fixed order: the same call
+ * gives the same bits.  Of few tokens x enters as 8-bit
  * pieces, up to four; where those do not hold 32 neighbouring values (an infinity, values
  * more than 2^36 apart), the call is slower.
  * One launch, or two where there is a workspace.  They are programmatic dependent ones:

@@ -7,8 +7,8 @@
 // that brings the group's largest magnitude to at most 448, and E4M3((x / s - h) 16)
 // with the scale s / 16.  8 bits less the 4 of h leave 4, so x / s is their sum exactly
 // where it is a multiple of 2^-13: always from 2^-6 on, 2^-14 of the largest magnitude.
-// Of 32 normal values one is below that with low bits set in 0.3% of the cases, beside
-// one 24 times louder in 4%.  What the two pieces leave of such a group is at most 2^-14
+// Of 32 normal values one is below that with low bits set in 0.2% of the cases, beside
+// one 24 times louder in 1.7%.  What the two pieces leave of such a group is at most 2^-14
 // and becomes two more, 2^22 finer.  A group that those do not hold either (an
 // infinity, values more than 2^36 apart) is added at the end in fp32 (add_rest).  So x
 // counts as it is, whatever its neighbours and however many tokens there are.
@@ -22,8 +22,9 @@
 //                warp the blocks of its own in turn.  More tokens are split by a launch
 //                of its own before (q4_split_kernel), while this one's first blocks of W
 //                are already on their way (8 x 8192 x 8192 14.4 us, 9 13.9).  Third and
-//                fourth pieces of either, from x in memory, one block in five of a
-//                token's, half of 32 tokens'.  Then the result out of tensor memory
+//                fourth pieces of either, from x in memory: for one block in a hundred of
+//                one token's, for two in five of 32 tokens'.  Then the result out of
+//                tensor memory
 //   next warp    tensor memory, scale words into it, MMA issue (four 32-wide steps per
 //                block)
 //   next warps   copies of W; copies of x or its pieces; W's scale words (BOX)
@@ -520,6 +521,8 @@ q4_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CU
             for (int j = 0; j < kAtOnce; ++j) all[j] = split_rest(v[j], &h[j], &l[j], &byte[j]);
             if (first) {
               if (PRE) {
+                // (a wait that may be left out: this warp saw the use before here arrive, so
+                // the phase is that one's or it is over)
                 ok = guard_wait(xempty0 + 8u * xt.i, xt.phase ^ 1u, ctl, p.guard, 78);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;

@@ -33,7 +33,7 @@
 // and take a little more (15360 x 8192 x 8192 1145 to 1170 us, 1.8 PFLOP/s; 512 44).  With
 // up to 192 the conversion and its hand-overs, about 0.46 us a block whatever the tokens
 // (128 x 38912 x 4096 34 us; 700 x 8192 x 8192 61; 4096 tokens evenly at 32 experts of
-// 2048 x 4096 64, unevenly 74, dy W 77 and 86 to 95).  Its groups take whole blocks, with
+// 2048 x 4096 63 to 70, unevenly 74, dy W 85 and 85 to 95).  Its groups take whole blocks, with
 // half the waits and addresses of half blocks (with those, and values by a table, 128 x
 // 38912 x 4096 took 40, 700 70, dy W 512 53).
 // Every wait on a shared-memory barrier is bounded; a wait that gives up records
@@ -528,7 +528,9 @@ q4_join_kernel(const float4 *__restrict__ parts, int n, int T, int quads, const 
 // sqrt(k n / most) of the cases, and a last wave behind others counts half.  Over four
 // draws of such loads, us by 256 tokens and by 192: 4096 at 32 of 2048 x 4096 72-74,
 // 78-80; 1001 at 8 of 1040 x 2080 16.1, 14.1; dy W 13-19, 17; 8192 at 64 of 1024 x 2048
-// 47-49, 49-50; dy W 58-59, 62.
+// 47-49, 49-50; dy W 58-59, 62.  Loads of other shapes, by 256 tokens: 4096 at 32 evenly 63, as
+// a router without preferences draws them 65, one expert with half of the tokens 79, falling
+// as 1 / rank 75; dy W 85, 86, 104, 97.
 struct Plan {
   int ntok, parts;
 };

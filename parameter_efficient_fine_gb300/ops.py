@@ -680,8 +680,9 @@ def dora_linear_q4(x: Tensor, wq: Tensor, wscale: Tensor, A: Tensor, B: Tensor, 
     norm and g = m / norm come from one of the norm ops on the values of the 4-bit
     weight (q4_load is exact in bfloat16) and carry no gradient; x, A, B and m do.  in is
     a multiple of 32 and out of 16; where A takes a gradient, the rank is a multiple of 8
-    up to 1024.  Where nothing takes a gradient, nothing is kept for one: serving a token
-    is the products and a compose."""
+    up to 1024.  Where something does, x and v are kept in 8 bits for the backward, which dA
+    and d_mag take from them (off by 2.6% of their norm, as in dora_linear_q8).  Where nothing
+    takes a gradient, nothing is kept for one: serving a token is the products and a compose."""
     if not (torch.is_grad_enabled() and any(t.requires_grad for t in (x, A, B, m))):
         _linear_q4_check(x, wq, wscale, A, B, m, g, norm)
         lora = (x @ A.to(x.dtype).t()) @ B.to(x.dtype).t()
