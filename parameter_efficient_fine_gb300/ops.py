@@ -69,13 +69,14 @@ from typing import Optional
 import torch
 from torch import Tensor
 
-from . import (_act, _expert_sort_sizes, _matmul_q4_sizes, _q4, _routed, _same, dora_compose_bwd, dora_compose_bwd_q8, dora_compose_bwd_q8_workspace, dora_compose_bwd_workspace,
-               dora_compose_fwd, dora_compose_fwd_q8, dora_expert_clear, dora_expert_return, dora_expert_return_bwd, dora_expert_send,
-               dora_expert_sort, dora_lora_grad_q8, dora_lora_grad_q8_workspace, dora_matmul_q4, dora_matmul_q4_t,
+from . import (_act, _expert_sort_sizes, _matmul_q4_sizes, _q4, _routed, _same, dora_compose_bwd, dora_compose_bwd_q8,
+               dora_compose_bwd_q8_workspace, dora_compose_bwd_workspace, dora_compose_fwd, dora_compose_fwd_q8,
+               dora_expert_clear, dora_expert_return, dora_expert_return_bwd, dora_expert_send, dora_expert_sort,
+               dora_lora_grad_q8, dora_lora_grad_q8_workspace, dora_matmul_q4, dora_matmul_q4_t,
                dora_matmul_q4_t_workspace, dora_matmul_q4_workspace, dora_matmul_q8, dora_matmul_q8_t,
-               dora_norm_factored, dora_norm_factored_bf16, dora_norm_factored_bf16_workspace,
-               dora_norm_factored_bwd, dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_q4_load,
-               dora_q4_store, dora_q8_load, dora_q8_store, dora_row_sumsq_bf16)
+               dora_norm_factored, dora_norm_factored_bf16, dora_norm_factored_bf16_workspace, dora_norm_factored_bwd,
+               dora_norm_factored_bwd_workspace, dora_norm_factored_workspace, dora_q4_load, dora_q4_store,
+               dora_q8_load, dora_q8_store, dora_row_sumsq_bf16)
 
 __all__ = ["norm_factored", "row_sumsq", "norm_factored_bf16", "compose", "compose_bwd", "norm_factored_bwd",
            "module", "dora_module", "q8_store", "q8_load", "compose_q8", "compose_bwd_q8", "matmul_q8", "matmul_q8_t",
